@@ -12,3 +12,9 @@ from .binding import (  # noqa: F401
     gdn_strerror, gdn_timing_enable, gdn_timing_read, gdn_version,
     header_functions, load_library, make_shape, new_ckpt,
 )
+from .layer import (  # noqa: F401
+    GDN_ACT_GELU, GDN_ACT_NONE, GDN_ACT_SILU, GdnConvShape, GdnLinearShape, GdnNormShape, GdnScanShape, gdn_conv_bwd,
+    gdn_conv_bwd_workspace_bytes, gdn_conv_fwd, gdn_linear_bwd, gdn_linear_bwd_workspace_bytes, gdn_linear_fwd,
+    gdn_linear_fwd_workspace_bytes, gdn_norm_bwd, gdn_norm_bwd_workspace_bytes, gdn_norm_fwd, gdn_scan_bwd,
+    gdn_scan_bwd_workspace_bytes, gdn_scan_ckpt_bytes, gdn_scan_fwd, gdn_scan_fwd_workspace_bytes,
+)

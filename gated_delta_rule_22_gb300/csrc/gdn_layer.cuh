@@ -1,0 +1,193 @@
+// gdn_layer.cuh -- parameter blocks, launchers and device helpers of the layer operators: the
+// short causal convolution, the selective state space scan, the group norm and the projection
+// (internal; not part of the C ABI).
+#pragma once
+
+#include "gdn_common.cuh"
+
+namespace gdn {
+
+enum { kActNone = 0, kActSilu = 1, kActGelu = 2 };
+
+// ---- shared with the C ABI's first file (gdn_api.cu)
+void api_clear_error();
+int api_cuda_status(cudaError_t e);
+int api_device_status_address(int **out);
+// 2-D tensor map of a row-major [rows][cols] array with `ld` elements between rows, box
+// {box_cols, box_rows}, 128-byte swizzle; what lies outside the array reads as zero.
+int api_rows_map(CUtensorMap *map, const void *ptr, bool bf16, uint64_t rows, uint64_t cols, uint64_t ld, int box_cols,
+                 int box_rows);
+
+// ---- parameter blocks
+struct ConvParams {
+    const void *x, *s0, *dy, *ds_T;
+    const float *w, *bias;
+    const int *lens;
+    void *y, *s_T, *dx, *ds0;
+    float *dw, *dbias;
+    float *part;            // backward: [slices][W + 1][C] partial sums of dw and dbias
+    long long ldx;
+    int B, T, C, W, act;
+};
+
+struct ScanParams {
+    const void *u, *dt, *B, *C, *z, *dy;
+    const float *A_log, *D, *dt_bias, *h0, *dh_T;
+    const int *lens;
+    void *y, *du, *ddt, *dB, *dC, *dz;
+    float *h_T, *ckpt, *dA_log, *dD, *ddt_bias, *dh0;
+    // sequence split: per (segment, b) the end state from a zero start (or, backward, the start
+    // adjoint from a zero end) [segs][B][C][N], turned in place into each segment's incoming state
+    // (adjoint), and the segment's sum of d [segs][B][C]
+    float *seg_state, *seg_sum;
+    float *part_bc;         // backward: [channel blocks of a group][B][T][G][2 N] partial dB, dC
+    float *part_c;          // backward: [segs][B][N + 2][C] partial dA, dD, ddt_bias
+    long long ldu, lddt, ldz, ldB, ldC;
+    int Bn, T, Cn, N, G, segs, seg_len;   // seg_len: steps per segment, a multiple of kScanTile
+};
+
+struct NormParams {
+    const void *x, *z, *dy;
+    const float *w, *b;
+    const float *stats_in;
+    void *y, *dx, *dz;
+    float *stats, *dw, *db;
+    float *part;            // backward: [slices][2][G D] partial sums of dw and db
+    long long ldx, ldz;
+    int M, G, D, act, center, slices;
+    float eps;
+};
+
+struct LinearParams {
+    const void *x, *W, *bias, *res, *pre_in, *dy;
+    void *y, *pre, *dx, *dW, *dbias;
+    char *ws;               // linear_fwd_workspace / linear_bwd_workspace bytes
+    int *status;
+    long long ldx, ldw, ldres;
+    int M, N, K, act;
+};
+
+constexpr int kScanTile = 16;   // steps between the scan's checkpoints, and of one staged tile
+
+// ---- geometry shared by the launchers and the size queries
+int conv_bwd_slices(const ConvParams &p);
+int scan_lanes(int N);                              // lanes that share one channel's states
+int scan_blocks(int C, int G, int N);               // channel blocks of one group
+void scan_split(ScanParams *p);                     // chooses segs and seg_len
+int norm_bwd_slices(int M, int G, int D, int dtype);
+size_t linear_fwd_workspace(const LinearParams &p, int dtype);
+size_t linear_bwd_workspace(const LinearParams &p, int dtype);
+
+// ---- launchers (dtype: 0 float32, 1 bfloat16)
+cudaError_t launch_conv_fwd(const ConvParams &p, int dtype, cudaStream_t s);
+cudaError_t launch_conv_bwd(const ConvParams &p, int dtype, cudaStream_t s);
+cudaError_t launch_scan_fwd(const ScanParams &p, int dtype, cudaStream_t s);
+cudaError_t launch_scan_bwd(const ScanParams &p, int dtype, cudaStream_t s);
+cudaError_t launch_norm_fwd(const NormParams &p, int dtype, cudaStream_t s);
+cudaError_t launch_norm_bwd(const NormParams &p, int dtype, cudaStream_t s);
+// These return a GDN_* code (they encode tensor maps).
+int launch_linear_fwd(const LinearParams &p, int dtype, cudaStream_t s);
+int launch_linear_bwd(const LinearParams &p, int dtype, cudaStream_t s);
+
+// ---- device helpers
+constexpr float kLog2e = 1.4426950408889634f;
+
+__device__ __forceinline__ float ex2(float x) {
+    float y;
+    asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
+    return y;
+}
+__device__ __forceinline__ float rcp(float x) {
+    float y;
+    asm("rcp.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
+    return y;
+}
+// 1 / (1 + exp(-x)) from the hardware's exp2 and reciprocal: a relative error of a few 2^-23 (an
+// exponent that overflows gives 1 / inf = 0).
+__device__ __forceinline__ float sigmoid_hw(float x) { return rcp(1.f + ex2(-x * kLog2e)); }
+__device__ __forceinline__ float silu_hw(float x) { return x * sigmoid_hw(x); }
+__device__ __forceinline__ float dsilu_hw(float x) {
+    const float s = sigmoid_hw(x);
+    return s * fmaf(x, 1.f - s, 1.f);
+}
+__device__ __forceinline__ float gelu_f(float x) { return 0.5f * x * (1.f + erff(x * 0.70710678f)); }
+__device__ __forceinline__ float dgelu_f(float x) {
+    return fmaf(x, 0.3989422804f * ex2(-0.5f * kLog2e * x * x), 0.5f * (1.f + erff(x * 0.70710678f)));
+}
+// act(x) and act'(x)
+template <int ACT>
+__device__ __forceinline__ float act_f(float x) {
+    return ACT == kActSilu ? silu_hw(x) : ACT == kActGelu ? gelu_f(x) : x;
+}
+template <int ACT>
+__device__ __forceinline__ float dact_f(float x) {
+    return ACT == kActSilu ? dsilu_hw(x) : ACT == kActGelu ? dgelu_f(x) : 1.f;
+}
+// softplus with its full relative accuracy for very negative x (log1p(e) ~ e)
+__device__ __forceinline__ float softplus_full(float x) { return x > 20.f ? x : log1pf(expf(x)); }
+
+// V consecutive elements as float, from an address aligned to V elements
+template <typename T, int V>
+__device__ __forceinline__ void load_vec(const T *p, float (&o)[V]) {
+    constexpr int BYTES = V * (int)sizeof(T);
+    if constexpr (sizeof(T) == 4) {
+        if constexpr (BYTES == 16) {
+            const float4 x = *reinterpret_cast<const float4 *>(p);
+            o[0] = x.x; o[1] = x.y; o[2] = x.z; o[3] = x.w;
+        } else if constexpr (BYTES == 8) {
+            const float2 x = *reinterpret_cast<const float2 *>(p);
+            o[0] = x.x; o[1] = x.y;
+        } else {
+            static_assert(V == 1, "vector width");
+            o[0] = to_f32(*p);
+        }
+    } else {
+        if constexpr (BYTES == 16) {
+            const uint4 x = *reinterpret_cast<const uint4 *>(p);
+            const uint32_t r[4] = {x.x, x.y, x.z, x.w};
+#pragma unroll
+            for (int i = 0; i < 4; ++i) {
+                o[2 * i] = __uint_as_float(r[i] << 16);
+                o[2 * i + 1] = __uint_as_float(r[i] & 0xffff0000u);
+            }
+        } else if constexpr (BYTES == 8) {
+            const uint2 x = *reinterpret_cast<const uint2 *>(p);
+            o[0] = __uint_as_float(x.x << 16); o[1] = __uint_as_float(x.x & 0xffff0000u);
+            o[2] = __uint_as_float(x.y << 16); o[3] = __uint_as_float(x.y & 0xffff0000u);
+        } else if constexpr (BYTES == 4) {
+            const uint32_t x = *reinterpret_cast<const uint32_t *>(p);
+            o[0] = __uint_as_float(x << 16); o[1] = __uint_as_float(x & 0xffff0000u);
+        } else {
+            static_assert(V == 1, "vector width");
+            o[0] = to_f32(*p);
+        }
+    }
+}
+__device__ __forceinline__ uint32_t pack_bf16(float lo, float hi) {
+    const __nv_bfloat162 v = __floats2bfloat162_rn(lo, hi);
+    return *reinterpret_cast<const uint32_t *>(&v);
+}
+template <typename T, int V>
+__device__ __forceinline__ void store_vec(T *p, const float (&o)[V]) {
+    constexpr int BYTES = V * (int)sizeof(T);
+    if constexpr (V == 1) {
+        *p = from_f32<T>(o[0]);
+    } else if constexpr (sizeof(T) == 4) {
+        if constexpr (BYTES == 16) *reinterpret_cast<float4 *>(p) = make_float4(o[0], o[1], o[2], o[3]);
+        else *reinterpret_cast<float2 *>(p) = make_float2(o[0], o[1]);
+    } else {
+        if constexpr (BYTES == 16)
+            *reinterpret_cast<uint4 *>(p) = make_uint4(pack_bf16(o[0], o[1]), pack_bf16(o[2], o[3]),
+                                                       pack_bf16(o[4], o[5]), pack_bf16(o[6], o[7]));
+        else if constexpr (BYTES == 8)
+            *reinterpret_cast<uint2 *>(p) = make_uint2(pack_bf16(o[0], o[1]), pack_bf16(o[2], o[3]));
+        else *reinterpret_cast<uint32_t *>(p) = pack_bf16(o[0], o[1]);
+    }
+}
+
+// Valid steps of batch row b.
+__device__ __forceinline__ int row_length(const int *lens, int b, int T) {
+    return lens == nullptr ? T : min(max(lens[b], 0), T);
+}
+
+}  // namespace gdn

@@ -1,0 +1,403 @@
+// gdn_norm.cu -- group norm over the channels of each row, with an activation or a gate, and its VJP.
+//
+// Row m, group g of D channels: xh = (x - mean) rstd, rstd = 1 / sqrt(var + eps) (center = 0: mean
+// taken as 0 and var as mean(x^2)), aff = xh w + b, y = act(aff) or y = aff act(z). Backward:
+//     daff = dy act'(aff)   or   daff = dy act(z), dz = dy aff act'(z)
+//     dxh = daff w,  dx = rstd (dxh - mean(dxh) - xh mean(dxh xh))   (center = 0: no mean(dxh) term)
+//     dw = sum_m daff xh,  db = sum_m daff
+// Bound by memory: x (and z, dy) are read once and stay in registers between the statistics and
+// the output. The mean is subtracted before the squares are summed.
+#include "gdn_layer.cuh"
+
+namespace gdn {
+
+namespace {
+
+constexpr int kNormThreads = 256;
+constexpr int kNormWarps = kNormThreads / 32;
+
+__device__ __forceinline__ float act_rt(int act, float x) {
+    return act == kActSilu ? silu_hw(x) : act == kActGelu ? gelu_f(x) : x;
+}
+__device__ __forceinline__ float dact_rt(int act, float x) {
+    return act == kActSilu ? dsilu_hw(x) : act == kActGelu ? dgelu_f(x) : 1.f;
+}
+
+template <int LPG>
+__device__ __forceinline__ float group_sum(float x) {
+#pragma unroll
+    for (int m = LPG / 2; m >= 1; m >>= 1) x += __shfl_xor_sync(kFullMask, x, m);
+    return x;
+}
+
+__device__ __forceinline__ float block_sum(float x, float *buf) {
+    x = warp_sum(x);
+    __syncthreads();
+    if ((threadIdx.x & 31) == 0) buf[threadIdx.x >> 5] = x;
+    __syncthreads();
+    float s = 0.f;
+#pragma unroll
+    for (int w = 0; w < kNormWarps; ++w) s += buf[w];
+    return s;
+}
+
+}  // namespace
+
+// LPG lanes per group, V neighbouring channels per lane, IT pieces: D <= LPG V IT. A warp takes
+// 32 / LPG groups of a row and keeps their w and b in registers over the rows that it walks.
+template <typename T, int V, int LPG, int IT>
+__global__ void __launch_bounds__(kNormThreads) norm_fwd_kernel(NormParams p) {
+    const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+    const int g = blockIdx.y * (32 / LPG) + lane / LPG, j = lane % LPG;
+    bool ok[IT];
+    float w[IT][V], b[IT][V];
+#pragma unroll
+    for (int i = 0; i < IT; ++i) {
+        const int e = (i * LPG + j) * V;
+        ok[i] = g < p.G && e < p.D;
+#pragma unroll
+        for (int v = 0; v < V; ++v) {
+            w[i][v] = ok[i] && p.w != nullptr ? p.w[(size_t)g * p.D + e + v] : 1.f;
+            b[i][v] = ok[i] && p.b != nullptr ? p.b[(size_t)g * p.D + e + v] : 0.f;
+        }
+    }
+    const float inv_D = 1.f / p.D;
+    const size_t col = (size_t)g * p.D + j * V;
+    for (int m = blockIdx.x * kNormWarps + warp; m < p.M; m += gridDim.x * kNormWarps) {
+        float x[IT][V], z[IT][V], s = 0.f, ss = 0.f;
+#pragma unroll
+        for (int i = 0; i < IT; ++i) {
+#pragma unroll
+            for (int v = 0; v < V; ++v) x[i][v] = z[i][v] = 0.f;
+            if (ok[i]) load_vec<T, V>(static_cast<const T *>(p.x) + (size_t)m * p.ldx + col + i * LPG * V, x[i]);
+            if (ok[i] && p.z != nullptr)
+                load_vec<T, V>(static_cast<const T *>(p.z) + (size_t)m * p.ldz + col + i * LPG * V, z[i]);
+#pragma unroll
+            for (int v = 0; v < V; ++v) s += x[i][v];
+        }
+        const float mean = p.center ? group_sum<LPG>(s) * inv_D : 0.f;
+#pragma unroll
+        for (int i = 0; i < IT; ++i)
+#pragma unroll
+            for (int v = 0; v < V; ++v) {
+                x[i][v] = ok[i] ? x[i][v] - mean : 0.f;
+                ss = fmaf(x[i][v], x[i][v], ss);
+            }
+        const float rstd = 1.f / sqrtf(fmaf(group_sum<LPG>(ss), inv_D, p.eps));
+        if (p.stats != nullptr && j == 0 && g < p.G)
+            *reinterpret_cast<float2 *>(p.stats + 2 * ((size_t)m * p.G + g)) = make_float2(mean, rstd);
+#pragma unroll
+        for (int i = 0; i < IT; ++i) {
+            if (!ok[i]) continue;
+            float o[V];
+#pragma unroll
+            for (int v = 0; v < V; ++v) {
+                const float aff = fmaf(x[i][v] * rstd, w[i][v], b[i][v]);
+                o[v] = p.z != nullptr ? aff * act_rt(p.act, z[i][v]) : act_rt(p.act, aff);
+            }
+            store_vec<T, V>(static_cast<T *>(p.y) + (size_t)m * p.G * p.D + col + i * LPG * V, o);
+        }
+    }
+}
+
+// The same layout. The parameter gradients are summed over a warp's rows, then over the CTA's warps
+// in ascending order, into the CTA's slice of the partial sums.
+template <typename T, int V, int LPG, int IT>
+__global__ void __launch_bounds__(kNormThreads) norm_bwd_kernel(NormParams p) {
+    __shared__ float sums[2][kNormWarps][32 * V * IT];
+    const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+    const int g = blockIdx.y * (32 / LPG) + lane / LPG, j = lane % LPG;
+    bool ok[IT];
+    float w[IT][V], b[IT][V], dw[IT][V], db[IT][V];
+#pragma unroll
+    for (int i = 0; i < IT; ++i) {
+        const int e = (i * LPG + j) * V;
+        ok[i] = g < p.G && e < p.D;
+#pragma unroll
+        for (int v = 0; v < V; ++v) {
+            w[i][v] = ok[i] && p.w != nullptr ? p.w[(size_t)g * p.D + e + v] : 1.f;
+            b[i][v] = ok[i] && p.b != nullptr ? p.b[(size_t)g * p.D + e + v] : 0.f;
+            dw[i][v] = db[i][v] = 0.f;
+        }
+    }
+    const float inv_D = 1.f / p.D;
+    const size_t col = (size_t)g * p.D + j * V;
+    for (int m = blockIdx.x * kNormWarps + warp; m < p.M; m += gridDim.x * kNormWarps) {
+        float xh[IT][V], dxh[IT][V], s1 = 0.f, s2 = 0.f;
+        float2 st = make_float2(0.f, 0.f);
+        if (g < p.G) st = *reinterpret_cast<const float2 *>(p.stats_in + 2 * ((size_t)m * p.G + g));
+#pragma unroll
+        for (int i = 0; i < IT; ++i) {
+            const size_t at = (size_t)m * p.G * p.D + col + i * LPG * V;
+            float x[V], z[V], dy[V], dz[V];
+#pragma unroll
+            for (int v = 0; v < V; ++v) x[v] = z[v] = dy[v] = 0.f;
+            if (ok[i]) {
+                load_vec<T, V>(static_cast<const T *>(p.x) + (size_t)m * p.ldx + col + i * LPG * V, x);
+                load_vec<T, V>(static_cast<const T *>(p.dy) + at, dy);
+                if (p.z != nullptr)
+                    load_vec<T, V>(static_cast<const T *>(p.z) + (size_t)m * p.ldz + col + i * LPG * V, z);
+            }
+#pragma unroll
+            for (int v = 0; v < V; ++v) {
+                xh[i][v] = ok[i] ? (x[v] - st.x) * st.y : 0.f;
+                const float aff = fmaf(xh[i][v], w[i][v], b[i][v]);
+                float daff;
+                if (p.z != nullptr) {
+                    if (p.act == kActSilu) {
+                        const float sg = sigmoid_hw(z[v]);
+                        daff = dy[v] * z[v] * sg;
+                        dz[v] = dy[v] * aff * sg * fmaf(z[v], 1.f - sg, 1.f);
+                    } else {
+                        daff = dy[v] * act_rt(p.act, z[v]);
+                        dz[v] = dy[v] * aff * dact_rt(p.act, z[v]);
+                    }
+                } else {
+                    daff = dy[v] * dact_rt(p.act, aff);
+                }
+                db[i][v] += daff;
+                dw[i][v] = fmaf(daff, xh[i][v], dw[i][v]);
+                dxh[i][v] = daff * w[i][v];
+                s1 += dxh[i][v];
+                s2 = fmaf(dxh[i][v], xh[i][v], s2);
+            }
+            if (ok[i] && p.dz != nullptr) store_vec<T, V>(static_cast<T *>(p.dz) + at, dz);
+        }
+        s1 = p.center ? group_sum<LPG>(s1) * inv_D : 0.f;
+        s2 = group_sum<LPG>(s2) * inv_D;
+#pragma unroll
+        for (int i = 0; i < IT; ++i) {
+            if (!ok[i]) continue;
+            float o[V];
+#pragma unroll
+            for (int v = 0; v < V; ++v) o[v] = st.y * (dxh[i][v] - s1 - xh[i][v] * s2);
+            store_vec<T, V>(static_cast<T *>(p.dx) + (size_t)m * p.G * p.D + col + i * LPG * V, o);
+        }
+    }
+#pragma unroll
+    for (int i = 0; i < IT; ++i)
+#pragma unroll
+        for (int v = 0; v < V; ++v) {
+            sums[0][warp][(i * 32 + lane) * V + v] = dw[i][v];
+            sums[1][warp][(i * 32 + lane) * V + v] = db[i][v];
+        }
+    __syncthreads();
+    const size_t C = (size_t)p.G * p.D;
+    for (int k = threadIdx.x; k < 2 * 32 * V * IT; k += kNormThreads) {
+        const int which = k / (32 * V * IT), n = k % (32 * V * IT), i = n / (32 * V), ln = n / V % 32, v = n % V;
+        const int gg = blockIdx.y * (32 / LPG) + ln / LPG, e = (i * LPG + ln % LPG) * V + v;
+        if (gg >= p.G || e >= p.D) continue;
+        float a = 0.f;
+#pragma unroll
+        for (int u = 0; u < kNormWarps; ++u) a += sums[which][u][n];
+        p.part[((size_t)blockIdx.x * 2 + which) * C + (size_t)gg * p.D + e] = a;
+    }
+}
+
+// Groups wider than a warp's registers take: a CTA per row and group, passes over the channels
+// through the caches.
+template <typename T>
+__global__ void __launch_bounds__(kNormThreads) norm_fwd_wide_kernel(NormParams p) {
+    __shared__ float buf[kNormWarps];
+    const int m = blockIdx.x, g = blockIdx.y;
+    const T *x = static_cast<const T *>(p.x) + (size_t)m * p.ldx + (size_t)g * p.D;
+    const T *z = static_cast<const T *>(p.z) + (size_t)m * p.ldz + (size_t)g * p.D;
+    T *y = static_cast<T *>(p.y) + ((size_t)m * p.G + g) * p.D;
+    const float inv_D = 1.f / p.D;
+    float mean = 0.f;
+    if (p.center) {
+        float s = 0.f;
+        for (int e = threadIdx.x; e < p.D; e += kNormThreads) s += to_f32(x[e]);
+        mean = block_sum(s, buf) * inv_D;
+    }
+    float ss = 0.f;
+    for (int e = threadIdx.x; e < p.D; e += kNormThreads) {
+        const float d = to_f32(x[e]) - mean;
+        ss = fmaf(d, d, ss);
+    }
+    const float rstd = 1.f / sqrtf(fmaf(block_sum(ss, buf), inv_D, p.eps));
+    if (p.stats != nullptr && threadIdx.x == 0)
+        *reinterpret_cast<float2 *>(p.stats + 2 * ((size_t)m * p.G + g)) = make_float2(mean, rstd);
+    for (int e = threadIdx.x; e < p.D; e += kNormThreads) {
+        const float w = p.w != nullptr ? p.w[(size_t)g * p.D + e] : 1.f, b = p.b != nullptr ? p.b[(size_t)g * p.D + e] : 0.f;
+        const float aff = fmaf((to_f32(x[e]) - mean) * rstd, w, b);
+        y[e] = from_f32<T>(p.z != nullptr ? aff * act_rt(p.act, to_f32(z[e])) : act_rt(p.act, aff));
+    }
+}
+
+// xh and daff of one channel
+template <typename T>
+__device__ __forceinline__ void norm_grad_at(const NormParams &p, size_t m, int g, int e, float2 st, float &xh,
+                                             float &daff, float &dz) {
+    const size_t ch = (size_t)g * p.D + e;
+    const float w = p.w != nullptr ? p.w[ch] : 1.f, b = p.b != nullptr ? p.b[ch] : 0.f;
+    const float dy = to_f32(static_cast<const T *>(p.dy)[m * p.G * p.D + ch]);
+    xh = (to_f32(static_cast<const T *>(p.x)[m * p.ldx + ch]) - st.x) * st.y;
+    const float aff = fmaf(xh, w, b);
+    if (p.z != nullptr) {
+        const float z = to_f32(static_cast<const T *>(p.z)[m * p.ldz + ch]);
+        daff = dy * act_rt(p.act, z);
+        dz = dy * aff * dact_rt(p.act, z);
+    } else {
+        daff = dy * dact_rt(p.act, aff);
+        dz = 0.f;
+    }
+}
+
+template <typename T>
+__global__ void __launch_bounds__(kNormThreads) norm_bwd_wide_kernel(NormParams p) {
+    __shared__ float buf[kNormWarps];
+    const int g = blockIdx.y;
+    const size_t m = blockIdx.x, out = (m * p.G + g) * p.D;
+    const float2 st = *reinterpret_cast<const float2 *>(p.stats_in + 2 * (m * p.G + g));
+    const float inv_D = 1.f / p.D;
+    float s1 = 0.f, s2 = 0.f;
+    for (int e = threadIdx.x; e < p.D; e += kNormThreads) {
+        float xh, daff, dz;
+        norm_grad_at<T>(p, m, g, e, st, xh, daff, dz);
+        const float dxh = daff * (p.w != nullptr ? p.w[(size_t)g * p.D + e] : 1.f);
+        s1 += dxh;
+        s2 = fmaf(dxh, xh, s2);
+        if (p.dz != nullptr) static_cast<T *>(p.dz)[out + e] = from_f32<T>(dz);
+    }
+    s1 = block_sum(s1, buf) * inv_D;
+    s2 = block_sum(s2, buf) * inv_D;
+    if (!p.center) s1 = 0.f;
+    for (int e = threadIdx.x; e < p.D; e += kNormThreads) {
+        float xh, daff, dz;
+        norm_grad_at<T>(p, m, g, e, st, xh, daff, dz);
+        const float dxh = daff * (p.w != nullptr ? p.w[(size_t)g * p.D + e] : 1.f);
+        static_cast<T *>(p.dx)[out + e] = from_f32<T>(st.y * (dxh - s1 - xh * s2));
+    }
+}
+
+// Partial dw, db of wide groups: a thread per channel and slice of the rows.
+template <typename T>
+__global__ void __launch_bounds__(kNormThreads) norm_bwd_wide_sums_kernel(NormParams p) {
+    const size_t C = (size_t)p.G * p.D, ch = (size_t)blockIdx.x * kNormThreads + threadIdx.x;
+    if (ch >= C) return;
+    const int g = (int)(ch / p.D), e = (int)(ch % p.D);
+    float dw = 0.f, db = 0.f;
+    for (size_t m = blockIdx.y; m < (size_t)p.M; m += gridDim.y) {
+        const float2 st = *reinterpret_cast<const float2 *>(p.stats_in + 2 * (m * p.G + g));
+        float xh, daff, dz;
+        norm_grad_at<T>(p, m, g, e, st, xh, daff, dz);
+        dw = fmaf(daff, xh, dw);
+        db += daff;
+    }
+    p.part[(size_t)blockIdx.y * 2 * C + ch] = dw;
+    p.part[((size_t)blockIdx.y * 2 + 1) * C + ch] = db;
+}
+
+// dw, db from the slices' partial sums, in ascending order.
+__global__ void __launch_bounds__(256) norm_reduce_kernel(NormParams p) {
+    const size_t C = (size_t)p.G * p.D, i = (size_t)blockIdx.x * 256 + threadIdx.x;
+    if (i >= 2 * C) return;
+    float *out = i < C ? p.dw : p.db;
+    if (out == nullptr) return;
+    double a = 0.0;
+    for (int s = 0; s < p.slices; ++s) a += (double)p.part[(size_t)s * 2 * C + i];
+    out[i % C] = (float)a;
+}
+
+namespace {
+
+// How a group lies on a warp: V channels per lane, lanes per group, pieces (0: the wide kernels).
+struct NormGeo {
+    int V, lanes, pieces;
+};
+NormGeo norm_geo(int D, int V) {
+    NormGeo q = {V, 8, 1};
+    while (q.lanes < 32 && q.lanes * V < D) q.lanes *= 2;
+    while (q.pieces < 16 && q.lanes * V * q.pieces < D) q.pieces *= 2;
+    if (q.lanes * V * q.pieces < D || V * q.pieces > 16) q.pieces = 0;
+    return q;
+}
+
+// Groups and row slices of the grid: about 8 CTAs per SM, at most one warp per row.
+int norm_slices(int M, int sets) {
+    const int most = (M + kNormWarps - 1) / kNormWarps, want = (152 * 8 + sets - 1) / sets;
+    return want < most ? want : most;
+}
+
+bool norm_aligned(const NormParams &p, int V, size_t e) {
+    return p.D % V == 0 && p.ldx % V == 0 && p.ldz % V == 0 && (uintptr_t)p.x % (V * e) == 0 && (uintptr_t)p.z % (V * e) == 0;
+}
+
+template <typename T, int V, int LPG, int IT>
+cudaError_t norm_launch(NormParams p, bool bwd, cudaStream_t s) {
+    const int sets = (p.G + 32 / LPG - 1) / (32 / LPG);
+    const dim3 grid(bwd ? p.slices : norm_slices(p.M, sets), sets);
+    const char *name = bwd ? "norm_bwd" : "norm_fwd";
+    timing_mark(name, 0, s);
+    if (bwd) norm_bwd_kernel<T, V, LPG, IT><<<grid, kNormThreads, 0, s>>>(p);
+    else norm_fwd_kernel<T, V, LPG, IT><<<grid, kNormThreads, 0, s>>>(p);
+    timing_mark(name, 1, s);
+    return cudaGetLastError();
+}
+
+template <typename T, int V>
+cudaError_t norm_pick(const NormParams &p, const NormGeo &q, bool bwd, cudaStream_t s) {
+    if (q.lanes == 8) return norm_launch<T, V, 8, 1>(p, bwd, s);
+    if (q.lanes == 16) return norm_launch<T, V, 16, 1>(p, bwd, s);
+    if (q.pieces == 1) return norm_launch<T, V, 32, 1>(p, bwd, s);
+    if (q.pieces == 2) return norm_launch<T, V, 32, 2>(p, bwd, s);
+    if constexpr (V <= 4) {
+        if (q.pieces == 4) return norm_launch<T, V, 32, 4>(p, bwd, s);
+    }
+    if constexpr (V == 1) {
+        if (q.pieces == 8) return norm_launch<T, V, 32, 8>(p, bwd, s);
+        if (q.pieces == 16) return norm_launch<T, V, 32, 16>(p, bwd, s);
+    }
+    return cudaErrorInvalidValue;
+}
+
+template <typename T>
+cudaError_t norm_wide(const NormParams &p, bool bwd, cudaStream_t s) {
+    const char *name = bwd ? "norm_bwd" : "norm_fwd";
+    timing_mark(name, 0, s);
+    if (bwd) norm_bwd_wide_kernel<T><<<dim3(p.M, p.G), kNormThreads, 0, s>>>(p);
+    else norm_fwd_wide_kernel<T><<<dim3(p.M, p.G), kNormThreads, 0, s>>>(p);
+    timing_mark(name, 1, s);
+    const cudaError_t e = cudaGetLastError();
+    if (e != cudaSuccess || !bwd || (p.dw == nullptr && p.db == nullptr)) return e;
+    const size_t C = (size_t)p.G * p.D;
+    timing_mark("norm_sums", 0, s);
+    norm_bwd_wide_sums_kernel<T><<<dim3((unsigned)((C + kNormThreads - 1) / kNormThreads), p.slices), kNormThreads, 0, s>>>(p);
+    timing_mark("norm_sums", 1, s);
+    return cudaGetLastError();
+}
+
+template <typename T>
+cudaError_t norm_any(const NormParams &p, bool bwd, cudaStream_t s) {
+    constexpr int W = sizeof(T) == 2 ? 8 : 4;
+    const bool vec = norm_aligned(p, W, sizeof(T));
+    const NormGeo q = norm_geo(p.D, vec ? W : 1);
+    if (q.pieces == 0) return norm_wide<T>(p, bwd, s);
+    return vec ? norm_pick<T, W>(p, q, bwd, s) : norm_pick<T, 1>(p, q, bwd, s);
+}
+
+}  // namespace
+
+// Slices of the rows whose partial dw, db the backward sums. The size query knows no addresses, so
+// the count goes by the widest layout whatever the alignment: 2 partial rows per slice.
+int norm_bwd_slices(int M, int G, int D, int dtype) {
+    const NormGeo q = norm_geo(D, D % (dtype == 0 ? 4 : 8) == 0 ? (dtype == 0 ? 4 : 8) : 1);
+    if (q.pieces == 0) return M < 64 ? M : 64;
+    return norm_slices(M, (G + 32 / q.lanes - 1) / (32 / q.lanes));
+}
+
+cudaError_t launch_norm_fwd(const NormParams &p, int dtype, cudaStream_t s) {
+    return dtype == 0 ? norm_any<float>(p, false, s) : norm_any<__nv_bfloat16>(p, false, s);
+}
+
+cudaError_t launch_norm_bwd(const NormParams &p, int dtype, cudaStream_t s) {
+    cudaError_t e = dtype == 0 ? norm_any<float>(p, true, s) : norm_any<__nv_bfloat16>(p, true, s);
+    if (e != cudaSuccess || (p.dw == nullptr && p.db == nullptr)) return e;
+    timing_mark("norm_reduce", 0, s);
+    norm_reduce_kernel<<<(unsigned)(((size_t)2 * p.G * p.D + 255) / 256), 256, 0, s>>>(p);
+    timing_mark("norm_reduce", 1, s);
+    return cudaGetLastError();
+}
+
+}  // namespace gdn

@@ -1,0 +1,262 @@
+// gdn_scan.cu -- selective state space scan, forward: prompts, the step of a single token, and the
+// split of long sequences.
+//
+//     d = softplus(dt + dt_bias),  A = -exp(A_log)
+//     h_t = exp(d A) h_{t-1} + d u B_t,   y_t = (C_t . h_t + D u) silu(z)
+//
+// Each state and step costs one exp2 and four float32 operations (d A log2 e, (d u) B, the update,
+// the product with C), each channel and step 2 to 4 elements of memory traffic: with 16 states the
+// exponentials bind, not the memory.
+#include "gdn_scan.cuh"
+
+namespace gdn {
+
+// LITE: the segment's end state from a zero start and its sum of d, nothing else (first pass over a
+// split sequence).
+template <int LPC, typename T, bool LITE>
+__global__ void __launch_bounds__(kScanThreads) scan_fwd_kernel(ScanParams p, bool vec) {
+    using G = ScanGeo<LPC>;
+    constexpr int CH = G::CH, NP = G::NP, V = G::V, KB = G::KB, TT = kScanTile;
+    __shared__ float2 sdx[TT][CH];              // d, d u
+    __shared__ __align__(16) float sB[TT][NP], sC[TT][NP];
+    __shared__ float score[TT][CH + 1];
+    const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
+    const ScanPlace q = scan_place<LPC>(p);
+    if (q.first >= q.last) return;
+    const int L = row_length(p.lens, q.b, p.T);
+    // this thread's staged elements: step ts of a tile, V channels from cv; and its states: channel
+    // ch, states n0 .. n0 + 3
+    const int ts = tid >> 4, cv = (tid & 15) * V, nv = q.nc - cv;
+    const int ch = warp * G::CPW + lane / LPC, n0 = 4 * (lane % LPC);
+    const bool live = ch < q.nc;
+    const int c = q.c0 + (live ? ch : 0);
+    const T *u = static_cast<const T *>(p.u) + (size_t)q.b * p.T * p.ldu + q.c0 + cv;
+    const T *dt = static_cast<const T *>(p.dt) + (size_t)q.b * p.T * p.lddt + q.c0 + cv;
+    const T *z = static_cast<const T *>(p.z) + (size_t)q.b * p.T * p.ldz + q.c0 + cv;
+    const T *Bm = static_cast<const T *>(p.B) + (size_t)q.b * p.T * p.ldB + q.g * p.N;
+    const T *Cm = static_cast<const T *>(p.C) + (size_t)q.b * p.T * p.ldC + q.g * p.N;
+    float A2[4], h[4] = {0.f, 0.f, 0.f, 0.f}, D[V], bias[V], sum_d[V];
+#pragma unroll
+    for (int k = 0; k < 4; ++k) A2[k] = n0 + k < p.N ? -expf(p.A_log[(size_t)c * p.N + n0 + k]) * kLog2e : 0.f;
+#pragma unroll
+    for (int v = 0; v < V; ++v) {
+        D[v] = p.D != nullptr && v < nv ? p.D[q.c0 + cv + v] : 0.f;
+        bias[v] = p.dt_bias != nullptr && v < nv ? p.dt_bias[q.c0 + cv + v] : 0.f;
+        sum_d[v] = 0.f;
+    }
+    const size_t state_row = ((size_t)q.b * p.Cn + c) * p.N;
+    if (!LITE && live) {
+        if (p.segs > 1) load_states(p.seg_state + (size_t)q.seg * p.Bn * p.Cn * p.N + state_row, n0, p.N, h);
+        else if (p.h0 != nullptr) load_states(p.h0 + state_row, n0, p.N, h);
+    }
+    float ru[V], rd[V], rz[V], rB[KB], rC[KB];
+    auto fetch = [&](int tile) {
+        const int t = tile * TT + ts, n = t < L ? nv : 0;
+        load_channels<T, V>(u + (size_t)t * p.ldu, n, vec, ru);
+        load_channels<T, V>(dt + (size_t)t * p.lddt, n, vec, rd);
+        if (!LITE && p.z != nullptr) load_channels<T, V>(z + (size_t)t * p.ldz, n, vec, rz);
+#pragma unroll
+        for (int k = 0; k < KB; ++k) {
+            const int e = tid + kScanThreads * k, tb = tile * TT + e / NP, n1 = e % NP;
+            const bool ok = tb < L && n1 < p.N;
+            rB[k] = ok ? to_f32(Bm[(size_t)tb * p.ldB + n1]) : 0.f;
+            if (!LITE) rC[k] = ok ? to_f32(Cm[(size_t)tb * p.ldC + n1]) : 0.f;
+        }
+    };
+    fetch(q.first);
+    for (int tile = q.first; tile < q.last; ++tile) {
+        const int t = tile * TT + ts;
+        float cu[V], cz[V];
+#pragma unroll
+        for (int v = 0; v < V; ++v) {
+            cu[v] = ru[v];
+            cz[v] = rz[v];
+            const float d = t < L ? softplus_full(rd[v] + bias[v]) : 0.f;
+            sum_d[v] += d;
+            sdx[ts][cv + v] = make_float2(d, d * ru[v]);
+        }
+#pragma unroll
+        for (int k = 0; k < KB; ++k) {
+            const int e = tid + kScanThreads * k;
+            sB[e / NP][e % NP] = rB[k];
+            if (!LITE) sC[e / NP][e % NP] = rC[k];
+        }
+        __syncthreads();
+        if (tile + 1 < q.last) fetch(tile + 1);
+        if (!LITE && p.ckpt != nullptr && live) {
+            const int tiles = (p.T + TT - 1) / TT;
+            store_states(p.ckpt + (((size_t)q.b * tiles + tile) * p.Cn + c) * p.N, n0, p.N, h);
+        }
+#pragma unroll
+        for (int i = 0; i < TT; ++i) {
+            const float2 dx = sdx[i][ch];
+            const float4 b4 = *reinterpret_cast<const float4 *>(&sB[i][n0]);
+            const float bb[4] = {b4.x, b4.y, b4.z, b4.w};
+            float core = 0.f;
+            float4 c4 = make_float4(0.f, 0.f, 0.f, 0.f);
+            if (!LITE) c4 = *reinterpret_cast<const float4 *>(&sC[i][n0]);
+            const float cc[4] = {c4.x, c4.y, c4.z, c4.w};
+#pragma unroll
+            for (int k = 0; k < 4; ++k) {
+                h[k] = fmaf(ex2(dx.x * A2[k]), h[k], dx.y * bb[k]);
+                if (!LITE) core = fmaf(cc[k], h[k], core);
+            }
+            if (!LITE) {
+                core = lane_sum<LPC>(core);
+                if (lane % LPC == 0) score[i][ch] = core;
+            }
+        }
+        __syncthreads();
+        if (!LITE && t < p.T) {
+            float o[V];
+#pragma unroll
+            for (int v = 0; v < V; ++v) {
+                const float core = fmaf(D[v], cu[v], score[ts][cv + v]);
+                o[v] = t < L ? (p.z != nullptr ? core * silu_hw(cz[v]) : core) : 0.f;
+            }
+            store_channels<T, V>(static_cast<T *>(p.y) + ((size_t)q.b * p.T + t) * p.Cn + q.c0 + cv, nv, vec, o);
+        }
+    }
+    if (LITE) {
+        if (live) store_states(p.seg_state + (size_t)q.seg * p.Bn * p.Cn * p.N + state_row, n0, p.N, h);
+        // the sum of d over the segment: over a thread's tiles, then over the 16 steps of a tile
+#pragma unroll
+        for (int v = 0; v < V; ++v) score[ts][cv + v] = sum_d[v];
+        __syncthreads();
+        if (tid < q.nc) {
+            float a = 0.f;
+            for (int i = 0; i < TT; ++i) a += score[i][tid];
+            p.seg_sum[((size_t)q.seg * p.Bn + q.b) * p.Cn + q.c0 + tid] = a;
+        }
+    } else if (p.h_T != nullptr && live && (p.segs == 1 || q.seg == p.segs - 1)) {
+        store_states(p.h_T + state_row, n0, p.N, h);
+    }
+}
+
+// One step (T = 1): a streaming pass over the states, LPC lanes per channel, h_T may be h0.
+template <int LPC, typename T>
+__global__ void __launch_bounds__(256) scan_step_kernel(ScanParams p) {
+    const size_t id = (size_t)blockIdx.x * 256 + threadIdx.x;
+    const size_t row = id / LPC;                       // (batch row, channel)
+    const int n0 = 4 * (int)(id % LPC);
+    const bool live = row < (size_t)p.Bn * p.Cn;
+    const int b = live ? (int)(row / p.Cn) : 0, c = live ? (int)(row % p.Cn) : 0, g = c / (p.Cn / p.G);
+    const bool on = live && row_length(p.lens, b, 1) == 1;
+    float h[4] = {0.f, 0.f, 0.f, 0.f}, core = 0.f, u = 0.f;
+    if (live && p.h0 != nullptr) load_states(p.h0 + row * p.N, n0, p.N, h);
+    if (on) {
+        u = to_f32(static_cast<const T *>(p.u)[(size_t)b * p.ldu + c]);
+        const float d = softplus_full(to_f32(static_cast<const T *>(p.dt)[(size_t)b * p.lddt + c]) +
+                                      (p.dt_bias != nullptr ? p.dt_bias[c] : 0.f));
+        const T *Bm = static_cast<const T *>(p.B) + (size_t)b * p.ldB + g * p.N;
+        const T *Cm = static_cast<const T *>(p.C) + (size_t)b * p.ldC + g * p.N;
+        float al[4];
+        load_states(p.A_log + (size_t)c * p.N, n0, p.N, al);
+#pragma unroll
+        for (int k = 0; k < 4; ++k) {
+            if (n0 + k >= p.N) break;
+            h[k] = fmaf(ex2(-expf(al[k]) * kLog2e * d), h[k], d * u * to_f32(Bm[n0 + k]));
+            core = fmaf(to_f32(Cm[n0 + k]), h[k], core);
+        }
+    }
+    core = lane_sum<LPC>(core);
+    if (!live) return;
+    if (n0 == 0) {
+        float y = 0.f;
+        if (on) {
+            y = core + (p.D != nullptr ? p.D[c] * u : 0.f);
+            if (p.z != nullptr) y *= silu_hw(to_f32(static_cast<const T *>(p.z)[(size_t)b * p.ldz + c]));
+        }
+        static_cast<T *>(p.y)[row] = from_f32<T>(y);
+    }
+    if (p.h_T != nullptr) store_states(p.h_T + row * p.N, n0, p.N, h);
+}
+
+__global__ void __launch_bounds__(256) scan_combine_kernel(ScanParams p, const float *start, float *out, bool reverse) {
+    const size_t n = (size_t)p.Bn * p.Cn * p.N, i = (size_t)blockIdx.x * 256 + threadIdx.x;
+    if (i >= n) return;
+    const size_t bc = i / p.N;
+    const float A2 = -expf(p.A_log[(bc % p.Cn) * p.N + i % p.N]) * kLog2e;
+    float X = start != nullptr ? start[i] : 0.f;
+    for (int k = 0; k < p.segs; ++k) {
+        const int s = reverse ? p.segs - 1 - k : k;
+        const float own = p.seg_state[(size_t)s * n + i];
+        p.seg_state[(size_t)s * n + i] = X;
+        X = fmaf(ex2(A2 * p.seg_sum[(size_t)s * p.Bn * p.Cn + bc]), X, own);
+    }
+    if (out != nullptr) out[i] = X;
+}
+
+cudaError_t launch_scan_combine(const ScanParams &p, const float *start, float *out, bool reverse, cudaStream_t s) {
+    const size_t n = (size_t)p.Bn * p.Cn * p.N;
+    timing_mark("scan_combine", 0, s);
+    scan_combine_kernel<<<(unsigned)((n + 255) / 256), 256, 0, s>>>(p, start, out, reverse);
+    timing_mark("scan_combine", 1, s);
+    return cudaGetLastError();
+}
+
+int scan_lanes(int N) { return N <= 16 ? 4 : N <= 32 ? 8 : 16; }
+
+int scan_blocks(int C, int G, int N) {
+    const int ch = kScanThreads / scan_lanes(N), per = C / G;
+    return (per + ch - 1) / ch;
+}
+
+// A split sequence is walked twice, so it is split only where its CTAs leave most SMs idle (under
+// 76 of the 152), into segments of at least 8 tiles, for about two CTAs per SM.
+void scan_split(ScanParams *p) {
+    const long long ctas = (long long)p->Bn * p->G * scan_blocks(p->Cn, p->G, p->N);
+    const int tiles = (p->T + kScanTile - 1) / kScanTile;
+    int segs = 1;
+    if (ctas < 76 && tiles >= 16) {
+        segs = (int)((304 + ctas - 1) / ctas);
+        if (segs > tiles / 8) segs = tiles / 8;
+    }
+    const int per = (tiles + segs - 1) / segs;
+    p->seg_len = per * kScanTile;
+    p->segs = (tiles + per - 1) / per;
+}
+
+namespace {
+
+template <int LPC, typename T>
+cudaError_t scan_fwd_launch(const ScanParams &p, cudaStream_t s) {
+    if (p.T == 1 && p.ckpt == nullptr) {
+        const size_t n = (size_t)p.Bn * p.Cn * LPC;
+        timing_mark("scan_step", 0, s);
+        scan_step_kernel<LPC, T><<<(unsigned)((n + 255) / 256), 256, 0, s>>>(p);
+        timing_mark("scan_step", 1, s);
+        return cudaGetLastError();
+    }
+    const dim3 grid(p.Bn * p.G * scan_blocks(p.Cn, p.G, p.N), p.segs);
+    const bool vec = scan_vec<T>(p, ScanGeo<LPC>::V);
+    cudaError_t e;
+    if (p.segs > 1) {
+        timing_mark("scan_fwd_ends", 0, s);
+        scan_fwd_kernel<LPC, T, true><<<grid, kScanThreads, 0, s>>>(p, vec);
+        timing_mark("scan_fwd_ends", 1, s);
+        if ((e = cudaGetLastError()) != cudaSuccess) return e;
+        if ((e = launch_scan_combine(p, p.h0, nullptr, false, s)) != cudaSuccess) return e;
+    }
+    timing_mark("scan_fwd", 0, s);
+    scan_fwd_kernel<LPC, T, false><<<grid, kScanThreads, 0, s>>>(p, vec);
+    timing_mark("scan_fwd", 1, s);
+    return cudaGetLastError();
+}
+
+template <typename T>
+cudaError_t scan_fwd_lanes(const ScanParams &p, cudaStream_t s) {
+    switch (scan_lanes(p.N)) {
+        case 4: return scan_fwd_launch<4, T>(p, s);
+        case 8: return scan_fwd_launch<8, T>(p, s);
+        default: return scan_fwd_launch<16, T>(p, s);
+    }
+}
+
+}  // namespace
+
+cudaError_t launch_scan_fwd(const ScanParams &p, int dtype, cudaStream_t s) {
+    return dtype == 0 ? scan_fwd_lanes<float>(p, s) : scan_fwd_lanes<__nv_bfloat16>(p, s);
+}
+
+}  // namespace gdn

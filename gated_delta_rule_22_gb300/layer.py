@@ -1,0 +1,402 @@
+"""Binding of the layer operators of libgdn.so (include/gdn.h): the short causal convolution, the
+selective state space scan, the group norm and the projection. Argument marshalling only, as in
+binding.py.
+
+Inputs that the header gives a row stride may be slices of a wider tensor along the last dimension
+(x[..., :C] of a contiguous tensor); everything else must be contiguous.
+"""
+from __future__ import annotations
+
+import ctypes
+
+from .binding import GDN_OK, GdnError, _check, _dtype_code, _require_cuda, _torch, load_library
+
+GDN_ACT_NONE, GDN_ACT_SILU, GDN_ACT_GELU = 0, 1, 2
+_ACTS = {"none": GDN_ACT_NONE, "silu": GDN_ACT_SILU, "gelu": GDN_ACT_GELU}
+_SCAN_TILE = 16   # steps between the scan's checkpoints
+
+_VP, _SZ, _LL, _I = ctypes.c_void_p, ctypes.c_size_t, ctypes.c_longlong, ctypes.c_int
+
+
+class GdnConvShape(ctypes.Structure):
+    _fields_ = [("B", _I), ("T", _I), ("C", _I), ("W", _I), ("act", _I), ("dtype", _I), ("ldx", _LL)]
+
+
+class GdnScanShape(ctypes.Structure):
+    _fields_ = [("B", _I), ("T", _I), ("C", _I), ("N", _I), ("G", _I), ("dtype", _I), ("ldu", _LL), ("lddt", _LL),
+                ("ldz", _LL), ("ldB", _LL), ("ldC", _LL)]
+
+
+class GdnNormShape(ctypes.Structure):
+    _fields_ = [("M", _I), ("G", _I), ("D", _I), ("act", _I), ("center", _I), ("dtype", _I), ("eps", ctypes.c_float),
+                ("ldx", _LL), ("ldz", _LL)]
+
+
+class GdnLinearShape(ctypes.Structure):
+    _fields_ = [("M", _I), ("N", _I), ("K", _I), ("act", _I), ("dtype", _I), ("ldx", _LL), ("ldw", _LL), ("ldres", _LL)]
+
+
+_declared = None
+
+
+def _library():
+    """libgdn.so with the signatures of the layer operators declared."""
+    global _declared
+    lib = load_library()
+    if _declared is lib:
+        return lib
+    P = ctypes.POINTER
+    for name, shape, args in (
+            ("gdn_conv_fwd", GdnConvShape, [_VP] * 8), ("gdn_conv_bwd", GdnConvShape, [_VP] * 12 + [_SZ, _VP]),
+            ("gdn_scan_fwd", GdnScanShape, [_VP] * 13 + [_SZ, _VP, _SZ, _VP]),
+            ("gdn_scan_bwd", GdnScanShape, [_VP] * 10 + [_SZ] + [_VP] * 12 + [_SZ, _VP]),
+            ("gdn_norm_fwd", GdnNormShape, [_VP] * 7), ("gdn_norm_bwd", GdnNormShape, [_VP] * 11 + [_SZ, _VP]),
+            ("gdn_linear_fwd", GdnLinearShape, [_VP] * 7 + [_SZ, _VP]),
+            ("gdn_linear_bwd", GdnLinearShape, [_VP] * 8 + [_SZ, _VP])):
+        f = getattr(lib, name)
+        f.restype, f.argtypes = ctypes.c_int, [P(shape)] + args
+    for name, shape in (("gdn_conv_bwd_workspace_bytes", GdnConvShape), ("gdn_scan_ckpt_bytes", GdnScanShape),
+                        ("gdn_scan_fwd_workspace_bytes", GdnScanShape), ("gdn_scan_bwd_workspace_bytes", GdnScanShape),
+                        ("gdn_norm_bwd_workspace_bytes", GdnNormShape),
+                        ("gdn_linear_fwd_workspace_bytes", GdnLinearShape),
+                        ("gdn_linear_bwd_workspace_bytes", GdnLinearShape)):
+        f = getattr(lib, name)
+        f.restype, f.argtypes = ctypes.c_size_t, [P(shape)]
+    _declared = lib
+    return lib
+
+
+def _act(act):
+    try:
+        return _ACTS[act]
+    except KeyError:
+        raise ValueError(f"act is {act!r}, expected one of {sorted(_ACTS)}") from None
+
+
+def _at(t):
+    return None if t is None else t.data_ptr()
+
+
+def _stream_of(stream, device):
+    return (stream if stream is not None else _torch().cuda.current_stream(device)).cuda_stream
+
+
+def _optional(name, t, shape, dtype, device):
+    if t is not None:
+        _check(name, t, shape, dtype, device)
+
+
+def _rows(name, t, shape, dtype, device, inner=1):
+    """Row stride (0: packed) of a tensor whose last `inner` dimensions are packed and whose leading
+    ones follow each other at one stride, as a slice of a contiguous tensor along its last dimension."""
+    if tuple(t.shape) != tuple(shape):
+        raise ValueError(f"{name} has shape {tuple(t.shape)}, expected {tuple(shape)}")
+    if t.dtype != dtype:
+        raise TypeError(f"{name} has dtype {t.dtype}, expected {dtype}")
+    if t.device != device:
+        raise ValueError(f"{name} is on {t.device}, expected {device}")
+    if t.is_contiguous():
+        return 0
+    width, packed = 1, True
+    for size, stride in zip(reversed(t.shape[-inner:]), reversed(t.stride()[-inner:])):
+        packed = packed and (size == 1 or stride == width)
+        width *= size
+    ld, rows = None, 1
+    for size, stride in zip(reversed(t.shape[:-inner]), reversed(t.stride()[:-inner])):
+        if size == 1:
+            continue
+        if ld is None and stride % rows == 0:
+            ld = stride // rows
+        packed = packed and ld is not None and stride == ld * rows
+        rows *= size
+    if not packed or (ld is not None and ld < width):
+        raise ValueError(f"{name} must be contiguous, or a slice of a contiguous tensor along its last dimension")
+    return 0 if ld is None else ld
+
+
+def _scratch(name, t, need, device):
+    """The caller's buffer, checked, or a new one for this call (None where nothing is needed)."""
+    if t is None:
+        return _torch().empty(need, dtype=_torch().uint8, device=device) if need else None
+    if t.device != device or not t.is_contiguous():
+        raise ValueError(f"{name} must be a contiguous tensor on {device}")
+    return t
+
+
+def _size(t):
+    return 0 if t is None else t.numel() * t.element_size()
+
+
+def _run(name, lib, shape, *args):
+    rc = getattr(lib, name)(ctypes.byref(shape), *args)
+    if rc != GDN_OK:
+        raise GdnError(name, rc, lib)
+
+
+def _check_lens(lens, B, dev):
+    if lens is not None:
+        _check("lens", lens, (B,), _torch().int32, dev)
+
+
+# ------------------------------------------------------------------- short causal convolution
+def _conv_args(x, w, bias, s0, lens, act):
+    torch = _torch()
+    B, T, C = x.shape
+    W = w.shape[-1]
+    dev, dt = x.device, x.dtype
+    ld = _rows("x", x, (B, T, C), dt, dev)
+    _check("w", w, (C, W), torch.float32, dev)
+    _optional("bias", bias, (C,), torch.float32, dev)
+    _optional("s0", s0, (B, W - 1, C), dt, dev)
+    _check_lens(lens, B, dev)
+    return GdnConvShape(B, T, C, W, _act(act), _dtype_code(x), ld)
+
+
+def gdn_conv_fwd(x, w, bias=None, s0=None, lens=None, *, act="silu", y=None, s_T=None, want_s_T=True, stream=None):
+    """y, s_T = gdn_conv_fwd(x, w[, bias, s0, lens]) on CUDA tensors (see include/gdn.h): the short
+    causal convolution of x [B, T, C] with taps w [C, W] and an activation ("silu" or "none"); s0 and
+    s_T [B, W-1, C] are the carried inputs (with T = 1, s_T may be s0: updated in place)."""
+    torch = _torch()
+    lib = _library()
+    shape = _conv_args(x, w, bias, s0, lens, act)
+    B, T, C, W, dev, dt = shape.B, shape.T, shape.C, shape.W, x.device, x.dtype
+    _optional("y", y, (B, T, C), dt, dev)
+    _optional("s_T", s_T, (B, W - 1, C), dt, dev)
+    _require_cuda(x)
+    if y is None:
+        y = torch.empty((B, T, C), dtype=dt, device=dev)
+    if s_T is None and want_s_T:
+        s_T = torch.empty((B, W - 1, C), dtype=dt, device=dev)
+    _run("gdn_conv_fwd", lib, shape, _at(x), _at(w), _at(bias), _at(s0), _at(lens), _at(y), _at(s_T), _stream_of(stream, dev))
+    return y, s_T
+
+
+def gdn_conv_bwd_workspace_bytes(shape: GdnConvShape) -> int:
+    return _library().gdn_conv_bwd_workspace_bytes(ctypes.byref(shape))
+
+
+def gdn_conv_bwd(x, w, dy, bias=None, s0=None, lens=None, ds_T=None, *, act="silu", workspace=None, want_ds0=True, stream=None):
+    """dict(dx, dw, dbias, ds0) = gdn_conv_bwd(x, w, dy, ...) for the inputs of gdn_conv_fwd; dw and
+    dbias are float32. ds0 is None with want_ds0=False."""
+    torch = _torch()
+    lib = _library()
+    shape = _conv_args(x, w, bias, s0, lens, act)
+    B, T, C, W, dev, dt = shape.B, shape.T, shape.C, shape.W, x.device, x.dtype
+    _check("dy", dy, (B, T, C), dt, dev)
+    _optional("ds_T", ds_T, (B, W - 1, C), dt, dev)
+    _require_cuda(x)
+    workspace = _scratch("workspace", workspace, lib.gdn_conv_bwd_workspace_bytes(ctypes.byref(shape)), dev)
+    out = {"dx": torch.empty((B, T, C), dtype=dt, device=dev), "dw": torch.empty((C, W), dtype=torch.float32, device=dev),
+           "dbias": torch.empty((C,), dtype=torch.float32, device=dev),
+           "ds0": torch.empty((B, W - 1, C), dtype=dt, device=dev) if want_ds0 else None}
+    _run("gdn_conv_bwd", lib, shape, _at(x), _at(w), _at(bias), _at(s0), _at(lens), _at(dy), _at(ds_T), _at(out["dx"]),
+         _at(out["dw"]), _at(out["dbias"]), _at(out["ds0"]), _at(workspace), _size(workspace), _stream_of(stream, dev))
+    return out
+
+
+# ------------------------------------------------------------------ selective state space scan
+def _scan_args(u, dt, A_log, B, C, D, dt_bias, z, lens):
+    torch = _torch()
+    Bn, T, Cn = u.shape
+    G, N = B.shape[-2:]
+    dev, ty = u.device, u.dtype
+    ldu, lddt = _rows("u", u, (Bn, T, Cn), ty, dev), _rows("dt", dt, (Bn, T, Cn), ty, dev)
+    ldz = 0 if z is None else _rows("z", z, (Bn, T, Cn), ty, dev)
+    ldB, ldC = _rows("B", B, (Bn, T, G, N), ty, dev, 2), _rows("C", C, (Bn, T, G, N), ty, dev, 2)
+    _check("A_log", A_log, (Cn, N), torch.float32, dev)
+    _optional("D", D, (Cn,), torch.float32, dev)
+    _optional("dt_bias", dt_bias, (Cn,), torch.float32, dev)
+    _check_lens(lens, Bn, dev)
+    return GdnScanShape(Bn, T, Cn, N, G, _dtype_code(u), ldu, lddt, ldz, ldB, ldC)
+
+
+def gdn_scan_ckpt_bytes(shape: GdnScanShape) -> int:
+    return _library().gdn_scan_ckpt_bytes(ctypes.byref(shape))
+
+
+def gdn_scan_fwd_workspace_bytes(shape: GdnScanShape) -> int:
+    return _library().gdn_scan_fwd_workspace_bytes(ctypes.byref(shape))
+
+
+def gdn_scan_bwd_workspace_bytes(shape: GdnScanShape) -> int:
+    return _library().gdn_scan_bwd_workspace_bytes(ctypes.byref(shape))
+
+
+def _scan_ckpt_shape(Bn, T, Cn, N):
+    return (Bn, -(-T // _SCAN_TILE), Cn, N)
+
+
+def gdn_scan_fwd(u, dt, A_log, B, C, D=None, dt_bias=None, z=None, h0=None, lens=None, *, y=None, h_T=None, ckpt=None,
+                 workspace=None, want_h_T=True, want_ckpt=False, stream=None):
+    """y, h_T, ckpt = gdn_scan_fwd(u, dt, A_log, B, C, ...) on CUDA tensors (see include/gdn.h): the
+    selective state space scan of u [B, T, C] with steps dt, state inputs and outputs B, C [B, T, G, N]
+    and gate z. ckpt [B, ceil(T / 16), C, N] (want_ckpt=True) is what gdn_scan_bwd needs. With T = 1
+    and no ckpt, h_T may be h0: the state updated in place."""
+    torch = _torch()
+    lib = _library()
+    shape = _scan_args(u, dt, A_log, B, C, D, dt_bias, z, lens)
+    Bn, T, Cn, N, dev = shape.B, shape.T, shape.C, shape.N, u.device
+    _optional("h0", h0, (Bn, Cn, N), torch.float32, dev)
+    _optional("y", y, (Bn, T, Cn), u.dtype, dev)
+    _optional("h_T", h_T, (Bn, Cn, N), torch.float32, dev)
+    _optional("ckpt", ckpt, _scan_ckpt_shape(Bn, T, Cn, N), torch.float32, dev)
+    _require_cuda(u)
+    if y is None:
+        y = torch.empty((Bn, T, Cn), dtype=u.dtype, device=dev)
+    if h_T is None and want_h_T:
+        h_T = torch.empty((Bn, Cn, N), dtype=torch.float32, device=dev)
+    if ckpt is None and want_ckpt:
+        ckpt = torch.empty(_scan_ckpt_shape(Bn, T, Cn, N), dtype=torch.float32, device=dev)
+    workspace = _scratch("workspace", workspace, 0 if T == 1 else lib.gdn_scan_fwd_workspace_bytes(ctypes.byref(shape)), dev)
+    _run("gdn_scan_fwd", lib, shape, _at(u), _at(dt), _at(A_log), _at(B), _at(C), _at(D), _at(dt_bias), _at(z), _at(h0),
+         _at(lens), _at(y), _at(h_T), _at(ckpt), _size(ckpt), _at(workspace), _size(workspace), _stream_of(stream, dev))
+    return y, h_T, ckpt
+
+
+def gdn_scan_bwd(u, dt, A_log, B, C, ckpt, dy, D=None, dt_bias=None, z=None, lens=None, dh_T=None, *, workspace=None,
+                 want_dh0=True, stream=None):
+    """dict(du, ddt, dA_log, dB, dC, dD, ddt_bias, dz, dh0) = gdn_scan_bwd(...) for the inputs and the
+    ckpt of gdn_scan_fwd. dD, ddt_bias and dz are None where their input was, dh0 with want_dh0=False."""
+    torch = _torch()
+    lib = _library()
+    shape = _scan_args(u, dt, A_log, B, C, D, dt_bias, z, lens)
+    Bn, T, Cn, N, G, dev, ty = shape.B, shape.T, shape.C, shape.N, shape.G, u.device, u.dtype
+    _check("ckpt", ckpt, _scan_ckpt_shape(Bn, T, Cn, N), torch.float32, dev)
+    _check("dy", dy, (Bn, T, Cn), ty, dev)
+    _optional("dh_T", dh_T, (Bn, Cn, N), torch.float32, dev)
+    _require_cuda(u)
+    workspace = _scratch("workspace", workspace, lib.gdn_scan_bwd_workspace_bytes(ctypes.byref(shape)), dev)
+    wide = lambda: torch.empty((Bn, T, Cn), dtype=ty, device=dev)  # noqa: E731
+    vec = lambda t: None if t is None else torch.empty((Cn,), dtype=torch.float32, device=dev)  # noqa: E731
+    out = {"du": wide(), "ddt": wide(), "dA_log": torch.empty((Cn, N), dtype=torch.float32, device=dev),
+           "dB": torch.empty((Bn, T, G, N), dtype=ty, device=dev), "dC": torch.empty((Bn, T, G, N), dtype=ty, device=dev),
+           "dD": vec(D), "ddt_bias": vec(dt_bias), "dz": None if z is None else wide(),
+           "dh0": torch.empty((Bn, Cn, N), dtype=torch.float32, device=dev) if want_dh0 else None}
+    _run("gdn_scan_bwd", lib, shape, _at(u), _at(dt), _at(A_log), _at(B), _at(C), _at(D), _at(dt_bias), _at(z), _at(lens),
+         _at(ckpt), _size(ckpt), _at(dy), _at(dh_T), _at(out["du"]), _at(out["ddt"]), _at(out["dA_log"]), _at(out["dB"]),
+         _at(out["dC"]), _at(out["dD"]), _at(out["ddt_bias"]), _at(out["dz"]), _at(out["dh0"]), _at(workspace),
+         _size(workspace), _stream_of(stream, dev))
+    return out
+
+
+# ---------------------------------------------------------------------------------- group norm
+def _norm_args(x, groups, w, b, z, act, eps, center):
+    torch = _torch()
+    dev, dt = x.device, x.dtype
+    C = x.shape[-1]
+    if groups < 1 or C % groups != 0:
+        raise ValueError(f"{C} channels do not split into {groups} groups")
+    rows = x.numel() // max(C, 1)
+    ldx = _rows("x", x, x.shape, dt, dev)
+    ldz = 0 if z is None else _rows("z", z, x.shape, dt, dev)
+    _optional("w", w, (C,), torch.float32, dev)
+    _optional("b", b, (C,), torch.float32, dev)
+    return GdnNormShape(rows, groups, C // groups, _act(act), 1 if center else 0, _dtype_code(x), eps, ldx, ldz)
+
+
+def gdn_norm_fwd(x, groups, w=None, b=None, z=None, *, act="silu", eps=1e-5, center=True, y=None, stats=None,
+                 want_stats=True, stream=None):
+    """y, stats = gdn_norm_fwd(x, groups[, w, b, z]) on CUDA tensors (see include/gdn.h): group norm
+    over the channels (last dimension) of every row of x, times w plus b, then the activation, or with
+    a gate z the product with act(z). center=False: root mean square. stats [..., groups, 2] is what
+    gdn_norm_bwd needs."""
+    torch = _torch()
+    lib = _library()
+    shape = _norm_args(x, groups, w, b, z, act, eps, center)
+    dev = x.device
+    stats_shape = tuple(x.shape[:-1]) + (groups, 2)
+    _optional("y", y, x.shape, x.dtype, dev)
+    _optional("stats", stats, stats_shape, torch.float32, dev)
+    _require_cuda(x)
+    if y is None:
+        y = torch.empty(x.shape, dtype=x.dtype, device=dev)
+    if stats is None and want_stats:
+        stats = torch.empty(stats_shape, dtype=torch.float32, device=dev)
+    _run("gdn_norm_fwd", lib, shape, _at(x), _at(w), _at(b), _at(z), _at(y), _at(stats), _stream_of(stream, dev))
+    return y, stats
+
+
+def gdn_norm_bwd_workspace_bytes(shape: GdnNormShape) -> int:
+    return _library().gdn_norm_bwd_workspace_bytes(ctypes.byref(shape))
+
+
+def gdn_norm_bwd(x, groups, stats, dy, w=None, b=None, z=None, *, act="silu", eps=1e-5, center=True, workspace=None,
+                 stream=None):
+    """dict(dx, dw, db, dz) = gdn_norm_bwd(x, groups, stats, dy[, w, b, z]) for the inputs and stats of
+    gdn_norm_fwd; dw, db (float32) and dz are None where their input was."""
+    torch = _torch()
+    lib = _library()
+    shape = _norm_args(x, groups, w, b, z, act, eps, center)
+    dev = x.device
+    _check("stats", stats, tuple(x.shape[:-1]) + (groups, 2), torch.float32, dev)
+    _check("dy", dy, x.shape, x.dtype, dev)
+    _require_cuda(x)
+    workspace = _scratch("workspace", workspace, lib.gdn_norm_bwd_workspace_bytes(ctypes.byref(shape)), dev)
+    like = lambda t: None if t is None else torch.empty(t.shape, dtype=t.dtype, device=dev)  # noqa: E731
+    out = {"dx": like(x), "dw": like(w), "db": like(b), "dz": like(z)}
+    _run("gdn_norm_bwd", lib, shape, _at(x), _at(w), _at(b), _at(z), _at(stats), _at(dy), _at(out["dx"]), _at(out["dw"]),
+         _at(out["db"]), _at(out["dz"]), _at(workspace), _size(workspace), _stream_of(stream, dev))
+    return out
+
+
+# ---------------------------------------------------------------------------------- projection
+def _linear_args(x, W, bias, res, act):
+    dev, dt = x.device, x.dtype
+    lead, K = tuple(x.shape[:-1]), x.shape[-1]
+    N = W.shape[0]
+    M = x.numel() // max(K, 1)
+    ldx, ldw = _rows("x", x, lead + (K,), dt, dev), _rows("W", W, (N, K), dt, dev)
+    _optional("bias", bias, (N,), dt, dev)
+    ldres = 0 if res is None else _rows("res", res, lead + (N,), dt, dev)
+    return GdnLinearShape(M, N, K, _act(act), _dtype_code(x), ldx, ldw, ldres), lead + (N,)
+
+
+def gdn_linear_fwd_workspace_bytes(shape: GdnLinearShape) -> int:
+    return _library().gdn_linear_fwd_workspace_bytes(ctypes.byref(shape))
+
+
+def gdn_linear_bwd_workspace_bytes(shape: GdnLinearShape) -> int:
+    return _library().gdn_linear_bwd_workspace_bytes(ctypes.byref(shape))
+
+
+def gdn_linear_fwd(x, W, bias=None, res=None, *, act="none", y=None, pre=None, want_pre=False, workspace=None, stream=None):
+    """y, pre = gdn_linear_fwd(x, W[, bias, res]) on CUDA tensors (see include/gdn.h):
+    y = act(x W^T + bias) + res for x [..., K] and W [N, K]. pre (want_pre=True) is the
+    pre-activation, which gdn_linear_bwd needs where act is not "none"."""
+    torch = _torch()
+    lib = _library()
+    shape, out_shape = _linear_args(x, W, bias, res, act)
+    dev, dt = x.device, x.dtype
+    _optional("y", y, out_shape, dt, dev)
+    _optional("pre", pre, out_shape, dt, dev)
+    _require_cuda(x)
+    if y is None:
+        y = torch.empty(out_shape, dtype=dt, device=dev)
+    if pre is None and want_pre:
+        pre = torch.empty(out_shape, dtype=dt, device=dev)
+    workspace = _scratch("workspace", workspace, lib.gdn_linear_fwd_workspace_bytes(ctypes.byref(shape)), dev)
+    _run("gdn_linear_fwd", lib, shape, _at(x), _at(W), _at(bias), _at(res), _at(y), _at(pre), _at(workspace),
+         _size(workspace), _stream_of(stream, dev))
+    return y, pre
+
+
+def gdn_linear_bwd(x, W, dy, pre=None, *, act="none", want_dx=True, want_dW=True, want_dbias=True, workspace=None,
+                   stream=None):
+    """dict(dx, dW, dbias) = gdn_linear_bwd(x, W, dy[, pre]) for the inputs of gdn_linear_fwd (the
+    gradient of res is dy itself). An entry is None with its want_... False."""
+    torch = _torch()
+    lib = _library()
+    shape, out_shape = _linear_args(x, W, None, None, act)
+    dev, dt = x.device, x.dtype
+    _check("dy", dy, out_shape, dt, dev)
+    _optional("pre", pre, out_shape, dt, dev)
+    if pre is None and shape.act != GDN_ACT_NONE:
+        raise ValueError("pre is needed: the pre-activation of gdn_linear_fwd (want_pre=True)")
+    _require_cuda(x)
+    workspace = _scratch("workspace", workspace, lib.gdn_linear_bwd_workspace_bytes(ctypes.byref(shape)), dev)
+    out = {"dx": torch.empty(x.shape, dtype=dt, device=dev) if want_dx else None,
+           "dW": torch.empty(W.shape, dtype=dt, device=dev) if want_dW else None,
+           "dbias": torch.empty((W.shape[0],), dtype=dt, device=dev) if want_dbias else None}
+    _run("gdn_linear_bwd", lib, shape, _at(x), _at(W), _at(pre), _at(dy), _at(out["dx"]), _at(out["dW"]), _at(out["dbias"]),
+         _at(workspace), _size(workspace), _stream_of(stream, dev))
+    return out

@@ -286,6 +286,150 @@ GDN_API int gdn_gates_bwd(const gdn_shape *shape, const void *a, const void *b, 
                           const float *dt_bias, const void *dg, const void *dbeta, void *da,
                           void *db, float *dA_log, float *ddt_bias, void *stream);
 
+/*
+ * ---- The operators that stand beside the recurrence in a layer: the short causal convolution in
+ * front of it, the selective state space scan (the sibling recurrence of hybrid stacks), the group
+ * norm with its gate behind it, and the projections around it.
+ *
+ * The conventions above hold, with these additions:
+ *   - Inputs that a shape gives a row stride (ldx, ldu, ...: elements from one step, or row, to the
+ *     next; 0 selects the packed width) may be column slices of a wider tensor: the stride between
+ *     batch rows is T times the row stride. Their addresses need only the alignment of their element
+ *     type. Everything else is packed and 16-byte aligned.
+ *   - Parameters that are small (convolution taps, norm weights, A_log, ...) and their gradients are
+ *     float32; arithmetic is float32.
+ *   - lens ([B] int32, may be NULL: every row has T steps; values are clamped to 0..T) gives each
+ *     row's number of valid steps. The steps behind them hold anything, NaN included: they are not
+ *     used, leave the carried state alone, and their outputs and gradients are written as zeros. A
+ *     row of length 0 passes its state through.
+ *   - The buffers of a call may not overlap, except where a call says so.
+ * Sizes: every size at least 1; a tensor of 2^40 elements or more, B or G above 65535, or rows
+ * (B * T, M) of 2^31 or more are GDN_ERR_UNSUPPORTED_SHAPE.
+ */
+typedef enum {
+    GDN_ACT_NONE = 0, /* x */
+    GDN_ACT_SILU = 1, /* x / (1 + exp(-x)) */
+    GDN_ACT_GELU = 2  /* x Phi(x), Phi the normal distribution function */
+} gdn_act;
+
+/*
+ * Short causal convolution over the steps, each channel by itself:
+ *     pre[b,t,c] = bias[c] + sum_{j < W} w[c,j] x[b, t-W+1+j, c],     y = act(pre)
+ * where x before step 0 is the carried state s0 (the W-1 inputs before the first step, oldest
+ * first; zeros if NULL). s_T is the state behind the last valid step.
+ *   x [B,T,C] (dtype, ldx)   w [C,W] float32   bias [C] float32 or NULL   y, dy, dx [B,T,C] (dtype)
+ *   s0, s_T, ds_T, ds0 [B,W-1,C] (dtype), each may be NULL
+ * W is 1 to 4 (else GDN_ERR_UNSUPPORTED_SHAPE); act none or SiLU. With T = 1 s_T may be s0 itself
+ * (the state updated in place). The backward returns dx, dw [C,W], dbias [C] (float32; NULL: not
+ * written) and ds0 for the cotangents dy and ds_T, computing pre again from x; its workspace of
+ * gdn_conv_bwd_workspace_bytes(shape) bytes holds partial sums of dw and dbias.
+ */
+typedef struct {
+    int B, T, C, W; /* batch rows, steps, channels, taps */
+    int act;        /* a gdn_act */
+    int dtype;      /* a gdn_dtype */
+    long long ldx;  /* elements between steps of x, 0: C */
+} gdn_conv_shape;
+
+GDN_API int gdn_conv_fwd(const gdn_conv_shape *shape, const void *x, const float *w, const float *bias,
+                         const void *s0, const int *lens, void *y, void *s_T, void *stream);
+GDN_API size_t gdn_conv_bwd_workspace_bytes(const gdn_conv_shape *shape);
+GDN_API int gdn_conv_bwd(const gdn_conv_shape *shape, const void *x, const float *w, const float *bias,
+                         const void *s0, const int *lens, const void *dy, const void *ds_T, void *dx, float *dw,
+                         float *dbias, void *ds0, void *workspace, size_t workspace_bytes, void *stream);
+
+/*
+ * Selective state space scan. For every channel c (of group g = c / (C / G)) and state n:
+ *     d = softplus(dt[b,t,c] + dt_bias[c]),   A = -exp(A_log[c,n])
+ *     h_t = exp(d A) h_{t-1} + d u[b,t,c] B[b,t,g,n]
+ *     core = sum_n C[b,t,g,n] h_t + D[c] u[b,t,c],     y = core * silu(z[b,t,c])   (z NULL: y = core)
+ *   u, dt, z, y, dy, du, ddt, dz [B,T,C] (dtype; u, dt, z with row strides)
+ *   B, C, dB, dC [B,T,G,N] (dtype; B, C with row strides)
+ *   A_log [C,N], D [C] (NULL: zeros), dt_bias [C] (NULL: zeros), float32, and their gradients
+ *   h0, h_T, dh_T, dh0 [B,C,N] float32, each may be NULL (h0, dh_T: zeros); h_T may be h0 with T = 1
+ * N is 1 to 64, C a multiple of G (else GDN_ERR_UNSUPPORTED_SHAPE).
+ *   ckpt       gdn_scan_ckpt_bytes(shape) bytes, written by the forward (NULL: nothing saved) and
+ *              read by the backward for the same inputs: the state at the start of every 16 steps,
+ *              [B, ceil(T / 16), C, N] float32.
+ *   workspace  gdn_scan_fwd_workspace_bytes / gdn_scan_bwd_workspace_bytes bytes (0: may be NULL).
+ * The backward returns du, ddt, dB, dC, dA_log and, where the pointers are not NULL, dD, ddt_bias,
+ * dz, dh0 (dz needs z).
+ */
+typedef struct {
+    int B, T, C, N, G; /* batch rows, steps, channels, states per channel, groups of B and C */
+    int dtype;         /* a gdn_dtype */
+    long long ldu, lddt, ldz; /* elements between steps, 0: C */
+    long long ldB, ldC;       /* elements between steps, 0: G * N */
+} gdn_scan_shape;
+
+GDN_API size_t gdn_scan_ckpt_bytes(const gdn_scan_shape *shape);
+GDN_API size_t gdn_scan_fwd_workspace_bytes(const gdn_scan_shape *shape);
+GDN_API size_t gdn_scan_bwd_workspace_bytes(const gdn_scan_shape *shape);
+GDN_API int gdn_scan_fwd(const gdn_scan_shape *shape, const void *u, const void *dt, const float *A_log,
+                         const void *B, const void *C, const float *D, const float *dt_bias, const void *z,
+                         const float *h0, const int *lens, void *y, float *h_T, float *ckpt, size_t ckpt_bytes,
+                         void *workspace, size_t workspace_bytes, void *stream);
+GDN_API int gdn_scan_bwd(const gdn_scan_shape *shape, const void *u, const void *dt, const float *A_log,
+                         const void *B, const void *C, const float *D, const float *dt_bias, const void *z,
+                         const int *lens, const float *ckpt, size_t ckpt_bytes, const void *dy, const float *dh_T,
+                         void *du, void *ddt, float *dA_log, void *dB, void *dC, float *dD, float *ddt_bias,
+                         void *dz, float *dh0, void *workspace, size_t workspace_bytes, void *stream);
+
+/*
+ * Group norm over the channels of each row (channels last; the statistics of a row do not reach
+ * into other rows, so that a causal layer stays causal), with an activation or a gate. Row m's
+ * channels are G groups of D:
+ *     center != 0:  xh = (x - mean) / sqrt(var + eps)    (mean and biased variance of the group)
+ *     center == 0:  xh = x / sqrt(mean(x^2) + eps)
+ *     aff = xh w + b,     y = act(aff)   (z NULL)   or   y = aff act(z)
+ *   x, z, y, dy, dx, dz [M,G,D] (dtype; x, z with row strides)   w, b [G,D] float32 or NULL (1, 0)
+ *   stats [M,G,2] float32 or NULL: mean and 1 / sqrt(var + eps), for the backward
+ * eps > 0 and finite. D is 1 to 65536. The backward returns dx and, where the pointers are not
+ * NULL, dw, db (float32) and dz (needs z); its workspace holds partial sums of dw and db.
+ */
+typedef struct {
+    int M, G, D;   /* rows, groups, channels of a group */
+    int act;       /* a gdn_act */
+    int center;    /* 0: root mean square, else mean and variance */
+    int dtype;     /* a gdn_dtype */
+    float eps;
+    long long ldx, ldz; /* elements between rows, 0: G * D */
+} gdn_norm_shape;
+
+GDN_API int gdn_norm_fwd(const gdn_norm_shape *shape, const void *x, const float *w, const float *b, const void *z,
+                         void *y, float *stats, void *stream);
+GDN_API size_t gdn_norm_bwd_workspace_bytes(const gdn_norm_shape *shape);
+GDN_API int gdn_norm_bwd(const gdn_norm_shape *shape, const void *x, const float *w, const float *b, const void *z,
+                         const float *stats, const void *dy, void *dx, float *dw, float *db, void *dz,
+                         void *workspace, size_t workspace_bytes, void *stream);
+
+/*
+ * Matrix product with bias, activation and residual:
+ *     pre = x W^T + bias,     y = act(pre) + res
+ *   x [M,K], W [N,K], res [M,N] (dtype, row strides; res may be NULL)   bias [N] (dtype) or NULL
+ *   y [M,N] (dtype)   pre [M,N] (dtype) or NULL: the pre-activation, for the backward
+ * The backward, for the cotangent dy [M,N] (dtype): dpre = dy act'(pre) (pre is needed unless act
+ * is none), dx = dpre W, dW = dpre^T x, dbias = sum over rows of dpre, each in dtype and each
+ * computed where its pointer is not NULL. The gradient of res is dy itself.
+ * workspace: gdn_linear_fwd_workspace_bytes / gdn_linear_bwd_workspace_bytes bytes (0: may be NULL).
+ */
+typedef struct {
+    int M, N, K;  /* rows, outputs, inputs */
+    int act;      /* a gdn_act */
+    int dtype;    /* a gdn_dtype */
+    long long ldx, ldw; /* elements between rows of x and of W, 0: K */
+    long long ldres;    /* elements between rows of res, 0: N */
+} gdn_linear_shape;
+
+GDN_API size_t gdn_linear_fwd_workspace_bytes(const gdn_linear_shape *shape);
+GDN_API size_t gdn_linear_bwd_workspace_bytes(const gdn_linear_shape *shape);
+GDN_API int gdn_linear_fwd(const gdn_linear_shape *shape, const void *x, const void *W, const void *bias,
+                           const void *res, void *y, void *pre, void *workspace, size_t workspace_bytes,
+                           void *stream);
+GDN_API int gdn_linear_bwd(const gdn_linear_shape *shape, const void *x, const void *W, const void *pre,
+                           const void *dy, void *dx, void *dW, void *dbias, void *workspace,
+                           size_t workspace_bytes, void *stream);
+
 /* Static description of a return code. */
 GDN_API const char *gdn_strerror(int code);
 

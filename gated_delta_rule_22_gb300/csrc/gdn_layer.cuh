@@ -13,10 +13,11 @@ enum { kActNone = 0, kActSilu = 1, kActGelu = 2 };
 void api_clear_error();
 int api_cuda_status(cudaError_t e);
 int api_device_status_address(int **out);
-// 2-D tensor map of a row-major [rows][cols] array with `ld` elements between rows, box
-// {box_cols, box_rows}, 128-byte swizzle; what lies outside the array reads as zero.
-int api_rows_map(CUtensorMap *map, const void *ptr, bool bf16, uint64_t rows, uint64_t cols, uint64_t ld, int box_cols,
-                 int box_rows);
+// 3-D tensor map of `planes` row-major bf16 [rows][cols] arrays with `ld` elements between rows
+// (planes rows * ld apart), box {box_cols, box_rows, 1}, 128-byte swizzle; what lies outside an array
+// reads as zero.
+int api_planes_map(CUtensorMap *map, const void *ptr, uint64_t cols, uint64_t rows, uint64_t planes, uint64_t ld, int box_cols,
+                   int box_rows);
 
 // ---- parameter blocks
 struct ConvParams {

@@ -131,6 +131,12 @@ int linear_plan(const gdn_linear_shape *s, gdn::LinearParams *p) {
     return GDN_OK;
 }
 
+// x and W with packed rows are read in place, so they are 16-byte aligned like every packed tensor.
+int linear_operands_ok(const gdn::LinearParams &p, const void *x, const void *W) {
+    if ((p.ldx == p.K && !aligned16(x)) || (p.ldw == p.K && !aligned16(W))) return GDN_ERR_MISALIGNED;
+    return GDN_OK;
+}
+
 }  // namespace
 
 extern "C" {
@@ -283,7 +289,8 @@ int gdn_linear_fwd(const gdn_linear_shape *shape, const void *x, const void *W, 
     if (rc != GDN_OK) return rc;
     const size_t need = gdn::linear_fwd_workspace(p, shape->dtype);
     if (!x || !W || !y || (need > 0 && !workspace)) return GDN_ERR_INVALID_ARG;
-    if ((rc = packed_ok({bias, y, pre, workspace})) != GDN_OK || (rc = strided_ok({x, W, res}, elem(shape->dtype))) != GDN_OK)
+    if ((rc = packed_ok({bias, y, pre, workspace})) != GDN_OK || (rc = strided_ok({x, W, res}, elem(shape->dtype))) != GDN_OK ||
+        (rc = linear_operands_ok(p, x, W)) != GDN_OK)
         return rc;
     if (workspace_bytes < need) return GDN_ERR_WORKSPACE_TOO_SMALL;
     gdn::api_clear_error();
@@ -299,7 +306,8 @@ int gdn_linear_bwd(const gdn_linear_shape *shape, const void *x, const void *W, 
     if (rc != GDN_OK) return rc;
     const size_t need = gdn::linear_bwd_workspace(p, shape->dtype);
     if (!x || !W || !dy || (need > 0 && !workspace) || (shape->act != GDN_ACT_NONE && !pre)) return GDN_ERR_INVALID_ARG;
-    if ((rc = packed_ok({pre, dy, dx, dW, dbias, workspace})) != GDN_OK || (rc = strided_ok({x, W}, elem(shape->dtype))) != GDN_OK)
+    if ((rc = packed_ok({pre, dy, dx, dW, dbias, workspace})) != GDN_OK || (rc = strided_ok({x, W}, elem(shape->dtype))) != GDN_OK ||
+        (rc = linear_operands_ok(p, x, W)) != GDN_OK)
         return rc;
     if (workspace_bytes < need) return GDN_ERR_WORKSPACE_TOO_SMALL;
     gdn::api_clear_error();

@@ -1,17 +1,63 @@
-// gdn_linear.cu -- matrix product with bias, activation and residual, and its gradients.
+// gdn_linear.cu -- matrix product with bias, activation and residual, and its gradients, on the
+// tcgen05 tensor cores.
 //
 //     pre = x W^T + bias,  y = act(pre) + res
 //     dpre = dy act'(pre),  dx = dpre W,  dW = dpre^T x,  dbias = sum_m dpre
+//
+// All three products are D[m][n] = sum_k A(m, k) B(n, k) with each operand either K-major (its rows
+// are m or n, as x, W in the forward) or MN-major (its rows are k, as W in dx, dpre and x in dW):
+// the tensor cores read both from what one TMA box puts into shared memory, so that nothing is
+// transposed in memory.
+//
+// float32 operands are held as three bf16 terms of 8 bits each (x = x0 + x1 + x2 to 24 bits); six of
+// the nine products of terms are summed, smallest first, by walking K once per product: the dropped
+// ones are below 2^-24 of the result. Six bf16 products cost about a quarter of the time of float32
+// arithmetic on the CUDA cores.
 #include "gdn_layer.cuh"
+#include "gdn_umma.cuh"
 
 namespace gdn {
 
 namespace {
 
-constexpr int kTile = 64, kDepth = 16;
+constexpr int kBM = 128, kBK = 64, kMaxBN = 256, kStages = 4;
+constexpr int kEpiWarps = 8, kGemmThreads = 64 + 32 * kEpiWarps;
+constexpr int kEpiPitch = 20;                       // floats per staged row of 16 columns
+constexpr int kStageBytes = (kBM + kMaxBN) * kBK * 2;
+constexpr size_t kGemmSmem = 1024 + (size_t)kStages * kStageBytes + kEpiWarps * 32 * kEpiPitch * 4 + 256;
 constexpr int kBiasSlices = 64;
+constexpr int kSms = 152;
 
 size_t up256(size_t n) { return (n + 255) / 256 * 256; }
+int up8(int n) { return (n + 7) / 8 * 8; }
+
+// The six products of the float32 terms (A's, B's), smallest first; bf16 has the last alone.
+__constant__ signed char kTermA[6] = {0, 2, 1, 0, 1, 0}, kTermB[6] = {2, 0, 1, 1, 0, 0};
+
+struct GemmParams {
+    const void *bias, *res;
+    void *out, *pre;
+    int *status;
+    long long ldres;
+    int M, N, kblocks, terms, act;
+    int BN, mt, nt, panel;      // tile columns, tiles along m and n, n tiles walked together
+    int vec;                    // 16-byte accesses of out, pre and res are aligned
+};
+
+__device__ __forceinline__ void tma_load_3d(void *dst, const CUtensorMap *map, uint64_t *bar, int c0, int c1, int c2) {
+    asm volatile(
+        "cp.async.bulk.tensor.3d.shared::cluster.global.mbarrier::complete_tx::bytes [%0], [%1, {%2, %3, %4}], [%5];" ::"r"(
+            smem_addr(dst)),
+        "l"(reinterpret_cast<uint64_t>(map)), "r"(c0), "r"(c1), "r"(c2), "r"(smem_addr(bar))
+        : "memory");
+}
+
+// 128-byte swizzled operand descriptors. K-major: rows of 64 K elements, 8-row atoms 1024 bytes
+// apart. MN-major: rows are K, 64 M/N elements wide; 8-row atoms 1024 bytes apart along K, the next
+// 64 M/N elements 64 rows (8192 bytes) further.
+__device__ __forceinline__ uint64_t sw128_desc(uint32_t start, bool mn) {
+    return umma_sdesc(start, mn ? 8192u : 16u, 1024u) | (uint64_t)2 << 61;
+}
 
 __device__ __forceinline__ float act_rt(int act, float x) {
     return act == kActSilu ? silu_hw(x) : act == kActGelu ? gelu_f(x) : x;
@@ -20,64 +66,241 @@ __device__ __forceinline__ float dact_rt(int act, float x) {
     return act == kActSilu ? dsilu_hw(x) : act == kActGelu ? dgelu_f(x) : 1.f;
 }
 
-// One operand: element (r, k) at p[r * rs + k * cs].
-template <typename T>
-struct Operand {
-    const T *p;
-    long long rs, cs;
-};
+// Tile t of the grid: panels of `panel` tile columns, within one the columns first.
+__device__ __forceinline__ void tile_at(const GemmParams &p, int t, int &m0, int &n0) {
+    const int per = p.panel * p.mt, q = t / per, r = t % per, w = min(p.panel, p.nt - q * p.panel);
+    m0 = r / w * kBM;
+    n0 = (q * p.panel + r % w) * p.BN;
+}
 
 }  // namespace
 
-// out[m][n] = act(sum_k A[m][k] B[n][k] + bias[n]) + res[m][n]
-template <typename T>
-__global__ void __launch_bounds__(256) linear_simple_kernel(Operand<T> A, Operand<T> B, int M, int N, int K, const T *bias,
-                                                            int act, const T *res, long long ldres, T *out, T *pre) {
-    __shared__ float sa[kDepth][kTile + 1], sb[kDepth][kTile + 1];
-    const int m0 = blockIdx.y * kTile, n0 = blockIdx.x * kTile, tx = threadIdx.x % 16, ty = threadIdx.x / 16;
-    float acc[4][4] = {};
-    for (int k0 = 0; k0 < K; k0 += kDepth) {
-        for (int e = threadIdx.x; e < kTile * kDepth; e += 256) {
-            const int r = e / kDepth, k = e % kDepth;
-            sa[k][r] = m0 + r < M && k0 + k < K ? to_f32(A.p[(m0 + r) * A.rs + (k0 + k) * A.cs]) : 0.f;
-            sb[k][r] = n0 + r < N && k0 + k < K ? to_f32(B.p[(n0 + r) * B.rs + (k0 + k) * B.cs]) : 0.f;
+// Warp 0 fetches the operand tiles (TMA, kStages deep), warp 1 issues the products into one of two
+// accumulators in tensor memory, warps 2-9 turn the other one into output: the epilogue of a tile
+// runs under the products of the next.
+template <bool A_MN, bool B_MN, typename T>
+__global__ void __launch_bounds__(kGemmThreads, 1)
+gemm_kernel(const __grid_constant__ CUtensorMap tmA, const __grid_constant__ CUtensorMap tmB, const GemmParams p) {
+    extern __shared__ unsigned char smem_raw[];
+    unsigned char *smem = reinterpret_cast<unsigned char *>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~(uintptr_t)1023);
+    float *stage_out = reinterpret_cast<float *>(smem + kStages * kStageBytes);
+    uint64_t *bars = reinterpret_cast<uint64_t *>(stage_out + kEpiWarps * 32 * kEpiPitch);
+    uint64_t *full = bars, *empty = bars + kStages, *acc_full = bars + 2 * kStages, *acc_empty = acc_full + 2;
+    uint32_t *tmem_slot = reinterpret_cast<uint32_t *>(acc_empty + 2);
+    const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+    if (threadIdx.x == 0) {
+        for (int i = 0; i < kStages; ++i) {
+            mbar_init(full + i, 1);
+            mbar_init(empty + i, 1);
         }
-        __syncthreads();
-#pragma unroll
-        for (int k = 0; k < kDepth; ++k) {
-            float a[4], b[4];
-#pragma unroll
-            for (int i = 0; i < 4; ++i) {
-                a[i] = sa[k][ty + 16 * i];
-                b[i] = sb[k][tx + 16 * i];
-            }
-#pragma unroll
-            for (int i = 0; i < 4; ++i)
-#pragma unroll
-                for (int j = 0; j < 4; ++j) acc[i][j] = fmaf(a[i], b[j], acc[i][j]);
+        for (int i = 0; i < 2; ++i) {
+            mbar_init(acc_full + i, 1);
+            mbar_init(acc_empty + i, kEpiWarps);
         }
-        __syncthreads();
+        fence_mbar_init();
+        tma_prefetch_map(&tmA);
+        tma_prefetch_map(&tmB);
     }
-    for (int i = 0; i < 4; ++i)
-        for (int j = 0; j < 4; ++j) {
-            const int m = m0 + ty + 16 * i, n = n0 + tx + 16 * j;
-            if (m >= M || n >= N) continue;
-            const float v = acc[i][j] + (bias != nullptr ? to_f32(bias[n]) : 0.f);
-            if (pre != nullptr) pre[(size_t)m * N + n] = from_f32<T>(v);
-            out[(size_t)m * N + n] = from_f32<T>(__fadd_rn(act_rt(act, v), res != nullptr ? to_f32(res[m * ldres + n]) : 0.f));
+    if (warp == 1) tmem_alloc(tmem_slot, 512);
+    tc_fence_before();
+    __syncthreads();
+    tc_fence_after();
+    const uint32_t tmem = *tmem_slot;
+    const int tiles = p.mt * p.nt, steps = p.kblocks * p.terms;
+    if (warp == 0) {
+        uint32_t it = 0;
+        bool ok = true;
+        if (lane == 0) {
+            for (int t = blockIdx.x; t < tiles && ok; t += gridDim.x) {
+                int m0, n0;
+                tile_at(p, t, m0, n0);
+                for (int s = 0; s < steps; ++s, ++it) {
+                    const int st = it % kStages, k0 = s % p.kblocks * kBK, term = 6 - p.terms + s / p.kblocks;
+                    if (!(ok = mbar_wait(empty + st, (it / kStages & 1) ^ 1))) {
+                        report_status(p.status, kStatusTimeout);
+                        break;
+                    }
+                    unsigned char *a = smem + st * kStageBytes, *b = a + kBM * kBK * 2;
+                    mbar_expect_tx(full + st, (kBM + p.BN) * kBK * 2);
+                    const int ta = kTermA[term], tb = kTermB[term];
+                    if (A_MN) {
+#pragma unroll
+                        for (int i = 0; i < kBM / 64; ++i) tma_load_3d(a + i * 8192, &tmA, full + st, m0 + 64 * i, k0, ta);
+                    } else {
+                        tma_load_3d(a, &tmA, full + st, k0, m0, ta);
+                    }
+                    if (B_MN) {
+                        for (int i = 0; i < p.BN / 64; ++i) tma_load_3d(b + i * 8192, &tmB, full + st, n0 + 64 * i, k0, tb);
+                    } else {
+                        tma_load_3d(b, &tmB, full + st, k0, n0, tb);
+                    }
+                }
+            }
+            // copies that nothing has waited for (only after a wait ran out) land before the CTA ends
+            if (!ok)
+                for (uint32_t i = it < kStages ? 0 : it - kStages; i < it; ++i) mbar_wait(full + i % kStages, i / kStages & 1);
         }
+        __syncwarp();
+    } else if (warp == 1) {
+        const uint32_t lead = elect_one_sync();
+        const uint32_t idesc = umma_idesc_t(1, kBM, p.BN, A_MN, B_MN);
+        uint32_t it = 0, n_tile = 0;
+        bool ok = true;
+        for (int t = blockIdx.x; t < tiles && ok; t += gridDim.x, ++n_tile) {
+            const int acc = n_tile & 1;
+            ok = mbar_wait(acc_empty + acc, (n_tile / 2 & 1) ^ 1);
+            tc_fence_after();
+            for (int s = 0; s < steps && ok; ++s, ++it) {
+                const int st = it % kStages;
+                ok = mbar_wait(full + st, it / kStages & 1);
+                if (!ok) break;
+                tc_fence_after();
+                const uint32_t base = smem_addr(smem) + st * kStageBytes;
+                uint64_t a = sw128_desc(base, A_MN), b = sw128_desc(base + kBM * kBK * 2, B_MN);
+#pragma unroll
+                for (int k = 0; k < kBK / 16; ++k) {
+                    umma_bf16_w(tmem + acc * kMaxBN, a, b, idesc, s > 0 || k > 0, lead);
+                    a += A_MN ? 2048 >> 4 : 32 >> 4;
+                    b += B_MN ? 2048 >> 4 : 32 >> 4;
+                }
+                umma_commit_w(empty + st, lead);
+            }
+            if (ok) umma_commit_w(acc_full + acc, lead);
+        }
+        if (!ok && lane == 0) report_status(p.status, kStatusTimeout);
+    } else {
+        const int quarter = warp & 3, half = (warp - 2) >> 2;      // tensor-memory lanes; 16-column chunks in turn
+        float *mine = stage_out + (warp - 2) * 32 * kEpiPitch;
+        const T *bias = static_cast<const T *>(p.bias), *res = static_cast<const T *>(p.res);
+        T *out = static_cast<T *>(p.out), *pre = static_cast<T *>(p.pre);
+        uint32_t n_tile = 0;
+        for (int t = blockIdx.x; t < tiles; t += gridDim.x, ++n_tile) {
+            const int acc = n_tile & 1;
+            int m0, n0;
+            tile_at(p, t, m0, n0);
+            if (!mbar_wait(acc_full + acc, n_tile / 2 & 1)) {
+                if (lane == 0) report_status(p.status, kStatusTimeout);
+                break;
+            }
+            tc_fence_after();
+            const int row0 = m0 + 32 * quarter, chunks = p.BN / 16;
+            for (int c = half; c < chunks; c += 2) {
+                float2 v[8];
+                tmem_ld16(tmem + ((uint32_t)(32 * quarter) << 16) + acc * kMaxBN + c * 16, v);
+                tmem_wait_ld();
+                if (c + 2 >= chunks) {                     // this warp's last read of the accumulator
+                    tc_fence_before();
+                    __syncwarp();
+                    if (lane == 0) mbar_arrive(acc_empty + acc);
+                }
+                const int col0 = n0 + c * 16;
+                if (row0 >= p.M || col0 >= p.N) continue;
+                // through shared memory, so that neighbouring lanes hold neighbouring columns
+#pragma unroll
+                for (int i = 0; i < 4; ++i)
+                    *reinterpret_cast<float4 *>(mine + lane * kEpiPitch + 4 * i) =
+                        make_float4(v[2 * i].x, v[2 * i].y, v[2 * i + 1].x, v[2 * i + 1].y);
+                __syncwarp();
+                if (p.vec) {
+                    constexpr int V = 16 / sizeof(T), LPR = 16 / V;    // columns per lane, lanes per row
+#pragma unroll
+                    for (int h = 0; h < LPR; ++h) {
+                        const int r = h * (32 / LPR) + lane / LPR, col = col0 + lane % LPR * V;
+                        const size_t row = row0 + r;
+                        if (row >= p.M || col >= p.N) continue;
+                        float o[V], e[V];
+#pragma unroll
+                        for (int i = 0; i < V / 4; ++i) {
+                            const float4 x = *reinterpret_cast<const float4 *>(mine + r * kEpiPitch + lane % LPR * V + 4 * i);
+                            o[4 * i] = x.x; o[4 * i + 1] = x.y; o[4 * i + 2] = x.z; o[4 * i + 3] = x.w;
+                        }
+                        if (bias != nullptr) {
+                            load_vec<T, V>(bias + col, e);
+#pragma unroll
+                            for (int i = 0; i < V; ++i) o[i] += e[i];
+                        }
+                        if (pre != nullptr) store_vec<T, V>(pre + row * p.N + col, o);
+#pragma unroll
+                        for (int i = 0; i < V; ++i) o[i] = act_rt(p.act, o[i]);
+                        if (res != nullptr) {
+                            load_vec<T, V>(res + row * p.ldres + col, e);
+#pragma unroll
+                            for (int i = 0; i < V; ++i) o[i] = __fadd_rn(o[i], e[i]);
+                        }
+                        store_vec<T, V>(out + row * p.N + col, o);
+                    }
+                } else {
+                    for (int h = 0; h < 16; ++h) {
+                        const int r = 2 * h + (lane >> 4), col = col0 + (lane & 15);
+                        const size_t row = row0 + r;
+                        if (row >= p.M || col >= p.N) continue;
+                        float o = mine[r * kEpiPitch + (lane & 15)];
+                        if (bias != nullptr) o += to_f32(bias[col]);
+                        if (pre != nullptr) pre[row * p.N + col] = from_f32<T>(o);
+                        o = act_rt(p.act, o);
+                        if (res != nullptr) o = __fadd_rn(o, to_f32(res[row * p.ldres + col]));
+                        out[row * p.N + col] = from_f32<T>(o);
+                    }
+                }
+                __syncwarp();
+            }
+        }
+    }
+    tc_fence_before();
+    __syncthreads();
+    tc_fence_after();
+    if (warp == 1) tmem_dealloc(tmem, 512);
 }
 
-// dpre = dy act'(pre) (dpre null: dy itself is it), and each slice of rows' column sums of it.
+// x as bf16 operand rows of `cols8` elements: a copy (bf16) or three terms (float32), planes of
+// [rows][cols8]. What lies past the `cols` columns is never read.
+__device__ __forceinline__ void split3(float x, __nv_bfloat16 (&t)[3]) {
+    t[0] = __float2bfloat16_rz(x);
+    const float r = x - __bfloat162float(t[0]);
+    const bool fine = r - r == 0.f;                // an infinity or NaN stays in the first term
+    t[1] = __float2bfloat16_rz(fine ? r : 0.f);
+    t[2] = __float2bfloat16_rn(fine ? r - __bfloat162float(t[1]) : 0.f);
+}
 template <typename T>
-__global__ void __launch_bounds__(256) linear_dpre_kernel(const T *dy, const T *pre, T *dpre, float *part, int M, int N, int act) {
+__global__ void __launch_bounds__(256) linear_pack_kernel(const T *x, long long ld, __nv_bfloat16 *out, int rows, int cols, int cols8) {
+    const int c = blockIdx.x * 256 + threadIdx.x;
+    if (c >= cols) return;
+    const size_t plane = (size_t)rows * cols8;
+    for (int r = blockIdx.y; r < rows; r += gridDim.y) {
+        const size_t at = (size_t)r * cols8 + c;
+        if constexpr (sizeof(T) == 2) {
+            out[at] = x[(size_t)r * ld + c];
+        } else {
+            __nv_bfloat16 t[3];
+            split3(x[(size_t)r * ld + c], t);
+#pragma unroll
+            for (int i = 0; i < 3; ++i) out[i * plane + at] = t[i];
+        }
+    }
+}
+
+// dpre = dy act'(pre) as an operand (null: dy is used as it is), and each slice of rows' column sums.
+// The rounding of dpre to bf16 is the operand format's; the bias sums take it before that.
+template <typename T>
+__global__ void __launch_bounds__(256) linear_dpre_kernel(const T *dy, const T *pre, __nv_bfloat16 *dpre, float *part, int M,
+                                                          int N, int N8, int act) {
     const int n = blockIdx.x * 256 + threadIdx.x;
     if (n >= N) return;
     float s = 0.f;
+    const size_t plane = (size_t)M * N8;
     for (size_t m = blockIdx.y; m < (size_t)M; m += gridDim.y) {
         float d = to_f32(dy[m * N + n]);
         if (act != kActNone) d *= dact_rt(act, to_f32(pre[m * N + n]));
-        if (dpre != nullptr) dpre[m * N + n] = from_f32<T>(d);
+        if (dpre != nullptr) {
+            if constexpr (sizeof(T) == 2) {
+                dpre[m * N8 + n] = __float2bfloat16_rn(d);
+            } else {
+                __nv_bfloat16 t[3];
+                split3(d, t);
+#pragma unroll
+                for (int i = 0; i < 3; ++i) dpre[i * plane + m * N8 + n] = t[i];
+            }
+        }
         s += d;
     }
     part[(size_t)blockIdx.y * N + n] = s;
@@ -92,68 +315,139 @@ __global__ void __launch_bounds__(256) linear_dbias_kernel(const float *part, T 
     dbias[n] = from_f32<T>(s);
 }
 
-size_t linear_fwd_workspace(const LinearParams &, int) { return 0; }
-
-size_t linear_bwd_workspace(const LinearParams &p, int dtype) {
-    return up256((size_t)p.M * p.N * (dtype == 0 ? 4 : 2)) + up256((size_t)kBiasSlices * p.N * 4);
-}
-
 namespace {
 
-template <typename T>
-cudaError_t product(const char *name, Operand<T> A, Operand<T> B, int M, int N, int K, const void *bias, int act, const void *res,
-                    long long ldres, void *out, void *pre, cudaStream_t s) {
+// Room for an operand's copy: float32 terms always, bf16 where TMA cannot read it in place (rows not
+// a multiple of 16 bytes apart) or might not be able to (a slice, whose address may be unaligned).
+size_t pack_bytes(long long rows, int cols, long long ld, int dtype) {
+    if (dtype == 0) return up256((size_t)3 * rows * up8(cols) * 2);
+    return ld % 8 != 0 || ld != cols ? up256((size_t)rows * up8(cols) * 2) : 0;
+}
+
+struct Operand {
+    const void *p;
+    long long ld;
+    int rows, cols;
+};
+
+// The operand as TMA can read it, copied to ws where it has to be.
+int pack(const Operand &in, Operand *out, char *ws, int dtype, cudaStream_t s) {
+    *out = in;
+    if (dtype != 0 && in.ld % 8 == 0 && (uintptr_t)in.p % 16 == 0) return 0;
+    const dim3 grid((in.cols + 255) / 256, in.rows < 4096 ? in.rows : 4096);
+    __nv_bfloat16 *to = reinterpret_cast<__nv_bfloat16 *>(ws);
+    const int cols8 = up8(in.cols);
+    timing_mark("linear_pack", 0, s);
+    if (dtype == 0) linear_pack_kernel<float><<<grid, 256, 0, s>>>(static_cast<const float *>(in.p), in.ld, to, in.rows, in.cols, cols8);
+    else linear_pack_kernel<__nv_bfloat16><<<grid, 256, 0, s>>>(static_cast<const __nv_bfloat16 *>(in.p), in.ld, to, in.rows, in.cols, cols8);
+    timing_mark("linear_pack", 1, s);
+    out->p = to;
+    out->ld = cols8;
+    return api_cuda_status(cudaGetLastError());
+}
+
+struct Epilogue {
+    const void *bias, *res;
+    long long ldres;
+    int act;
+    void *out, *pre;
+};
+
+template <bool A_MN, bool B_MN, typename T>
+int gemm(const char *name, const Operand &A, const Operand &B, int M, int N, int K, const Epilogue &e, int *status, cudaStream_t s) {
+    GemmParams p = {};
+    p.bias = e.bias; p.res = e.res; p.ldres = e.ldres; p.act = e.act; p.out = e.out; p.pre = e.pre; p.status = status;
+    p.M = M; p.N = N;
+    p.kblocks = (K + kBK - 1) / kBK;
+    const int planes = sizeof(T) == 4 ? 3 : 1;
+    p.terms = sizeof(T) == 4 ? 6 : 1;
+    p.BN = N <= 64 ? 64 : N <= 128 ? 128 : kMaxBN;
+    p.mt = (M + kBM - 1) / kBM;
+    p.nt = (N + p.BN - 1) / p.BN;
+    p.panel = p.nt < 16 ? p.nt : 16;
+    const int V = 16 / (int)sizeof(T);
+    p.vec = N % V == 0 && (uintptr_t)e.res % 16 == 0 && e.ldres % V == 0;
+    CUtensorMap tmA, tmB;
+    int rc;
+    if ((rc = api_planes_map(&tmA, A.p, A.cols, A.rows, planes, A.ld, kBK, A_MN ? 64 : kBM)) != 0) return rc;
+    if ((rc = api_planes_map(&tmB, B.p, B.cols, B.rows, planes, B.ld, kBK, B_MN ? 64 : p.BN)) != 0) return rc;
+    cudaError_t err = cudaFuncSetAttribute(gemm_kernel<A_MN, B_MN, T>, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)kGemmSmem);
+    if (err != cudaSuccess) return api_cuda_status(err);
+    const long long tiles = (long long)p.mt * p.nt;
     timing_mark(name, 0, s);
-    linear_simple_kernel<T><<<dim3((N + kTile - 1) / kTile, (M + kTile - 1) / kTile), 256, 0, s>>>(
-        A, B, M, N, K, static_cast<const T *>(bias), act, static_cast<const T *>(res), ldres, static_cast<T *>(out),
-        static_cast<T *>(pre));
+    gemm_kernel<A_MN, B_MN, T><<<(int)(tiles < kSms ? tiles : kSms), kGemmThreads, kGemmSmem, s>>>(tmA, tmB, p);
     timing_mark(name, 1, s);
-    return cudaGetLastError();
+    return api_cuda_status(cudaGetLastError());
 }
 
 template <typename T>
-cudaError_t bwd_any(const LinearParams &p, cudaStream_t s) {
-    cudaError_t e = cudaSuccess;
-    const T *dpre = static_cast<const T *>(p.dy);
-    float *part = reinterpret_cast<float *>(p.ws + up256((size_t)p.M * p.N * sizeof(T)));
-    if (p.act != kActNone || p.dbias != nullptr) {
-        T *to = p.act != kActNone ? reinterpret_cast<T *>(p.ws) : nullptr;
+int fwd_any(const LinearParams &p, int dtype, cudaStream_t s) {
+    Operand x = {p.x, p.ldx, p.M, p.K}, w = {p.W, p.ldw, p.N, p.K};
+    char *ws = p.ws;
+    int rc;
+    if ((rc = pack(x, &x, ws, dtype, s)) != 0) return rc;
+    ws += pack_bytes(p.M, p.K, p.ldx, dtype);
+    if ((rc = pack(w, &w, ws, dtype, s)) != 0) return rc;
+    return gemm<false, false, T>("linear_fwd", x, w, p.M, p.N, p.K, {p.bias, p.res, p.ldres, p.act, p.y, p.pre}, p.status, s);
+}
+
+template <typename T>
+int bwd_any(const LinearParams &p, int dtype, cudaStream_t s) {
+    Operand x = {p.x, p.ldx, p.M, p.K}, w = {p.W, p.ldw, p.N, p.K}, d = {p.dy, p.N, p.M, p.N};
+    char *ws = p.ws;
+    float *part = reinterpret_cast<float *>(ws);
+    ws += up256((size_t)kBiasSlices * p.N * 4);
+    const bool own_dpre = dtype == 0 || p.act != kActNone || p.N % 8 != 0;
+    int rc;
+    if (own_dpre || p.dbias != nullptr) {
+        __nv_bfloat16 *to = own_dpre ? reinterpret_cast<__nv_bfloat16 *>(ws) : nullptr;
         const int slices = p.M < kBiasSlices ? p.M : kBiasSlices;
         timing_mark("linear_dpre", 0, s);
         linear_dpre_kernel<T><<<dim3((p.N + 255) / 256, slices), 256, 0, s>>>(
-            static_cast<const T *>(p.dy), static_cast<const T *>(p.pre_in), to, part, p.M, p.N, p.act);
+            static_cast<const T *>(p.dy), static_cast<const T *>(p.pre_in), to, part, p.M, p.N, up8(p.N), p.act);
         timing_mark("linear_dpre", 1, s);
-        if ((e = cudaGetLastError()) != cudaSuccess) return e;
-        if (to != nullptr) dpre = to;
+        if ((rc = api_cuda_status(cudaGetLastError())) != 0) return rc;
+        if (to != nullptr) d = {to, up8(p.N), p.M, p.N};
         if (p.dbias != nullptr) {
             timing_mark("linear_dbias", 0, s);
             linear_dbias_kernel<T><<<(p.N + 255) / 256, 256, 0, s>>>(part, static_cast<T *>(p.dbias), slices, p.N);
             timing_mark("linear_dbias", 1, s);
-            if ((e = cudaGetLastError()) != cudaSuccess) return e;
+            if ((rc = api_cuda_status(cudaGetLastError())) != 0) return rc;
         }
     }
-    const Operand<T> x_t = {static_cast<const T *>(p.x), 1, p.ldx}, w_t = {static_cast<const T *>(p.W), 1, p.ldw};
-    if (p.dx != nullptr)
-        e = product<T>("linear_dx", Operand<T>{dpre, p.N, 1}, w_t, p.M, p.K, p.N, nullptr, kActNone, nullptr, 0, p.dx, nullptr, s);
-    if (e == cudaSuccess && p.dW != nullptr)
-        e = product<T>("linear_dw", Operand<T>{dpre, 1, p.N}, x_t, p.N, p.K, p.M, nullptr, kActNone, nullptr, 0, p.dW, nullptr, s);
-    return e;
+    if (own_dpre) ws += up256((size_t)(dtype == 0 ? 3 : 1) * p.M * up8(p.N) * 2);
+    if (p.dx != nullptr) {
+        if ((rc = pack(w, &w, ws, dtype, s)) != 0) return rc;
+        if ((rc = gemm<false, true, T>("linear_dx", d, w, p.M, p.K, p.N, {nullptr, nullptr, 0, kActNone, p.dx, nullptr}, p.status, s)) != 0)
+            return rc;
+    }
+    ws += pack_bytes(p.N, p.K, p.ldw, dtype);
+    if (p.dW != nullptr) {
+        if ((rc = pack(x, &x, ws, dtype, s)) != 0) return rc;
+        rc = gemm<true, true, T>("linear_dw", d, x, p.N, p.K, p.M, {nullptr, nullptr, 0, kActNone, p.dW, nullptr}, p.status, s);
+        if (rc != 0) return rc;
+    }
+    return 0;
 }
 
 }  // namespace
 
+size_t linear_fwd_workspace(const LinearParams &p, int dtype) {
+    return pack_bytes(p.M, p.K, p.ldx, dtype) + pack_bytes(p.N, p.K, p.ldw, dtype);
+}
+
+size_t linear_bwd_workspace(const LinearParams &p, int dtype) {
+    const bool own_dpre = dtype == 0 || p.act != kActNone || p.N % 8 != 0;
+    return up256((size_t)kBiasSlices * p.N * 4) + (own_dpre ? up256((size_t)(dtype == 0 ? 3 : 1) * p.M * up8(p.N) * 2) : 0) +
+           pack_bytes(p.M, p.K, p.ldx, dtype) + pack_bytes(p.N, p.K, p.ldw, dtype);
+}
+
 int launch_linear_fwd(const LinearParams &p, int dtype, cudaStream_t s) {
-    if (dtype == 0)
-        return api_cuda_status(product<float>("linear_fwd", {static_cast<const float *>(p.x), p.ldx, 1},
-                                              {static_cast<const float *>(p.W), p.ldw, 1}, p.M, p.N, p.K, p.bias, p.act, p.res,
-                                              p.ldres, p.y, p.pre, s));
-    return api_cuda_status(product<__nv_bfloat16>("linear_fwd", {static_cast<const __nv_bfloat16 *>(p.x), p.ldx, 1},
-                                                  {static_cast<const __nv_bfloat16 *>(p.W), p.ldw, 1}, p.M, p.N, p.K, p.bias,
-                                                  p.act, p.res, p.ldres, p.y, p.pre, s));
+    return dtype == 0 ? fwd_any<float>(p, dtype, s) : fwd_any<__nv_bfloat16>(p, dtype, s);
 }
 
 int launch_linear_bwd(const LinearParams &p, int dtype, cudaStream_t s) {
-    return api_cuda_status(dtype == 0 ? bwd_any<float>(p, s) : bwd_any<__nv_bfloat16>(p, s));
+    return dtype == 0 ? bwd_any<float>(p, dtype, s) : bwd_any<__nv_bfloat16>(p, dtype, s);
 }
 
 }  // namespace gdn

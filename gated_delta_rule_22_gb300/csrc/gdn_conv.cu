@@ -37,36 +37,55 @@ __device__ __forceinline__ void load_input(const ConvParams &p, int W, int b, in
                            p.s0 != nullptr && t >= 1 - W, o);
 }
 
+// Channels in pairs, for the packed float32 instructions (V = 1: the second of the pair is unused).
+template <int V>
+constexpr int kPairs = V / 2 > 0 ? V / 2 : 1;
+
+template <int V>
+__device__ __forceinline__ void to_pairs(const float (&x)[V], float2 (&o)[kPairs<V>]) {
+#pragma unroll
+    for (int i = 0; i < kPairs<V>; ++i) o[i] = make_float2(x[V > 1 ? 2 * i : 0], V > 1 ? x[2 * i + 1] : 0.f);
+}
+template <int V>
+__device__ __forceinline__ void from_pairs(const float2 (&x)[kPairs<V>], float (&o)[V]) {
+#pragma unroll
+    for (int v = 0; v < V; ++v) o[v] = v % 2 ? x[v / 2].y : x[v / 2].x;
+}
+
+// The taps and the bias of V channels.
 template <int W, int V>
-__device__ __forceinline__ void load_taps(const ConvParams &p, int c, float (&w)[V][W], float (&bias)[V]) {
-    if constexpr (V % 4 == 0) {
-        float flat[V * W];
+__device__ __forceinline__ void load_taps(const ConvParams &p, int c, float2 (&w)[W][kPairs<V>], float2 (&bias)[kPairs<V>]) {
+    float flat[V * W], bs[V];
+    if constexpr (V * W % 4 == 0) {
 #pragma unroll
         for (int i = 0; i < V * W / 4; ++i) {
             const float4 q = *reinterpret_cast<const float4 *>(p.w + (size_t)c * W + 4 * i);
             flat[4 * i] = q.x; flat[4 * i + 1] = q.y; flat[4 * i + 2] = q.z; flat[4 * i + 3] = q.w;
         }
-#pragma unroll
-        for (int v = 0; v < V; ++v)
-#pragma unroll
-            for (int j = 0; j < W; ++j) w[v][j] = flat[v * W + j];
     } else {
 #pragma unroll
-        for (int v = 0; v < V; ++v)
-#pragma unroll
-            for (int j = 0; j < W; ++j) w[v][j] = p.w[(size_t)(c + v) * W + j];
+        for (int i = 0; i < V * W; ++i) flat[i] = p.w[(size_t)c * W + i];
     }
 #pragma unroll
-    for (int v = 0; v < V; ++v) bias[v] = p.bias ? p.bias[c + v] : 0.f;
+    for (int v = 0; v < V; ++v) bs[v] = p.bias ? p.bias[c + v] : 0.f;
+    to_pairs<V>(bs, bias);
+#pragma unroll
+    for (int j = 0; j < W; ++j) {
+        float col[V];
+#pragma unroll
+        for (int v = 0; v < V; ++v) col[v] = flat[v * W + j];
+        to_pairs<V>(col, w[j]);
+    }
 }
 
 }  // namespace
 
 // Threads over (batch row, run of `run` steps, V channels). The thread of a row's first run also
-// writes the state behind the row's last valid step.
+// writes the state behind the row's last valid step. The next U steps' inputs are loaded before the
+// present ones are used; groups of U steps inside the row and the run take a path without tests.
 template <typename T, int W, int V>
 __global__ void __launch_bounds__(kConvThreads) conv_fwd_kernel(ConvParams p, int run, int runs) {
-    constexpr int U = 4;                                   // steps loaded ahead
+    constexpr int U = 4, P = kPairs<V>;
     const int CV = p.C / V;
     const size_t id = (size_t)blockIdx.x * kConvThreads + threadIdx.x;
     if (id >= (size_t)p.B * runs * CV) return;
@@ -74,14 +93,25 @@ __global__ void __launch_bounds__(kConvThreads) conv_fwd_kernel(ConvParams p, in
     const size_t rb = id / CV;
     const int r = (int)(rb % runs), b = (int)(rb / runs);
     const int L = row_length(p.lens, b, p.T);
-    const int t0 = r * run, t1 = min(t0 + run, p.T);
-    float w[V][W], bias[V], win[W][V];
+    const int t0 = r * run, t1 = min(t0 + run, p.T), t_in = min(t1, L);
+    const T *x = static_cast<const T *>(p.x) + (size_t)b * p.T * p.ldx + c;
+    T *y = static_cast<T *>(p.y) + (size_t)b * p.T * p.C + c;
+    Raw<T, V> next[U];
+    auto fetch = [&](int t) {
+#pragma unroll
+        for (int i = 0; i < U; ++i) {
+            next[i] = Raw<T, V>();
+            if (t + i < t_in) next[i] = load_raw<T, V>(x + (size_t)(t + i) * p.ldx);
+        }
+    };
+    fetch(t0);
+    float2 w[W][P], bias[P], win[W][P];
     load_taps<W, V>(p, c, w, bias);
 #pragma unroll
     for (int i = 0; i < W - 1; ++i) {
-#pragma unroll
-        for (int v = 0; v < V; ++v) win[i][v] = 0.f;
-        if (t0 + i - (W - 1) < L) load_input<T, V>(p, W, b, t0 + i - (W - 1), c, win[i]);
+        float e[V] = {};
+        if (t0 + i - (W - 1) < L) load_input<T, V>(p, W, b, t0 + i - (W - 1), c, e);
+        to_pairs<V>(e, win[i]);
     }
     if (r == 0 && p.s_T != nullptr) {
         float keep[W][V];
@@ -91,132 +121,185 @@ __global__ void __launch_bounds__(kConvThreads) conv_fwd_kernel(ConvParams p, in
 #pragma unroll
         for (int j = 0; j < W - 1; ++j) store_vec<T, V>(out + (size_t)j * p.C, keep[j]);
     }
-    const T *x = static_cast<const T *>(p.x) + (size_t)b * p.T * p.ldx + c;
-    T *y = static_cast<T *>(p.y) + (size_t)b * p.T * p.C + c;
+    auto step = [&](const Raw<T, V> &in, int t, bool valid) {
+        float o[V], e[V];
+        unpack<T, V>(in, e);
+        to_pairs<V>(e, win[W - 1]);
+        float2 pre[P];
+#pragma unroll
+        for (int i = 0; i < P; ++i) {
+            pre[i] = bias[i];
+#pragma unroll
+            for (int j = 0; j < W; ++j) pre[i] = __ffma2_rn(w[j][i], win[j][i], pre[i]);
+#pragma unroll
+            for (int j = 0; j < W - 1; ++j) win[j][i] = win[j + 1][i];
+        }
+        from_pairs<V>(pre, o);
+#pragma unroll
+        for (int v = 0; v < V; ++v) o[v] = valid ? (p.act == kActSilu ? silu_hw(o[v]) : o[v]) : 0.f;
+        store_vec<T, V>(y + (size_t)t * p.C, o);
+    };
     for (int t = t0; t < t1; t += U) {
-        float in[U][V];
+        Raw<T, V> in[U];
 #pragma unroll
-        for (int i = 0; i < U; ++i) load_or_zero<T, V>(x + (size_t)(t + i) * p.ldx, t + i < min(t1, L), in[i]);
+        for (int i = 0; i < U; ++i) in[i] = next[i];
+        fetch(t + U);
+        if (t + U <= t_in) {
 #pragma unroll
-        for (int i = 0; i < U; ++i) {
-            if (t + i >= t1) break;
-            float o[V];
+            for (int i = 0; i < U; ++i) step(in[i], t + i, true);
+        } else {
 #pragma unroll
-            for (int v = 0; v < V; ++v) {
-                win[W - 1][v] = in[i][v];
-                float pre = bias[v];
-#pragma unroll
-                for (int j = 0; j < W; ++j) pre = fmaf(w[v][j], win[j][v], pre);
-                o[v] = t + i < L ? (p.act == kActSilu ? silu_hw(pre) : pre) : 0.f;
-#pragma unroll
-                for (int j = 0; j < W - 1; ++j) win[j][v] = win[j + 1][v];
-            }
-            store_vec<T, V>(y + (size_t)(t + i) * p.C, o);
+            for (int i = 0; i < U; ++i)
+                if (t + i < t1) step(in[i], t + i, t + i < L);
         }
     }
 }
 
-// A CTA takes 32 V channels and 8 runs of steps (one per warp) of one batch row. The parameter sums
-// go over a thread's steps, then over the CTA's warps in ascending order, into the CTA's slice of
-// the partial sums: a fixed order.
+// A CTA takes 32 V channels and 8 runs of steps (one per warp) of one batch row. A thread forms dpre
+// for its run and the W-1 steps before it; dx[s] is complete, and stored, at step s + W-1, so a run
+// stores the inputs from W-1 steps before it on, and the row's last run goes on for W-1 steps behind
+// the row (where dpre is 0). The parameter sums go over a thread's steps, then over the CTA's warps in
+// ascending order, into the CTA's slice of the partial sums: a fixed order.
 template <typename T, int W, int V>
-__global__ void __launch_bounds__(32 * kConvBwdWarps) conv_bwd_kernel(ConvParams p, int run, int slices_row) {
+__global__ void __launch_bounds__(32 * kConvBwdWarps, 2) conv_bwd_kernel(ConvParams p, int run, int slices_row) {
     __shared__ float sums[kConvBwdWarps][W + 1][32 * V];
+    constexpr int U = 4, P = kPairs<V>;
     const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
     const int c = (blockIdx.y * 32 + lane) * V;
     const int b = blockIdx.x / slices_row, sl = blockIdx.x % slices_row;
     const int L = row_length(p.lens, b, p.T);
     const int t0 = (sl * kConvBwdWarps + warp) * run, t1 = min(t0 + run, p.T);
-    float dw[W][V], db[V];
+    float2 dw[W][P], db[P];
 #pragma unroll
-    for (int v = 0; v < V; ++v) {
-        db[v] = 0.f;
+    for (int i = 0; i < P; ++i) {
+        db[i] = make_float2(0.f, 0.f);
 #pragma unroll
-        for (int j = 0; j < W; ++j) dw[j][v] = 0.f;
+        for (int j = 0; j < W; ++j) dw[j][i] = make_float2(0.f, 0.f);
     }
     if (c < p.C && t0 < t1) {
-        float w[V][W], bias[V], win[W][V], dwin[W][V];
-        load_taps<W, V>(p, c, w, bias);
-#pragma unroll
-        for (int i = 0; i < W; ++i)
-#pragma unroll
-            for (int v = 0; v < V; ++v) win[i][v] = dwin[i][v] = 0.f;
-#pragma unroll
-        for (int i = 0; i < W - 1; ++i)
-            if (t0 + i - (W - 1) < L) load_input<T, V>(p, W, b, t0 + i - (W - 1), c, win[i]);
+        const int t_in = min(t1, L), t_end = t1 == p.T ? t1 + W - 1 : t1;
         const T *x = static_cast<const T *>(p.x) + (size_t)b * p.T * p.ldx + c;
         const T *dy = static_cast<const T *>(p.dy) + (size_t)b * p.T * p.C + c;
         const T *ds_T = static_cast<const T *>(p.ds_T) + (size_t)b * (W - 1) * p.C + c;
         T *dx = static_cast<T *>(p.dx) + (size_t)b * p.T * p.C + c;
         T *ds0 = static_cast<T *>(p.ds0) + (size_t)b * (W - 1) * p.C + c;
-        constexpr int U = 4;
-        for (int tb = t0; tb < t1 + W - 1; tb += U) {
-            float xin[U][V], din[U][V];
+        Raw<T, V> next_x[U], next_d[U];
+        auto fetch = [&](int t) {
 #pragma unroll
             for (int i = 0; i < U; ++i) {
-                const bool ok = tb + i < min(t1 + W - 1, L);
-                load_or_zero<T, V>(x + (size_t)(tb + i) * p.ldx, ok, xin[i]);
-                load_or_zero<T, V>(dy + (size_t)(tb + i) * p.C, ok, din[i]);
+                next_x[i] = next_d[i] = Raw<T, V>();
+                if (t + i < t_in) {
+                    next_x[i] = load_raw<T, V>(x + (size_t)(t + i) * p.ldx);
+                    next_d[i] = load_raw<T, V>(dy + (size_t)(t + i) * p.C);
+                }
+            }
+        };
+        fetch(t0);
+        float2 w[W][P], bias[P], win[W][P], dwin[W][P];
+        load_taps<W, V>(p, c, w, bias);
+        // dpre of one step from the window whose newest input is in place, into dwin[W - 1]
+        auto grad = [&](const float (&d)[V], bool valid) {
+            float2 pre[P];
+            float e[V];
+#pragma unroll
+            for (int i = 0; i < P; ++i) {
+                pre[i] = bias[i];
+#pragma unroll
+                for (int j = 0; j < W; ++j) pre[i] = __ffma2_rn(w[j][i], win[j][i], pre[i]);
+            }
+            from_pairs<V>(pre, e);
+#pragma unroll
+            for (int v = 0; v < V; ++v) e[v] = valid ? (p.act == kActSilu ? d[v] * dsilu_hw(e[v]) : d[v]) : 0.f;
+            to_pairs<V>(e, dwin[W - 1]);
+        };
+        auto shift = [&](float2(&a)[W][P]) {
+#pragma unroll
+            for (int j = 0; j < W - 1; ++j)
+#pragma unroll
+                for (int i = 0; i < P; ++i) a[j][i] = a[j + 1][i];
+        };
+        // the windows in front of the run: inputs from t0 - 2 (W-1) on, dpre from t0 - (W-1) on
+#pragma unroll
+        for (int j = 0; j < W; ++j)
+#pragma unroll
+            for (int i = 0; i < P; ++i) win[j][i] = dwin[j][i] = make_float2(0.f, 0.f);
+#pragma unroll
+        for (int i = 0; i < 2 * (W - 1); ++i) {
+            const int t = t0 - 2 * (W - 1) + i;
+            float e[V] = {}, d[V] = {};
+            if (t < L) load_input<T, V>(p, W, b, t, c, e);
+            to_pairs<V>(e, win[W - 1]);
+            if (i >= W - 1) {
+                const bool valid = t >= 0 && t < L;
+                if (valid) load_vec<T, V>(dy + (size_t)t * p.C, d);
+                grad(d, valid);
+                shift(dwin);
+            }
+            shift(win);
+        }
+        // one step: the sums, and dx of the input W-1 steps back
+        auto step = [&](const Raw<T, V> &xin, const Raw<T, V> &din, bool valid, float (&o)[V]) {
+            float e[V], d[V];
+            unpack<T, V>(xin, e);
+            unpack<T, V>(din, d);
+            to_pairs<V>(e, win[W - 1]);
+            grad(d, valid);
+            float2 s[P];
+#pragma unroll
+            for (int i = 0; i < P; ++i) {
+                db[i] = __fadd2_rn(db[i], dwin[W - 1][i]);
+#pragma unroll
+                for (int j = 0; j < W; ++j) dw[j][i] = __ffma2_rn(dwin[W - 1][i], win[j][i], dw[j][i]);
+                s[i] = __fmul2_rn(w[0][i], dwin[W - 1][i]);
+#pragma unroll
+                for (int j = 1; j < W; ++j) s[i] = __ffma2_rn(w[j][i], dwin[W - 1 - j][i], s[i]);
+            }
+            from_pairs<V>(s, o);
+            shift(win);
+            shift(dwin);
+        };
+        for (int tb = t0; tb < t_end; tb += U) {
+            Raw<T, V> xin[U], din[U];
+#pragma unroll
+            for (int i = 0; i < U; ++i) {
+                xin[i] = next_x[i];
+                din[i] = next_d[i];
+            }
+            fetch(tb + U);
+            float o[V];
+            if (tb >= W - 1 && tb + U <= t_in) {      // inside the row: the state takes no part
+#pragma unroll
+                for (int i = 0; i < U; ++i) {
+                    step(xin[i], din[i], true, o);
+                    store_vec<T, V>(dx + (size_t)(tb + i - (W - 1)) * p.C, o);
+                }
+                continue;
             }
 #pragma unroll
             for (int i = 0; i < U; ++i) {
-                const int t = tb + i;
-                if (t >= t1 + W - 1) break;
-                float o[V];
+                const int t = tb + i, s = t - (W - 1);
+                if (t >= t_end) break;
+                step(xin[i], din[i], t < L, o);
+                // s is input s of the row, or row t of the state in front of it; either may be one of
+                // the W-1 inputs behind the last valid step
+                const int j = s - (L - (W - 1));
+                if (p.ds_T != nullptr && j >= 0 && j < W - 1) {
+                    float e[V];
+                    load_vec<T, V>(ds_T + (size_t)j * p.C, e);
 #pragma unroll
-                for (int v = 0; v < V; ++v) {
-                    win[W - 1][v] = xin[i][v];
-                    float pre = bias[v];
-#pragma unroll
-                    for (int j = 0; j < W; ++j) pre = fmaf(w[v][j], win[j][v], pre);
-                    const float dpre = t < L ? (p.act == kActSilu ? din[i][v] * dsilu_hw(pre) : din[i][v]) : 0.f;
-                    dwin[W - 1][v] = dpre;
-                    if (t < t1) {
-                        db[v] += dpre;
-#pragma unroll
-                        for (int j = 0; j < W; ++j) dw[j][v] = fmaf(dpre, win[j][v], dw[j][v]);
-                    }
-                    o[v] = 0.f;
-#pragma unroll
-                    for (int j = 0; j < W; ++j) o[v] = fmaf(w[v][j], dwin[W - 1 - j][v], o[v]);
-#pragma unroll
-                    for (int j = 0; j < W - 1; ++j) {
-                        win[j][v] = win[j + 1][v];
-                        dwin[j][v] = dwin[j + 1][v];
-                    }
+                    for (int v = 0; v < V; ++v) o[v] += e[v];
                 }
-                const int s = t - (W - 1);            // the input whose gradient is complete now
-                if (s >= t0) {
-                    const int j = s - (L - (W - 1));  // its place in the state behind the row, if any
-                    if (p.ds_T != nullptr && j >= 0 && j < W - 1) {
-                        float e[V];
-                        load_vec<T, V>(ds_T + (size_t)j * p.C, e);
-#pragma unroll
-                        for (int v = 0; v < V; ++v) o[v] += e[v];
-                    }
-                    if (s >= L) {
-#pragma unroll
-                        for (int v = 0; v < V; ++v) o[v] = 0.f;
-                    }
-                    store_vec<T, V>(dx + (size_t)s * p.C, o);
-                } else if (t0 == 0 && p.ds0 != nullptr) {
-                    const int j = t - L;              // row t of s0 is row t - L of the state behind the row
-                    if (p.ds_T != nullptr && j >= 0) {
-                        float e[V];
-                        load_vec<T, V>(ds_T + (size_t)j * p.C, e);
-#pragma unroll
-                        for (int v = 0; v < V; ++v) o[v] += e[v];
-                    }
-                    store_vec<T, V>(ds0 + (size_t)t * p.C, o);
-                }
+                if (s >= 0) store_vec<T, V>(dx + (size_t)s * p.C, o);
+                else if (p.ds0 != nullptr) store_vec<T, V>(ds0 + (size_t)t * p.C, o);
             }
         }
     }
 #pragma unroll
-    for (int v = 0; v < V; ++v) {
-        sums[warp][W][lane * V + v] = db[v];
+    for (int j = 0; j <= W; ++j) {
+        float e[V];
+        from_pairs<V>(j < W ? dw[j < W ? j : 0] : db, e);
 #pragma unroll
-        for (int j = 0; j < W; ++j) sums[warp][j][lane * V + v] = dw[j][v];
+        for (int v = 0; v < V; ++v) sums[warp][j][lane * V + v] = e[v];
     }
     __syncthreads();
     for (int i = threadIdx.x; i < (W + 1) * 32 * V; i += 32 * kConvBwdWarps) {
@@ -229,15 +312,13 @@ __global__ void __launch_bounds__(32 * kConvBwdWarps) conv_bwd_kernel(ConvParams
     }
 }
 
-// dw[c][j] and dbias[c] from the slices' partial sums, in ascending order.
+// dw[c][j] and dbias[c] from the slices' partial sums.
 __global__ void __launch_bounds__(256) conv_reduce_kernel(ConvParams p, int slices) {
-    const int W = p.W;
-    const size_t i = (size_t)blockIdx.x * 256 + threadIdx.x;
-    if (i >= (size_t)(W + 1) * p.C) return;
+    const size_t n = (size_t)(p.W + 1) * p.C, i = (size_t)blockIdx.x * 32 + threadIdx.x;
+    const double a = slice_sum(p.part, slices, n);
+    if (threadIdx.x >= 32 || i >= n) return;
     const int j = (int)(i / p.C), c = (int)(i % p.C);
-    double a = 0.0;
-    for (int s = 0; s < slices; ++s) a += (double)p.part[((size_t)s * (W + 1) + j) * p.C + c];
-    if (j < W) p.dw[(size_t)c * W + j] = (float)a;
+    if (j < p.W) p.dw[(size_t)c * p.W + j] = (float)a;
     else if (p.dbias != nullptr) p.dbias[c] = (float)a;
 }
 
@@ -281,7 +362,7 @@ cudaError_t conv_bwd_launch(const ConvParams &p, cudaStream_t s) {
     cudaError_t e = cudaGetLastError();
     if (e != cudaSuccess) return e;
     timing_mark("conv_reduce", 0, s);
-    conv_reduce_kernel<<<(unsigned)(((size_t)(W + 1) * p.C + 255) / 256), 256, 0, s>>>(p, slices);
+    conv_reduce_kernel<<<(unsigned)(((size_t)(W + 1) * p.C + 31) / 32), 256, 0, s>>>(p, slices);
     timing_mark("conv_reduce", 1, s);
     return cudaGetLastError();
 }
@@ -314,7 +395,7 @@ int conv_bwd_slices(const ConvParams &p) {
 
 cudaError_t launch_conv_fwd(const ConvParams &p, int dtype, cudaStream_t s) {
     if (dtype == 0) return conv_aligned(p, 4, 4) ? conv_fwd_taps<float, 4>(p, s) : conv_fwd_taps<float, 1>(p, s);
-    return conv_aligned(p, 8, 2) ? conv_fwd_taps<__nv_bfloat16, 8>(p, s) : conv_fwd_taps<__nv_bfloat16, 1>(p, s);
+    return conv_aligned(p, 4, 2) ? conv_fwd_taps<__nv_bfloat16, 4>(p, s) : conv_fwd_taps<__nv_bfloat16, 1>(p, s);
 }
 
 cudaError_t launch_conv_bwd(const ConvParams &p, int dtype, cudaStream_t s) {

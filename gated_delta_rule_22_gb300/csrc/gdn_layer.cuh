@@ -186,6 +186,49 @@ __device__ __forceinline__ void store_vec(T *p, const float (&o)[V]) {
     }
 }
 
+// V consecutive elements as they lie in memory, and as floats: loads that are started ahead hold
+// the fewest registers.
+template <int BYTES>
+struct RawType;
+template <>
+struct RawType<16> { using type = uint4; };
+template <>
+struct RawType<8> { using type = uint2; };
+template <>
+struct RawType<4> { using type = uint32_t; };
+template <>
+struct RawType<2> { using type = unsigned short; };
+template <typename T, int V>
+using Raw = typename RawType<V * (int)sizeof(T)>::type;
+
+template <typename T, int V>
+__device__ __forceinline__ Raw<T, V> load_raw(const T *p) { return *reinterpret_cast<const Raw<T, V> *>(p); }
+template <typename T, int V>
+__device__ __forceinline__ void unpack(const Raw<T, V> &r, float (&o)[V]) {
+    load_vec<T, V>(reinterpret_cast<const T *>(&r), o);
+}
+
+// Sum over the slices of partial sums part[slice][n] of column blockIdx.x * 32 + threadIdx.x % 32, for
+// a CTA of 256 threads: eight threads take every eighth slice of a column, then their sums are added in
+// order (float64 throughout: the order is fixed and the sum is exact to float32). Valid in the first
+// 32 threads.
+__device__ __forceinline__ double slice_sum(const float *part, int slices, size_t n) {
+    __shared__ double sums[8][32];
+    const int col = threadIdx.x & 31, lane = threadIdx.x >> 5;
+    const size_t i = (size_t)blockIdx.x * 32 + col;
+    double a = 0.0;
+    if (i < n)
+#pragma unroll 4
+        for (int s = lane; s < slices; s += 8) a += (double)part[(size_t)s * n + i];
+    sums[lane][col] = a;
+    __syncthreads();
+    double t = 0.0;
+    if (lane == 0)
+#pragma unroll
+        for (int k = 0; k < 8; ++k) t += sums[k][col];
+    return t;
+}
+
 // Valid steps of batch row b.
 __device__ __forceinline__ int row_length(const int *lens, int b, int T) {
     return lens == nullptr ? T : min(max(lens[b], 0), T);

@@ -289,15 +289,13 @@ __global__ void __launch_bounds__(kNormThreads) norm_bwd_wide_sums_kernel(NormPa
     p.part[((size_t)blockIdx.y * 2 + 1) * C + ch] = db;
 }
 
-// dw, db from the slices' partial sums, in ascending order.
+// dw, db from the slices' partial sums.
 __global__ void __launch_bounds__(256) norm_reduce_kernel(NormParams p) {
-    const size_t C = (size_t)p.G * p.D, i = (size_t)blockIdx.x * 256 + threadIdx.x;
-    if (i >= 2 * C) return;
+    const size_t C = (size_t)p.G * p.D, i = (size_t)blockIdx.x * 32 + threadIdx.x;
+    const double a = slice_sum(p.part, p.slices, 2 * C);
+    if (threadIdx.x >= 32 || i >= 2 * C) return;
     float *out = i < C ? p.dw : p.db;
-    if (out == nullptr) return;
-    double a = 0.0;
-    for (int s = 0; s < p.slices; ++s) a += (double)p.part[(size_t)s * 2 * C + i];
-    out[i % C] = (float)a;
+    if (out != nullptr) out[i % C] = (float)a;
 }
 
 namespace {
@@ -395,7 +393,7 @@ cudaError_t launch_norm_bwd(const NormParams &p, int dtype, cudaStream_t s) {
     cudaError_t e = dtype == 0 ? norm_any<float>(p, true, s) : norm_any<__nv_bfloat16>(p, true, s);
     if (e != cudaSuccess || (p.dw == nullptr && p.db == nullptr)) return e;
     timing_mark("norm_reduce", 0, s);
-    norm_reduce_kernel<<<(unsigned)(((size_t)2 * p.G * p.D + 255) / 256), 256, 0, s>>>(p);
+    norm_reduce_kernel<<<(unsigned)(((size_t)2 * p.G * p.D + 31) / 32), 256, 0, s>>>(p);
     timing_mark("norm_reduce", 1, s);
     return cudaGetLastError();
 }

@@ -284,12 +284,11 @@ __global__ void __launch_bounds__(256) scan_reduce_bc_kernel(ScanParams p, int b
     else static_cast<T *>(p.dC)[row * p.N + m - p.N] = from_f32<T>(s);
 }
 
-// dA_log, dD, ddt_bias: over the segments and batch rows, in ascending order.
+// dA_log, dD, ddt_bias: over the segments and batch rows.
 __global__ void __launch_bounds__(256) scan_reduce_c_kernel(ScanParams p) {
-    const size_t n = (size_t)(p.N + 2) * p.Cn, i = (size_t)blockIdx.x * 256 + threadIdx.x;
-    if (i >= n) return;
-    double s = 0.0;
-    for (int k = 0; k < p.segs * p.Bn; ++k) s += (double)p.part_c[(size_t)k * n + i];
+    const size_t n = (size_t)(p.N + 2) * p.Cn, i = (size_t)blockIdx.x * 32 + threadIdx.x;
+    const double s = slice_sum(p.part_c, p.segs * p.Bn, n);
+    if (threadIdx.x >= 32 || i >= n) return;
     const int m = (int)(i / p.Cn), c = (int)(i % p.Cn);
     if (m < p.N) {
         const size_t o = (size_t)c * p.N + m;
@@ -330,7 +329,7 @@ cudaError_t scan_bwd_launch(const ScanParams &p, cudaStream_t s) {
     timing_mark("scan_reduce", 1, s);
     if ((e = cudaGetLastError()) != cudaSuccess) return e;
     timing_mark("scan_reduce", 0, s);
-    scan_reduce_c_kernel<<<(unsigned)((m + 255) / 256), 256, 0, s>>>(p);
+    scan_reduce_c_kernel<<<(unsigned)((m + 31) / 32), 256, 0, s>>>(p);
     timing_mark("scan_reduce", 1, s);
     return cudaGetLastError();
 }

@@ -9,7 +9,10 @@ from __future__ import annotations
 
 import ctypes
 
-from .binding import GDN_OK, GdnError, _check, _dtype_code, _require_cuda, _torch, load_library
+import torch
+
+from .binding import GDN_OK, GdnError, _dtype_code, _require_cuda, load_library
+from .binding import _check as _check_in_words
 
 GDN_ACT_NONE, GDN_ACT_SILU, GDN_ACT_GELU = 0, 1, 2
 _ACTS = {"none": GDN_ACT_NONE, "silu": GDN_ACT_SILU, "gelu": GDN_ACT_GELU}
@@ -78,7 +81,14 @@ def _at(t):
 
 
 def _stream_of(stream, device):
-    return (stream if stream is not None else _torch().cuda.current_stream(device)).cuda_stream
+    return stream.cuda_stream if stream is not None else torch._C._cuda_getCurrentRawStream(device.index)
+
+
+def _check(name, t, shape, dtype, device):
+    """binding._check, whose comparisons in words run only for a tensor that one of these refuses: a
+    single-token call is shorter than its checks otherwise."""
+    if t.shape != shape or t.dtype is not dtype or t.device != device or not t.is_contiguous():
+        _check_in_words(name, t, shape, dtype, device)
 
 
 def _optional(name, t, shape, dtype, device):
@@ -89,9 +99,9 @@ def _optional(name, t, shape, dtype, device):
 def _rows(name, t, shape, dtype, device, inner=1):
     """Row stride (0: packed) of a tensor whose last `inner` dimensions are packed and whose leading
     ones follow each other at one stride, as a slice of a contiguous tensor along its last dimension."""
-    if tuple(t.shape) != tuple(shape):
+    if t.shape != shape:
         raise ValueError(f"{name} has shape {tuple(t.shape)}, expected {tuple(shape)}")
-    if t.dtype != dtype:
+    if t.dtype is not dtype:
         raise TypeError(f"{name} has dtype {t.dtype}, expected {dtype}")
     if t.device != device:
         raise ValueError(f"{name} is on {t.device}, expected {device}")
@@ -117,7 +127,7 @@ def _rows(name, t, shape, dtype, device, inner=1):
 def _scratch(name, t, need, device):
     """The caller's buffer, checked, or a new one for this call (None where nothing is needed)."""
     if t is None:
-        return _torch().empty(need, dtype=_torch().uint8, device=device) if need else None
+        return torch.empty(need, dtype=torch.uint8, device=device) if need else None
     if t.device != device or not t.is_contiguous():
         raise ValueError(f"{name} must be a contiguous tensor on {device}")
     return t
@@ -135,12 +145,11 @@ def _run(name, lib, shape, *args):
 
 def _check_lens(lens, B, dev):
     if lens is not None:
-        _check("lens", lens, (B,), _torch().int32, dev)
+        _check("lens", lens, (B,), torch.int32, dev)
 
 
 # ------------------------------------------------------------------- short causal convolution
 def _conv_args(x, w, bias, s0, lens, act):
-    torch = _torch()
     B, T, C = x.shape
     W = w.shape[-1]
     dev, dt = x.device, x.dtype
@@ -156,7 +165,6 @@ def gdn_conv_fwd(x, w, bias=None, s0=None, lens=None, *, act="silu", y=None, s_T
     """y, s_T = gdn_conv_fwd(x, w[, bias, s0, lens]) on CUDA tensors (see include/gdn.h): the short
     causal convolution of x [B, T, C] with taps w [C, W] and an activation ("silu" or "none"); s0 and
     s_T [B, W-1, C] are the carried inputs (with T = 1, s_T may be s0: updated in place)."""
-    torch = _torch()
     lib = _library()
     shape = _conv_args(x, w, bias, s0, lens, act)
     B, T, C, W, dev, dt = shape.B, shape.T, shape.C, shape.W, x.device, x.dtype
@@ -178,7 +186,6 @@ def gdn_conv_bwd_workspace_bytes(shape: GdnConvShape) -> int:
 def gdn_conv_bwd(x, w, dy, bias=None, s0=None, lens=None, ds_T=None, *, act="silu", workspace=None, want_ds0=True, stream=None):
     """dict(dx, dw, dbias, ds0) = gdn_conv_bwd(x, w, dy, ...) for the inputs of gdn_conv_fwd; dw and
     dbias are float32. ds0 is None with want_ds0=False."""
-    torch = _torch()
     lib = _library()
     shape = _conv_args(x, w, bias, s0, lens, act)
     B, T, C, W, dev, dt = shape.B, shape.T, shape.C, shape.W, x.device, x.dtype
@@ -196,7 +203,6 @@ def gdn_conv_bwd(x, w, dy, bias=None, s0=None, lens=None, ds_T=None, *, act="sil
 
 # ------------------------------------------------------------------ selective state space scan
 def _scan_args(u, dt, A_log, B, C, D, dt_bias, z, lens):
-    torch = _torch()
     Bn, T, Cn = u.shape
     G, N = B.shape[-2:]
     dev, ty = u.device, u.dtype
@@ -232,7 +238,6 @@ def gdn_scan_fwd(u, dt, A_log, B, C, D=None, dt_bias=None, z=None, h0=None, lens
     selective state space scan of u [B, T, C] with steps dt, state inputs and outputs B, C [B, T, G, N]
     and gate z. ckpt [B, ceil(T / 16), C, N] (want_ckpt=True) is what gdn_scan_bwd needs. With T = 1
     and no ckpt, h_T may be h0: the state updated in place."""
-    torch = _torch()
     lib = _library()
     shape = _scan_args(u, dt, A_log, B, C, D, dt_bias, z, lens)
     Bn, T, Cn, N, dev = shape.B, shape.T, shape.C, shape.N, u.device
@@ -257,7 +262,6 @@ def gdn_scan_bwd(u, dt, A_log, B, C, ckpt, dy, D=None, dt_bias=None, z=None, len
                  want_dh0=True, stream=None):
     """dict(du, ddt, dA_log, dB, dC, dD, ddt_bias, dz, dh0) = gdn_scan_bwd(...) for the inputs and the
     ckpt of gdn_scan_fwd. dD, ddt_bias and dz are None where their input was, dh0 with want_dh0=False."""
-    torch = _torch()
     lib = _library()
     shape = _scan_args(u, dt, A_log, B, C, D, dt_bias, z, lens)
     Bn, T, Cn, N, G, dev, ty = shape.B, shape.T, shape.C, shape.N, shape.G, u.device, u.dtype
@@ -281,7 +285,6 @@ def gdn_scan_bwd(u, dt, A_log, B, C, ckpt, dy, D=None, dt_bias=None, z=None, len
 
 # ---------------------------------------------------------------------------------- group norm
 def _norm_args(x, groups, w, b, z, act, eps, center):
-    torch = _torch()
     dev, dt = x.device, x.dtype
     C = x.shape[-1]
     if groups < 1 or C % groups != 0:
@@ -300,7 +303,6 @@ def gdn_norm_fwd(x, groups, w=None, b=None, z=None, *, act="silu", eps=1e-5, cen
     over the channels (last dimension) of every row of x, times w plus b, then the activation, or with
     a gate z the product with act(z). center=False: root mean square. stats [..., groups, 2] is what
     gdn_norm_bwd needs."""
-    torch = _torch()
     lib = _library()
     shape = _norm_args(x, groups, w, b, z, act, eps, center)
     dev = x.device
@@ -324,7 +326,6 @@ def gdn_norm_bwd(x, groups, stats, dy, w=None, b=None, z=None, *, act="silu", ep
                  stream=None):
     """dict(dx, dw, db, dz) = gdn_norm_bwd(x, groups, stats, dy[, w, b, z]) for the inputs and stats of
     gdn_norm_fwd; dw, db (float32) and dz are None where their input was."""
-    torch = _torch()
     lib = _library()
     shape = _norm_args(x, groups, w, b, z, act, eps, center)
     dev = x.device
@@ -363,7 +364,6 @@ def gdn_linear_fwd(x, W, bias=None, res=None, *, act="none", y=None, pre=None, w
     """y, pre = gdn_linear_fwd(x, W[, bias, res]) on CUDA tensors (see include/gdn.h):
     y = act(x W^T + bias) + res for x [..., K] and W [N, K]. pre (want_pre=True) is the
     pre-activation, which gdn_linear_bwd needs where act is not "none"."""
-    torch = _torch()
     lib = _library()
     shape, out_shape = _linear_args(x, W, bias, res, act)
     dev, dt = x.device, x.dtype
@@ -384,7 +384,6 @@ def gdn_linear_bwd(x, W, dy, pre=None, *, act="none", want_dx=True, want_dW=True
                    stream=None):
     """dict(dx, dW, dbias) = gdn_linear_bwd(x, W, dy[, pre]) for the inputs of gdn_linear_fwd (the
     gradient of res is dy itself). An entry is None with its want_... False."""
-    torch = _torch()
     lib = _library()
     shape, out_shape = _linear_args(x, W, None, None, act)
     dev, dt = x.device, x.dtype

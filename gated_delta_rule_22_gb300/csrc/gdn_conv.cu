@@ -78,14 +78,56 @@ __device__ __forceinline__ void load_taps(const ConvParams &p, int c, float2 (&w
     }
 }
 
+// A thread's own inputs of the next steps, kBlocks blocks of kStep steps: asynchronous copies into its
+// own places in shared memory (no other thread reads them, so no barrier is needed), which keep some
+// 50 KB per SM in flight without registers. Elements of 2 bytes alone (V = 1, bf16) are below the
+// smallest copy: they are loaded where they are used.
+constexpr int kStep = 4, kBlocks = 2;
+
+template <typename T, int V, int THREADS>
+struct Ring {
+    static constexpr bool kAsync = V * sizeof(T) >= 4;
+    static constexpr int kBytes = kAsync ? kBlocks * kStep * THREADS * V * (int)sizeof(T) : 0;
+    Raw<T, V> *mine;
+    const T *src;
+    long long ld;
+    int end;              // steps from `end` on read as zeros
+
+    __device__ __forceinline__ Ring(void *smem, const T *src, long long ld, int end)
+        : mine(static_cast<Raw<T, V> *>(smem) + threadIdx.x), src(src), ld(ld), end(end) {}
+    // starts the copies of steps t .. t + kStep - 1, block number blk
+    __device__ __forceinline__ void start(int blk, int t) {
+        if constexpr (kAsync) {
+#pragma unroll
+            for (int i = 0; i < kStep; ++i) {
+                const bool ok = t + i < end;
+                const T *from = ok ? src + (size_t)(t + i) * ld : src;
+                const uint32_t to = smem_addr(mine + ((blk & (kBlocks - 1)) * kStep + i) * THREADS);
+                if constexpr (V * sizeof(T) == 16)
+                    asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(to), "l"(from), "r"(ok ? 16 : 0) : "memory");
+                else
+                    asm volatile("cp.async.ca.shared.global [%0], [%1], %3, %2;" ::"r"(to), "l"(from),
+                                 "r"(ok ? (int)(V * sizeof(T)) : 0), "n"(V * (int)sizeof(T))
+                                 : "memory");
+            }
+        }
+    }
+    // step i of block blk, which begins at step t
+    __device__ __forceinline__ void get(int blk, int i, int t, float (&o)[V]) const {
+        if constexpr (kAsync) unpack<T, V>(mine[((blk & (kBlocks - 1)) * kStep + i) * THREADS], o);
+        else load_or_zero<T, V>(src + (size_t)(t + i) * ld, t + i < end, o);
+    }
+};
+
 }  // namespace
 
 // Threads over (batch row, run of `run` steps, V channels). The thread of a row's first run also
 // writes the state behind the row's last valid step. The next U steps' inputs are loaded before the
 // present ones are used; groups of U steps inside the row and the run take a path without tests.
 template <typename T, int W, int V>
-__global__ void __launch_bounds__(kConvThreads) conv_fwd_kernel(ConvParams p, int run, int runs) {
-    constexpr int U = 4, P = kPairs<V>;
+__global__ void __launch_bounds__(kConvThreads, 4) conv_fwd_kernel(ConvParams p, int run, int runs) {
+    constexpr int U = kStep, P = kPairs<V>;
+    extern __shared__ __align__(16) unsigned char smem[];
     const int CV = p.C / V;
     const size_t id = (size_t)blockIdx.x * kConvThreads + threadIdx.x;
     if (id >= (size_t)p.B * runs * CV) return;
@@ -96,15 +138,12 @@ __global__ void __launch_bounds__(kConvThreads) conv_fwd_kernel(ConvParams p, in
     const int t0 = r * run, t1 = min(t0 + run, p.T), t_in = min(t1, L);
     const T *x = static_cast<const T *>(p.x) + (size_t)b * p.T * p.ldx + c;
     T *y = static_cast<T *>(p.y) + (size_t)b * p.T * p.C + c;
-    Raw<T, V> next[U];
-    auto fetch = [&](int t) {
+    Ring<T, V, kConvThreads> in(smem, x, p.ldx, t_in);
 #pragma unroll
-        for (int i = 0; i < U; ++i) {
-            next[i] = Raw<T, V>();
-            if (t + i < t_in) next[i] = load_raw<T, V>(x + (size_t)(t + i) * p.ldx);
-        }
-    };
-    fetch(t0);
+    for (int k = 0; k < kBlocks - 1; ++k) {
+        in.start(k, t0 + k * U);
+        cp_async_commit();
+    }
     float2 w[W][P], bias[P], win[W][P];
     load_taps<W, V>(p, c, w, bias);
 #pragma unroll
@@ -121,36 +160,37 @@ __global__ void __launch_bounds__(kConvThreads) conv_fwd_kernel(ConvParams p, in
 #pragma unroll
         for (int j = 0; j < W - 1; ++j) store_vec<T, V>(out + (size_t)j * p.C, keep[j]);
     }
-    auto step = [&](const Raw<T, V> &in, int t, bool valid) {
+    auto step = [&](int blk, int i, int tb, bool valid) {
         float o[V], e[V];
-        unpack<T, V>(in, e);
+        in.get(blk, i, tb, e);
         to_pairs<V>(e, win[W - 1]);
         float2 pre[P];
 #pragma unroll
-        for (int i = 0; i < P; ++i) {
-            pre[i] = bias[i];
+        for (int q = 0; q < P; ++q) {
+            pre[q] = bias[q];
 #pragma unroll
-            for (int j = 0; j < W; ++j) pre[i] = __ffma2_rn(w[j][i], win[j][i], pre[i]);
+            for (int j = 0; j < W; ++j) pre[q] = __ffma2_rn(w[j][q], win[j][q], pre[q]);
 #pragma unroll
-            for (int j = 0; j < W - 1; ++j) win[j][i] = win[j + 1][i];
+            for (int j = 0; j < W - 1; ++j) win[j][q] = win[j + 1][q];
+            if (p.act == kActSilu) pre[q] = __fmul2_rn(pre[q], sigmoid2_hw(pre[q]));
         }
         from_pairs<V>(pre, o);
+        if (!valid)
 #pragma unroll
-        for (int v = 0; v < V; ++v) o[v] = valid ? (p.act == kActSilu ? silu_hw(o[v]) : o[v]) : 0.f;
-        store_vec<T, V>(y + (size_t)t * p.C, o);
+            for (int v = 0; v < V; ++v) o[v] = 0.f;
+        store_vec<T, V>(y + (size_t)(tb + i) * p.C, o);
     };
-    for (int t = t0; t < t1; t += U) {
-        Raw<T, V> in[U];
+    for (int tb = t0, blk = 0; tb < t1; tb += U, ++blk) {
+        in.start(blk + kBlocks - 1, tb + (kBlocks - 1) * U);
+        cp_async_commit();
+        cp_async_wait<kBlocks - 1>();
+        if (tb + U <= t_in) {
 #pragma unroll
-        for (int i = 0; i < U; ++i) in[i] = next[i];
-        fetch(t + U);
-        if (t + U <= t_in) {
-#pragma unroll
-            for (int i = 0; i < U; ++i) step(in[i], t + i, true);
+            for (int i = 0; i < U; ++i) step(blk, i, tb, true);
         } else {
 #pragma unroll
             for (int i = 0; i < U; ++i)
-                if (t + i < t1) step(in[i], t + i, t + i < L);
+                if (tb + i < t1) step(blk, i, tb, tb + i < L);
         }
     }
 }
@@ -162,8 +202,10 @@ __global__ void __launch_bounds__(kConvThreads) conv_fwd_kernel(ConvParams p, in
 // ascending order, into the CTA's slice of the partial sums: a fixed order.
 template <typename T, int W, int V>
 __global__ void __launch_bounds__(32 * kConvBwdWarps, 2) conv_bwd_kernel(ConvParams p, int run, int slices_row) {
-    __shared__ float sums[kConvBwdWarps][W + 1][32 * V];
-    constexpr int U = 4, P = kPairs<V>;
+    constexpr int U = kStep, P = kPairs<V>;
+    using In = Ring<T, V, 32 * kConvBwdWarps>;
+    extern __shared__ __align__(16) unsigned char smem[];
+    auto &sums = *reinterpret_cast<float(*)[kConvBwdWarps][W + 1][32 * V]>(smem);   // over the rings, behind the steps
     const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
     const int c = (blockIdx.y * 32 + lane) * V;
     const int b = blockIdx.x / slices_row, sl = blockIdx.x % slices_row;
@@ -183,34 +225,32 @@ __global__ void __launch_bounds__(32 * kConvBwdWarps, 2) conv_bwd_kernel(ConvPar
         const T *ds_T = static_cast<const T *>(p.ds_T) + (size_t)b * (W - 1) * p.C + c;
         T *dx = static_cast<T *>(p.dx) + (size_t)b * p.T * p.C + c;
         T *ds0 = static_cast<T *>(p.ds0) + (size_t)b * (W - 1) * p.C + c;
-        Raw<T, V> next_x[U], next_d[U];
-        auto fetch = [&](int t) {
-#pragma unroll
-            for (int i = 0; i < U; ++i) {
-                next_x[i] = next_d[i] = Raw<T, V>();
-                if (t + i < t_in) {
-                    next_x[i] = load_raw<T, V>(x + (size_t)(t + i) * p.ldx);
-                    next_d[i] = load_raw<T, V>(dy + (size_t)(t + i) * p.C);
-                }
-            }
+        In in_x(smem, x, p.ldx, t_in), in_d(smem + In::kBytes, dy, p.C, t_in);
+        auto start = [&](int blk, int t) {
+            in_x.start(blk, t);
+            in_d.start(blk, t);
+            cp_async_commit();
         };
-        fetch(t0);
+#pragma unroll
+        for (int k = 0; k < kBlocks - 1; ++k) start(k, t0 + k * U);
         float2 w[W][P], bias[P], win[W][P], dwin[W][P];
         load_taps<W, V>(p, c, w, bias);
         // dpre of one step from the window whose newest input is in place, into dwin[W - 1]
         auto grad = [&](const float (&d)[V], bool valid) {
-            float2 pre[P];
-            float e[V];
+            float2 dd[P];
+            to_pairs<V>(d, dd);
 #pragma unroll
-            for (int i = 0; i < P; ++i) {
-                pre[i] = bias[i];
+            for (int q = 0; q < P; ++q) {
+                float2 pre = bias[q];
 #pragma unroll
-                for (int j = 0; j < W; ++j) pre[i] = __ffma2_rn(w[j][i], win[j][i], pre[i]);
+                for (int j = 0; j < W; ++j) pre = __ffma2_rn(w[j][q], win[j][q], pre);
+                if (p.act == kActSilu) {              // silu' = s (1 + pre (1 - s))
+                    const float2 one = make_float2(1.f, 1.f), sg = sigmoid2_hw(pre);
+                    const float2 up = __ffma2_rn(pre, __ffma2_rn(sg, make_float2(-1.f, -1.f), one), one);
+                    dd[q] = __fmul2_rn(dd[q], __fmul2_rn(sg, up));
+                }
+                dwin[W - 1][q] = valid ? dd[q] : make_float2(0.f, 0.f);
             }
-            from_pairs<V>(pre, e);
-#pragma unroll
-            for (int v = 0; v < V; ++v) e[v] = valid ? (p.act == kActSilu ? d[v] * dsilu_hw(e[v]) : d[v]) : 0.f;
-            to_pairs<V>(e, dwin[W - 1]);
         };
         auto shift = [&](float2(&a)[W][P]) {
 #pragma unroll
@@ -238,39 +278,34 @@ __global__ void __launch_bounds__(32 * kConvBwdWarps, 2) conv_bwd_kernel(ConvPar
             shift(win);
         }
         // one step: the sums, and dx of the input W-1 steps back
-        auto step = [&](const Raw<T, V> &xin, const Raw<T, V> &din, bool valid, float (&o)[V]) {
+        auto step = [&](int blk, int i, int tb, bool valid, float (&o)[V]) {
             float e[V], d[V];
-            unpack<T, V>(xin, e);
-            unpack<T, V>(din, d);
+            in_x.get(blk, i, tb, e);
+            in_d.get(blk, i, tb, d);
             to_pairs<V>(e, win[W - 1]);
             grad(d, valid);
             float2 s[P];
 #pragma unroll
-            for (int i = 0; i < P; ++i) {
-                db[i] = __fadd2_rn(db[i], dwin[W - 1][i]);
+            for (int q = 0; q < P; ++q) {
+                db[q] = __fadd2_rn(db[q], dwin[W - 1][q]);
 #pragma unroll
-                for (int j = 0; j < W; ++j) dw[j][i] = __ffma2_rn(dwin[W - 1][i], win[j][i], dw[j][i]);
-                s[i] = __fmul2_rn(w[0][i], dwin[W - 1][i]);
+                for (int j = 0; j < W; ++j) dw[j][q] = __ffma2_rn(dwin[W - 1][q], win[j][q], dw[j][q]);
+                s[q] = __fmul2_rn(w[0][q], dwin[W - 1][q]);
 #pragma unroll
-                for (int j = 1; j < W; ++j) s[i] = __ffma2_rn(w[j][i], dwin[W - 1 - j][i], s[i]);
+                for (int j = 1; j < W; ++j) s[q] = __ffma2_rn(w[j][q], dwin[W - 1 - j][q], s[q]);
             }
             from_pairs<V>(s, o);
             shift(win);
             shift(dwin);
         };
-        for (int tb = t0; tb < t_end; tb += U) {
-            Raw<T, V> xin[U], din[U];
-#pragma unroll
-            for (int i = 0; i < U; ++i) {
-                xin[i] = next_x[i];
-                din[i] = next_d[i];
-            }
-            fetch(tb + U);
+        for (int tb = t0, blk = 0; tb < t_end; tb += U, ++blk) {
+            start(blk + kBlocks - 1, tb + (kBlocks - 1) * U);
+            cp_async_wait<kBlocks - 1>();
             float o[V];
             if (tb >= W - 1 && tb + U <= t_in) {      // inside the row: the state takes no part
 #pragma unroll
                 for (int i = 0; i < U; ++i) {
-                    step(xin[i], din[i], true, o);
+                    step(blk, i, tb, true, o);
                     store_vec<T, V>(dx + (size_t)(tb + i - (W - 1)) * p.C, o);
                 }
                 continue;
@@ -279,7 +314,7 @@ __global__ void __launch_bounds__(32 * kConvBwdWarps, 2) conv_bwd_kernel(ConvPar
             for (int i = 0; i < U; ++i) {
                 const int t = tb + i, s = t - (W - 1);
                 if (t >= t_end) break;
-                step(xin[i], din[i], t < L, o);
+                step(blk, i, tb, t < L, o);
                 // s is input s of the row, or row t of the state in front of it; either may be one of
                 // the W-1 inputs behind the last valid step
                 const int j = s - (L - (W - 1));
@@ -294,6 +329,8 @@ __global__ void __launch_bounds__(32 * kConvBwdWarps, 2) conv_bwd_kernel(ConvPar
             }
         }
     }
+    cp_async_wait<0>();
+    __syncthreads();
 #pragma unroll
     for (int j = 0; j <= W; ++j) {
         float e[V];
@@ -328,10 +365,10 @@ bool conv_aligned(const ConvParams &p, int V, size_t e) {
     return p.C % V == 0 && p.ldx % V == 0 && (uintptr_t)p.x % (V * e) == 0;
 }
 
-// Steps per warp of the backward: up to 32, fewer while that leaves under 512 CTAs (3 per SM).
+// Steps per warp of the backward: up to 128, fewer while that leaves under 512 CTAs (3 per SM).
 int conv_bwd_run(const ConvParams &p) {
     int run = (p.T + kConvBwdWarps - 1) / kConvBwdWarps;
-    run = run > 32 ? 32 : run;
+    run = run > 128 ? 128 : run;
     const long long cols = (p.C + 127) / 128;
     while (run > 8 && cols * p.B * ((p.T + kConvBwdWarps * run - 1) / (kConvBwdWarps * run)) < 512) run /= 2;
     return run;
@@ -339,15 +376,20 @@ int conv_bwd_run(const ConvParams &p) {
 
 template <typename T, int W, int V>
 cudaError_t conv_fwd_launch(const ConvParams &p, cudaStream_t s) {
-    // Steps per thread: each run reads W-1 inputs again, so up to 32, fewer while the threads would
+    // Steps per thread: each run reads W-1 inputs again, so up to 64, fewer while the threads would
     // not fill the SMs.
     const size_t cv = p.C / V;
-    int run = 32;
+    int run = 64;
     while (run > 1 && (size_t)p.B * ((p.T + run - 1) / run) * cv < (size_t)152 * 1024) run /= 2;
     const int runs = (p.T + run - 1) / run;
     const size_t n = (size_t)p.B * runs * cv;
     timing_mark("conv_fwd", 0, s);
-    conv_fwd_kernel<T, W, V><<<(unsigned)((n + kConvThreads - 1) / kConvThreads), kConvThreads, 0, s>>>(p, run, runs);
+    constexpr int smem = Ring<T, V, kConvThreads>::kBytes;
+    if (smem > 48 * 1024) {
+        const cudaError_t e = cudaFuncSetAttribute(conv_fwd_kernel<T, W, V>, cudaFuncAttributeMaxDynamicSharedMemorySize, smem);
+        if (e != cudaSuccess) return e;
+    }
+    conv_fwd_kernel<T, W, V><<<(unsigned)((n + kConvThreads - 1) / kConvThreads), kConvThreads, smem, s>>>(p, run, runs);
     timing_mark("conv_fwd", 1, s);
     return cudaGetLastError();
 }
@@ -357,9 +399,13 @@ cudaError_t conv_bwd_launch(const ConvParams &p, cudaStream_t s) {
     const int run = conv_bwd_run(p), slices_row = (p.T + kConvBwdWarps * run - 1) / (kConvBwdWarps * run);
     const int slices = p.B * slices_row;
     timing_mark("conv_bwd", 0, s);
-    conv_bwd_kernel<T, W, V><<<dim3(slices, (p.C + 32 * V - 1) / (32 * V)), 32 * kConvBwdWarps, 0, s>>>(p, run, slices_row);
+    constexpr int ring = 2 * Ring<T, V, 32 * kConvBwdWarps>::kBytes, sums = kConvBwdWarps * (W + 1) * 32 * V * 4;
+    constexpr int smem = ring > sums ? ring : sums;
+    cudaError_t e = cudaFuncSetAttribute(conv_bwd_kernel<T, W, V>, cudaFuncAttributeMaxDynamicSharedMemorySize, smem);
+    if (e != cudaSuccess) return e;
+    conv_bwd_kernel<T, W, V><<<dim3(slices, (p.C + 32 * V - 1) / (32 * V)), 32 * kConvBwdWarps, smem, s>>>(p, run, slices_row);
     timing_mark("conv_bwd", 1, s);
-    cudaError_t e = cudaGetLastError();
+    e = cudaGetLastError();
     if (e != cudaSuccess) return e;
     timing_mark("conv_reduce", 0, s);
     conv_reduce_kernel<<<(unsigned)(((size_t)(W + 1) * p.C + 31) / 32), 256, 0, s>>>(p, slices);

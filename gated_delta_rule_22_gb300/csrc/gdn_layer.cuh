@@ -106,6 +106,11 @@ __device__ __forceinline__ float rcp(float x) {
 // 1 / (1 + exp(-x)) from the hardware's exp2 and reciprocal: a relative error of a few 2^-23 (an
 // exponent that overflows gives 1 / inf = 0).
 __device__ __forceinline__ float sigmoid_hw(float x) { return rcp(1.f + ex2(-x * kLog2e)); }
+__device__ __forceinline__ float2 sigmoid2_hw(float2 x) {
+    const float2 e = __fmul2_rn(x, make_float2(-kLog2e, -kLog2e));
+    const float2 d = __fadd2_rn(make_float2(ex2(e.x), ex2(e.y)), make_float2(1.f, 1.f));
+    return make_float2(rcp(d.x), rcp(d.y));
+}
 __device__ __forceinline__ float silu_hw(float x) { return x * sigmoid_hw(x); }
 __device__ __forceinline__ float dsilu_hw(float x) {
     const float s = sigmoid_hw(x);

@@ -129,8 +129,34 @@ template <int ACT>
 __device__ __forceinline__ float dact_f(float x) {
     return ACT == kActSilu ? dsilu_hw(x) : ACT == kActGelu ? dgelu_f(x) : 1.f;
 }
-// softplus with its full relative accuracy for very negative x (log1p(e) ~ e)
-__device__ __forceinline__ float softplus_full(float x) { return x > 20.f ? x : log1pf(expf(x)); }
+// softplus(x) = max(x, 0) + log1p(exp(-|x|)), and the logistic function of x from the same exponential.
+// exp(-|x|): the product with log2 e is carried to twice float32, so that the hardware's exp2 sees no
+// rounded argument. log1p(e) for e in [0, 1]: 2 atanh(e / (2 + e)) by the series of atanh, whose
+// argument is at most 1/3 (seven terms: 1.4e-8 relative), with full relative accuracy for small e.
+__device__ __forceinline__ void softplus_full(float x, float &sp, float &sg) {
+    const float ax = fminf(fabsf(x), 200.f), hi = -ax * kLog2e;
+    const float lo = fmaf(-ax, 1.925963033e-8f, fmaf(-ax, kLog2e, -hi));
+    float e = ex2(hi);
+    e = fmaf(e, lo * 0.69314718f, e);
+    const float d = 2.f + e, r = rcp(d);
+    float s = e * r;
+    s = fmaf(r, fmaf(-s, d, e), s);
+    const float q = s * s;
+    float f = fmaf(q, 1.f / 13.f, 1.f / 11.f);
+    f = fmaf(q, f, 1.f / 9.f);
+    f = fmaf(q, f, 1.f / 7.f);
+    f = fmaf(q, f, 1.f / 5.f);
+    f = fmaf(q, f, 1.f / 3.f);
+    f = fmaf(q, f, 1.f);
+    sp = fmaf(2.f * s, f, x <= 0.f ? 0.f : x);      // a NaN stays one
+    const float r1 = rcp(1.f + e);
+    sg = x >= 0.f ? r1 : e * r1;
+}
+__device__ __forceinline__ float softplus_full(float x) {
+    float sp, sg;
+    softplus_full(x, sp, sg);
+    return sp;
+}
 
 // V consecutive elements as float, from an address aligned to V elements
 template <typename T, int V>

@@ -12,14 +12,14 @@
 namespace gdn {
 
 // LITE: the segment's end state from a zero start and its sum of d, nothing else (first pass over a
-// split sequence).
-template <int LPC, typename T, bool LITE>
-__global__ void __launch_bounds__(kScanThreads) scan_fwd_kernel(ScanParams p, bool vec) {
+// split sequence). The next tile's inputs are loaded while a tile is walked.
+template <int LPC, typename T, bool VEC, bool LITE>
+__global__ void __launch_bounds__(kScanThreads) scan_fwd_kernel(ScanParams p) {
     using G = ScanGeo<LPC>;
     constexpr int CH = G::CH, NP = G::NP, V = G::V, KB = G::KB, TT = kScanTile;
     __shared__ float2 sdx[TT][CH];              // d, d u
     __shared__ __align__(16) float sB[TT][NP], sC[TT][NP];
-    __shared__ float score[TT][CH + 1];
+    __shared__ float score[TT][G::SP];
     const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
     const ScanPlace q = scan_place<LPC>(p);
     if (q.first >= q.last) return;
@@ -35,9 +35,29 @@ __global__ void __launch_bounds__(kScanThreads) scan_fwd_kernel(ScanParams p, bo
     const T *z = static_cast<const T *>(p.z) + (size_t)q.b * p.T * p.ldz + q.c0 + cv;
     const T *Bm = static_cast<const T *>(p.B) + (size_t)q.b * p.T * p.ldB + q.g * p.N;
     const T *Cm = static_cast<const T *>(p.C) + (size_t)q.b * p.T * p.ldC + q.g * p.N;
-    float A2[4], h[4] = {0.f, 0.f, 0.f, 0.f}, D[V], bias[V], sum_d[V];
+    Staged<T, V, VEC> ru, rd, rz;
+    T rB[KB], rC[KB];
+    auto fetch = [&](int tile) {
+        const int t = tile * TT + ts, n = t < L ? nv : 0;
+        ru.load(u + (size_t)t * p.ldu, n);
+        rd.load(dt + (size_t)t * p.lddt, n);
+        if (!LITE && p.z != nullptr) rz.load(z + (size_t)t * p.ldz, n);
 #pragma unroll
-    for (int k = 0; k < 4; ++k) A2[k] = n0 + k < p.N ? -expf(p.A_log[(size_t)c * p.N + n0 + k]) * kLog2e : 0.f;
+        for (int k = 0; k < KB; ++k) {
+            const int e = tid + kScanThreads * k, tb = tile * TT + e / NP, n1 = e % NP;
+            const bool ok = tb < L && n1 < p.N;
+            rB[k] = rC[k] = from_f32<T>(0.f);
+            if (ok) rB[k] = Bm[(size_t)tb * p.ldB + n1];
+            if (!LITE && ok) rC[k] = Cm[(size_t)tb * p.ldC + n1];
+        }
+    };
+    fetch(q.first);
+    float2 A2[2], h[2] = {make_float2(0.f, 0.f), make_float2(0.f, 0.f)};
+    float al[4], D[V], bias[V], sum_d[V];
+#pragma unroll
+    for (int k = 0; k < 4; ++k) al[k] = n0 + k < p.N ? -expf(p.A_log[(size_t)c * p.N + n0 + k]) * kLog2e : 0.f;
+    A2[0] = make_float2(al[0], al[1]);
+    A2[1] = make_float2(al[2], al[3]);
 #pragma unroll
     for (int v = 0; v < V; ++v) {
         D[v] = p.D != nullptr && v < nv ? p.D[q.c0 + cv + v] : 0.f;
@@ -45,80 +65,78 @@ __global__ void __launch_bounds__(kScanThreads) scan_fwd_kernel(ScanParams p, bo
         sum_d[v] = 0.f;
     }
     const size_t state_row = ((size_t)q.b * p.Cn + c) * p.N;
+    float hs[4] = {0.f, 0.f, 0.f, 0.f};
     if (!LITE && live) {
-        if (p.segs > 1) load_states(p.seg_state + (size_t)q.seg * p.Bn * p.Cn * p.N + state_row, n0, p.N, h);
-        else if (p.h0 != nullptr) load_states(p.h0 + state_row, n0, p.N, h);
+        if (p.segs > 1) load_states(p.seg_state + (size_t)q.seg * p.Bn * p.Cn * p.N + state_row, n0, p.N, hs);
+        else if (p.h0 != nullptr) load_states(p.h0 + state_row, n0, p.N, hs);
     }
-    float ru[V], rd[V], rz[V], rB[KB], rC[KB];
-    auto fetch = [&](int tile) {
-        const int t = tile * TT + ts, n = t < L ? nv : 0;
-        load_channels<T, V>(u + (size_t)t * p.ldu, n, vec, ru);
-        load_channels<T, V>(dt + (size_t)t * p.lddt, n, vec, rd);
-        if (!LITE && p.z != nullptr) load_channels<T, V>(z + (size_t)t * p.ldz, n, vec, rz);
-#pragma unroll
-        for (int k = 0; k < KB; ++k) {
-            const int e = tid + kScanThreads * k, tb = tile * TT + e / NP, n1 = e % NP;
-            const bool ok = tb < L && n1 < p.N;
-            rB[k] = ok ? to_f32(Bm[(size_t)tb * p.ldB + n1]) : 0.f;
-            if (!LITE) rC[k] = ok ? to_f32(Cm[(size_t)tb * p.ldC + n1]) : 0.f;
-        }
-    };
-    fetch(q.first);
+    h[0] = make_float2(hs[0], hs[1]);
+    h[1] = make_float2(hs[2], hs[3]);
     for (int tile = q.first; tile < q.last; ++tile) {
         const int t = tile * TT + ts;
-        float cu[V], cz[V];
+        float cu[V], cd[V];
+        ru.get(cu);
+        rd.get(cd);
+        const Staged<T, V, VEC> cz = rz;
 #pragma unroll
         for (int v = 0; v < V; ++v) {
-            cu[v] = ru[v];
-            cz[v] = rz[v];
-            const float d = t < L ? softplus_full(rd[v] + bias[v]) : 0.f;
+            const float d = t < L ? softplus_full(cd[v] + bias[v]) : 0.f;
             sum_d[v] += d;
-            sdx[ts][cv + v] = make_float2(d, d * ru[v]);
+            sdx[ts][cv + v] = make_float2(d, d * cu[v]);
         }
 #pragma unroll
         for (int k = 0; k < KB; ++k) {
             const int e = tid + kScanThreads * k;
-            sB[e / NP][e % NP] = rB[k];
-            if (!LITE) sC[e / NP][e % NP] = rC[k];
+            sB[e / NP][e % NP] = to_f32(rB[k]);
+            if (!LITE) sC[e / NP][e % NP] = to_f32(rC[k]);
         }
         __syncthreads();
         if (tile + 1 < q.last) fetch(tile + 1);
         if (!LITE && p.ckpt != nullptr && live) {
             const int tiles = (p.T + TT - 1) / TT;
-            store_states(p.ckpt + (((size_t)q.b * tiles + tile) * p.Cn + c) * p.N, n0, p.N, h);
+            const float o[4] = {h[0].x, h[0].y, h[1].x, h[1].y};
+            store_states(p.ckpt + (((size_t)q.b * tiles + tile) * p.Cn + c) * p.N, n0, p.N, o);
         }
 #pragma unroll
-        for (int i = 0; i < TT; ++i) {
-            const float2 dx = sdx[i][ch];
-            const float4 b4 = *reinterpret_cast<const float4 *>(&sB[i][n0]);
-            const float bb[4] = {b4.x, b4.y, b4.z, b4.w};
-            float core = 0.f;
-            float4 c4 = make_float4(0.f, 0.f, 0.f, 0.f);
-            if (!LITE) c4 = *reinterpret_cast<const float4 *>(&sC[i][n0]);
-            const float cc[4] = {c4.x, c4.y, c4.z, c4.w};
+        for (int i0 = 0; i0 < TT; i0 += 4) {
+            float core[4];
 #pragma unroll
-            for (int k = 0; k < 4; ++k) {
-                h[k] = fmaf(ex2(dx.x * A2[k]), h[k], dx.y * bb[k]);
-                if (!LITE) core = fmaf(cc[k], h[k], core);
+            for (int i = 0; i < 4; ++i) {
+                const float2 dx = sdx[i0 + i][ch];
+                const float4 b4 = *reinterpret_cast<const float4 *>(&sB[i0 + i][n0]);
+                const float2 b2[2] = {make_float2(b4.x, b4.y), make_float2(b4.z, b4.w)};
+                float4 c4 = make_float4(0.f, 0.f, 0.f, 0.f);
+                if (!LITE) c4 = *reinterpret_cast<const float4 *>(&sC[i0 + i][n0]);
+                const float2 c2[2] = {make_float2(c4.x, c4.y), make_float2(c4.z, c4.w)};
+                float2 sum;
+#pragma unroll
+                for (int k = 0; k < 2; ++k) {
+                    const float2 x = __fmul2_rn(make_float2(dx.x, dx.x), A2[k]);
+                    h[k] = __ffma2_rn(make_float2(ex2(x.x), ex2(x.y)), h[k], __fmul2_rn(make_float2(dx.y, dx.y), b2[k]));
+                    if (!LITE) sum = k == 0 ? __fmul2_rn(c2[0], h[0]) : __ffma2_rn(c2[1], h[1], sum);
+                }
+                if (!LITE) core[i] = sum.x + sum.y;
             }
             if (!LITE) {
-                core = lane_sum<LPC>(core);
-                if (lane % LPC == 0) score[i][ch] = core;
+                const float r = lane_sum4<LPC>(core, lane);
+                if (lane % LPC < 4) score[i0 + (lane & 3)][ch] = r;
             }
         }
         __syncthreads();
         if (!LITE && t < p.T) {
-            float o[V];
+            float o[V], zz[V];
+            cz.get(zz);
 #pragma unroll
             for (int v = 0; v < V; ++v) {
                 const float core = fmaf(D[v], cu[v], score[ts][cv + v]);
-                o[v] = t < L ? (p.z != nullptr ? core * silu_hw(cz[v]) : core) : 0.f;
+                o[v] = t < L ? (p.z != nullptr ? core * silu_hw(zz[v]) : core) : 0.f;
             }
-            store_channels<T, V>(static_cast<T *>(p.y) + ((size_t)q.b * p.T + t) * p.Cn + q.c0 + cv, nv, vec, o);
+            store_channels<T, V>(static_cast<T *>(p.y) + ((size_t)q.b * p.T + t) * p.Cn + q.c0 + cv, nv, VEC, o);
         }
     }
+    const float out[4] = {h[0].x, h[0].y, h[1].x, h[1].y};
     if (LITE) {
-        if (live) store_states(p.seg_state + (size_t)q.seg * p.Bn * p.Cn * p.N + state_row, n0, p.N, h);
+        if (live) store_states(p.seg_state + (size_t)q.seg * p.Bn * p.Cn * p.N + state_row, n0, p.N, out);
         // the sum of d over the segment: over a thread's tiles, then over the 16 steps of a tile
 #pragma unroll
         for (int v = 0; v < V; ++v) score[ts][cv + v] = sum_d[v];
@@ -128,8 +146,8 @@ __global__ void __launch_bounds__(kScanThreads) scan_fwd_kernel(ScanParams p, bo
             for (int i = 0; i < TT; ++i) a += score[i][tid];
             p.seg_sum[((size_t)q.seg * p.Bn + q.b) * p.Cn + q.c0 + tid] = a;
         }
-    } else if (p.h_T != nullptr && live && (p.segs == 1 || q.seg == p.segs - 1)) {
-        store_states(p.h_T + state_row, n0, p.N, h);
+    } else if (p.h_T != nullptr && live && q.seg == p.segs - 1) {
+        store_states(p.h_T + state_row, n0, p.N, out);
     }
 }
 
@@ -219,6 +237,23 @@ void scan_split(ScanParams *p) {
 
 namespace {
 
+template <int LPC, typename T, bool VEC>
+cudaError_t scan_fwd_prompt(const ScanParams &p, cudaStream_t s) {
+    const dim3 grid(p.Bn * p.G * scan_blocks(p.Cn, p.G, p.N), p.segs);
+    cudaError_t e;
+    if (p.segs > 1) {
+        timing_mark("scan_fwd_ends", 0, s);
+        scan_fwd_kernel<LPC, T, VEC, true><<<grid, kScanThreads, 0, s>>>(p);
+        timing_mark("scan_fwd_ends", 1, s);
+        if ((e = cudaGetLastError()) != cudaSuccess) return e;
+        if ((e = launch_scan_combine(p, p.h0, nullptr, false, s)) != cudaSuccess) return e;
+    }
+    timing_mark("scan_fwd", 0, s);
+    scan_fwd_kernel<LPC, T, VEC, false><<<grid, kScanThreads, 0, s>>>(p);
+    timing_mark("scan_fwd", 1, s);
+    return cudaGetLastError();
+}
+
 template <int LPC, typename T>
 cudaError_t scan_fwd_launch(const ScanParams &p, cudaStream_t s) {
     if (p.T == 1 && p.ckpt == nullptr) {
@@ -228,20 +263,7 @@ cudaError_t scan_fwd_launch(const ScanParams &p, cudaStream_t s) {
         timing_mark("scan_step", 1, s);
         return cudaGetLastError();
     }
-    const dim3 grid(p.Bn * p.G * scan_blocks(p.Cn, p.G, p.N), p.segs);
-    const bool vec = scan_vec<T>(p, ScanGeo<LPC>::V);
-    cudaError_t e;
-    if (p.segs > 1) {
-        timing_mark("scan_fwd_ends", 0, s);
-        scan_fwd_kernel<LPC, T, true><<<grid, kScanThreads, 0, s>>>(p, vec);
-        timing_mark("scan_fwd_ends", 1, s);
-        if ((e = cudaGetLastError()) != cudaSuccess) return e;
-        if ((e = launch_scan_combine(p, p.h0, nullptr, false, s)) != cudaSuccess) return e;
-    }
-    timing_mark("scan_fwd", 0, s);
-    scan_fwd_kernel<LPC, T, false><<<grid, kScanThreads, 0, s>>>(p, vec);
-    timing_mark("scan_fwd", 1, s);
-    return cudaGetLastError();
+    return scan_vec<T>(p, ScanGeo<LPC>::V) ? scan_fwd_prompt<LPC, T, true>(p, s) : scan_fwd_prompt<LPC, T, false>(p, s);
 }
 
 template <typename T>

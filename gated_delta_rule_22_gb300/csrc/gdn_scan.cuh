@@ -23,18 +23,36 @@ struct ScanGeo {
     static constexpr int NP = 4 * LPC;                      // states per channel, padded
     static constexpr int V = CH * kScanTile / kScanThreads; // staged elements per thread (4, 2, 1)
     static constexpr int KB = NP * kScanTile / kScanThreads;// staged elements of B (of C) per thread
+    static constexpr int SP = CH + CPW;                     // pitch of a row of sums: no bank conflicts
 };
 
-// V elements from channel position p on; those past `n` are zero.
-template <typename T, int V>
-__device__ __forceinline__ void load_channels(const T *p, int n, bool vec, float (&o)[V]) {
-    if (vec && n >= V) {
-        load_vec<T, V>(p, o);
-    } else {
-#pragma unroll
-        for (int v = 0; v < V; ++v) o[v] = v < n ? to_f32(p[v]) : 0.f;
+// V staged elements as they were loaded. VEC: one access of V elements where all of them exist; the
+// others one by one. They are turned into floats only where they are used, a tile later: an instruction
+// that needs them earlier would wait for memory.
+template <typename T, int V, bool VEC>
+struct Staged {
+    Raw<T, V> raw;
+    __device__ __forceinline__ void load(const T *p, int n) {
+        raw = Raw<T, V>();
+        if (n > 0) raw = load_raw<T, V>(p);
     }
-}
+    __device__ __forceinline__ void get(float (&o)[V]) const { unpack<T, V>(raw, o); }
+};
+template <typename T, int V>
+struct Staged<T, V, false> {
+    T e[V];
+    __device__ __forceinline__ void load(const T *p, int n) {
+#pragma unroll
+        for (int v = 0; v < V; ++v) {
+            e[v] = from_f32<T>(0.f);
+            if (v < n) e[v] = p[v];
+        }
+    }
+    __device__ __forceinline__ void get(float (&o)[V]) const {
+#pragma unroll
+        for (int v = 0; v < V; ++v) o[v] = to_f32(e[v]);
+    }
+};
 template <typename T, int V>
 __device__ __forceinline__ void store_channels(T *p, int n, bool vec, const float (&o)[V]) {
     if (vec && n >= V) {
@@ -64,6 +82,19 @@ __device__ __forceinline__ void store_states(float *p, int n0, int N, const floa
         for (int k = 0; k < 4; ++k)
             if (n0 + k < N) p[n0 + k] = o[k];
     }
+}
+
+// Sums four values (steps i0 .. i0 + 3) over the LPC lanes of a channel by exchanging halves: the
+// lanes with lane % 4 = j get the sum of value j.
+template <int LPC>
+__device__ __forceinline__ float lane_sum4(const float (&v)[4], int lane) {
+    const bool up2 = lane & 2, up1 = lane & 1;
+    const float a = (up2 ? v[2] : v[0]) + __shfl_xor_sync(kFullMask, up2 ? v[0] : v[2], 2);
+    const float b = (up2 ? v[3] : v[1]) + __shfl_xor_sync(kFullMask, up2 ? v[1] : v[3], 2);
+    float r = (up1 ? b : a) + __shfl_xor_sync(kFullMask, up1 ? a : b, 1);
+#pragma unroll
+    for (int m = 4; m < LPC; m <<= 1) r += __shfl_xor_sync(kFullMask, r, m);
+    return r;
 }
 
 // Sum over the LPC lanes of a channel.

@@ -352,11 +352,11 @@ __global__ void __launch_bounds__(32 * kConvBwdWarps, 2) conv_bwd_kernel(ConvPar
 // dw[c][j] and dbias[c] from the slices' partial sums.
 __global__ void __launch_bounds__(256) conv_reduce_kernel(ConvParams p, int slices) {
     const size_t n = (size_t)(p.W + 1) * p.C, i = (size_t)blockIdx.x * 32 + threadIdx.x;
-    const double a = slice_sum(p.part, slices, n);
+    const float a = slice_sum(p.part, slices, n);
     if (threadIdx.x >= 32 || i >= n) return;
     const int j = (int)(i / p.C), c = (int)(i % p.C);
-    if (j < p.W) p.dw[(size_t)c * p.W + j] = (float)a;
-    else if (p.dbias != nullptr) p.dbias[c] = (float)a;
+    if (j < p.W) p.dw[(size_t)c * p.W + j] = a;
+    else if (p.dbias != nullptr) p.dbias[c] = a;
 }
 
 namespace {

@@ -74,7 +74,7 @@ constexpr int kScanTile = 16;   // steps between the scan's checkpoints, and of 
 int conv_bwd_slices(const ConvParams &p);
 int scan_lanes(int N);                              // lanes that share one channel's states
 int scan_blocks(int C, int G, int N);               // channel blocks of one group
-void scan_split(ScanParams *p);                     // chooses segs and seg_len
+void scan_split(ScanParams *p, bool bwd);           // chooses segs and seg_len
 int norm_bwd_slices(int M, int G, int D, int dtype);
 size_t linear_fwd_workspace(const LinearParams &p, int dtype);
 size_t linear_bwd_workspace(const LinearParams &p, int dtype);
@@ -239,25 +239,34 @@ __device__ __forceinline__ void unpack(const Raw<T, V> &r, float (&o)[V]) {
     load_vec<T, V>(reinterpret_cast<const T *>(&r), o);
 }
 
+// x + y in float32, what the addition lost added to `lost` (two-sum).
+__device__ __forceinline__ void add_comp(float &x, float &lost, float y) {
+    const float s = __fadd_rn(x, y), bb = __fadd_rn(s, -x);
+    lost = __fadd_rn(lost, __fadd_rn(__fadd_rn(x, -__fadd_rn(s, -bb)), __fadd_rn(y, -bb)));
+    x = s;
+}
+
 // Sum over the slices of partial sums part[slice][n] of column blockIdx.x * 32 + threadIdx.x % 32, for
 // a CTA of 256 threads: eight threads take every eighth slice of a column, then their sums are added in
-// order (float64 throughout: the order is fixed and the sum is exact to float32). Valid in the first
-// 32 threads.
-__device__ __forceinline__ double slice_sum(const float *part, int slices, size_t n) {
-    __shared__ double sums[8][32];
+// order. Compensated float32: as exact as float64 here, whose rate on this GPU is a sixty-fourth. Valid
+// in the first 32 threads.
+__device__ __forceinline__ float slice_sum(const float *part, int slices, size_t n) {
+    __shared__ float2 sums[8][32];
     const int col = threadIdx.x & 31, lane = threadIdx.x >> 5;
     const size_t i = (size_t)blockIdx.x * 32 + col;
-    double a = 0.0;
+    float a = 0.f, lost = 0.f;
     if (i < n)
 #pragma unroll 4
-        for (int s = lane; s < slices; s += 8) a += (double)part[(size_t)s * n + i];
-    sums[lane][col] = a;
+        for (int s = lane; s < slices; s += 8) add_comp(a, lost, part[(size_t)s * n + i]);
+    sums[lane][col] = make_float2(a, lost);
     __syncthreads();
-    double t = 0.0;
     if (lane == 0)
 #pragma unroll
-        for (int k = 0; k < 8; ++k) t += sums[k][col];
-    return t;
+        for (int k = 1; k < 8; ++k) {
+            add_comp(a, lost, sums[k][col].x);
+            lost += sums[k][col].y;
+        }
+    return a + lost;
 }
 
 // Valid steps of batch row b.

@@ -54,7 +54,7 @@ int conv_plan(const gdn_conv_shape *s, gdn::ConvParams *p) {
 
 size_t conv_ws(const gdn::ConvParams &p) { return up256((size_t)gdn::conv_bwd_slices(p) * (p.W + 1) * p.C * 4); }
 
-int scan_plan(const gdn_scan_shape *s, gdn::ScanParams *p) {
+int scan_plan(const gdn_scan_shape *s, gdn::ScanParams *p, bool bwd) {
     if (s == nullptr || s->B <= 0 || s->T <= 0 || s->C <= 0 || s->N <= 0 || s->G <= 0) return GDN_ERR_INVALID_ARG;
     if (s->ldu < 0 || s->lddt < 0 || s->ldz < 0 || s->ldB < 0 || s->ldC < 0 || !dtype_ok(s->dtype)) return GDN_ERR_INVALID_ARG;
     if (s->N > 64 || s->C % s->G != 0 || s->B > 65535 || s->G > 65535 || s->C > (1 << 22)) return GDN_ERR_UNSUPPORTED_SHAPE;
@@ -76,7 +76,7 @@ int scan_plan(const gdn_scan_shape *s, gdn::ScanParams *p) {
         (double)s->B * s->C * s->N >= 2147483648.0 * 32.0 || rows * s->G * 2 * s->N >= 2147483648.0 * 64.0)
         return GDN_ERR_UNSUPPORTED_SHAPE;
     p->Bn = s->B; p->T = s->T; p->Cn = s->C; p->N = s->N; p->G = s->G;
-    gdn::scan_split(p);
+    gdn::scan_split(p, bwd);
     return GDN_OK;
 }
 
@@ -178,24 +178,24 @@ int gdn_conv_bwd(const gdn_conv_shape *shape, const void *x, const float *w, con
 
 size_t gdn_scan_ckpt_bytes(const gdn_scan_shape *shape) {
     gdn::ScanParams p;
-    return scan_plan(shape, &p) == GDN_OK ? scan_ckpt_total(p) : 0;
+    return scan_plan(shape, &p, false) == GDN_OK ? scan_ckpt_total(p) : 0;
 }
 
 size_t gdn_scan_fwd_workspace_bytes(const gdn_scan_shape *shape) {
     gdn::ScanParams p;
-    return scan_plan(shape, &p) == GDN_OK ? scan_seg_bytes(p) : 0;
+    return scan_plan(shape, &p, false) == GDN_OK ? scan_seg_bytes(p) : 0;
 }
 
 size_t gdn_scan_bwd_workspace_bytes(const gdn_scan_shape *shape) {
     gdn::ScanParams p;
-    return scan_plan(shape, &p) == GDN_OK ? scan_bwd_ws(p) : 0;
+    return scan_plan(shape, &p, true) == GDN_OK ? scan_bwd_ws(p) : 0;
 }
 
 int gdn_scan_fwd(const gdn_scan_shape *shape, const void *u, const void *dt, const float *A_log, const void *B,
                  const void *C, const float *D, const float *dt_bias, const void *z, const float *h0, const int *lens,
                  void *y, float *h_T, float *ckpt, size_t ckpt_bytes, void *workspace, size_t workspace_bytes, void *stream) {
     gdn::ScanParams p;
-    int rc = scan_plan(shape, &p);
+    int rc = scan_plan(shape, &p, false);
     if (rc != GDN_OK) return rc;
     if (!u || !dt || !A_log || !B || !C || !y || (scan_seg_bytes(p) > 0 && !workspace)) return GDN_ERR_INVALID_ARG;
     if (h_T != nullptr && h_T == h0 && p.T != 1) return GDN_ERR_INVALID_ARG;
@@ -216,7 +216,7 @@ int gdn_scan_bwd(const gdn_scan_shape *shape, const void *u, const void *dt, con
                  size_t ckpt_bytes, const void *dy, const float *dh_T, void *du, void *ddt, float *dA_log, void *dB, void *dC,
                  float *dD, float *ddt_bias, void *dz, float *dh0, void *workspace, size_t workspace_bytes, void *stream) {
     gdn::ScanParams p;
-    int rc = scan_plan(shape, &p);
+    int rc = scan_plan(shape, &p, true);
     if (rc != GDN_OK) return rc;
     if (!u || !dt || !A_log || !B || !C || !ckpt || !dy || !du || !ddt || !dA_log || !dB || !dC || !workspace)
         return GDN_ERR_INVALID_ARG;

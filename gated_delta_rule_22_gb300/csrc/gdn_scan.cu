@@ -14,10 +14,10 @@ namespace gdn {
 // LITE: the segment's end state from a zero start and its sum of d, nothing else (first pass over a
 // split sequence). The next tile's inputs are loaded while a tile is walked.
 template <int LPC, typename T, bool VEC, bool LITE>
-__global__ void __launch_bounds__(kScanThreads) scan_fwd_kernel(ScanParams p) {
+__global__ void __launch_bounds__(kScanThreads, 3) scan_fwd_kernel(ScanParams p) {
     using G = ScanGeo<LPC>;
     constexpr int CH = G::CH, NP = G::NP, V = G::V, KB = G::KB, TT = kScanTile;
-    __shared__ float2 sdx[TT][CH];              // d, d u
+    __shared__ __align__(16) float2 sdx[TT][CH];   // d, d u
     __shared__ __align__(16) float sB[TT][NP], sC[TT][NP];
     __shared__ float score[TT][G::SP];
     const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
@@ -82,7 +82,14 @@ __global__ void __launch_bounds__(kScanThreads) scan_fwd_kernel(ScanParams p) {
         for (int v = 0; v < V; ++v) {
             const float d = t < L ? softplus_full(cd[v] + bias[v]) : 0.f;
             sum_d[v] += d;
-            sdx[ts][cv + v] = make_float2(d, d * cu[v]);
+            cd[v] = d;
+        }
+        if constexpr (V == 1) {
+            sdx[ts][cv] = make_float2(cd[0], cd[0] * cu[0]);
+        } else {
+#pragma unroll
+            for (int v = 0; v < V; v += 2)
+                *reinterpret_cast<float4 *>(&sdx[ts][cv + v]) = make_float4(cd[v], cd[v] * cu[v], cd[v + 1], cd[v + 1] * cu[v + 1]);
         }
 #pragma unroll
         for (int k = 0; k < KB; ++k) {
@@ -97,23 +104,42 @@ __global__ void __launch_bounds__(kScanThreads) scan_fwd_kernel(ScanParams p) {
             const float o[4] = {h[0].x, h[0].y, h[1].x, h[1].y};
             store_states(p.ckpt + (((size_t)q.b * tiles + tile) * p.Cn + c) * p.N, n0, p.N, o);
         }
-#pragma unroll
-        for (int i0 = 0; i0 < TT; i0 += 4) {
-            float core[4];
+        // four steps at a time: what does not depend on the state (decays, d u B) is formed for the next
+        // four before the chain of the present four, whose only latency is one multiply-add per step
+        struct Group {
+            float2 a[4][2], x[4][2], c[4][2];
+        };
+        auto prepare = [&](int i0, Group &o) {
 #pragma unroll
             for (int i = 0; i < 4; ++i) {
                 const float2 dx = sdx[i0 + i][ch];
                 const float4 b4 = *reinterpret_cast<const float4 *>(&sB[i0 + i][n0]);
                 const float2 b2[2] = {make_float2(b4.x, b4.y), make_float2(b4.z, b4.w)};
-                float4 c4 = make_float4(0.f, 0.f, 0.f, 0.f);
-                if (!LITE) c4 = *reinterpret_cast<const float4 *>(&sC[i0 + i][n0]);
-                const float2 c2[2] = {make_float2(c4.x, c4.y), make_float2(c4.z, c4.w)};
+#pragma unroll
+                for (int k = 0; k < 2; ++k) {
+                    o.a[i][k] = decay2(dx.x, A2[k]);
+                    o.x[i][k] = __fmul2_rn(make_float2(dx.y, dx.y), b2[k]);
+                }
+                if (!LITE) {
+                    const float4 c4 = *reinterpret_cast<const float4 *>(&sC[i0 + i][n0]);
+                    o.c[i][0] = make_float2(c4.x, c4.y);
+                    o.c[i][1] = make_float2(c4.z, c4.w);
+                }
+            }
+        };
+        Group now, then;
+        prepare(0, now);
+#pragma unroll
+        for (int i0 = 0; i0 < TT; i0 += 4) {
+            if (i0 + 4 < TT) prepare(i0 + 4, then);
+            float core[4];
+#pragma unroll
+            for (int i = 0; i < 4; ++i) {
                 float2 sum;
 #pragma unroll
                 for (int k = 0; k < 2; ++k) {
-                    const float2 x = __fmul2_rn(make_float2(dx.x, dx.x), A2[k]);
-                    h[k] = __ffma2_rn(make_float2(ex2(x.x), ex2(x.y)), h[k], __fmul2_rn(make_float2(dx.y, dx.y), b2[k]));
-                    if (!LITE) sum = k == 0 ? __fmul2_rn(c2[0], h[0]) : __ffma2_rn(c2[1], h[1], sum);
+                    h[k] = __ffma2_rn(now.a[i][k], h[k], now.x[i][k]);
+                    if (!LITE) sum = k == 0 ? __fmul2_rn(now.c[i][0], h[0]) : __ffma2_rn(now.c[i][1], h[1], sum);
                 }
                 if (!LITE) core[i] = sum.x + sum.y;
             }
@@ -121,6 +147,7 @@ __global__ void __launch_bounds__(kScanThreads) scan_fwd_kernel(ScanParams p) {
                 const float r = lane_sum4<LPC>(core, lane);
                 if (lane % LPC < 4) score[i0 + (lane & 3)][ch] = r;
             }
+            now = then;
         }
         __syncthreads();
         if (!LITE && t < p.T) {
@@ -173,7 +200,7 @@ __global__ void __launch_bounds__(256) scan_step_kernel(ScanParams p) {
 #pragma unroll
         for (int k = 0; k < 4; ++k) {
             if (n0 + k >= p.N) break;
-            h[k] = fmaf(ex2(-expf(al[k]) * kLog2e * d), h[k], d * u * to_f32(Bm[n0 + k]));
+            h[k] = fmaf(ex2(fmaf(-expf(al[k]) * kLog2e, d, kExp2Centre)), h[k], d * u * to_f32(Bm[n0 + k]));
             core = fmaf(to_f32(Cm[n0 + k]), h[k], core);
         }
     }
@@ -213,6 +240,8 @@ cudaError_t launch_scan_combine(const ScanParams &p, const float *start, float *
     return cudaGetLastError();
 }
 
+constexpr int kBwdSplitBelow = 304, kBwdSplitWant = 304;
+
 int scan_lanes(int N) { return N <= 16 ? 4 : N <= 32 ? 8 : 16; }
 
 int scan_blocks(int C, int G, int N) {
@@ -220,14 +249,17 @@ int scan_blocks(int C, int G, int N) {
     return (per + ch - 1) / ch;
 }
 
-// A split sequence is walked twice, so it is split only where its CTAs leave most SMs idle (under
-// 76 of the 152), into segments of at least 8 tiles, for about two CTAs per SM.
-void scan_split(ScanParams *p) {
+// A split sequence is walked twice (the first pass costs the forward about 0.7 of the second, the
+// backward about 0.3), so it is split only where its CTAs leave the SMs short of warps: the forward
+// below half a CTA of 8 warps per SM, the backward below three of 4 warps, into segments of at least
+// 8 tiles.
+void scan_split(ScanParams *p, bool bwd) {
     const long long ctas = (long long)p->Bn * p->G * scan_blocks(p->Cn, p->G, p->N);
     const int tiles = (p->T + kScanTile - 1) / kScanTile;
+    const int below = bwd ? kBwdSplitBelow : 76, want = bwd ? kBwdSplitWant : 304;
     int segs = 1;
-    if (ctas < 76 && tiles >= 16) {
-        segs = (int)((304 + ctas - 1) / ctas);
+    if (ctas < below && tiles >= 16) {
+        segs = (int)((want + ctas - 1) / ctas);
         if (segs > tiles / 8) segs = tiles / 8;
     }
     const int per = (tiles + segs - 1) / segs;

@@ -9,6 +9,8 @@
 // the output. The mean is subtracted before the squares are summed.
 #include "gdn_layer.cuh"
 
+#include <type_traits>
+
 namespace gdn {
 
 namespace {
@@ -43,60 +45,169 @@ __device__ __forceinline__ float block_sum(float x, float *buf) {
 
 }  // namespace
 
-// LPG lanes per group, V neighbouring channels per lane, IT pieces: D <= LPG V IT. A warp takes
-// 32 / LPG groups of a row and keeps their w and b in registers over the rows that it walks.
-template <typename T, int V, int LPG, int IT>
-__global__ void __launch_bounds__(kNormThreads) norm_fwd_kernel(NormParams p) {
-    const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
-    const int g = blockIdx.y * (32 / LPG) + lane / LPG, j = lane % LPG;
-    bool ok[IT];
-    float w[IT][V], b[IT][V];
+// A lane's E elements as pairs, for the packed float32 instructions (E = 1: the second is unused).
+template <int E>
+struct Pairs {
+    static constexpr int N = (E + 1) / 2;
+    float2 p[N];
+    __device__ __forceinline__ void fill(float x) {
 #pragma unroll
-    for (int i = 0; i < IT; ++i) {
-        const int e = (i * LPG + j) * V;
-        ok[i] = g < p.G && e < p.D;
-#pragma unroll
-        for (int v = 0; v < V; ++v) {
-            w[i][v] = ok[i] && p.w != nullptr ? p.w[(size_t)g * p.D + e + v] : 1.f;
-            b[i][v] = ok[i] && p.b != nullptr ? p.b[(size_t)g * p.D + e + v] : 0.f;
-        }
+        for (int i = 0; i < N; ++i) p[i] = make_float2(x, x);
     }
-    const float inv_D = 1.f / p.D;
-    const size_t col = (size_t)g * p.D + j * V;
-    for (int m = blockIdx.x * kNormWarps + warp; m < p.M; m += gridDim.x * kNormWarps) {
-        float x[IT][V], z[IT][V], s = 0.f, ss = 0.f;
+    __device__ __forceinline__ void set(int e, float x) {
+        if (e % 2) p[e / 2].y = x;
+        else p[e / 2].x = x;
+    }
+    __device__ __forceinline__ float get(int e) const { return e % 2 ? p[e / 2].y : p[e / 2].x; }
+    __device__ __forceinline__ float total() const {
+        float2 s = p[0];
 #pragma unroll
-        for (int i = 0; i < IT; ++i) {
+        for (int i = 1; i < N; ++i) s = __fadd2_rn(s, p[i]);
+        return E == 1 ? s.x : s.x + s.y;
+    }
+};
+
+// act(x) and, where asked, act'(x) of a pair
+template <int ACT>
+__device__ __forceinline__ float2 act2(float2 x) {
+    if (ACT == kActSilu) return __fmul2_rn(x, sigmoid2_hw(x));
+    if (ACT == kActGelu) return make_float2(gelu_f(x.x), gelu_f(x.y));
+    return x;
+}
+template <int ACT>
+__device__ __forceinline__ float2 act2(float2 x, float2 &slope) {
+    if (ACT == kActSilu) {
+        const float2 one = make_float2(1.f, 1.f), s = sigmoid2_hw(x);
+        slope = __fmul2_rn(s, __ffma2_rn(x, __ffma2_rn(s, make_float2(-1.f, -1.f), one), one));
+        return __fmul2_rn(x, s);
+    }
+    if (ACT == kActGelu) {
+        slope = make_float2(dgelu_f(x.x), dgelu_f(x.y));
+        return make_float2(gelu_f(x.x), gelu_f(x.y));
+    }
+    slope = make_float2(1.f, 1.f);
+    return x;
+}
+
+// f<ACT>() for the activation of the call: the test is made once per row, not per element.
+template <typename F>
+__device__ __forceinline__ void with_act(int act, F f) {
+    if (act == kActSilu) f(std::integral_constant<int, kActSilu>());
+    else if (act == kActGelu) f(std::integral_constant<int, kActGelu>());
+    else f(std::integral_constant<int, kActNone>());
+}
+
+// Where a lane's elements lie: LPG lanes per group, V neighbouring channels per lane, IT pieces
+// (D <= LPG V IT). A warp takes 32 / LPG groups of a row.
+template <typename T, int V, int LPG, int IT>
+struct NormLane {
+    static constexpr int E = V * IT;
+    int g, j;
+    size_t col;
+    bool ok[IT], full;
+    __device__ __forceinline__ explicit NormLane(const NormParams &p) {
+        const int lane = threadIdx.x & 31;
+        g = blockIdx.y * (32 / LPG) + lane / LPG;
+        j = lane % LPG;
+        col = (size_t)g * p.D + j * V;
 #pragma unroll
-            for (int v = 0; v < V; ++v) x[i][v] = z[i][v] = 0.f;
-            if (ok[i]) load_vec<T, V>(static_cast<const T *>(p.x) + (size_t)m * p.ldx + col + i * LPG * V, x[i]);
-            if (ok[i] && p.z != nullptr)
-                load_vec<T, V>(static_cast<const T *>(p.z) + (size_t)m * p.ldz + col + i * LPG * V, z[i]);
-#pragma unroll
-            for (int v = 0; v < V; ++v) s += x[i][v];
-        }
-        const float mean = p.center ? group_sum<LPG>(s) * inv_D : 0.f;
+        for (int i = 0; i < IT; ++i) ok[i] = g < p.G && (i * LPG + j) * V < p.D;
+        full = p.D == LPG * V * IT && p.G % (32 / LPG) == 0;
+    }
+    // parameters of the lane's channels (w, b), or `other`
+    __device__ __forceinline__ void params(const float *w, float other, Pairs<E> &o) const {
+        o.fill(other);
+        if (w == nullptr) return;
 #pragma unroll
         for (int i = 0; i < IT; ++i)
+            if (ok[i])
 #pragma unroll
-            for (int v = 0; v < V; ++v) {
-                x[i][v] = ok[i] ? x[i][v] - mean : 0.f;
-                ss = fmaf(x[i][v], x[i][v], ss);
-            }
-        const float rstd = 1.f / sqrtf(fmaf(group_sum<LPG>(ss), inv_D, p.eps));
-        if (p.stats != nullptr && j == 0 && g < p.G)
-            *reinterpret_cast<float2 *>(p.stats + 2 * ((size_t)m * p.G + g)) = make_float2(mean, rstd);
+                for (int v = 0; v < V; ++v) o.set(i * V + v, w[col + i * LPG * V + v]);
+    }
+    __device__ __forceinline__ void load(const void *t, size_t at, Raw<T, V> (&o)[IT]) const {
 #pragma unroll
         for (int i = 0; i < IT; ++i) {
-            if (!ok[i]) continue;
-            float o[V];
-#pragma unroll
-            for (int v = 0; v < V; ++v) {
-                const float aff = fmaf(x[i][v] * rstd, w[i][v], b[i][v]);
-                o[v] = p.z != nullptr ? aff * act_rt(p.act, z[i][v]) : act_rt(p.act, aff);
-            }
-            store_vec<T, V>(static_cast<T *>(p.y) + (size_t)m * p.G * p.D + col + i * LPG * V, o);
+            o[i] = Raw<T, V>();
+            if (ok[i]) o[i] = load_raw<T, V>(static_cast<const T *>(t) + at + col + i * LPG * V);
         }
+    }
+    __device__ __forceinline__ void floats(const Raw<T, V> (&r)[IT], Pairs<E> &o) const {
+        if (E == 1) o.p[0].y = 0.f;
+#pragma unroll
+        for (int i = 0; i < IT; ++i) {
+            float e[V];
+            unpack<T, V>(r[i], e);
+#pragma unroll
+            for (int v = 0; v < V; ++v) o.set(i * V + v, e[v]);
+        }
+    }
+    __device__ __forceinline__ void store(void *t, size_t at, const Pairs<E> &x) const {
+#pragma unroll
+        for (int i = 0; i < IT; ++i) {
+            float e[V];
+#pragma unroll
+            for (int v = 0; v < V; ++v) e[v] = x.get(i * V + v);
+            if (ok[i]) store_vec<T, V>(static_cast<T *>(t) + at + col + i * LPG * V, e);
+        }
+    }
+    // zeros in the places beyond the group
+    __device__ __forceinline__ void mask(Pairs<E> &x) const {
+        if (full) return;
+#pragma unroll
+        for (int e = 0; e < E; ++e)
+            if (!ok[e / V]) x.set(e, 0.f);
+    }
+};
+
+// A warp keeps its groups' w and b in registers over the rows that it walks, and loads the next row
+// while it works on one.
+template <typename T, int V, int LPG, int IT>
+__global__ void __launch_bounds__(kNormThreads) norm_fwd_kernel(NormParams p) {
+    constexpr int E = V * IT, P = Pairs<E>::N;
+    const NormLane<T, V, LPG, IT> at(p);
+    const int rows = gridDim.x * kNormWarps;
+    int m = blockIdx.x * kNormWarps + (threadIdx.x >> 5);
+    Raw<T, V> rx[IT], rz[IT];
+    auto fetch = [&](int row) {
+        at.load(p.x, (size_t)row * p.ldx, rx);
+        if (p.z != nullptr) at.load(p.z, (size_t)row * p.ldz, rz);
+    };
+    if (m < p.M) fetch(m);
+    Pairs<E> w, b;
+    at.params(p.w, 1.f, w);
+    at.params(p.b, 0.f, b);
+    const float inv_D = 1.f / p.D;
+    for (; m < p.M; m += rows) {
+        Pairs<E> x, z;
+        at.floats(rx, x);
+        if (p.z != nullptr) at.floats(rz, z);
+        if (m + rows < p.M) fetch(m + rows);
+        float mean = 0.f;
+        if (p.center) {
+            mean = group_sum<LPG>(x.total()) * inv_D;
+#pragma unroll
+            for (int i = 0; i < P; ++i) x.p[i] = __fadd2_rn(x.p[i], make_float2(-mean, -mean));
+            at.mask(x);
+        }
+        Pairs<E> sq;
+#pragma unroll
+        for (int i = 0; i < P; ++i) sq.p[i] = __fmul2_rn(x.p[i], x.p[i]);
+        const float rstd = 1.f / sqrtf(fmaf(group_sum<LPG>(sq.total()), inv_D, p.eps));
+        if (p.stats != nullptr && at.j == 0 && at.g < p.G)
+            *reinterpret_cast<float2 *>(p.stats + 2 * ((size_t)m * p.G + at.g)) = make_float2(mean, rstd);
+        with_act(p.act, [&](auto act) {
+            constexpr int ACT = decltype(act)::value;
+#pragma unroll
+            for (int i = 0; i < P; ++i) x.p[i] = __ffma2_rn(__fmul2_rn(x.p[i], make_float2(rstd, rstd)), w.p[i], b.p[i]);
+            if (p.z != nullptr) {
+#pragma unroll
+                for (int i = 0; i < P; ++i) x.p[i] = __fmul2_rn(x.p[i], act2<ACT>(z.p[i]));
+            } else {
+#pragma unroll
+                for (int i = 0; i < P; ++i) x.p[i] = act2<ACT>(x.p[i]);
+            }
+        });
+        at.store(p.y, (size_t)m * p.G * p.D, x);
     }
 }
 
@@ -104,87 +215,79 @@ __global__ void __launch_bounds__(kNormThreads) norm_fwd_kernel(NormParams p) {
 // in ascending order, into the CTA's slice of the partial sums.
 template <typename T, int V, int LPG, int IT>
 __global__ void __launch_bounds__(kNormThreads) norm_bwd_kernel(NormParams p) {
-    __shared__ float sums[2][kNormWarps][32 * V * IT];
+    constexpr int E = V * IT, P = Pairs<E>::N;
+    __shared__ float sums[2][kNormWarps][32 * E];
     const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
-    const int g = blockIdx.y * (32 / LPG) + lane / LPG, j = lane % LPG;
-    bool ok[IT];
-    float w[IT][V], b[IT][V], dw[IT][V], db[IT][V];
-#pragma unroll
-    for (int i = 0; i < IT; ++i) {
-        const int e = (i * LPG + j) * V;
-        ok[i] = g < p.G && e < p.D;
-#pragma unroll
-        for (int v = 0; v < V; ++v) {
-            w[i][v] = ok[i] && p.w != nullptr ? p.w[(size_t)g * p.D + e + v] : 1.f;
-            b[i][v] = ok[i] && p.b != nullptr ? p.b[(size_t)g * p.D + e + v] : 0.f;
-            dw[i][v] = db[i][v] = 0.f;
-        }
-    }
+    const NormLane<T, V, LPG, IT> at(p);
+    const int rows = gridDim.x * kNormWarps;
+    int m = blockIdx.x * kNormWarps + warp;
+    const size_t C = (size_t)p.G * p.D;
+    Raw<T, V> rx[IT], rz[IT], ry[IT];
+    float2 rs = make_float2(0.f, 0.f);
+    auto fetch = [&](int row) {
+        at.load(p.x, (size_t)row * p.ldx, rx);
+        at.load(p.dy, (size_t)row * C, ry);
+        if (p.z != nullptr) at.load(p.z, (size_t)row * p.ldz, rz);
+        if (at.g < p.G) rs = *reinterpret_cast<const float2 *>(p.stats_in + 2 * ((size_t)row * p.G + at.g));
+    };
+    if (m < p.M) fetch(m);
+    Pairs<E> w, b, dw, db;
+    at.params(p.w, 1.f, w);
+    at.params(p.b, 0.f, b);
+    dw.fill(0.f);
+    db.fill(0.f);
     const float inv_D = 1.f / p.D;
-    const size_t col = (size_t)g * p.D + j * V;
-    for (int m = blockIdx.x * kNormWarps + warp; m < p.M; m += gridDim.x * kNormWarps) {
-        float xh[IT][V], dxh[IT][V], s1 = 0.f, s2 = 0.f;
-        float2 st = make_float2(0.f, 0.f);
-        if (g < p.G) st = *reinterpret_cast<const float2 *>(p.stats_in + 2 * ((size_t)m * p.G + g));
+    for (; m < p.M; m += rows) {
+        Pairs<E> x, z, g;
+        const float2 st = rs;
+        at.floats(rx, x);
+        at.floats(ry, g);
+        if (p.z != nullptr) at.floats(rz, z);
+        if (m + rows < p.M) fetch(m + rows);
 #pragma unroll
-        for (int i = 0; i < IT; ++i) {
-            const size_t at = (size_t)m * p.G * p.D + col + i * LPG * V;
-            float x[V], z[V], dy[V], dz[V];
+        for (int i = 0; i < P; ++i) x.p[i] = __fmul2_rn(__fadd2_rn(x.p[i], make_float2(-st.x, -st.x)), make_float2(st.y, st.y));
+        at.mask(x);
+        with_act(p.act, [&](auto act) {
+            constexpr int ACT = decltype(act)::value;
 #pragma unroll
-            for (int v = 0; v < V; ++v) x[v] = z[v] = dy[v] = 0.f;
-            if (ok[i]) {
-                load_vec<T, V>(static_cast<const T *>(p.x) + (size_t)m * p.ldx + col + i * LPG * V, x);
-                load_vec<T, V>(static_cast<const T *>(p.dy) + at, dy);
-                if (p.z != nullptr)
-                    load_vec<T, V>(static_cast<const T *>(p.z) + (size_t)m * p.ldz + col + i * LPG * V, z);
-            }
-#pragma unroll
-            for (int v = 0; v < V; ++v) {
-                xh[i][v] = ok[i] ? (x[v] - st.x) * st.y : 0.f;
-                const float aff = fmaf(xh[i][v], w[i][v], b[i][v]);
-                float daff;
+            for (int i = 0; i < P; ++i) {
+                const float2 aff = __ffma2_rn(x.p[i], w.p[i], b.p[i]);
+                float2 slope;
                 if (p.z != nullptr) {
-                    if (p.act == kActSilu) {
-                        const float sg = sigmoid_hw(z[v]);
-                        daff = dy[v] * z[v] * sg;
-                        dz[v] = dy[v] * aff * sg * fmaf(z[v], 1.f - sg, 1.f);
-                    } else {
-                        daff = dy[v] * act_rt(p.act, z[v]);
-                        dz[v] = dy[v] * aff * dact_rt(p.act, z[v]);
-                    }
+                    const float2 gate = act2<ACT>(z.p[i], slope);
+                    z.p[i] = __fmul2_rn(__fmul2_rn(g.p[i], aff), slope);      // dz
+                    g.p[i] = __fmul2_rn(g.p[i], gate);
                 } else {
-                    daff = dy[v] * dact_rt(p.act, aff);
+                    act2<ACT>(aff, slope);
+                    g.p[i] = __fmul2_rn(g.p[i], slope);
                 }
-                db[i][v] += daff;
-                dw[i][v] = fmaf(daff, xh[i][v], dw[i][v]);
-                dxh[i][v] = daff * w[i][v];
-                s1 += dxh[i][v];
-                s2 = fmaf(dxh[i][v], xh[i][v], s2);
             }
-            if (ok[i] && p.dz != nullptr) store_vec<T, V>(static_cast<T *>(p.dz) + at, dz);
-        }
-        s1 = p.center ? group_sum<LPG>(s1) * inv_D : 0.f;
-        s2 = group_sum<LPG>(s2) * inv_D;
+        });
+        Pairs<E> gx;
 #pragma unroll
-        for (int i = 0; i < IT; ++i) {
-            if (!ok[i]) continue;
-            float o[V];
-#pragma unroll
-            for (int v = 0; v < V; ++v) o[v] = st.y * (dxh[i][v] - s1 - xh[i][v] * s2);
-            store_vec<T, V>(static_cast<T *>(p.dx) + (size_t)m * p.G * p.D + col + i * LPG * V, o);
+        for (int i = 0; i < P; ++i) {                     // g: daff, then dxh
+            db.p[i] = __fadd2_rn(db.p[i], g.p[i]);
+            dw.p[i] = __ffma2_rn(g.p[i], x.p[i], dw.p[i]);
+            g.p[i] = __fmul2_rn(g.p[i], w.p[i]);
+            gx.p[i] = __fmul2_rn(g.p[i], x.p[i]);
         }
+        if (p.dz != nullptr) at.store(p.dz, (size_t)m * C, z);
+        const float s1 = p.center ? group_sum<LPG>(g.total()) * inv_D : 0.f, s2 = group_sum<LPG>(gx.total()) * inv_D;
+#pragma unroll
+        for (int i = 0; i < P; ++i)
+            x.p[i] = __fmul2_rn(__fadd2_rn(__ffma2_rn(x.p[i], make_float2(-s2, -s2), g.p[i]), make_float2(-s1, -s1)), make_float2(st.y, st.y));
+        at.store(p.dx, (size_t)m * C, x);
     }
 #pragma unroll
     for (int i = 0; i < IT; ++i)
 #pragma unroll
         for (int v = 0; v < V; ++v) {
-            sums[0][warp][(i * 32 + lane) * V + v] = dw[i][v];
-            sums[1][warp][(i * 32 + lane) * V + v] = db[i][v];
+            sums[0][warp][(i * 32 + lane) * V + v] = dw.get(i * V + v);
+            sums[1][warp][(i * 32 + lane) * V + v] = db.get(i * V + v);
         }
     __syncthreads();
-    const size_t C = (size_t)p.G * p.D;
-    for (int k = threadIdx.x; k < 2 * 32 * V * IT; k += kNormThreads) {
-        const int which = k / (32 * V * IT), n = k % (32 * V * IT), i = n / (32 * V), ln = n / V % 32, v = n % V;
+    for (int k = threadIdx.x; k < 2 * 32 * E; k += kNormThreads) {
+        const int which = k / (32 * E), n = k % (32 * E), i = n / (32 * V), ln = n / V % 32, v = n % V;
         const int gg = blockIdx.y * (32 / LPG) + ln / LPG, e = (i * LPG + ln % LPG) * V + v;
         if (gg >= p.G || e >= p.D) continue;
         float a = 0.f;
@@ -312,9 +415,9 @@ NormGeo norm_geo(int D, int V) {
     return q;
 }
 
-// Groups and row slices of the grid: about 8 CTAs per SM, at most one warp per row.
+// Groups and row slices of the grid: about 4 CTAs per SM, at most one warp per row.
 int norm_slices(int M, int sets) {
-    const int most = (M + kNormWarps - 1) / kNormWarps, want = (152 * 8 + sets - 1) / sets;
+    const int most = (M + kNormWarps - 1) / kNormWarps, want = (152 * 4 + sets - 1) / sets;
     return want < most ? want : most;
 }
 

@@ -851,20 +851,21 @@ void api_clear_error() { g_last_error[0] = '\0'; }
 int api_cuda_status(cudaError_t e) { return cuda_status(e); }
 int api_device_status_address(int **out) { return device_status_address(out); }
 
-int api_planes_map(CUtensorMap *map, const void *ptr, uint64_t cols, uint64_t rows, uint64_t planes, uint64_t ld, int box_cols,
-                   int box_rows) {
+int api_planes_map(CUtensorMap *map, const void *ptr, uint64_t cols, uint64_t rows, uint64_t planes, uint64_t ld, int box_rows,
+                   int box_blocks) {
     PFN_cuTensorMapEncodeTiled_v12000 enc = tensor_map_encoder();
     if (enc == nullptr) {
         snprintf(g_last_error, sizeof g_last_error, "cuTensorMapEncodeTiled is not available from the driver");
         return GDN_ERR_CUDA;
     }
-    const cuuint64_t dims[3] = {cols, rows, planes};
-    const cuuint64_t strides[2] = {ld * 2, rows * ld * 2};
-    const cuuint32_t box[3] = {(cuuint32_t)box_cols, (cuuint32_t)box_rows, 1};
-    const cuuint32_t estride[3] = {1, 1, 1};
-    const CUresult r = enc(map, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 3, const_cast<void *>(ptr), dims, strides, box, estride,
-                           CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
-                           CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE);
+    const bool blocks = box_blocks > 0;
+    const cuuint64_t dims[4] = {blocks ? 64 : cols, rows, blocks ? cols / 64 : planes, planes};
+    const cuuint64_t strides[3] = {ld * 2, blocks ? 128 : rows * ld * 2, rows * ld * 2};
+    const cuuint32_t box[4] = {64, (cuuint32_t)box_rows, blocks ? (cuuint32_t)box_blocks : 1, 1};
+    const cuuint32_t estride[4] = {1, 1, 1, 1};
+    const CUresult r = enc(map, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, blocks ? 4 : 3, const_cast<void *>(ptr), dims, strides, box,
+                           estride, CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B,
+                           CU_TENSOR_MAP_L2_PROMOTION_L2_256B, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE);
     if (r != CUDA_SUCCESS) {
         snprintf(g_last_error, sizeof g_last_error, "cuTensorMapEncodeTiled failed with CUresult %d", (int)r);
         return GDN_ERR_CUDA;

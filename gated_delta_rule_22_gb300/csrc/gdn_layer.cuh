@@ -13,11 +13,12 @@ enum { kActNone = 0, kActSilu = 1, kActGelu = 2 };
 void api_clear_error();
 int api_cuda_status(cudaError_t e);
 int api_device_status_address(int **out);
-// 3-D tensor map of `planes` row-major bf16 [rows][cols] arrays with `ld` elements between rows
-// (planes rows * ld apart), box {box_cols, box_rows, 1}, 128-byte swizzle; what lies outside an array
-// reads as zero.
-int api_planes_map(CUtensorMap *map, const void *ptr, uint64_t cols, uint64_t rows, uint64_t planes, uint64_t ld, int box_cols,
-                   int box_rows);
+// Tensor map of `planes` row-major bf16 [rows][cols] arrays with `ld` elements between rows (planes
+// rows * ld apart), 128-byte swizzle; what lies outside an array reads as zero. box_blocks = 0: 3-D
+// {cols, rows, planes}, box {64, box_rows, 1}. Else (cols a multiple of 64) 4-D {64, rows, cols / 64,
+// planes}, box {64, box_rows, box_blocks, 1}: box_blocks neighbouring boxes of 64 columns by one copy.
+int api_planes_map(CUtensorMap *map, const void *ptr, uint64_t cols, uint64_t rows, uint64_t planes, uint64_t ld, int box_rows,
+                   int box_blocks);
 
 // ---- parameter blocks
 struct ConvParams {

@@ -13,6 +13,7 @@
 // the nine products of terms are summed, smallest first, by walking K once per product: the dropped
 // ones are below 2^-24 of the result. Six bf16 products cost about a quarter of the time of float32
 // arithmetic on the CUDA cores.
+#include "gdn.h"
 #include "gdn_layer.cuh"
 #include "gdn_umma.cuh"
 
@@ -20,13 +21,14 @@ namespace gdn {
 
 namespace {
 
-constexpr int kBM = 128, kBK = 64, kMaxBN = 256, kStages = 4;
-constexpr int kEpiWarps = 8, kGemmThreads = 64 + 32 * kEpiWarps;
+constexpr int kBM = 128, kBK = 64, kMaxBN = 256, kStages = 6;   // per CTA of a pair: 128 rows, 64 deep
+constexpr int kPairs = 76;                          // pairs of SMs
+constexpr int kEpiWarps = 8, kGemmThreads = 96 + 32 * kEpiWarps;   // + two fetching warps, one issuing
 constexpr int kEpiPitch = 20;                       // floats per staged row of 16 columns
-constexpr int kStageBytes = (kBM + kMaxBN) * kBK * 2;
+constexpr int kBox = 64 * kBK * 2;                  // one TMA box: 64 rows x 128 bytes
+constexpr int kStageBytes = 4 * kBox;               // two boxes of A, two of B
 constexpr size_t kGemmSmem = 1024 + (size_t)kStages * kStageBytes + kEpiWarps * 32 * kEpiPitch * 4 + 256;
 constexpr int kBiasSlices = 64;
-constexpr int kSms = 152;
 
 size_t up256(size_t n) { return (n + 255) / 256 * 256; }
 int up8(int n) { return (n + 7) / 8 * 8; }
@@ -34,27 +36,119 @@ int up8(int n) { return (n + 7) / 8 * 8; }
 // The six products of the float32 terms (A's, B's), smallest first; bf16 has the last alone.
 __constant__ signed char kTermA[6] = {0, 2, 1, 0, 1, 0}, kTermB[6] = {2, 0, 1, 1, 0, 0};
 
+// What a pair of CTAs computes at once: rows m0 .. m0 + 255, columns n0 .. n0 + BN - 1. Items are
+// numbered: whole tiles of 256 columns (within a panel of columns the columns first); then the tiles
+// of an incomplete last round, cut into halves of 128 columns where that lets every pair take at most
+// one; then the tiles of the last, narrower columns, of as many columns as are left (in 32s).
 struct GemmParams {
     const void *bias, *res;
     void *out, *pre;
     int *status;
     long long ldres;
     int M, N, kblocks, terms, act;
-    int BN, mt, nt, panel;      // tile columns, tiles along m and n, n tiles walked together
+    int mt, nt, panel;          // tiles along m and n (of 256 columns), n tiles walked together
+    int whole, halves, edge;    // whole tiles, half tiles, columns of the edge tiles
+    int items;
     int vec;                    // 16-byte accesses of out, pre and res are aligned
+    int a_blocks, b_blocks;     // MN-major operands of whole 64-column blocks
 };
 
-__device__ __forceinline__ void tma_load_3d(void *dst, const CUtensorMap *map, uint64_t *bar, int c0, int c1, int c2) {
+__device__ __forceinline__ void item_at(const GemmParams &p, int i, int &m0, int &n0, int &BN) {
+    int t = i;
+    BN = kMaxBN;
+    if (i >= p.whole + p.halves) {
+        m0 = (i - p.whole - p.halves) * 2 * kBM;
+        n0 = p.nt * kMaxBN;
+        BN = p.edge;
+        return;
+    }
+    if (i >= p.whole) t = p.whole + (i - p.whole) / 2;
+    const int per = p.panel * p.mt, q = t / per, r = t % per, w = min(p.panel, p.nt - q * p.panel);
+    m0 = r / w * 2 * kBM;
+    n0 = (q * p.panel + r % w) * kMaxBN;
+    if (i >= p.whole) {
+        BN = kMaxBN / 2;
+        n0 += (i - p.whole) % 2 * BN;
+    }
+}
+
+// ---- a pair of CTAs (cta_group::2): products issued by the even one read both CTAs' shared memory and
+// write both CTAs' tensor memory
+__device__ __forceinline__ uint32_t cta_rank() {
+    uint32_t r;
+    asm volatile("mov.u32 %0, %%cluster_ctarank;" : "=r"(r));
+    return r;
+}
+__device__ __forceinline__ uint32_t leader_addr(const void *p) {      // the even CTA's copy of a shared variable
+    uint32_t a;
+    asm volatile("mapa.shared::cluster.u32 %0, %1, %2;" : "=r"(a) : "r"(smem_addr(p)), "r"(0));
+    return a;
+}
+__device__ __forceinline__ void cluster_sync() {
+    asm volatile("barrier.cluster.arrive.release.aligned;\n barrier.cluster.wait.acquire.aligned;" ::: "memory");
+}
+__device__ __forceinline__ void arrive_cluster(uint32_t bar) {
+    asm volatile("mbarrier.arrive.release.cluster.shared::cluster.b64 _, [%0];" ::"r"(bar) : "memory");
+}
+// a TMA load into this CTA's shared memory whose bytes count on a barrier of either CTA of the pair
+__device__ __forceinline__ void tma_load_pair(uint32_t dst, const CUtensorMap *map, uint32_t bar, int c0, int c1, int c2) {
     asm volatile(
-        "cp.async.bulk.tensor.3d.shared::cluster.global.mbarrier::complete_tx::bytes [%0], [%1, {%2, %3, %4}], [%5];" ::"r"(
-            smem_addr(dst)),
-        "l"(reinterpret_cast<uint64_t>(map)), "r"(c0), "r"(c1), "r"(c2), "r"(smem_addr(bar))
+        "cp.async.bulk.tensor.3d.cta_group::2.shared::cluster.global.mbarrier::complete_tx::bytes [%0], [%1, {%2, %3, %4}], "
+        "[%5];" ::"r"(dst),
+        "l"(reinterpret_cast<uint64_t>(map)), "r"(c0), "r"(c1), "r"(c2), "r"(bar)
+        : "memory");
+}
+__device__ __forceinline__ void tma_load_pair(uint32_t dst, const CUtensorMap *map, uint32_t bar, int c0, int c1, int c2, int c3) {
+    asm volatile(
+        "cp.async.bulk.tensor.4d.cta_group::2.shared::cluster.global.mbarrier::complete_tx::bytes [%0], [%1, {%2, %3, %4, %5}], "
+        "[%6];" ::"r"(dst),
+        "l"(reinterpret_cast<uint64_t>(map)), "r"(c0), "r"(c1), "r"(c2), "r"(c3), "r"(bar)
+        : "memory");
+}
+// One operand's tile of a stage: `boxes` boxes of 64 rows (or columns) from mn, K from k0. The number of
+// copies is what counts: each costs its warp a few hundred cycles, so a tile is one copy wherever a
+// map can describe it (an MN-major array of whole 64-column blocks: both boxes at once; `half` is the
+// map of one box).
+template <bool MN>
+__device__ __forceinline__ void load_tile(uint32_t dst, const CUtensorMap *map, const CUtensorMap *half, bool blocks, int boxes,
+                                          uint32_t bar, int mn, int k0, int term) {
+    if (!MN) {
+        tma_load_pair(dst, boxes == 2 ? map : half, bar, k0, mn, term);
+    } else if (blocks) {
+        tma_load_pair(dst, boxes == 2 ? map : half, bar, 0, k0, mn / 64, term);
+    } else {
+        tma_load_pair(dst, half, bar, mn, k0, term);
+        if (boxes == 2) tma_load_pair(dst + kBox, half, bar, mn + 64, k0, term);
+    }
+}
+__device__ __forceinline__ void pair_tmem_alloc(uint32_t *slot, uint32_t ncols) {
+    asm volatile("tcgen05.alloc.cta_group::2.sync.aligned.shared::cta.b32 [%0], %1;" ::"r"(smem_addr(slot)), "r"(ncols) : "memory");
+    asm volatile("tcgen05.relinquish_alloc_permit.cta_group::2.sync.aligned;" ::: "memory");
+}
+__device__ __forceinline__ void pair_tmem_dealloc(uint32_t taddr, uint32_t ncols) {
+    asm volatile("tcgen05.dealloc.cta_group::2.sync.aligned.b32 %0, %1;" ::"r"(taddr), "r"(ncols) : "memory");
+}
+__device__ __forceinline__ void pair_umma_bf16(uint32_t d_tmem, uint64_t adesc, uint64_t bdesc, uint32_t idesc, bool accumulate,
+                                               uint32_t lead) {
+    asm volatile(
+        "{\n .reg .pred p, q;\n setp.ne.b32 p, %4, 0;\n setp.ne.b32 q, %5, 0;\n"
+        " @q tcgen05.mma.cta_group::2.kind::f16 [%0], %1, %2, %3, p;\n}" ::"r"(d_tmem),
+        "l"(adesc), "l"(bdesc), "r"(idesc), "r"((uint32_t)accumulate), "r"(lead)
+        : "memory");
+}
+// completion of the earlier products arrives once on both CTAs' copies of `bar`
+__device__ __forceinline__ void pair_commit(uint64_t *bar, uint32_t lead) {
+    asm volatile(
+        "{\n .reg .pred q;\n setp.ne.b32 q, %1, 0;\n"
+        " @q tcgen05.commit.cta_group::2.mbarrier::arrive::one.shared::cluster.multicast::cluster.b64 [%0], %2;\n}" ::"r"(
+            smem_addr(bar)),
+        "r"(lead), "h"((unsigned short)3)
         : "memory");
 }
 
 // 128-byte swizzled operand descriptors. K-major: rows of 64 K elements, 8-row atoms 1024 bytes
 // apart. MN-major: rows are K, 64 M/N elements wide; 8-row atoms 1024 bytes apart along K, the next
-// 64 M/N elements 64 rows (8192 bytes) further.
+// 64 M/N elements one box (8192 bytes) further.
 __device__ __forceinline__ uint64_t sw128_desc(uint32_t start, bool mn) {
     return umma_sdesc(start, mn ? 8192u : 16u, 1024u) | (uint64_t)2 << 61;
 }
@@ -66,21 +160,17 @@ __device__ __forceinline__ float dact_rt(int act, float x) {
     return act == kActSilu ? dsilu_hw(x) : act == kActGelu ? dgelu_f(x) : 1.f;
 }
 
-// Tile t of the grid: panels of `panel` tile columns, within one the columns first.
-__device__ __forceinline__ void tile_at(const GemmParams &p, int t, int &m0, int &n0) {
-    const int per = p.panel * p.mt, q = t / per, r = t % per, w = min(p.panel, p.nt - q * p.panel);
-    m0 = r / w * kBM;
-    n0 = (q * p.panel + r % w) * p.BN;
-}
-
 }  // namespace
 
-// Warp 0 fetches the operand tiles (TMA, kStages deep), warp 1 issues the products into one of two
-// accumulators in tensor memory, warps 2-9 turn the other one into output: the epilogue of a tile
-// runs under the products of the next.
+// A pair of CTAs shares each tile: CTA r holds rows 128 r .. 128 r + 127 of A's 256 and half of B's
+// columns, so that each operand element is fetched into one SM only: with 128 x 256 tiles of single
+// CTAs the tiles' way from L2 (27 TB/s at full rate) was the bound, 1.36 PFLOP/s. In each CTA warps 0
+// and 2 fetch (TMA, kStages deep), warp 1 of the even CTA issues the products into one of two accumulators
+// in tensor memory, and warps 3-10 turn the other one into output under the products of the next tile.
 template <bool A_MN, bool B_MN, typename T>
-__global__ void __launch_bounds__(kGemmThreads, 1)
-gemm_kernel(const __grid_constant__ CUtensorMap tmA, const __grid_constant__ CUtensorMap tmB, const GemmParams p) {
+__global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kGemmThreads, 1)
+gemm_kernel(const __grid_constant__ CUtensorMap tmA, const __grid_constant__ CUtensorMap tmA_half,
+            const __grid_constant__ CUtensorMap tmB, const __grid_constant__ CUtensorMap tmB_half, const GemmParams p) {
     extern __shared__ unsigned char smem_raw[];
     unsigned char *smem = reinterpret_cast<unsigned char *>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~(uintptr_t)1023);
     float *stage_out = reinterpret_cast<float *>(smem + kStages * kStageBytes);
@@ -88,6 +178,7 @@ gemm_kernel(const __grid_constant__ CUtensorMap tmA, const __grid_constant__ CUt
     uint64_t *full = bars, *empty = bars + kStages, *acc_full = bars + 2 * kStages, *acc_empty = acc_full + 2;
     uint32_t *tmem_slot = reinterpret_cast<uint32_t *>(acc_empty + 2);
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+    const int rank = (int)cta_rank(), pair = blockIdx.x >> 1, pairs = gridDim.x >> 1;
     if (threadIdx.x == 0) {
         for (int i = 0; i < kStages; ++i) {
             mbar_init(full + i, 1);
@@ -95,137 +186,172 @@ gemm_kernel(const __grid_constant__ CUtensorMap tmA, const __grid_constant__ CUt
         }
         for (int i = 0; i < 2; ++i) {
             mbar_init(acc_full + i, 1);
-            mbar_init(acc_empty + i, kEpiWarps);
+            mbar_init(acc_empty + i, 2 * kEpiWarps);
         }
         fence_mbar_init();
-        tma_prefetch_map(&tmA);
-        tma_prefetch_map(&tmB);
+        tma_prefetch_map(A_MN && !p.a_blocks ? &tmA_half : &tmA);
+        tma_prefetch_map(B_MN && !p.b_blocks ? &tmB_half : &tmB);
     }
-    if (warp == 1) tmem_alloc(tmem_slot, 512);
+    if (warp == 1) pair_tmem_alloc(tmem_slot, 512);
     tc_fence_before();
     __syncthreads();
+    cluster_sync();
     tc_fence_after();
     const uint32_t tmem = *tmem_slot;
-    const int tiles = p.mt * p.nt, steps = p.kblocks * p.terms;
-    if (warp == 0) {
+    const int steps = p.kblocks * p.terms;
+    if (warp == 0 || warp == 2) {                  // one fetches A, the other B
         uint32_t it = 0;
         bool ok = true;
         if (lane == 0) {
-            for (int t = blockIdx.x; t < tiles && ok; t += gridDim.x) {
-                int m0, n0;
-                tile_at(p, t, m0, n0);
-                for (int s = 0; s < steps; ++s, ++it) {
-                    const int st = it % kStages, k0 = s % p.kblocks * kBK, term = 6 - p.terms + s / p.kblocks;
-                    if (!(ok = mbar_wait(empty + st, (it / kStages & 1) ^ 1))) {
-                        report_status(p.status, kStatusTimeout);
-                        break;
-                    }
-                    unsigned char *a = smem + st * kStageBytes, *b = a + kBM * kBK * 2;
-                    mbar_expect_tx(full + st, (kBM + p.BN) * kBK * 2);
+            int st = 0;
+            uint32_t phase = 1;
+            for (int i = pair; i < p.items && ok; i += pairs) {
+                int m0, n0, BN;
+                item_at(p, i, m0, n0, BN);
+                const int boxes = (BN / 2 + 63) / 64, am = m0 + rank * kBM, bn = n0 + rank * (BN / 2);
+                for (int term = 6 - p.terms; term < 6 && ok; ++term) {
                     const int ta = kTermA[term], tb = kTermB[term];
-                    if (A_MN) {
-#pragma unroll
-                        for (int i = 0; i < kBM / 64; ++i) tma_load_3d(a + i * 8192, &tmA, full + st, m0 + 64 * i, k0, ta);
-                    } else {
-                        tma_load_3d(a, &tmA, full + st, k0, m0, ta);
-                    }
-                    if (B_MN) {
-                        for (int i = 0; i < p.BN / 64; ++i) tma_load_3d(b + i * 8192, &tmB, full + st, n0 + 64 * i, k0, tb);
-                    } else {
-                        tma_load_3d(b, &tmB, full + st, k0, n0, tb);
+                    for (int k = 0; k < p.kblocks; ++k, ++it) {
+                        if (!(ok = mbar_wait(empty + st, phase))) {
+                            report_status(p.status, kStatusTimeout);
+                            break;
+                        }
+                        const uint32_t a = smem_addr(smem) + st * kStageBytes, bar = leader_addr(full + st);
+                        if (warp == 0) {
+                            if (rank == 0) mbar_expect_tx(full + st, 2 * (2 + boxes) * kBox);
+                            load_tile<A_MN>(a, &tmA, &tmA_half, p.a_blocks, 2, bar, am, k * kBK, ta);
+                        } else {
+                            load_tile<B_MN>(a + 2 * kBox, &tmB, &tmB_half, p.b_blocks, boxes, bar, bn, k * kBK, tb);
+                        }
+                        if (++st == kStages) {
+                            st = 0;
+                            phase ^= 1;
+                        }
                     }
                 }
             }
             // copies that nothing has waited for (only after a wait ran out) land before the CTA ends
-            if (!ok)
+            if (!ok && rank == 0)
                 for (uint32_t i = it < kStages ? 0 : it - kStages; i < it; ++i) mbar_wait(full + i % kStages, i / kStages & 1);
         }
         __syncwarp();
     } else if (warp == 1) {
-        const uint32_t lead = elect_one_sync();
-        const uint32_t idesc = umma_idesc_t(1, kBM, p.BN, A_MN, B_MN);
-        uint32_t it = 0, n_tile = 0;
-        bool ok = true;
-        for (int t = blockIdx.x; t < tiles && ok; t += gridDim.x, ++n_tile) {
-            const int acc = n_tile & 1;
-            ok = mbar_wait(acc_empty + acc, (n_tile / 2 & 1) ^ 1);
-            tc_fence_after();
-            for (int s = 0; s < steps && ok; ++s, ++it) {
-                const int st = it % kStages;
-                ok = mbar_wait(full + st, it / kStages & 1);
-                if (!ok) break;
+        if (rank == 0) {
+            const uint32_t lead = elect_one_sync();
+            uint32_t n_tile = 0, phase = 0;
+            int st = 0;
+            bool ok = true;
+            for (int i = pair; i < p.items && ok; i += pairs, ++n_tile) {
+                int m0, n0, BN;
+                item_at(p, i, m0, n0, BN);
+                const uint32_t idesc = umma_idesc_t(1, 2 * kBM, BN, A_MN, B_MN);
+                const int acc = n_tile & 1;
+                ok = mbar_wait(acc_empty + acc, (n_tile / 2 & 1) ^ 1);
                 tc_fence_after();
-                const uint32_t base = smem_addr(smem) + st * kStageBytes;
-                uint64_t a = sw128_desc(base, A_MN), b = sw128_desc(base + kBM * kBK * 2, B_MN);
+                for (int s = 0; s < steps; ++s) {
+                    ok = ok && mbar_wait(full + st, phase);
+                    if (!ok) break;
+                    tc_fence_after();
+                    const uint32_t base = smem_addr(smem) + st * kStageBytes;
+                    uint64_t a = sw128_desc(base, A_MN), b = sw128_desc(base + 2 * kBox, B_MN);
 #pragma unroll
-                for (int k = 0; k < kBK / 16; ++k) {
-                    umma_bf16_w(tmem + acc * kMaxBN, a, b, idesc, s > 0 || k > 0, lead);
-                    a += A_MN ? 2048 >> 4 : 32 >> 4;
-                    b += B_MN ? 2048 >> 4 : 32 >> 4;
+                    for (int k = 0; k < kBK / 16; ++k) {
+                        pair_umma_bf16(tmem + acc * kMaxBN, a, b, idesc, s > 0 || k > 0, lead);
+                        a += A_MN ? 2048 >> 4 : 32 >> 4;
+                        b += B_MN ? 2048 >> 4 : 32 >> 4;
+                    }
+                    pair_commit(empty + st, lead);
+                    if (++st == kStages) {
+                        st = 0;
+                        phase ^= 1;
+                    }
                 }
-                umma_commit_w(empty + st, lead);
+                if (ok) pair_commit(acc_full + acc, lead);
             }
-            if (ok) umma_commit_w(acc_full + acc, lead);
+            if (!ok && lane == 0) report_status(p.status, kStatusTimeout);
         }
-        if (!ok && lane == 0) report_status(p.status, kStatusTimeout);
     } else {
-        const int quarter = warp & 3, half = (warp - 2) >> 2;      // tensor-memory lanes; 16-column chunks in turn
-        float *mine = stage_out + (warp - 2) * 32 * kEpiPitch;
+        const int quarter = warp & 3, half = (warp - 3) >> 2;      // tensor-memory lanes; 16-column chunks in turn
+        float *mine = stage_out + (warp - 3) * 32 * kEpiPitch;
         const T *bias = static_cast<const T *>(p.bias), *res = static_cast<const T *>(p.res);
         T *out = static_cast<T *>(p.out), *pre = static_cast<T *>(p.pre);
+        constexpr int V = 16 / sizeof(T), LPR = 16 / V, RPP = 32 / LPR;    // columns per lane, lanes per row, rows per pass
         uint32_t n_tile = 0;
-        for (int t = blockIdx.x; t < tiles; t += gridDim.x, ++n_tile) {
+        for (int i = pair; i < p.items; i += pairs, ++n_tile) {
             const int acc = n_tile & 1;
-            int m0, n0;
-            tile_at(p, t, m0, n0);
+            int m0, n0, BN;
+            item_at(p, i, m0, n0, BN);
+            const int row0 = m0 + rank * kBM + 32 * quarter, chunks = BN / 16;
+            // the residual and bias of a chunk, loaded a chunk ahead
+            Raw<T, V> next_res[LPR], next_bias;
+            auto fetch = [&](int c) {
+                const int col = n0 + c * 16 + lane % LPR * V;
+                const bool in = p.vec && c < chunks && col < p.N;
+                next_bias = Raw<T, V>();
+                if (in && bias != nullptr) next_bias = load_raw<T, V>(bias + col);
+#pragma unroll
+                for (int h = 0; h < LPR; ++h) {
+                    const int row = row0 + h * RPP + lane / LPR;
+                    next_res[h] = Raw<T, V>();
+                    if (in && res != nullptr && row < p.M) next_res[h] = load_raw<T, V>(res + (size_t)row * p.ldres + col);
+                }
+            };
+            fetch(half);
             if (!mbar_wait(acc_full + acc, n_tile / 2 & 1)) {
                 if (lane == 0) report_status(p.status, kStatusTimeout);
                 break;
             }
             tc_fence_after();
-            const int row0 = m0 + 32 * quarter, chunks = p.BN / 16;
+            const uint32_t drained = leader_addr(acc_empty + acc);
             for (int c = half; c < chunks; c += 2) {
                 float2 v[8];
                 tmem_ld16(tmem + ((uint32_t)(32 * quarter) << 16) + acc * kMaxBN + c * 16, v);
+                Raw<T, V> now_res[LPR], now_bias = next_bias;
+#pragma unroll
+                for (int h = 0; h < LPR; ++h) now_res[h] = next_res[h];
+                fetch(c + 2);
                 tmem_wait_ld();
                 if (c + 2 >= chunks) {                     // this warp's last read of the accumulator
                     tc_fence_before();
                     __syncwarp();
-                    if (lane == 0) mbar_arrive(acc_empty + acc);
+                    if (lane == 0) arrive_cluster(drained);
                 }
                 const int col0 = n0 + c * 16;
                 if (row0 >= p.M || col0 >= p.N) continue;
                 // through shared memory, so that neighbouring lanes hold neighbouring columns
 #pragma unroll
-                for (int i = 0; i < 4; ++i)
-                    *reinterpret_cast<float4 *>(mine + lane * kEpiPitch + 4 * i) =
-                        make_float4(v[2 * i].x, v[2 * i].y, v[2 * i + 1].x, v[2 * i + 1].y);
+                for (int j = 0; j < 4; ++j)
+                    *reinterpret_cast<float4 *>(mine + lane * kEpiPitch + 4 * j) =
+                        make_float4(v[2 * j].x, v[2 * j].y, v[2 * j + 1].x, v[2 * j + 1].y);
                 __syncwarp();
                 if (p.vec) {
-                    constexpr int V = 16 / sizeof(T), LPR = 16 / V;    // columns per lane, lanes per row
+                    float bs[V];
+                    unpack<T, V>(now_bias, bs);
 #pragma unroll
                     for (int h = 0; h < LPR; ++h) {
-                        const int r = h * (32 / LPR) + lane / LPR, col = col0 + lane % LPR * V;
+                        const int r = h * RPP + lane / LPR, col = col0 + lane % LPR * V;
                         const size_t row = row0 + r;
                         if (row >= p.M || col >= p.N) continue;
                         float o[V], e[V];
 #pragma unroll
-                        for (int i = 0; i < V / 4; ++i) {
-                            const float4 x = *reinterpret_cast<const float4 *>(mine + r * kEpiPitch + lane % LPR * V + 4 * i);
-                            o[4 * i] = x.x; o[4 * i + 1] = x.y; o[4 * i + 2] = x.z; o[4 * i + 3] = x.w;
+                        for (int j = 0; j < V / 4; ++j) {
+                            const float4 x = *reinterpret_cast<const float4 *>(mine + r * kEpiPitch + lane % LPR * V + 4 * j);
+                            o[4 * j] = x.x; o[4 * j + 1] = x.y; o[4 * j + 2] = x.z; o[4 * j + 3] = x.w;
                         }
-                        if (bias != nullptr) {
-                            load_vec<T, V>(bias + col, e);
 #pragma unroll
-                            for (int i = 0; i < V; ++i) o[i] += e[i];
-                        }
+                        for (int j = 0; j < V; ++j) o[j] += bs[j];
                         if (pre != nullptr) store_vec<T, V>(pre + row * p.N + col, o);
+                        if (p.act == kActSilu) {
 #pragma unroll
-                        for (int i = 0; i < V; ++i) o[i] = act_rt(p.act, o[i]);
+                            for (int j = 0; j < V; ++j) o[j] = silu_hw(o[j]);
+                        } else if (p.act == kActGelu) {
+#pragma unroll
+                            for (int j = 0; j < V; ++j) o[j] = gelu_f(o[j]);
+                        }
                         if (res != nullptr) {
-                            load_vec<T, V>(res + row * p.ldres + col, e);
+                            unpack<T, V>(now_res[h], e);
 #pragma unroll
-                            for (int i = 0; i < V; ++i) o[i] = __fadd_rn(o[i], e[i]);
+                            for (int j = 0; j < V; ++j) o[j] = __fadd_rn(o[j], e[j]);
                         }
                         store_vec<T, V>(out + row * p.N + col, o);
                     }
@@ -248,8 +374,9 @@ gemm_kernel(const __grid_constant__ CUtensorMap tmA, const __grid_constant__ CUt
     }
     tc_fence_before();
     __syncthreads();
+    cluster_sync();                                // the pair's products and arrivals are over
     tc_fence_after();
-    if (warp == 1) tmem_dealloc(tmem, 512);
+    if (warp == 1) pair_tmem_dealloc(tmem, 512);
 }
 
 // x as bf16 operand rows of `cols8` elements: a copy (bf16) or three terms (float32), planes of
@@ -361,21 +488,37 @@ int gemm(const char *name, const Operand &A, const Operand &B, int M, int N, int
     p.kblocks = (K + kBK - 1) / kBK;
     const int planes = sizeof(T) == 4 ? 3 : 1;
     p.terms = sizeof(T) == 4 ? 6 : 1;
-    p.BN = N <= 64 ? 64 : N <= 128 ? 128 : kMaxBN;
-    p.mt = (M + kBM - 1) / kBM;
-    p.nt = (N + p.BN - 1) / p.BN;
-    p.panel = p.nt < 16 ? p.nt : 16;
+    // a product with an odd number of columns left gets narrower tiles at the end
+    p.mt = (M + 2 * kBM - 1) / (2 * kBM);
+    p.nt = N / kMaxBN;
+    const int unit = B_MN && B.cols % 64 == 0 ? 128 : 32;   // each CTA's half starts on a 64-column block
+    p.edge = (N % kMaxBN + unit - 1) / unit * unit;
+    p.panel = p.nt < 8 ? (p.nt > 0 ? p.nt : 1) : 8;
+    const long long tiles = (long long)p.mt * p.nt;
+    const int last = (int)(tiles % kPairs);            // tiles of an incomplete last round
+    if (tiles > 0x3fffffffLL) return GDN_ERR_UNSUPPORTED_SHAPE;
+    p.halves = last > 0 && last <= kPairs / 2 ? 2 * last : 0;
+    p.whole = (int)tiles - p.halves / 2;
+    p.items = p.whole + p.halves + (p.edge > 0 ? p.mt : 0);
     const int V = 16 / (int)sizeof(T);
     p.vec = N % V == 0 && (uintptr_t)e.res % 16 == 0 && e.ldres % V == 0;
-    CUtensorMap tmA, tmB;
+    CUtensorMap tm[4];                                 // A, one box of A, B, one box of B
     int rc;
-    if ((rc = api_planes_map(&tmA, A.p, A.cols, A.rows, planes, A.ld, kBK, A_MN ? 64 : kBM)) != 0) return rc;
-    if ((rc = api_planes_map(&tmB, B.p, B.cols, B.rows, planes, B.ld, kBK, B_MN ? 64 : p.BN)) != 0) return rc;
+    for (int i = 0; i < 4; ++i) {
+        const Operand &o = i < 2 ? A : B;
+        const bool mn = i < 2 ? A_MN : B_MN, blocks = mn && o.cols % 64 == 0;
+        const int boxes = 2 - i % 2;
+        (i < 2 ? p.a_blocks : p.b_blocks) = blocks;
+        if (mn && !blocks && boxes == 2) {             // not used
+            tm[i] = {};
+            continue;
+        }
+        if ((rc = api_planes_map(&tm[i], o.p, o.cols, o.rows, planes, o.ld, mn ? kBK : 64 * boxes, blocks ? boxes : 0)) != 0) return rc;
+    }
     cudaError_t err = cudaFuncSetAttribute(gemm_kernel<A_MN, B_MN, T>, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)kGemmSmem);
     if (err != cudaSuccess) return api_cuda_status(err);
-    const long long tiles = (long long)p.mt * p.nt;
     timing_mark(name, 0, s);
-    gemm_kernel<A_MN, B_MN, T><<<(int)(tiles < kSms ? tiles : kSms), kGemmThreads, kGemmSmem, s>>>(tmA, tmB, p);
+    gemm_kernel<A_MN, B_MN, T><<<2 * (p.items < kPairs ? p.items : kPairs), kGemmThreads, kGemmSmem, s>>>(tm[0], tm[1], tm[2], tm[3], p);
     timing_mark(name, 1, s);
     return api_cuda_status(cudaGetLastError());
 }

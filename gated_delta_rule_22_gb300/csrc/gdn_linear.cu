@@ -21,14 +21,17 @@ namespace gdn {
 
 namespace {
 
-constexpr int kBM = 128, kBK = 64, kMaxBN = 256, kStages = 6;   // per CTA of a pair: 128 rows, 64 deep
+constexpr int kBM = 128, kBK = 64, kMaxBN = 256, kStages = 5;   // per CTA of a pair: 128 rows, 64 deep
 constexpr int kPairs = 76;                          // pairs of SMs
 constexpr int kEpiWarps = 8, kGemmThreads = 96 + 32 * kEpiWarps;   // + two fetching warps, one issuing
-constexpr int kEpiPitch = 20;                       // floats per staged row of 16 columns
+constexpr int kChunk = 32, kEpiPitch = kChunk + 4;  // columns an epilogue warp takes at once; floats per staged row
 constexpr int kBox = 64 * kBK * 2;                  // one TMA box: 64 rows x 128 bytes
 constexpr int kStageBytes = 4 * kBox;               // two boxes of A, two of B
 constexpr size_t kGemmSmem = 1024 + (size_t)kStages * kStageBytes + kEpiWarps * 32 * kEpiPitch * 4 + 256;
-constexpr int kBiasSlices = 64;
+constexpr int kBiasSlices = 128;
+// float32 only: K blocks per run of the tensor cores' accumulator, whose additions truncate; each run's
+// sum is added in float32 registers with rounding, which keeps the error at that of float32 arithmetic.
+constexpr int kRun = 4;
 
 size_t up256(size_t n) { return (n + 255) / 256 * 256; }
 int up8(int n) { return (n + 7) / 8 * 8; }
@@ -40,12 +43,15 @@ __constant__ signed char kTermA[6] = {0, 2, 1, 0, 1, 0}, kTermB[6] = {2, 0, 1, 1
 // numbered: whole tiles of 256 columns (within a panel of columns the columns first); then the tiles
 // of an incomplete last round, cut into halves of 128 columns where that lets every pair take at most
 // one; then the tiles of the last, narrower columns, of as many columns as are left (in 32s).
+template <typename T>
+constexpr int kTileN = sizeof(T) == 4 ? 128 : kMaxBN;   // columns of a whole tile
+
 struct GemmParams {
     const void *bias, *res;
     void *out, *pre;
     int *status;
     long long ldres;
-    int M, N, kblocks, terms, act;
+    int M, N, kblocks, run, act;   // run: K blocks per accumulation
     int mt, nt, panel;          // tiles along m and n (of 256 columns), n tiles walked together
     int whole, halves, edge;    // whole tiles, half tiles, columns of the edge tiles
     int items;
@@ -53,21 +59,22 @@ struct GemmParams {
     int a_blocks, b_blocks;     // MN-major operands of whole 64-column blocks
 };
 
+template <int TN>
 __device__ __forceinline__ void item_at(const GemmParams &p, int i, int &m0, int &n0, int &BN) {
     int t = i;
-    BN = kMaxBN;
+    BN = TN;
     if (i >= p.whole + p.halves) {
         m0 = (i - p.whole - p.halves) * 2 * kBM;
-        n0 = p.nt * kMaxBN;
+        n0 = p.nt * TN;
         BN = p.edge;
         return;
     }
     if (i >= p.whole) t = p.whole + (i - p.whole) / 2;
     const int per = p.panel * p.mt, q = t / per, r = t % per, w = min(p.panel, p.nt - q * p.panel);
     m0 = r / w * 2 * kBM;
-    n0 = (q * p.panel + r % w) * kMaxBN;
+    n0 = (q * p.panel + r % w) * TN;
     if (i >= p.whole) {
-        BN = kMaxBN / 2;
+        BN = TN / 2;
         n0 += (i - p.whole) % 2 * BN;
     }
 }
@@ -156,9 +163,6 @@ __device__ __forceinline__ uint64_t sw128_desc(uint32_t start, bool mn) {
 __device__ __forceinline__ float act_rt(int act, float x) {
     return act == kActSilu ? silu_hw(x) : act == kActGelu ? gelu_f(x) : x;
 }
-__device__ __forceinline__ float dact_rt(int act, float x) {
-    return act == kActSilu ? dsilu_hw(x) : act == kActGelu ? dgelu_f(x) : 1.f;
-}
 
 }  // namespace
 
@@ -198,7 +202,7 @@ gemm_kernel(const __grid_constant__ CUtensorMap tmA, const __grid_constant__ CUt
     cluster_sync();
     tc_fence_after();
     const uint32_t tmem = *tmem_slot;
-    const int steps = p.kblocks * p.terms;
+    constexpr int TN = kTileN<T>, TERMS = sizeof(T) == 4 ? 6 : 1;
     if (warp == 0 || warp == 2) {                  // one fetches A, the other B
         uint32_t it = 0;
         bool ok = true;
@@ -207,11 +211,12 @@ gemm_kernel(const __grid_constant__ CUtensorMap tmA, const __grid_constant__ CUt
             uint32_t phase = 1;
             for (int i = pair; i < p.items && ok; i += pairs) {
                 int m0, n0, BN;
-                item_at(p, i, m0, n0, BN);
+                item_at<TN>(p, i, m0, n0, BN);
                 const int boxes = (BN / 2 + 63) / 64, am = m0 + rank * kBM, bn = n0 + rank * (BN / 2);
-                for (int term = 6 - p.terms; term < 6 && ok; ++term) {
+                for (int kr = 0; kr < p.kblocks && ok; kr += p.run)
+                for (int term = 6 - TERMS; term < 6 && ok; ++term) {
                     const int ta = kTermA[term], tb = kTermB[term];
-                    for (int k = 0; k < p.kblocks; ++k, ++it) {
+                    for (int k = kr; k < min(kr + p.run, p.kblocks); ++k, ++it) {
                         if (!(ok = mbar_wait(empty + st, phase))) {
                             report_status(p.status, kStatusTimeout);
                             break;
@@ -241,101 +246,152 @@ gemm_kernel(const __grid_constant__ CUtensorMap tmA, const __grid_constant__ CUt
             uint32_t n_tile = 0, phase = 0;
             int st = 0;
             bool ok = true;
-            for (int i = pair; i < p.items && ok; i += pairs, ++n_tile) {
+            for (int i = pair; i < p.items && ok; i += pairs) {
                 int m0, n0, BN;
-                item_at(p, i, m0, n0, BN);
+                item_at<TN>(p, i, m0, n0, BN);
                 const uint32_t idesc = umma_idesc_t(1, 2 * kBM, BN, A_MN, B_MN);
-                const int acc = n_tile & 1;
-                ok = mbar_wait(acc_empty + acc, (n_tile / 2 & 1) ^ 1);
-                tc_fence_after();
-                for (int s = 0; s < steps; ++s) {
-                    ok = ok && mbar_wait(full + st, phase);
-                    if (!ok) break;
+                for (int kr = 0; kr < p.kblocks && ok; kr += p.run, ++n_tile) {
+                    const int acc = n_tile & 1, steps = min(p.run, p.kblocks - kr) * TERMS;
+                    ok = mbar_wait(acc_empty + acc, (n_tile / 2 & 1) ^ 1);
                     tc_fence_after();
-                    const uint32_t base = smem_addr(smem) + st * kStageBytes;
-                    uint64_t a = sw128_desc(base, A_MN), b = sw128_desc(base + 2 * kBox, B_MN);
+                    for (int s = 0; s < steps; ++s) {
+                        ok = ok && mbar_wait(full + st, phase);
+                        if (!ok) break;
+                        tc_fence_after();
+                        const uint32_t base = smem_addr(smem) + st * kStageBytes;
+                        uint64_t a = sw128_desc(base, A_MN), b = sw128_desc(base + 2 * kBox, B_MN);
 #pragma unroll
-                    for (int k = 0; k < kBK / 16; ++k) {
-                        pair_umma_bf16(tmem + acc * kMaxBN, a, b, idesc, s > 0 || k > 0, lead);
-                        a += A_MN ? 2048 >> 4 : 32 >> 4;
-                        b += B_MN ? 2048 >> 4 : 32 >> 4;
+                        for (int k = 0; k < kBK / 16; ++k) {
+                            pair_umma_bf16(tmem + acc * kMaxBN, a, b, idesc, s > 0 || k > 0, lead);
+                            a += A_MN ? 2048 >> 4 : 32 >> 4;
+                            b += B_MN ? 2048 >> 4 : 32 >> 4;
+                        }
+                        pair_commit(empty + st, lead);
+                        if (++st == kStages) {
+                            st = 0;
+                            phase ^= 1;
+                        }
                     }
-                    pair_commit(empty + st, lead);
-                    if (++st == kStages) {
-                        st = 0;
-                        phase ^= 1;
-                    }
+                    if (ok) pair_commit(acc_full + acc, lead);
                 }
-                if (ok) pair_commit(acc_full + acc, lead);
             }
             if (!ok && lane == 0) report_status(p.status, kStatusTimeout);
         }
     } else {
-        const int quarter = warp & 3, half = (warp - 3) >> 2;      // tensor-memory lanes; 16-column chunks in turn
+        const int quarter = warp & 3, half = (warp - 3) >> 2;      // tensor-memory lanes; chunks in turn
         float *mine = stage_out + (warp - 3) * 32 * kEpiPitch;
         const T *bias = static_cast<const T *>(p.bias), *res = static_cast<const T *>(p.res);
         T *out = static_cast<T *>(p.out), *pre = static_cast<T *>(p.pre);
-        constexpr int V = 16 / sizeof(T), LPR = 16 / V, RPP = 32 / LPR;    // columns per lane, lanes per row, rows per pass
+        constexpr int V = 16 / sizeof(T), LPR = kChunk / V, RPP = 32 / LPR;   // columns per lane, lanes per row, rows per pass
+        constexpr int CW = TN / (2 * kChunk);          // chunks of a tile per warp
+        const int lr = lane / LPR, lc = lane % LPR * V;
         uint32_t n_tile = 0;
-        for (int i = pair; i < p.items; i += pairs, ++n_tile) {
-            const int acc = n_tile & 1;
+        bool ok = true;
+        for (int i = pair; i < p.items && ok; i += pairs) {
             int m0, n0, BN;
-            item_at(p, i, m0, n0, BN);
-            const int row0 = m0 + rank * kBM + 32 * quarter, chunks = BN / 16;
+            item_at<TN>(p, i, m0, n0, BN);
+            const int row0 = m0 + rank * kBM + 32 * quarter, chunks = BN / kChunk;
             // the residual and bias of a chunk, loaded a chunk ahead
             Raw<T, V> next_res[LPR], next_bias;
             auto fetch = [&](int c) {
-                const int col = n0 + c * 16 + lane % LPR * V;
+                const int col = n0 + c * kChunk + lc;
                 const bool in = p.vec && c < chunks && col < p.N;
                 next_bias = Raw<T, V>();
                 if (in && bias != nullptr) next_bias = load_raw<T, V>(bias + col);
+                if (res == nullptr) return;
 #pragma unroll
                 for (int h = 0; h < LPR; ++h) {
-                    const int row = row0 + h * RPP + lane / LPR;
-                    next_res[h] = Raw<T, V>();
-                    if (in && res != nullptr && row < p.M) next_res[h] = load_raw<T, V>(res + (size_t)row * p.ldres + col);
+                    const int row = row0 + h * RPP + lr;
+                    if (in && row < p.M) next_res[h] = load_raw<T, V>(res + (size_t)row * p.ldres + col);
                 }
             };
             fetch(half);
-            if (!mbar_wait(acc_full + acc, n_tile / 2 & 1)) {
-                if (lane == 0) report_status(p.status, kStatusTimeout);
-                break;
+            float sum[sizeof(T) == 4 ? CW : 1][kChunk];    // float32: the sum of the runs so far
+            if constexpr (sizeof(T) == 4) {
+#pragma unroll
+                for (int k = 0; k < CW; ++k)
+#pragma unroll
+                    for (int j = 0; j < kChunk; ++j) sum[k][j] = 0.f;
             }
-            tc_fence_after();
-            const uint32_t drained = leader_addr(acc_empty + acc);
-            for (int c = half; c < chunks; c += 2) {
-                float2 v[8];
-                tmem_ld16(tmem + ((uint32_t)(32 * quarter) << 16) + acc * kMaxBN + c * 16, v);
+            uint32_t src = 0, drained = 0;
+            auto begin_run = [&]() {
+                const int acc = n_tile & 1;
+                if (!mbar_wait(acc_full + acc, n_tile / 2 & 1)) {
+                    if (lane == 0) report_status(p.status, kStatusTimeout);
+                    return false;
+                }
+                ++n_tile;
+                tc_fence_after();
+                src = tmem + ((uint32_t)(32 * quarter) << 16) + acc * kMaxBN;
+                drained = leader_addr(acc_empty + acc);
+                return true;
+            };
+            auto end_run = [&]() {                     // this warp's last read of the accumulator is over
+                tc_fence_before();
+                __syncwarp();
+                if (lane == 0) arrive_cluster(drained);
+            };
+            auto read = [&](int c, float2 (&v)[kChunk / 2]) {
+                tmem_ld16(src + c * kChunk, *reinterpret_cast<float2(*)[8]>(v));
+                tmem_ld16(src + c * kChunk + 16, *reinterpret_cast<float2(*)[8]>(v + 8));
+            };
+            if constexpr (sizeof(T) == 4) {
+                for (int kr = p.run; kr < p.kblocks && ok; kr += p.run) {      // all runs but the last
+                    if (!(ok = begin_run())) break;
+#pragma unroll
+                    for (int k = 0; k < CW; ++k) {
+                        if (half + 2 * k >= chunks) continue;
+                        float2 v[kChunk / 2];
+                        read(half + 2 * k, v);
+                        tmem_wait_ld();
+#pragma unroll
+                        for (int j = 0; j < kChunk / 2; ++j) {
+                            sum[k][2 * j] += v[j].x;
+                            sum[k][2 * j + 1] += v[j].y;
+                        }
+                    }
+                    end_run();
+                }
+            }
+            if (!ok || !(ok = begin_run())) break;
+            if (half >= chunks) {
+                end_run();
+                continue;
+            }
+            float2 ahead[kChunk / 2];
+            read(half, ahead);
+            // one chunk; `acc` the float32 sum of the earlier runs
+            auto finish = [&](int c, const float *acc) {
+                tmem_wait_ld();
+                // through shared memory, so that neighbouring lanes hold neighbouring columns
+#pragma unroll
+                for (int j = 0; j < kChunk / 4; ++j) {
+                    float4 x = make_float4(ahead[2 * j].x, ahead[2 * j].y, ahead[2 * j + 1].x, ahead[2 * j + 1].y);
+                    if constexpr (sizeof(T) == 4) {
+                        x.x += acc[4 * j]; x.y += acc[4 * j + 1]; x.z += acc[4 * j + 2]; x.w += acc[4 * j + 3];
+                    }
+                    *reinterpret_cast<float4 *>(mine + lane * kEpiPitch + 4 * j) = x;
+                }
+                if (c + 2 < chunks) read(c + 2, ahead);
+                else end_run();
                 Raw<T, V> now_res[LPR], now_bias = next_bias;
 #pragma unroll
                 for (int h = 0; h < LPR; ++h) now_res[h] = next_res[h];
                 fetch(c + 2);
-                tmem_wait_ld();
-                if (c + 2 >= chunks) {                     // this warp's last read of the accumulator
-                    tc_fence_before();
-                    __syncwarp();
-                    if (lane == 0) arrive_cluster(drained);
-                }
-                const int col0 = n0 + c * 16;
-                if (row0 >= p.M || col0 >= p.N) continue;
-                // through shared memory, so that neighbouring lanes hold neighbouring columns
-#pragma unroll
-                for (int j = 0; j < 4; ++j)
-                    *reinterpret_cast<float4 *>(mine + lane * kEpiPitch + 4 * j) =
-                        make_float4(v[2 * j].x, v[2 * j].y, v[2 * j + 1].x, v[2 * j + 1].y);
                 __syncwarp();
+                const int col0 = n0 + c * kChunk;
                 if (p.vec) {
                     float bs[V];
                     unpack<T, V>(now_bias, bs);
 #pragma unroll
                     for (int h = 0; h < LPR; ++h) {
-                        const int r = h * RPP + lane / LPR, col = col0 + lane % LPR * V;
+                        const int r = h * RPP + lr, col = col0 + lc;
                         const size_t row = row0 + r;
                         if (row >= p.M || col >= p.N) continue;
                         float o[V], e[V];
 #pragma unroll
                         for (int j = 0; j < V / 4; ++j) {
-                            const float4 x = *reinterpret_cast<const float4 *>(mine + r * kEpiPitch + lane % LPR * V + 4 * j);
+                            const float4 x = *reinterpret_cast<const float4 *>(mine + r * kEpiPitch + lc + 4 * j);
                             o[4 * j] = x.x; o[4 * j + 1] = x.y; o[4 * j + 2] = x.z; o[4 * j + 3] = x.w;
                         }
 #pragma unroll
@@ -356,12 +412,12 @@ gemm_kernel(const __grid_constant__ CUtensorMap tmA, const __grid_constant__ CUt
                         store_vec<T, V>(out + row * p.N + col, o);
                     }
                 } else {
-                    for (int h = 0; h < 16; ++h) {
-                        const int r = 2 * h + (lane >> 4), col = col0 + (lane & 15);
+                    const int col = col0 + lane;
+                    const float b = bias != nullptr && col < p.N ? to_f32(bias[col]) : 0.f;
+                    for (int r = 0; r < 32 && row0 + r < p.M; ++r) {
+                        if (col >= p.N) continue;
                         const size_t row = row0 + r;
-                        if (row >= p.M || col >= p.N) continue;
-                        float o = mine[r * kEpiPitch + (lane & 15)];
-                        if (bias != nullptr) o += to_f32(bias[col]);
+                        float o = mine[r * kEpiPitch + lane] + b;
                         if (pre != nullptr) pre[row * p.N + col] = from_f32<T>(o);
                         o = act_rt(p.act, o);
                         if (res != nullptr) o = __fadd_rn(o, to_f32(res[row * p.ldres + col]));
@@ -369,6 +425,14 @@ gemm_kernel(const __grid_constant__ CUtensorMap tmA, const __grid_constant__ CUt
                     }
                 }
                 __syncwarp();
+            };
+            if constexpr (sizeof(T) == 4) {
+#pragma unroll
+                for (int k = 0; k < CW; ++k)
+                    if (half + 2 * k < chunks) finish(half + 2 * k, sum[k]);
+            } else {
+#pragma unroll 1
+                for (int c = half; c < chunks; c += 2) finish(c, nullptr);
             }
         }
     }
@@ -388,58 +452,100 @@ __device__ __forceinline__ void split3(float x, __nv_bfloat16 (&t)[3]) {
     t[1] = __float2bfloat16_rz(fine ? r : 0.f);
     t[2] = __float2bfloat16_rn(fine ? r - __bfloat162float(t[1]) : 0.f);
 }
-template <typename T>
+// V elements of a row, as the operand's planes from `out` on (`plane` elements apart)
+template <typename T, int V>
+__device__ __forceinline__ void store_operand(__nv_bfloat16 *out, size_t plane, const float (&x)[V]) {
+    if constexpr (sizeof(T) == 2) {
+        store_vec<__nv_bfloat16, V>(out, x);
+    } else {
+        __nv_bfloat16 t[V][3];
+#pragma unroll
+        for (int v = 0; v < V; ++v) split3(x[v], t[v]);
+#pragma unroll
+        for (int i = 0; i < 3; ++i) {
+            float e[V];                                // exact: terms are bf16
+#pragma unroll
+            for (int v = 0; v < V; ++v) e[v] = __bfloat162float(t[v][i]);
+            store_vec<__nv_bfloat16, V>(out + i * plane, e);
+        }
+    }
+}
+template <typename T, int V>
 __global__ void __launch_bounds__(256) linear_pack_kernel(const T *x, long long ld, __nv_bfloat16 *out, int rows, int cols, int cols8) {
-    const int c = blockIdx.x * 256 + threadIdx.x;
+    const int c = (blockIdx.x * 256 + threadIdx.x) * V;
     if (c >= cols) return;
     const size_t plane = (size_t)rows * cols8;
-    for (int r = blockIdx.y; r < rows; r += gridDim.y) {
-        const size_t at = (size_t)r * cols8 + c;
-        if constexpr (sizeof(T) == 2) {
-            out[at] = x[(size_t)r * ld + c];
-        } else {
-            __nv_bfloat16 t[3];
-            split3(x[(size_t)r * ld + c], t);
+    int r = blockIdx.y;
+    constexpr int U = 4;                               // rows in flight per thread
+    for (; r + (U - 1) * (int)gridDim.y < rows; r += U * gridDim.y) {
+        Raw<T, V> in[U];
 #pragma unroll
-            for (int i = 0; i < 3; ++i) out[i * plane + at] = t[i];
+        for (int i = 0; i < U; ++i) in[i] = load_raw<T, V>(x + (size_t)(r + i * gridDim.y) * ld + c);
+#pragma unroll
+        for (int i = 0; i < U; ++i) {
+            float e[V];
+            unpack<T, V>(in[i], e);
+            store_operand<T, V>(out + (size_t)(r + i * gridDim.y) * cols8 + c, plane, e);
         }
+    }
+    for (; r < rows; r += gridDim.y) {
+        float e[V];
+        load_vec<T, V>(x + (size_t)r * ld + c, e);
+        store_operand<T, V>(out + (size_t)r * cols8 + c, plane, e);
     }
 }
 
 // dpre = dy act'(pre) as an operand (null: dy is used as it is), and each slice of rows' column sums.
-// The rounding of dpre to bf16 is the operand format's; the bias sums take it before that.
-template <typename T>
+// The rounding of dpre to bf16 is the operand format's; the bias sums take it before that. A CTA takes
+// 64 V columns and four rows at a time.
+template <typename T, int V>
 __global__ void __launch_bounds__(256) linear_dpre_kernel(const T *dy, const T *pre, __nv_bfloat16 *dpre, float *part, int M,
                                                           int N, int N8, int act) {
-    const int n = blockIdx.x * 256 + threadIdx.x;
-    if (n >= N) return;
-    float s = 0.f;
-    const size_t plane = (size_t)M * N8;
-    for (size_t m = blockIdx.y; m < (size_t)M; m += gridDim.y) {
-        float d = to_f32(dy[m * N + n]);
-        if (act != kActNone) d *= dact_rt(act, to_f32(pre[m * N + n]));
-        if (dpre != nullptr) {
-            if constexpr (sizeof(T) == 2) {
-                dpre[m * N8 + n] = __float2bfloat16_rn(d);
-            } else {
-                __nv_bfloat16 t[3];
-                split3(d, t);
+    __shared__ float sums[4][64 * V];
+    const int cg = threadIdx.x & 63, rl = threadIdx.x >> 6, n = (blockIdx.x * 64 + cg) * V;
+    float s[V] = {};
+    if (n < N) {
+        const size_t plane = (size_t)M * N8;
+        const int step = 4 * gridDim.y;
+        Raw<T, V> next_d = Raw<T, V>(), next_p = Raw<T, V>();
+        auto fetch = [&](int m) {
+            if (m >= M) return;
+            next_d = load_raw<T, V>(dy + (size_t)m * N + n);
+            if (act != kActNone) next_p = load_raw<T, V>(pre + (size_t)m * N + n);
+        };
+        int m = blockIdx.y * 4 + rl;
+        fetch(m);
+        for (; m < M; m += step) {
+            float d[V], q[V];
+            unpack<T, V>(next_d, d);
+            unpack<T, V>(next_p, q);
+            fetch(m + step);
+            if (act == kActSilu) {
 #pragma unroll
-                for (int i = 0; i < 3; ++i) dpre[i * plane + m * N8 + n] = t[i];
+                for (int v = 0; v < V; ++v) d[v] *= dsilu_hw(q[v]);
+            } else if (act == kActGelu) {
+#pragma unroll
+                for (int v = 0; v < V; ++v) d[v] *= dgelu_f(q[v]);
             }
+            if (dpre != nullptr) store_operand<T, V>(dpre + (size_t)m * N8 + n, plane, d);
+#pragma unroll
+            for (int v = 0; v < V; ++v) s[v] += d[v];
         }
-        s += d;
     }
-    part[(size_t)blockIdx.y * N + n] = s;
+#pragma unroll
+    for (int v = 0; v < V; ++v) sums[rl][cg * V + v] = s[v];
+    __syncthreads();
+    for (int i = threadIdx.x; i < 64 * V; i += 256) {
+        const int c = blockIdx.x * 64 * V + i;
+        if (c < N) part[(size_t)blockIdx.y * N + c] = (sums[0][i] + sums[1][i]) + (sums[2][i] + sums[3][i]);
+    }
 }
 
 template <typename T>
 __global__ void __launch_bounds__(256) linear_dbias_kernel(const float *part, T *dbias, int slices, int N) {
-    const int n = blockIdx.x * 256 + threadIdx.x;
-    if (n >= N) return;
-    float s = 0.f;
-    for (int k = 0; k < slices; ++k) s += part[(size_t)k * N + n];
-    dbias[n] = from_f32<T>(s);
+    const int n = blockIdx.x * 32 + threadIdx.x;
+    const float s = slice_sum(part, slices, N);
+    if (threadIdx.x < 32 && n < N) dbias[n] = from_f32<T>(s);
 }
 
 namespace {
@@ -461,12 +567,22 @@ struct Operand {
 int pack(const Operand &in, Operand *out, char *ws, int dtype, cudaStream_t s) {
     *out = in;
     if (dtype != 0 && in.ld % 8 == 0 && (uintptr_t)in.p % 16 == 0) return 0;
-    const dim3 grid((in.cols + 255) / 256, in.rows < 4096 ? in.rows : 4096);
     __nv_bfloat16 *to = reinterpret_cast<__nv_bfloat16 *>(ws);
     const int cols8 = up8(in.cols);
     timing_mark("linear_pack", 0, s);
-    if (dtype == 0) linear_pack_kernel<float><<<grid, 256, 0, s>>>(static_cast<const float *>(in.p), in.ld, to, in.rows, in.cols, cols8);
-    else linear_pack_kernel<__nv_bfloat16><<<grid, 256, 0, s>>>(static_cast<const __nv_bfloat16 *>(in.p), in.ld, to, in.rows, in.cols, cols8);
+    auto launch = [&](auto kernel, auto *src, int V) {
+        const int cols = (in.cols / V + 255) / 256, most = (kPairs * 2 * 16 + cols - 1) / cols;
+        kernel<<<dim3(cols, in.rows < most ? in.rows : most), 256, 0, s>>>(src, in.ld, to, in.rows, in.cols, cols8);
+    };
+    if (dtype == 0) {
+        const float *src = static_cast<const float *>(in.p);
+        if (in.cols % 4 == 0 && in.ld % 4 == 0 && (uintptr_t)in.p % 16 == 0) launch(linear_pack_kernel<float, 4>, src, 4);
+        else launch(linear_pack_kernel<float, 1>, src, 1);
+    } else {
+        const __nv_bfloat16 *src = static_cast<const __nv_bfloat16 *>(in.p);
+        if (in.cols % 2 == 0 && in.ld % 2 == 0 && (uintptr_t)in.p % 4 == 0) launch(linear_pack_kernel<__nv_bfloat16, 2>, src, 2);
+        else launch(linear_pack_kernel<__nv_bfloat16, 1>, src, 1);
+    }
     timing_mark("linear_pack", 1, s);
     out->p = to;
     out->ld = cols8;
@@ -487,17 +603,18 @@ int gemm(const char *name, const Operand &A, const Operand &B, int M, int N, int
     p.M = M; p.N = N;
     p.kblocks = (K + kBK - 1) / kBK;
     const int planes = sizeof(T) == 4 ? 3 : 1;
-    p.terms = sizeof(T) == 4 ? 6 : 1;
+    p.run = sizeof(T) == 4 ? kRun : p.kblocks;
+    constexpr int TN = kTileN<T>;
     // a product with an odd number of columns left gets narrower tiles at the end
     p.mt = (M + 2 * kBM - 1) / (2 * kBM);
-    p.nt = N / kMaxBN;
+    p.nt = N / TN;
     const int unit = B_MN && B.cols % 64 == 0 ? 128 : 32;   // each CTA's half starts on a 64-column block
-    p.edge = (N % kMaxBN + unit - 1) / unit * unit;
+    p.edge = (N % TN + unit - 1) / unit * unit;
     p.panel = p.nt < 8 ? (p.nt > 0 ? p.nt : 1) : 8;
     const long long tiles = (long long)p.mt * p.nt;
     const int last = (int)(tiles % kPairs);            // tiles of an incomplete last round
     if (tiles > 0x3fffffffLL) return GDN_ERR_UNSUPPORTED_SHAPE;
-    p.halves = last > 0 && last <= kPairs / 2 ? 2 * last : 0;
+    p.halves = TN == kMaxBN && last > 0 && last <= kPairs / 2 ? 2 * last : 0;
     p.whole = (int)tiles - p.halves / 2;
     p.items = p.whole + p.halves + (p.edge > 0 ? p.mt : 0);
     const int V = 16 / (int)sizeof(T);
@@ -544,16 +661,20 @@ int bwd_any(const LinearParams &p, int dtype, cudaStream_t s) {
     int rc;
     if (own_dpre || p.dbias != nullptr) {
         __nv_bfloat16 *to = own_dpre ? reinterpret_cast<__nv_bfloat16 *>(ws) : nullptr;
-        const int slices = p.M < kBiasSlices ? p.M : kBiasSlices;
+        constexpr int V = 16 / (int)sizeof(T);
+        const T *dy = static_cast<const T *>(p.dy), *pre = static_cast<const T *>(p.pre_in);
+        const int slices = (p.M + 3) / 4 < kBiasSlices ? (p.M + 3) / 4 : kBiasSlices;
         timing_mark("linear_dpre", 0, s);
-        linear_dpre_kernel<T><<<dim3((p.N + 255) / 256, slices), 256, 0, s>>>(
-            static_cast<const T *>(p.dy), static_cast<const T *>(p.pre_in), to, part, p.M, p.N, up8(p.N), p.act);
+        if (p.N % V == 0)
+            linear_dpre_kernel<T, V><<<dim3((p.N + 64 * V - 1) / (64 * V), slices), 256, 0, s>>>(dy, pre, to, part, p.M, p.N, up8(p.N), p.act);
+        else
+            linear_dpre_kernel<T, 1><<<dim3((p.N + 63) / 64, slices), 256, 0, s>>>(dy, pre, to, part, p.M, p.N, up8(p.N), p.act);
         timing_mark("linear_dpre", 1, s);
         if ((rc = api_cuda_status(cudaGetLastError())) != 0) return rc;
         if (to != nullptr) d = {to, up8(p.N), p.M, p.N};
         if (p.dbias != nullptr) {
             timing_mark("linear_dbias", 0, s);
-            linear_dbias_kernel<T><<<(p.N + 255) / 256, 256, 0, s>>>(part, static_cast<T *>(p.dbias), slices, p.N);
+            linear_dbias_kernel<T><<<(p.N + 31) / 32, 256, 0, s>>>(part, static_cast<T *>(p.dbias), slices, p.N);
             timing_mark("linear_dbias", 1, s);
             if ((rc = api_cuda_status(cudaGetLastError())) != 0) return rc;
         }

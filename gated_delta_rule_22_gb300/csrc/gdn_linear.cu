@@ -443,6 +443,226 @@ gemm_kernel(const __grid_constant__ CUtensorMap tmA, const __grid_constant__ CUt
     if (warp == 1) pair_tmem_dealloc(tmem, 512);
 }
 
+// ---- few rows (decode): a stream over the weights
+//
+// With up to 64 rows the product is bound by the bytes of W. It is computed the other way round, D[n][m]
+// = W x^T: 128 rows of W are the tensor cores' M, the rows of x (padded to 16, 32 or 64) their N. The
+// CTAs of a cluster share one tile of W's rows, each with its part of K, so that every SM streams; their
+// partial sums meet in shared memory (cluster rank order) and each CTA finishes its share of the rows.
+constexpr int kTokThreads = 64 + 128;
+
+template <int MP>
+struct TokGeo {
+    static constexpr int kStage = 2 * kBox + MP * kBK * 2;
+    static constexpr int kDepth = MP == 16 ? 6 : MP == 32 ? 5 : 4;      // two CTAs' stages fit one SM
+    static constexpr size_t kSmem = 1024 + (size_t)kDepth * kStage + 256;
+    static_assert(128 * MP * 4 <= kDepth * kStage, "the partial sums take the stages' place");
+};
+
+struct TokenParams {
+    const void *bias, *res;
+    void *out, *pre;
+    int *status;
+    long long ldres;
+    int M, N, kblocks, per, act;     // per: K blocks of one CTA
+};
+
+__device__ __forceinline__ void tma_load_3d(void *dst, const CUtensorMap *map, uint64_t *bar, int c0, int c1, int c2) {
+    asm volatile(
+        "cp.async.bulk.tensor.3d.shared::cluster.global.mbarrier::complete_tx::bytes [%0], [%1, {%2, %3, %4}], [%5];" ::"r"(
+            smem_addr(dst)),
+        "l"(reinterpret_cast<uint64_t>(map)), "r"(c0), "r"(c1), "r"(c2), "r"(smem_addr(bar))
+        : "memory");
+}
+
+template <int MP>
+__global__ void __launch_bounds__(kTokThreads) linear_token_kernel(const __grid_constant__ CUtensorMap tmW,
+                                                                   const __grid_constant__ CUtensorMap tmX, const TokenParams p) {
+    using T = __nv_bfloat16;
+    using G = TokGeo<MP>;
+    extern __shared__ unsigned char smem_raw[];
+    unsigned char *smem = reinterpret_cast<unsigned char *>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~(uintptr_t)1023);
+    float *partial = reinterpret_cast<float *>(smem);               // [MP][128], over the stages
+    uint64_t *bars = reinterpret_cast<uint64_t *>(smem + G::kDepth * G::kStage);
+    uint64_t *full = bars, *empty = bars + G::kDepth, *done = empty + G::kDepth;
+    uint32_t *tmem_slot = reinterpret_cast<uint32_t *>(done + 1);
+    const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+    const int splits = gridDim.x, rank = blockIdx.x, n0 = blockIdx.y * 128;
+    const int k_first = rank * p.per, steps = max(min(p.per, p.kblocks - k_first), 0);
+    if (threadIdx.x == 0) {
+        for (int i = 0; i < G::kDepth; ++i) {
+            mbar_init(full + i, 1);
+            mbar_init(empty + i, 1);
+        }
+        mbar_init(done, 1);
+        fence_mbar_init();
+        tma_prefetch_map(&tmW);
+        tma_prefetch_map(&tmX);
+    }
+    if (warp == 1) tmem_alloc(tmem_slot, MP < 32 ? 32 : MP);
+    tc_fence_before();
+    __syncthreads();
+    tc_fence_after();
+    const uint32_t tmem = *tmem_slot;
+    if (warp == 0) {
+        if (lane == 0) {
+            bool ok = true;
+            int s = 0;
+            for (; s < steps; ++s) {
+                const int st = s % G::kDepth;
+                if (!(ok = mbar_wait(empty + st, (s / G::kDepth & 1) ^ 1))) break;
+                unsigned char *w = smem + st * G::kStage;
+                mbar_expect_tx(full + st, G::kStage);
+                tma_load_3d(w, &tmW, full + st, (k_first + s) * kBK, n0, 0);
+                tma_load_3d(w + 2 * kBox, &tmX, full + st, (k_first + s) * kBK, 0, 0);
+            }
+            if (!ok) {                            // what was started lands before the CTA ends
+                report_status(p.status, kStatusTimeout);
+                for (int i = s < G::kDepth ? 0 : s - G::kDepth; i < s; ++i) mbar_wait(full + i % G::kDepth, i / G::kDepth & 1);
+            }
+        }
+        __syncwarp();
+    } else if (warp == 1) {
+        const uint32_t lead = elect_one_sync();
+        const uint32_t idesc = umma_idesc(1, 128, MP);
+        bool ok = true;
+        for (int s = 0; s < steps; ++s) {
+            const int st = s % G::kDepth;
+            if (!(ok = mbar_wait(full + st, s / G::kDepth & 1))) break;
+            tc_fence_after();
+            const uint32_t base = smem_addr(smem) + st * G::kStage;
+            uint64_t a = sw128_desc(base, false), b = sw128_desc(base + 2 * kBox, false);
+#pragma unroll
+            for (int k = 0; k < kBK / 16; ++k) {
+                umma_bf16_w(tmem, a, b, idesc, s > 0 || k > 0, lead);
+                a += 32 >> 4;
+                b += 32 >> 4;
+            }
+            umma_commit_w(empty + st, lead);
+        }
+        if (ok) umma_commit_w(done, lead);
+        else if (lane == 0) report_status(p.status, kStatusTimeout);
+    } else {
+        const int quarter = warp & 3;
+        bool ok = true;
+        if (steps > 0 && !(ok = mbar_wait(done, 0)) && lane == 0) report_status(p.status, kStatusTimeout);
+        tc_fence_after();
+        // every product has read its stage: the partial sums go there, [m][row of W]
+#pragma unroll
+        for (int c = 0; c < MP; c += 16) {
+            float2 v[8];
+            if (steps > 0 && ok) {
+                tmem_ld16(tmem + ((uint32_t)(32 * quarter) << 16) + c, v);
+                tmem_wait_ld();
+            } else {
+#pragma unroll
+                for (int j = 0; j < 8; ++j) v[j] = make_float2(0.f, 0.f);
+            }
+#pragma unroll
+            for (int j = 0; j < 8; ++j) {
+                partial[(c + 2 * j) * 128 + 32 * quarter + lane] = v[j].x;
+                partial[(c + 2 * j + 1) * 128 + 32 * quarter + lane] = v[j].y;
+            }
+        }
+        tc_fence_before();
+    }
+    __syncthreads();
+    cluster_sync();
+    const int rows = 128 / splits, mine = rank * rows;
+    const T *bias = static_cast<const T *>(p.bias), *res = static_cast<const T *>(p.res);
+    for (int e = threadIdx.x; e < rows * p.M; e += kTokThreads) {
+        const int r = mine + e % rows, m = e / rows, n = n0 + r;
+        if (n >= p.N) continue;
+        const uint32_t at = smem_addr(partial + m * 128 + r);
+        float v = 0.f;
+        for (int k = 0; k < splits; ++k) {
+            uint32_t remote;
+            float x;
+            asm volatile("mapa.shared::cluster.u32 %0, %1, %2;" : "=r"(remote) : "r"(at), "r"(k));
+            asm volatile("ld.shared::cluster.f32 %0, [%1];" : "=f"(x) : "r"(remote));
+            v += x;
+        }
+        if (bias != nullptr) v += to_f32(bias[n]);
+        const size_t o = (size_t)m * p.N + n;
+        if (p.pre != nullptr) static_cast<T *>(p.pre)[o] = from_f32<T>(v);
+        v = act_rt(p.act, v);
+        if (res != nullptr) v = __fadd_rn(v, to_f32(res[(size_t)m * p.ldres + n]));
+        static_cast<T *>(p.out)[o] = from_f32<T>(v);
+    }
+    cluster_sync();                               // nobody leaves while its partial sums are read
+    if (warp == 1) {
+        tc_fence_after();
+        tmem_dealloc(tmem, MP < 32 ? 32 : MP);
+    }
+}
+
+// Few rows of float32, or of bf16 that TMA cannot read in place: the same stream on the CUDA cores. A
+// warp takes four rows of W and a slice of K, with MT rows of x at a time; `slices` warps of a CTA share
+// four rows of W.
+template <typename T, int V, int MT>
+__global__ void __launch_bounds__(256) linear_stream_kernel(const T *x, long long ldx, const T *W, long long ldw, const T *bias,
+                                                            const T *res, long long ldres, T *out, T *pre, int M, int N, int K,
+                                                            int act, int slices) {
+    __shared__ float sums[8][4][MT];
+    const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+    const int group = warp / slices, slice = warp % slices;
+    const int n0 = (blockIdx.x * (8 / slices) + group) * 4, m0 = blockIdx.y * MT;
+    const int steps = (K + 32 * V - 1) / (32 * V), per = (steps + slices - 1) / slices;
+    float acc[4][MT];
+#pragma unroll
+    for (int r = 0; r < 4; ++r)
+#pragma unroll
+        for (int m = 0; m < MT; ++m) acc[r][m] = 0.f;
+    Raw<T, V> next[4];
+    auto fetch = [&](int s) {
+        const int k = (s * 32 + lane) * V;
+#pragma unroll
+        for (int r = 0; r < 4; ++r) {
+            next[r] = Raw<T, V>();
+            if (k < K && n0 + r < N) next[r] = load_raw<T, V>(W + (size_t)(n0 + r) * ldw + k);
+        }
+    };
+    const int first = slice * per, last = min(first + per, steps);
+    if (first < last) fetch(first);
+    for (int s = first; s < last; ++s) {
+        float w[4][V];
+#pragma unroll
+        for (int r = 0; r < 4; ++r) unpack<T, V>(next[r], w[r]);
+        if (s + 1 < last) fetch(s + 1);
+        const int k = (s * 32 + lane) * V;
+        if (k >= K) continue;
+#pragma unroll
+        for (int m = 0; m < MT; ++m) {                 // rows past the last repeat it: no branch in the stream
+            float e[V];
+            load_vec<T, V>(x + (size_t)min(m0 + m, M - 1) * ldx + k, e);
+#pragma unroll
+            for (int r = 0; r < 4; ++r)
+#pragma unroll
+                for (int v = 0; v < V; ++v) acc[r][m] = fmaf(w[r][v], e[v], acc[r][m]);
+        }
+    }
+#pragma unroll
+    for (int r = 0; r < 4; ++r)
+#pragma unroll
+        for (int m = 0; m < MT; ++m) {
+            const float t = warp_sum(acc[r][m]);
+            if (lane == 0) sums[warp][r][m] = t;
+        }
+    __syncthreads();
+    for (int e = threadIdx.x; e < 8 / slices * 4 * MT; e += 256) {
+        const int g = e / (4 * MT), r = e % 4, m = e / 4 % MT, n = (blockIdx.x * (8 / slices) + g) * 4 + r;
+        if (n >= N || m0 + m >= M) continue;
+        float v = 0.f;
+        for (int k = 0; k < slices; ++k) v += sums[g * slices + k][r][m];
+        if (bias != nullptr) v += to_f32(bias[n]);
+        const size_t o = (size_t)(m0 + m) * N + n;
+        if (pre != nullptr) pre[o] = from_f32<T>(v);
+        v = act_rt(act, v);
+        if (res != nullptr) v = __fadd_rn(v, to_f32(res[(size_t)(m0 + m) * ldres + n]));
+        out[o] = from_f32<T>(v);
+    }
+}
+
 // x as bf16 operand rows of `cols8` elements: a copy (bf16) or three terms (float32), planes of
 // [rows][cols8]. What lies past the `cols` columns is never read.
 __device__ __forceinline__ void split3(float x, __nv_bfloat16 (&t)[3]) {
@@ -640,8 +860,76 @@ int gemm(const char *name, const Operand &A, const Operand &B, int M, int N, int
     return api_cuda_status(cudaGetLastError());
 }
 
+constexpr int kStreamRows = 32, kNotTaken = 1;
+
+template <int MP>
+int token_launch(const LinearParams &p, cudaStream_t s) {
+    using G = TokGeo<MP>;
+    TokenParams t = {p.bias, p.res, p.y, p.pre, p.status, p.ldres, p.M, p.N, (p.K + kBK - 1) / kBK, 0, p.act};
+    const int tiles = (p.N + 127) / 128;
+    int splits = 8;                                    // at most two CTAs per SM, at least two K blocks each
+    while (splits > 1 && (tiles * splits > 4 * kPairs || t.kblocks < 2 * splits)) splits /= 2;
+    t.per = (t.kblocks + splits - 1) / splits;
+    CUtensorMap w, x;
+    int rc;
+    if ((rc = api_planes_map(&w, p.W, p.K, p.N, 1, p.ldw, 128, 0)) != 0) return rc;
+    if ((rc = api_planes_map(&x, p.x, p.K, p.M, 1, p.ldx, MP, 0)) != 0) return rc;
+    cudaError_t e = cudaFuncSetAttribute(linear_token_kernel<MP>, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)G::kSmem);
+    if (e != cudaSuccess) return api_cuda_status(e);
+    cudaLaunchConfig_t cfg = {};
+    cfg.gridDim = dim3(splits, tiles);
+    cfg.blockDim = kTokThreads;
+    cfg.dynamicSmemBytes = G::kSmem;
+    cfg.stream = s;
+    cudaLaunchAttribute attr[1];
+    attr[0].id = cudaLaunchAttributeClusterDimension;
+    attr[0].val.clusterDim.x = splits;
+    attr[0].val.clusterDim.y = attr[0].val.clusterDim.z = 1;
+    cfg.attrs = attr;
+    cfg.numAttrs = 1;
+    timing_mark("linear_token", 0, s);
+    e = cudaLaunchKernelEx(&cfg, linear_token_kernel<MP>, w, x, t);
+    timing_mark("linear_token", 1, s);
+    return api_cuda_status(e);
+}
+
+template <typename T, int V, int MT>
+int stream_launch(const LinearParams &p, cudaStream_t s) {
+    const int groups = (p.N + 3) / 4, steps = (p.K + 32 * V - 1) / (32 * V);
+    int slices = 1;                                    // warps per four rows: until there are 16 warps per SM
+    while (slices < 8 && groups * slices < 2 * kPairs * 16 && steps >= 4 * slices) slices *= 2;
+    const int per = 8 / slices;
+    timing_mark("linear_stream", 0, s);
+    linear_stream_kernel<T, V, MT><<<dim3((groups + per - 1) / per, (p.M + MT - 1) / MT), 256, 0, s>>>(
+        static_cast<const T *>(p.x), p.ldx, static_cast<const T *>(p.W), p.ldw, static_cast<const T *>(p.bias),
+        static_cast<const T *>(p.res), p.ldres, static_cast<T *>(p.y), static_cast<T *>(p.pre), p.M, p.N, p.K, p.act, slices);
+    timing_mark("linear_stream", 1, s);
+    return api_cuda_status(cudaGetLastError());
+}
+template <typename T, int V>
+int stream_rows(const LinearParams &p, cudaStream_t s) {
+    return p.M <= 2 ? stream_launch<T, V, 2>(p, s) : p.M <= 4 ? stream_launch<T, V, 4>(p, s)
+         : p.M <= 8 ? stream_launch<T, V, 8>(p, s) : stream_launch<T, V, 16>(p, s);
+}
+
+// The decode forms: bf16 rows that TMA reads in place, up to 64 of them, on the tensor cores; else, up
+// to 32 (beyond that packing W for the tensor cores costs less than streaming it more than twice), on
+// the CUDA cores.
+template <typename T>
+int token_any(const LinearParams &p, cudaStream_t s) {
+    constexpr int V = 16 / sizeof(T);
+    const uintptr_t at = (uintptr_t)p.x | (uintptr_t)p.W;
+    if (sizeof(T) == 2 && p.M <= 64 && p.ldx % 8 == 0 && p.ldw % 8 == 0 && at % 16 == 0)
+        return p.M <= 16 ? token_launch<16>(p, s) : p.M <= 32 ? token_launch<32>(p, s) : token_launch<64>(p, s);
+    if (p.M > kStreamRows) return kNotTaken;
+    const bool vec = p.K % V == 0 && p.ldx % V == 0 && p.ldw % V == 0 && at % 16 == 0;
+    return vec ? stream_rows<T, V>(p, s) : stream_rows<T, 1>(p, s);
+}
+
 template <typename T>
 int fwd_any(const LinearParams &p, int dtype, cudaStream_t s) {
+    const int few = token_any<T>(p, s);
+    if (few != kNotTaken) return few;
     Operand x = {p.x, p.ldx, p.M, p.K}, w = {p.W, p.ldw, p.N, p.K};
     char *ws = p.ws;
     int rc;
@@ -697,6 +985,7 @@ int bwd_any(const LinearParams &p, int dtype, cudaStream_t s) {
 }  // namespace
 
 size_t linear_fwd_workspace(const LinearParams &p, int dtype) {
+    if (p.M <= kStreamRows) return 0;
     return pack_bytes(p.M, p.K, p.ldx, dtype) + pack_bytes(p.N, p.K, p.ldw, dtype);
 }
 

@@ -12,98 +12,178 @@
 namespace gdn {
 
 // LITE: the segment's end state from a zero start and its sum of d, nothing else (first pass over a
-// split sequence). The next tile's inputs are loaded while a tile is walked.
+// split sequence).
+//
+// Eight warps hold the states and do nothing but the recurrence; four more stage the tiles (loads a
+// tile ahead, softplus) and finish the outputs. With as few channels as a layer has there are about
+// two state warps per scheduler, which then have the helpers' work to hide their latencies, and no
+// phases of their own that leave the recurrence idle. Two tiles are in flight; named barriers full[2]
+// (staged) and done[2] (walked) hand them over.
 template <int LPC, typename T, bool VEC, bool LITE>
-__global__ void __launch_bounds__(kScanThreads, 3) scan_fwd_kernel(ScanParams p) {
+__global__ void __launch_bounds__(kScanThreads + kScanHelpers, 2) scan_fwd_kernel(ScanParams p) {
     using G = ScanGeo<LPC>;
-    constexpr int CH = G::CH, NP = G::NP, V = G::V, KB = G::KB, TT = kScanTile;
-    __shared__ __align__(16) float2 sdx[TT][CH];   // d, d u
-    __shared__ __align__(16) float sB[TT][NP], sC[TT][NP];
-    __shared__ float score[TT][G::SP];
+    constexpr int CH = G::CH, NP = G::NP, V = G::V, TT = kScanTile, ALL = kScanThreads + kScanHelpers;
+    constexpr int kFull = 1, kDone = 3;
+    __shared__ __align__(16) float2 sdx[2][TT][CH];   // d, d u
+    __shared__ __align__(16) float sB[2][TT][NP], sC[2][TT][NP];
+    __shared__ float score[2][TT][G::SP];
+    __shared__ __align__(16) T su[2][TT][CH], sz[2][TT][CH];
     const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
     const ScanPlace q = scan_place<LPC>(p);
     if (q.first >= q.last) return;
     const int L = row_length(p.lens, q.b, p.T);
-    // this thread's staged elements: step ts of a tile, V channels from cv; and its states: channel
-    // ch, states n0 .. n0 + 3
-    const int ts = tid >> 4, cv = (tid & 15) * V, nv = q.nc - cv;
+    if (tid >= kScanThreads) {
+        constexpr int KB = NP * TT / kScanHelpers, PASS = TT * CH / V / kScanHelpers;
+        // staged elements: steps ts and ts + 8 of a tile, V channels from cv
+        const int h = tid - kScanThreads, ts = h >> 4, cv = (h & 15) * V, nv = q.nc - cv;
+        const T *u = static_cast<const T *>(p.u) + (size_t)q.b * p.T * p.ldu + q.c0 + cv;
+        const T *dt = static_cast<const T *>(p.dt) + (size_t)q.b * p.T * p.lddt + q.c0 + cv;
+        const T *z = static_cast<const T *>(p.z) + (size_t)q.b * p.T * p.ldz + q.c0 + cv;
+        T *y = static_cast<T *>(p.y) + (size_t)q.b * p.T * p.Cn + q.c0 + cv;
+        const T *Bm = static_cast<const T *>(p.B) + (size_t)q.b * p.T * p.ldB + q.g * p.N;
+        const T *Cm = static_cast<const T *>(p.C) + (size_t)q.b * p.T * p.ldC + q.g * p.N;
+        Staged<T, V, VEC> ru[PASS], rd[PASS], rz[PASS];
+        T rB[KB], rC[KB];
+        auto fetch = [&](int tile) {
+#pragma unroll
+            for (int i = 0; i < PASS; ++i) {
+                const int t = tile * TT + ts + 8 * i, n = t < L ? nv : 0;
+                ru[i].load(u + (size_t)t * p.ldu, n);
+                rd[i].load(dt + (size_t)t * p.lddt, n);
+                if (!LITE && p.z != nullptr) rz[i].load(z + (size_t)t * p.ldz, n);
+            }
+#pragma unroll
+            for (int k = 0; k < KB; ++k) {
+                const int e = h + kScanHelpers * k, tb = tile * TT + e / NP, n1 = e % NP;
+                const bool ok = tb < L && n1 < p.N;
+                rB[k] = rC[k] = from_f32<T>(0.f);
+                if (ok) rB[k] = Bm[(size_t)tb * p.ldB + n1];
+                if (!LITE && ok) rC[k] = Cm[(size_t)tb * p.ldC + n1];
+            }
+        };
+        float D[V], bias[V], sum_d[V];
+#pragma unroll
+        for (int v = 0; v < V; ++v) {
+            D[v] = p.D != nullptr && v < nv ? p.D[q.c0 + cv + v] : 0.f;
+            bias[v] = p.dt_bias != nullptr && v < nv ? p.dt_bias[q.c0 + cv + v] : 0.f;
+            sum_d[v] = 0.f;
+        }
+        auto stage = [&](int tile) {
+            const int buf = tile & 1;
+#pragma unroll
+            for (int i = 0; i < PASS; ++i) {
+                const int st = ts + 8 * i, t = tile * TT + st;
+                float uu[V], dd[V];
+                ru[i].get(uu);
+                rd[i].get(dd);
+                if constexpr (V == 1) {
+                    dd[0] = softplus_full(dd[0] + bias[0]);
+                } else {
+#pragma unroll
+                    for (int v = 0; v < V; v += 2) {
+                        const float2 d = softplus2_full(make_float2(dd[v] + bias[v], dd[v + 1] + bias[v + 1]));
+                        dd[v] = d.x;
+                        dd[v + 1] = d.y;
+                    }
+                }
+                if (t >= L)
+#pragma unroll
+                    for (int v = 0; v < V; ++v) dd[v] = 0.f;
+                if constexpr (V == 1) {
+                    sdx[buf][st][cv] = make_float2(dd[0], dd[0] * uu[0]);
+                } else {
+#pragma unroll
+                    for (int v = 0; v < V; v += 2)
+                        *reinterpret_cast<float4 *>(&sdx[buf][st][cv + v]) = make_float4(dd[v], dd[v] * uu[v], dd[v + 1], dd[v + 1] * uu[v + 1]);
+                }
+                if (LITE) {
+#pragma unroll
+                    for (int v = 0; v < V; ++v) sum_d[v] += dd[v];
+                } else {
+                    ru[i].keep(&su[buf][st][cv]);
+                    if (p.z != nullptr) rz[i].keep(&sz[buf][st][cv]);
+                }
+            }
+#pragma unroll
+            for (int k = 0; k < KB; ++k) {
+                const int e = h + kScanHelpers * k;
+                sB[buf][e / NP][e % NP] = to_f32(rB[k]);
+                if (!LITE) sC[buf][e / NP][e % NP] = to_f32(rC[k]);
+            }
+            if (tile + 1 < q.last) fetch(tile + 1);
+            named_bar_arrive(kFull + buf, ALL);
+        };
+        fetch(q.first);
+        stage(q.first);
+        if (q.first + 1 < q.last) stage(q.first + 1);
+        for (int tile = q.first; tile < q.last; ++tile) {
+            const int buf = tile & 1;
+            named_bar_sync(kDone + buf, ALL);
+            if (!LITE) {
+#pragma unroll
+                for (int i = 0; i < PASS; ++i) {
+                    const int st = ts + 8 * i, t = tile * TT + st;
+                    if (t >= p.T) continue;
+                    float o[V], uu[V], zz[V];
+                    load_vec<T, V>(&su[buf][st][cv], uu);
+#pragma unroll
+                    for (int v = 0; v < V; ++v) o[v] = fmaf(D[v], uu[v], score[buf][st][cv + v]);
+                    if (p.z != nullptr) {
+                        load_vec<T, V>(&sz[buf][st][cv], zz);
+#pragma unroll
+                        for (int v = 0; v < V; ++v) o[v] *= silu_hw(zz[v]);
+                    }
+                    if (t >= L)
+#pragma unroll
+                        for (int v = 0; v < V; ++v) o[v] = 0.f;
+                    store_channels<T, V>(y + (size_t)t * p.Cn, nv, VEC, o);
+                }
+            }
+            if (tile + 2 < q.last) stage(tile + 2);
+        }
+        if (LITE) {
+            // the sum of d over the segment: over a thread's tiles, then over its eight steps of a tile
+#pragma unroll
+            for (int v = 0; v < V; ++v) score[0][ts][cv + v] = sum_d[v];
+            named_bar_sync(kDone + 2, kScanHelpers);
+            for (int cc = h; cc < q.nc; cc += kScanHelpers) {
+                float a = 0.f;
+                for (int i = 0; i < 8; ++i) a += score[0][i][cc];
+                p.seg_sum[((size_t)q.seg * p.Bn + q.b) * p.Cn + q.c0 + cc] = a;
+            }
+        }
+        return;
+    }
+    // this lane's states: channel ch, states n0 .. n0 + 3
     const int ch = warp * G::CPW + lane / LPC, n0 = 4 * (lane % LPC);
     const bool live = ch < q.nc;
     const int c = q.c0 + (live ? ch : 0);
-    const T *u = static_cast<const T *>(p.u) + (size_t)q.b * p.T * p.ldu + q.c0 + cv;
-    const T *dt = static_cast<const T *>(p.dt) + (size_t)q.b * p.T * p.lddt + q.c0 + cv;
-    const T *z = static_cast<const T *>(p.z) + (size_t)q.b * p.T * p.ldz + q.c0 + cv;
-    const T *Bm = static_cast<const T *>(p.B) + (size_t)q.b * p.T * p.ldB + q.g * p.N;
-    const T *Cm = static_cast<const T *>(p.C) + (size_t)q.b * p.T * p.ldC + q.g * p.N;
-    Staged<T, V, VEC> ru, rd, rz;
-    T rB[KB], rC[KB];
-    auto fetch = [&](int tile) {
-        const int t = tile * TT + ts, n = t < L ? nv : 0;
-        ru.load(u + (size_t)t * p.ldu, n);
-        rd.load(dt + (size_t)t * p.lddt, n);
-        if (!LITE && p.z != nullptr) rz.load(z + (size_t)t * p.ldz, n);
+    float2 A2[2], h[2];
+    {
+        float e[4];
 #pragma unroll
-        for (int k = 0; k < KB; ++k) {
-            const int e = tid + kScanThreads * k, tb = tile * TT + e / NP, n1 = e % NP;
-            const bool ok = tb < L && n1 < p.N;
-            rB[k] = rC[k] = from_f32<T>(0.f);
-            if (ok) rB[k] = Bm[(size_t)tb * p.ldB + n1];
-            if (!LITE && ok) rC[k] = Cm[(size_t)tb * p.ldC + n1];
-        }
-    };
-    fetch(q.first);
-    float2 A2[2], h[2] = {make_float2(0.f, 0.f), make_float2(0.f, 0.f)};
-    float al[4], D[V], bias[V], sum_d[V];
-#pragma unroll
-    for (int k = 0; k < 4; ++k) al[k] = n0 + k < p.N ? -expf(p.A_log[(size_t)c * p.N + n0 + k]) * kLog2e : 0.f;
-    A2[0] = make_float2(al[0], al[1]);
-    A2[1] = make_float2(al[2], al[3]);
-#pragma unroll
-    for (int v = 0; v < V; ++v) {
-        D[v] = p.D != nullptr && v < nv ? p.D[q.c0 + cv + v] : 0.f;
-        bias[v] = p.dt_bias != nullptr && v < nv ? p.dt_bias[q.c0 + cv + v] : 0.f;
-        sum_d[v] = 0.f;
+        for (int k = 0; k < 4; ++k) e[k] = n0 + k < p.N ? -expf(p.A_log[(size_t)c * p.N + n0 + k]) * kLog2e : 0.f;
+        A2[0] = make_float2(e[0], e[1]);
+        A2[1] = make_float2(e[2], e[3]);
     }
     const size_t state_row = ((size_t)q.b * p.Cn + c) * p.N;
-    float hs[4] = {0.f, 0.f, 0.f, 0.f};
-    if (!LITE && live) {
-        if (p.segs > 1) load_states(p.seg_state + (size_t)q.seg * p.Bn * p.Cn * p.N + state_row, n0, p.N, hs);
-        else if (p.h0 != nullptr) load_states(p.h0 + state_row, n0, p.N, hs);
+    {
+        float e[4] = {0.f, 0.f, 0.f, 0.f};
+        if (!LITE && live) {
+            if (p.segs > 1) load_states(p.seg_state + (size_t)q.seg * p.Bn * p.Cn * p.N + state_row, n0, p.N, e);
+            else if (p.h0 != nullptr) load_states(p.h0 + state_row, n0, p.N, e);
+        }
+        h[0] = make_float2(e[0], e[1]);
+        h[1] = make_float2(e[2], e[3]);
     }
-    h[0] = make_float2(hs[0], hs[1]);
-    h[1] = make_float2(hs[2], hs[3]);
+    const int tiles = (p.T + TT - 1) / TT;
     for (int tile = q.first; tile < q.last; ++tile) {
-        const int t = tile * TT + ts;
-        float cu[V], cd[V];
-        ru.get(cu);
-        rd.get(cd);
-        const Staged<T, V, VEC> cz = rz;
-#pragma unroll
-        for (int v = 0; v < V; ++v) {
-            const float d = t < L ? softplus_full(cd[v] + bias[v]) : 0.f;
-            sum_d[v] += d;
-            cd[v] = d;
-        }
-        if constexpr (V == 1) {
-            sdx[ts][cv] = make_float2(cd[0], cd[0] * cu[0]);
-        } else {
-#pragma unroll
-            for (int v = 0; v < V; v += 2)
-                *reinterpret_cast<float4 *>(&sdx[ts][cv + v]) = make_float4(cd[v], cd[v] * cu[v], cd[v + 1], cd[v + 1] * cu[v + 1]);
-        }
-#pragma unroll
-        for (int k = 0; k < KB; ++k) {
-            const int e = tid + kScanThreads * k;
-            sB[e / NP][e % NP] = to_f32(rB[k]);
-            if (!LITE) sC[e / NP][e % NP] = to_f32(rC[k]);
-        }
-        __syncthreads();
-        if (tile + 1 < q.last) fetch(tile + 1);
+        const int buf = tile & 1;
         if (!LITE && p.ckpt != nullptr && live) {
-            const int tiles = (p.T + TT - 1) / TT;
             const float o[4] = {h[0].x, h[0].y, h[1].x, h[1].y};
             store_states(p.ckpt + (((size_t)q.b * tiles + tile) * p.Cn + c) * p.N, n0, p.N, o);
         }
+        named_bar_sync(kFull + buf, ALL);
         // four steps at a time: what does not depend on the state (decays, d u B) is formed for the next
         // four before the chain of the present four, whose only latency is one multiply-add per step
         struct Group {
@@ -112,8 +192,8 @@ __global__ void __launch_bounds__(kScanThreads, 3) scan_fwd_kernel(ScanParams p)
         auto prepare = [&](int i0, Group &o) {
 #pragma unroll
             for (int i = 0; i < 4; ++i) {
-                const float2 dx = sdx[i0 + i][ch];
-                const float4 b4 = *reinterpret_cast<const float4 *>(&sB[i0 + i][n0]);
+                const float2 dx = sdx[buf][i0 + i][ch];
+                const float4 b4 = *reinterpret_cast<const float4 *>(&sB[buf][i0 + i][n0]);
                 const float2 b2[2] = {make_float2(b4.x, b4.y), make_float2(b4.z, b4.w)};
 #pragma unroll
                 for (int k = 0; k < 2; ++k) {
@@ -121,7 +201,7 @@ __global__ void __launch_bounds__(kScanThreads, 3) scan_fwd_kernel(ScanParams p)
                     o.x[i][k] = __fmul2_rn(make_float2(dx.y, dx.y), b2[k]);
                 }
                 if (!LITE) {
-                    const float4 c4 = *reinterpret_cast<const float4 *>(&sC[i0 + i][n0]);
+                    const float4 c4 = *reinterpret_cast<const float4 *>(&sC[buf][i0 + i][n0]);
                     o.c[i][0] = make_float2(c4.x, c4.y);
                     o.c[i][1] = make_float2(c4.z, c4.w);
                 }
@@ -145,34 +225,15 @@ __global__ void __launch_bounds__(kScanThreads, 3) scan_fwd_kernel(ScanParams p)
             }
             if (!LITE) {
                 const float r = lane_sum4<LPC>(core, lane);
-                if (lane % LPC < 4) score[i0 + (lane & 3)][ch] = r;
+                if (lane % LPC < 4) score[buf][i0 + (lane & 3)][ch] = r;
             }
             now = then;
         }
-        __syncthreads();
-        if (!LITE && t < p.T) {
-            float o[V], zz[V];
-            cz.get(zz);
-#pragma unroll
-            for (int v = 0; v < V; ++v) {
-                const float core = fmaf(D[v], cu[v], score[ts][cv + v]);
-                o[v] = t < L ? (p.z != nullptr ? core * silu_hw(zz[v]) : core) : 0.f;
-            }
-            store_channels<T, V>(static_cast<T *>(p.y) + ((size_t)q.b * p.T + t) * p.Cn + q.c0 + cv, nv, VEC, o);
-        }
+        named_bar_arrive(kDone + buf, ALL);
     }
     const float out[4] = {h[0].x, h[0].y, h[1].x, h[1].y};
     if (LITE) {
         if (live) store_states(p.seg_state + (size_t)q.seg * p.Bn * p.Cn * p.N + state_row, n0, p.N, out);
-        // the sum of d over the segment: over a thread's tiles, then over the 16 steps of a tile
-#pragma unroll
-        for (int v = 0; v < V; ++v) score[ts][cv + v] = sum_d[v];
-        __syncthreads();
-        if (tid < q.nc) {
-            float a = 0.f;
-            for (int i = 0; i < TT; ++i) a += score[i][tid];
-            p.seg_sum[((size_t)q.seg * p.Bn + q.b) * p.Cn + q.c0 + tid] = a;
-        }
     } else if (p.h_T != nullptr && live && q.seg == p.segs - 1) {
         store_states(p.h_T + state_row, n0, p.N, out);
     }
@@ -240,7 +301,7 @@ cudaError_t launch_scan_combine(const ScanParams &p, const float *start, float *
     return cudaGetLastError();
 }
 
-constexpr int kBwdSplitBelow = 304, kBwdSplitWant = 304;
+constexpr int kBwdSplitBelow = 304, kBwdSplitWant = 768, kFwdSplitBelow = 76, kFwdSplitWant = 448;
 
 int scan_lanes(int N) { return N <= 16 ? 4 : N <= 32 ? 8 : 16; }
 
@@ -256,7 +317,7 @@ int scan_blocks(int C, int G, int N) {
 void scan_split(ScanParams *p, bool bwd) {
     const long long ctas = (long long)p->Bn * p->G * scan_blocks(p->Cn, p->G, p->N);
     const int tiles = (p->T + kScanTile - 1) / kScanTile;
-    const int below = bwd ? kBwdSplitBelow : 76, want = bwd ? kBwdSplitWant : 304;
+    const int below = bwd ? kBwdSplitBelow : kFwdSplitBelow, want = bwd ? kBwdSplitWant : kFwdSplitWant;
     int segs = 1;
     if (ctas < below && tiles >= 16) {
         segs = (int)((want + ctas - 1) / ctas);
@@ -275,13 +336,13 @@ cudaError_t scan_fwd_prompt(const ScanParams &p, cudaStream_t s) {
     cudaError_t e;
     if (p.segs > 1) {
         timing_mark("scan_fwd_ends", 0, s);
-        scan_fwd_kernel<LPC, T, VEC, true><<<grid, kScanThreads, 0, s>>>(p);
+        scan_fwd_kernel<LPC, T, VEC, true><<<grid, kScanThreads + kScanHelpers, 0, s>>>(p);
         timing_mark("scan_fwd_ends", 1, s);
         if ((e = cudaGetLastError()) != cudaSuccess) return e;
         if ((e = launch_scan_combine(p, p.h0, nullptr, false, s)) != cudaSuccess) return e;
     }
     timing_mark("scan_fwd", 0, s);
-    scan_fwd_kernel<LPC, T, VEC, false><<<grid, kScanThreads, 0, s>>>(p);
+    scan_fwd_kernel<LPC, T, VEC, false><<<grid, kScanThreads + kScanHelpers, 0, s>>>(p);
     timing_mark("scan_fwd", 1, s);
     return cudaGetLastError();
 }

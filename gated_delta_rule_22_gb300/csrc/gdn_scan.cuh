@@ -2,8 +2,8 @@
 // (internal; not part of the C ABI).
 //
 // Layout of the work. The states of one channel lie on LPC neighbouring lanes (4, 8 or 16), four
-// states on each, so that N up to 16, 32 or 64 states take one pass; a CTA of 8 warps holds
-// CH = 256 / LPC channels of one group of one batch row and walks the steps in tiles of 16. The
+// states on each, so that N up to 16, 32 or 64 states take one pass; a CTA holds CH =
+// 256 / LPC channels of one group of one batch row and walks the steps in tiles of 16. The
 // per-step inputs of a tile (d, d u, B, C and in the backward the cotangent) are staged in shared
 // memory as float32: each is read by every lane that needs it as a broadcast, softplus is computed
 // once per channel and step, and the global accesses of the channels-last tensors stay wide.
@@ -13,8 +13,12 @@
 
 namespace gdn {
 
-constexpr int kScanThreads = 256;
-constexpr int kScanWarps = kScanThreads / 32;
+constexpr int kScanThreads = 256;     // that hold states, in the forward (and the channels of a CTA)
+constexpr int kScanHelpers = 128;     // that stage inputs and finish outputs
+
+__device__ __forceinline__ void named_bar_arrive(int id, int n) {
+    asm volatile("bar.arrive %0, %1;" ::"r"(id), "r"(n) : "memory");
+}
 
 template <int LPC>
 struct ScanGeo {
@@ -22,7 +26,6 @@ struct ScanGeo {
     static constexpr int CPW = 32 / LPC;                    // channels per warp
     static constexpr int NP = 4 * LPC;                      // states per channel, padded
     static constexpr int V = CH * kScanTile / kScanThreads; // staged elements per thread (4, 2, 1)
-    static constexpr int KB = NP * kScanTile / kScanThreads;// staged elements of B (of C) per thread
     static constexpr int SP = CH + CPW;                     // pitch of a row of sums: no bank conflicts
 };
 

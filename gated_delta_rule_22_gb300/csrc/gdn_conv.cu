@@ -352,7 +352,7 @@ __global__ void __launch_bounds__(32 * kConvBwdWarps, 2) conv_bwd_kernel(ConvPar
 // dw[c][j] and dbias[c] from the slices' partial sums.
 __global__ void __launch_bounds__(256) conv_reduce_kernel(ConvParams p, int slices) {
     const size_t n = (size_t)(p.W + 1) * p.C, i = (size_t)blockIdx.x * 32 + threadIdx.x;
-    const float a = slice_sum(p.part, slices, n);
+    const float a = slice_sum(p.part, slices, n, blockIdx.x);
     if (threadIdx.x >= 32 || i >= n) return;
     const int j = (int)(i / p.C), c = (int)(i % p.C);
     if (j < p.W) p.dw[(size_t)c * p.W + j] = a;
@@ -386,7 +386,7 @@ cudaError_t conv_fwd_launch(const ConvParams &p, cudaStream_t s) {
     timing_mark("conv_fwd", 0, s);
     constexpr int smem = Ring<T, V, kConvThreads>::kBytes;
     if (smem > 48 * 1024) {
-        const cudaError_t e = cudaFuncSetAttribute(conv_fwd_kernel<T, W, V>, cudaFuncAttributeMaxDynamicSharedMemorySize, smem);
+        const cudaError_t e = allow_smem<conv_fwd_kernel<T, W, V>>(smem);
         if (e != cudaSuccess) return e;
     }
     conv_fwd_kernel<T, W, V><<<(unsigned)((n + kConvThreads - 1) / kConvThreads), kConvThreads, smem, s>>>(p, run, runs);
@@ -401,7 +401,7 @@ cudaError_t conv_bwd_launch(const ConvParams &p, cudaStream_t s) {
     timing_mark("conv_bwd", 0, s);
     constexpr int ring = 2 * Ring<T, V, 32 * kConvBwdWarps>::kBytes, sums = kConvBwdWarps * (W + 1) * 32 * V * 4;
     constexpr int smem = ring > sums ? ring : sums;
-    cudaError_t e = cudaFuncSetAttribute(conv_bwd_kernel<T, W, V>, cudaFuncAttributeMaxDynamicSharedMemorySize, smem);
+    cudaError_t e = allow_smem<conv_bwd_kernel<T, W, V>>(smem);
     if (e != cudaSuccess) return e;
     conv_bwd_kernel<T, W, V><<<dim3(slices, (p.C + 32 * V - 1) / (32 * V)), 32 * kConvBwdWarps, smem, s>>>(p, run, slices_row);
     timing_mark("conv_bwd", 1, s);

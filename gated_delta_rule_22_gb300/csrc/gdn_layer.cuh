@@ -5,6 +5,8 @@
 
 #include "gdn_common.cuh"
 
+#include <atomic>
+
 namespace gdn {
 
 enum { kActNone = 0, kActSilu = 1, kActGelu = 2 };
@@ -90,6 +92,21 @@ cudaError_t launch_norm_bwd(const NormParams &p, int dtype, cudaStream_t s);
 // These return a GDN_* code (they encode tensor maps).
 int launch_linear_fwd(const LinearParams &p, int dtype, cudaStream_t s);
 int launch_linear_bwd(const LinearParams &p, int dtype, cudaStream_t s);
+
+// Raises a kernel's limit of dynamic shared memory, once per device (the call costs about a
+// microsecond, as much as a third of a launch).
+template <auto Kernel>
+inline cudaError_t allow_smem(int bytes) {
+    static std::atomic<unsigned long long> done{0};
+    int dev = 0;
+    cudaError_t e = cudaGetDevice(&dev);
+    if (e != cudaSuccess) return e;
+    const unsigned long long bit = dev < 64 ? 1ull << dev : 0;
+    if (done.load(std::memory_order_relaxed) & bit) return cudaSuccess;
+    e = cudaFuncSetAttribute(Kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, bytes);
+    if (e == cudaSuccess) done.fetch_or(bit, std::memory_order_relaxed);
+    return e;
+}
 
 // ---- device helpers
 constexpr float kLog2e = 1.4426950408889634f;
@@ -266,14 +283,14 @@ __device__ __forceinline__ void add_comp(float &x, float &lost, float y) {
     x = s;
 }
 
-// Sum over the slices of partial sums part[slice][n] of column blockIdx.x * 32 + threadIdx.x % 32, for
-// a CTA of 256 threads: eight threads take every eighth slice of a column, then their sums are added in
+// Sum over the slices of partial sums part[slice][n] of column block * 32 + threadIdx.x % 32, for a CTA
+// of 256 threads: eight threads take every eighth slice of a column, then their sums are added in
 // order. Compensated float32: as exact as float64 here, whose rate on this GPU is a sixty-fourth. Valid
 // in the first 32 threads.
-__device__ __forceinline__ float slice_sum(const float *part, int slices, size_t n) {
+__device__ __forceinline__ float slice_sum(const float *part, int slices, size_t n, unsigned block) {
     __shared__ float2 sums[8][32];
     const int col = threadIdx.x & 31, lane = threadIdx.x >> 5;
-    const size_t i = (size_t)blockIdx.x * 32 + col;
+    const size_t i = (size_t)block * 32 + col;
     float a = 0.f, lost = 0.f;
     if (i < n)
 #pragma unroll 4

@@ -194,7 +194,6 @@ gemm_kernel(const __grid_constant__ CUtensorMap tmA, const __grid_constant__ CUt
         }
         fence_mbar_init();
         tma_prefetch_map(A_MN && !p.a_blocks ? &tmA_half : &tmA);
-        tma_prefetch_map(B_MN && !p.b_blocks ? &tmB_half : &tmB);
     }
     if (warp == 1) pair_tmem_alloc(tmem_slot, 512);
     tc_fence_before();
@@ -764,7 +763,7 @@ __global__ void __launch_bounds__(256) linear_dpre_kernel(const T *dy, const T *
 template <typename T>
 __global__ void __launch_bounds__(256) linear_dbias_kernel(const float *part, T *dbias, int slices, int N) {
     const int n = blockIdx.x * 32 + threadIdx.x;
-    const float s = slice_sum(part, slices, N);
+    const float s = slice_sum(part, slices, N, blockIdx.x);
     if (threadIdx.x < 32 && n < N) dbias[n] = from_f32<T>(s);
 }
 
@@ -839,20 +838,22 @@ int gemm(const char *name, const Operand &A, const Operand &B, int M, int N, int
     p.items = p.whole + p.halves + (p.edge > 0 ? p.mt : 0);
     const int V = 16 / (int)sizeof(T);
     p.vec = N % V == 0 && (uintptr_t)e.res % 16 == 0 && e.ldres % V == 0;
-    CUtensorMap tm[4];                                 // A, one box of A, B, one box of B
+    CUtensorMap tm[4] = {};                            // A, one box of A, B, one box of B: those in use
+    const bool a_blocks = A_MN && A.cols % 64 == 0, b_blocks = B_MN && B.cols % 64 == 0;
+    const bool a_boxes = A_MN && !a_blocks, b_boxes = B_MN && !b_blocks;
+    const bool use[4] = {!a_boxes, a_boxes, !b_boxes && (p.whole > 0 || p.edge > 128),
+                         b_boxes || p.halves > 0 || (p.edge > 0 && p.edge <= 128) || TN <= 128};
+    p.a_blocks = a_blocks;
+    p.b_blocks = b_blocks;
     int rc;
     for (int i = 0; i < 4; ++i) {
         const Operand &o = i < 2 ? A : B;
-        const bool mn = i < 2 ? A_MN : B_MN, blocks = mn && o.cols % 64 == 0;
+        const bool mn = i < 2 ? A_MN : B_MN, blocks = i < 2 ? a_blocks : b_blocks;
         const int boxes = 2 - i % 2;
-        (i < 2 ? p.a_blocks : p.b_blocks) = blocks;
-        if (mn && !blocks && boxes == 2) {             // not used
-            tm[i] = {};
-            continue;
-        }
-        if ((rc = api_planes_map(&tm[i], o.p, o.cols, o.rows, planes, o.ld, mn ? kBK : 64 * boxes, blocks ? boxes : 0)) != 0) return rc;
+        if (use[i] && (rc = api_planes_map(&tm[i], o.p, o.cols, o.rows, planes, o.ld, mn ? kBK : 64 * boxes, blocks ? boxes : 0)) != 0)
+            return rc;
     }
-    cudaError_t err = cudaFuncSetAttribute(gemm_kernel<A_MN, B_MN, T>, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)kGemmSmem);
+    cudaError_t err = allow_smem<gemm_kernel<A_MN, B_MN, T>>((int)kGemmSmem);
     if (err != cudaSuccess) return api_cuda_status(err);
     timing_mark(name, 0, s);
     gemm_kernel<A_MN, B_MN, T><<<2 * (p.items < kPairs ? p.items : kPairs), kGemmThreads, kGemmSmem, s>>>(tm[0], tm[1], tm[2], tm[3], p);
@@ -874,7 +875,7 @@ int token_launch(const LinearParams &p, cudaStream_t s) {
     int rc;
     if ((rc = api_planes_map(&w, p.W, p.K, p.N, 1, p.ldw, 128, 0)) != 0) return rc;
     if ((rc = api_planes_map(&x, p.x, p.K, p.M, 1, p.ldx, MP, 0)) != 0) return rc;
-    cudaError_t e = cudaFuncSetAttribute(linear_token_kernel<MP>, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)G::kSmem);
+    cudaError_t e = allow_smem<linear_token_kernel<MP>>((int)G::kSmem);
     if (e != cudaSuccess) return api_cuda_status(e);
     cudaLaunchConfig_t cfg = {};
     cfg.gridDim = dim3(splits, tiles);

@@ -395,7 +395,7 @@ __global__ void __launch_bounds__(kNormThreads) norm_bwd_wide_sums_kernel(NormPa
 // dw, db from the slices' partial sums.
 __global__ void __launch_bounds__(256) norm_reduce_kernel(NormParams p) {
     const size_t C = (size_t)p.G * p.D, i = (size_t)blockIdx.x * 32 + threadIdx.x;
-    const float a = slice_sum(p.part, p.slices, 2 * C);
+    const float a = slice_sum(p.part, p.slices, 2 * C, blockIdx.x);
     if (threadIdx.x >= 32 || i >= 2 * C) return;
     float *out = i < C ? p.dw : p.db;
     if (out != nullptr) out[i % C] = a;

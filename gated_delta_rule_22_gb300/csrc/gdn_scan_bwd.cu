@@ -406,23 +406,22 @@ __global__ void __launch_bounds__(kRevThreads, kRevCtas) scan_bwd_kernel(ScanPar
     }
 }
 
-// dB, dC: over the channel blocks of their group.
+// The last sums: dB, dC over the channel blocks of their group (the CTAs below n_bc), dA_log, dD and
+// ddt_bias over the segments and batch rows (the others).
 template <typename T>
-__global__ void __launch_bounds__(256) scan_reduce_bc_kernel(ScanParams p, int blocks) {
-    const size_t n = (size_t)p.Bn * p.T * p.G * 2 * p.N, i = (size_t)blockIdx.x * 32 + threadIdx.x;
-    const float s = slice_sum(p.part_bc, blocks, n);
+__global__ void __launch_bounds__(256) scan_reduce_kernel(ScanParams p, int blocks, unsigned n_bc) {
+    const bool bc = blockIdx.x < n_bc;
+    const unsigned blk = bc ? blockIdx.x : blockIdx.x - n_bc;
+    const size_t n = bc ? (size_t)p.Bn * p.T * p.G * 2 * p.N : (size_t)(p.N + 2) * p.Cn, i = (size_t)blk * 32 + threadIdx.x;
+    const float s = slice_sum(bc ? p.part_bc : p.part_c, bc ? blocks : p.segs * p.Bn, n, blk);
     if (threadIdx.x >= 32 || i >= n) return;
-    const size_t row = i / (2 * p.N);
-    const int m = (int)(i % (2 * p.N));
-    if (m < p.N) static_cast<T *>(p.dB)[row * p.N + m] = from_f32<T>(s);
-    else static_cast<T *>(p.dC)[row * p.N + m - p.N] = from_f32<T>(s);
-}
-
-// dA_log, dD, ddt_bias: over the segments and batch rows.
-__global__ void __launch_bounds__(256) scan_reduce_c_kernel(ScanParams p) {
-    const size_t n = (size_t)(p.N + 2) * p.Cn, i = (size_t)blockIdx.x * 32 + threadIdx.x;
-    const float s = slice_sum(p.part_c, p.segs * p.Bn, n);
-    if (threadIdx.x >= 32 || i >= n) return;
+    if (bc) {
+        const size_t row = i / (2 * p.N);
+        const int m = (int)(i % (2 * p.N));
+        if (m < p.N) static_cast<T *>(p.dB)[row * p.N + m] = from_f32<T>(s);
+        else static_cast<T *>(p.dC)[row * p.N + m - p.N] = from_f32<T>(s);
+        return;
+    }
     const int m = (int)(i / p.Cn), c = (int)(i % p.Cn);
     if (m < p.N) {
         const size_t o = (size_t)c * p.N + m;
@@ -438,8 +437,7 @@ namespace {
 
 template <int LPC, typename T, bool VEC, bool LITE>
 cudaError_t scan_bwd_one(const ScanParams &p, cudaStream_t s) {
-    const cudaError_t e = cudaFuncSetAttribute(scan_bwd_kernel<LPC, T, VEC, LITE>, cudaFuncAttributeMaxDynamicSharedMemorySize,
-                                               (int)sizeof(BwdSmem<LPC, T>));
+    const cudaError_t e = allow_smem<scan_bwd_kernel<LPC, T, VEC, LITE>>((int)sizeof(BwdSmem<LPC, T>));
     if (e != cudaSuccess) return e;
     const dim3 grid(p.Bn * p.G * scan_blocks(p.Cn, p.G, p.N), p.segs);
     const char *name = LITE ? "scan_bwd_ends" : "scan_bwd";
@@ -464,12 +462,9 @@ cudaError_t scan_bwd_launch(const ScanParams &p, cudaStream_t s) {
     cudaError_t e = scan_vec<T>(p, ScanGeo<LPC>::V) ? scan_bwd_prompt<LPC, T, true>(p, s) : scan_bwd_prompt<LPC, T, false>(p, s);
     if (e != cudaSuccess) return e;
     const size_t n = (size_t)p.Bn * p.T * p.G * 2 * p.N, m = (size_t)(p.N + 2) * p.Cn;
+    const unsigned n_bc = (unsigned)((n + 31) / 32), n_c = (unsigned)((m + 31) / 32);
     timing_mark("scan_reduce", 0, s);
-    scan_reduce_bc_kernel<T><<<(unsigned)((n + 31) / 32), 256, 0, s>>>(p, scan_blocks(p.Cn, p.G, p.N));
-    timing_mark("scan_reduce", 1, s);
-    if ((e = cudaGetLastError()) != cudaSuccess) return e;
-    timing_mark("scan_reduce", 0, s);
-    scan_reduce_c_kernel<<<(unsigned)((m + 31) / 32), 256, 0, s>>>(p);
+    scan_reduce_kernel<T><<<n_bc + n_c, 256, 0, s>>>(p, scan_blocks(p.Cn, p.G, p.N), n_bc);
     timing_mark("scan_reduce", 1, s);
     return cudaGetLastError();
 }

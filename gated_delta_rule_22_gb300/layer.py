@@ -84,6 +84,10 @@ def _stream_of(stream, device):
     return stream.cuda_stream if stream is not None else torch._C._cuda_getCurrentRawStream(device.index)
 
 
+def _type(t):
+    return 1 if t.dtype is torch.bfloat16 else _dtype_code(t)
+
+
 def _check(name, t, shape, dtype, device):
     """binding._check, whose comparisons in words run only for a tensor that one of these refuses: a
     single-token call is shorter than its checks otherwise."""
@@ -91,22 +95,17 @@ def _check(name, t, shape, dtype, device):
         _check_in_words(name, t, shape, dtype, device)
 
 
-def _optional(name, t, shape, dtype, device):
-    if t is not None:
-        _check(name, t, shape, dtype, device)
-
-
 def _rows(name, t, shape, dtype, device, inner=1):
     """Row stride (0: packed) of a tensor whose last `inner` dimensions are packed and whose leading
     ones follow each other at one stride, as a slice of a contiguous tensor along its last dimension."""
+    if t.is_contiguous() and t.shape == shape and t.dtype is dtype and t.device == device:
+        return 0
     if t.shape != shape:
         raise ValueError(f"{name} has shape {tuple(t.shape)}, expected {tuple(shape)}")
     if t.dtype is not dtype:
         raise TypeError(f"{name} has dtype {t.dtype}, expected {dtype}")
     if t.device != device:
         raise ValueError(f"{name} is on {t.device}, expected {device}")
-    if t.is_contiguous():
-        return 0
     width, packed = 1, True
     for size, stride in zip(reversed(t.shape[-inner:]), reversed(t.stride()[-inner:])):
         packed = packed and (size == 1 or stride == width)
@@ -127,7 +126,7 @@ def _rows(name, t, shape, dtype, device, inner=1):
 def _scratch(name, t, need, device):
     """The caller's buffer, checked, or a new one for this call (None where nothing is needed)."""
     if t is None:
-        return torch.empty(need, dtype=torch.uint8, device=device) if need else None
+        return _empty(need, dtype=torch.uint8, device=device) if need else None
     if t.device != device or not t.is_contiguous():
         raise ValueError(f"{name} must be a contiguous tensor on {device}")
     return t
@@ -137,15 +136,19 @@ def _size(t):
     return 0 if t is None else t.numel() * t.element_size()
 
 
-def _run(name, lib, shape, *args):
-    rc = getattr(lib, name)(ctypes.byref(shape), *args)
-    if rc != GDN_OK:
-        raise GdnError(name, rc, lib)
+def _raise(name, rc):
+    raise GdnError(name, rc, _library())
 
 
-def _check_lens(lens, B, dev):
-    if lens is not None:
-        _check("lens", lens, (B,), torch.int32, dev)
+# A single token's step takes the GPU a few microseconds, less than a Python call with this many
+# arguments: the code below looks up, converts and calls no more than it has to.
+_empty, _empty_like, _byref = torch.empty, torch.empty_like, ctypes.byref
+_BF16, _F32, _I32 = torch.bfloat16, torch.float32, torch.int32
+
+
+def _new_like(t):
+    """A packed tensor of t's shape and type."""
+    return _empty_like(t) if t.is_contiguous() else _empty(t.shape, dtype=t.dtype, device=t.device)
 
 
 # ------------------------------------------------------------------- short causal convolution
@@ -154,11 +157,14 @@ def _conv_args(x, w, bias, s0, lens, act):
     W = w.shape[-1]
     dev, dt = x.device, x.dtype
     ld = _rows("x", x, (B, T, C), dt, dev)
-    _check("w", w, (C, W), torch.float32, dev)
-    _optional("bias", bias, (C,), torch.float32, dev)
-    _optional("s0", s0, (B, W - 1, C), dt, dev)
-    _check_lens(lens, B, dev)
-    return GdnConvShape(B, T, C, W, _act(act), _dtype_code(x), ld)
+    _check("w", w, (C, W), _F32, dev)
+    if bias is not None:
+        _check("bias", bias, (C,), _F32, dev)
+    if s0 is not None:
+        _check("s0", s0, (B, W - 1, C), dt, dev)
+    if lens is not None:
+        _check("lens", lens, (B,), _I32, dev)
+    return GdnConvShape(B, T, C, W, _act(act), _type(x), ld)
 
 
 def gdn_conv_fwd(x, w, bias=None, s0=None, lens=None, *, act="silu", y=None, s_T=None, want_s_T=True, stream=None):
@@ -168,14 +174,19 @@ def gdn_conv_fwd(x, w, bias=None, s0=None, lens=None, *, act="silu", y=None, s_T
     lib = _library()
     shape = _conv_args(x, w, bias, s0, lens, act)
     B, T, C, W, dev, dt = shape.B, shape.T, shape.C, shape.W, x.device, x.dtype
-    _optional("y", y, (B, T, C), dt, dev)
-    _optional("s_T", s_T, (B, W - 1, C), dt, dev)
-    _require_cuda(x)
+    if y is not None:
+        _check("y", y, (B, T, C), dt, dev)
+    if s_T is not None:
+        _check("s_T", s_T, (B, W - 1, C), dt, dev)
+    if not x.is_cuda:
+        _require_cuda(x)
     if y is None:
-        y = torch.empty((B, T, C), dtype=dt, device=dev)
+        y = _new_like(x)
     if s_T is None and want_s_T:
-        s_T = torch.empty((B, W - 1, C), dtype=dt, device=dev)
-    _run("gdn_conv_fwd", lib, shape, _at(x), _at(w), _at(bias), _at(s0), _at(lens), _at(y), _at(s_T), _stream_of(stream, dev))
+        s_T = _empty((B, W - 1, C), dtype=dt, device=dev) if s0 is None else _empty_like(s0)
+    rc = lib.gdn_conv_fwd(_byref(shape), x.data_ptr(), w.data_ptr(), _at(bias), _at(s0), _at(lens), _at(y), _at(s_T), _stream_of(stream, dev))
+    if rc:
+        _raise("gdn_conv_fwd", rc)
     return y, s_T
 
 
@@ -190,14 +201,18 @@ def gdn_conv_bwd(x, w, dy, bias=None, s0=None, lens=None, ds_T=None, *, act="sil
     shape = _conv_args(x, w, bias, s0, lens, act)
     B, T, C, W, dev, dt = shape.B, shape.T, shape.C, shape.W, x.device, x.dtype
     _check("dy", dy, (B, T, C), dt, dev)
-    _optional("ds_T", ds_T, (B, W - 1, C), dt, dev)
-    _require_cuda(x)
-    workspace = _scratch("workspace", workspace, lib.gdn_conv_bwd_workspace_bytes(ctypes.byref(shape)), dev)
-    out = {"dx": torch.empty((B, T, C), dtype=dt, device=dev), "dw": torch.empty((C, W), dtype=torch.float32, device=dev),
-           "dbias": torch.empty((C,), dtype=torch.float32, device=dev),
-           "ds0": torch.empty((B, W - 1, C), dtype=dt, device=dev) if want_ds0 else None}
-    _run("gdn_conv_bwd", lib, shape, _at(x), _at(w), _at(bias), _at(s0), _at(lens), _at(dy), _at(ds_T), _at(out["dx"]),
+    if ds_T is not None:
+        _check("ds_T", ds_T, (B, W - 1, C), dt, dev)
+    if not x.is_cuda:
+        _require_cuda(x)
+    workspace = _scratch("workspace", workspace, lib.gdn_conv_bwd_workspace_bytes(_byref(shape)), dev)
+    out = {"dx": _empty_like(dy), "dw": _empty_like(w),
+           "dbias": _empty((C,), dtype=_F32, device=dev),
+           "ds0": _empty((B, W - 1, C), dtype=dt, device=dev) if want_ds0 else None}
+    rc = lib.gdn_conv_bwd(_byref(shape), x.data_ptr(), w.data_ptr(), _at(bias), _at(s0), _at(lens), dy.data_ptr(), _at(ds_T), _at(out["dx"]),
          _at(out["dw"]), _at(out["dbias"]), _at(out["ds0"]), _at(workspace), _size(workspace), _stream_of(stream, dev))
+    if rc:
+        _raise("gdn_conv_bwd", rc)
     return out
 
 
@@ -209,11 +224,14 @@ def _scan_args(u, dt, A_log, B, C, D, dt_bias, z, lens):
     ldu, lddt = _rows("u", u, (Bn, T, Cn), ty, dev), _rows("dt", dt, (Bn, T, Cn), ty, dev)
     ldz = 0 if z is None else _rows("z", z, (Bn, T, Cn), ty, dev)
     ldB, ldC = _rows("B", B, (Bn, T, G, N), ty, dev, 2), _rows("C", C, (Bn, T, G, N), ty, dev, 2)
-    _check("A_log", A_log, (Cn, N), torch.float32, dev)
-    _optional("D", D, (Cn,), torch.float32, dev)
-    _optional("dt_bias", dt_bias, (Cn,), torch.float32, dev)
-    _check_lens(lens, Bn, dev)
-    return GdnScanShape(Bn, T, Cn, N, G, _dtype_code(u), ldu, lddt, ldz, ldB, ldC)
+    _check("A_log", A_log, (Cn, N), _F32, dev)
+    if D is not None:
+        _check("D", D, (Cn,), _F32, dev)
+    if dt_bias is not None:
+        _check("dt_bias", dt_bias, (Cn,), _F32, dev)
+    if lens is not None:
+        _check("lens", lens, (Bn,), _I32, dev)
+    return GdnScanShape(Bn, T, Cn, N, G, _type(u), ldu, lddt, ldz, ldB, ldC)
 
 
 def gdn_scan_ckpt_bytes(shape: GdnScanShape) -> int:
@@ -241,20 +259,27 @@ def gdn_scan_fwd(u, dt, A_log, B, C, D=None, dt_bias=None, z=None, h0=None, lens
     lib = _library()
     shape = _scan_args(u, dt, A_log, B, C, D, dt_bias, z, lens)
     Bn, T, Cn, N, dev = shape.B, shape.T, shape.C, shape.N, u.device
-    _optional("h0", h0, (Bn, Cn, N), torch.float32, dev)
-    _optional("y", y, (Bn, T, Cn), u.dtype, dev)
-    _optional("h_T", h_T, (Bn, Cn, N), torch.float32, dev)
-    _optional("ckpt", ckpt, _scan_ckpt_shape(Bn, T, Cn, N), torch.float32, dev)
-    _require_cuda(u)
+    if h0 is not None:
+        _check("h0", h0, (Bn, Cn, N), _F32, dev)
+    if y is not None:
+        _check("y", y, (Bn, T, Cn), u.dtype, dev)
+    if h_T is not None:
+        _check("h_T", h_T, (Bn, Cn, N), _F32, dev)
+    if ckpt is not None:
+        _check("ckpt", ckpt, _scan_ckpt_shape(Bn, T, Cn, N), _F32, dev)
+    if not u.is_cuda:
+        _require_cuda(u)
     if y is None:
-        y = torch.empty((Bn, T, Cn), dtype=u.dtype, device=dev)
+        y = _new_like(u)
     if h_T is None and want_h_T:
-        h_T = torch.empty((Bn, Cn, N), dtype=torch.float32, device=dev)
+        h_T = _empty((Bn, Cn, N), dtype=_F32, device=dev) if h0 is None else _empty_like(h0)
     if ckpt is None and want_ckpt:
-        ckpt = torch.empty(_scan_ckpt_shape(Bn, T, Cn, N), dtype=torch.float32, device=dev)
+        ckpt = _empty(_scan_ckpt_shape(Bn, T, Cn, N), dtype=_F32, device=dev)
     workspace = _scratch("workspace", workspace, 0 if T == 1 else lib.gdn_scan_fwd_workspace_bytes(ctypes.byref(shape)), dev)
-    _run("gdn_scan_fwd", lib, shape, _at(u), _at(dt), _at(A_log), _at(B), _at(C), _at(D), _at(dt_bias), _at(z), _at(h0),
+    rc = lib.gdn_scan_fwd(_byref(shape), u.data_ptr(), dt.data_ptr(), A_log.data_ptr(), B.data_ptr(), C.data_ptr(), _at(D), _at(dt_bias), _at(z), _at(h0),
          _at(lens), _at(y), _at(h_T), _at(ckpt), _size(ckpt), _at(workspace), _size(workspace), _stream_of(stream, dev))
+    if rc:
+        _raise("gdn_scan_fwd", rc)
     return y, h_T, ckpt
 
 
@@ -265,21 +290,24 @@ def gdn_scan_bwd(u, dt, A_log, B, C, ckpt, dy, D=None, dt_bias=None, z=None, len
     lib = _library()
     shape = _scan_args(u, dt, A_log, B, C, D, dt_bias, z, lens)
     Bn, T, Cn, N, G, dev, ty = shape.B, shape.T, shape.C, shape.N, shape.G, u.device, u.dtype
-    _check("ckpt", ckpt, _scan_ckpt_shape(Bn, T, Cn, N), torch.float32, dev)
+    _check("ckpt", ckpt, _scan_ckpt_shape(Bn, T, Cn, N), _F32, dev)
     _check("dy", dy, (Bn, T, Cn), ty, dev)
-    _optional("dh_T", dh_T, (Bn, Cn, N), torch.float32, dev)
-    _require_cuda(u)
+    if dh_T is not None:
+        _check("dh_T", dh_T, (Bn, Cn, N), _F32, dev)
+    if not u.is_cuda:
+        _require_cuda(u)
     workspace = _scratch("workspace", workspace, lib.gdn_scan_bwd_workspace_bytes(ctypes.byref(shape)), dev)
-    wide = lambda: torch.empty((Bn, T, Cn), dtype=ty, device=dev)  # noqa: E731
-    vec = lambda t: None if t is None else torch.empty((Cn,), dtype=torch.float32, device=dev)  # noqa: E731
-    out = {"du": wide(), "ddt": wide(), "dA_log": torch.empty((Cn, N), dtype=torch.float32, device=dev),
-           "dB": torch.empty((Bn, T, G, N), dtype=ty, device=dev), "dC": torch.empty((Bn, T, G, N), dtype=ty, device=dev),
-           "dD": vec(D), "ddt_bias": vec(dt_bias), "dz": None if z is None else wide(),
-           "dh0": torch.empty((Bn, Cn, N), dtype=torch.float32, device=dev) if want_dh0 else None}
-    _run("gdn_scan_bwd", lib, shape, _at(u), _at(dt), _at(A_log), _at(B), _at(C), _at(D), _at(dt_bias), _at(z), _at(lens),
-         _at(ckpt), _size(ckpt), _at(dy), _at(dh_T), _at(out["du"]), _at(out["ddt"]), _at(out["dA_log"]), _at(out["dB"]),
+    vec = lambda t: None if t is None else _empty_like(t)  # noqa: E731
+    out = {"du": _empty_like(dy), "ddt": _empty_like(dy), "dA_log": _empty_like(A_log),
+           "dB": _new_like(B), "dC": _new_like(C),
+           "dD": vec(D), "ddt_bias": vec(dt_bias), "dz": None if z is None else _empty_like(dy),
+           "dh0": _empty((Bn, Cn, N), dtype=_F32, device=dev) if want_dh0 else None}
+    rc = lib.gdn_scan_bwd(_byref(shape), u.data_ptr(), dt.data_ptr(), A_log.data_ptr(), B.data_ptr(), C.data_ptr(), _at(D), _at(dt_bias), _at(z), _at(lens),
+         _at(ckpt), _size(ckpt), dy.data_ptr(), _at(dh_T), _at(out["du"]), _at(out["ddt"]), _at(out["dA_log"]), _at(out["dB"]),
          _at(out["dC"]), _at(out["dD"]), _at(out["ddt_bias"]), _at(out["dz"]), _at(out["dh0"]), _at(workspace),
          _size(workspace), _stream_of(stream, dev))
+    if rc:
+        _raise("gdn_scan_bwd", rc)
     return out
 
 
@@ -292,9 +320,11 @@ def _norm_args(x, groups, w, b, z, act, eps, center):
     rows = x.numel() // max(C, 1)
     ldx = _rows("x", x, x.shape, dt, dev)
     ldz = 0 if z is None else _rows("z", z, x.shape, dt, dev)
-    _optional("w", w, (C,), torch.float32, dev)
-    _optional("b", b, (C,), torch.float32, dev)
-    return GdnNormShape(rows, groups, C // groups, _act(act), 1 if center else 0, _dtype_code(x), eps, ldx, ldz)
+    if w is not None:
+        _check("w", w, (C,), _F32, dev)
+    if b is not None:
+        _check("b", b, (C,), _F32, dev)
+    return GdnNormShape(rows, groups, C // groups, _act(act), 1 if center else 0, _type(x), eps, ldx, ldz)
 
 
 def gdn_norm_fwd(x, groups, w=None, b=None, z=None, *, act="silu", eps=1e-5, center=True, y=None, stats=None,
@@ -307,14 +337,19 @@ def gdn_norm_fwd(x, groups, w=None, b=None, z=None, *, act="silu", eps=1e-5, cen
     shape = _norm_args(x, groups, w, b, z, act, eps, center)
     dev = x.device
     stats_shape = tuple(x.shape[:-1]) + (groups, 2)
-    _optional("y", y, x.shape, x.dtype, dev)
-    _optional("stats", stats, stats_shape, torch.float32, dev)
-    _require_cuda(x)
+    if y is not None:
+        _check("y", y, x.shape, x.dtype, dev)
+    if stats is not None:
+        _check("stats", stats, stats_shape, _F32, dev)
+    if not x.is_cuda:
+        _require_cuda(x)
     if y is None:
-        y = torch.empty(x.shape, dtype=x.dtype, device=dev)
+        y = _new_like(x)
     if stats is None and want_stats:
-        stats = torch.empty(stats_shape, dtype=torch.float32, device=dev)
-    _run("gdn_norm_fwd", lib, shape, _at(x), _at(w), _at(b), _at(z), _at(y), _at(stats), _stream_of(stream, dev))
+        stats = _empty(stats_shape, dtype=_F32, device=dev)
+    rc = lib.gdn_norm_fwd(_byref(shape), x.data_ptr(), _at(w), _at(b), _at(z), _at(y), _at(stats), _stream_of(stream, dev))
+    if rc:
+        _raise("gdn_norm_fwd", rc)
     return y, stats
 
 
@@ -329,14 +364,17 @@ def gdn_norm_bwd(x, groups, stats, dy, w=None, b=None, z=None, *, act="silu", ep
     lib = _library()
     shape = _norm_args(x, groups, w, b, z, act, eps, center)
     dev = x.device
-    _check("stats", stats, tuple(x.shape[:-1]) + (groups, 2), torch.float32, dev)
+    _check("stats", stats, tuple(x.shape[:-1]) + (groups, 2), _F32, dev)
     _check("dy", dy, x.shape, x.dtype, dev)
-    _require_cuda(x)
+    if not x.is_cuda:
+        _require_cuda(x)
     workspace = _scratch("workspace", workspace, lib.gdn_norm_bwd_workspace_bytes(ctypes.byref(shape)), dev)
-    like = lambda t: None if t is None else torch.empty(t.shape, dtype=t.dtype, device=dev)  # noqa: E731
-    out = {"dx": like(x), "dw": like(w), "db": like(b), "dz": like(z)}
-    _run("gdn_norm_bwd", lib, shape, _at(x), _at(w), _at(b), _at(z), _at(stats), _at(dy), _at(out["dx"]), _at(out["dw"]),
+    like = lambda t, of: None if t is None else _empty_like(of)  # noqa: E731
+    out = {"dx": _empty_like(dy), "dw": like(w, w), "db": like(b, b), "dz": like(z, dy)}
+    rc = lib.gdn_norm_bwd(_byref(shape), x.data_ptr(), _at(w), _at(b), _at(z), stats.data_ptr(), dy.data_ptr(), _at(out["dx"]), _at(out["dw"]),
          _at(out["db"]), _at(out["dz"]), _at(workspace), _size(workspace), _stream_of(stream, dev))
+    if rc:
+        _raise("gdn_norm_bwd", rc)
     return out
 
 
@@ -347,9 +385,10 @@ def _linear_args(x, W, bias, res, act):
     N = W.shape[0]
     M = x.numel() // max(K, 1)
     ldx, ldw = _rows("x", x, lead + (K,), dt, dev), _rows("W", W, (N, K), dt, dev)
-    _optional("bias", bias, (N,), dt, dev)
+    if bias is not None:
+        _check("bias", bias, (N,), dt, dev)
     ldres = 0 if res is None else _rows("res", res, lead + (N,), dt, dev)
-    return GdnLinearShape(M, N, K, _act(act), _dtype_code(x), ldx, ldw, ldres), lead + (N,)
+    return GdnLinearShape(M, N, K, _act(act), _type(x), ldx, ldw, ldres), lead + (N,)
 
 
 def gdn_linear_fwd_workspace_bytes(shape: GdnLinearShape) -> int:
@@ -367,16 +406,21 @@ def gdn_linear_fwd(x, W, bias=None, res=None, *, act="none", y=None, pre=None, w
     lib = _library()
     shape, out_shape = _linear_args(x, W, bias, res, act)
     dev, dt = x.device, x.dtype
-    _optional("y", y, out_shape, dt, dev)
-    _optional("pre", pre, out_shape, dt, dev)
-    _require_cuda(x)
+    if y is not None:
+        _check("y", y, out_shape, dt, dev)
+    if pre is not None:
+        _check("pre", pre, out_shape, dt, dev)
+    if not x.is_cuda:
+        _require_cuda(x)
     if y is None:
-        y = torch.empty(out_shape, dtype=dt, device=dev)
+        y = _empty(out_shape, dtype=dt, device=dev)
     if pre is None and want_pre:
-        pre = torch.empty(out_shape, dtype=dt, device=dev)
+        pre = _empty(out_shape, dtype=dt, device=dev)
     workspace = _scratch("workspace", workspace, lib.gdn_linear_fwd_workspace_bytes(ctypes.byref(shape)), dev)
-    _run("gdn_linear_fwd", lib, shape, _at(x), _at(W), _at(bias), _at(res), _at(y), _at(pre), _at(workspace),
+    rc = lib.gdn_linear_fwd(_byref(shape), x.data_ptr(), W.data_ptr(), _at(bias), _at(res), _at(y), _at(pre), _at(workspace),
          _size(workspace), _stream_of(stream, dev))
+    if rc:
+        _raise("gdn_linear_fwd", rc)
     return y, pre
 
 
@@ -388,14 +432,18 @@ def gdn_linear_bwd(x, W, dy, pre=None, *, act="none", want_dx=True, want_dW=True
     shape, out_shape = _linear_args(x, W, None, None, act)
     dev, dt = x.device, x.dtype
     _check("dy", dy, out_shape, dt, dev)
-    _optional("pre", pre, out_shape, dt, dev)
+    if pre is not None:
+        _check("pre", pre, out_shape, dt, dev)
     if pre is None and shape.act != GDN_ACT_NONE:
         raise ValueError("pre is needed: the pre-activation of gdn_linear_fwd (want_pre=True)")
-    _require_cuda(x)
+    if not x.is_cuda:
+        _require_cuda(x)
     workspace = _scratch("workspace", workspace, lib.gdn_linear_bwd_workspace_bytes(ctypes.byref(shape)), dev)
-    out = {"dx": torch.empty(x.shape, dtype=dt, device=dev) if want_dx else None,
-           "dW": torch.empty(W.shape, dtype=dt, device=dev) if want_dW else None,
-           "dbias": torch.empty((W.shape[0],), dtype=dt, device=dev) if want_dbias else None}
-    _run("gdn_linear_bwd", lib, shape, _at(x), _at(W), _at(pre), _at(dy), _at(out["dx"]), _at(out["dW"]), _at(out["dbias"]),
+    out = {"dx": _new_like(x) if want_dx else None,
+           "dW": _new_like(W) if want_dW else None,
+           "dbias": _empty((W.shape[0],), dtype=dt, device=dev) if want_dbias else None}
+    rc = lib.gdn_linear_bwd(_byref(shape), x.data_ptr(), W.data_ptr(), _at(pre), dy.data_ptr(), _at(out["dx"]), _at(out["dW"]), _at(out["dbias"]),
          _at(workspace), _size(workspace), _stream_of(stream, dev))
+    if rc:
+        _raise("gdn_linear_bwd", rc)
     return out

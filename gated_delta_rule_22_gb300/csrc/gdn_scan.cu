@@ -239,43 +239,92 @@ __global__ void __launch_bounds__(kScanThreads + kScanHelpers, 2) scan_fwd_kerne
     }
 }
 
-// One step (T = 1): a streaming pass over the states, LPC lanes per channel, h_T may be h0.
+// One step (T = 1): a streaming pass over the states, bound by their bytes (read and written once). LPC
+// lanes take one channel of four batch rows, so that A is formed once for four states; lane r forms
+// row r's d and finishes its output. h_T may be h0.
 template <int LPC, typename T>
-__global__ void __launch_bounds__(256) scan_step_kernel(ScanParams p) {
-    const size_t id = (size_t)blockIdx.x * 256 + threadIdx.x;
-    const size_t row = id / LPC;                       // (batch row, channel)
-    const int n0 = 4 * (int)(id % LPC);
-    const bool live = row < (size_t)p.Bn * p.Cn;
-    const int b = live ? (int)(row / p.Cn) : 0, c = live ? (int)(row % p.Cn) : 0, g = c / (p.Cn / p.G);
-    const bool on = live && row_length(p.lens, b, 1) == 1;
-    float h[4] = {0.f, 0.f, 0.f, 0.f}, core = 0.f, u = 0.f;
-    if (live && p.h0 != nullptr) load_states(p.h0 + row * p.N, n0, p.N, h);
-    if (on) {
-        u = to_f32(static_cast<const T *>(p.u)[(size_t)b * p.ldu + c]);
-        const float d = softplus_full(to_f32(static_cast<const T *>(p.dt)[(size_t)b * p.lddt + c]) +
-                                      (p.dt_bias != nullptr ? p.dt_bias[c] : 0.f));
-        const T *Bm = static_cast<const T *>(p.B) + (size_t)b * p.ldB + g * p.N;
-        const T *Cm = static_cast<const T *>(p.C) + (size_t)b * p.ldC + g * p.N;
-        float al[4];
-        load_states(p.A_log + (size_t)c * p.N, n0, p.N, al);
+__global__ void __launch_bounds__(256) scan_step_kernel(ScanParams p, bool vec) {
+    const int lane = threadIdx.x & 31, j = threadIdx.x % LPC, n0 = 4 * j, mine = j & 3, base = lane & ~(LPC - 1);
+    const int c = (int)((blockIdx.x * 256 + threadIdx.x) / LPC), b0 = blockIdx.y * 4;
+    const bool live = c < p.Cn;
+    const int cc = live ? c : 0, g = p.G == 1 ? 0 : cc / (p.Cn / p.G);
+    float h[4][4], Bv[4][4], Cv[4][4];
+    bool on[4];
+    const size_t state = (size_t)p.Cn * p.N, first = (size_t)b0 * state + (size_t)cc * p.N + n0;
+    const T *Bm = static_cast<const T *>(p.B) + (size_t)b0 * p.ldB + g * p.N + n0;
+    const T *Cm = static_cast<const T *>(p.C) + (size_t)b0 * p.ldC + g * p.N + n0;
+    if (vec && b0 + 4 <= p.Bn && p.lens == nullptr && p.h0 != nullptr && (p.N & 3) == 0 && n0 < p.N) {
+        // four whole rows: all loads in flight at once
+        Raw<T, 4> rb[4], rc[4];
+        float4 rh[4];
+#pragma unroll
+        for (int r = 0; r < 4; ++r) rh[r] = __ldcs(reinterpret_cast<const float4 *>(p.h0 + first + r * state));
+#pragma unroll
+        for (int r = 0; r < 4; ++r) {
+            rb[r] = load_raw<T, 4>(Bm + r * p.ldB);
+            rc[r] = load_raw<T, 4>(Cm + r * p.ldC);
+            on[r] = live;
+        }
+#pragma unroll
+        for (int r = 0; r < 4; ++r) {
+            unpack<T, 4>(rb[r], Bv[r]);
+            unpack<T, 4>(rc[r], Cv[r]);
+            h[r][0] = rh[r].x; h[r][1] = rh[r].y; h[r][2] = rh[r].z; h[r][3] = rh[r].w;
+        }
+    } else {
+#pragma unroll
+        for (int r = 0; r < 4; ++r) {
+            const bool row = live && b0 + r < p.Bn;
+            on[r] = row && row_length(p.lens, b0 + r, 1) == 1;
+#pragma unroll
+            for (int k = 0; k < 4; ++k) {
+                const bool in = n0 + k < p.N;
+                h[r][k] = Bv[r][k] = Cv[r][k] = 0.f;
+                if (row && in && p.h0 != nullptr) h[r][k] = p.h0[first + r * state + k];
+                if (on[r] && in) {
+                    Bv[r][k] = to_f32(Bm[r * p.ldB + k]);
+                    Cv[r][k] = to_f32(Cm[r * p.ldC + k]);
+                }
+            }
+        }
+    }
+    const int bm = b0 + mine;
+    const bool on_m = live && bm < p.Bn && row_length(p.lens, bm, 1) == 1;
+    float u = 0.f, z = 0.f, d = 0.f, A2[4];
+    if (on_m) {
+        u = to_f32(static_cast<const T *>(p.u)[(size_t)bm * p.ldu + cc]);
+        if (p.z != nullptr) z = to_f32(static_cast<const T *>(p.z)[(size_t)bm * p.ldz + cc]);
+        d = softplus_full(to_f32(static_cast<const T *>(p.dt)[(size_t)bm * p.lddt + cc]) + (p.dt_bias != nullptr ? p.dt_bias[cc] : 0.f));
+    }
+    load_states(p.A_log + (size_t)cc * p.N, n0, p.N, A2);
+#pragma unroll
+    for (int k = 0; k < 4; ++k) A2[k] = n0 + k < p.N ? -expf(A2[k]) * kLog2e : 0.f;
+    float core[4];
+#pragma unroll
+    for (int r = 0; r < 4; ++r) {
+        const float dr = __shfl_sync(kFullMask, d, base + r), xu = __shfl_sync(kFullMask, d * u, base + r);
+        core[r] = 0.f;
+        if (!on[r]) continue;                          // the same for all lanes of a channel
 #pragma unroll
         for (int k = 0; k < 4; ++k) {
-            if (n0 + k >= p.N) break;
-            h[k] = fmaf(ex2(fmaf(-expf(al[k]) * kLog2e, d, kExp2Centre)), h[k], d * u * to_f32(Bm[n0 + k]));
-            core = fmaf(to_f32(Cm[n0 + k]), h[k], core);
+            h[r][k] = fmaf(ex2(fmaf(A2[k], dr, kExp2Centre)), h[r][k], xu * Bv[r][k]);
+            core[r] = fmaf(Cv[r][k], h[r][k], core[r]);
         }
     }
-    core = lane_sum<LPC>(core);
+    const float sum = lane_sum4<LPC>(core, lane);
     if (!live) return;
-    if (n0 == 0) {
+    if (j < 4 && bm < p.Bn) {
         float y = 0.f;
-        if (on) {
-            y = core + (p.D != nullptr ? p.D[c] * u : 0.f);
-            if (p.z != nullptr) y *= silu_hw(to_f32(static_cast<const T *>(p.z)[(size_t)b * p.ldz + c]));
+        if (on_m) {
+            y = sum + (p.D != nullptr ? p.D[cc] * u : 0.f);
+            if (p.z != nullptr) y *= silu_hw(z);
         }
-        static_cast<T *>(p.y)[row] = from_f32<T>(y);
+        static_cast<T *>(p.y)[(size_t)bm * p.Cn + cc] = from_f32<T>(y);
     }
-    if (p.h_T != nullptr) store_states(p.h_T + row * p.N, n0, p.N, h);
+    if (p.h_T == nullptr) return;
+#pragma unroll
+    for (int r = 0; r < 4; ++r)
+        if (b0 + r < p.Bn) store_states(p.h_T + first - n0 + r * state, n0, p.N, h[r]);
 }
 
 __global__ void __launch_bounds__(256) scan_combine_kernel(ScanParams p, const float *start, float *out, bool reverse) {
@@ -284,11 +333,23 @@ __global__ void __launch_bounds__(256) scan_combine_kernel(ScanParams p, const f
     const size_t bc = i / p.N;
     const float A2 = -expf(p.A_log[(bc % p.Cn) * p.N + i % p.N]) * kLog2e;
     float X = start != nullptr ? start[i] : 0.f;
-    for (int k = 0; k < p.segs; ++k) {
-        const int s = reverse ? p.segs - 1 - k : k;
-        const float own = p.seg_state[(size_t)s * n + i];
-        p.seg_state[(size_t)s * n + i] = X;
-        X = fmaf(ex2(A2 * p.seg_sum[(size_t)s * p.Bn * p.Cn + bc]), X, own);
+    constexpr int U = 8;                               // segments loaded together
+    for (int k0 = 0; k0 < p.segs; k0 += U) {
+        float own[U], decay[U];
+#pragma unroll
+        for (int k = 0; k < U; ++k) {
+            const int s = reverse ? p.segs - 1 - k0 - k : k0 + k;
+            if (k0 + k >= p.segs) break;
+            own[k] = p.seg_state[(size_t)s * n + i];
+            decay[k] = p.seg_sum[(size_t)s * p.Bn * p.Cn + bc];
+        }
+#pragma unroll
+        for (int k = 0; k < U; ++k) {
+            const int s = reverse ? p.segs - 1 - k0 - k : k0 + k;
+            if (k0 + k >= p.segs) break;
+            p.seg_state[(size_t)s * n + i] = X;
+            X = fmaf(ex2(A2 * decay[k]), X, own[k]);
+        }
     }
     if (out != nullptr) out[i] = X;
 }
@@ -310,10 +371,11 @@ int scan_blocks(int C, int G, int N) {
     return (per + ch - 1) / ch;
 }
 
-// A split sequence is walked twice (the first pass costs the forward about 0.7 of the second, the
-// backward about 0.3), so it is split only where its CTAs leave the SMs short of warps: the forward
-// below half a CTA of 8 warps per SM, the backward below three of 4 warps, into segments of at least
-// 8 tiles.
+// A split sequence is walked twice (the first pass costs the forward 0.65 of the second, the backward
+// 0.2), so it is split only where its CTAs leave the SMs short of warps: the forward below half a CTA
+// per SM, the backward below two, into about three (five) CTAs per SM. A segment has at least 4 (2)
+// tiles: with few channels each tile is a latency of some microseconds, which shorter segments hide
+// (3 x 333 steps of 518 x 11 states, forward and backward: 147 us with 8 tiles, 86 us with 2 to 4).
 void scan_split(ScanParams *p, bool bwd) {
     const long long ctas = (long long)p->Bn * p->G * scan_blocks(p->Cn, p->G, p->N);
     const int tiles = (p->T + kScanTile - 1) / kScanTile;
@@ -321,7 +383,8 @@ void scan_split(ScanParams *p, bool bwd) {
     int segs = 1;
     if (ctas < below && tiles >= 16) {
         segs = (int)((want + ctas - 1) / ctas);
-        if (segs > tiles / 8) segs = tiles / 8;
+        const int most = tiles / (bwd ? 2 : 4);
+        if (segs > most) segs = most;
     }
     const int per = (tiles + segs - 1) / segs;
     p->seg_len = per * kScanTile;
@@ -350,9 +413,10 @@ cudaError_t scan_fwd_prompt(const ScanParams &p, cudaStream_t s) {
 template <int LPC, typename T>
 cudaError_t scan_fwd_launch(const ScanParams &p, cudaStream_t s) {
     if (p.T == 1 && p.ckpt == nullptr) {
-        const size_t n = (size_t)p.Bn * p.Cn * LPC;
+        const size_t a = 4 * sizeof(T);
+        const bool vec = p.N % 4 == 0 && p.ldB % 4 == 0 && p.ldC % 4 == 0 && (uintptr_t)p.B % a == 0 && (uintptr_t)p.C % a == 0;
         timing_mark("scan_step", 0, s);
-        scan_step_kernel<LPC, T><<<(unsigned)((n + 255) / 256), 256, 0, s>>>(p);
+        scan_step_kernel<LPC, T><<<dim3((unsigned)(((size_t)p.Cn * LPC + 255) / 256), (p.Bn + 3) / 4), 256, 0, s>>>(p, vec);
         timing_mark("scan_step", 1, s);
         return cudaGetLastError();
     }

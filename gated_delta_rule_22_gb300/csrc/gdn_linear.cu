@@ -202,6 +202,8 @@ gemm_kernel(const __grid_constant__ CUtensorMap tmA, const __grid_constant__ CUt
     tc_fence_after();
     const uint32_t tmem = *tmem_slot;
     constexpr int TN = kTileN<T>, TERMS = sizeof(T) == 4 ? 6 : 1;
+    griddep_launch();
+    griddep_wait();                                // the set-up above ran under the previous kernel's end
     if (warp == 0 || warp == 2) {                  // one fetches A, the other B
         uint32_t it = 0;
         bool ok = true;
@@ -691,6 +693,8 @@ __device__ __forceinline__ void store_operand(__nv_bfloat16 *out, size_t plane, 
 }
 template <typename T, int V>
 __global__ void __launch_bounds__(256) linear_pack_kernel(const T *x, long long ld, __nv_bfloat16 *out, int rows, int cols, int cols8) {
+    griddep_launch();
+    griddep_wait();
     const int c = (blockIdx.x * 256 + threadIdx.x) * V;
     if (c >= cols) return;
     const size_t plane = (size_t)rows * cols8;
@@ -721,6 +725,8 @@ template <typename T, int V>
 __global__ void __launch_bounds__(256) linear_dpre_kernel(const T *dy, const T *pre, __nv_bfloat16 *dpre, float *part, int M,
                                                           int N, int N8, int act) {
     __shared__ float sums[4][64 * V];
+    griddep_launch();
+    griddep_wait();
     const int cg = threadIdx.x & 63, rl = threadIdx.x >> 6, n = (blockIdx.x * 64 + cg) * V;
     float s[V] = {};
     if (n < N) {
@@ -762,6 +768,8 @@ __global__ void __launch_bounds__(256) linear_dpre_kernel(const T *dy, const T *
 
 template <typename T>
 __global__ void __launch_bounds__(256) linear_dbias_kernel(const float *part, T *dbias, int slices, int N) {
+    griddep_launch();
+    griddep_wait();
     const int n = blockIdx.x * 32 + threadIdx.x;
     const float s = slice_sum(part, slices, N, blockIdx.x);
     if (threadIdx.x < 32 && n < N) dbias[n] = from_f32<T>(s);
@@ -791,21 +799,22 @@ int pack(const Operand &in, Operand *out, char *ws, int dtype, cudaStream_t s) {
     timing_mark("linear_pack", 0, s);
     auto launch = [&](auto kernel, auto *src, int V) {
         const int cols = (in.cols / V + 255) / 256, most = (kPairs * 2 * 16 + cols - 1) / cols;
-        kernel<<<dim3(cols, in.rows < most ? in.rows : most), 256, 0, s>>>(src, in.ld, to, in.rows, in.cols, cols8);
+        return launch_pdl(kernel, dim3(cols, in.rows < most ? in.rows : most), dim3(256), 0, s, src, in.ld, to, in.rows, in.cols, cols8);
     };
+    cudaError_t e;
     if (dtype == 0) {
         const float *src = static_cast<const float *>(in.p);
-        if (in.cols % 4 == 0 && in.ld % 4 == 0 && (uintptr_t)in.p % 16 == 0) launch(linear_pack_kernel<float, 4>, src, 4);
-        else launch(linear_pack_kernel<float, 1>, src, 1);
+        if (in.cols % 4 == 0 && in.ld % 4 == 0 && (uintptr_t)in.p % 16 == 0) e = launch(linear_pack_kernel<float, 4>, src, 4);
+        else e = launch(linear_pack_kernel<float, 1>, src, 1);
     } else {
         const __nv_bfloat16 *src = static_cast<const __nv_bfloat16 *>(in.p);
-        if (in.cols % 2 == 0 && in.ld % 2 == 0 && (uintptr_t)in.p % 4 == 0) launch(linear_pack_kernel<__nv_bfloat16, 2>, src, 2);
-        else launch(linear_pack_kernel<__nv_bfloat16, 1>, src, 1);
+        if (in.cols % 2 == 0 && in.ld % 2 == 0 && (uintptr_t)in.p % 4 == 0) e = launch(linear_pack_kernel<__nv_bfloat16, 2>, src, 2);
+        else e = launch(linear_pack_kernel<__nv_bfloat16, 1>, src, 1);
     }
     timing_mark("linear_pack", 1, s);
     out->p = to;
     out->ld = cols8;
-    return api_cuda_status(cudaGetLastError());
+    return api_cuda_status(e);
 }
 
 struct Epilogue {
@@ -856,9 +865,10 @@ int gemm(const char *name, const Operand &A, const Operand &B, int M, int N, int
     cudaError_t err = allow_smem<gemm_kernel<A_MN, B_MN, T>>((int)kGemmSmem);
     if (err != cudaSuccess) return api_cuda_status(err);
     timing_mark(name, 0, s);
-    gemm_kernel<A_MN, B_MN, T><<<2 * (p.items < kPairs ? p.items : kPairs), kGemmThreads, kGemmSmem, s>>>(tm[0], tm[1], tm[2], tm[3], p);
+    err = launch_pdl(gemm_kernel<A_MN, B_MN, T>, dim3(2 * (p.items < kPairs ? p.items : kPairs)), dim3(kGemmThreads), kGemmSmem, s, tm[0],
+                     tm[1], tm[2], tm[3], p);
     timing_mark(name, 1, s);
-    return api_cuda_status(cudaGetLastError());
+    return api_cuda_status(err);
 }
 
 constexpr int kStreamRows = 32, kNotTaken = 1;
@@ -954,18 +964,18 @@ int bwd_any(const LinearParams &p, int dtype, cudaStream_t s) {
         const T *dy = static_cast<const T *>(p.dy), *pre = static_cast<const T *>(p.pre_in);
         const int slices = (p.M + 3) / 4 < kBiasSlices ? (p.M + 3) / 4 : kBiasSlices;
         timing_mark("linear_dpre", 0, s);
-        if (p.N % V == 0)
-            linear_dpre_kernel<T, V><<<dim3((p.N + 64 * V - 1) / (64 * V), slices), 256, 0, s>>>(dy, pre, to, part, p.M, p.N, up8(p.N), p.act);
-        else
-            linear_dpre_kernel<T, 1><<<dim3((p.N + 63) / 64, slices), 256, 0, s>>>(dy, pre, to, part, p.M, p.N, up8(p.N), p.act);
+        auto launch = [&](auto kernel, int v) {
+            return launch_pdl(kernel, dim3((p.N + 64 * v - 1) / (64 * v), slices), dim3(256), 0, s, dy, pre, to, part, p.M, p.N, up8(p.N), p.act);
+        };
+        cudaError_t e = p.N % V == 0 ? launch(linear_dpre_kernel<T, V>, V) : launch(linear_dpre_kernel<T, 1>, 1);
         timing_mark("linear_dpre", 1, s);
-        if ((rc = api_cuda_status(cudaGetLastError())) != 0) return rc;
+        if ((rc = api_cuda_status(e)) != 0) return rc;
         if (to != nullptr) d = {to, up8(p.N), p.M, p.N};
         if (p.dbias != nullptr) {
             timing_mark("linear_dbias", 0, s);
-            linear_dbias_kernel<T><<<(p.N + 31) / 32, 256, 0, s>>>(part, static_cast<T *>(p.dbias), slices, p.N);
+            e = launch_pdl(linear_dbias_kernel<T>, dim3((p.N + 31) / 32), dim3(256), 0, s, part, static_cast<T *>(p.dbias), slices, p.N);
             timing_mark("linear_dbias", 1, s);
-            if ((rc = api_cuda_status(cudaGetLastError())) != 0) return rc;
+            if ((rc = api_cuda_status(e)) != 0) return rc;
         }
     }
     if (own_dpre) ws += up256((size_t)(dtype == 0 ? 3 : 1) * p.M * up8(p.N) * 2);

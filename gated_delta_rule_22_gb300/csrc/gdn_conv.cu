@@ -81,8 +81,8 @@ __device__ __forceinline__ void load_taps(const ConvParams &p, int c, float2 (&w
 // A thread's own inputs of the next steps, kBlocks blocks of kStep steps: asynchronous copies into its
 // own places in shared memory (no other thread reads them, so no barrier is needed), which keep some
 // 50 KB per SM in flight without registers. Elements of 2 bytes alone (V = 1, bf16) are below the
-// smallest copy: they are loaded where they are used.
-constexpr int kStep = 4, kBlocks = 2;
+// smallest copy: they are loaded a block ahead into registers.
+constexpr int kStep = 8, kBlocks = 2;
 
 template <typename T, int V, int THREADS>
 struct Ring {
@@ -92,6 +92,8 @@ struct Ring {
     const T *src;
     long long ld;
     int end;              // steps from `end` on read as zeros
+    T now[kAsync ? 1 : kStep], next[kAsync ? 1 : kStep];
+    static_assert(kBlocks == 2, "the register form holds two blocks");
 
     __device__ __forceinline__ Ring(void *smem, const T *src, long long ld, int end)
         : mine(static_cast<Raw<T, V> *>(smem) + threadIdx.x), src(src), ld(ld), end(end) {}
@@ -110,12 +112,19 @@ struct Ring {
                                  "r"(ok ? (int)(V * sizeof(T)) : 0), "n"(V * (int)sizeof(T))
                                  : "memory");
             }
+        } else {
+#pragma unroll
+            for (int i = 0; i < kStep; ++i) {
+                now[i] = next[i];
+                next[i] = from_f32<T>(0.f);
+                if (t + i < end) next[i] = src[(size_t)(t + i) * ld];
+            }
         }
     }
-    // step i of block blk, which begins at step t
-    __device__ __forceinline__ void get(int blk, int i, int t, float (&o)[V]) const {
+    // step i of block blk
+    __device__ __forceinline__ void get(int blk, int i, float (&o)[V]) const {
         if constexpr (kAsync) unpack<T, V>(mine[((blk & (kBlocks - 1)) * kStep + i) * THREADS], o);
-        else load_or_zero<T, V>(src + (size_t)(t + i) * ld, t + i < end, o);
+        else o[0] = to_f32(now[i]);
     }
 };
 
@@ -124,7 +133,7 @@ struct Ring {
 // Threads over (batch row, run of `run` steps, V channels). The thread of a row's first run also
 // writes the state behind the row's last valid step. The next U steps' inputs are loaded before the
 // present ones are used; groups of U steps inside the row and the run take a path without tests.
-template <typename T, int W, int V>
+template <typename T, int W, int V, bool SILU>
 __global__ void __launch_bounds__(kConvThreads, 4) conv_fwd_kernel(ConvParams p, int run, int runs) {
     constexpr int U = kStep, P = kPairs<V>;
     extern __shared__ __align__(16) unsigned char smem[];
@@ -162,7 +171,7 @@ __global__ void __launch_bounds__(kConvThreads, 4) conv_fwd_kernel(ConvParams p,
     }
     auto step = [&](int blk, int i, int tb, bool valid) {
         float o[V], e[V];
-        in.get(blk, i, tb, e);
+        in.get(blk, i, e);
         to_pairs<V>(e, win[W - 1]);
         float2 pre[P];
 #pragma unroll
@@ -172,7 +181,7 @@ __global__ void __launch_bounds__(kConvThreads, 4) conv_fwd_kernel(ConvParams p,
             for (int j = 0; j < W; ++j) pre[q] = __ffma2_rn(w[j][q], win[j][q], pre[q]);
 #pragma unroll
             for (int j = 0; j < W - 1; ++j) win[j][q] = win[j + 1][q];
-            if (p.act == kActSilu) pre[q] = __fmul2_rn(pre[q], sigmoid2_hw(pre[q]));
+            if (SILU) pre[q] = __fmul2_rn(pre[q], sigmoid2_hw(pre[q]));
         }
         from_pairs<V>(pre, o);
         if (!valid)
@@ -200,7 +209,7 @@ __global__ void __launch_bounds__(kConvThreads, 4) conv_fwd_kernel(ConvParams p,
 // stores the inputs from W-1 steps before it on, and the row's last run goes on for W-1 steps behind
 // the row (where dpre is 0). The parameter sums go over a thread's steps, then over the CTA's warps in
 // ascending order, into the CTA's slice of the partial sums: a fixed order.
-template <typename T, int W, int V>
+template <typename T, int W, int V, bool SILU>
 __global__ void __launch_bounds__(32 * kConvBwdWarps, 2) conv_bwd_kernel(ConvParams p, int run, int slices_row) {
     constexpr int U = kStep, P = kPairs<V>;
     using In = Ring<T, V, 32 * kConvBwdWarps>;
@@ -244,7 +253,7 @@ __global__ void __launch_bounds__(32 * kConvBwdWarps, 2) conv_bwd_kernel(ConvPar
                 float2 pre = bias[q];
 #pragma unroll
                 for (int j = 0; j < W; ++j) pre = __ffma2_rn(w[j][q], win[j][q], pre);
-                if (p.act == kActSilu) {              // silu' = s (1 + pre (1 - s))
+                if (SILU) {              // silu' = s (1 + pre (1 - s))
                     const float2 one = make_float2(1.f, 1.f), sg = sigmoid2_hw(pre);
                     const float2 up = __ffma2_rn(pre, __ffma2_rn(sg, make_float2(-1.f, -1.f), one), one);
                     dd[q] = __fmul2_rn(dd[q], __fmul2_rn(sg, up));
@@ -280,8 +289,8 @@ __global__ void __launch_bounds__(32 * kConvBwdWarps, 2) conv_bwd_kernel(ConvPar
         // one step: the sums, and dx of the input W-1 steps back
         auto step = [&](int blk, int i, int tb, bool valid, float (&o)[V]) {
             float e[V], d[V];
-            in_x.get(blk, i, tb, e);
-            in_d.get(blk, i, tb, d);
+            in_x.get(blk, i, e);
+            in_d.get(blk, i, d);
             to_pairs<V>(e, win[W - 1]);
             grad(d, valid);
             float2 s[P];
@@ -365,16 +374,16 @@ bool conv_aligned(const ConvParams &p, int V, size_t e) {
     return p.C % V == 0 && p.ldx % V == 0 && (uintptr_t)p.x % (V * e) == 0;
 }
 
-// Steps per warp of the backward: up to 128, fewer while that leaves under 512 CTAs (3 per SM).
+// Steps per warp of the backward: up to 256, fewer while that leaves under 512 CTAs (3 per SM).
 int conv_bwd_run(const ConvParams &p) {
     int run = (p.T + kConvBwdWarps - 1) / kConvBwdWarps;
-    run = run > 128 ? 128 : run;
+    run = run > 256 ? 256 : run;
     const long long cols = (p.C + 127) / 128;
     while (run > 8 && cols * p.B * ((p.T + kConvBwdWarps * run - 1) / (kConvBwdWarps * run)) < 512) run /= 2;
     return run;
 }
 
-template <typename T, int W, int V>
+template <typename T, int W, int V, bool SILU>
 cudaError_t conv_fwd_launch(const ConvParams &p, cudaStream_t s) {
     // Steps per thread: each run reads W-1 inputs again, so up to 64, fewer while the threads would
     // not fill the SMs.
@@ -386,24 +395,24 @@ cudaError_t conv_fwd_launch(const ConvParams &p, cudaStream_t s) {
     timing_mark("conv_fwd", 0, s);
     constexpr int smem = Ring<T, V, kConvThreads>::kBytes;
     if (smem > 48 * 1024) {
-        const cudaError_t e = allow_smem<conv_fwd_kernel<T, W, V>>(smem);
+        const cudaError_t e = allow_smem<conv_fwd_kernel<T, W, V, SILU>>(smem);
         if (e != cudaSuccess) return e;
     }
-    conv_fwd_kernel<T, W, V><<<(unsigned)((n + kConvThreads - 1) / kConvThreads), kConvThreads, smem, s>>>(p, run, runs);
+    conv_fwd_kernel<T, W, V, SILU><<<(unsigned)((n + kConvThreads - 1) / kConvThreads), kConvThreads, smem, s>>>(p, run, runs);
     timing_mark("conv_fwd", 1, s);
     return cudaGetLastError();
 }
 
-template <typename T, int W, int V>
+template <typename T, int W, int V, bool SILU>
 cudaError_t conv_bwd_launch(const ConvParams &p, cudaStream_t s) {
     const int run = conv_bwd_run(p), slices_row = (p.T + kConvBwdWarps * run - 1) / (kConvBwdWarps * run);
     const int slices = p.B * slices_row;
     timing_mark("conv_bwd", 0, s);
     constexpr int ring = 2 * Ring<T, V, 32 * kConvBwdWarps>::kBytes, sums = kConvBwdWarps * (W + 1) * 32 * V * 4;
     constexpr int smem = ring > sums ? ring : sums;
-    cudaError_t e = allow_smem<conv_bwd_kernel<T, W, V>>(smem);
+    cudaError_t e = allow_smem<conv_bwd_kernel<T, W, V, SILU>>(smem);
     if (e != cudaSuccess) return e;
-    conv_bwd_kernel<T, W, V><<<dim3(slices, (p.C + 32 * V - 1) / (32 * V)), 32 * kConvBwdWarps, smem, s>>>(p, run, slices_row);
+    conv_bwd_kernel<T, W, V, SILU><<<dim3(slices, (p.C + 32 * V - 1) / (32 * V)), 32 * kConvBwdWarps, smem, s>>>(p, run, slices_row);
     timing_mark("conv_bwd", 1, s);
     e = cudaGetLastError();
     if (e != cudaSuccess) return e;
@@ -413,23 +422,26 @@ cudaError_t conv_bwd_launch(const ConvParams &p, cudaStream_t s) {
     return cudaGetLastError();
 }
 
-template <typename T, int V>
-cudaError_t conv_fwd_taps(const ConvParams &p, cudaStream_t s) {
-    switch (p.W) {
-        case 1: return conv_fwd_launch<T, 1, V>(p, s);
-        case 2: return conv_fwd_launch<T, 2, V>(p, s);
-        case 3: return conv_fwd_launch<T, 3, V>(p, s);
-        default: return conv_fwd_launch<T, 4, V>(p, s);
-    }
+template <typename T, int W, int V>
+cudaError_t conv_act(const ConvParams &p, bool bwd, cudaStream_t s) {
+    if (bwd) return p.act == kActSilu ? conv_bwd_launch<T, W, V, true>(p, s) : conv_bwd_launch<T, W, V, false>(p, s);
+    return p.act == kActSilu ? conv_fwd_launch<T, W, V, true>(p, s) : conv_fwd_launch<T, W, V, false>(p, s);
 }
 template <typename T, int V>
-cudaError_t conv_bwd_taps(const ConvParams &p, cudaStream_t s) {
+cudaError_t conv_taps(const ConvParams &p, bool bwd, cudaStream_t s) {
     switch (p.W) {
-        case 1: return conv_bwd_launch<T, 1, V>(p, s);
-        case 2: return conv_bwd_launch<T, 2, V>(p, s);
-        case 3: return conv_bwd_launch<T, 3, V>(p, s);
-        default: return conv_bwd_launch<T, 4, V>(p, s);
+        case 1: return conv_act<T, 1, V>(p, bwd, s);
+        case 2: return conv_act<T, 2, V>(p, bwd, s);
+        case 3: return conv_act<T, 3, V>(p, bwd, s);
+        default: return conv_act<T, 4, V>(p, bwd, s);
     }
+}
+
+// Four channels per thread, or two or one where four are not aligned.
+cudaError_t conv_any(const ConvParams &p, int dtype, bool bwd, cudaStream_t s) {
+    if (dtype == 0) return conv_aligned(p, 4, 4) ? conv_taps<float, 4>(p, bwd, s) : conv_taps<float, 1>(p, bwd, s);
+    if (conv_aligned(p, 4, 2)) return conv_taps<__nv_bfloat16, 4>(p, bwd, s);
+    return conv_aligned(p, 2, 2) ? conv_taps<__nv_bfloat16, 2>(p, bwd, s) : conv_taps<__nv_bfloat16, 1>(p, bwd, s);
 }
 
 }  // namespace
@@ -439,14 +451,7 @@ int conv_bwd_slices(const ConvParams &p) {
     return p.B * ((p.T + kConvBwdWarps * run - 1) / (kConvBwdWarps * run));
 }
 
-cudaError_t launch_conv_fwd(const ConvParams &p, int dtype, cudaStream_t s) {
-    if (dtype == 0) return conv_aligned(p, 4, 4) ? conv_fwd_taps<float, 4>(p, s) : conv_fwd_taps<float, 1>(p, s);
-    return conv_aligned(p, 4, 2) ? conv_fwd_taps<__nv_bfloat16, 4>(p, s) : conv_fwd_taps<__nv_bfloat16, 1>(p, s);
-}
-
-cudaError_t launch_conv_bwd(const ConvParams &p, int dtype, cudaStream_t s) {
-    if (dtype == 0) return conv_aligned(p, 4, 4) ? conv_bwd_taps<float, 4>(p, s) : conv_bwd_taps<float, 1>(p, s);
-    return conv_aligned(p, 4, 2) ? conv_bwd_taps<__nv_bfloat16, 4>(p, s) : conv_bwd_taps<__nv_bfloat16, 1>(p, s);
-}
+cudaError_t launch_conv_fwd(const ConvParams &p, int dtype, cudaStream_t s) { return conv_any(p, dtype, false, s); }
+cudaError_t launch_conv_bwd(const ConvParams &p, int dtype, cudaStream_t s) { return conv_any(p, dtype, true, s); }
 
 }  // namespace gdn

@@ -25,12 +25,37 @@ __device__ __forceinline__ float dact_rt(int act, float x) {
     return act == kActSilu ? dsilu_hw(x) : act == kActGelu ? dgelu_f(x) : 1.f;
 }
 
+// Sums over the LPG lanes of a group (a part of a warp; kNormThreads: the CTA, through shared memory,
+// two buffers in turn so that one barrier per sum is enough).
 template <int LPG>
-__device__ __forceinline__ float group_sum(float x) {
+struct GroupSum {
+    int turn = 0;
+    __device__ __forceinline__ float2 operator()(float2 x) {
+        constexpr int W = LPG < 32 ? LPG : 32;
 #pragma unroll
-    for (int m = LPG / 2; m >= 1; m >>= 1) x += __shfl_xor_sync(kFullMask, x, m);
-    return x;
-}
+        for (int m = W / 2; m >= 1; m >>= 1)
+            x = __fadd2_rn(x, make_float2(__shfl_xor_sync(kFullMask, x.x, m), __shfl_xor_sync(kFullMask, x.y, m)));
+        if constexpr (LPG > 32) {
+            __shared__ float2 buf[2][kNormWarps];
+            if ((threadIdx.x & 31) == 0) buf[turn][threadIdx.x >> 5] = x;
+            __syncthreads();
+            x = buf[turn][0];
+#pragma unroll
+            for (int w = 1; w < kNormWarps; ++w) x = __fadd2_rn(x, buf[turn][w]);
+            turn ^= 1;
+        }
+        return x;
+    }
+    __device__ __forceinline__ float operator()(float x) {
+        if constexpr (LPG > 32) {
+            return (*this)(make_float2(x, 0.f)).x;
+        } else {
+#pragma unroll
+            for (int m = LPG / 2; m >= 1; m >>= 1) x += __shfl_xor_sync(kFullMask, x, m);
+            return x;
+        }
+    }
+};
 
 __device__ __forceinline__ float block_sum(float x, float *buf) {
     x = warp_sum(x);
@@ -98,21 +123,22 @@ __device__ __forceinline__ void with_act(int act, F f) {
 }
 
 // Where a lane's elements lie: LPG lanes per group, V neighbouring channels per lane, IT pieces
-// (D <= LPG V IT). A warp takes 32 / LPG groups of a row.
+// (D <= LPG V IT). A warp takes 32 / LPG groups of a row; with LPG = kNormThreads a CTA takes one group.
 template <typename T, int V, int LPG, int IT>
 struct NormLane {
-    static constexpr int E = V * IT;
+    static constexpr int E = V * IT, kGroups = LPG < 32 ? 32 / LPG : 1;    // groups of a warp (or CTA)
+    static constexpr int kRows = LPG <= 32 ? kNormWarps : 1;               // rows that a CTA takes at once
     int g, j;
     size_t col;
     bool ok[IT], full;
     __device__ __forceinline__ explicit NormLane(const NormParams &p) {
-        const int lane = threadIdx.x & 31;
-        g = blockIdx.y * (32 / LPG) + lane / LPG;
+        const int lane = LPG <= 32 ? threadIdx.x & 31 : threadIdx.x;
+        g = blockIdx.y * kGroups + lane / LPG;
         j = lane % LPG;
         col = (size_t)g * p.D + j * V;
 #pragma unroll
         for (int i = 0; i < IT; ++i) ok[i] = g < p.G && (i * LPG + j) * V < p.D;
-        full = p.D == LPG * V * IT && p.G % (32 / LPG) == 0;
+        full = p.D == LPG * V * IT && p.G % kGroups == 0;
     }
     // parameters of the lane's channels (w, b), or `other`
     __device__ __forceinline__ void params(const float *w, float other, Pairs<E> &o) const {
@@ -165,8 +191,9 @@ template <typename T, int V, int LPG, int IT>
 __global__ void __launch_bounds__(kNormThreads) norm_fwd_kernel(NormParams p) {
     constexpr int E = V * IT, P = Pairs<E>::N;
     const NormLane<T, V, LPG, IT> at(p);
-    const int rows = gridDim.x * kNormWarps;
-    int m = blockIdx.x * kNormWarps + (threadIdx.x >> 5);
+    GroupSum<LPG> group_sum;
+    const int rows = gridDim.x * at.kRows;
+    int m = blockIdx.x * at.kRows + (threadIdx.x >> 5) % at.kRows;
     Raw<T, V> rx[IT], rz[IT];
     auto fetch = [&](int row) {
         at.load(p.x, (size_t)row * p.ldx, rx);
@@ -184,7 +211,7 @@ __global__ void __launch_bounds__(kNormThreads) norm_fwd_kernel(NormParams p) {
         if (m + rows < p.M) fetch(m + rows);
         float mean = 0.f;
         if (p.center) {
-            mean = group_sum<LPG>(x.total()) * inv_D;
+            mean = group_sum(x.total()) * inv_D;
 #pragma unroll
             for (int i = 0; i < P; ++i) x.p[i] = __fadd2_rn(x.p[i], make_float2(-mean, -mean));
             at.mask(x);
@@ -192,7 +219,7 @@ __global__ void __launch_bounds__(kNormThreads) norm_fwd_kernel(NormParams p) {
         Pairs<E> sq;
 #pragma unroll
         for (int i = 0; i < P; ++i) sq.p[i] = __fmul2_rn(x.p[i], x.p[i]);
-        const float rstd = 1.f / sqrtf(fmaf(group_sum<LPG>(sq.total()), inv_D, p.eps));
+        const float rstd = 1.f / sqrtf(fmaf(group_sum(sq.total()), inv_D, p.eps));
         if (p.stats != nullptr && at.j == 0 && at.g < p.G)
             *reinterpret_cast<float2 *>(p.stats + 2 * ((size_t)m * p.G + at.g)) = make_float2(mean, rstd);
         with_act(p.act, [&](auto act) {
@@ -216,11 +243,11 @@ __global__ void __launch_bounds__(kNormThreads) norm_fwd_kernel(NormParams p) {
 template <typename T, int V, int LPG, int IT>
 __global__ void __launch_bounds__(kNormThreads) norm_bwd_kernel(NormParams p) {
     constexpr int E = V * IT, P = Pairs<E>::N;
-    __shared__ float sums[2][kNormWarps][32 * E];
     const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
     const NormLane<T, V, LPG, IT> at(p);
-    const int rows = gridDim.x * kNormWarps;
-    int m = blockIdx.x * kNormWarps + warp;
+    GroupSum<LPG> group_sum;
+    const int rows = gridDim.x * at.kRows;
+    int m = blockIdx.x * at.kRows + warp % at.kRows;
     const size_t C = (size_t)p.G * p.D;
     Raw<T, V> rx[IT], rz[IT], ry[IT];
     float2 rs = make_float2(0.f, 0.f);
@@ -272,32 +299,45 @@ __global__ void __launch_bounds__(kNormThreads) norm_bwd_kernel(NormParams p) {
             gx.p[i] = __fmul2_rn(g.p[i], x.p[i]);
         }
         if (p.dz != nullptr) at.store(p.dz, (size_t)m * C, z);
-        const float s1 = p.center ? group_sum<LPG>(g.total()) * inv_D : 0.f, s2 = group_sum<LPG>(gx.total()) * inv_D;
+        const float2 sums = group_sum(make_float2(g.total(), gx.total()));
+        const float s1 = p.center ? sums.x * inv_D : 0.f, s2 = sums.y * inv_D;
 #pragma unroll
         for (int i = 0; i < P; ++i)
             x.p[i] = __fmul2_rn(__fadd2_rn(__ffma2_rn(x.p[i], make_float2(-s2, -s2), g.p[i]), make_float2(-s1, -s1)), make_float2(st.y, st.y));
         at.store(p.dx, (size_t)m * C, x);
     }
+    float *part = p.part + (size_t)blockIdx.x * 2 * C;
+    if constexpr (LPG > 32) {                             // every thread has channels of its own
 #pragma unroll
-    for (int i = 0; i < IT; ++i)
-#pragma unroll
-        for (int v = 0; v < V; ++v) {
-            sums[0][warp][(i * 32 + lane) * V + v] = dw.get(i * V + v);
-            sums[1][warp][(i * 32 + lane) * V + v] = db.get(i * V + v);
+        for (int e = 0; e < E; ++e) {
+            const int c = (e / V * LPG + at.j) * V + e % V;
+            if (!at.ok[e / V]) continue;
+            part[(size_t)at.g * p.D + c] = dw.get(e);
+            part[C + (size_t)at.g * p.D + c] = db.get(e);
         }
-    __syncthreads();
-    for (int k = threadIdx.x; k < 2 * 32 * E; k += kNormThreads) {
-        const int which = k / (32 * E), n = k % (32 * E), i = n / (32 * V), ln = n / V % 32, v = n % V;
-        const int gg = blockIdx.y * (32 / LPG) + ln / LPG, e = (i * LPG + ln % LPG) * V + v;
-        if (gg >= p.G || e >= p.D) continue;
-        float a = 0.f;
+    } else {
+        __shared__ float sums[2][kNormWarps][32 * E];
 #pragma unroll
-        for (int u = 0; u < kNormWarps; ++u) a += sums[which][u][n];
-        p.part[((size_t)blockIdx.x * 2 + which) * C + (size_t)gg * p.D + e] = a;
+        for (int i = 0; i < IT; ++i)
+#pragma unroll
+            for (int v = 0; v < V; ++v) {
+                sums[0][warp][(i * 32 + lane) * V + v] = dw.get(i * V + v);
+                sums[1][warp][(i * 32 + lane) * V + v] = db.get(i * V + v);
+            }
+        __syncthreads();
+        for (int k = threadIdx.x; k < 2 * 32 * E; k += kNormThreads) {
+            const int which = k / (32 * E), n = k % (32 * E), i = n / (32 * V), ln = n / V % 32, v = n % V;
+            const int gg = blockIdx.y * at.kGroups + ln / LPG, e = (i * LPG + ln % LPG) * V + v;
+            if (gg >= p.G || e >= p.D) continue;
+            float a = 0.f;
+#pragma unroll
+            for (int u = 0; u < kNormWarps; ++u) a += sums[which][u][n];
+            part[which * C + (size_t)gg * p.D + e] = a;
+        }
     }
 }
 
-// Groups wider than a warp's registers take: a CTA per row and group, passes over the channels
+// Groups wider than a CTA's registers take: a CTA per row and group, passes over the channels
 // through the caches.
 template <typename T>
 __global__ void __launch_bounds__(kNormThreads) norm_fwd_wide_kernel(NormParams p) {
@@ -403,21 +443,24 @@ __global__ void __launch_bounds__(256) norm_reduce_kernel(NormParams p) {
 
 namespace {
 
-// How a group lies on a warp: V channels per lane, lanes per group, pieces (0: the wide kernels).
+// How a group lies on the lanes: V channels per lane, lanes per group (up to a warp, then a whole CTA),
+// pieces of at most 16 channels in all (0: the wide kernels).
 struct NormGeo {
     int V, lanes, pieces;
 };
 NormGeo norm_geo(int D, int V) {
     NormGeo q = {V, 8, 1};
     while (q.lanes < 32 && q.lanes * V < D) q.lanes *= 2;
-    while (q.pieces < 16 && q.lanes * V * q.pieces < D) q.pieces *= 2;
-    if (q.lanes * V * q.pieces < D || V * q.pieces > 16) q.pieces = 0;
+    if (q.lanes * V < D && D > 512) q.lanes = kNormThreads;
+    while (q.lanes * V * q.pieces < D) q.pieces *= 2;
+    if (V * q.pieces > 16) q.pieces = 0;
     return q;
 }
 
-// Groups and row slices of the grid: about 4 CTAs per SM, at most one warp per row.
-int norm_slices(int M, int sets) {
-    const int most = (M + kNormWarps - 1) / kNormWarps, want = (152 * 4 + sets - 1) / sets;
+// Groups and row slices of the grid: about 4 CTAs per SM, at most one warp (or CTA) per row.
+int norm_slices(int M, int G, const NormGeo &q) {
+    const int sets = q.lanes < 32 ? (G + 32 / q.lanes - 1) / (32 / q.lanes) : G, rows = q.lanes <= 32 ? kNormWarps : 1;
+    const int most = (M + rows - 1) / rows, want = (152 * 4 + sets - 1) / sets;
     return want < most ? want : most;
 }
 
@@ -427,8 +470,8 @@ bool norm_aligned(const NormParams &p, int V, size_t e) {
 
 template <typename T, int V, int LPG, int IT>
 cudaError_t norm_launch(NormParams p, bool bwd, cudaStream_t s) {
-    const int sets = (p.G + 32 / LPG - 1) / (32 / LPG);
-    const dim3 grid(bwd ? p.slices : norm_slices(p.M, sets), sets);
+    const int groups = NormLane<T, V, LPG, IT>::kGroups;
+    const dim3 grid(bwd ? p.slices : norm_slices(p.M, p.G, {V, LPG, IT}), (p.G + groups - 1) / groups);
     const char *name = bwd ? "norm_bwd" : "norm_fwd";
     timing_mark(name, 0, s);
     if (bwd) norm_bwd_kernel<T, V, LPG, IT><<<grid, kNormThreads, 0, s>>>(p);
@@ -437,20 +480,26 @@ cudaError_t norm_launch(NormParams p, bool bwd, cudaStream_t s) {
     return cudaGetLastError();
 }
 
+template <typename T, int V, int LPG>
+cudaError_t norm_pieces(const NormParams &p, const NormGeo &q, bool bwd, cudaStream_t s) {
+    if (q.pieces == 1) return norm_launch<T, V, LPG, 1>(p, bwd, s);
+    if (q.pieces == 2) return norm_launch<T, V, LPG, 2>(p, bwd, s);
+    if constexpr (V <= 4) {
+        if (q.pieces == 4) return norm_launch<T, V, LPG, 4>(p, bwd, s);
+    }
+    if constexpr (V <= 2) {
+        if (q.pieces == 8) return norm_launch<T, V, LPG, 8>(p, bwd, s);
+    }
+    if constexpr (V == 1) {
+        if (q.pieces == 16) return norm_launch<T, V, LPG, 16>(p, bwd, s);
+    }
+    return cudaErrorInvalidValue;
+}
 template <typename T, int V>
 cudaError_t norm_pick(const NormParams &p, const NormGeo &q, bool bwd, cudaStream_t s) {
     if (q.lanes == 8) return norm_launch<T, V, 8, 1>(p, bwd, s);
     if (q.lanes == 16) return norm_launch<T, V, 16, 1>(p, bwd, s);
-    if (q.pieces == 1) return norm_launch<T, V, 32, 1>(p, bwd, s);
-    if (q.pieces == 2) return norm_launch<T, V, 32, 2>(p, bwd, s);
-    if constexpr (V <= 4) {
-        if (q.pieces == 4) return norm_launch<T, V, 32, 4>(p, bwd, s);
-    }
-    if constexpr (V == 1) {
-        if (q.pieces == 8) return norm_launch<T, V, 32, 8>(p, bwd, s);
-        if (q.pieces == 16) return norm_launch<T, V, 32, 16>(p, bwd, s);
-    }
-    return cudaErrorInvalidValue;
+    return q.lanes == 32 ? norm_pieces<T, V, 32>(p, q, bwd, s) : norm_pieces<T, V, kNormThreads>(p, q, bwd, s);
 }
 
 template <typename T>
@@ -471,21 +520,26 @@ cudaError_t norm_wide(const NormParams &p, bool bwd, cudaStream_t s) {
 
 template <typename T>
 cudaError_t norm_any(const NormParams &p, bool bwd, cudaStream_t s) {
-    constexpr int W = sizeof(T) == 2 ? 8 : 4;
-    const bool vec = norm_aligned(p, W, sizeof(T));
-    const NormGeo q = norm_geo(p.D, vec ? W : 1);
+    constexpr int W = sizeof(T) == 2 ? 8 : 4;          // 16 bytes; else pairs, or single channels
+    const int V = norm_aligned(p, W, sizeof(T)) ? W : norm_aligned(p, 2, sizeof(T)) ? 2 : 1;
+    const NormGeo q = norm_geo(p.D, V);
     if (q.pieces == 0) return norm_wide<T>(p, bwd, s);
-    return vec ? norm_pick<T, W>(p, q, bwd, s) : norm_pick<T, 1>(p, q, bwd, s);
+    if constexpr (W == 8) {
+        // 8 channels per lane would leave half of the CTA idle
+        if (V == W && q.lanes == kNormThreads && p.D <= 4 * kNormThreads) return norm_launch<T, 4, kNormThreads, 1>(p, bwd, s);
+    }
+    return V == W ? norm_pick<T, W>(p, q, bwd, s) : V == 2 ? norm_pick<T, 2>(p, q, bwd, s) : norm_pick<T, 1>(p, q, bwd, s);
 }
 
 }  // namespace
 
 // Slices of the rows whose partial dw, db the backward sums. The size query knows no addresses, so
-// the count goes by the widest layout whatever the alignment: 2 partial rows per slice.
+// the count goes by the widest layout that D allows, whatever the alignment.
 int norm_bwd_slices(int M, int G, int D, int dtype) {
-    const NormGeo q = norm_geo(D, D % (dtype == 0 ? 4 : 8) == 0 ? (dtype == 0 ? 4 : 8) : 1);
+    const int W = dtype == 0 ? 4 : 8;
+    const NormGeo q = norm_geo(D, D % W == 0 ? W : D % 2 == 0 ? 2 : 1);
     if (q.pieces == 0) return M < 64 ? M : 64;
-    return norm_slices(M, (G + 32 / q.lanes - 1) / (32 / q.lanes));
+    return norm_slices(M, G, q);
 }
 
 cudaError_t launch_norm_fwd(const NormParams &p, int dtype, cudaStream_t s) {

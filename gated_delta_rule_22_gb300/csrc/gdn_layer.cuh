@@ -170,12 +170,12 @@ __device__ __forceinline__ void softplus_full(float x, float &sp, float &sg) {
     const float r1 = rcp(1.f + e);
     sg = x >= 0.f ? r1 : e * r1;
 }
-// The same for two values at once (packed instructions), without the logistic function.
-__device__ __forceinline__ float2 softplus2_full(float2 x) {
+// The same for two values at once (packed instructions).
+__device__ __forceinline__ float2 softplus2_full(float2 x, float2 &e) {
     const float2 ax = make_float2(fminf(fabsf(x.x), 200.f), fminf(fabsf(x.y), 200.f));
     const float2 l = make_float2(-kLog2e, -kLog2e), hi = __fmul2_rn(ax, l);
     const float2 lo = __ffma2_rn(ax, make_float2(-1.925963033e-8f, -1.925963033e-8f), __ffma2_rn(ax, l, make_float2(-hi.x, -hi.y)));
-    float2 e = make_float2(ex2(hi.x), ex2(hi.y));
+    e = make_float2(ex2(hi.x), ex2(hi.y));
     e = __ffma2_rn(e, __fmul2_rn(lo, make_float2(0.69314718f, 0.69314718f)), e);
     const float2 d = __fadd2_rn(e, make_float2(2.f, 2.f)), r = make_float2(rcp(d.x), rcp(d.y));
     float2 s = __fmul2_rn(e, r);
@@ -188,6 +188,17 @@ __device__ __forceinline__ float2 softplus2_full(float2 x) {
     f = __ffma2_rn(q, f, make_float2(1.f / 3.f, 1.f / 3.f));
     f = __ffma2_rn(q, f, make_float2(1.f, 1.f));
     return __ffma2_rn(__fadd2_rn(s, s), f, make_float2(x.x <= 0.f ? 0.f : x.x, x.y <= 0.f ? 0.f : x.y));
+}
+__device__ __forceinline__ float2 softplus2_full(float2 x) {
+    float2 e;
+    return softplus2_full(x, e);
+}
+// softplus and the logistic function
+__device__ __forceinline__ void softplus2_full(float2 x, float2 &sp, float2 &sg) {
+    float2 e;
+    sp = softplus2_full(x, e);
+    const float2 d = __fadd2_rn(e, make_float2(1.f, 1.f)), r = make_float2(rcp(d.x), rcp(d.y));
+    sg = __fmul2_rn(r, make_float2(x.x >= 0.f ? 1.f : e.x, x.y >= 0.f ? 1.f : e.y));
 }
 __device__ __forceinline__ float softplus_full(float x) {
     float sp, sg;

@@ -362,7 +362,7 @@ cudaError_t launch_scan_combine(const ScanParams &p, const float *start, float *
     return cudaGetLastError();
 }
 
-constexpr int kBwdSplitBelow = 304, kBwdSplitWant = 768, kFwdSplitBelow = 76, kFwdSplitWant = 448;
+constexpr int kRoundsLow = 2, kRoundsHigh = 8;
 
 int scan_lanes(int N) { return N <= 16 ? 4 : N <= 32 ? 8 : 16; }
 
@@ -373,18 +373,26 @@ int scan_blocks(int C, int G, int N) {
 
 // A split sequence is walked twice (the first pass costs the forward 0.65 of the second, the backward
 // 0.2), so it is split only where its CTAs leave the SMs short of warps: the forward below half a CTA
-// per SM, the backward below two, into about three (five) CTAs per SM. A segment has at least 4 (2)
-// tiles: with few channels each tile is a latency of some microseconds, which shorter segments hide
-// (3 x 333 steps of 518 x 11 states, forward and backward: 147 us with 8 tiles, 86 us with 2 to 4).
+// per SM, the backward below two. A segment has at least 4 (2) tiles: with few channels each tile is a
+// latency of some microseconds, which shorter segments hide (3 x 333 steps of 518 x 11 states, forward
+// and backward: 147 us with 8 tiles, 81 us with 2 to 4). Of the counts that give the SMs, which hold two
+// CTAs each, kRoundsLow to kRoundsHigh rounds, the first that fills its last round to 95 percent, else the fullest.
 void scan_split(ScanParams *p, bool bwd) {
     const long long ctas = (long long)p->Bn * p->G * scan_blocks(p->Cn, p->G, p->N);
-    const int tiles = (p->T + kScanTile - 1) / kScanTile;
-    const int below = bwd ? kBwdSplitBelow : kFwdSplitBelow, want = bwd ? kBwdSplitWant : kFwdSplitWant;
+    const int tiles = (p->T + kScanTile - 1) / kScanTile, slots = 304, most = tiles / (bwd ? 2 : 4);
     int segs = 1;
-    if (ctas < below && tiles >= 16) {
-        segs = (int)((want + ctas - 1) / ctas);
-        const int most = tiles / (bwd ? 2 : 4);
-        if (segs > most) segs = most;
+    if (ctas < (bwd ? 304 : 76) && tiles >= 16) {
+        const int low = (int)((kRoundsLow * slots + ctas - 1) / ctas), high = (int)(kRoundsHigh * slots / ctas);
+        double best = 0.0;
+        segs = low < most ? low : most;
+        for (int n = segs; n <= high && n <= most && best < 0.95; ++n) {
+            const long long all = ctas * n, rounds = (all + slots - 1) / slots;
+            const double full = (double)all / (double)(rounds * slots);
+            if (full > best) {
+                best = full;
+                segs = n;
+            }
+        }
     }
     const int per = (tiles + segs - 1) / segs;
     p->seg_len = per * kScanTile;

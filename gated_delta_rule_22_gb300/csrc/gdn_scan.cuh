@@ -33,10 +33,11 @@ struct ScanGeo {
 // exp2 is low by 1.8e-8 to 2.6e-8 on average (measured on [-0.1, -0.001]); a bias adds up over all of
 // those steps, so the argument carries its opposite: the error of dA_log halves, at no cost.
 constexpr float kExp2Centre = 2.5e-8f;
-__device__ __forceinline__ float2 decay2(float d, float2 A2) {
-    const float2 x = __ffma2_rn(make_float2(d, d), A2, make_float2(kExp2Centre, kExp2Centre));
+__device__ __forceinline__ float2 decay2(float2 d, float2 A2) {
+    const float2 x = __ffma2_rn(d, A2, make_float2(kExp2Centre, kExp2Centre));
     return make_float2(ex2(x.x), ex2(x.y));
 }
+__device__ __forceinline__ float2 decay2(float d, float2 A2) { return decay2(make_float2(d, d), A2); }
 
 // V staged elements as they were loaded. VEC: one access of V elements where all of them exist; the
 // others one by one. They are turned into floats only where they are used, a tile later: an instruction

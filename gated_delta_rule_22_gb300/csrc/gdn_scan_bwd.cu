@@ -21,7 +21,7 @@ namespace gdn {
 
 namespace {
 
-constexpr int kRevThreads = 128, kRevWarps = kRevThreads / 32, kHalf = kScanTile / 2, kRevCtas = 3;
+constexpr int kRevThreads = 128, kRevWarps = kRevThreads / 32, kHalf = kScanTile / 2, kRevCtas = 2;
 
 // The order of a lane's states: register k holds state n0 + (k ^ order).
 template <int LPC>
@@ -51,9 +51,19 @@ struct BwdSmem {
     T u[TT][CH], z[TT][CH], dy[TT][CH];
 };
 
-// V floats from or to shared memory (aligned to V floats)
+// V floats from shared memory (aligned to V floats)
 template <int V>
 __device__ __forceinline__ void lds(const float *p, float (&o)[V]) { load_vec<float, V>(p, o); }
+// the pairs (x, x) of two neighbouring values
+__device__ __forceinline__ void lds_pairs(const float *p, float2 (&o)[2]) {
+    const float2 x = *reinterpret_cast<const float2 *>(p);
+    o[0] = both(x.x);
+    o[1] = both(x.y);
+}
+__device__ __forceinline__ float2 dsilu2_hw(float2 x) {
+    const float2 one = make_float2(1.f, 1.f), s = sigmoid2_hw(x);
+    return __fmul2_rn(s, __ffma2_rn(x, __ffma2_rn(s, make_float2(-1.f, -1.f), one), one));
+}
 
 }  // namespace
 
@@ -166,12 +176,27 @@ __global__ void __launch_bounds__(kRevThreads, kRevCtas) scan_bwd_kernel(ScanPar
             if (!LITE) ru[i].get(uu);
             if (p.z != nullptr) rz[i].get(zz);
             lds<V>(sm.bias + cv, bias);
+            if constexpr (V == 1) {
+                softplus_full(dd[0] + bias[0], dd[0], sg[0]);
+                dc[0] = p.z != nullptr ? yy[0] * silu_hw(zz[0]) : yy[0];
+            } else {
+#pragma unroll
+                for (int v = 0; v < V; v += 2) {
+                    float2 sp, s2, c2 = make_float2(yy[v], yy[v + 1]);
+                    softplus2_full(make_float2(dd[v] + bias[v], dd[v + 1] + bias[v + 1]), sp, s2);
+                    if (p.z != nullptr) {
+                        const float2 z2 = make_float2(zz[v], zz[v + 1]);
+                        c2 = __fmul2_rn(c2, __fmul2_rn(z2, sigmoid2_hw(z2)));
+                    }
+                    dd[v] = sp.x; dd[v + 1] = sp.y;
+                    sg[v] = s2.x; sg[v + 1] = s2.y;
+                    dc[v] = c2.x; dc[v + 1] = c2.y;
+                }
+            }
 #pragma unroll
             for (int v = 0; v < V; ++v) {
-                softplus_full(dd[v] + bias[v], dd[v], sg[v]);
                 if (t >= L) dd[v] = 0.f;
                 if (LITE) sum_d[v] += dd[v];
-                dc[v] = p.z != nullptr ? yy[v] * silu_hw(zz[v]) : yy[v];
                 xu[v] = dd[v] * uu[v];
             }
             store_vec<float, V>(&sm.d[st][cv], dd);
@@ -206,29 +231,32 @@ __global__ void __launch_bounds__(kRevThreads, kRevCtas) scan_bwd_kernel(ScanPar
             for (int i = TT - 1; i >= 0; --i) {
                 const float4 c4 = lds4(&sm.C[i][order][n0]);
                 const float2 c2[2] = {make_float2(c4.x, c4.y), make_float2(c4.z, c4.w)};
-                float d[2], dc[2];
-                lds<2>(&sm.d[i][cb], d);
-                lds<2>(&sm.dc[i][cb], dc);
+                float2 d[2], dc[2];
+                lds_pairs(&sm.d[i][cb], d);
+                lds_pairs(&sm.dc[i][cb], dc);
 #pragma unroll
                 for (int r = 0; r < 2; ++r)
 #pragma unroll
                     for (int k = 0; k < 2; ++k)
-                        ge[r][k] = __fmul2_rn(__ffma2_rn(both(dc[r]), c2[k], ge[r][k]), decay2(d[r], A2[r][k]));
+                        ge[r][k] = __fmul2_rn(__ffma2_rn(dc[r], c2[k], ge[r][k]), decay2(d[r], A2[r][k]));
             }
             __syncthreads();
             continue;
         }
-        auto forward = [&](int i, const float2 (&h)[2][2], float2 (&to)[2][2]) {
+        auto forward = [&](int i, const float2 (&h)[2][2], float2 (&to)[2][2], float2 (&a)[2][2]) {
             const float4 b4 = lds4(&sm.B[i][order][n0]);
             const float2 b2[2] = {make_float2(b4.x, b4.y), make_float2(b4.z, b4.w)};
-            float d[2], xu[2];
-            lds<2>(&sm.d[i][cb], d);
-            lds<2>(&sm.xu[i][cb], xu);
+            float2 d[2], xu[2];
+            lds_pairs(&sm.d[i][cb], d);
+            lds_pairs(&sm.xu[i][cb], xu);
 #pragma unroll
             for (int r = 0; r < 2; ++r)
 #pragma unroll
                 for (int k = 0; k < 2; ++k)
-                    to[r][k] = __ffma2_rn(decay2(d[r], A2[r][k]), h[r][k], __fmul2_rn(both(xu[r]), b2[k]));
+                {
+                    a[r][k] = decay2(d[r], A2[r][k]);
+                    to[r][k] = __ffma2_rn(a[r][k], h[r][k], __fmul2_rn(xu[r], b2[k]));
+                }
         };
         float2 mid[2][2], tile_dA[2][2];
 #pragma unroll
@@ -239,16 +267,19 @@ __global__ void __launch_bounds__(kRevThreads, kRevCtas) scan_bwd_kernel(ScanPar
                 tile_dA[r][k] = both(0.f);
             }
 #pragma unroll
-        for (int i = 0; i < kHalf; ++i) forward(i, mid, mid);
+        for (int i = 0; i < kHalf; ++i) {
+            float2 a[2][2];
+            forward(i, mid, mid, a);
+        }
 #pragma unroll 1
         for (int half = 1; half >= 0; --half) {
-            float2 h[kHalf + 1][2][2];
+            float2 h[kHalf + 1][2][2], a[kHalf][2][2];
 #pragma unroll
             for (int r = 0; r < 2; ++r)
 #pragma unroll
                 for (int k = 0; k < 2; ++k) h[0][r][k] = half ? mid[r][k] : start[r][k];
 #pragma unroll
-            for (int i = 0; i < kHalf; ++i) forward(half * kHalf + i, h[i], h[i + 1]);
+            for (int i = 0; i < kHalf; ++i) forward(half * kHalf + i, h[i], h[i + 1], a[i]);
 #pragma unroll
             for (int j = kHalf - 1; j >= 0; --j) {
                 const int i = half * kHalf + j;
@@ -256,21 +287,22 @@ __global__ void __launch_bounds__(kRevThreads, kRevCtas) scan_bwd_kernel(ScanPar
                 const float2 b2[2] = {make_float2(b4.x, b4.y), make_float2(b4.z, b4.w)};
                 const float2 c2[2] = {make_float2(c4.x, c4.y), make_float2(c4.z, c4.w)};
                 float2 gB[2], gC[2];
-                float sums[2][3], d[2], xu[2], dc[2];   // sums: dsu, sum kept A log2 e, C . h
-                lds<2>(&sm.d[i][cb], d);
-                lds<2>(&sm.xu[i][cb], xu);
-                lds<2>(&sm.dc[i][cb], dc);
+                float sums[2][3];                       // dsu, sum kept A log2 e, C . h
+                float2 d[2], xu[2], dc[2];
+                lds_pairs(&sm.d[i][cb], d);
+                lds_pairs(&sm.xu[i][cb], xu);
+                lds_pairs(&sm.dc[i][cb], dc);
 #pragma unroll
                 for (int r = 0; r < 2; ++r) {
                     float2 dsu, kd, core;
 #pragma unroll
                     for (int k = 0; k < 2; ++k) {
-                        const float2 e = __ffma2_rn(both(dc[r]), c2[k], ge[r][k]);
-                        gB[k] = r == 0 ? __fmul2_rn(e, both(xu[r])) : __ffma2_rn(e, both(xu[r]), gB[k]);
-                        gC[k] = r == 0 ? __fmul2_rn(both(dc[r]), h[j + 1][0][k]) : __ffma2_rn(both(dc[r]), h[j + 1][1][k], gC[k]);
-                        ge[r][k] = __fmul2_rn(e, decay2(d[r], A2[r][k]));
+                        const float2 e = __ffma2_rn(dc[r], c2[k], ge[r][k]);
+                        gB[k] = r == 0 ? __fmul2_rn(e, xu[r]) : __ffma2_rn(e, xu[r], gB[k]);
+                        gC[k] = r == 0 ? __fmul2_rn(dc[r], h[j + 1][0][k]) : __ffma2_rn(dc[r], h[j + 1][1][k], gC[k]);
+                        ge[r][k] = __fmul2_rn(e, a[j][r][k]);
                         const float2 kept = __fmul2_rn(ge[r][k], h[j][r][k]);
-                        tile_dA[r][k] = __ffma2_rn(kept, both(d[r]), tile_dA[r][k]);
+                        tile_dA[r][k] = __ffma2_rn(kept, d[r], tile_dA[r][k]);
                         dsu = k == 0 ? __fmul2_rn(e, b2[0]) : __ffma2_rn(e, b2[1], dsu);
                         core = k == 0 ? __fmul2_rn(c2[0], h[j + 1][r][0]) : __ffma2_rn(c2[1], h[j + 1][r][1], core);
                         kd = k == 0 ? __fmul2_rn(kept, A2[r][0]) : __ffma2_rn(kept, A2[r][1], kd);
@@ -342,11 +374,23 @@ __global__ void __launch_bounds__(kRevThreads, kRevCtas) scan_bwd_kernel(ScanPar
             for (int v = 0; v < V; ++v) zz[v] = 0.f;
             if (p.z != nullptr) load_vec<T, V>(&sm.z[st][cv], zz);
             const bool on = t < L;
+            if (p.z != nullptr) {
+                if constexpr (V == 1) {
+                    zz[0] = dsilu_hw(zz[0]);
+                } else {
+#pragma unroll
+                    for (int v = 0; v < V; v += 2) {
+                        const float2 q2 = dsilu2_hw(make_float2(zz[v], zz[v + 1]));
+                        zz[v] = q2.x;
+                        zz[v + 1] = q2.y;
+                    }
+                }
+            }
 #pragma unroll
             for (int v = 0; v < V; ++v) {
                 du[v] = on ? fmaf(dsu[v], d[v], D[v] * dc[v]) : 0.f;
                 ddt[v] = on ? fmaf(dsu[v], uu[v], kd[v] * 0.69314718f) * sg[v] : 0.f;
-                dz[v] = on ? yy[v] * fmaf(D[v], uu[v], core[v]) * dsilu_hw(zz[v]) : 0.f;
+                dz[v] = on ? yy[v] * fmaf(D[v], uu[v], core[v]) * zz[v] : 0.f;
                 sum_D[v] += on ? dc[v] * uu[v] : 0.f;
                 sum_b[v] += ddt[v];
             }

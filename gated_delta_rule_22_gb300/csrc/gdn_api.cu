@@ -936,11 +936,11 @@ const char *gdn_strerror(int code) {
     switch (code) {
         case GDN_OK: return "success";
         case GDN_ERR_INVALID_ARG: return "invalid argument (NULL shape or required pointer, size <= 0, or bad dtype)";
-        case GDN_ERR_MISALIGNED: return "a pointer is not 16-byte aligned";
-        case GDN_ERR_UNSUPPORTED_SHAPE: return "unsupported shape (Hv % Hk, Dk, Dv, chunk or tensor size)";
+        case GDN_ERR_MISALIGNED: return "a pointer is not 16-byte aligned (an input with a row stride: not aligned to its element type)";
+        case GDN_ERR_UNSUPPORTED_SHAPE: return "unsupported shape (Hv % Hk, Dk, Dv, chunk, taps, states, groups or tensor size)";
         case GDN_ERR_BUFFER_TOO_SMALL:
             return "a caller buffer is too small (ckpt_bytes < gdn_ckpt_bytes() or workspace_bytes < "
-                   "gdn_bwd_workspace_bytes())";
+                   "gdn_bwd_workspace_bytes(), or the call's own size query)";
         case GDN_ERR_CUDA: return "CUDA runtime error (see gdn_last_error)";
         case GDN_ERR_TIMEOUT: return "a bounded device-side wait timed out";
         case GDN_ERR_SCRATCH_LIMIT:

@@ -73,7 +73,7 @@ int scan_plan(const gdn_scan_shape *s, gdn::ScanParams *p, bool bwd) {
         (double)s->B * s->C * 16 >= kMaxElements)
         return GDN_ERR_UNSUPPORTED_SHAPE;
     if ((double)s->B * s->G * gdn::scan_blocks(s->C, s->G, s->N) >= 2147483648.0 ||
-        (double)s->B * s->C * s->N >= 2147483648.0 * 32.0 || rows * s->G * 2 * s->N >= 2147483648.0 * 64.0)
+        (double)s->B * s->C * s->N >= 2147483648.0 * 32.0 || rows * s->G * 2 * s->N + (double)s->C * (s->N + 2) >= 2147483647.0 * 32.0)
         return GDN_ERR_UNSUPPORTED_SHAPE;
     p->Bn = s->B; p->T = s->T; p->Cn = s->C; p->N = s->N; p->G = s->G;
     gdn::scan_split(p, bwd);

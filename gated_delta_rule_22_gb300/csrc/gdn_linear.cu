@@ -54,22 +54,32 @@ struct GemmParams {
     int M, N, kblocks, run, act;   // run: K blocks per accumulation
     int mt, nt, panel;          // tiles along m and n (of 256 columns), n tiles walked together
     int whole, halves, edge;    // whole tiles, half tiles, columns of the edge tiles
-    int items;
+    int light, light_edges;     // the first pair of those with the fewest other items, and the edge tiles that go to these alone
     int vec;                    // 16-byte accesses of out, pre and res are aligned
     int a_blocks, b_blocks;     // MN-major operands of whole 64-column blocks
 };
 
+// The n-th item of a pair of CTAs; false behind its last. Whole and half tiles go round; so do the edge
+// tiles, but the first ones only among the pairs that would otherwise end a round earlier.
 template <int TN>
-__device__ __forceinline__ void item_at(const GemmParams &p, int i, int &m0, int &n0, int &BN) {
-    int t = i;
-    BN = TN;
-    if (i >= p.whole + p.halves) {
-        m0 = (i - p.whole - p.halves) * 2 * kBM;
+__device__ __forceinline__ bool item_of(const GemmParams &p, int n, int &m0, int &n0, int &BN) {
+    const int pair = blockIdx.x >> 1, pairs = gridDim.x >> 1, main = p.whole + p.halves;
+    int i = pair + n * pairs;
+    if (i >= main) {
+        const int k = n - (pair < main ? (main - pair + pairs - 1) / pairs : 0), lights = pairs - p.light;   // its k-th edge tile
+        int e = p.edge > 0 ? 0 : p.mt, first = 0;
+        if (pair >= p.light) {
+            first = (p.light_edges - (pair - p.light) + lights - 1) / lights;      // its share of the first ones
+            if (k < first) e = pair - p.light + k * lights;
+        }
+        if (k >= first) e += p.light_edges + pair + (k - first) * pairs;
+        m0 = e * 2 * kBM;
         n0 = p.nt * TN;
         BN = p.edge;
-        return;
+        return e < p.mt;
     }
-    if (i >= p.whole) t = p.whole + (i - p.whole) / 2;
+    BN = TN;
+    const int t = i >= p.whole ? p.whole + (i - p.whole) / 2 : i;
     const int per = p.panel * p.mt, q = t / per, r = t % per, w = min(p.panel, p.nt - q * p.panel);
     m0 = r / w * 2 * kBM;
     n0 = (q * p.panel + r % w) * TN;
@@ -77,6 +87,7 @@ __device__ __forceinline__ void item_at(const GemmParams &p, int i, int &m0, int
         BN = TN / 2;
         n0 += (i - p.whole) % 2 * BN;
     }
+    return true;
 }
 
 // ---- a pair of CTAs (cta_group::2): products issued by the even one read both CTAs' shared memory and
@@ -182,7 +193,7 @@ gemm_kernel(const __grid_constant__ CUtensorMap tmA, const __grid_constant__ CUt
     uint64_t *full = bars, *empty = bars + kStages, *acc_full = bars + 2 * kStages, *acc_empty = acc_full + 2;
     uint32_t *tmem_slot = reinterpret_cast<uint32_t *>(acc_empty + 2);
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
-    const int rank = (int)cta_rank(), pair = blockIdx.x >> 1, pairs = gridDim.x >> 1;
+    const int rank = (int)cta_rank();
     if (threadIdx.x == 0) {
         for (int i = 0; i < kStages; ++i) {
             mbar_init(full + i, 1);
@@ -210,9 +221,8 @@ gemm_kernel(const __grid_constant__ CUtensorMap tmA, const __grid_constant__ CUt
         if (lane == 0) {
             int st = 0;
             uint32_t phase = 1;
-            for (int i = pair; i < p.items && ok; i += pairs) {
-                int m0, n0, BN;
-                item_at<TN>(p, i, m0, n0, BN);
+            int m0, n0, BN;
+            for (int i = 0; ok && item_of<TN>(p, i, m0, n0, BN); ++i) {
                 const int boxes = (BN / 2 + 63) / 64, am = m0 + rank * kBM, bn = n0 + rank * (BN / 2);
                 for (int kr = 0; kr < p.kblocks && ok; kr += p.run)
                 for (int term = 6 - TERMS; term < 6 && ok; ++term) {
@@ -247,9 +257,8 @@ gemm_kernel(const __grid_constant__ CUtensorMap tmA, const __grid_constant__ CUt
             uint32_t n_tile = 0, phase = 0;
             int st = 0;
             bool ok = true;
-            for (int i = pair; i < p.items && ok; i += pairs) {
-                int m0, n0, BN;
-                item_at<TN>(p, i, m0, n0, BN);
+            int m0, n0, BN;
+            for (int i = 0; ok && item_of<TN>(p, i, m0, n0, BN); ++i) {
                 const uint32_t idesc = umma_idesc_t(1, 2 * kBM, BN, A_MN, B_MN);
                 for (int kr = 0; kr < p.kblocks && ok; kr += p.run, ++n_tile) {
                     const int acc = n_tile & 1, steps = min(p.run, p.kblocks - kr) * TERMS;
@@ -288,9 +297,8 @@ gemm_kernel(const __grid_constant__ CUtensorMap tmA, const __grid_constant__ CUt
         const int lr = lane / LPR, lc = lane % LPR * V;
         uint32_t n_tile = 0;
         bool ok = true;
-        for (int i = pair; i < p.items && ok; i += pairs) {
-            int m0, n0, BN;
-            item_at<TN>(p, i, m0, n0, BN);
+        int m0, n0, BN;
+        for (int i = 0; ok && item_of<TN>(p, i, m0, n0, BN); ++i) {
             const int row0 = m0 + rank * kBM + 32 * quarter, chunks = BN / kChunk;
             // the residual and bias of a chunk, loaded a chunk ahead
             Raw<T, V> next_res[LPR], next_bias;
@@ -844,7 +852,11 @@ int gemm(const char *name, const Operand &A, const Operand &B, int M, int N, int
     if (tiles > 0x3fffffffLL) return GDN_ERR_UNSUPPORTED_SHAPE;
     p.halves = TN == kMaxBN && last > 0 && last <= kPairs / 2 ? 2 * last : 0;
     p.whole = (int)tiles - p.halves / 2;
-    p.items = p.whole + p.halves + (p.edge > 0 ? p.mt : 0);
+    const int items = p.whole + p.halves + (p.edge > 0 ? p.mt : 0), pairs = items < kPairs ? items : kPairs;
+    // an edge tile costs about (its columns + 64) / 320 of a whole one: that many fit into a round
+    p.light = (p.whole + p.halves) % pairs;
+    const int room = (pairs - p.light) * (320 / (p.edge + 64));
+    p.light_edges = p.edge == 0 ? 0 : p.mt < room ? p.mt : room;
     const int V = 16 / (int)sizeof(T);
     p.vec = N % V == 0 && (uintptr_t)e.res % 16 == 0 && e.ldres % V == 0;
     CUtensorMap tm[4] = {};                            // A, one box of A, B, one box of B: those in use
@@ -865,7 +877,7 @@ int gemm(const char *name, const Operand &A, const Operand &B, int M, int N, int
     cudaError_t err = allow_smem<gemm_kernel<A_MN, B_MN, T>>((int)kGemmSmem);
     if (err != cudaSuccess) return api_cuda_status(err);
     timing_mark(name, 0, s);
-    err = launch_pdl(gemm_kernel<A_MN, B_MN, T>, dim3(2 * (p.items < kPairs ? p.items : kPairs)), dim3(kGemmThreads), kGemmSmem, s, tm[0],
+    err = launch_pdl(gemm_kernel<A_MN, B_MN, T>, dim3(2 * pairs), dim3(kGemmThreads), kGemmSmem, s, tm[0],
                      tm[1], tm[2], tm[3], p);
     timing_mark(name, 1, s);
     return api_cuda_status(err);

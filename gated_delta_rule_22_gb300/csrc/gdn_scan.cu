@@ -20,7 +20,7 @@ namespace gdn {
 // phases of their own that leave the recurrence idle. Two tiles are in flight; named barriers full[2]
 // (staged) and done[2] (walked) hand them over.
 template <int LPC, typename T, bool VEC, bool LITE>
-__global__ void __launch_bounds__(kScanThreads + kScanHelpers, 2) scan_fwd_kernel(ScanParams p) {
+__global__ void __launch_bounds__(kScanThreads + kScanHelpers, LITE ? 3 : 2) scan_fwd_kernel(ScanParams p) {
     using G = ScanGeo<LPC>;
     constexpr int CH = G::CH, NP = G::NP, V = G::V, TT = kScanTile, ALL = kScanThreads + kScanHelpers;
     constexpr int kFull = 1, kDone = 3;

@@ -69,7 +69,7 @@ __device__ __forceinline__ float2 dsilu2_hw(float2 x) {
 
 // LITE: the segment's start adjoint from a zero end and its sum of d, nothing else.
 template <int LPC, typename T, bool VEC, bool LITE>
-__global__ void __launch_bounds__(kRevThreads, kRevCtas) scan_bwd_kernel(ScanParams p) {
+__global__ void __launch_bounds__(kRevThreads, LITE ? 4 : kRevCtas) scan_bwd_kernel(ScanParams p) {
     using G = ScanGeo<LPC>;
     constexpr int CH = G::CH, NP = G::NP, V = G::V, TT = kScanTile, KB = NP * TT / kRevThreads;
     constexpr int PASS = TT * CH / V / kRevThreads;               // staged groups of V per thread (2)

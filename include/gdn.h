@@ -74,7 +74,8 @@ typedef struct {
 enum {
     GDN_OK = 0,
     GDN_ERR_INVALID_ARG = -1,       /* NULL shape or required pointer, a size <= 0, bad dtype */
-    GDN_ERR_MISALIGNED = -2,        /* a pointer not 16-byte aligned */
+    GDN_ERR_MISALIGNED = -2,        /* a pointer not 16-byte aligned (an input with a row stride: not
+                                       aligned to its element type) */
     GDN_ERR_UNSUPPORTED_SHAPE = -3, /* Hv % Hk != 0, Dk not in {32,64,96,128,160,192,224,256},
                                        Dv % 4 != 0 or Dv > 4096, chunk outside 1..128,
                                        B or Hv > 65535, or a tensor too large to index */
@@ -304,6 +305,8 @@ GDN_API int gdn_gates_bwd(const gdn_shape *shape, const void *a, const void *b, 
  *     used, leave the carried state alone, and their outputs and gradients are written as zeros. A
  *     row of length 0 passes its state through.
  *   - The buffers of a call may not overlap, except where a call says so.
+ *   - Results are bitwise deterministic. How the scan splits a sequence and the projection its sums
+ *     depends on all of a call's sizes, so there a row's last bits may differ between batch sizes.
  * Sizes: every size at least 1; a tensor of 2^40 elements or more, B or G above 65535, or rows
  * (B * T, M) of 2^31 or more are GDN_ERR_UNSUPPORTED_SHAPE.
  */

@@ -382,3 +382,113 @@ def test_refusals_reach_the_caller(gdn):
         gdn.gdn_linear_fwd(x, torch.zeros(4, 8))
     with pytest.raises(ValueError, match="workspace"):
         gdn.gdn_conv_bwd(x, w[:, :4].contiguous(), x, workspace=torch.zeros(1 << 20, dtype=torch.uint8))
+
+
+# --------------------------------------------------------------- offsets beyond 32 bits, more forms
+def test_rows_far_apart(gdn):
+    """Slices of a tensor of more than 2^31 elements: row offsets beyond 32 bits."""
+    wide = torch.empty(40000, 65536, device="cuda", dtype=torch.bfloat16)
+    r = Draw(12, "bf16")
+    far = slice(39990, 40000)
+    x = wide[:, 65536 - 128:]
+    x.copy_(r.normal(40000, 128))
+    y, _ = gdn.gdn_norm_fwd(x, 2)
+    check("norm", {"y": y[far]}, {"y": R.norm(d64(x[far]), 2, None, None, None, "silu", 1e-5, True)})
+    taps = r.normal(128, 4, dtype=torch.float32)
+    y, _ = gdn.gdn_conv_fwd(x[None], taps)
+    ref, _ = R.conv(d64(x[None, 39980:]), d64(taps), None, None, None, "silu")
+    check("conv", {"y": y[:, far]}, {"y": ref[:, -10:]})
+    W = r.normal(72, 128)
+    y, _ = gdn.gdn_linear_fwd(x, W)
+    check("linear", {"y": y[far]}, {"y": R.linear(d64(x[far]), d64(W), None, None, "none")})
+    u, B, C = x[None, :, :64], x[None, :, 64:80].unflatten(2, (1, 16)), x[None, :, 80:96].unflatten(2, (1, 16))
+    A_log = torch.zeros(64, 16, device="cuda") + 1.0
+    y, _, _ = gdn.gdn_scan_fwd(u, u, A_log, B, C)        # decays of about exp(-2): the last steps forget the rest
+    part = [d64(t[:, 39900:]) for t in (u, B, C)]
+    ref, _ = R.scan(part[0], part[0], d64(A_log), part[1], part[2], None, None, None, None, None)
+    check("scan", {"y": y[:, far]}, {"y": ref[:, -10:]})
+
+
+@pytest.mark.parametrize("case", [(30, 2, 1024, "bf16", 0, True, "silu", True, True), (17, 1, 4096, "bf16", 0, False, "gelu", True, True),
+                                  (9, 1, 4096, "f32", 0, True, "silu", False, True), (21, 2, 700, "f32", 2, True, "silu", True, True),
+                                  (40, 3, 66, "bf16", 2, True, "silu", True, True), (5, 1, 5000, "bf16", 0, True, "silu", True, True)], ids=str)
+def test_norm_layouts(gdn, case):
+    """Groups held by a whole CTA, pairs of channels, and groups beyond a CTA's registers."""
+    test_norm(gdn, case)
+
+
+@pytest.mark.parametrize("case", [(20, 3000, 40, "bf16", 0, "silu", True, True), (33, 70, 130, "f32", 0, "gelu", True, True),
+                                  (64, 200, 136, "bf16", 0, "gelu", True, True), (600, 300, 2000, "bf16", 0, "silu", True, False),
+                                  (257, 513, 129, "f32", 0, "none", True, True), (2600, 2056, 320, "bf16", 0, "none", False, False)], ids=str)
+def test_linear_layouts(gdn, case):
+    """Few rows in each of their paddings, tiles of several rounds with halves and edges, float32 runs."""
+    test_linear(gdn, case)
+
+
+def test_linear_gradient_against_differences(gdn):
+    """dx and dW against central differences of the float64 definition along random directions."""
+    r = Draw(21, "f32")
+    x, W, dy = r.normal(65, 70), r.normal(50, 70, scale=0.12), r.normal(65, 50)
+    _, pre = gdn.gdn_linear_fwd(x, W, act="gelu", want_pre=True)
+    d = gdn.gdn_linear_bwd(x, W, dy, pre, act="gelu")
+    f = lambda a, b: (R.linear(a, b, None, None, "gelu") * d64(dy)).sum().item()  # noqa: E731
+    h = 1e-5
+    for name, way in (("dx", d64(r.normal(65, 70))), ("dW", d64(r.normal(50, 70)))):
+        step = (way * h, 0.0) if name == "dx" else (0.0, way * h)
+        numeric = (f(d64(x) + step[0], d64(W) + step[1]) - f(d64(x) - step[0], d64(W) - step[1])) / (2 * h)
+        scale = (torch.linalg.vector_norm(d64(d[name])) * torch.linalg.vector_norm(way)).item()
+        assert abs((d64(d[name]) * way).sum().item() - numeric) <= 1e-5 * scale, name
+
+
+def test_conv_and_norm_gradients_against_differences(gdn):
+    r = Draw(22, "f32")
+    h = 1e-5
+    x, w, b, dy = r.normal(2, 30, 12), r.normal(12, 4), r.normal(12), r.normal(2, 30, 12)
+    d = gdn.gdn_conv_bwd(x, w, dy, b, want_ds0=False)
+    f = lambda **k: (R.conv(k["x"], k["w"], k["bias"], None, None, "silu")[0] * d64(dy)).sum().item()  # noqa: E731
+    cases = [(f, d, dict(x=x, w=w, bias=b))]
+    x, w, b, z, dn = r.normal(20, 96), r.normal(96), r.normal(96), r.normal(20, 96), r.normal(20, 96)
+    _, stats = gdn.gdn_norm_fwd(x, 4, w, b, z)
+    g = lambda **k: (R.norm(k["x"], 4, k["w"], k["b"], k["z"], "silu", 1e-5, True) * d64(dn)).sum().item()  # noqa: E731
+    cases.append((g, gdn.gdn_norm_bwd(x, 4, stats, dn, w, b, z), dict(x=x, w=w, b=b, z=z)))
+    for fn, grads, leaves in cases:
+        leaves = {k: d64(v) for k, v in leaves.items()}
+        for k, v in leaves.items():
+            way = d64(r.normal(*v.shape))
+            numeric = (fn(**{**leaves, k: v + h * way}) - fn(**{**leaves, k: v - h * way})) / (2 * h)
+            got = d64(grads["d" + k])
+            scale = (torch.linalg.vector_norm(got) * torch.linalg.vector_norm(way)).item()
+            assert abs((got * way).sum().item() - numeric) <= 1e-5 * scale, k
+
+
+def test_in_a_cuda_graph(gdn):
+    """The calls capture into a graph (caller's buffers, nothing allocated by the library) and replay."""
+    r = Draw(30, "bf16")
+    x, w = r.normal(4, 1, 256), r.normal(256, 4, dtype=torch.float32)
+    W, s0, h0 = r.normal(264, 256, scale=0.06), r.normal(4, 3, 256), r.normal(4, 256, 16, dtype=torch.float32)
+    A_log, bc = r.normal(256, 16, dtype=torch.float32), r.normal(4, 1, 1, 16)
+
+    def step(s, h):
+        a, _ = gdn.gdn_linear_fwd(x, W, act="silu")
+        b, _ = gdn.gdn_conv_fwd(a[..., :256], w, None, s, s_T=s)
+        c, _, _ = gdn.gdn_scan_fwd(b, b, A_log, bc, bc, h0=h, h_T=h)
+        return gdn.gdn_norm_fwd(c, 4, want_stats=False)[0]
+
+    s1, h1 = s0.clone(), h0.clone()
+    want = [step(s1, h1) for _ in range(3)]
+    s2, h2 = s0.clone(), h0.clone()
+    side = torch.cuda.Stream()
+    side.wait_stream(torch.cuda.current_stream())
+    with torch.cuda.stream(side):
+        step(s2, h2)                                    # warm up: first calls set kernel attributes
+    torch.cuda.current_stream().wait_stream(side)
+    s2.copy_(s0)
+    h2.copy_(h0)
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph):
+        out = step(s2, h2)
+    for k in range(3):
+        graph.replay()
+        torch.cuda.synchronize()
+        assert torch.equal(out, want[k]), k
+    assert torch.equal(s2, s1) and torch.equal(h2, h1)

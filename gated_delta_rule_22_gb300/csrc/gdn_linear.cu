@@ -423,14 +423,25 @@ gemm_kernel(const __grid_constant__ CUtensorMap tmA, const __grid_constant__ CUt
                 } else {
                     const int col = col0 + lane;
                     const float b = bias != nullptr && col < p.N ? to_f32(bias[col]) : 0.f;
-                    for (int r = 0; r < 32 && row0 + r < p.M; ++r) {
-                        if (col >= p.N) continue;
-                        const size_t row = row0 + r;
-                        float o = mine[r * kEpiPitch + lane] + b;
-                        if (pre != nullptr) pre[row * p.N + col] = from_f32<T>(o);
-                        o = act_rt(p.act, o);
-                        if (res != nullptr) o = __fadd_rn(o, to_f32(res[row * p.ldres + col]));
-                        out[row * p.N + col] = from_f32<T>(o);
+                    constexpr int U = 8;               // rows whose residuals are loaded together
+#pragma unroll 1
+                    for (int r0 = 0; r0 < 32 && row0 + r0 < p.M && col < p.N; r0 += U) {
+                        const size_t at = (size_t)(row0 + r0) * p.N + col;
+                        const int rows = min(U, p.M - row0 - r0);
+                        T e[U];
+                        if (res != nullptr)
+#pragma unroll
+                            for (int r = 0; r < U; ++r)
+                                if (r < rows) e[r] = res[(size_t)(row0 + r0 + r) * p.ldres + col];
+#pragma unroll
+                        for (int r = 0; r < U; ++r) {
+                            if (r >= rows) break;
+                            float o = mine[(r0 + r) * kEpiPitch + lane] + b;
+                            if (pre != nullptr) pre[at + (size_t)r * p.N] = from_f32<T>(o);
+                            o = act_rt(p.act, o);
+                            if (res != nullptr) o = __fadd_rn(o, to_f32(e[r]));
+                            out[at + (size_t)r * p.N] = from_f32<T>(o);
+                        }
                     }
                 }
                 __syncwarp();

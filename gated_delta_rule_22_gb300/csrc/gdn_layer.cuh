@@ -138,15 +138,6 @@ __device__ __forceinline__ float gelu_f(float x) { return 0.5f * x * (1.f + erff
 __device__ __forceinline__ float dgelu_f(float x) {
     return fmaf(x, 0.3989422804f * ex2(-0.5f * kLog2e * x * x), 0.5f * (1.f + erff(x * 0.70710678f)));
 }
-// act(x) and act'(x)
-template <int ACT>
-__device__ __forceinline__ float act_f(float x) {
-    return ACT == kActSilu ? silu_hw(x) : ACT == kActGelu ? gelu_f(x) : x;
-}
-template <int ACT>
-__device__ __forceinline__ float dact_f(float x) {
-    return ACT == kActSilu ? dsilu_hw(x) : ACT == kActGelu ? dgelu_f(x) : 1.f;
-}
 // softplus(x) = max(x, 0) + log1p(exp(-|x|)), and the logistic function of x from the same exponential.
 // exp(-|x|): the product with log2 e is carried to twice float32, so that the hardware's exp2 sees no
 // rounded argument. log1p(e) for e in [0, 1]: 2 atanh(e / (2 + e)) by the series of atanh, whose

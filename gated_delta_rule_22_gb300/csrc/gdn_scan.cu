@@ -11,31 +11,48 @@
 
 namespace gdn {
 
+template <int LPC, typename T>
+struct FwdSmem {
+    using G = ScanGeo<LPC>;
+    static constexpr int CH = G::CH, NP = G::NP, TT = kScanTile;
+    float4 dx[2][TT][CH / 2];                         // of two channels: d, d, d u, d u
+    float2 B[2][TT][NP], C[2][TT][NP];                // each value twice
+    float core[2][TT][G::SP];
+    T u[2][TT][CH], z[2][TT][CH];
+};
+
 // LITE: the segment's end state from a zero start and its sum of d, nothing else (first pass over a
 // split sequence).
 //
-// Eight warps hold the states and do nothing but the recurrence; four more stage the tiles (loads a
-// tile ahead, softplus) and finish the outputs. With as few channels as a layer has there are about
-// two state warps per scheduler, which then have the helpers' work to hide their latencies, and no
-// phases of their own that leave the recurrence idle. Two tiles are in flight; named barriers full[2]
-// (staged) and done[2] (walked) hand them over.
+// Four warps hold the states and do nothing but the recurrence; four more stage the tiles (loads a
+// tile ahead, softplus) and finish the outputs, so that the recurrence has no phases in which it
+// idles. Two tiles are in flight; named barriers full[2] (staged) and done[2] (walked) hand them over.
+// A lane's states are pairs over two channels, not over two states: d and d u come as pairs from shared
+// memory, B and C (the same for both) are staged twice, and C . h needs no sum across a pair. With
+// the helpers' work that is 67 instructions per step of 256 states, against 75 with one channel per lane.
+//
+// Measured on 2 x 2048 steps of 4096 channels x 16 states, bf16, with checkpoints: 147 us (5 us of it
+// the clock's), against 153 with one channel per lane; 1 x 4096 steps, split, without checkpoints: 62
+// for the ends, 100 for the outputs (65 and 111). Not the exponentials bind (29 us at 32 per clock and SM)
+// nor the memory (20 us and 10 for checkpoints), but latency: instructions issue in 46 % of the cycles, and
+// leaving out the exponentials, the sums over lanes, softplus, or the outputs takes off 5 % at most each.
+// CTAs per SM: three, with 80 registers, where N <= 16 (8 x 1024 steps of 8192 channels: 411 us, 423
+// with two); two where N is larger (2 x 2048 steps of 4096 x 64: 723 us, 748 with three).
 template <int LPC, typename T, bool VEC, bool LITE>
-__global__ void __launch_bounds__(kScanThreads + kScanHelpers, LITE ? 3 : 2) scan_fwd_kernel(ScanParams p) {
+__global__ void __launch_bounds__(kStateThreads + kScanHelpers, LPC == 4 ? 3 : 2) scan_fwd_kernel(ScanParams p) {
     using G = ScanGeo<LPC>;
-    constexpr int CH = G::CH, NP = G::NP, V = G::V, TT = kScanTile, ALL = kScanThreads + kScanHelpers;
+    constexpr int NP = G::NP, V = G::V, TT = kScanTile, ALL = kStateThreads + kScanHelpers;
     constexpr int kFull = 1, kDone = 3;
-    __shared__ __align__(16) float2 sdx[2][TT][CH];   // d, d u
-    __shared__ __align__(16) float sB[2][TT][NP], sC[2][TT][NP];
-    __shared__ float score[2][TT][G::SP];
-    __shared__ __align__(16) T su[2][TT][CH], sz[2][TT][CH];
+    extern __shared__ __align__(16) unsigned char smem_raw[];
+    FwdSmem<LPC, T> &sm = *reinterpret_cast<FwdSmem<LPC, T> *>(smem_raw);
     const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
     const ScanPlace q = scan_place<LPC>(p);
     if (q.first >= q.last) return;
     const int L = row_length(p.lens, q.b, p.T);
-    if (tid >= kScanThreads) {
-        constexpr int KB = NP * TT / kScanHelpers, PASS = TT * CH / V / kScanHelpers;
-        // staged elements: steps ts and ts + 8 of a tile, V channels from cv
-        const int h = tid - kScanThreads, ts = h >> 4, cv = (h & 15) * V, nv = q.nc - cv;
+    if (tid >= kStateThreads) {
+        constexpr int KB = NP * TT / kScanHelpers, ROWS = kScanHelpers / 16, PASS = TT / ROWS;
+        // staged elements: steps ts, ts + ROWS, ... of a tile, V channels from cv
+        const int h = tid - kStateThreads, ts = h >> 4, cv = (h & 15) * V, nv = q.nc - cv;
         const T *u = static_cast<const T *>(p.u) + (size_t)q.b * p.T * p.ldu + q.c0 + cv;
         const T *dt = static_cast<const T *>(p.dt) + (size_t)q.b * p.T * p.lddt + q.c0 + cv;
         const T *z = static_cast<const T *>(p.z) + (size_t)q.b * p.T * p.ldz + q.c0 + cv;
@@ -47,7 +64,7 @@ __global__ void __launch_bounds__(kScanThreads + kScanHelpers, LITE ? 3 : 2) sca
         auto fetch = [&](int tile) {
 #pragma unroll
             for (int i = 0; i < PASS; ++i) {
-                const int t = tile * TT + ts + 8 * i, n = t < L ? nv : 0;
+                const int t = tile * TT + ts + ROWS * i, n = t < L ? nv : 0;
                 ru[i].load(u + (size_t)t * p.ldu, n);
                 rd[i].load(dt + (size_t)t * p.lddt, n);
                 if (!LITE && p.z != nullptr) rz[i].load(z + (size_t)t * p.ldz, n);
@@ -72,7 +89,7 @@ __global__ void __launch_bounds__(kScanThreads + kScanHelpers, LITE ? 3 : 2) sca
             const int buf = tile & 1;
 #pragma unroll
             for (int i = 0; i < PASS; ++i) {
-                const int st = ts + 8 * i, t = tile * TT + st;
+                const int st = ts + ROWS * i, t = tile * TT + st;
                 float uu[V], dd[V];
                 ru[i].get(uu);
                 rd[i].get(dd);
@@ -90,25 +107,28 @@ __global__ void __launch_bounds__(kScanThreads + kScanHelpers, LITE ? 3 : 2) sca
 #pragma unroll
                     for (int v = 0; v < V; ++v) dd[v] = 0.f;
                 if constexpr (V == 1) {
-                    sdx[buf][st][cv] = make_float2(dd[0], dd[0] * uu[0]);
+                    float *to = reinterpret_cast<float *>(&sm.dx[buf][st][cv / 2]) + (cv & 1);
+                    to[0] = dd[0];
+                    to[2] = dd[0] * uu[0];
                 } else {
 #pragma unroll
                     for (int v = 0; v < V; v += 2)
-                        *reinterpret_cast<float4 *>(&sdx[buf][st][cv + v]) = make_float4(dd[v], dd[v] * uu[v], dd[v + 1], dd[v + 1] * uu[v + 1]);
+                        sm.dx[buf][st][(cv + v) / 2] = make_float4(dd[v], dd[v + 1], dd[v] * uu[v], dd[v + 1] * uu[v + 1]);
                 }
                 if (LITE) {
 #pragma unroll
                     for (int v = 0; v < V; ++v) sum_d[v] += dd[v];
                 } else {
-                    ru[i].keep(&su[buf][st][cv]);
-                    if (p.z != nullptr) rz[i].keep(&sz[buf][st][cv]);
+                    ru[i].keep(&sm.u[buf][st][cv]);
+                    if (p.z != nullptr) rz[i].keep(&sm.z[buf][st][cv]);
                 }
             }
 #pragma unroll
             for (int k = 0; k < KB; ++k) {
                 const int e = h + kScanHelpers * k;
-                sB[buf][e / NP][e % NP] = to_f32(rB[k]);
-                if (!LITE) sC[buf][e / NP][e % NP] = to_f32(rC[k]);
+                const float fb = to_f32(rB[k]), fc = to_f32(rC[k]);
+                sm.B[buf][e / NP][e % NP] = make_float2(fb, fb);
+                if (!LITE) sm.C[buf][e / NP][e % NP] = make_float2(fc, fc);
             }
             if (tile + 1 < q.last) fetch(tile + 1);
             named_bar_arrive(kFull + buf, ALL);
@@ -122,14 +142,14 @@ __global__ void __launch_bounds__(kScanThreads + kScanHelpers, LITE ? 3 : 2) sca
             if (!LITE) {
 #pragma unroll
                 for (int i = 0; i < PASS; ++i) {
-                    const int st = ts + 8 * i, t = tile * TT + st;
+                    const int st = ts + ROWS * i, t = tile * TT + st;
                     if (t >= p.T) continue;
                     float o[V], uu[V], zz[V];
-                    load_vec<T, V>(&su[buf][st][cv], uu);
+                    load_vec<T, V>(&sm.u[buf][st][cv], uu);
 #pragma unroll
-                    for (int v = 0; v < V; ++v) o[v] = fmaf(D[v], uu[v], score[buf][st][cv + v]);
+                    for (int v = 0; v < V; ++v) o[v] = fmaf(D[v], uu[v], sm.core[buf][st][cv + v]);
                     if (p.z != nullptr) {
-                        load_vec<T, V>(&sz[buf][st][cv], zz);
+                        load_vec<T, V>(&sm.z[buf][st][cv], zz);
 #pragma unroll
                         for (int v = 0; v < V; ++v) o[v] *= silu_hw(zz[v]);
                     }
@@ -142,106 +162,106 @@ __global__ void __launch_bounds__(kScanThreads + kScanHelpers, LITE ? 3 : 2) sca
             if (tile + 2 < q.last) stage(tile + 2);
         }
         if (LITE) {
-            // the sum of d over the segment: over a thread's tiles, then over its eight steps of a tile
+            // the sum of d over the segment: over a thread's tiles, then over the threads of a channel
 #pragma unroll
-            for (int v = 0; v < V; ++v) score[0][ts][cv + v] = sum_d[v];
+            for (int v = 0; v < V; ++v) sm.core[0][ts][cv + v] = sum_d[v];
             named_bar_sync(kDone + 2, kScanHelpers);
             for (int cc = h; cc < q.nc; cc += kScanHelpers) {
                 float a = 0.f;
-                for (int i = 0; i < 8; ++i) a += score[0][i][cc];
+                for (int i = 0; i < ROWS; ++i) a += sm.core[0][i][cc];
                 p.seg_sum[((size_t)q.seg * p.Bn + q.b) * p.Cn + q.c0 + cc] = a;
             }
         }
         return;
     }
-    // this lane's states: channel ch, states n0 .. n0 + 3
-    const int ch = warp * G::CPW + lane / LPC, n0 = 4 * (lane % LPC);
-    const bool live = ch < q.nc;
-    const int c = q.c0 + (live ? ch : 0);
-    float2 A2[2], h[2];
-    {
-        float e[4];
+    // this lane's states: n0 .. n0 + 3 of channels ch and ch + 1, as pairs over the channels
+    const int pr = warp * G::CPW + lane / LPC, ch = 2 * pr, n0 = 4 * (lane % LPC);
+    const bool live[2] = {ch < q.nc, ch + 1 < q.nc};
+    const int c[2] = {q.c0 + (live[0] ? ch : 0), q.c0 + (live[1] ? ch + 1 : 0)};
+    const size_t row = (size_t)q.b * p.Cn * p.N, seg_row = (size_t)q.seg * p.Bn * p.Cn * p.N + row;
+    auto load = [&](const float *rows, float2 (&o)[4]) {
+        float e[2][4];
 #pragma unroll
-        for (int k = 0; k < 4; ++k) e[k] = n0 + k < p.N ? -expf(p.A_log[(size_t)c * p.N + n0 + k]) * kLog2e : 0.f;
-        A2[0] = make_float2(e[0], e[1]);
-        A2[1] = make_float2(e[2], e[3]);
-    }
-    const size_t state_row = ((size_t)q.b * p.Cn + c) * p.N;
-    {
-        float e[4] = {0.f, 0.f, 0.f, 0.f};
-        if (!LITE && live) {
-            if (p.segs > 1) load_states(p.seg_state + (size_t)q.seg * p.Bn * p.Cn * p.N + state_row, n0, p.N, e);
-            else if (p.h0 != nullptr) load_states(p.h0 + state_row, n0, p.N, e);
+        for (int r = 0; r < 2; ++r) {
+#pragma unroll
+            for (int k = 0; k < 4; ++k) e[r][k] = 0.f;
+            if (live[r]) load_states(rows + (size_t)c[r] * p.N, n0, p.N, e[r]);
         }
-        h[0] = make_float2(e[0], e[1]);
-        h[1] = make_float2(e[2], e[3]);
+#pragma unroll
+        for (int k = 0; k < 4; ++k) o[k] = make_float2(e[0][k], e[1][k]);
+    };
+    auto store = [&](float *rows, const float2 (&o)[4]) {
+        const float e[2][4] = {{o[0].x, o[1].x, o[2].x, o[3].x}, {o[0].y, o[1].y, o[2].y, o[3].y}};
+#pragma unroll
+        for (int r = 0; r < 2; ++r)
+            if (live[r]) store_states(rows + (size_t)c[r] * p.N, n0, p.N, e[r]);
+    };
+    float2 A2[4], h[4];
+    load(p.A_log, A2);
+#pragma unroll
+    for (int k = 0; k < 4; ++k) {
+        A2[k] = n0 + k < p.N ? make_float2(-expf(A2[k].x) * kLog2e, -expf(A2[k].y) * kLog2e) : make_float2(0.f, 0.f);
+        h[k] = make_float2(0.f, 0.f);
+    }
+    if (!LITE) {
+        if (p.segs > 1) load(p.seg_state + seg_row, h);
+        else if (p.h0 != nullptr) load(p.h0 + row, h);
     }
     const int tiles = (p.T + TT - 1) / TT;
     for (int tile = q.first; tile < q.last; ++tile) {
         const int buf = tile & 1;
-        if (!LITE && p.ckpt != nullptr && live) {
-            const float o[4] = {h[0].x, h[0].y, h[1].x, h[1].y};
-            store_states(p.ckpt + (((size_t)q.b * tiles + tile) * p.Cn + c) * p.N, n0, p.N, o);
-        }
+        if (!LITE && p.ckpt != nullptr) store(p.ckpt + ((size_t)q.b * tiles + tile) * p.Cn * p.N, h);
         named_bar_sync(kFull + buf, ALL);
-        // four steps at a time: what does not depend on the state (decays, d u B) is formed for the next
-        // four before the chain of the present four, whose only latency is one multiply-add per step
-        struct Group {
-            float2 a[4][2], x[4][2], c[4][2];
+        // what does not depend on the state (decays, d u B) is formed for the next step before the
+        // present one's multiply-adds
+        struct Step {
+            float2 a[4], x[4];
         };
-        auto prepare = [&](int i0, Group &o) {
+        auto prepare = [&](int i, Step &o) {
+            const float4 dx = sm.dx[buf][i][pr];
+            const float4 *b4 = reinterpret_cast<const float4 *>(&sm.B[buf][i][n0]);
+            const float4 b01 = b4[0], b23 = b4[1];
+            const float2 b2[4] = {make_float2(b01.x, b01.y), make_float2(b01.z, b01.w), make_float2(b23.x, b23.y),
+                                  make_float2(b23.z, b23.w)};
 #pragma unroll
-            for (int i = 0; i < 4; ++i) {
-                const float2 dx = sdx[buf][i0 + i][ch];
-                const float4 b4 = *reinterpret_cast<const float4 *>(&sB[buf][i0 + i][n0]);
-                const float2 b2[2] = {make_float2(b4.x, b4.y), make_float2(b4.z, b4.w)};
-#pragma unroll
-                for (int k = 0; k < 2; ++k) {
-                    o.a[i][k] = decay2(dx.x, A2[k]);
-                    o.x[i][k] = __fmul2_rn(make_float2(dx.y, dx.y), b2[k]);
-                }
-                if (!LITE) {
-                    const float4 c4 = *reinterpret_cast<const float4 *>(&sC[buf][i0 + i][n0]);
-                    o.c[i][0] = make_float2(c4.x, c4.y);
-                    o.c[i][1] = make_float2(c4.z, c4.w);
-                }
+            for (int k = 0; k < 4; ++k) {
+                o.a[k] = decay2(make_float2(dx.x, dx.y), A2[k]);
+                o.x[k] = __fmul2_rn(make_float2(dx.z, dx.w), b2[k]);
             }
         };
-        Group now, then;
+        Step now, then;
+        float2 core[4];
         prepare(0, now);
 #pragma unroll
-        for (int i0 = 0; i0 < TT; i0 += 4) {
-            if (i0 + 4 < TT) prepare(i0 + 4, then);
-            float core[4];
+        for (int i = 0; i < TT; ++i) {
+            if (i + 1 < TT) prepare(i + 1, then);
 #pragma unroll
-            for (int i = 0; i < 4; ++i) {
-                float2 sum;
-#pragma unroll
-                for (int k = 0; k < 2; ++k) {
-                    h[k] = __ffma2_rn(now.a[i][k], h[k], now.x[i][k]);
-                    if (!LITE) sum = k == 0 ? __fmul2_rn(now.c[i][0], h[0]) : __ffma2_rn(now.c[i][1], h[1], sum);
-                }
-                if (!LITE) core[i] = sum.x + sum.y;
-            }
+            for (int k = 0; k < 4; ++k) h[k] = __ffma2_rn(now.a[k], h[k], now.x[k]);
             if (!LITE) {
-                const float r = lane_sum4<LPC>(core, lane);
-                if (lane % LPC < 4) score[buf][i0 + (lane & 3)][ch] = r;
+                const float4 *c4 = reinterpret_cast<const float4 *>(&sm.C[buf][i][n0]);
+                const float4 c01 = c4[0], c23 = c4[1];
+                float2 sum = __fmul2_rn(make_float2(c01.x, c01.y), h[0]);
+                sum = __ffma2_rn(make_float2(c01.z, c01.w), h[1], sum);
+                sum = __ffma2_rn(make_float2(c23.x, c23.y), h[2], sum);
+                core[i & 3] = __ffma2_rn(make_float2(c23.z, c23.w), h[3], sum);
+                if (i % 4 == 3) {
+                    const float2 r = lane_sum4<LPC>(core, lane);
+                    if (lane % LPC < 4) *reinterpret_cast<float2 *>(&sm.core[buf][i - 3 + (lane & 3)][ch]) = r;
+                }
             }
             now = then;
         }
         named_bar_arrive(kDone + buf, ALL);
     }
-    const float out[4] = {h[0].x, h[0].y, h[1].x, h[1].y};
-    if (LITE) {
-        if (live) store_states(p.seg_state + (size_t)q.seg * p.Bn * p.Cn * p.N + state_row, n0, p.N, out);
-    } else if (p.h_T != nullptr && live && q.seg == p.segs - 1) {
-        store_states(p.h_T + state_row, n0, p.N, out);
-    }
+    if (LITE) store(p.seg_state + seg_row, h);
+    else if (p.h_T != nullptr && q.seg == p.segs - 1) store(p.h_T + row, h);
 }
 
 // One step (T = 1): a streaming pass over the states, bound by their bytes (read and written once). LPC
 // lanes take one channel of four batch rows, so that A is formed once for four states; lane r forms
-// row r's d and finishes its output. h_T may be h0.
+// row r's d and finishes its output. h_T may be h0. 64 rows of 4096 channels x 16 states: 10 us, 3.5
+// TB/s (the states' 34 MB stay in L2 from step to step); by the prompt kernel, whose tiles would hold
+// one step of 16, 41 us.
 template <int LPC, typename T>
 __global__ void __launch_bounds__(256) scan_step_kernel(ScanParams p, bool vec) {
     const int lane = threadIdx.x & 31, j = threadIdx.x % LPC, n0 = 4 * j, mine = j & 3, base = lane & ~(LPC - 1);
@@ -373,9 +393,11 @@ int scan_blocks(int C, int G, int N) {
 
 // A split sequence is walked twice (the first pass costs the forward 0.65 of the second, the backward
 // 0.2), so it is split only where its CTAs leave the SMs short of warps: the forward below half a CTA
-// per SM, the backward below two. A segment has at least 4 (2) tiles: with few channels each tile is a
-// latency of some microseconds, which shorter segments hide (3 x 333 steps of 518 x 11 states, forward
-// and backward: 147 us with 8 tiles, 81 us with 2 to 4). Of the counts that give the SMs, which hold two
+// per SM (1 x 4096 steps of 4096 channels x 16 states, 64 CTAs: 175 us split, 275 whole; 2 x 2048 steps,
+// 128 CTAs: 200 split, 151 whole), the backward below two (the latter: 402 us split, 535 whole). A segment
+// has at least 4 (2) tiles: with few channels each tile is a latency of some microseconds, which shorter
+// segments hide (3 x 333 steps of 518 x 11 states, forward and backward: 147 us with 8 tiles, 81 us with 2
+// to 4, 143 whole). Of the counts that give the SMs, which hold two
 // CTAs each, kRoundsLow to kRoundsHigh rounds, the first that fills its last round to 95 percent, else the fullest.
 void scan_split(ScanParams *p, bool bwd) {
     const long long ctas = (long long)p->Bn * p->G * scan_blocks(p->Cn, p->G, p->N);
@@ -401,21 +423,29 @@ void scan_split(ScanParams *p, bool bwd) {
 
 namespace {
 
+template <int LPC, typename T, bool VEC, bool LITE>
+cudaError_t scan_fwd_one(const ScanParams &p, cudaStream_t s) {
+    constexpr int smem = (int)sizeof(FwdSmem<LPC, T>);
+    if (smem > 48 * 1024) {
+        const cudaError_t e = allow_smem<scan_fwd_kernel<LPC, T, VEC, LITE>>(smem);
+        if (e != cudaSuccess) return e;
+    }
+    const dim3 grid(p.Bn * p.G * scan_blocks(p.Cn, p.G, p.N), p.segs);
+    const char *name = LITE ? "scan_fwd_ends" : "scan_fwd";
+    timing_mark(name, 0, s);
+    scan_fwd_kernel<LPC, T, VEC, LITE><<<grid, kStateThreads + kScanHelpers, smem, s>>>(p);
+    timing_mark(name, 1, s);
+    return cudaGetLastError();
+}
+
 template <int LPC, typename T, bool VEC>
 cudaError_t scan_fwd_prompt(const ScanParams &p, cudaStream_t s) {
-    const dim3 grid(p.Bn * p.G * scan_blocks(p.Cn, p.G, p.N), p.segs);
     cudaError_t e;
     if (p.segs > 1) {
-        timing_mark("scan_fwd_ends", 0, s);
-        scan_fwd_kernel<LPC, T, VEC, true><<<grid, kScanThreads + kScanHelpers, 0, s>>>(p);
-        timing_mark("scan_fwd_ends", 1, s);
-        if ((e = cudaGetLastError()) != cudaSuccess) return e;
+        if ((e = scan_fwd_one<LPC, T, VEC, true>(p, s)) != cudaSuccess) return e;
         if ((e = launch_scan_combine(p, p.h0, nullptr, false, s)) != cudaSuccess) return e;
     }
-    timing_mark("scan_fwd", 0, s);
-    scan_fwd_kernel<LPC, T, VEC, false><<<grid, kScanThreads + kScanHelpers, 0, s>>>(p);
-    timing_mark("scan_fwd", 1, s);
-    return cudaGetLastError();
+    return scan_fwd_one<LPC, T, VEC, false>(p, s);
 }
 
 template <int LPC, typename T>

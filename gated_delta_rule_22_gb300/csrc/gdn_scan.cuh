@@ -1,8 +1,8 @@
 // gdn_scan.cuh -- what the selective state space scan's forward and backward kernels share
 // (internal; not part of the C ABI).
 //
-// Layout of the work. The states of one channel lie on LPC neighbouring lanes (4, 8 or 16), four
-// states on each, so that N up to 16, 32 or 64 states take one pass; a CTA holds CH =
+// Layout of the work. The states of two channels lie on LPC neighbouring lanes (4, 8 or 16), four
+// states of each channel on a lane, so that N up to 16, 32 or 64 states take one pass; a CTA holds CH =
 // 256 / LPC channels of one group of one batch row and walks the steps in tiles of 16. The
 // per-step inputs of a tile (d, d u, B, C and in the backward the cotangent) are staged in shared
 // memory as float32: each is read by every lane that needs it as a broadcast, softplus is computed
@@ -13,8 +13,9 @@
 
 namespace gdn {
 
-constexpr int kScanThreads = 256;     // that hold states, in the forward (and the channels of a CTA)
-constexpr int kScanHelpers = 128;     // that stage inputs and finish outputs
+constexpr int kScanThreads = 256;     // lanes of a CTA's channels at four states each
+constexpr int kStateThreads = 128;    // of the forward that hold states: two channels each
+constexpr int kScanHelpers = 128;     // of the forward that stage inputs and finish outputs
 
 __device__ __forceinline__ void named_bar_arrive(int id, int n) {
     asm volatile("bar.arrive %0, %1;" ::"r"(id), "r"(n) : "memory");
@@ -102,6 +103,10 @@ __device__ __forceinline__ void store_states(float *p, int n0, int N, const floa
     }
 }
 
+__device__ __forceinline__ float2 shfl2(float2 v, int m) {
+    return make_float2(__shfl_xor_sync(kFullMask, v.x, m), __shfl_xor_sync(kFullMask, v.y, m));
+}
+
 // Sums four values (steps i0 .. i0 + 3) over the LPC lanes of a channel by exchanging halves: the
 // lanes with lane % 4 = j get the sum of value j.
 template <int LPC>
@@ -115,12 +120,15 @@ __device__ __forceinline__ float lane_sum4(const float (&v)[4], int lane) {
     return r;
 }
 
-// Sum over the LPC lanes of a channel.
 template <int LPC>
-__device__ __forceinline__ float lane_sum(float x) {
+__device__ __forceinline__ float2 lane_sum4(const float2 (&v)[4], int lane) {
+    const bool up2 = lane & 2, up1 = lane & 1;
+    const float2 a = __fadd2_rn(up2 ? v[2] : v[0], shfl2(up2 ? v[0] : v[2], 2));
+    const float2 b = __fadd2_rn(up2 ? v[3] : v[1], shfl2(up2 ? v[1] : v[3], 2));
+    float2 r = __fadd2_rn(up1 ? b : a, shfl2(up1 ? a : b, 1));
 #pragma unroll
-    for (int m = LPC / 2; m >= 1; m >>= 1) x += __shfl_xor_sync(kFullMask, x, m);
-    return x;
+    for (int m = 4; m < LPC; m <<= 1) r = __fadd2_rn(r, shfl2(r, m));
+    return r;
 }
 
 // The CTA's place: channels c0 .. c0 + nc of group g of batch row b, segment seg of the steps.

@@ -15,6 +15,12 @@
 // their states, and their two channels, in different order, chosen so that every lane keeps its first
 // registers and sends the others, without selects. Per state and step that takes half of the
 // instructions and of the shared-memory passes that one channel per group takes.
+//
+// Measured on 2 x 2048 steps of 4096 channels x 16 states, bf16, in 7 segments: 67 us for the segments'
+// start adjoints, 319 us for the sweep, 18 and 4 us for the sums and the combination. The sweep issues 217
+// instructions per step of 256 states, in 53 % of the cycles, with two CTAs of 252 registers per SM: it is
+// bound by instructions and their latency, not by its 140 MB. Decays formed twice instead of kept (three
+// CTAs per SM) and segments of any count: 83 us more, forward and backward.
 #include "gdn_scan.cuh"
 
 namespace gdn {
@@ -31,9 +37,6 @@ __device__ __forceinline__ int state_order(int lane) {
     return (lane >> 4 & 1) * 2;
 }
 
-__device__ __forceinline__ float2 shfl2(float2 v, int m) {
-    return make_float2(__shfl_xor_sync(kFullMask, v.x, m), __shfl_xor_sync(kFullMask, v.y, m));
-}
 __device__ __forceinline__ float2 both(float x) { return make_float2(x, x); }
 __device__ __forceinline__ float4 lds4(const float *p) { return *reinterpret_cast<const float4 *>(p); }
 

@@ -10,6 +10,9 @@
 // A thread takes V neighbouring channels (16 bytes) and walks a run of steps with the last W-1
 // inputs in registers, so that x is read once and the taps once per run. Each channel's W products
 // are far below the memory time: the kernels are bound by the bytes of x and y (and dy, dx).
+// Measured on 8 x 4096 steps of 8192 channels, 4 taps, SiLU, bf16: forward 161 us, 6.7 TB/s, a plain
+// copy's rate; backward 290 us, 5.6 TB/s of x, dy and dx, instructions issuing in 53 % of the cycles:
+// it forms pre and its sigmoid again, and adds up W + 1 sums per channel.
 #include "gdn_layer.cuh"
 
 namespace gdn {
@@ -374,7 +377,9 @@ bool conv_aligned(const ConvParams &p, int V, size_t e) {
     return p.C % V == 0 && p.ldx % V == 0 && (uintptr_t)p.x % (V * e) == 0;
 }
 
-// Steps per warp of the backward: up to 256, fewer while that leaves under 512 CTAs (3 per SM).
+// Steps per warp of the backward: up to 256, fewer while that leaves under 512 CTAs (3 per SM). 8 x
+// 4096 steps of 8192 channels: 290 us, 318 with runs of 64, whose first steps are read twice; 4 x 128
+// steps of 1024 channels, where runs are cut to 8: 7 us, 9 uncut.
 int conv_bwd_run(const ConvParams &p) {
     int run = (p.T + kConvBwdWarps - 1) / kConvBwdWarps;
     run = run > 256 ? 256 : run;
@@ -386,7 +391,8 @@ int conv_bwd_run(const ConvParams &p) {
 template <typename T, int W, int V, bool SILU>
 cudaError_t conv_fwd_launch(const ConvParams &p, cudaStream_t s) {
     // Steps per thread: each run reads W-1 inputs again, so up to 64, fewer while the threads would
-    // not fill the SMs.
+    // not fill the SMs. 8 x 4096 steps of 8192 channels: 161 us, 208 with runs of 16; 4 x 128 steps of
+    // 1024 channels, where runs are cut to 1: 6 us, 10 uncut.
     const size_t cv = p.C / V;
     int run = 64;
     while (run > 1 && (size_t)p.B * ((p.T + run - 1) / run) * cv < (size_t)152 * 1024) run /= 2;
@@ -437,7 +443,8 @@ cudaError_t conv_taps(const ConvParams &p, bool bwd, cudaStream_t s) {
     }
 }
 
-// Four channels per thread, or two or one where four are not aligned.
+// Four channels per thread, or two or one where four are not aligned (forward and backward of 8 x 4096
+// steps of 8192 channels: 462 us by fours, 596 by pairs, 1034 one by one).
 cudaError_t conv_any(const ConvParams &p, int dtype, bool bwd, cudaStream_t s) {
     if (dtype == 0) return conv_aligned(p, 4, 4) ? conv_taps<float, 4>(p, bwd, s) : conv_taps<float, 1>(p, bwd, s);
     if (conv_aligned(p, 4, 2)) return conv_taps<__nv_bfloat16, 4>(p, bwd, s);

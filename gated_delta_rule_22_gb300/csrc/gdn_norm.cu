@@ -6,7 +6,9 @@
 //     dxh = daff w,  dx = rstd (dxh - mean(dxh) - xh mean(dxh xh))   (center = 0: no mean(dxh) term)
 //     dw = sum_m daff xh,  db = sum_m daff
 // Bound by memory: x (and z, dy) are read once and stay in registers between the statistics and
-// the output. The mean is subtracted before the squares are summed.
+// the output. The mean is subtracted before the squares are summed. Measured on 32768 rows of 32
+// groups of 128 channels with a gate, bf16: forward 132 us, 6.1 TB/s; backward 243 us, 5.5 TB/s of x, z,
+// dy, dx and dz. 8192 rows of one group of 4096: 41 and 92 us, 4.9 and 3.6 TB/s, a barrier per sum.
 #include "gdn_layer.cuh"
 
 #include <type_traits>
@@ -444,7 +446,8 @@ __global__ void __launch_bounds__(256) norm_reduce_kernel(NormParams p) {
 namespace {
 
 // How a group lies on the lanes: V channels per lane, lanes per group (up to a warp, then a whole CTA),
-// pieces of at most 16 channels in all (0: the wide kernels).
+// pieces of at most 16 channels in all (0: the wide kernels, which read a row again for each sum: 8192
+// rows of 4096 channels, forward and backward, 345 us against 154 with a row in a CTA's registers).
 struct NormGeo {
     int V, lanes, pieces;
 };
@@ -457,7 +460,8 @@ NormGeo norm_geo(int D, int V) {
     return q;
 }
 
-// Groups and row slices of the grid: about 4 CTAs per SM, at most one warp (or CTA) per row.
+// Groups and row slices of the grid: about 4 CTAs per SM, at most one warp (or CTA) per row (32768 rows
+// of 32 x 128 channels, forward and backward: 385 us; 428 with 2 per SM, 393 with 8).
 int norm_slices(int M, int G, const NormGeo &q) {
     const int sets = q.lanes < 32 ? (G + 32 / q.lanes - 1) / (32 / q.lanes) : G, rows = q.lanes <= 32 ? kNormWarps : 1;
     const int most = (M + rows - 1) / rows, want = (152 * 4 + sets - 1) / sets;
@@ -520,7 +524,8 @@ cudaError_t norm_wide(const NormParams &p, bool bwd, cudaStream_t s) {
 
 template <typename T>
 cudaError_t norm_any(const NormParams &p, bool bwd, cudaStream_t s) {
-    constexpr int W = sizeof(T) == 2 ? 8 : 4;          // 16 bytes; else pairs, or single channels
+    // 16 bytes; else pairs (the same case: 431 us against 385), or single channels
+    constexpr int W = sizeof(T) == 2 ? 8 : 4;
     const int V = norm_aligned(p, W, sizeof(T)) ? W : norm_aligned(p, 2, sizeof(T)) ? 2 : 1;
     const NormGeo q = norm_geo(p.D, V);
     if (q.pieces == 0) return norm_wide<T>(p, bwd, s);

@@ -16,7 +16,7 @@ struct FwdSmem {
     using G = ScanGeo<LPC>;
     static constexpr int CH = G::CH, NP = G::NP, TT = kScanTile;
     float4 dx[2][TT][CH / 2];                         // of two channels: d, d, d u, d u
-    float2 B[2][TT][NP], C[2][TT][NP];                // each value twice
+    float B[2][TT][NP], C[2][TT][NP];
     float core[2][TT][G::SP];
     T u[2][TT][CH], z[2][TT][CH];
 };
@@ -27,19 +27,20 @@ struct FwdSmem {
 // Four warps hold the states and do nothing but the recurrence; four more stage the tiles (loads a
 // tile ahead, softplus) and finish the outputs, so that the recurrence has no phases in which it
 // idles. Two tiles are in flight; named barriers full[2] (staged) and done[2] (walked) hand them over.
-// A lane's states are pairs over two channels, not over two states: d and d u come as pairs from shared
-// memory, B and C (the same for both) are staged twice, and C . h needs no sum across a pair. With
-// the helpers' work that is 67 instructions per step of 256 states, against 75 with one channel per lane.
+// A lane holds four states of two channels: what binds is shared memory, whose 16-byte loads take four
+// cycles per warp however many lanes read the same address, and B and C then serve two channels. d and
+// d u come in one load for both and are made pairs in registers: staged in pairs, or B and C twice (pairs
+// over the channels), the loads grow by more than the moves cost (forward of 2 x 2048 steps 147 us
+// against 138; of 4096 x 64 states 723 against 438).
 //
-// Measured on 2 x 2048 steps of 4096 channels x 16 states, bf16, with checkpoints: 147 us (5 us of it
-// the clock's), against 153 with one channel per lane; 1 x 4096 steps, split, without checkpoints: 62
-// for the ends, 100 for the outputs (65 and 111). Not the exponentials bind (29 us at 32 per clock and SM)
-// nor the memory (20 us and 10 for checkpoints), but latency: instructions issue in 46 % of the cycles, and
-// leaving out the exponentials, the sums over lanes, softplus, or the outputs takes off 5 % at most each.
-// CTAs per SM: three, with 80 registers, where N <= 16 (8 x 1024 steps of 8192 channels: 411 us, 423
-// with two); two where N is larger (2 x 2048 steps of 4096 x 64: 723 us, 748 with three).
+// Measured on 2 x 2048 steps of 4096 channels x 16 states, bf16, with checkpoints: 134 us, against 153 with
+// one channel per lane; 1 x 4096 steps, split, without checkpoints: 63 us for the ends, 93 for the outputs.
+// Not the exponentials bind (29 us at 32 per clock and SM) nor the memory (20 us, and 10 for
+// checkpoints), but the loads from shared memory and the latency of one or two state warps per scheduler.
+// Two CTAs per SM: with three, and 80 registers, the split prompt takes 161 us in all instead of 167, but
+// the 128 CTAs of the first case, one per SM at any rate, 160 us instead of 134.
 template <int LPC, typename T, bool VEC, bool LITE>
-__global__ void __launch_bounds__(kStateThreads + kScanHelpers, LPC == 4 ? 3 : 2) scan_fwd_kernel(ScanParams p) {
+__global__ void __launch_bounds__(kStateThreads + kScanHelpers, 2) scan_fwd_kernel(ScanParams p) {
     using G = ScanGeo<LPC>;
     constexpr int NP = G::NP, V = G::V, TT = kScanTile, ALL = kStateThreads + kScanHelpers;
     constexpr int kFull = 1, kDone = 3;
@@ -126,9 +127,8 @@ __global__ void __launch_bounds__(kStateThreads + kScanHelpers, LPC == 4 ? 3 : 2
 #pragma unroll
             for (int k = 0; k < KB; ++k) {
                 const int e = h + kScanHelpers * k;
-                const float fb = to_f32(rB[k]), fc = to_f32(rC[k]);
-                sm.B[buf][e / NP][e % NP] = make_float2(fb, fb);
-                if (!LITE) sm.C[buf][e / NP][e % NP] = make_float2(fc, fc);
+                sm.B[buf][e / NP][e % NP] = to_f32(rB[k]);
+                if (!LITE) sm.C[buf][e / NP][e % NP] = to_f32(rC[k]);
             }
             if (tile + 1 < q.last) fetch(tile + 1);
             named_bar_arrive(kFull + buf, ALL);
@@ -179,30 +179,32 @@ __global__ void __launch_bounds__(kStateThreads + kScanHelpers, LPC == 4 ? 3 : 2
     const bool live[2] = {ch < q.nc, ch + 1 < q.nc};
     const int c[2] = {q.c0 + (live[0] ? ch : 0), q.c0 + (live[1] ? ch + 1 : 0)};
     const size_t row = (size_t)q.b * p.Cn * p.N, seg_row = (size_t)q.seg * p.Bn * p.Cn * p.N + row;
-    auto load = [&](const float *rows, float2 (&o)[4]) {
-        float e[2][4];
+    auto load = [&](const float *rows, float2 (&o)[2][2]) {
 #pragma unroll
         for (int r = 0; r < 2; ++r) {
-#pragma unroll
-            for (int k = 0; k < 4; ++k) e[r][k] = 0.f;
-            if (live[r]) load_states(rows + (size_t)c[r] * p.N, n0, p.N, e[r]);
+            float e[4] = {0.f, 0.f, 0.f, 0.f};
+            if (live[r]) load_states(rows + (size_t)c[r] * p.N, n0, p.N, e);
+            o[r][0] = make_float2(e[0], e[1]);
+            o[r][1] = make_float2(e[2], e[3]);
         }
-#pragma unroll
-        for (int k = 0; k < 4; ++k) o[k] = make_float2(e[0][k], e[1][k]);
     };
-    auto store = [&](float *rows, const float2 (&o)[4]) {
-        const float e[2][4] = {{o[0].x, o[1].x, o[2].x, o[3].x}, {o[0].y, o[1].y, o[2].y, o[3].y}};
+    auto store = [&](float *rows, const float2 (&o)[2][2]) {
 #pragma unroll
-        for (int r = 0; r < 2; ++r)
-            if (live[r]) store_states(rows + (size_t)c[r] * p.N, n0, p.N, e[r]);
+        for (int r = 0; r < 2; ++r) {
+            const float e[4] = {o[r][0].x, o[r][0].y, o[r][1].x, o[r][1].y};
+            if (live[r]) store_states(rows + (size_t)c[r] * p.N, n0, p.N, e);
+        }
     };
-    float2 A2[4], h[4];
+    float2 A2[2][2], h[2][2];
     load(p.A_log, A2);
 #pragma unroll
-    for (int k = 0; k < 4; ++k) {
-        A2[k] = n0 + k < p.N ? make_float2(-expf(A2[k].x) * kLog2e, -expf(A2[k].y) * kLog2e) : make_float2(0.f, 0.f);
-        h[k] = make_float2(0.f, 0.f);
-    }
+    for (int r = 0; r < 2; ++r)
+#pragma unroll
+        for (int k = 0; k < 2; ++k) {
+            const int n = n0 + 2 * k;
+            A2[r][k] = make_float2(n < p.N ? -expf(A2[r][k].x) * kLog2e : 0.f, n + 1 < p.N ? -expf(A2[r][k].y) * kLog2e : 0.f);
+            h[r][k] = make_float2(0.f, 0.f);
+        }
     if (!LITE) {
         if (p.segs > 1) load(p.seg_state + seg_row, h);
         else if (p.h0 != nullptr) load(p.h0 + row, h);
@@ -215,19 +217,19 @@ __global__ void __launch_bounds__(kStateThreads + kScanHelpers, LPC == 4 ? 3 : 2
         // what does not depend on the state (decays, d u B) is formed for the next step before the
         // present one's multiply-adds
         struct Step {
-            float2 a[4], x[4];
+            float2 a[2][2], x[2][2];
         };
         auto prepare = [&](int i, Step &o) {
-            const float4 dx = sm.dx[buf][i][pr];
-            const float4 *b4 = reinterpret_cast<const float4 *>(&sm.B[buf][i][n0]);
-            const float4 b01 = b4[0], b23 = b4[1];
-            const float2 b2[4] = {make_float2(b01.x, b01.y), make_float2(b01.z, b01.w), make_float2(b23.x, b23.y),
-                                  make_float2(b23.z, b23.w)};
+            const float4 dx = sm.dx[buf][i][pr], b4 = *reinterpret_cast<const float4 *>(&sm.B[buf][i][n0]);
+            const float d[2] = {dx.x, dx.y}, x[2] = {dx.z, dx.w};
+            const float2 b2[2] = {make_float2(b4.x, b4.y), make_float2(b4.z, b4.w)};
 #pragma unroll
-            for (int k = 0; k < 4; ++k) {
-                o.a[k] = decay2(make_float2(dx.x, dx.y), A2[k]);
-                o.x[k] = __fmul2_rn(make_float2(dx.z, dx.w), b2[k]);
-            }
+            for (int r = 0; r < 2; ++r)
+#pragma unroll
+                for (int k = 0; k < 2; ++k) {
+                    o.a[r][k] = decay2(d[r], A2[r][k]);
+                    o.x[r][k] = __fmul2_rn(make_float2(x[r], x[r]), b2[k]);
+                }
         };
         Step now, then;
         float2 core[4];
@@ -236,14 +238,16 @@ __global__ void __launch_bounds__(kStateThreads + kScanHelpers, LPC == 4 ? 3 : 2
         for (int i = 0; i < TT; ++i) {
             if (i + 1 < TT) prepare(i + 1, then);
 #pragma unroll
-            for (int k = 0; k < 4; ++k) h[k] = __ffma2_rn(now.a[k], h[k], now.x[k]);
+            for (int r = 0; r < 2; ++r)
+#pragma unroll
+                for (int k = 0; k < 2; ++k) h[r][k] = __ffma2_rn(now.a[r][k], h[r][k], now.x[r][k]);
             if (!LITE) {
-                const float4 *c4 = reinterpret_cast<const float4 *>(&sm.C[buf][i][n0]);
-                const float4 c01 = c4[0], c23 = c4[1];
-                float2 sum = __fmul2_rn(make_float2(c01.x, c01.y), h[0]);
-                sum = __ffma2_rn(make_float2(c01.z, c01.w), h[1], sum);
-                sum = __ffma2_rn(make_float2(c23.x, c23.y), h[2], sum);
-                core[i & 3] = __ffma2_rn(make_float2(c23.z, c23.w), h[3], sum);
+                const float4 c4 = *reinterpret_cast<const float4 *>(&sm.C[buf][i][n0]);
+                float2 sum[2];
+#pragma unroll
+                for (int r = 0; r < 2; ++r)
+                    sum[r] = __ffma2_rn(make_float2(c4.z, c4.w), h[r][1], __fmul2_rn(make_float2(c4.x, c4.y), h[r][0]));
+                core[i & 3] = make_float2(sum[0].x + sum[0].y, sum[1].x + sum[1].y);
                 if (i % 4 == 3) {
                     const float2 r = lane_sum4<LPC>(core, lane);
                     if (lane % LPC < 4) *reinterpret_cast<float2 *>(&sm.core[buf][i - 3 + (lane & 3)][ch]) = r;
@@ -393,8 +397,8 @@ int scan_blocks(int C, int G, int N) {
 
 // A split sequence is walked twice (the first pass costs the forward 0.65 of the second, the backward
 // 0.2), so it is split only where its CTAs leave the SMs short of warps: the forward below half a CTA
-// per SM (1 x 4096 steps of 4096 channels x 16 states, 64 CTAs: 175 us split, 275 whole; 2 x 2048 steps,
-// 128 CTAs: 200 split, 151 whole), the backward below two (the latter: 402 us split, 535 whole). A segment
+// per SM (1 x 4096 steps of 4096 channels x 16 states, 64 CTAs: 167 us split, 275 whole; 2 x 2048 steps,
+// 128 CTAs: 169 split, 134 whole), the backward below two (the latter: 402 us split, 535 whole). A segment
 // has at least 4 (2) tiles: with few channels each tile is a latency of some microseconds, which shorter
 // segments hide (3 x 333 steps of 518 x 11 states, forward and backward: 147 us with 8 tiles, 81 us with 2
 // to 4, 143 whole). Of the counts that give the SMs, which hold two

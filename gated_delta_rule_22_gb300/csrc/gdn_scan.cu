@@ -6,7 +6,7 @@
 //
 // Each state and step costs one exp2 and four float32 operations (d A log2 e, (d u) B, the update,
 // the product with C), each channel and step 2 to 4 elements of memory traffic: with 16 states the
-// exponentials bind, not the memory.
+// exponentials' time is the floor, not the memory's.
 #include "gdn_scan.cuh"
 
 namespace gdn {

@@ -34,13 +34,14 @@ struct FwdSmem {
 // against 138; of 4096 x 64 states 723 against 438).
 //
 // Measured on 2 x 2048 steps of 4096 channels x 16 states, bf16, with checkpoints: 134 us, against 153 with
-// one channel per lane; 1 x 4096 steps, split, without checkpoints: 63 us for the ends, 93 for the outputs.
+// one channel per lane; 1 x 4096 steps, split, without checkpoints: 60 us for the ends, 90 for the outputs.
 // Not the exponentials bind (29 us at 32 per clock and SM) nor the memory (20 us, and 10 for
 // checkpoints), but the loads from shared memory and the latency of one or two state warps per scheduler.
-// Two CTAs per SM: with three, and 80 registers, the split prompt takes 161 us in all instead of 167, but
-// the 128 CTAs of the first case, one per SM at any rate, 160 us instead of 134.
-template <int LPC, typename T, bool VEC, bool LITE>
-__global__ void __launch_bounds__(kStateThreads + kScanHelpers, 2) scan_fwd_kernel(ScanParams p) {
+// CTAS per SM: three, with 80 registers, where there are more CTAs than two per SM (the split prompt
+// takes 161 us in all instead of 167, 8 x 1024 steps of 8192 channels 356 instead of 366), else two (the
+// 128 CTAs of the first case, one per SM at any rate, take 160 us instead of 134 with 80 registers).
+template <int LPC, typename T, bool VEC, bool LITE, int CTAS>
+__global__ void __launch_bounds__(kStateThreads + kScanHelpers, CTAS) scan_fwd_kernel(ScanParams p) {
     using G = ScanGeo<LPC>;
     constexpr int NP = G::NP, V = G::V, TT = kScanTile, ALL = kStateThreads + kScanHelpers;
     constexpr int kFull = 1, kDone = 3;
@@ -397,7 +398,7 @@ int scan_blocks(int C, int G, int N) {
 
 // A split sequence is walked twice (the first pass costs the forward 0.65 of the second, the backward
 // 0.2), so it is split only where its CTAs leave the SMs short of warps: the forward below half a CTA
-// per SM (1 x 4096 steps of 4096 channels x 16 states, 64 CTAs: 167 us split, 275 whole; 2 x 2048 steps,
+// per SM (1 x 4096 steps of 4096 channels x 16 states, 64 CTAs: 160 us split, 275 whole; 2 x 2048 steps,
 // 128 CTAs: 169 split, 134 whole), the backward below two (the latter: 402 us split, 535 whole). A segment
 // has at least 4 (2) tiles: with few channels each tile is a latency of some microseconds, which shorter
 // segments hide (3 x 333 steps of 518 x 11 states, forward and backward: 147 us with 8 tiles, 81 us with 2
@@ -427,29 +428,33 @@ void scan_split(ScanParams *p, bool bwd) {
 
 namespace {
 
-template <int LPC, typename T, bool VEC, bool LITE>
-cudaError_t scan_fwd_one(const ScanParams &p, cudaStream_t s) {
+template <int LPC, typename T, bool VEC, bool LITE, int CTAS>
+cudaError_t scan_fwd_one(const ScanParams &p, dim3 grid, cudaStream_t s) {
     constexpr int smem = (int)sizeof(FwdSmem<LPC, T>);
     if (smem > 48 * 1024) {
-        const cudaError_t e = allow_smem<scan_fwd_kernel<LPC, T, VEC, LITE>>(smem);
+        const cudaError_t e = allow_smem<scan_fwd_kernel<LPC, T, VEC, LITE, CTAS>>(smem);
         if (e != cudaSuccess) return e;
     }
-    const dim3 grid(p.Bn * p.G * scan_blocks(p.Cn, p.G, p.N), p.segs);
     const char *name = LITE ? "scan_fwd_ends" : "scan_fwd";
     timing_mark(name, 0, s);
-    scan_fwd_kernel<LPC, T, VEC, LITE><<<grid, kStateThreads + kScanHelpers, smem, s>>>(p);
+    scan_fwd_kernel<LPC, T, VEC, LITE, CTAS><<<grid, kStateThreads + kScanHelpers, smem, s>>>(p);
     timing_mark(name, 1, s);
     return cudaGetLastError();
+}
+template <int LPC, typename T, bool VEC, bool LITE>
+cudaError_t scan_fwd_ctas(const ScanParams &p, cudaStream_t s) {
+    const dim3 grid(p.Bn * p.G * scan_blocks(p.Cn, p.G, p.N), p.segs);
+    return (long long)grid.x * grid.y > 304 ? scan_fwd_one<LPC, T, VEC, LITE, 3>(p, grid, s) : scan_fwd_one<LPC, T, VEC, LITE, 2>(p, grid, s);
 }
 
 template <int LPC, typename T, bool VEC>
 cudaError_t scan_fwd_prompt(const ScanParams &p, cudaStream_t s) {
     cudaError_t e;
     if (p.segs > 1) {
-        if ((e = scan_fwd_one<LPC, T, VEC, true>(p, s)) != cudaSuccess) return e;
+        if ((e = scan_fwd_ctas<LPC, T, VEC, true>(p, s)) != cudaSuccess) return e;
         if ((e = launch_scan_combine(p, p.h0, nullptr, false, s)) != cudaSuccess) return e;
     }
-    return scan_fwd_one<LPC, T, VEC, false>(p, s);
+    return scan_fwd_ctas<LPC, T, VEC, false>(p, s);
 }
 
 template <int LPC, typename T>

@@ -153,10 +153,29 @@ def make_shape(B, T, Hk, Hv, Dk, Dv, chunk=64, dtype=GDN_F32) -> GdnShape:
     return GdnShape(B, T, Hk, Hv, Dk, Dv, chunk, dtype)
 
 
-def _stream(stream, device=None):
+def _stream(device=None):
+    return ctypes.c_void_p(_torch().cuda.current_stream(device).cuda_stream)
+
+
+def _under(stream, call, args):
+    """call(**args) on `stream` instead of the current stream. What the call allocates (its scratch,
+    its outputs) comes from that stream's memory: the caching allocator hands memory out again in
+    the order of the stream that it was allocated for, so scratch from another stream's memory would be
+    overwritten while the call's kernels still use it. Every tensor of the call is marked as used on
+    both streams, so that its memory is not reused before both are done with it. (The caller still
+    orders the streams: inputs are ready on `stream`, outputs are waited for.)"""
     torch = _torch()
-    s = stream if stream is not None else torch.cuda.current_stream(device)
-    return ctypes.c_void_p(s.cuda_stream)
+    args = {k: v for k, v in args.items() if k != "stream"}
+    caller = torch.cuda.current_stream(stream.device)
+    with torch.cuda.stream(stream):
+        out = call(**args)
+    if caller != stream:
+        for v in (*args.values(), out):
+            for t in v.values() if isinstance(v, dict) else v if isinstance(v, tuple) else (v,):
+                if isinstance(t, torch.Tensor) and t.is_cuda:
+                    t.record_stream(stream)
+                    t.record_stream(caller)
+    return out
 
 
 def gdn_timing_enable(on: bool = True) -> None:
@@ -223,6 +242,8 @@ def gdn_fwd(q, k, v, g, beta, S0=None, chunk=64, *, y=None, S_T=None, ckpt=None,
     """y, S_T, ckpt = gdn_fwd(q, k, v, g, beta[, S0]) on CUDA tensors (see include/gdn.h).
     ckpt is the [B, Hv, NC, Dv, Dk] view of the saved-for-backward buffer (new_ckpt), or None
     with want_ckpt=False (inference / decode: nothing is saved)."""
+    if stream is not None:
+        return _under(stream, gdn_fwd, locals())
     torch = _torch()
     lib = load_library()
     shape = _shape_of(q, v, chunk)
@@ -248,7 +269,7 @@ def gdn_fwd(q, k, v, g, beta, S0=None, chunk=64, *, y=None, S_T=None, ckpt=None,
     if ckpt is None and want_ckpt:
         ckpt = new_ckpt(q, v, chunk)
     rc = lib.gdn_fwd(ctypes.byref(shape), _ptr(q), _ptr(k), _ptr(v), _ptr(g), _ptr(beta), _ptr(S0),
-                     _ptr(y), _ptr(S_T), _ptr(ckpt), 0 if ckpt is None else _room(ckpt), _stream(stream, dev))
+                     _ptr(y), _ptr(S_T), _ptr(ckpt), 0 if ckpt is None else _room(ckpt), _stream(dev))
     if rc != GDN_OK:
         raise GdnError("gdn_fwd", rc, lib)
     return y, S_T, ckpt
@@ -292,6 +313,8 @@ def gdn_bwd(q, k, v, g, beta, ckpt, dy, dS_T=None, chunk=64, *, workspace=None, 
     """dict(dq, dk, dv, dg, dbeta, dS0) = gdn_bwd(...) on CUDA tensors (see include/gdn.h).
     workspace: a device tensor of at least gdn_bwd_workspace_bytes bytes, or None (allocated
     here for this call)."""
+    if stream is not None:
+        return _under(stream, gdn_bwd, locals())
     torch = _torch()
     lib = load_library()
     shape, out = _bwd_prepare(q, k, v, g, beta, ckpt, dy, dS_T, chunk, out, want_dS0, workspace)
@@ -301,7 +324,7 @@ def gdn_bwd(q, k, v, g, beta, ckpt, dy, dS_T=None, chunk=64, *, workspace=None, 
     rc = lib.gdn_bwd(ctypes.byref(shape), _ptr(q), _ptr(k), _ptr(v), _ptr(g), _ptr(beta), _ptr(ckpt),
                      _room(ckpt), _ptr(dy), _ptr(dS_T), _ptr(out["dq"]), _ptr(out["dk"]), _ptr(out["dv"]),
                      _ptr(out["dg"]), _ptr(out["dbeta"]), _ptr(out.get("dS0")), _ptr(workspace),
-                     workspace.numel() * workspace.element_size(), _stream(stream, q.device))
+                     workspace.numel() * workspace.element_size(), _stream(q.device))
     if rc != GDN_OK:
         raise GdnError("gdn_bwd", rc, lib)
     return out
@@ -327,6 +350,8 @@ def gdn_fwd_infer(q, k, v, g, beta, S0=None, *, y=None, S_T=None, workspace=None
     """y, S_T = gdn_fwd_infer(q, k, v, g, beta[, S0]): the inference forward on the tensor cores
     (include/gdn.h): nothing saved; the per-chunk products go to `workspace`
     (gdn_infer_workspace_bytes, allocated here when None)."""
+    if stream is not None:
+        return _under(stream, gdn_fwd_infer, locals())
     torch = _torch()
     lib = load_library()
     shape = _shape_of(q, v, 64)
@@ -345,7 +370,7 @@ def gdn_fwd_infer(q, k, v, g, beta, S0=None, *, y=None, S_T=None, workspace=None
         S_T = torch.empty((B, Hv, Dv, Dk), dtype=torch.float32, device=dev)
     workspace = _workspace(workspace, lib.gdn_infer_workspace_bytes(ctypes.byref(shape)), dev)
     rc = lib.gdn_fwd_infer(ctypes.byref(shape), _ptr(q), _ptr(k), _ptr(v), _ptr(g), _ptr(beta), _ptr(S0), _ptr(y),
-                           _ptr(S_T), _ptr(workspace), _room(workspace), _stream(stream, dev))
+                           _ptr(S_T), _ptr(workspace), _room(workspace), _stream(dev))
     if rc != GDN_OK:
         raise GdnError("gdn_fwd_infer", rc, lib)
     return y, S_T
@@ -391,6 +416,8 @@ def gdn_fwd_rc(q, k, v, g, beta, S0=None, *, y=None, S_T=None, ckpt=None, worksp
     """y, S_T, ckpt = gdn_fwd_rc(...): the forward of the re-computation mode (include/gdn.h):
     ckpt holds only the chunk-start states and the residuals (new_rc_ckpt when None); the
     per-chunk products go to `workspace` (gdn_rc_fwd_workspace_bytes, allocated here when None)."""
+    if stream is not None:
+        return _under(stream, gdn_fwd_rc, locals())
     torch = _torch()
     lib = load_library()
     shape = _shape_of(q, v, 64)
@@ -411,7 +438,7 @@ def gdn_fwd_rc(q, k, v, g, beta, S0=None, *, y=None, S_T=None, ckpt=None, worksp
         ckpt = new_rc_ckpt(q, v)
     workspace = _workspace(workspace, lib.gdn_rc_fwd_workspace_bytes(ctypes.byref(shape)), dev)
     rc = lib.gdn_fwd_rc(ctypes.byref(shape), _ptr(q), _ptr(k), _ptr(v), _ptr(g), _ptr(beta), _ptr(S0), _ptr(y),
-                        _ptr(S_T), _ptr(ckpt), _room(ckpt), _ptr(workspace), _room(workspace), _stream(stream, dev))
+                        _ptr(S_T), _ptr(ckpt), _room(ckpt), _ptr(workspace), _room(workspace), _stream(dev))
     if rc != GDN_OK:
         raise GdnError("gdn_fwd_rc", rc, lib)
     return y, S_T, ckpt
@@ -420,6 +447,8 @@ def gdn_fwd_rc(q, k, v, g, beta, S0=None, *, y=None, S_T=None, ckpt=None, worksp
 def gdn_bwd_rc(q, k, v, g, beta, ckpt, dy, dS_T=None, *, workspace=None, out=None, want_dS0=True, stream=None):
     """dict(dq, dk, dv, dg, dbeta, dS0) = gdn_bwd_rc(...): the backward of the re-computation
     mode for the saved buffer of gdn_fwd_rc (include/gdn.h)."""
+    if stream is not None:
+        return _under(stream, gdn_bwd_rc, locals())
     torch = _torch()
     lib = load_library()
     B, T, Hk, Dk = q.shape
@@ -440,7 +469,7 @@ def gdn_bwd_rc(q, k, v, g, beta, ckpt, dy, dS_T=None, *, workspace=None, out=Non
     rc = lib.gdn_bwd_rc(ctypes.byref(shape), _ptr(q), _ptr(k), _ptr(v), _ptr(g), _ptr(beta), _ptr(ckpt),
                         _room(ckpt), _ptr(dy), _ptr(dS_T), _ptr(out["dq"]), _ptr(out["dk"]), _ptr(out["dv"]),
                         _ptr(out["dg"]), _ptr(out["dbeta"]), _ptr(out.get("dS0")), _ptr(workspace),
-                        _room(workspace), _stream(stream, dev))
+                        _room(workspace), _stream(dev))
     if rc != GDN_OK:
         raise GdnError("gdn_bwd_rc", rc, lib)
     return out
@@ -452,6 +481,8 @@ def gdn_fwd_seg(q, k, v, g, beta, S0=None, segments=2, *, y=None, S_T=None, ckpt
     sequence-parallel forward (see include/gdn.h). ckpt is a uint8 device tensor of
     gdn_seg_ckpt_bytes bytes (allocated here when None); workspace likewise
     (gdn_seg_workspace_bytes, allocated here for this call when None)."""
+    if stream is not None:
+        return _under(stream, gdn_fwd_seg, locals())
     torch = _torch()
     lib = load_library()
     shape = _shape_of(q, v, 64)
@@ -483,7 +514,7 @@ def gdn_fwd_seg(q, k, v, g, beta, S0=None, segments=2, *, y=None, S_T=None, ckpt
         workspace = torch.empty(max(need_ws, 16), dtype=torch.uint8, device=dev)
     rc = lib.gdn_fwd_seg(ctypes.byref(shape), segments, _ptr(q), _ptr(k), _ptr(v), _ptr(g), _ptr(beta), _ptr(S0),
                          _ptr(y), _ptr(S_T), _ptr(ckpt), _room(ckpt), _ptr(workspace), _room(workspace),
-                         _stream(stream, dev))
+                         _stream(dev))
     if rc != GDN_OK:
         raise GdnError("gdn_fwd_seg", rc, lib)
     return y, S_T, ckpt
@@ -493,6 +524,8 @@ def gdn_bwd_seg(q, k, v, g, beta, ckpt, dy, dS_T=None, segments=2, *, workspace=
                 stream=None):
     """dict(dq, dk, dv, dg, dbeta, dS0) = gdn_bwd_seg(...): the sequence-parallel backward for
     the saved buffer of gdn_fwd_seg with the same segments (see include/gdn.h)."""
+    if stream is not None:
+        return _under(stream, gdn_bwd_seg, locals())
     torch = _torch()
     lib = load_library()
     B, T, Hk, Dk = q.shape
@@ -518,7 +551,7 @@ def gdn_bwd_seg(q, k, v, g, beta, ckpt, dy, dS_T=None, segments=2, *, workspace=
     rc = lib.gdn_bwd_seg(ctypes.byref(shape), segments, _ptr(q), _ptr(k), _ptr(v), _ptr(g), _ptr(beta), _ptr(ckpt),
                          _room(ckpt), _ptr(dy), _ptr(dS_T), _ptr(out["dq"]), _ptr(out["dk"]), _ptr(out["dv"]),
                          _ptr(out["dg"]), _ptr(out["dbeta"]), _ptr(out.get("dS0")), _ptr(workspace),
-                         _room(workspace), _stream(stream, dev))
+                         _room(workspace), _stream(dev))
     if rc != GDN_OK:
         raise GdnError("gdn_bwd_seg", rc, lib)
     return out
@@ -529,12 +562,14 @@ def gdn_bwd_noalloc(q, k, v, g, beta, ckpt, dy, dS_T=None, chunk=64, *, out=None
     """gdn_bwd with the library's fixed device scratch instead of a workspace (see
     include/gdn.h: calls that overlap on one GPU race on that scratch). Pass `out` to
     allocate nothing here either."""
+    if stream is not None:
+        return _under(stream, gdn_bwd_noalloc, locals())
     lib = load_library()
     shape, out = _bwd_prepare(q, k, v, g, beta, ckpt, dy, dS_T, chunk, out, want_dS0)
     rc = lib.gdn_bwd_noalloc(ctypes.byref(shape), _ptr(q), _ptr(k), _ptr(v), _ptr(g), _ptr(beta), _ptr(ckpt),
                              _room(ckpt), _ptr(dy), _ptr(dS_T), _ptr(out["dq"]), _ptr(out["dk"]), _ptr(out["dv"]),
                              _ptr(out["dg"]), _ptr(out["dbeta"]), _ptr(out.get("dS0")),
-                             _stream(stream, q.device))
+                             _stream(q.device))
     if rc != GDN_OK:
         raise GdnError("gdn_bwd_noalloc", rc, lib)
     return out
@@ -549,8 +584,10 @@ def gdn_device_status() -> int:
 def gdn_debug_wait_probe(polls: int = 1000, stream=None) -> None:
     """Enqueue the timeout-path probe (include/gdn.h): one CTA whose bounded wait runs out after
     `polls` polls and records GDN_ERR_TIMEOUT in the device status word."""
+    if stream is not None:
+        return _under(stream, gdn_debug_wait_probe, locals())
     lib = load_library()
-    rc = lib.gdn_debug_wait_probe(int(polls), _stream(stream))
+    rc = lib.gdn_debug_wait_probe(int(polls), _stream())
     if rc != GDN_OK:
         raise GdnError("gdn_debug_wait_probe", rc, lib)
 
@@ -586,6 +623,8 @@ def gdn_gates_fwd(a, b, A_log, dt_bias, *, Hk=None, Dk=32, Dv=4, stream=None):
     """g, beta = gdn_gates_fwd(a, b, A_log, dt_bias) on CUDA tensors (see include/gdn.h).
     a, b [B, T, Hv] (float32 or bfloat16); A_log, dt_bias [Hv] float32. Hk, Dk, Dv only
     complete the layer shape the library checks (defaults: Hk = Hv, Dk = 32, Dv = 4)."""
+    if stream is not None:
+        return _under(stream, gdn_gates_fwd, locals())
     torch = _torch()
     lib = load_library()
     B, T, Hv = a.shape
@@ -598,7 +637,7 @@ def gdn_gates_fwd(a, b, A_log, dt_bias, *, Hk=None, Dk=32, Dv=4, stream=None):
     g = torch.empty_like(a)
     beta = torch.empty_like(a)
     rc = lib.gdn_gates_fwd(ctypes.byref(shape), _ptr(a), _ptr(b), _ptr(A_log), _ptr(dt_bias), _ptr(g),
-                           _ptr(beta), _stream(stream, a.device))
+                           _ptr(beta), _stream(a.device))
     if rc != GDN_OK:
         raise GdnError("gdn_gates_fwd", rc, lib)
     return g, beta
@@ -606,6 +645,8 @@ def gdn_gates_fwd(a, b, A_log, dt_bias, *, Hk=None, Dk=32, Dv=4, stream=None):
 
 def gdn_gates_bwd(a, b, A_log, dt_bias, dg, dbeta, *, Hk=None, Dk=32, Dv=4, stream=None):
     """dict(da, db, dA_log, ddt_bias) = gdn_gates_bwd(...) on CUDA tensors (see include/gdn.h)."""
+    if stream is not None:
+        return _under(stream, gdn_gates_bwd, locals())
     torch = _torch()
     lib = load_library()
     B, T, Hv = a.shape
@@ -619,7 +660,7 @@ def gdn_gates_bwd(a, b, A_log, dt_bias, dg, dbeta, *, Hk=None, Dk=32, Dv=4, stre
            "dA_log": torch.empty_like(A_log), "ddt_bias": torch.empty_like(dt_bias)}
     rc = lib.gdn_gates_bwd(ctypes.byref(shape), _ptr(a), _ptr(b), _ptr(A_log), _ptr(dt_bias), _ptr(dg),
                            _ptr(dbeta), _ptr(out["da"]), _ptr(out["db"]), _ptr(out["dA_log"]),
-                           _ptr(out["ddt_bias"]), _stream(stream, a.device))
+                           _ptr(out["ddt_bias"]), _stream(a.device))
     if rc != GDN_OK:
         raise GdnError("gdn_gates_bwd", rc, lib)
     return out

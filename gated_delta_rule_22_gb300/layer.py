@@ -3,7 +3,8 @@ selective state space scan, the group norm and the projection. Argument marshall
 binding.py.
 
 Inputs that the header gives a row stride may be slices of a wider tensor along the last dimension
-(x[..., :C] of a contiguous tensor); everything else must be contiguous.
+(x[..., :C] of a contiguous tensor); everything else must be contiguous. A call with stream=s is the
+call under torch.cuda.stream(s).
 """
 from __future__ import annotations
 
@@ -11,7 +12,7 @@ import ctypes
 
 import torch
 
-from .binding import GDN_OK, GdnError, _dtype_code, _require_cuda, load_library
+from .binding import GDN_OK, GdnError, _dtype_code, _require_cuda, _under, load_library
 from .binding import _check as _check_in_words
 
 GDN_ACT_NONE, GDN_ACT_SILU, GDN_ACT_GELU = 0, 1, 2
@@ -80,8 +81,8 @@ def _at(t):
     return None if t is None else t.data_ptr()
 
 
-def _stream_of(stream, device):
-    return stream.cuda_stream if stream is not None else torch._C._cuda_getCurrentRawStream(device.index)
+def _stream_of(device):
+    return torch._C._cuda_getCurrentRawStream(device.index)
 
 
 def _type(t):
@@ -171,6 +172,8 @@ def gdn_conv_fwd(x, w, bias=None, s0=None, lens=None, *, act="silu", y=None, s_T
     """y, s_T = gdn_conv_fwd(x, w[, bias, s0, lens]) on CUDA tensors (see include/gdn.h): the short
     causal convolution of x [B, T, C] with taps w [C, W] and an activation ("silu" or "none"); s0 and
     s_T [B, W-1, C] are the carried inputs (with T = 1, s_T may be s0: updated in place)."""
+    if stream is not None:
+        return _under(stream, gdn_conv_fwd, locals())
     lib = _library()
     shape = _conv_args(x, w, bias, s0, lens, act)
     B, T, C, W, dev, dt = shape.B, shape.T, shape.C, shape.W, x.device, x.dtype
@@ -184,7 +187,7 @@ def gdn_conv_fwd(x, w, bias=None, s0=None, lens=None, *, act="silu", y=None, s_T
         y = _new_like(x)
     if s_T is None and want_s_T:
         s_T = _empty((B, W - 1, C), dtype=dt, device=dev) if s0 is None else _empty_like(s0)
-    rc = lib.gdn_conv_fwd(_byref(shape), x.data_ptr(), w.data_ptr(), _at(bias), _at(s0), _at(lens), _at(y), _at(s_T), _stream_of(stream, dev))
+    rc = lib.gdn_conv_fwd(_byref(shape), x.data_ptr(), w.data_ptr(), _at(bias), _at(s0), _at(lens), _at(y), _at(s_T), _stream_of(dev))
     if rc:
         _raise("gdn_conv_fwd", rc)
     return y, s_T
@@ -197,6 +200,8 @@ def gdn_conv_bwd_workspace_bytes(shape: GdnConvShape) -> int:
 def gdn_conv_bwd(x, w, dy, bias=None, s0=None, lens=None, ds_T=None, *, act="silu", workspace=None, want_ds0=True, stream=None):
     """dict(dx, dw, dbias, ds0) = gdn_conv_bwd(x, w, dy, ...) for the inputs of gdn_conv_fwd; dw and
     dbias are float32. ds0 is None with want_ds0=False."""
+    if stream is not None:
+        return _under(stream, gdn_conv_bwd, locals())
     lib = _library()
     shape = _conv_args(x, w, bias, s0, lens, act)
     B, T, C, W, dev, dt = shape.B, shape.T, shape.C, shape.W, x.device, x.dtype
@@ -210,7 +215,7 @@ def gdn_conv_bwd(x, w, dy, bias=None, s0=None, lens=None, ds_T=None, *, act="sil
            "dbias": _empty((C,), dtype=_F32, device=dev),
            "ds0": _empty((B, W - 1, C), dtype=dt, device=dev) if want_ds0 else None}
     rc = lib.gdn_conv_bwd(_byref(shape), x.data_ptr(), w.data_ptr(), _at(bias), _at(s0), _at(lens), dy.data_ptr(), _at(ds_T), _at(out["dx"]),
-         _at(out["dw"]), _at(out["dbias"]), _at(out["ds0"]), _at(workspace), _size(workspace), _stream_of(stream, dev))
+         _at(out["dw"]), _at(out["dbias"]), _at(out["ds0"]), _at(workspace), _size(workspace), _stream_of(dev))
     if rc:
         _raise("gdn_conv_bwd", rc)
     return out
@@ -256,6 +261,8 @@ def gdn_scan_fwd(u, dt, A_log, B, C, D=None, dt_bias=None, z=None, h0=None, lens
     selective state space scan of u [B, T, C] with steps dt, state inputs and outputs B, C [B, T, G, N]
     and gate z. ckpt [B, ceil(T / 16), C, N] (want_ckpt=True) is what gdn_scan_bwd needs. With T = 1
     and no ckpt, h_T may be h0: the state updated in place."""
+    if stream is not None:
+        return _under(stream, gdn_scan_fwd, locals())
     lib = _library()
     shape = _scan_args(u, dt, A_log, B, C, D, dt_bias, z, lens)
     Bn, T, Cn, N, dev = shape.B, shape.T, shape.C, shape.N, u.device
@@ -277,7 +284,7 @@ def gdn_scan_fwd(u, dt, A_log, B, C, D=None, dt_bias=None, z=None, h0=None, lens
         ckpt = _empty(_scan_ckpt_shape(Bn, T, Cn, N), dtype=_F32, device=dev)
     workspace = _scratch("workspace", workspace, 0 if T == 1 else lib.gdn_scan_fwd_workspace_bytes(ctypes.byref(shape)), dev)
     rc = lib.gdn_scan_fwd(_byref(shape), u.data_ptr(), dt.data_ptr(), A_log.data_ptr(), B.data_ptr(), C.data_ptr(), _at(D), _at(dt_bias), _at(z), _at(h0),
-         _at(lens), _at(y), _at(h_T), _at(ckpt), _size(ckpt), _at(workspace), _size(workspace), _stream_of(stream, dev))
+         _at(lens), _at(y), _at(h_T), _at(ckpt), _size(ckpt), _at(workspace), _size(workspace), _stream_of(dev))
     if rc:
         _raise("gdn_scan_fwd", rc)
     return y, h_T, ckpt
@@ -287,6 +294,8 @@ def gdn_scan_bwd(u, dt, A_log, B, C, ckpt, dy, D=None, dt_bias=None, z=None, len
                  want_dh0=True, stream=None):
     """dict(du, ddt, dA_log, dB, dC, dD, ddt_bias, dz, dh0) = gdn_scan_bwd(...) for the inputs and the
     ckpt of gdn_scan_fwd. dD, ddt_bias and dz are None where their input was, dh0 with want_dh0=False."""
+    if stream is not None:
+        return _under(stream, gdn_scan_bwd, locals())
     lib = _library()
     shape = _scan_args(u, dt, A_log, B, C, D, dt_bias, z, lens)
     Bn, T, Cn, N, G, dev, ty = shape.B, shape.T, shape.C, shape.N, shape.G, u.device, u.dtype
@@ -305,7 +314,7 @@ def gdn_scan_bwd(u, dt, A_log, B, C, ckpt, dy, D=None, dt_bias=None, z=None, len
     rc = lib.gdn_scan_bwd(_byref(shape), u.data_ptr(), dt.data_ptr(), A_log.data_ptr(), B.data_ptr(), C.data_ptr(), _at(D), _at(dt_bias), _at(z), _at(lens),
          _at(ckpt), _size(ckpt), dy.data_ptr(), _at(dh_T), _at(out["du"]), _at(out["ddt"]), _at(out["dA_log"]), _at(out["dB"]),
          _at(out["dC"]), _at(out["dD"]), _at(out["ddt_bias"]), _at(out["dz"]), _at(out["dh0"]), _at(workspace),
-         _size(workspace), _stream_of(stream, dev))
+         _size(workspace), _stream_of(dev))
     if rc:
         _raise("gdn_scan_bwd", rc)
     return out
@@ -333,6 +342,8 @@ def gdn_norm_fwd(x, groups, w=None, b=None, z=None, *, act="silu", eps=1e-5, cen
     over the channels (last dimension) of every row of x, times w plus b, then the activation, or with
     a gate z the product with act(z). center=False: root mean square. stats [..., groups, 2] is what
     gdn_norm_bwd needs."""
+    if stream is not None:
+        return _under(stream, gdn_norm_fwd, locals())
     lib = _library()
     shape = _norm_args(x, groups, w, b, z, act, eps, center)
     dev = x.device
@@ -347,7 +358,7 @@ def gdn_norm_fwd(x, groups, w=None, b=None, z=None, *, act="silu", eps=1e-5, cen
         y = _new_like(x)
     if stats is None and want_stats:
         stats = _empty(stats_shape, dtype=_F32, device=dev)
-    rc = lib.gdn_norm_fwd(_byref(shape), x.data_ptr(), _at(w), _at(b), _at(z), _at(y), _at(stats), _stream_of(stream, dev))
+    rc = lib.gdn_norm_fwd(_byref(shape), x.data_ptr(), _at(w), _at(b), _at(z), _at(y), _at(stats), _stream_of(dev))
     if rc:
         _raise("gdn_norm_fwd", rc)
     return y, stats
@@ -361,6 +372,8 @@ def gdn_norm_bwd(x, groups, stats, dy, w=None, b=None, z=None, *, act="silu", ep
                  stream=None):
     """dict(dx, dw, db, dz) = gdn_norm_bwd(x, groups, stats, dy[, w, b, z]) for the inputs and stats of
     gdn_norm_fwd; dw, db (float32) and dz are None where their input was."""
+    if stream is not None:
+        return _under(stream, gdn_norm_bwd, locals())
     lib = _library()
     shape = _norm_args(x, groups, w, b, z, act, eps, center)
     dev = x.device
@@ -372,7 +385,7 @@ def gdn_norm_bwd(x, groups, stats, dy, w=None, b=None, z=None, *, act="silu", ep
     like = lambda t, of: None if t is None else _empty_like(of)  # noqa: E731
     out = {"dx": _empty_like(dy), "dw": like(w, w), "db": like(b, b), "dz": like(z, dy)}
     rc = lib.gdn_norm_bwd(_byref(shape), x.data_ptr(), _at(w), _at(b), _at(z), stats.data_ptr(), dy.data_ptr(), _at(out["dx"]), _at(out["dw"]),
-         _at(out["db"]), _at(out["dz"]), _at(workspace), _size(workspace), _stream_of(stream, dev))
+         _at(out["db"]), _at(out["dz"]), _at(workspace), _size(workspace), _stream_of(dev))
     if rc:
         _raise("gdn_norm_bwd", rc)
     return out
@@ -403,6 +416,8 @@ def gdn_linear_fwd(x, W, bias=None, res=None, *, act="none", y=None, pre=None, w
     """y, pre = gdn_linear_fwd(x, W[, bias, res]) on CUDA tensors (see include/gdn.h):
     y = act(x W^T + bias) + res for x [..., K] and W [N, K]. pre (want_pre=True) is the
     pre-activation, which gdn_linear_bwd needs where act is not "none"."""
+    if stream is not None:
+        return _under(stream, gdn_linear_fwd, locals())
     lib = _library()
     shape, out_shape = _linear_args(x, W, bias, res, act)
     dev, dt = x.device, x.dtype
@@ -418,7 +433,7 @@ def gdn_linear_fwd(x, W, bias=None, res=None, *, act="none", y=None, pre=None, w
         pre = _empty(out_shape, dtype=dt, device=dev)
     workspace = _scratch("workspace", workspace, lib.gdn_linear_fwd_workspace_bytes(ctypes.byref(shape)), dev)
     rc = lib.gdn_linear_fwd(_byref(shape), x.data_ptr(), W.data_ptr(), _at(bias), _at(res), _at(y), _at(pre), _at(workspace),
-         _size(workspace), _stream_of(stream, dev))
+         _size(workspace), _stream_of(dev))
     if rc:
         _raise("gdn_linear_fwd", rc)
     return y, pre
@@ -428,6 +443,8 @@ def gdn_linear_bwd(x, W, dy, pre=None, *, act="none", want_dx=True, want_dW=True
                    stream=None):
     """dict(dx, dW, dbias) = gdn_linear_bwd(x, W, dy[, pre]) for the inputs of gdn_linear_fwd (the
     gradient of res is dy itself). An entry is None with its want_... False."""
+    if stream is not None:
+        return _under(stream, gdn_linear_bwd, locals())
     lib = _library()
     shape, out_shape = _linear_args(x, W, None, None, act)
     dev, dt = x.device, x.dtype
@@ -443,7 +460,7 @@ def gdn_linear_bwd(x, W, dy, pre=None, *, act="none", want_dx=True, want_dW=True
            "dW": _new_like(W) if want_dW else None,
            "dbias": _empty((W.shape[0],), dtype=dt, device=dev) if want_dbias else None}
     rc = lib.gdn_linear_bwd(_byref(shape), x.data_ptr(), W.data_ptr(), _at(pre), dy.data_ptr(), _at(out["dx"]), _at(out["dW"]), _at(out["dbias"]),
-         _at(workspace), _size(workspace), _stream_of(stream, dev))
+         _at(workspace), _size(workspace), _stream_of(dev))
     if rc:
         _raise("gdn_linear_bwd", rc)
     return out

@@ -153,8 +153,18 @@ def make_shape(B, T, Hk, Hv, Dk, Dv, chunk=64, dtype=GDN_F32) -> GdnShape:
     return GdnShape(B, T, Hk, Hv, Dk, Dv, chunk, dtype)
 
 
+def _other_device(device, current):
+    return ValueError(f"tensors are on {device}, and the library launches on the current device, {current}; "
+                      f"call under torch.cuda.device({device.index})")
+
+
 def _stream(device=None):
-    return ctypes.c_void_p(_torch().cuda.current_stream(device).cuda_stream)
+    """The current stream's handle. The library launches on the current device: tensors of another one
+    would reach its kernels as foreign addresses."""
+    cuda = _torch().cuda
+    if device is not None and device.index is not None and device.index != cuda.current_device():
+        raise _other_device(device, cuda.current_device())
+    return ctypes.c_void_p(cuda.current_stream(device).cuda_stream)
 
 
 def _under(stream, call, args):

@@ -12,7 +12,7 @@ import ctypes
 
 import torch
 
-from .binding import GDN_OK, GdnError, _dtype_code, _require_cuda, _under, load_library
+from .binding import GDN_OK, GdnError, _dtype_code, _other_device, _require_cuda, _under, load_library
 from .binding import _check as _check_in_words
 
 GDN_ACT_NONE, GDN_ACT_SILU, GDN_ACT_GELU = 0, 1, 2
@@ -82,6 +82,9 @@ def _at(t):
 
 
 def _stream_of(device):
+    """binding._stream"""
+    if device.index != _current_device():
+        raise _other_device(device, _current_device())
     return torch._C._cuda_getCurrentRawStream(device.index)
 
 
@@ -144,6 +147,7 @@ def _raise(name, rc):
 # A single token's step takes the GPU a few microseconds, less than a Python call with this many
 # arguments: the code below looks up, converts and calls no more than it has to.
 _empty, _empty_like, _byref = torch.empty, torch.empty_like, ctypes.byref
+_current_device = torch._C._cuda_getDevice
 _BF16, _F32, _I32 = torch.bfloat16, torch.float32, torch.int32
 
 

@@ -97,3 +97,16 @@ def test_memory_of_an_explicit_stream(world, name):
     launches.clear()
     CALLS[name](None)
     assert allocs and set(allocs) == {0} and launches == [0]
+
+
+def test_tensors_of_a_device_that_is_not_current(monkeypatch):
+    """The library launches on the current device: other devices' tensors are refused before that."""
+    other = torch.device("cuda", 1)
+    monkeypatch.setattr(Ly, "_current_device", lambda: 0, raising=False)
+    monkeypatch.setattr(torch.cuda, "current_device", lambda: 0)
+    monkeypatch.setattr(torch.cuda, "current_stream", lambda device: Stream(0))
+    monkeypatch.setattr(torch._C, "_cuda_getCurrentRawStream", lambda index: 0)
+    for stream in (B._stream, Ly._stream_of):
+        with pytest.raises(ValueError, match="current device"):
+            stream(other)
+    assert B._stream(torch.device("cuda", 0)).value in (0, None) and Ly._stream_of(torch.device("cuda", 0)) == 0

@@ -17,6 +17,7 @@ HEADER = os.path.join(os.path.dirname(_PKG), "include", "gdn.h")
 GDN_F32, GDN_BF16 = 0, 1
 GDN_OK = 0
 GDN_ERR_UNSUPPORTED_SHAPE = -3
+INT_MAX = 2 ** 31 - 1
 
 
 class GdnShape(ctypes.Structure):
@@ -149,7 +150,14 @@ def _require_cuda(t):
         raise ValueError(f"tensors are on {t.device}; the library takes CUDA tensors")
 
 
+def _int_sizes(call, *sizes):
+    """Sizes beyond the ABI's 32-bit ints, which ctypes would cut without a word, are refused."""
+    if max(sizes) > INT_MAX:
+        raise GdnError(call, GDN_ERR_UNSUPPORTED_SHAPE, load_library())
+
+
 def make_shape(B, T, Hk, Hv, Dk, Dv, chunk=64, dtype=GDN_F32) -> GdnShape:
+    _int_sizes("make_shape", B, T, Hk, Hv, Dk, Dv, chunk)
     return GdnShape(B, T, Hk, Hv, Dk, Dv, chunk, dtype)
 
 

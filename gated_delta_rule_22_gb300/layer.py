@@ -12,7 +12,8 @@ import ctypes
 
 import torch
 
-from .binding import GDN_OK, GdnError, _dtype_code, _other_device, _require_cuda, _under, load_library
+from .binding import (GDN_OK, INT_MAX, GdnError, _dtype_code, _int_sizes, _other_device, _require_cuda, _under,
+                      load_library)
 from .binding import _check as _check_in_words
 
 GDN_ACT_NONE, GDN_ACT_SILU, GDN_ACT_GELU = 0, 1, 2
@@ -161,6 +162,8 @@ def _conv_args(x, w, bias, s0, lens, act):
     B, T, C = x.shape
     W = w.shape[-1]
     dev, dt = x.device, x.dtype
+    if x.numel() > INT_MAX or W > INT_MAX:
+        _int_sizes("gdn_conv", B, T, C, W)
     ld = _rows("x", x, (B, T, C), dt, dev)
     _check("w", w, (C, W), _F32, dev)
     if bias is not None:
@@ -230,6 +233,8 @@ def _scan_args(u, dt, A_log, B, C, D, dt_bias, z, lens):
     Bn, T, Cn = u.shape
     G, N = B.shape[-2:]
     dev, ty = u.device, u.dtype
+    if u.numel() > INT_MAX or B.numel() > INT_MAX:
+        _int_sizes("gdn_scan", Bn, T, Cn, N, G)
     ldu, lddt = _rows("u", u, (Bn, T, Cn), ty, dev), _rows("dt", dt, (Bn, T, Cn), ty, dev)
     ldz = 0 if z is None else _rows("z", z, (Bn, T, Cn), ty, dev)
     ldB, ldC = _rows("B", B, (Bn, T, G, N), ty, dev, 2), _rows("C", C, (Bn, T, G, N), ty, dev, 2)
@@ -331,6 +336,8 @@ def _norm_args(x, groups, w, b, z, act, eps, center):
     if groups < 1 or C % groups != 0:
         raise ValueError(f"{C} channels do not split into {groups} groups")
     rows = x.numel() // max(C, 1)
+    if x.numel() > INT_MAX:
+        _int_sizes("gdn_norm", rows, groups, C // groups)
     ldx = _rows("x", x, x.shape, dt, dev)
     ldz = 0 if z is None else _rows("z", z, x.shape, dt, dev)
     if w is not None:
@@ -401,6 +408,8 @@ def _linear_args(x, W, bias, res, act):
     lead, K = tuple(x.shape[:-1]), x.shape[-1]
     N = W.shape[0]
     M = x.numel() // max(K, 1)
+    if x.numel() > INT_MAX or W.numel() > INT_MAX:
+        _int_sizes("gdn_linear", M, N, K)
     ldx, ldw = _rows("x", x, lead + (K,), dt, dev), _rows("W", W, (N, K), dt, dev)
     if bias is not None:
         _check("bias", bias, (N,), dt, dev)

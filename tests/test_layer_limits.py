@@ -1,0 +1,44 @@
+"""Sizes at the limits of the layer operators, without a GPU: tensors are shapes alone (device
+"meta"), pointers of ABI calls are fake addresses that are never dereferenced."""
+import ctypes
+import os
+
+import pytest
+
+from gated_delta_rule_22_gb300 import binding as B
+from gated_delta_rule_22_gb300 import layer as Ly
+
+torch = pytest.importorskip("torch")
+from test_layer_host import CALLS, call, conv_shape, linear_shape, norm_shape, scan_shape  # noqa: E402
+
+UNSUPPORTED = -3
+LONG = 2 ** 32 + 5
+
+
+@pytest.fixture(scope="module")
+def lib():
+    if not os.path.exists(B.LIB_PATH):
+        from gated_delta_rule_22_gb300 import build
+        build.build()
+    return Ly._library()
+
+
+def meta(*shape, dtype=torch.bfloat16):
+    return torch.empty(*shape, dtype=dtype, device="meta")
+
+
+@pytest.mark.parametrize("name,make", [
+    ("conv", lambda: Ly.gdn_conv_fwd(meta(1, LONG, 1), meta(1, 4, dtype=torch.float32))),
+    ("conv", lambda: Ly.gdn_conv_bwd(meta(LONG, 1, 1), meta(1, 4, dtype=torch.float32), meta(LONG, 1, 1))),
+    ("scan", lambda: Ly.gdn_scan_fwd(meta(1, LONG, 1), meta(1, LONG, 1), meta(1, 1, dtype=torch.float32), meta(1, LONG, 1, 1),
+                                     meta(1, LONG, 1, 1))),
+    ("norm", lambda: Ly.gdn_norm_fwd(meta(LONG, 1), 1)),
+    ("norm", lambda: Ly.gdn_norm_fwd(meta(2, LONG // 2 + 1, 1), 1)),
+    ("linear", lambda: Ly.gdn_linear_fwd(meta(LONG, 1), meta(4, 1))),
+    ("linear", lambda: Ly.gdn_linear_bwd(meta(4, 1), meta(LONG, 1), meta(4, LONG))),
+    ("gates", lambda: B.make_shape(1, LONG, 1, 1, 32, 4)),
+])
+def test_sizes_beyond_32_bits_are_refused_not_cut(lib, name, make):
+    with pytest.raises(B.GdnError) as e:
+        make()
+    assert e.value.code == UNSUPPORTED

@@ -10,6 +10,9 @@ namespace {
 
 constexpr double kMaxElements = 1099511627776.0;   // 2^40
 constexpr long long kMaxLd = 1LL << 40;
+// Row and step counters are 32-bit ints that run past the last row by up to one round of a kernel (the
+// norm's 608 x 8 warps, the convolution's 8 x 256 steps and the steps that it loads ahead).
+constexpr double kMaxRows = 2147483648.0 - 65536.0;
 
 size_t up256(size_t n) { return (n + 255) / 256 * 256; }
 
@@ -46,7 +49,7 @@ int conv_plan(const gdn_conv_shape *s, gdn::ConvParams *p) {
     *p = {};
     const int rc = row_stride(s->ldx, s->C, &p->ldx);
     if (rc != GDN_OK) return rc;
-    if ((double)s->B * s->T >= 2147483648.0 || (double)s->B * s->T * (double)p->ldx >= kMaxElements)
+    if ((double)s->B * s->T >= kMaxRows || (double)s->B * s->T * (double)p->ldx >= kMaxElements)
         return GDN_ERR_UNSUPPORTED_SHAPE;
     p->B = s->B; p->T = s->T; p->C = s->C; p->W = s->W; p->act = s->act;
     return GDN_OK;
@@ -69,7 +72,7 @@ int scan_plan(const gdn_scan_shape *s, gdn::ScanParams *p, bool bwd) {
     long long widest = p->ldu;
     for (long long ld : {p->lddt, p->ldz, p->ldB, p->ldC}) widest = ld > widest ? ld : widest;
     // the largest tensors: the strided inputs, the checkpoints, the backward's partial sums
-    if (rows >= 2147483648.0 || rows * (double)widest >= kMaxElements || rows * s->C * s->N / 8.0 >= kMaxElements ||
+    if (rows >= kMaxRows || rows * (double)widest >= kMaxElements || rows * s->C * s->N / 8.0 >= kMaxElements ||
         (double)s->B * s->C * 16 >= kMaxElements)
         return GDN_ERR_UNSUPPORTED_SHAPE;
     if ((double)s->B * s->G * gdn::scan_blocks(s->C, s->G, s->N) >= 2147483648.0 ||
@@ -101,7 +104,7 @@ size_t scan_bwd_ws(const gdn::ScanParams &p) { return scan_seg_bytes(p) + scan_p
 int norm_plan(const gdn_norm_shape *s, gdn::NormParams *p) {
     if (s == nullptr || s->M <= 0 || s->G <= 0 || s->D <= 0 || s->ldx < 0 || s->ldz < 0) return GDN_ERR_INVALID_ARG;
     if (!dtype_ok(s->dtype) || !act_ok(s->act) || !(s->eps > 0.f) || !isfinite(s->eps)) return GDN_ERR_INVALID_ARG;
-    if (s->G > 65535 || s->D > 65536) return GDN_ERR_UNSUPPORTED_SHAPE;
+    if (s->M >= kMaxRows || s->G > 65535 || s->D > 65536) return GDN_ERR_UNSUPPORTED_SHAPE;
     *p = {};
     const long long C = (long long)s->G * s->D;
     int rc;

@@ -308,7 +308,7 @@ GDN_API int gdn_gates_bwd(const gdn_shape *shape, const void *a, const void *b, 
  *   - Results are bitwise deterministic. How the scan splits a sequence and the projection its sums
  *     depends on all of a call's sizes, so there a row's last bits may differ between batch sizes.
  * Sizes: every size at least 1; a tensor of 2^40 elements or more, B or G above 65535, or rows
- * (B * T, M) of 2^31 or more are GDN_ERR_UNSUPPORTED_SHAPE.
+ * (B * T, M) of 2^31 - 65536 or more are GDN_ERR_UNSUPPORTED_SHAPE.
  */
 typedef enum {
     GDN_ACT_NONE = 0, /* x */

@@ -1,0 +1,39 @@
+"""The layer operators at the edges of what they take: the largest and the most awkward sizes,
+states and values that are not finite, single rows at any address. References and tolerances are
+those of test_gpu_layer.py."""
+import pytest
+
+pytestmark = pytest.mark.gpu
+torch = pytest.importorskip("torch")
+import layer_reference as R  # noqa: E402
+from test_gpu_layer import TOL, Draw, check, clean, d64, gdn, scan_inputs  # noqa: E402,F401
+
+F32, BF16 = torch.float32, torch.bfloat16
+
+
+def test_the_most_rows(gdn):  # noqa: F811
+    """The largest number of rows: 32-bit counters that end near 2^31."""
+    n = 2 ** 31 - 65537
+    r = Draw(1, "bf16")
+    x = torch.empty(n, 1, dtype=BF16, device="cuda")
+    x.view(-1).copy_(r.normal(1 << 20).repeat(2048)[:n])
+    dy = x.flip(0)
+    at = [slice(0, 2000), slice(n // 2, n // 2 + 2000), slice(n - 2000, n)]
+    y, stats = gdn.gdn_norm_fwd(x, 1, act="silu", center=False)
+    d = gdn.gdn_norm_bwd(x, 1, stats, dy, act="silu", center=False)
+    for s in at:
+        (y64,), g = R.with_grads(lambda x: R.norm(x, 1, None, None, None, "silu", 1e-5, False), {"x": d64(x[s])}, (d64(dy[s]),))
+        check("norm", {"y": y[s]}, {"y": y64})
+        # dx cancels to x * eps / (x^2 + eps)^1.5: its error is that of its two terms
+        assert ((d["dx"][s].double() - g["x"]).abs() <= 2 ** -8 * g["x"].abs() + 1e-5 * d64(dy[s] / x[s]).abs()).all()
+    del y, stats, d
+    taps = r.normal(1, 4, dtype=F32)
+    y, s_T = gdn.gdn_conv_fwd(x[None], taps)
+    d = gdn.gdn_conv_bwd(x[None], taps, dy[None], want_ds0=False)
+    for s in at[1:]:
+        wide = slice(s.start - 6, s.stop)
+        (y64, s64), g = R.with_grads(lambda x: R.conv(x, d64(taps), None, None, None, "silu"), {"x": d64(x[None, wide])}, (d64(dy[None, wide]), None))
+        check("conv", {"y": y[:, s]}, {"y": y64[:, 6:]})
+        inner = slice(3, 2000 + 6 - (0 if s.stop == n else 3))
+        check("conv", {"dx": d["dx"][:, wide][:, inner]}, {"dx": g["x"][:, inner]})
+    assert torch.equal(s_T[0], x[-3:])

@@ -9,7 +9,7 @@ from gated_delta_rule_22_gb300 import binding as B
 from gated_delta_rule_22_gb300 import layer as Ly
 
 torch = pytest.importorskip("torch")
-from test_layer_host import CALLS, call, conv_shape, linear_shape, norm_shape, scan_shape  # noqa: E402
+from test_layer_host import call, conv_shape, norm_shape, scan_shape  # noqa: E402
 
 UNSUPPORTED = -3
 LONG = 2 ** 32 + 5
@@ -42,3 +42,21 @@ def test_sizes_beyond_32_bits_are_refused_not_cut(lib, name, make):
     with pytest.raises(B.GdnError) as e:
         make()
     assert e.value.code == UNSUPPORTED
+
+
+MOST = 2 ** 31 - 65537
+
+
+@pytest.mark.parametrize("name,make,kw", [
+    ("gdn_conv", conv_shape, lambda n: dict(B=1, T=n, C=1)),
+    ("gdn_scan", scan_shape, lambda n: dict(B=1, T=n, C=1, N=1, G=1)),
+    ("gdn_norm", norm_shape, lambda n: dict(M=n, G=1, D=1)),
+])
+def test_rows_whose_counters_would_overflow(lib, name, make, kw):
+    """Counters run past the last row by up to a round: the last 65536 values of an int are not taken."""
+    size = getattr(lib, name + "_bwd_workspace_bytes")
+    assert size(ctypes.byref(make(**kw(MOST)))) > 0
+    for n in (MOST + 1, 2 ** 31 - 1):
+        assert size(ctypes.byref(make(**kw(n)))) == 0
+        for way in ("_fwd", "_bwd"):
+            assert call(lib, name + way, make(**kw(n))) == UNSUPPORTED

@@ -219,7 +219,7 @@ __global__ void __launch_bounds__(32 * kConvBwdWarps, 2) conv_bwd_kernel(ConvPar
     extern __shared__ __align__(16) unsigned char smem[];
     auto &sums = *reinterpret_cast<float(*)[kConvBwdWarps][W + 1][32 * V]>(smem);   // over the rings, behind the steps
     const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
-    const int c = (blockIdx.y * 32 + lane) * V;
+    const int c0 = (int)(blockIdx.y + blockIdx.z * gridDim.y) * 32 * V, c = c0 + lane * V;   // may lie past the channels
     const int b = blockIdx.x / slices_row, sl = blockIdx.x % slices_row;
     const int L = row_length(p.lens, b, p.T);
     const int t0 = (sl * kConvBwdWarps + warp) * run, t1 = min(t0 + run, p.T);
@@ -353,11 +353,11 @@ __global__ void __launch_bounds__(32 * kConvBwdWarps, 2) conv_bwd_kernel(ConvPar
     __syncthreads();
     for (int i = threadIdx.x; i < (W + 1) * 32 * V; i += 32 * kConvBwdWarps) {
         const int j = i / (32 * V), cc = i % (32 * V);
-        if (blockIdx.y * 32 * V + cc >= p.C) continue;
+        if (c0 + cc >= p.C) continue;
         float a = 0.f;
 #pragma unroll
         for (int k = 0; k < kConvBwdWarps; ++k) a += sums[k][j][cc];
-        p.part[((size_t)blockIdx.x * (W + 1) + j) * p.C + blockIdx.y * 32 * V + cc] = a;
+        p.part[((size_t)blockIdx.x * (W + 1) + j) * p.C + c0 + cc] = a;
     }
 }
 
@@ -418,7 +418,9 @@ cudaError_t conv_bwd_launch(const ConvParams &p, cudaStream_t s) {
     constexpr int smem = ring > sums ? ring : sums;
     cudaError_t e = allow_smem<conv_bwd_kernel<T, W, V, SILU>>(smem);
     if (e != cudaSuccess) return e;
-    conv_bwd_kernel<T, W, V, SILU><<<dim3(slices, (p.C + 32 * V - 1) / (32 * V)), 32 * kConvBwdWarps, smem, s>>>(p, run, slices_row);
+    // blocks of channels over y and, where one axis of the grid (65535) does not hold them, z
+    const int blocks = (p.C + 32 * V - 1) / (32 * V), z = (blocks + 65534) / 65535, y = (blocks + z - 1) / z;
+    conv_bwd_kernel<T, W, V, SILU><<<dim3(slices, y, z), 32 * kConvBwdWarps, smem, s>>>(p, run, slices_row);
     timing_mark("conv_bwd", 1, s);
     e = cudaGetLastError();
     if (e != cudaSuccess) return e;

@@ -37,3 +37,13 @@ def test_the_most_rows(gdn):  # noqa: F811
         inner = slice(3, 2000 + 6 - (0 if s.stop == n else 3))
         check("conv", {"dx": d["dx"][:, wide][:, inner]}, {"dx": g["x"][:, inner]})
     assert torch.equal(s_T[0], x[-3:])
+
+
+@pytest.mark.parametrize("C", [2097152 + 1, 4194303])
+def test_conv_of_more_channel_blocks_than_an_axis_of_the_grid(gdn, C):  # noqa: F811
+    r = Draw(2, "bf16")
+    x, w, dy = r.normal(1, 2, C), r.normal(C, 2, dtype=F32), r.normal(1, 2, C)
+    y, s_T = gdn.gdn_conv_fwd(x, w, act="none")
+    d = gdn.gdn_conv_bwd(x, w, dy, act="none", want_ds0=False)
+    (y64, s64), g = R.with_grads(lambda x, w: R.conv(x, w, None, None, None, "none"), {"x": d64(x), "w": d64(w)}, (d64(dy), None))
+    check("conv", {"y": y, "s_T": s_T, **d}, {"y": y64, "s_T": s64, "dx": g["x"], "dw": g["w"]})

@@ -299,9 +299,11 @@ __global__ void __launch_bounds__(32 * kConvBwdWarps, 2) conv_bwd_kernel(ConvPar
             float2 s[P];
 #pragma unroll
             for (int q = 0; q < P; ++q) {
-                db[q] = __fadd2_rn(db[q], dwin[W - 1][q]);
+                if (valid) {             // 0 x a carried state that is not finite would be NaN
+                    db[q] = __fadd2_rn(db[q], dwin[W - 1][q]);
 #pragma unroll
-                for (int j = 0; j < W; ++j) dw[j][q] = __ffma2_rn(dwin[W - 1][q], win[j][q], dw[j][q]);
+                    for (int j = 0; j < W; ++j) dw[j][q] = __ffma2_rn(dwin[W - 1][q], win[j][q], dw[j][q]);
+                }
                 s[q] = __fmul2_rn(w[0][q], dwin[W - 1][q]);
 #pragma unroll
                 for (int j = 1; j < W; ++j) s[q] = __ffma2_rn(w[j][q], dwin[W - 1 - j][q], s[q]);

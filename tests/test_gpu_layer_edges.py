@@ -47,3 +47,22 @@ def test_conv_of_more_channel_blocks_than_an_axis_of_the_grid(gdn, C):  # noqa: 
     d = gdn.gdn_conv_bwd(x, w, dy, act="none", want_ds0=False)
     (y64, s64), g = R.with_grads(lambda x, w: R.conv(x, w, None, None, None, "none"), {"x": d64(x), "w": d64(w)}, (d64(dy), None))
     check("conv", {"y": y, "s_T": s_T, **d}, {"y": y64, "s_T": s64, "dx": g["x"], "dw": g["w"]})
+
+
+@pytest.mark.parametrize("act", ["silu", "none"])
+@pytest.mark.parametrize("bad", [float("nan"), float("inf")])
+def test_conv_state_that_is_not_finite(gdn, bad, act):  # noqa: F811
+    """The state of a row without valid steps takes no part in the parameters' gradients, and that of a
+    row of one step only through that step."""
+    r = Draw(3, "bf16")
+    lens = torch.tensor([9, 0, 1], dtype=torch.int32, device="cuda")
+    t = dict(x=r.normal(3, 9, 24), w=r.normal(24, 4, dtype=F32), bias=r.normal(24, dtype=F32), s0=r.normal(3, 3, 24))
+    dy, ds_T = r.normal(3, 9, 24), r.normal(3, 3, 24)
+    t["s0"][1] = bad
+    t["s0"][2, 2, :8] = bad
+    d = gdn.gdn_conv_bwd(t["x"], t["w"], dy, t["bias"], t["s0"], lens, ds_T, act=act)
+    leaves = {k: d64(clean(v, lens) if k == "x" else v) for k, v in t.items()}
+    leaves["s0"][1] = 0.0
+    _, g = R.with_grads(lambda x, w, bias, s0: R.conv(x, w, bias, s0, lens, act), leaves, (d64(clean(dy, lens)), d64(ds_T)))
+    assert torch.isfinite(d["dw"][8:]).all() and torch.isfinite(d["dbias"][8:]).all()
+    check("conv", d, {"d" + k: v for k, v in g.items()})

@@ -143,7 +143,21 @@ __global__ void __launch_bounds__(kRevThreads, LITE ? 4 : kRevCtas) scan_bwd_ker
         }
         if (!LITE) load_mine(p.ckpt + ((size_t)q.b * tiles + tile) * p.Cn * p.N, rh);
     };
-    fetch(q.last - 1);
+    // the segment's tiles with valid steps are [q.first, live). Those behind them pass the adjoint on and
+    // have no gradients; a state that is not finite (a row without valid steps may carry one) would make
+    // NaN of the zeros that they would add.
+    const int live = min(q.last, max(q.first, (L + TT - 1) / TT));
+    if (live > q.first) fetch(live - 1);
+    if (!LITE)
+        for (int t = live * TT + ts; t < min(q.last * TT, p.T); t += 8) {
+            const float zero[V] = {};
+            const size_t at = row + (size_t)t * p.Cn;
+            store_channels<T, V>(static_cast<T *>(p.du) + at, nv, VEC, zero);
+            store_channels<T, V>(static_cast<T *>(p.ddt) + at, nv, VEC, zero);
+            if (p.dz != nullptr) store_channels<T, V>(static_cast<T *>(p.dz) + at, nv, VEC, zero);
+            float *part = p.part_bc + ((((size_t)q.blk * p.Bn + q.b) * p.T + t) * p.G + q.g) * (2 * p.N);
+            for (int n = tid & 15; n < 2 * p.N; n += 16) part[n] = 0.f;
+        }
     for (int i = tid; i < CH; i += kRevThreads) {
         sm.D[i] = p.D != nullptr && i < q.nc ? p.D[q.c0 + i] : 0.f;
         sm.bias[i] = p.dt_bias != nullptr && i < q.nc ? p.dt_bias[q.c0 + i] : 0.f;
@@ -167,7 +181,7 @@ __global__ void __launch_bounds__(kRevThreads, LITE ? 4 : kRevCtas) scan_bwd_ker
 #pragma unroll
     for (int v = 0; v < V; ++v) sum_d[v] = sum_D[v] = sum_b[v] = 0.f;
     __syncthreads();
-    for (int tile = q.last - 1; tile >= q.first; --tile) {
+    for (int tile = live - 1; tile >= q.first; --tile) {
 #pragma unroll
         for (int i = 0; i < PASS; ++i) {
             const int t = tile * TT + ts + 8 * i, st = ts + 8 * i;
@@ -409,6 +423,7 @@ __global__ void __launch_bounds__(kRevThreads, LITE ? 4 : kRevCtas) scan_bwd_ker
             float s = 0.f;
 #pragma unroll
             for (int w = 0; w < kRevWarps; ++w) s += sm.bc[w][i][n];
+            if (tb >= L) s = 0.f;
             p.part_bc[((((size_t)q.blk * p.Bn + q.b) * p.T + tb) * p.G + q.g) * (2 * p.N) + (n / NP) * p.N + n % NP] = s;
         }
         __syncthreads();

@@ -11,6 +11,12 @@ from test_gpu_layer import TOL, Draw, check, clean, d64, gdn, scan_inputs  # noq
 F32, BF16 = torch.float32, torch.bfloat16
 
 
+def same(a, b):
+    """Equal values, NaN (of any payload) equal to NaN."""
+    return torch.equal(torch.isnan(a), torch.isnan(b)) and torch.equal(a.nan_to_num(nan=0.0, posinf=float("inf"), neginf=float("-inf")),
+                                                                       b.nan_to_num(nan=0.0, posinf=float("inf"), neginf=float("-inf")))
+
+
 def test_the_most_rows(gdn):  # noqa: F811
     """The largest number of rows: 32-bit counters that end near 2^31."""
     n = 2 ** 31 - 65537
@@ -66,3 +72,41 @@ def test_conv_state_that_is_not_finite(gdn, bad, act):  # noqa: F811
     _, g = R.with_grads(lambda x, w, bias, s0: R.conv(x, w, bias, s0, lens, act), leaves, (d64(clean(dy, lens)), d64(ds_T)))
     assert torch.isfinite(d["dw"][8:]).all() and torch.isfinite(d["dbias"][8:]).all()
     check("conv", d, {"d" + k: v for k, v in g.items()})
+
+
+@pytest.mark.parametrize("T", [1, 16, 40, 1030])
+@pytest.mark.parametrize("which", ["h0", "dh_T"])
+def test_scan_state_of_a_row_without_steps(gdn, T, which):  # noqa: F811
+    """A state (or its cotangent) that is not finite in a row without valid steps passes through and
+    takes no part in any gradient. (T = 1030 is split into segments.)"""
+    t, lens, dy, dh_T = scan_inputs((3, T, 24, 8, 2, "f32", 0, True, [T, 0, (T + 1) // 2], True, True))
+    bad = t["h0"] if which == "h0" else dh_T
+    bad[1], bad[1, ::2] = float("nan"), float("inf")
+    order = ("u", "dt", "A_log", "B", "C", "D", "dt_bias", "z")
+    args = [t[k] for k in order]
+    y, h_T, ckpt = gdn.gdn_scan_fwd(*args, t["h0"], lens, want_ckpt=True)
+    d = gdn.gdn_scan_bwd(*args[:5], ckpt, dy, *args[5:], lens, dh_T)
+    assert same(h_T[1], t["h0"][1]) and not y[1].any() and same(d["dh0"][1], dh_T[1])
+    keep = bad.clone()
+    keep[1] = 0.0
+    leaves = {k: d64(clean(v, lens) if k in ("u", "dt", "B", "C", "z") else v) for k, v in t.items()}
+    cot = [dy, dh_T]
+    if which == "h0":
+        leaves["h0"] = d64(keep)
+    else:
+        cot[1] = keep
+    _, g = R.with_grads(lambda **k: R.scan(lens=lens, **k), leaves, (d64(clean(cot[0], lens)), d64(cot[1])))
+    g["h0"][1] = d64(dh_T[1])
+    check("scan grads", d, {"d" + k: v for k, v in g.items()})
+
+
+def test_scan_gradients_behind_a_row_are_zeros(gdn):  # noqa: F811
+    """Zeros behind the valid steps, also where the row's own state is not finite."""
+    t, lens, dy, dh_T = scan_inputs((2, 75, 40, 32, 1, "f32", 0, True, [75, 35], True, True))
+    t["h0"][1] = float("nan")
+    args = [t[k] for k in ("u", "dt", "A_log", "B", "C", "D", "dt_bias", "z")]
+    y, _, ckpt = gdn.gdn_scan_fwd(*args, t["h0"], lens, want_ckpt=True)
+    d = gdn.gdn_scan_bwd(*args[:5], ckpt, dy, *args[5:], lens, dh_T)
+    for out in (y, *(d[k] for k in ("du", "ddt", "dB", "dC", "dz"))):
+        assert not out[1, 35:].any() and torch.isfinite(out[0]).all()
+    assert torch.isnan(y[1, :35]).all()

@@ -72,6 +72,7 @@ struct LinearParams {
 };
 
 constexpr int kScanTile = 16;   // steps between the scan's checkpoints, and of one staged tile
+constexpr int kLinearFewRows = 32;   // rows that the projection's forward streams on the CUDA cores where TMA cannot read
 
 // ---- geometry shared by the launchers and the size queries
 int conv_bwd_slices(const ConvParams &p);

@@ -134,9 +134,11 @@ int linear_plan(const gdn_linear_shape *s, gdn::LinearParams *p) {
     return GDN_OK;
 }
 
-// x and W with packed rows are read in place, so they are 16-byte aligned like every packed tensor.
-int linear_operands_ok(const gdn::LinearParams &p, const void *x, const void *W) {
-    if ((p.ldx == p.K && !aligned16(x)) || (p.ldw == p.K && !aligned16(W))) return GDN_ERR_MISALIGNED;
+// bf16 x and W with packed rows are read in place by TMA, so they are 16-byte aligned like every packed
+// tensor. A single row has room for a copy, and the forward of few rows reads any address.
+int linear_operands_ok(const gdn::LinearParams &p, int dtype, const void *x, const void *W, bool bwd) {
+    if (dtype == GDN_F32 || (!bwd && p.M <= gdn::kLinearFewRows)) return GDN_OK;
+    if ((p.ldx == p.K && p.M > 1 && !aligned16(x)) || (p.ldw == p.K && p.N > 1 && !aligned16(W))) return GDN_ERR_MISALIGNED;
     return GDN_OK;
 }
 
@@ -293,7 +295,7 @@ int gdn_linear_fwd(const gdn_linear_shape *shape, const void *x, const void *W, 
     const size_t need = gdn::linear_fwd_workspace(p, shape->dtype);
     if (!x || !W || !y || (need > 0 && !workspace)) return GDN_ERR_INVALID_ARG;
     if ((rc = packed_ok({bias, y, pre, workspace})) != GDN_OK || (rc = strided_ok({x, W, res}, elem(shape->dtype))) != GDN_OK ||
-        (rc = linear_operands_ok(p, x, W)) != GDN_OK)
+        (rc = linear_operands_ok(p, shape->dtype, x, W, false)) != GDN_OK)
         return rc;
     if (workspace_bytes < need) return GDN_ERR_WORKSPACE_TOO_SMALL;
     gdn::api_clear_error();
@@ -310,7 +312,7 @@ int gdn_linear_bwd(const gdn_linear_shape *shape, const void *x, const void *W, 
     const size_t need = gdn::linear_bwd_workspace(p, shape->dtype);
     if (!x || !W || !dy || (need > 0 && !workspace) || (shape->act != GDN_ACT_NONE && !pre)) return GDN_ERR_INVALID_ARG;
     if ((rc = packed_ok({pre, dy, dx, dW, dbias, workspace})) != GDN_OK || (rc = strided_ok({x, W}, elem(shape->dtype))) != GDN_OK ||
-        (rc = linear_operands_ok(p, x, W)) != GDN_OK)
+        (rc = linear_operands_ok(p, shape->dtype, x, W, true)) != GDN_OK)
         return rc;
     if (workspace_bytes < need) return GDN_ERR_WORKSPACE_TOO_SMALL;
     gdn::api_clear_error();

@@ -801,10 +801,11 @@ __global__ void __launch_bounds__(256) linear_dbias_kernel(const float *part, T 
 namespace {
 
 // Room for an operand's copy: float32 terms always, bf16 where TMA cannot read it in place (rows not
-// a multiple of 16 bytes apart) or might not be able to (a slice, whose address may be unaligned).
+// a multiple of 16 bytes apart) or might not be able to (a slice or a single row, whose address may be
+// unaligned).
 size_t pack_bytes(long long rows, int cols, long long ld, int dtype) {
     if (dtype == 0) return up256((size_t)3 * rows * up8(cols) * 2);
-    return ld % 8 != 0 || ld != cols ? up256((size_t)rows * up8(cols) * 2) : 0;
+    return ld % 8 != 0 || ld != cols || rows == 1 ? up256((size_t)rows * up8(cols) * 2) : 0;
 }
 
 struct Operand {
@@ -903,7 +904,7 @@ int gemm(const char *name, const Operand &A, const Operand &B, int M, int N, int
     return api_cuda_status(err);
 }
 
-constexpr int kStreamRows = 32, kNotTaken = 1;
+constexpr int kNotTaken = 1;
 
 template <int MP>
 int token_launch(const LinearParams &p, cudaStream_t s) {
@@ -966,7 +967,7 @@ int token_any(const LinearParams &p, cudaStream_t s) {
     const uintptr_t at = (uintptr_t)p.x | (uintptr_t)p.W;
     if (sizeof(T) == 2 && p.M <= 64 && p.ldx % 8 == 0 && p.ldw % 8 == 0 && at % 16 == 0)
         return p.M <= 16 ? token_launch<16>(p, s) : p.M <= 32 ? token_launch<32>(p, s) : token_launch<64>(p, s);
-    if (p.M > kStreamRows) return kNotTaken;
+    if (p.M > kLinearFewRows) return kNotTaken;
     const bool vec = p.K % V == 0 && p.ldx % V == 0 && p.ldw % V == 0 && at % 16 == 0;
     return vec ? stream_rows<T, V>(p, s) : stream_rows<T, 1>(p, s);
 }
@@ -1030,7 +1031,7 @@ int bwd_any(const LinearParams &p, int dtype, cudaStream_t s) {
 }  // namespace
 
 size_t linear_fwd_workspace(const LinearParams &p, int dtype) {
-    if (p.M <= kStreamRows) return 0;
+    if (p.M <= kLinearFewRows) return 0;
     return pack_bytes(p.M, p.K, p.ldx, dtype) + pack_bytes(p.N, p.K, p.ldw, dtype);
 }
 

@@ -296,8 +296,8 @@ GDN_API int gdn_gates_bwd(const gdn_shape *shape, const void *a, const void *b, 
  *   - Inputs that a shape gives a row stride (ldx, ldu, ...: elements from one step, or row, to the
  *     next; 0 selects the packed width) may be column slices of a wider tensor: the stride between
  *     batch rows is T times the row stride. Their addresses need only the alignment of their element
- *     type (the projection's x and W with packed rows: 16 bytes). Everything else is packed and
- *     16-byte aligned.
+ *     type (more than one packed bf16 row of the projection's x or W: 16 bytes, except in its
+ *     forward with M <= 32). Everything else is packed and 16-byte aligned.
  *   - Parameters that are small (convolution taps, norm weights, A_log, ...) and their gradients are
  *     float32; arithmetic is float32.
  *   - lens ([B] int32, may be NULL: every row has T steps; values are clamped to 0..T) gives each

@@ -110,3 +110,34 @@ def test_scan_gradients_behind_a_row_are_zeros(gdn):  # noqa: F811
     for out in (y, *(d[k] for k in ("du", "ddt", "dB", "dC", "dz"))):
         assert not out[1, 35:].any() and torch.isfinite(out[0]).all()
     assert torch.isnan(y[1, :35]).all()
+
+
+@pytest.mark.parametrize("dtype", ["bf16", "f32"])
+@pytest.mark.parametrize("M,N", [(1, 24), (1, 1), (5, 1), (64, 1), (1, 700)])
+def test_linear_single_rows_at_any_address(gdn, M, N, dtype):  # noqa: F811
+    """A slice with one row counts as contiguous, wherever it begins. (With an activation the bf16 rounding of
+    a single pre-activation would be scaled by the slope's condition: float32 only.)"""
+    r, act = Draw(5, dtype), "silu" if dtype == "f32" else "none"
+    for K in (40, 41):
+        x, W, dy, bias, res = r.normal(M, 200)[:, 3:3 + K], r.normal(N, 200)[:, 5:5 + K], r.normal(M, N), r.normal(N), r.normal(M, 1000)[:, 1:1 + N]
+        y, pre = gdn.gdn_linear_fwd(x, W, bias, res, act=act, want_pre=True)
+        d = gdn.gdn_linear_bwd(x, W, dy, pre, act=act)
+        leaves = dict(x=d64(x), W=d64(W), bias=d64(bias))
+        (y64,), g = R.with_grads(lambda x, W, bias: R.linear(x, W, bias, d64(res), act), leaves, (d64(dy),))
+        check("linear", {"y": y, **d}, {"y": y64, **{"d" + k: v for k, v in g.items()}})
+
+
+@pytest.mark.parametrize("dtype", ["bf16", "f32"])
+@pytest.mark.parametrize("M,N,K", [(3, 24, 40), (16, 8, 24), (32, 70, 33)])
+def test_linear_few_packed_rows_at_any_address(gdn, M, N, K, dtype):  # noqa: F811
+    r = Draw(6, dtype)
+    x, W = r.normal(M * K + 1)[1:].view(M, K), r.normal(N * K + 1)[1:].view(N, K)
+    y, _ = gdn.gdn_linear_fwd(x, W)
+    check("linear", {"y": y}, {"y": d64(x) @ d64(W).t()})
+    if dtype == "f32":
+        dy = r.normal(M, N)
+        check("linear", gdn.gdn_linear_bwd(x, W, dy), {"dx": d64(dy) @ d64(W), "dW": d64(dy).t() @ d64(x)})
+    else:
+        with pytest.raises(gdn.GdnError) as e:          # the gradients' products read bf16 rows in place
+            gdn.gdn_linear_bwd(x, W, r.normal(M, N))
+        assert e.value.code == -2

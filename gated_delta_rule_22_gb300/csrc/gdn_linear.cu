@@ -9,9 +9,10 @@
 // the tensor cores read both from what one TMA box puts into shared memory, so that nothing is
 // transposed in memory.
 //
-// float32 operands are held as three bf16 terms of 8 bits each (x = x0 + x1 + x2 to 24 bits); six of
-// the nine products of terms are summed, smallest first, by walking K once per product: the dropped
-// ones are below 2^-24 of the result. 2048 x 4096 x 8192 takes 0.8 ms, 0.085 of it for the terms: 173
+// float32 operands are held as three bf16 terms (x = x0 + x1 + x2 exactly, each term the rest rounded to
+// nearest: |x1| <= 2^-8 |x|, |x2| <= 2^-17 |x|, of either sign); six of the nine products of terms are
+// summed, smallest first, by walking K once per product: the dropped ones are together below 2^-23.9 of
+// the product, of either sign. 2048 x 4096 x 8192 takes 0.8 ms, 0.085 of it for the terms: 173
 // TFLOP/s, where the CUDA cores' float32 arithmetic ends at 75.
 //
 // Measured in bf16, 8192 x 2048 x 8192 with a residual: 153 us in short bursts, 1.80 PFLOP/s; 173 under
@@ -690,10 +691,11 @@ __global__ void __launch_bounds__(256) linear_stream_kernel(const T *x, long lon
 // x as bf16 operand rows of `cols8` elements: a copy (bf16) or three terms (float32), planes of
 // [rows][cols8]. What lies past the `cols` columns is never read.
 __device__ __forceinline__ void split3(float x, __nv_bfloat16 (&t)[3]) {
-    t[0] = __float2bfloat16_rz(x);
+    // the largest values, which would round to infinity, are cut
+    t[0] = fabsf(x) < 0x1.ffp127f ? __float2bfloat16_rn(x) : __float2bfloat16_rz(x);
     const float r = x - __bfloat162float(t[0]);
     const bool fine = r - r == 0.f;                // an infinity or NaN stays in the first term
-    t[1] = __float2bfloat16_rz(fine ? r : 0.f);
+    t[1] = __float2bfloat16_rn(fine ? r : 0.f);
     t[2] = __float2bfloat16_rn(fine ? r - __bfloat162float(t[1]) : 0.f);
 }
 // V elements of a row, as the operand's planes from `out` on (`plane` elements apart)

@@ -141,3 +141,36 @@ def test_linear_few_packed_rows_at_any_address(gdn, M, N, K, dtype):  # noqa: F8
         with pytest.raises(gdn.GdnError) as e:          # the gradients' products read bf16 rows in place
             gdn.gdn_linear_bwd(x, W, r.normal(M, N))
         assert e.value.code == -2
+
+
+@pytest.mark.parametrize("tail", [0x007f7f, 0x008080, 0x00ff7f, 0x7fffff, None])
+def test_linear_float32_products_hold_24_bits(gdn, tail):  # noqa: F811
+    """One product per output, so that nothing averages out: the terms that the tensor cores' form of
+    float32 drops are below 2^-23.9 of it, its last addition cuts less than 2^-23: 2^-22 in all."""
+    r = Draw(7, "f32")
+
+    def values(n):
+        v = torch.rand(n, device="cuda", generator=r.g) + 1
+        v = v if tail is None else (v.view(torch.int32) & ~0xffff | tail).view(F32)
+        return v * torch.sign(torch.randn(n, device="cuda", generator=r.g))
+
+    M, N, K = 300, 200, 70
+    x, W, dy = torch.zeros(M, K, device="cuda"), torch.zeros(N, K, device="cuda"), torch.zeros(M, N, device="cuda")
+    x[:, 3], W[:, 3], dy[:, 5] = values(M), values(N), values(M)
+    y, _ = gdn.gdn_linear_fwd(x, W)
+    assert ((d64(y) - d64(x) @ d64(W).t()).abs() <= 2.0 ** -22 * (d64(x) @ d64(W).t()).abs()).all()
+    W[5] = values(K)
+    dx = gdn.gdn_linear_bwd(x, W, dy)["dx"]
+    ref = d64(dy) @ d64(W)
+    assert ((d64(dx) - ref).abs() <= 2.0 ** -22 * ref.abs()).all()
+
+
+def test_linear_float32_of_the_largest_values(gdn):  # noqa: F811
+    """Values that bf16 would round to infinity."""
+    top = torch.finfo(F32).max
+    x, W = torch.zeros(64, 40, device="cuda"), torch.zeros(48, 40, device="cuda")
+    x[:, 0] = torch.linspace(0.9, 1.0, 64, device="cuda") * top
+    x[1::2] *= -1
+    W[:, 0] = torch.linspace(0.1, 0.99, 48, device="cuda")
+    y, _ = gdn.gdn_linear_fwd(x, W)
+    assert R.rel(y, d64(x) @ d64(W).t()) <= TOL[F32]

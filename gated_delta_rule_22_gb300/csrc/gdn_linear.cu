@@ -12,8 +12,9 @@
 // float32 operands are held as three bf16 terms (x = x0 + x1 + x2 exactly, each term the rest rounded to
 // nearest: |x1| <= 2^-8 |x|, |x2| <= 2^-17 |x|, of either sign); six of the nine products of terms are
 // summed, smallest first, by walking K once per product: the dropped ones are together below 2^-23.9 of
-// the product, of either sign. 2048 x 4096 x 8192 takes 0.8 ms, 0.085 of it for the terms: 173
-// TFLOP/s, where the CUDA cores' float32 arithmetic ends at 75.
+// the product, of either sign. Outputs that infinities make NaN on the way are formed again in float32.
+// 2048 x 4096 x 8192 takes 0.8 ms, 0.085 of it for the terms: 173 TFLOP/s, where the CUDA cores' float32
+// arithmetic ends at 75.
 //
 // Measured in bf16, 8192 x 2048 x 8192 with a residual: 153 us in short bursts, 1.80 PFLOP/s; 173 under
 // the power cap when it runs on and on, 1.59 PFLOP/s (cuBLAS, measured the same ways, on a square case:
@@ -62,7 +63,31 @@ struct GemmParams {
     int light, light_edges;     // the first pair of those with the fewest other items, and the edge tiles that go to these alone
     int vec;                    // 16-byte accesses of out, pre and res are aligned
     int a_blocks, b_blocks;     // MN-major operands of whole 64-column blocks
+    const __nv_bfloat16 *a, *b; // float32: the operands' terms, planes of rows of lda (ldb) elements, K terms deep
+    size_t a_plane, b_plane;
+    long long lda, ldb;
+    int K;
 };
+
+// One output of a float32 product by a warp, in float32 arithmetic on the CUDA cores, for outputs that
+// the six products made NaN: an infinity by a zero or opposite second or third term is not an infinity
+// by the value. The sum ends early where it is NaN.
+template <bool A_MN, bool B_MN>
+__device__ __forceinline__ float dot_of_terms(const GemmParams &p, int m, int n) {
+    const int lane = threadIdx.x & 31;
+    auto value = [](const __nv_bfloat16 *t, size_t plane) {
+        return __bfloat162float(t[0]) + (__bfloat162float(t[plane]) + __bfloat162float(t[2 * plane]));
+    };
+    float s = 0.f;
+    for (int k0 = 0; k0 < p.K && !__any_sync(kFullMask, s != s); k0 += 32 * 8)
+#pragma unroll
+        for (int i = 0; i < 8; ++i) {
+            const size_t k = k0 + 32 * i + lane;
+            if (k >= p.K) break;
+            s = fmaf(value(p.a + (A_MN ? k * p.lda + m : m * p.lda + k), p.a_plane), value(p.b + (B_MN ? k * p.ldb + n : n * p.ldb + k), p.b_plane), s);
+        }
+    return warp_sum(s);
+}
 
 // The n-th item of a pair of CTAs; false behind its last. Whole and half tiles go round; so do the edge
 // tiles, but the first ones only among the pairs that would otherwise end a round earlier.
@@ -301,7 +326,7 @@ gemm_kernel(const __grid_constant__ CUtensorMap tmA, const __grid_constant__ CUt
         constexpr int CW = TN / (2 * kChunk);          // chunks of a tile per warp
         const int lr = lane / LPR, lc = lane % LPR * V;
         uint32_t n_tile = 0;
-        bool ok = true;
+        bool ok = true, odd = false;               // odd: float32, a NaN among this lane's sums
         int m0, n0, BN;
         for (int i = 0; ok && item_of<TN>(p, i, m0, n0, BN); ++i) {
             const int row0 = m0 + rank * kBM + 32 * quarter, chunks = BN / kChunk;
@@ -383,6 +408,7 @@ gemm_kernel(const __grid_constant__ CUtensorMap tmA, const __grid_constant__ CUt
                     float4 x = make_float4(ahead[2 * j].x, ahead[2 * j].y, ahead[2 * j + 1].x, ahead[2 * j + 1].y);
                     if constexpr (sizeof(T) == 4) {
                         x.x += acc[4 * j]; x.y += acc[4 * j + 1]; x.z += acc[4 * j + 2]; x.w += acc[4 * j + 3];
+                        odd |= x.x != x.x || x.y != x.y || x.z != x.z || x.w != x.w;
                     }
                     *reinterpret_cast<float4 *>(mine + lane * kEpiPitch + 4 * j) = x;
                 }
@@ -459,6 +485,27 @@ gemm_kernel(const __grid_constant__ CUtensorMap tmA, const __grid_constant__ CUt
 #pragma unroll 1
                 for (int c = half; c < chunks; c += 2) finish(c, nullptr);
             }
+        }
+        if constexpr (sizeof(T) == 4) {
+            // the warp's NaN outputs once more (nothing waits for this with a limit: the products are over)
+            if (__any_sync(kFullMask, odd && ok))
+                for (int i = 0; item_of<TN>(p, i, m0, n0, BN); ++i)
+                    for (int c = half; c < BN / kChunk; c += 2)
+                        for (int r = 0; r < 32; ++r) {
+                            const int row = m0 + rank * kBM + 32 * quarter + r, col = n0 + c * kChunk + lane;
+                            const bool in = row < p.M && col < p.N;
+                            const float is = in ? out[(size_t)row * p.N + col] : 0.f;
+                            for (unsigned nan = __ballot_sync(kFullMask, is != is); nan != 0; nan &= nan - 1) {
+                                const int who = __ffs(nan) - 1;
+                                float o = dot_of_terms<A_MN, B_MN>(p, row, col - lane + who);
+                                if (lane != who) continue;
+                                if (bias != nullptr) o += bias[col];
+                                if (pre != nullptr) pre[(size_t)row * p.N + col] = o;
+                                o = act_rt(p.act, o);
+                                if (res != nullptr) o = __fadd_rn(o, res[(size_t)row * p.ldres + col]);
+                                out[(size_t)row * p.N + col] = o;
+                            }
+                        }
         }
     }
     tc_fence_before();
@@ -854,7 +901,9 @@ template <bool A_MN, bool B_MN, typename T>
 int gemm(const char *name, const Operand &A, const Operand &B, int M, int N, int K, const Epilogue &e, int *status, cudaStream_t s) {
     GemmParams p = {};
     p.bias = e.bias; p.res = e.res; p.ldres = e.ldres; p.act = e.act; p.out = e.out; p.pre = e.pre; p.status = status;
-    p.M = M; p.N = N;
+    p.M = M; p.N = N; p.K = K;
+    p.a = static_cast<const __nv_bfloat16 *>(A.p); p.lda = A.ld; p.a_plane = (size_t)A.rows * A.ld;
+    p.b = static_cast<const __nv_bfloat16 *>(B.p); p.ldb = B.ld; p.b_plane = (size_t)B.rows * B.ld;
     p.kblocks = (K + kBK - 1) / kBK;
     const int planes = sizeof(T) == 4 ? 3 : 1;
     p.run = sizeof(T) == 4 ? kRun : p.kblocks;

@@ -174,3 +174,23 @@ def test_linear_float32_of_the_largest_values(gdn):  # noqa: F811
     W[:, 0] = torch.linspace(0.1, 0.99, 48, device="cuda")
     y, _ = gdn.gdn_linear_fwd(x, W)
     assert R.rel(y, d64(x) @ d64(W).t()) <= TOL[F32]
+
+
+@pytest.mark.parametrize("dtype", ["f32", "bf16"])
+@pytest.mark.parametrize("M,N,K", [(4, 50, 70), (64, 50, 70), (300, 130, 72), (300, 130, 700)])
+def test_linear_infinities(gdn, M, N, K, dtype):  # noqa: F811
+    """Infinities and NaN where the definition has them, whatever the number of rows: an infinity by a
+    value of few bits, by its opposite, by zero, by another infinity."""
+    r = Draw(8, dtype)
+    x, W, dy = r.normal(M, K), r.normal(N, K, scale=K ** -0.5), r.normal(M, N)
+    W[:, :40] = torch.sign(W[:, :40])                   # nothing in the second and third terms
+    inf = float("inf")
+    x[0, 5], x[1, 6], x[2, 50], x[3, 1], x[3, 2] = inf, -inf, inf, inf, inf
+    W[4, 5], W[7, 11], W[9, 5] = 0.0, inf, -inf
+    dy[1, 3], dy[2, 8] = inf, float("nan")
+    y, _ = gdn.gdn_linear_fwd(x, W)
+    d = gdn.gdn_linear_bwd(x, W, dy)
+    for got, ref in ((y, d64(x) @ d64(W).t()), (d["dx"], d64(dy) @ d64(W)), (d["dW"], d64(dy).t() @ d64(x))):
+        for f in (torch.isnan, torch.isposinf, torch.isneginf):
+            assert torch.equal(f(got), f(ref)), f
+        assert R.rel(got, ref) <= TOL[got.dtype]

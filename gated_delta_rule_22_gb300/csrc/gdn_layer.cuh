@@ -306,7 +306,7 @@ __device__ __forceinline__ float slice_sum(const float *part, int slices, size_t
             add_comp(a, lost, sums[k][col].x);
             lost += sums[k][col].y;
         }
-    return a + lost;
+    return lost == lost ? a + lost : a;            // a sum that is infinite has lost infinity - infinity
 }
 
 // Valid steps of batch row b.

@@ -194,3 +194,27 @@ def test_linear_infinities(gdn, M, N, K, dtype):  # noqa: F811
         for f in (torch.isnan, torch.isposinf, torch.isneginf):
             assert torch.equal(f(got), f(ref)), f
         assert R.rel(got, ref) <= TOL[got.dtype]
+
+
+def test_parameter_gradients_that_overflow(gdn):  # noqa: F811
+    """Sums over rows that hold an infinity are that infinity, in every operator's parameter gradients."""
+    r = Draw(9, "f32")
+    inf = float("inf")
+
+    def expect(got, ref):
+        for f in (torch.isnan, torch.isposinf, torch.isneginf):
+            assert torch.equal(f(got), f(ref)), f
+        assert R.rel(got, ref) <= TOL[F32]
+
+    dy = r.normal(300, 48)
+    dy[7, 3], dy[9, 4], dy[11, 5], dy[12, 5], dy[13, 6] = inf, -inf, inf, -inf, float("nan")
+    x, W = r.normal(300, 40), r.normal(48, 40)
+    expect(gdn.gdn_linear_bwd(x, W, dy, want_dx=False)["dbias"], d64(dy).sum(0))
+    xn, b = r.normal(300, 48), r.normal(48)
+    _, stats = gdn.gdn_norm_fwd(xn, 3, None, b, act="none")
+    expect(gdn.gdn_norm_bwd(xn, 3, stats, dy, None, b, act="none")["db"], d64(dy).sum(0))
+    xc, w = r.normal(1, 300, 48), r.normal(48, 4)
+    expect(gdn.gdn_conv_bwd(xc, w, dy[None], act="none", want_ds0=False)["dbias"], d64(dy).sum(0))
+    u, A_log, bc, D = torch.ones(1, 300, 48, device="cuda"), r.normal(48, 8), r.normal(1, 300, 1, 8), r.normal(48)
+    _, _, ckpt = gdn.gdn_scan_fwd(u, u, A_log, bc, bc, D, want_ckpt=True)
+    expect(gdn.gdn_scan_bwd(u, u, A_log, bc, bc, ckpt, dy[None], D)["dD"], d64(dy).sum(0))

@@ -23,6 +23,8 @@
 #include "gdn_layer.cuh"
 #include "gdn_umma.cuh"
 
+#include <algorithm>
+
 namespace gdn {
 
 namespace {
@@ -35,9 +37,14 @@ constexpr int kBox = 64 * kBK * 2;                  // one TMA box: 64 rows x 12
 constexpr int kStageBytes = 4 * kBox;               // two boxes of A, two of B
 constexpr size_t kGemmSmem = 1024 + (size_t)kStages * kStageBytes + kEpiWarps * 32 * kEpiPitch * 4 + 256;
 constexpr int kBiasSlices = 128;
-// float32 only: K blocks per run of the tensor cores' accumulator, whose additions truncate; each run's
-// sum is added in float32 registers with rounding, which keeps the error at that of float32 arithmetic.
-constexpr int kRun = 4;
+// K blocks per run of the tensor cores' accumulator, whose additions truncate: a sum of one sign loses some
+// 1e-7 of itself per product of 16 (measured: 2.4 % over 4e6 rows). Each run's sum is added in float32
+// with rounding. float32: short runs, added in registers, keep the error at that of float32
+// arithmetic. bf16: a run of 4096 products loses at most some 4e-4, a fifth of the output's rounding; only
+// K above 65536 takes more than one, added in the workspace, which costs (dW of 32768 x 2048 x 2048 cut
+// into two runs: 169 us, 153 in one).
+template <typename T>
+constexpr int kRun = sizeof(T) == 4 ? 4 : 1024;
 
 size_t up256(size_t n) { return (n + 255) / 256 * 256; }
 int up8(int n) { return (n + 7) / 8 * 8; }
@@ -55,9 +62,11 @@ constexpr int kTileN = sizeof(T) == 4 ? 128 : kMaxBN;   // columns of a whole ti
 struct GemmParams {
     const void *bias, *res;
     void *out, *pre;
+    float *partial;             // bf16, more than one run: the sum of the earlier ones, [32 rows][32 columns] in the lanes' order
     int *status;
     long long ldres;
     int M, N, kblocks, run, act;   // run: K blocks per accumulation
+    int chunks;                 // partial: 32-column chunks of a row of tiles
     int mt, nt, panel;          // tiles along m and n (of 256 columns), n tiles walked together
     int whole, halves, edge;    // whole tiles, half tiles, columns of the edge tiles
     int light, light_edges;     // the first pair of those with the fewest other items, and the edge tiles that go to these alone
@@ -392,6 +401,31 @@ gemm_kernel(const __grid_constant__ CUtensorMap tmA, const __grid_constant__ CUt
                     end_run();
                 }
             }
+            auto partial_at = [&](int c) {
+                return reinterpret_cast<float4 *>(p.partial) + ((size_t)(row0 >> 5) * p.chunks + (n0 / kChunk + c)) * (kChunk * 8) + lane;
+            };
+            if constexpr (sizeof(T) == 2) {
+                for (int kr = p.run; kr < p.kblocks && ok; kr += p.run) {
+                    if (!(ok = begin_run())) break;
+#pragma unroll 1
+                    for (int c = half; c < chunks; c += 2) {
+                        float2 v[kChunk / 2];
+                        read(c, v);
+                        tmem_wait_ld();
+                        float4 *at = partial_at(c);
+#pragma unroll
+                        for (int j = 0; j < kChunk / 4; ++j) {
+                            float4 x = make_float4(v[2 * j].x, v[2 * j].y, v[2 * j + 1].x, v[2 * j + 1].y);
+                            if (kr > p.run) {
+                                const float4 y = at[32 * j];
+                                x.x += y.x; x.y += y.y; x.z += y.z; x.w += y.w;
+                            }
+                            at[32 * j] = x;
+                        }
+                    }
+                    end_run();
+                }
+            }
             if (!ok || !(ok = begin_run())) break;
             if (half >= chunks) {
                 end_run();
@@ -409,6 +443,9 @@ gemm_kernel(const __grid_constant__ CUtensorMap tmA, const __grid_constant__ CUt
                     if constexpr (sizeof(T) == 4) {
                         x.x += acc[4 * j]; x.y += acc[4 * j + 1]; x.z += acc[4 * j + 2]; x.w += acc[4 * j + 3];
                         odd |= x.x != x.x || x.y != x.y || x.z != x.z || x.w != x.w;
+                    } else if (p.partial != nullptr) {
+                        const float4 y = partial_at(c)[32 * j];
+                        x.x += y.x; x.y += y.y; x.z += y.z; x.w += y.w;
                     }
                     *reinterpret_cast<float4 *>(mine + lane * kEpiPitch + 4 * j) = x;
                 }
@@ -895,7 +932,14 @@ struct Epilogue {
     long long ldres;
     int act;
     void *out, *pre;
+    float *partial;             // partial_bytes
 };
+
+// Sums of a product's earlier runs (bf16).
+size_t partial_bytes(long long M, long long N, long long K, int dtype) {
+    if (dtype == 0 || K <= (long long)kRun<__nv_bfloat16> * kBK) return 0;
+    return (size_t)((M + 2 * kBM - 1) / (2 * kBM) * (2 * kBM)) * ((N + 127) / 128 * 128) * 4;
+}
 
 template <bool A_MN, bool B_MN, typename T>
 int gemm(const char *name, const Operand &A, const Operand &B, int M, int N, int K, const Epilogue &e, int *status, cudaStream_t s) {
@@ -906,13 +950,15 @@ int gemm(const char *name, const Operand &A, const Operand &B, int M, int N, int
     p.b = static_cast<const __nv_bfloat16 *>(B.p); p.ldb = B.ld; p.b_plane = (size_t)B.rows * B.ld;
     p.kblocks = (K + kBK - 1) / kBK;
     const int planes = sizeof(T) == 4 ? 3 : 1;
-    p.run = sizeof(T) == 4 ? kRun : p.kblocks;
+    p.run = p.kblocks < kRun<T> ? p.kblocks : kRun<T>;
+    p.partial = sizeof(T) == 2 && p.kblocks > p.run ? e.partial : nullptr;
     constexpr int TN = kTileN<T>;
     // a product with an odd number of columns left gets narrower tiles at the end
     p.mt = (M + 2 * kBM - 1) / (2 * kBM);
     p.nt = N / TN;
     const int unit = B_MN && B.cols % 64 == 0 ? 128 : 32;   // each CTA's half starts on a 64-column block
     p.edge = (N % TN + unit - 1) / unit * unit;
+    p.chunks = (p.nt * TN + p.edge) / kChunk;
     // panels of 8 tiles of columns: a round's tiles then share rows of both operands in L2 (8192 x 2048 x
     // 8192: 171 us sustained with panels of 8, 181 of 1; the products of a gradient of 4100 x 2056 x 2040,
     // with edge tiles dealt round as well, 39 and 38 us against 53 and 62)
@@ -965,6 +1011,7 @@ int token_launch(const LinearParams &p, cudaStream_t s) {
     // at most two CTAs per SM, at least two K blocks each (64 rows, 8192 x 2048: 13 us, 27 by one CTA per tile)
     int splits = 8;
     while (splits > 1 && (tiles * splits > 4 * kPairs || t.kblocks < 2 * splits)) splits /= 2;
+    while ((t.kblocks + splits - 1) / splits > kRun<__nv_bfloat16>) splits *= 2;     // up to 8: see token_any
     t.per = (t.kblocks + splits - 1) / splits;
     CUtensorMap w, x;
     int rc;
@@ -1016,7 +1063,8 @@ template <typename T>
 int token_any(const LinearParams &p, cudaStream_t s) {
     constexpr int V = 16 / sizeof(T);
     const uintptr_t at = (uintptr_t)p.x | (uintptr_t)p.W;
-    if (sizeof(T) == 2 && p.M <= 64 && p.ldx % 8 == 0 && p.ldw % 8 == 0 && at % 16 == 0)
+    const bool short_runs = p.K <= 8 * kRun<__nv_bfloat16> * kBK;      // of each of a cluster's CTAs
+    if (sizeof(T) == 2 && p.M <= 64 && short_runs && p.ldx % 8 == 0 && p.ldw % 8 == 0 && at % 16 == 0)
         return p.M <= 16 ? token_launch<16>(p, s) : p.M <= 32 ? token_launch<32>(p, s) : token_launch<64>(p, s);
     if (p.M > kLinearFewRows) return kNotTaken;
     const bool vec = p.K % V == 0 && p.ldx % V == 0 && p.ldw % V == 0 && at % 16 == 0;
@@ -1033,7 +1081,8 @@ int fwd_any(const LinearParams &p, int dtype, cudaStream_t s) {
     if ((rc = pack(x, &x, ws, dtype, s)) != 0) return rc;
     ws += pack_bytes(p.M, p.K, p.ldx, dtype);
     if ((rc = pack(w, &w, ws, dtype, s)) != 0) return rc;
-    return gemm<false, false, T>("linear_fwd", x, w, p.M, p.N, p.K, {p.bias, p.res, p.ldres, p.act, p.y, p.pre}, p.status, s);
+    float *partial = reinterpret_cast<float *>(ws + pack_bytes(p.N, p.K, p.ldw, dtype));
+    return gemm<false, false, T>("linear_fwd", x, w, p.M, p.N, p.K, {p.bias, p.res, p.ldres, p.act, p.y, p.pre, partial}, p.status, s);
 }
 
 template <typename T>
@@ -1065,15 +1114,17 @@ int bwd_any(const LinearParams &p, int dtype, cudaStream_t s) {
         }
     }
     if (own_dpre) ws += up256((size_t)(dtype == 0 ? 3 : 1) * p.M * up8(p.N) * 2);
+    // the two products' partial sums take the same place, one after the other
+    float *partial = reinterpret_cast<float *>(ws + pack_bytes(p.N, p.K, p.ldw, dtype) + pack_bytes(p.M, p.K, p.ldx, dtype));
     if (p.dx != nullptr) {
         if ((rc = pack(w, &w, ws, dtype, s)) != 0) return rc;
-        if ((rc = gemm<false, true, T>("linear_dx", d, w, p.M, p.K, p.N, {nullptr, nullptr, 0, kActNone, p.dx, nullptr}, p.status, s)) != 0)
+        if ((rc = gemm<false, true, T>("linear_dx", d, w, p.M, p.K, p.N, {nullptr, nullptr, 0, kActNone, p.dx, nullptr, partial}, p.status, s)) != 0)
             return rc;
     }
     ws += pack_bytes(p.N, p.K, p.ldw, dtype);
     if (p.dW != nullptr) {
         if ((rc = pack(x, &x, ws, dtype, s)) != 0) return rc;
-        rc = gemm<true, true, T>("linear_dw", d, x, p.N, p.K, p.M, {nullptr, nullptr, 0, kActNone, p.dW, nullptr}, p.status, s);
+        rc = gemm<true, true, T>("linear_dw", d, x, p.N, p.K, p.M, {nullptr, nullptr, 0, kActNone, p.dW, nullptr, partial}, p.status, s);
         if (rc != 0) return rc;
     }
     return 0;
@@ -1083,13 +1134,14 @@ int bwd_any(const LinearParams &p, int dtype, cudaStream_t s) {
 
 size_t linear_fwd_workspace(const LinearParams &p, int dtype) {
     if (p.M <= kLinearFewRows) return 0;
-    return pack_bytes(p.M, p.K, p.ldx, dtype) + pack_bytes(p.N, p.K, p.ldw, dtype);
+    return pack_bytes(p.M, p.K, p.ldx, dtype) + pack_bytes(p.N, p.K, p.ldw, dtype) + partial_bytes(p.M, p.N, p.K, dtype);
 }
 
 size_t linear_bwd_workspace(const LinearParams &p, int dtype) {
     const bool own_dpre = dtype == 0 || p.act != kActNone || p.N % 8 != 0;
     return up256((size_t)kBiasSlices * p.N * 4) + (own_dpre ? up256((size_t)(dtype == 0 ? 3 : 1) * p.M * up8(p.N) * 2) : 0) +
-           pack_bytes(p.M, p.K, p.ldx, dtype) + pack_bytes(p.N, p.K, p.ldw, dtype);
+           pack_bytes(p.M, p.K, p.ldx, dtype) + pack_bytes(p.N, p.K, p.ldw, dtype) +
+           std::max(partial_bytes(p.M, p.K, p.N, dtype), partial_bytes(p.N, p.K, p.M, dtype));
 }
 
 int launch_linear_fwd(const LinearParams &p, int dtype, cudaStream_t s) {

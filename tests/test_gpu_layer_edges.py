@@ -218,3 +218,41 @@ def test_parameter_gradients_that_overflow(gdn):  # noqa: F811
     u, A_log, bc, D = torch.ones(1, 300, 48, device="cuda"), r.normal(48, 8), r.normal(1, 300, 1, 8), r.normal(48)
     _, _, ckpt = gdn.gdn_scan_fwd(u, u, A_log, bc, bc, D, want_ckpt=True)
     expect(gdn.gdn_scan_bwd(u, u, A_log, bc, bc, ckpt, dy[None], D)["dD"], d64(dy).sum(0))
+
+
+def _one_sign(r, *shape):
+    return (torch.rand(*shape, device="cuda", generator=r.g) + 1).to(BF16)
+
+
+def _product64(a, b):
+    """a b^T of [M, K] and [N, K], by parts of K."""
+    return sum(d64(x) @ d64(y).t() for x, y in zip(a.split(1 << 18, 1), b.split(1 << 18, 1)))
+
+
+def test_linear_gradient_of_many_rows(gdn):  # noqa: F811
+    """4e6 rows of one sign: the tensor cores' accumulation, which truncates, alone would lose 2.4 %."""
+    r = Draw(10, "bf16")
+    x, dy, W = _one_sign(r, 4000000, 64), _one_sign(r, 4000000, 64), r.normal(64, 64)
+    d = gdn.gdn_linear_bwd(x, W, dy, want_dx=False)
+    check("many rows", d, {"dW": _product64(dy.t(), x.t()), "dbias": dy.double().sum(0)})
+
+
+@pytest.mark.parametrize("M,N,K,act", [(70, 40, 2000000, "none"), (300, 520, 70008, "silu"), (64, 72, 70000, "gelu"), (64, 72, 540000, "none"),
+                                       (16, 256, 100000, "none"), (7, 100, 540000, "silu"), (2600, 2056, 65600, "none"),
+                                       (260, 130, 65537, "silu")], ids=str)
+def test_linear_long_sums(gdn, M, N, K, act):  # noqa: F811
+    """Products over long K in several runs: partial sums in whole, half and edge tiles, in both gradients
+    (over M and over N), and in the decode forms."""
+    r = Draw(11, "bf16")
+    x, W, bias, res = _one_sign(r, M, K), _one_sign(r, N, K) / K, r.normal(N), r.normal(M, N)
+    y, pre = gdn.gdn_linear_fwd(x, W, bias, res, act=act, want_pre=True)
+    core = _product64(x, W)
+    check("long", {"y": y, "pre": pre}, {"y": R.act(act, core + d64(bias)) + d64(res), "pre": core + d64(bias)})
+    # the same sizes as gradients: K rows give dW, K outputs give dx
+    dy, a = _one_sign(r, K, N), _one_sign(r, K, M)
+    dW = gdn.gdn_linear_bwd(a, r.normal(N, M), dy, want_dx=False, want_dbias=False)["dW"]
+    check("long dW", {"dW": dW}, {"dW": _product64(dy.t(), a.t())})
+    if M * K < 1 << 27:
+        dy, Wl = _one_sign(r, M, K), _one_sign(r, K, N)
+        dx = gdn.gdn_linear_bwd(r.normal(M, N), Wl, dy, want_dW=False, want_dbias=False)["dx"]
+        check("long dx", {"dx": dx}, {"dx": _product64(dy, Wl.t())})

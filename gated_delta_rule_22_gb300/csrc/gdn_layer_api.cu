@@ -128,7 +128,8 @@ int linear_plan(const gdn_linear_shape *s, gdn::LinearParams *p) {
     if ((double)s->M * (double)p->ldx >= kMaxElements || (double)s->N * (double)p->ldw >= kMaxElements ||
         (double)s->M * (double)p->ldres >= kMaxElements)
         return GDN_ERR_UNSUPPORTED_SHAPE;
-    // grids of tiles of 64 rows on the y axis
+    // with room to spare for 32-bit counters of rows, of tiles and of K steps times products, and for the
+    // decode form's grid (N / 128 on the y axis)
     if (s->M > 4000000 || s->N > 4000000 || s->K > 4000000) return GDN_ERR_UNSUPPORTED_SHAPE;
     p->M = s->M; p->N = s->N; p->K = s->K; p->act = s->act;
     return GDN_OK;

@@ -307,8 +307,9 @@ GDN_API int gdn_gates_bwd(const gdn_shape *shape, const void *a, const void *b, 
  *   - The buffers of a call may not overlap, except where a call says so.
  *   - Results are bitwise deterministic. How the scan splits a sequence and the projection its sums
  *     depends on all of a call's sizes, so there a row's last bits may differ between batch sizes.
- * Sizes: every size at least 1; a tensor of 2^40 elements or more, B or G above 65535, or rows
- * (B * T, M) of 2^31 - 65536 or more are GDN_ERR_UNSUPPORTED_SHAPE.
+ * Sizes: every size at least 1; a tensor of 2^40 elements or more, B or G above 65535, rows (B * T,
+ * M) of 2^31 - 65536 or more, more than 2^22 channels of the convolution or the scan, and M, N or K
+ * of the projection above 4000000 are GDN_ERR_UNSUPPORTED_SHAPE.
  */
 typedef enum {
     GDN_ACT_NONE = 0, /* x */

@@ -76,3 +76,21 @@ def test_linear_alignment(lib):
             assert call(lib, "gdn_linear_fwd", linear_shape(**kw), **{word: off}, **small) == code
     for kw, word, code in ((dict(M=5), "x", -2), (dict(M=5), "W", -2), (dict(M=1), "x", -4), (dict(N=1), "W", -4)):
         assert call(lib, "gdn_linear_bwd", linear_shape(**kw), **{word: off}, **small) == code
+
+
+@pytest.mark.parametrize("name,make,most,kw", [
+    ("gdn_conv", conv_shape, 1 << 22, lambda n: dict(B=1, T=2, C=n)),
+    ("gdn_scan", scan_shape, 1 << 22, lambda n: dict(B=1, T=2, C=n, N=1, G=1)),
+    ("gdn_norm", norm_shape, 65535, lambda n: dict(M=1, G=n, D=1)),
+    ("gdn_norm", norm_shape, 65536, lambda n: dict(M=1, G=1, D=n)),
+    ("gdn_linear", linear_shape, 4000000, lambda n: dict(M=n)),
+    ("gdn_linear", linear_shape, 4000000, lambda n: dict(N=n)),
+    ("gdn_linear", linear_shape, 4000000, lambda n: dict(K=n)),
+])
+def test_documented_sizes(lib, name, make, most, kw):
+    """The limits that the header gives, from both sides."""
+    size = getattr(lib, name + "_bwd_workspace_bytes")
+    assert size(ctypes.byref(make(**kw(most)))) > 0
+    assert call(lib, name + "_bwd", make(**kw(most)), **{"#workspace": 0}) == -4
+    for way in ("_fwd", "_bwd"):
+        assert call(lib, name + way, make(**kw(most + 1))) == UNSUPPORTED

@@ -59,6 +59,13 @@ struct GroupSum {
     }
 };
 
+// sum / D with one correction of the quotient by its remainder: the product with 1 / D alone is often an
+// ulp off, and a group of equal values then has a variance, which counts where ulp^2 nears eps.
+__device__ __forceinline__ float mean_of(float sum, int D, float inv_D) {
+    const float q = sum * inv_D;
+    return fmaf(fmaf(-q, (float)D, sum), inv_D, q);
+}
+
 __device__ __forceinline__ float block_sum(float x, float *buf) {
     x = warp_sum(x);
     __syncthreads();
@@ -213,7 +220,7 @@ __global__ void __launch_bounds__(kNormThreads) norm_fwd_kernel(NormParams p) {
         if (m + rows < p.M) fetch(m + rows);
         float mean = 0.f;
         if (p.center) {
-            mean = group_sum(x.total()) * inv_D;
+            mean = mean_of(group_sum(x.total()), p.D, inv_D);
 #pragma unroll
             for (int i = 0; i < P; ++i) x.p[i] = __fadd2_rn(x.p[i], make_float2(-mean, -mean));
             at.mask(x);
@@ -353,7 +360,7 @@ __global__ void __launch_bounds__(kNormThreads) norm_fwd_wide_kernel(NormParams 
     if (p.center) {
         float s = 0.f;
         for (int e = threadIdx.x; e < p.D; e += kNormThreads) s += to_f32(x[e]);
-        mean = block_sum(s, buf) * inv_D;
+        mean = mean_of(block_sum(s, buf), p.D, inv_D);
     }
     float ss = 0.f;
     for (int e = threadIdx.x; e < p.D; e += kNormThreads) {

@@ -256,3 +256,16 @@ def test_linear_long_sums(gdn, M, N, K, act):  # noqa: F811
         dy, Wl = _one_sign(r, M, K), _one_sign(r, K, N)
         dx = gdn.gdn_linear_bwd(r.normal(M, N), Wl, dy, want_dW=False, want_dbias=False)["dx"]
         check("long dx", {"dx": dx}, {"dx": _product64(dy, Wl.t())})
+
+
+@pytest.mark.parametrize("dtype", ["bf16", "f32"])
+@pytest.mark.parametrize("D", [3, 63, 100, 168, 700, 1025, 5000])
+def test_norm_of_large_constant_groups(gdn, D, dtype):  # noqa: F811
+    """Groups of equal values far from 0 (their sums are exact in float32): no variance, xh is 0 and the
+    output act(b). A mean that is an ulp off would give xh up to 0.02."""
+    c = torch.arange(128, 256, device="cuda").float() * 4                 # 512 to 1020
+    x = c[:, None].expand(128, 2 * D).contiguous().to(Draw(1, dtype).dtype)
+    b = torch.linspace(-2, 2, 2 * D, device="cuda")
+    y, stats = gdn.gdn_norm_fwd(x, 2, None, b, act="silu")
+    check("norm", {"y": y}, {"y": R.act("silu", b.double()).expand(128, 2 * D)})
+    assert torch.equal(stats[..., 0], c[:, None].expand(128, 2))

@@ -698,6 +698,7 @@ __global__ void __launch_bounds__(kTokThreads) linear_token_kernel(const __grid_
         if (res != nullptr) v = __fadd_rn(v, to_f32(res[(size_t)m * p.ldres + n]));
         static_cast<T *>(p.out)[o] = from_f32<T>(v);
     }
+    __syncthreads();                              // the loop above leaves warps divided; the cluster's barrier is for whole ones
     cluster_sync();                               // nobody leaves while its partial sums are read
     if (warp == 1) {
         tc_fence_after();

@@ -269,3 +269,18 @@ def test_norm_of_large_constant_groups(gdn, D, dtype):  # noqa: F811
     y, stats = gdn.gdn_norm_fwd(x, 2, None, b, act="silu")
     check("norm", {"y": y}, {"y": R.act("silu", b.double()).expand(128, 2 * D)})
     assert torch.equal(stats[..., 0], c[:, None].expand(128, 2))
+
+
+@pytest.mark.parametrize("case", [(3, 1, 24, 32, 1, "bf16", 0, True, None, True, True), (5, 1, 18, 23, 2, "f32", 0, True, [1, 0, 1, 1, 0], True, True),
+                                  (2, 1, 40, 64, 1, "f32", 0, True, None, False, True), (6, 1, 20, 49, 2, "bf16", 8, True, None, True, False),
+                                  (9, 1, 35, 20, 5, "bf16", 3, False, [1, 1, 0, 1, 1, 0, 1, 1, 1], True, True)], ids=str)
+def test_scan_steps_of_many_states(gdn, case):  # noqa: F811
+    """Single steps where 8 or 16 lanes share a channel, and their state updated in place."""
+    t, lens, _, _ = scan_inputs(case)
+    args = [t[k] for k in ("u", "dt", "A_log", "B", "C", "D", "dt_bias", "z")]
+    y, h, _ = gdn.gdn_scan_fwd(*args, t["h0"], lens)
+    y64, h64 = R.scan(lens=lens, **{k: d64(clean(v, lens) if k in ("u", "dt", "B", "C", "z") else v) for k, v in t.items()})
+    check("scan", {"y": y, "h_T": h}, {"y": y64, "h_T": h64})
+    if t["h0"] is not None:
+        y2, h2, _ = gdn.gdn_scan_fwd(*args, t["h0"], lens, h_T=t["h0"])
+        assert h2 is t["h0"] and torch.equal(h2, h) and torch.equal(y2, y)

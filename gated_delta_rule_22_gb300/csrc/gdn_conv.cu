@@ -299,10 +299,11 @@ __global__ void __launch_bounds__(32 * kConvBwdWarps, 2) conv_bwd_kernel(ConvPar
             float2 s[P];
 #pragma unroll
             for (int q = 0; q < P; ++q) {
-                if (valid) {             // 0 x a carried state that is not finite would be NaN
-                    db[q] = __fadd2_rn(db[q], dwin[W - 1][q]);
+                db[q] = __fadd2_rn(db[q], dwin[W - 1][q]);
 #pragma unroll
-                    for (int j = 0; j < W; ++j) dw[j][q] = __ffma2_rn(dwin[W - 1][q], win[j][q], dw[j][q]);
+                for (int j = 0; j < W; ++j) {    // 0 x a carried state that is not finite would be NaN
+                    const float2 in = valid ? win[j][q] : make_float2(0.f, 0.f);
+                    dw[j][q] = __ffma2_rn(dwin[W - 1][q], in, dw[j][q]);
                 }
                 s[q] = __fmul2_rn(w[0][q], dwin[W - 1][q]);
 #pragma unroll

@@ -47,9 +47,9 @@ _declared = None
 def _library():
     """libgdn.so with the signatures of the layer operators declared."""
     global _declared
+    if _declared is not None:
+        return _declared
     lib = load_library()
-    if _declared is lib:
-        return lib
     P = ctypes.POINTER
     for name, shape, args in (
             ("gdn_conv_fwd", GdnConvShape, [_VP] * 8), ("gdn_conv_bwd", GdnConvShape, [_VP] * 12 + [_SZ, _VP]),
@@ -84,9 +84,10 @@ def _at(t):
 
 def _stream_of(device):
     """binding._stream"""
-    if device.index != _current_device():
+    index = device.index
+    if index != _current_device():
         raise _other_device(device, _current_device())
-    return torch._C._cuda_getCurrentRawStream(device.index)
+    return _raw_stream(index)
 
 
 def _type(t):
@@ -148,7 +149,7 @@ def _raise(name, rc):
 # A single token's step takes the GPU a few microseconds, less than a Python call with this many
 # arguments: the code below looks up, converts and calls no more than it has to.
 _empty, _empty_like, _byref = torch.empty, torch.empty_like, ctypes.byref
-_current_device = torch._C._cuda_getDevice
+_current_device, _raw_stream = torch._C._cuda_getDevice, torch._C._cuda_getCurrentRawStream
 _BF16, _F32, _I32 = torch.bfloat16, torch.float32, torch.int32
 
 
@@ -172,7 +173,7 @@ def _conv_args(x, w, bias, s0, lens, act):
         _check("s0", s0, (B, W - 1, C), dt, dev)
     if lens is not None:
         _check("lens", lens, (B,), _I32, dev)
-    return GdnConvShape(B, T, C, W, _act(act), _type(x), ld)
+    return GdnConvShape(B, T, C, W, _act(act), _type(x), ld), B, T, C, W
 
 
 def gdn_conv_fwd(x, w, bias=None, s0=None, lens=None, *, act="silu", y=None, s_T=None, want_s_T=True, stream=None):
@@ -182,8 +183,8 @@ def gdn_conv_fwd(x, w, bias=None, s0=None, lens=None, *, act="silu", y=None, s_T
     if stream is not None:
         return _under(stream, gdn_conv_fwd, locals())
     lib = _library()
-    shape = _conv_args(x, w, bias, s0, lens, act)
-    B, T, C, W, dev, dt = shape.B, shape.T, shape.C, shape.W, x.device, x.dtype
+    shape, B, T, C, W = _conv_args(x, w, bias, s0, lens, act)
+    dev, dt = x.device, x.dtype
     if y is not None:
         _check("y", y, (B, T, C), dt, dev)
     if s_T is not None:
@@ -210,8 +211,8 @@ def gdn_conv_bwd(x, w, dy, bias=None, s0=None, lens=None, ds_T=None, *, act="sil
     if stream is not None:
         return _under(stream, gdn_conv_bwd, locals())
     lib = _library()
-    shape = _conv_args(x, w, bias, s0, lens, act)
-    B, T, C, W, dev, dt = shape.B, shape.T, shape.C, shape.W, x.device, x.dtype
+    shape, B, T, C, W = _conv_args(x, w, bias, s0, lens, act)
+    dev, dt = x.device, x.dtype
     _check("dy", dy, (B, T, C), dt, dev)
     if ds_T is not None:
         _check("ds_T", ds_T, (B, W - 1, C), dt, dev)
@@ -245,7 +246,7 @@ def _scan_args(u, dt, A_log, B, C, D, dt_bias, z, lens):
         _check("dt_bias", dt_bias, (Cn,), _F32, dev)
     if lens is not None:
         _check("lens", lens, (Bn,), _I32, dev)
-    return GdnScanShape(Bn, T, Cn, N, G, _type(u), ldu, lddt, ldz, ldB, ldC)
+    return GdnScanShape(Bn, T, Cn, N, G, _type(u), ldu, lddt, ldz, ldB, ldC), Bn, T, Cn, N
 
 
 def gdn_scan_ckpt_bytes(shape: GdnScanShape) -> int:
@@ -273,8 +274,8 @@ def gdn_scan_fwd(u, dt, A_log, B, C, D=None, dt_bias=None, z=None, h0=None, lens
     if stream is not None:
         return _under(stream, gdn_scan_fwd, locals())
     lib = _library()
-    shape = _scan_args(u, dt, A_log, B, C, D, dt_bias, z, lens)
-    Bn, T, Cn, N, dev = shape.B, shape.T, shape.C, shape.N, u.device
+    shape, Bn, T, Cn, N = _scan_args(u, dt, A_log, B, C, D, dt_bias, z, lens)
+    dev = u.device
     if h0 is not None:
         _check("h0", h0, (Bn, Cn, N), _F32, dev)
     if y is not None:
@@ -291,7 +292,8 @@ def gdn_scan_fwd(u, dt, A_log, B, C, D=None, dt_bias=None, z=None, h0=None, lens
         h_T = _empty((Bn, Cn, N), dtype=_F32, device=dev) if h0 is None else _empty_like(h0)
     if ckpt is None and want_ckpt:
         ckpt = _empty(_scan_ckpt_shape(Bn, T, Cn, N), dtype=_F32, device=dev)
-    workspace = _scratch("workspace", workspace, 0 if T == 1 else lib.gdn_scan_fwd_workspace_bytes(ctypes.byref(shape)), dev)
+    if workspace is not None or T > 1:                 # a single step needs none
+        workspace = _scratch("workspace", workspace, lib.gdn_scan_fwd_workspace_bytes(ctypes.byref(shape)), dev)
     rc = lib.gdn_scan_fwd(_byref(shape), u.data_ptr(), dt.data_ptr(), A_log.data_ptr(), B.data_ptr(), C.data_ptr(), _at(D), _at(dt_bias), _at(z), _at(h0),
          _at(lens), _at(y), _at(h_T), _at(ckpt), _size(ckpt), _at(workspace), _size(workspace), _stream_of(dev))
     if rc:
@@ -306,8 +308,8 @@ def gdn_scan_bwd(u, dt, A_log, B, C, ckpt, dy, D=None, dt_bias=None, z=None, len
     if stream is not None:
         return _under(stream, gdn_scan_bwd, locals())
     lib = _library()
-    shape = _scan_args(u, dt, A_log, B, C, D, dt_bias, z, lens)
-    Bn, T, Cn, N, G, dev, ty = shape.B, shape.T, shape.C, shape.N, shape.G, u.device, u.dtype
+    shape, Bn, T, Cn, N = _scan_args(u, dt, A_log, B, C, D, dt_bias, z, lens)
+    dev, ty = u.device, u.dtype
     _check("ckpt", ckpt, _scan_ckpt_shape(Bn, T, Cn, N), _F32, dev)
     _check("dy", dy, (Bn, T, Cn), ty, dev)
     if dh_T is not None:

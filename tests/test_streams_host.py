@@ -105,7 +105,7 @@ def test_tensors_of_a_device_that_is_not_current(monkeypatch):
     monkeypatch.setattr(Ly, "_current_device", lambda: 0, raising=False)
     monkeypatch.setattr(torch.cuda, "current_device", lambda: 0)
     monkeypatch.setattr(torch.cuda, "current_stream", lambda device: Stream(0))
-    monkeypatch.setattr(torch._C, "_cuda_getCurrentRawStream", lambda index: 0)
+    monkeypatch.setattr(Ly, "_raw_stream", lambda index: 0)
     for stream in (B._stream, Ly._stream_of):
         with pytest.raises(ValueError, match="current device"):
             stream(other)

@@ -148,16 +148,6 @@ __global__ void __launch_bounds__(kRevThreads, LITE ? 4 : kRevCtas) scan_bwd_ker
     // NaN of the zeros that they would add.
     const int live = min(q.last, max(q.first, (L + TT - 1) / TT));
     if (live > q.first) fetch(live - 1);
-    if (!LITE)
-        for (int t = live * TT + ts; t < min(q.last * TT, p.T); t += 8) {
-            const float zero[V] = {};
-            const size_t at = row + (size_t)t * p.Cn;
-            store_channels<T, V>(static_cast<T *>(p.du) + at, nv, VEC, zero);
-            store_channels<T, V>(static_cast<T *>(p.ddt) + at, nv, VEC, zero);
-            if (p.dz != nullptr) store_channels<T, V>(static_cast<T *>(p.dz) + at, nv, VEC, zero);
-            float *part = p.part_bc + ((((size_t)q.blk * p.Bn + q.b) * p.T + t) * p.G + q.g) * (2 * p.N);
-            for (int n = tid & 15; n < 2 * p.N; n += 16) part[n] = 0.f;
-        }
     for (int i = tid; i < CH; i += kRevThreads) {
         sm.D[i] = p.D != nullptr && i < q.nc ? p.D[q.c0 + i] : 0.f;
         sm.bias[i] = p.dt_bias != nullptr && i < q.nc ? p.dt_bias[q.c0 + i] : 0.f;
@@ -440,6 +430,15 @@ __global__ void __launch_bounds__(kRevThreads, LITE ? 4 : kRevCtas) scan_bwd_ker
             p.seg_sum[((size_t)q.seg * p.Bn + q.b) * p.Cn + q.c0 + tid] = x;
         }
         return;
+    }
+    for (int t = live * TT + ts; t < min(q.last * TT, p.T); t += 8) {
+        const float zero[V] = {};
+        const size_t at = row + (size_t)t * p.Cn;
+        store_channels<T, V>(static_cast<T *>(p.du) + at, nv, VEC, zero);
+        store_channels<T, V>(static_cast<T *>(p.ddt) + at, nv, VEC, zero);
+        if (p.dz != nullptr) store_channels<T, V>(static_cast<T *>(p.dz) + at, nv, VEC, zero);
+        float *part = p.part_bc + ((((size_t)q.blk * p.Bn + q.b) * p.T + t) * p.G + q.g) * (2 * p.N);
+        for (int n = tid & 15; n < 2 * p.N; n += 16) part[n] = 0.f;
     }
     if (p.segs == 1 && p.dh0 != nullptr) store_mine(p.dh0 + q.b * states, ge);
     float *part = p.part_c + ((size_t)q.seg * p.Bn + q.b) * (p.N + 2) * p.Cn;

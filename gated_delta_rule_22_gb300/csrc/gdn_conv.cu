@@ -7,12 +7,12 @@
 //     dpre = dy act'(pre),   dx~[s] = sum_j w[j] dpre[s+W-1-j] (+ ds_T where s is one of the last
 //     W-1 inputs),   dw[j] = sum_t dpre[t] x~[t-W+1+j],   dbias = sum_t dpre[t]
 //
-// A thread takes V neighbouring channels (16 bytes) and walks a run of steps with the last W-1
-// inputs in registers, so that x is read once and the taps once per run. Each channel's W products
+// A thread takes V neighbouring channels (four, fewer where they are not aligned) and walks a run of
+// steps with the last W-1 inputs in registers, so that x is read once and the taps once per run. Each channel's W products
 // are far below the memory time: the kernels are bound by the bytes of x and y (and dy, dx).
 // Measured on 8 x 4096 steps of 8192 channels, 4 taps, SiLU, bf16: forward 161 us, 6.7 TB/s, a plain
 // copy's rate; backward 290 us, 5.6 TB/s of x, dy and dx, instructions issuing in 53 % of the cycles:
-// it forms pre and its sigmoid again, and adds up W + 1 sums per channel.
+// it forms pre and its sigmoid again, and adds up W + 1 sums per channel. float32: 322 and 497 us.
 #include "gdn_layer.cuh"
 
 namespace gdn {

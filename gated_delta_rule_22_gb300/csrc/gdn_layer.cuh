@@ -122,8 +122,9 @@ __device__ __forceinline__ float rcp(float x) {
     asm("rcp.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
     return y;
 }
-// 1 / (1 + exp(-x)) from the hardware's exp2 and reciprocal: a relative error of a few 2^-23 (an
-// exponent that overflows gives 1 / inf = 0).
+// 1 / (1 + exp(-x)) from the hardware's exp2 and reciprocal: a relative error of a few 2^-23, and for
+// negative x of |x| 2^-24 more, as the product x log2 e is rounded (20 x 2^-23 at -40, where the value
+// itself is 4e-18). An exponent that overflows gives 1 / inf = 0.
 __device__ __forceinline__ float sigmoid_hw(float x) { return rcp(1.f + ex2(-x * kLog2e)); }
 __device__ __forceinline__ float2 sigmoid2_hw(float2 x) {
     const float2 e = __fmul2_rn(x, make_float2(-kLog2e, -kLog2e));
@@ -140,9 +141,10 @@ __device__ __forceinline__ float dgelu_f(float x) {
     return fmaf(x, 0.3989422804f * ex2(-0.5f * kLog2e * x * x), 0.5f * (1.f + erff(x * 0.70710678f)));
 }
 // softplus(x) = max(x, 0) + log1p(exp(-|x|)), and the logistic function of x from the same exponential.
-// exp(-|x|): the product with log2 e is carried to twice float32, so that the hardware's exp2 sees no
-// rounded argument. log1p(e) for e in [0, 1]: 2 atanh(e / (2 + e)) by the series of atanh, whose
-// argument is at most 1/3 (seven terms: 1.4e-8 relative), with full relative accuracy for small e.
+// exp(-|x|): the product with log2 e is carried to twice float32 (Dekker's two-term product, by fused
+// multiply-adds), so that the hardware's exp2 sees no rounded argument. log1p(e) for e in [0, 1]: 2 atanh(e / (2 + e)) by the series of atanh, whose
+// argument, a quotient with one Newton correction by its remainder, is at most 1/3 (seven terms:
+// 1.4e-8 relative), with full relative accuracy for small e.
 __device__ __forceinline__ void softplus_full(float x, float &sp, float &sg) {
     const float ax = fminf(fabsf(x), 200.f), hi = -ax * kLog2e;
     const float lo = fmaf(-ax, 1.925963033e-8f, fmaf(-ax, kLog2e, -hi));

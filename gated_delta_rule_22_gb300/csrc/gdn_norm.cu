@@ -8,7 +8,7 @@
 // Bound by memory: x (and z, dy) are read once and stay in registers between the statistics and
 // the output. The mean is subtracted before the squares are summed. Measured on 32768 rows of 32
 // groups of 128 channels with a gate, bf16: forward 132 us, 6.1 TB/s; backward 243 us, 5.5 TB/s of x, z,
-// dy, dx and dz. 8192 rows of one group of 4096: 41 and 92 us, 4.9 and 3.6 TB/s, a barrier per sum.
+// dy, dx and dz (float32: 253 and 486 us). 8192 rows of one group of 4096: 41 and 92 us, 4.9 and 3.6 TB/s, a barrier per sum.
 #include "gdn_layer.cuh"
 
 #include <type_traits>

@@ -34,7 +34,8 @@ struct FwdSmem {
 // against 138; of 4096 x 64 states 723 against 438).
 //
 // Measured on 2 x 2048 steps of 4096 channels x 16 states, bf16, with checkpoints: 134 us, against 153 with
-// one channel per lane; 1 x 4096 steps, split, without checkpoints: 60 us for the ends, 90 for the outputs.
+// one channel per lane; 1 x 4096 steps, split, without checkpoints: 60 us for the ends, 90 for the outputs
+// (float32: 142 us without checkpoints; 164 for the split).
 // Not the exponentials bind (29 us at 32 per clock and SM) nor the memory (20 us, and 10 for
 // checkpoints), but the loads from shared memory and the latency of one or two state warps per scheduler.
 // CTAS per SM: three, with 80 registers, where there are more CTAs than two per SM (the split prompt

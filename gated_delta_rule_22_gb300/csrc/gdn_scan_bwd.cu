@@ -431,6 +431,7 @@ __global__ void __launch_bounds__(kRevThreads, LITE ? 4 : kRevCtas) scan_bwd_ker
         }
         return;
     }
+    if (p.segs == 1 && p.dh0 != nullptr) store_mine(p.dh0 + q.b * states, ge);
     for (int t = live * TT + ts; t < min(q.last * TT, p.T); t += 8) {
         const float zero[V] = {};
         const size_t at = row + (size_t)t * p.Cn;
@@ -440,7 +441,6 @@ __global__ void __launch_bounds__(kRevThreads, LITE ? 4 : kRevCtas) scan_bwd_ker
         float *part = p.part_bc + ((((size_t)q.blk * p.Bn + q.b) * p.T + t) * p.G + q.g) * (2 * p.N);
         for (int n = tid & 15; n < 2 * p.N; n += 16) part[n] = 0.f;
     }
-    if (p.segs == 1 && p.dh0 != nullptr) store_mine(p.dh0 + q.b * states, ge);
     float *part = p.part_c + ((size_t)q.seg * p.Bn + q.b) * (p.N + 2) * p.Cn;
 #pragma unroll
     for (int r = 0; r < 2; ++r) {

@@ -80,7 +80,8 @@ struct GemmParams {
 
 // One output of a float32 product by a warp, in float32 arithmetic on the CUDA cores, for outputs that
 // the six products made NaN: an infinity by a zero or opposite second or third term is not an infinity
-// by the value. The sum ends early where it is NaN.
+// by the value. The sum ends early where it is NaN. Meant for few outputs: 2048 x 4096 x 8192 takes 0.78 ms
+// where all sums are finite, 14 ms where everything is NaN, 0.34 s with an infinity in every row of x.
 template <bool A_MN, bool B_MN>
 __device__ __forceinline__ float dot_of_terms(const GemmParams &p, int m, int n) {
     const int lane = threadIdx.x & 31;

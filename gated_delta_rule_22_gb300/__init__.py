@@ -16,9 +16,11 @@ from .binding import (  # noqa: F401
 )
 # The layer operators' binding needs torch at import; the rest of the package does not before a call.
 _LAYER = (
-    "GDN_ACT_GELU", "GDN_ACT_NONE", "GDN_ACT_SILU", "GdnConvShape", "GdnLinearShape", "GdnNormShape", "GdnScanShape", "gdn_conv_bwd",
-    "gdn_conv_bwd_workspace_bytes", "gdn_conv_fwd", "gdn_linear_bwd", "gdn_linear_bwd_workspace_bytes", "gdn_linear_fwd",
-    "gdn_linear_fwd_workspace_bytes", "gdn_norm_bwd", "gdn_norm_bwd_workspace_bytes", "gdn_norm_fwd", "gdn_scan_bwd",
+    "GDN_ACT_GELU", "GDN_ACT_NONE", "GDN_ACT_SILU", "GdnConvShape", "GdnLinattnShape", "GdnLinearShape", "GdnNormShape", "GdnResnormShape",
+    "GdnScanShape", "gdn_conv_bwd", "gdn_conv_bwd_workspace_bytes", "gdn_conv_fwd", "gdn_linattn_bwd", "gdn_linattn_bwd_workspace_bytes",
+    "gdn_linattn_fwd", "gdn_linattn_fwd_workspace_bytes", "gdn_linear_bwd", "gdn_linear_bwd_workspace_bytes", "gdn_linear_fwd",
+    "gdn_linear_fwd_workspace_bytes", "gdn_norm_bwd", "gdn_norm_bwd_workspace_bytes", "gdn_norm_fwd", "gdn_resnorm_bwd",
+    "gdn_resnorm_bwd_workspace_bytes", "gdn_resnorm_fwd", "gdn_scan_bwd",
     "gdn_scan_bwd_workspace_bytes", "gdn_scan_ckpt_bytes", "gdn_scan_fwd", "gdn_scan_fwd_workspace_bytes",
 )
 

@@ -1,6 +1,6 @@
 // gdn_layer.cuh -- parameter blocks, launchers and device helpers of the layer operators: the
-// short causal convolution, the selective state space scan, the group norm and the projection
-// (internal; not part of the C ABI).
+// short causal convolution, the selective state space scan, the linear attention with a decay, the
+// group norm, the norms around a block and the projection (internal; not part of the C ABI).
 #pragma once
 
 #include "gdn_common.cuh"
@@ -71,6 +71,48 @@ struct LinearParams {
     int M, N, K, act;
 };
 
+// One sweep of the linear attention: over the steps of a row, in order or (rev) backwards, with a state
+// X of [Dc][Db], started from init:
+//     X <- g X + outer(c_t, b_t)  (rev: the first step does not decay init),   out_t = X a_t
+// The forward is one, and so is each gradient: dq is (dy, v, k), dk backwards (v, dy, q), dv backwards
+// (k, q, dy), for (a, b, c).
+struct LinattnSweep {
+    const void *a, *b, *c;
+    const float *init;         // the state before the first step taken; null: zeros
+    float *last;               // the state behind the last (rev: decayed once more); null: not wanted
+    void *out;                 // [B][T][Ho][Dc] in the call's type, or (sums) float32 by value head
+    long long lda, ldb, ldc;   // elements between steps
+    int a_keys, b_keys, c_keys;   // the operand's heads are key heads
+    int Db, Dc, rev;
+    int init_t;                // init lies transposed, [Db][Dc]
+    int sums;                  // out is float32 [B][T][Hv][Dc], to be summed over the value heads of a key head
+};
+
+struct LinattnParams {
+    LinattnSweep sweep[3];
+    int sweeps;
+    const float *g;
+    const int *lens;
+    int *status;
+    int B, T, Hk, Hv, Dk, Dv;
+    // backward with shared keys: the float32 sums of dq and dk by value head, and their outputs
+    float *part_dq, *part_dk;
+    void *dq, *dk;
+};
+
+struct ResnormParams {
+    const void *x, *h, *z, *dy, *dr;
+    const float *scale, *w_post, *w_pre, *stats_in;
+    void *r, *y, *dx, *dh, *dz;
+    float *stats, *dscale, *dw_post, *dw_pre;
+    float *part;               // backward: [ctas][3][D] partial sums of dscale, dw_post, dw_pre
+    float *part_z;             // backward, gate_rows > 1: [units][D] partial sums of dz before act'(z)
+    long long ldx, ldh, ldz;
+    int M, D, gate_rows, act, post, pre;
+    int unit, per_gate, units, ctas;   // backward: rows of a unit, units of a row of z, units, CTAs that take them
+    float eps;
+};
+
 constexpr int kScanTile = 16;   // steps between the scan's checkpoints, and of one staged tile
 constexpr int kLinearFewRows = 32;   // rows that the projection's forward streams on the CUDA cores where TMA cannot read
 
@@ -80,6 +122,7 @@ int scan_lanes(int N);                              // lanes that share one chan
 int scan_blocks(int C, int G, int N);               // channel blocks of one group
 void scan_split(ScanParams *p, bool bwd);           // chooses segs and seg_len
 int norm_bwd_slices(int M, int G, int D, int dtype);
+void resnorm_units(ResnormParams *p, int dtype);   // chooses unit, per_gate, units and ctas
 size_t linear_fwd_workspace(const LinearParams &p, int dtype);
 size_t linear_bwd_workspace(const LinearParams &p, int dtype);
 
@@ -90,6 +133,10 @@ cudaError_t launch_scan_fwd(const ScanParams &p, int dtype, cudaStream_t s);
 cudaError_t launch_scan_bwd(const ScanParams &p, int dtype, cudaStream_t s);
 cudaError_t launch_norm_fwd(const NormParams &p, int dtype, cudaStream_t s);
 cudaError_t launch_norm_bwd(const NormParams &p, int dtype, cudaStream_t s);
+cudaError_t launch_linattn_step(const LinattnParams &p, int dtype, cudaStream_t s);    // T = 1, the forward's sweep
+cudaError_t launch_linattn_steps(const LinattnParams &p, int dtype, cudaStream_t s);   // all sweeps, then the sums over heads
+cudaError_t launch_resnorm_fwd(const ResnormParams &p, int dtype, cudaStream_t s);
+cudaError_t launch_resnorm_bwd(const ResnormParams &p, int dtype, cudaStream_t s);
 // These return a GDN_* code (they encode tensor maps).
 int launch_linear_fwd(const LinearParams &p, int dtype, cudaStream_t s);
 int launch_linear_bwd(const LinearParams &p, int dtype, cudaStream_t s);

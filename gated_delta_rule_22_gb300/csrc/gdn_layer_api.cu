@@ -135,6 +135,54 @@ int linear_plan(const gdn_linear_shape *s, gdn::LinearParams *p) {
     return GDN_OK;
 }
 
+int linattn_plan(const gdn_linattn_shape *s, gdn::LinattnParams *p, long long (&ld)[3]) {
+    if (s == nullptr || s->B <= 0 || s->T <= 0 || s->Hk <= 0 || s->Hv <= 0 || s->Dk <= 0 || s->Dv <= 0) return GDN_ERR_INVALID_ARG;
+    if (s->ldq < 0 || s->ldk < 0 || s->ldv < 0 || !dtype_ok(s->dtype)) return GDN_ERR_INVALID_ARG;
+    if (s->Hv % s->Hk != 0 || s->Dk > 256 || s->Dv > 256 || s->B > 65535 || s->Hv > 65535) return GDN_ERR_UNSUPPORTED_SHAPE;
+    *p = {};
+    const long long keys = (long long)s->Hk * s->Dk, values = (long long)s->Hv * s->Dv;
+    int rc;
+    if ((rc = row_stride(s->ldq, keys, &ld[0])) != GDN_OK || (rc = row_stride(s->ldk, keys, &ld[1])) != GDN_OK ||
+        (rc = row_stride(s->ldv, values, &ld[2])) != GDN_OK)
+        return rc;
+    const double rows = (double)s->B * s->T;
+    long long widest = (long long)s->Hv * s->Dk;        // of dq and dk by value head
+    for (long long w : ld) widest = w > widest ? w : widest;
+    if (rows >= kMaxRows || rows * (double)widest >= kMaxElements || (double)s->B * s->Hv * s->Dk * s->Dv >= kMaxElements)
+        return GDN_ERR_UNSUPPORTED_SHAPE;
+    p->B = s->B; p->T = s->T; p->Hk = s->Hk; p->Hv = s->Hv; p->Dk = s->Dk; p->Dv = s->Dv;
+    return GDN_OK;
+}
+
+// Backward with shared keys: dq and dk by value head, float32.
+size_t linattn_part_bytes(const gdn::LinattnParams &p) {
+    return p.Hv == p.Hk ? 0 : up256((size_t)p.B * p.T * p.Hv * p.Dk * 4);
+}
+size_t linattn_bwd_ws(const gdn::LinattnParams &p) { return 2 * linattn_part_bytes(p); }
+
+int resnorm_plan(const gdn_resnorm_shape *s, gdn::ResnormParams *p) {
+    if (s == nullptr || s->M <= 0 || s->D <= 0 || s->gate_rows < 0 || s->ldx < 0 || s->ldh < 0 || s->ldz < 0) return GDN_ERR_INVALID_ARG;
+    if (!dtype_ok(s->dtype) || !act_ok(s->act) || !(s->eps > 0.f) || !isfinite(s->eps)) return GDN_ERR_INVALID_ARG;
+    *p = {};
+    p->gate_rows = s->gate_rows == 0 ? 1 : s->gate_rows;
+    if (s->M % p->gate_rows != 0) return GDN_ERR_INVALID_ARG;
+    if (s->M >= kMaxRows || s->D > 16384) return GDN_ERR_UNSUPPORTED_SHAPE;
+    int rc;
+    if ((rc = row_stride(s->ldx, s->D, &p->ldx)) != GDN_OK || (rc = row_stride(s->ldh, s->D, &p->ldh)) != GDN_OK ||
+        (rc = row_stride(s->ldz, s->D, &p->ldz)) != GDN_OK)
+        return rc;
+    for (long long ld : {p->ldx, p->ldh, p->ldz})
+        if ((double)s->M * (double)ld >= kMaxElements) return GDN_ERR_UNSUPPORTED_SHAPE;
+    p->M = s->M; p->D = s->D; p->act = s->act; p->post = s->post != 0; p->pre = s->pre != 0; p->eps = s->eps;
+    gdn::resnorm_units(p, s->dtype);
+    return GDN_OK;
+}
+
+size_t resnorm_part_bytes(const gdn::ResnormParams &p) { return up256((size_t)p.ctas * 3 * p.D * 4); }
+size_t resnorm_ws(const gdn::ResnormParams &p) {
+    return resnorm_part_bytes(p) + (p.gate_rows > 1 ? up256((size_t)p.units * p.D * 4) : 0);
+}
+
 // bf16 x and W with packed rows are read in place by TMA, so they are 16-byte aligned like every packed
 // tensor. A single row has room for a copy, and the forward of few rows reads any address.
 int linear_operands_ok(const gdn::LinearParams &p, int dtype, const void *x, const void *W, bool bwd) {
@@ -320,6 +368,100 @@ int gdn_linear_bwd(const gdn_linear_shape *shape, const void *x, const void *W, 
     p.x = x; p.W = W; p.pre_in = pre; p.dy = dy; p.dx = dx; p.dW = dW; p.dbias = dbias; p.ws = static_cast<char *>(workspace);
     if ((rc = gdn::api_device_status_address(&p.status)) != GDN_OK) return rc;
     return gdn::launch_linear_bwd(p, shape->dtype, (cudaStream_t)stream);
+}
+
+size_t gdn_linattn_fwd_workspace_bytes(const gdn_linattn_shape *) { return 0; }
+
+size_t gdn_linattn_bwd_workspace_bytes(const gdn_linattn_shape *shape) {
+    gdn::LinattnParams p;
+    long long ld[3];
+    return linattn_plan(shape, &p, ld) == GDN_OK ? linattn_bwd_ws(p) : 0;
+}
+
+int gdn_linattn_fwd(const gdn_linattn_shape *shape, const void *q, const void *k, const void *v, const float *g, const float *S0,
+                    const int *lens, void *y, float *S_T, void *workspace, size_t, void *stream) {
+    gdn::LinattnParams p;
+    long long ld[3];
+    int rc = linattn_plan(shape, &p, ld);
+    if (rc != GDN_OK) return rc;
+    if (!q || !k || !v || !g || !y) return GDN_ERR_INVALID_ARG;
+    if (S_T != nullptr && S_T == S0 && p.T != 1) return GDN_ERR_INVALID_ARG;
+    if ((rc = packed_ok({g, S0, lens, y, S_T, workspace})) != GDN_OK || (rc = strided_ok({q, k, v}, elem(shape->dtype))) != GDN_OK) return rc;
+    gdn::api_clear_error();
+    p.g = g; p.lens = lens;
+    p.sweeps = 1;
+    p.sweep[0] = {q, k, v, S0, S_T, y, ld[0], ld[1], ld[2], 1, 1, 0, p.Dk, p.Dv, 0, 0, 0};
+    if (p.T == 1) return gdn::api_cuda_status(gdn::launch_linattn_step(p, shape->dtype, (cudaStream_t)stream));
+    return gdn::api_cuda_status(gdn::launch_linattn_steps(p, shape->dtype, (cudaStream_t)stream));
+}
+
+int gdn_linattn_bwd(const gdn_linattn_shape *shape, const void *q, const void *k, const void *v, const float *g, const float *S0,
+                    const int *lens, const void *dy, const float *dS_T, void *dq, void *dk, void *dv, float *dS0, void *workspace,
+                    size_t workspace_bytes, void *stream) {
+    gdn::LinattnParams p;
+    long long ld[3];
+    int rc = linattn_plan(shape, &p, ld);
+    if (rc != GDN_OK) return rc;
+    const size_t need = linattn_bwd_ws(p);
+    if (!q || !k || !v || !g || !dy || !dq || !dk || !dv || (need > 0 && !workspace)) return GDN_ERR_INVALID_ARG;
+    if ((rc = packed_ok({g, S0, lens, dy, dS_T, dq, dk, dv, dS0, workspace})) != GDN_OK ||
+        (rc = strided_ok({q, k, v}, elem(shape->dtype))) != GDN_OK)
+        return rc;
+    if (workspace_bytes < need) return GDN_ERR_WORKSPACE_TOO_SMALL;
+    gdn::api_clear_error();
+    p.g = g; p.lens = lens;
+    const int shared = p.Hv != p.Hk;
+    void *out_q = dq, *out_k = dk;
+    if (shared) {
+        p.part_dq = static_cast<float *>(workspace);
+        p.part_dk = reinterpret_cast<float *>(static_cast<char *>(workspace) + linattn_part_bytes(p));
+        p.dq = dq; p.dk = dk;
+        out_q = p.part_dq; out_k = p.part_dk;
+    }
+    const long long ldy = (long long)p.Hv * p.Dv;
+    p.sweeps = 3;
+    p.sweep[0] = {dy, v, k, S0, nullptr, out_q, ldy, ld[2], ld[1], 0, 0, 1, p.Dv, p.Dk, 0, 1, shared};
+    p.sweep[1] = {v, dy, q, dS_T, nullptr, out_k, ld[2], ldy, ld[0], 0, 0, 1, p.Dv, p.Dk, 1, 1, shared};
+    p.sweep[2] = {k, q, dy, dS_T, dS0, dv, ld[1], ld[0], ldy, 1, 1, 0, p.Dk, p.Dv, 1, 0, 0};
+    return gdn::api_cuda_status(gdn::launch_linattn_steps(p, shape->dtype, (cudaStream_t)stream));
+}
+
+int gdn_resnorm_fwd(const gdn_resnorm_shape *shape, const void *x, const void *h, const void *z, const float *scale, const float *w_post,
+                    const float *w_pre, void *r, void *y, float *stats, void *stream) {
+    gdn::ResnormParams p;
+    int rc = resnorm_plan(shape, &p);
+    if (rc != GDN_OK) return rc;
+    if (!x || !h || !r || (p.pre != 0) != (y != nullptr) || (w_post && !p.post) || (w_pre && !p.pre)) return GDN_ERR_INVALID_ARG;
+    if (r == x && p.ldx != p.D) return GDN_ERR_INVALID_ARG;
+    if ((rc = packed_ok({scale, w_post, w_pre, r, y, stats})) != GDN_OK || (rc = strided_ok({x, h, z}, elem(shape->dtype))) != GDN_OK) return rc;
+    gdn::api_clear_error();
+    p.x = x; p.h = h; p.z = z; p.scale = scale; p.w_post = w_post; p.w_pre = w_pre; p.r = r; p.y = y; p.stats = stats;
+    return gdn::api_cuda_status(gdn::launch_resnorm_fwd(p, shape->dtype, (cudaStream_t)stream));
+}
+
+size_t gdn_resnorm_bwd_workspace_bytes(const gdn_resnorm_shape *shape) {
+    gdn::ResnormParams p;
+    return resnorm_plan(shape, &p) == GDN_OK ? resnorm_ws(p) : 0;
+}
+
+int gdn_resnorm_bwd(const gdn_resnorm_shape *shape, const void *x, const void *h, const void *z, const float *scale, const float *w_post,
+                    const float *w_pre, const float *stats, const void *dy, const void *dr, void *dx, void *dh, void *dz, float *dscale,
+                    float *dw_post, float *dw_pre, void *workspace, size_t workspace_bytes, void *stream) {
+    gdn::ResnormParams p;
+    int rc = resnorm_plan(shape, &p);
+    if (rc != GDN_OK) return rc;
+    if (!x || !h || !stats || !dx || !dh || !workspace || (p.pre != 0) != (dy != nullptr) || (!p.pre && !dr)) return GDN_ERR_INVALID_ARG;
+    if ((dz && !z) || ((w_post || dw_post) && !p.post) || ((w_pre || dw_pre) && !p.pre)) return GDN_ERR_INVALID_ARG;
+    if ((rc = packed_ok({scale, w_post, w_pre, stats, dy, dr, dx, dh, dz, dscale, dw_post, dw_pre, workspace})) != GDN_OK ||
+        (rc = strided_ok({x, h, z}, elem(shape->dtype))) != GDN_OK)
+        return rc;
+    if (workspace_bytes < resnorm_ws(p)) return GDN_ERR_WORKSPACE_TOO_SMALL;
+    gdn::api_clear_error();
+    p.x = x; p.h = h; p.z = z; p.scale = scale; p.w_post = w_post; p.w_pre = w_pre; p.stats_in = stats; p.dy = dy; p.dr = dr;
+    p.dx = dx; p.dh = dh; p.dz = dz; p.dscale = dscale; p.dw_post = dw_post; p.dw_pre = dw_pre;
+    p.part = static_cast<float *>(workspace);
+    p.part_z = reinterpret_cast<float *>(static_cast<char *>(workspace) + resnorm_part_bytes(p));
+    return gdn::api_cuda_status(gdn::launch_resnorm_bwd(p, shape->dtype, (cudaStream_t)stream));
 }
 
 }  // extern "C"

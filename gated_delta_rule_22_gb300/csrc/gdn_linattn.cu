@@ -1,0 +1,295 @@
+// gdn_linattn.cu -- linear attention with a constant decay for each value head: the single step, the
+// step-by-step form of prompts and gradients (float32, and bf16 that TMA cannot read), and the sums of dq and
+// dk over the value heads of a key head. (gdn_linattn_chunk.cu holds the chunked form.)
+//
+//     S_t = g S_{t-1} + v_t k_t^T,   y_t = S_t q_t
+//     dq_t = S_t^T dy_t;   R_t = g R_{t+1} + dy_t q_t^T,   dk_t = R_t^T v_t,   dv_t = R_t k_t,   dS0 = g R_0
+//
+// Forward and gradients are the same sweep (LinattnSweep in gdn_layer.cuh) over other operands, so that one
+// kernel computes them all.
+#include "gdn_layer.cuh"
+
+namespace gdn {
+
+namespace {
+
+constexpr int kStepThreads = 256;
+constexpr int kStepRowsPerThread = 4;
+
+constexpr int kWalkThreads = 256, kWalkWarps = kWalkThreads / 32;
+constexpr int kWalkRows = 8;                            // state rows of a warp
+constexpr int kWalkBlock = kWalkWarps * kWalkRows;      // state rows of a CTA
+constexpr int kWalkTile = 16;                           // steps staged at once
+
+constexpr int kSumThreads = 256;
+
+}  // namespace
+
+// ---- one step: a pass over the state, every element read once and written once. LPR lanes share a state
+// row (lane j holds columns V j + V LPR m), kStepRowsPerThread rows each, all loaded before the first is used.
+template <typename T, int V, int LPR, int NP>
+__global__ void __launch_bounds__(kStepThreads) linattn_step_kernel(const LinattnParams p) {
+    constexpr int RPT = kStepRowsPerThread, SLOTS = kStepThreads / LPR;
+    const LinattnSweep &w = p.sweep[0];
+    const int lane = threadIdx.x % LPR, slot = threadIdx.x / LPR;
+    const int h = blockIdx.y, b = blockIdx.z, hk = h / (p.Hv / p.Hk), Dk = p.Dk, Dv = p.Dv;
+    const size_t head = (size_t)b * p.Hv + h;
+    const bool on = row_length(p.lens, b, 1) > 0;
+    const int row0 = blockIdx.x * SLOTS * RPT + slot;
+    const float *S0 = w.init == nullptr ? nullptr : w.init + head * Dv * Dk;
+    float s[RPT][NP][V];
+#pragma unroll
+    for (int r = 0; r < RPT; ++r)
+#pragma unroll
+        for (int m = 0; m < NP; ++m) {
+            const int row = row0 + r * SLOTS, col = (m * LPR + lane) * V;
+#pragma unroll
+            for (int i = 0; i < V; ++i) s[r][m][i] = 0.f;
+            if (S0 != nullptr && row < Dv && col < Dk) load_vec<float, V>(S0 + (size_t)row * Dk + col, s[r][m]);
+        }
+    if (on) {
+        const T *q = static_cast<const T *>(w.a) + (size_t)b * w.lda + (size_t)hk * Dk;
+        const T *k = static_cast<const T *>(w.b) + (size_t)b * w.ldb + (size_t)hk * Dk;
+        const T *v = static_cast<const T *>(w.c) + (size_t)b * w.ldc + (size_t)h * Dv;
+        const float g = p.g[h];
+        float kk[NP][V], qq[NP][V];
+#pragma unroll
+        for (int m = 0; m < NP; ++m)
+#pragma unroll
+            for (int i = 0; i < V; ++i) {              // q and k may lie at any address
+                const int col = (m * LPR + lane) * V + i;
+                kk[m][i] = col < Dk ? to_f32(k[col]) : 0.f;
+                qq[m][i] = col < Dk ? to_f32(q[col]) : 0.f;
+            }
+#pragma unroll
+        for (int r = 0; r < RPT; ++r) {
+            const int row = row0 + r * SLOTS;
+            const float c = row < Dv ? to_f32(v[row]) : 0.f;
+            float y = 0.f;
+#pragma unroll
+            for (int m = 0; m < NP; ++m)
+#pragma unroll
+                for (int i = 0; i < V; ++i) {
+                    s[r][m][i] = fmaf(g, s[r][m][i], c * kk[m][i]);
+                    y = fmaf(s[r][m][i], qq[m][i], y);
+                }
+#pragma unroll
+            for (int m = LPR / 2; m >= 1; m >>= 1) y += __shfl_xor_sync(kFullMask, y, m);
+            if (lane == 0 && row < Dv) static_cast<T *>(w.out)[head * Dv + row] = from_f32<T>(y);
+        }
+    } else if (lane == 0) {
+#pragma unroll
+        for (int r = 0; r < RPT; ++r)
+            if (row0 + r * SLOTS < Dv) static_cast<T *>(w.out)[head * Dv + row0 + r * SLOTS] = from_f32<T>(0.f);
+    }
+    if (w.last == nullptr) return;
+#pragma unroll
+    for (int r = 0; r < RPT; ++r)
+#pragma unroll
+        for (int m = 0; m < NP; ++m) {
+            const int row = row0 + r * SLOTS, col = (m * LPR + lane) * V;
+            if (row < Dv && col < Dk) store_vec<float, V>(w.last + (head * Dv + row) * Dk + col, s[r][m]);
+        }
+}
+
+// ---- step by step. A warp holds kWalkRows rows of the state X [Dc][Db] in registers, lane l the columns
+// 2 l + 64 m and the next (pairs, for the packed instructions); a CTA holds kWalkBlock rows of one sweep,
+// head and batch row and stages kWalkTile steps of a, b and c in shared memory as float32, the next tile's
+// elements in registers meanwhile. A step is two packed instructions and a half per pair of state elements,
+// and nine shuffles for the eight rows' outputs.
+template <typename T, int E2>
+__global__ void __launch_bounds__(kWalkThreads) linattn_walk_kernel(const LinattnParams p, int blocks0, int blocks1) {
+    constexpr int W = 64 * E2;                          // staged columns of a and b
+    constexpr int LA = kWalkTile * W / kWalkThreads, LC = kWalkTile * kWalkBlock / kWalkThreads;
+    __shared__ __align__(16) float sa[kWalkTile][W], sb[kWalkTile][W], sc[kWalkTile][kWalkBlock];
+    const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
+    const int which = (int)blockIdx.x < blocks0 ? 0 : (int)blockIdx.x < blocks0 + blocks1 ? 1 : 2;
+    const LinattnSweep &w = p.sweep[which];
+    const int block = blockIdx.x - (which == 0 ? 0 : which == 1 ? blocks0 : blocks0 + blocks1);
+    const int h = blockIdx.y, b = blockIdx.z, hk = h / (p.Hv / p.Hk), T_ = p.T;
+    const int Db = w.Db, Dc = w.Dc, e0 = block * kWalkBlock, row0 = e0 + warp * kWalkRows;
+    const int n = row_length(p.lens, b, T_);
+    const float g = p.g[h];
+    const size_t head = (size_t)b * p.Hv + h;
+    const T *a_ = static_cast<const T *>(w.a) + (size_t)b * T_ * w.lda + (size_t)(w.a_keys ? hk : h) * Db;
+    const T *b_ = static_cast<const T *>(w.b) + (size_t)b * T_ * w.ldb + (size_t)(w.b_keys ? hk : h) * Db;
+    const T *c_ = static_cast<const T *>(w.c) + (size_t)b * T_ * w.ldc + (size_t)(w.c_keys ? hk : h) * Dc + e0;
+    // the state
+    float2 s[kWalkRows][E2];
+    auto place = [&](int r, int m, int i) {             // of an element of the state in init and last
+        const int row = row0 + r, col = 2 * lane + 64 * m + i;
+        return w.init_t ? (head * Db + col) * Dc + row : (head * Dc + row) * Db + col;
+    };
+    auto inside = [&](int r, int m, int i) { return row0 + r < Dc && 2 * lane + 64 * m + i < Db; };
+#pragma unroll
+    for (int r = 0; r < kWalkRows; ++r)
+#pragma unroll
+        for (int m = 0; m < E2; ++m) {
+            s[r][m].x = w.init != nullptr && inside(r, m, 0) ? w.init[place(r, m, 0)] : 0.f;
+            s[r][m].y = w.init != nullptr && inside(r, m, 1) ? w.init[place(r, m, 1)] : 0.f;
+        }
+    const int tiles = (n + kWalkTile - 1) / kWalkTile;
+    T ra[LA], rb[LA], rc[LC];
+    auto fetch = [&](int tile) {
+        const int t0 = tile * kWalkTile;
+#pragma unroll
+        for (int i = 0; i < LA; ++i) {
+            const int t = t0 + (tid + i * kWalkThreads) / W, col = (tid + i * kWalkThreads) % W;
+            const bool ok = t < n && col < Db;
+            ra[i] = ok ? a_[(size_t)t * w.lda + col] : from_f32<T>(0.f);
+            rb[i] = ok ? b_[(size_t)t * w.ldb + col] : from_f32<T>(0.f);
+        }
+#pragma unroll
+        for (int i = 0; i < LC; ++i) {
+            const int t = t0 + (tid + i * kWalkThreads) / kWalkBlock, row = (tid + i * kWalkThreads) % kWalkBlock;
+            rc[i] = t < n && e0 + row < Dc ? c_[(size_t)t * w.ldc + row] : from_f32<T>(0.f);
+        }
+    };
+    // outputs: a row of a value head, or (keys of their own) of its key head
+    const size_t out_step = (size_t)p.Hv * Dc;          // where the heads are summed later, and where Hk == Hv
+    const size_t out0 = (size_t)b * T_ * out_step + (size_t)h * Dc;
+    auto put = [&](int t, int row, float x) {
+        const size_t at = out0 + (size_t)t * out_step + row;
+        if (w.sums) static_cast<float *>(w.out)[at] = x;
+        else static_cast<T *>(w.out)[at] = from_f32<T>(x);
+    };
+    if (tiles > 0) fetch(w.rev ? tiles - 1 : 0);
+    bool first = w.rev != 0;                            // backwards the first step does not decay the state
+    for (int it = 0; it < tiles; ++it) {
+        const int tile = w.rev ? tiles - 1 - it : it, t0 = tile * kWalkTile, steps = min(kWalkTile, n - t0);
+        __syncthreads();
+#pragma unroll
+        for (int i = 0; i < LA; ++i) {
+            const int j = tid + i * kWalkThreads;
+            sa[j / W][j % W] = to_f32(ra[i]);
+            sb[j / W][j % W] = to_f32(rb[i]);
+        }
+#pragma unroll
+        for (int i = 0; i < LC; ++i) {
+            const int j = tid + i * kWalkThreads;
+            sc[j / kWalkBlock][j % kWalkBlock] = to_f32(rc[i]);
+        }
+        __syncthreads();
+        if (it + 1 < tiles) fetch(w.rev ? tile - 1 : tile + 1);
+        if (row0 >= Dc) continue;                       // (a warp without rows stages only)
+        for (int k = 0; k < steps; ++k) {
+            const int i = w.rev ? steps - 1 - k : k;
+            const float gs = first ? 1.f : g;
+            const float2 g2 = make_float2(gs, gs);
+            first = false;
+            float2 av[E2], bv[E2];
+#pragma unroll
+            for (int m = 0; m < E2; ++m) {
+                av[m] = *reinterpret_cast<const float2 *>(&sa[i][2 * lane + 64 * m]);
+                bv[m] = *reinterpret_cast<const float2 *>(&sb[i][2 * lane + 64 * m]);
+            }
+            float y[kWalkRows];
+#pragma unroll
+            for (int r = 0; r < kWalkRows; ++r) {
+                const float c = sc[i][warp * kWalkRows + r];
+                const float2 c2 = make_float2(c, c);
+                float2 acc = make_float2(0.f, 0.f);
+#pragma unroll
+                for (int m = 0; m < E2; ++m) {
+                    s[r][m] = __ffma2_rn(g2, s[r][m], __fmul2_rn(c2, bv[m]));
+                    acc = __ffma2_rn(s[r][m], av[m], acc);
+                }
+                y[r] = acc.x + acc.y;
+            }
+            const float sum = transpose_reduce<kWalkRows>(y, lane);    // lane l: row l / 4
+            const int row = row0 + (lane >> 2);
+            if ((lane & 3) == 0 && row < Dc) put(t0 + i, row, sum);
+        }
+    }
+    for (int i = tid; i < (T_ - n) * kWalkBlock; i += kWalkThreads)    // zeros behind the row
+        if (e0 + i % kWalkBlock < Dc) put(n + i / kWalkBlock, e0 + i % kWalkBlock, 0.f);
+    if (w.last != nullptr) {
+        const float gl = w.rev && n > 0 ? g : 1.f;
+#pragma unroll
+        for (int r = 0; r < kWalkRows; ++r)
+#pragma unroll
+            for (int m = 0; m < E2; ++m) {
+                if (inside(r, m, 0)) w.last[place(r, m, 0)] = gl * s[r][m].x;
+                if (inside(r, m, 1)) w.last[place(r, m, 1)] = gl * s[r][m].y;
+            }
+    }
+}
+
+// ---- dq and dk: the float32 rows of the value heads of a key head, added in ascending order
+template <typename T>
+__global__ void __launch_bounds__(kSumThreads) linattn_sum_kernel(const LinattnParams p) {
+    const float *part = blockIdx.y == 0 ? p.part_dq : p.part_dk;
+    T *out = static_cast<T *>(blockIdx.y == 0 ? p.dq : p.dk);
+    const int group = p.Hv / p.Hk, D = p.Dk;
+    const size_t n = (size_t)p.B * p.T * p.Hk * D;
+    for (size_t i = (size_t)blockIdx.x * kSumThreads + threadIdx.x; i < n; i += (size_t)gridDim.x * kSumThreads) {
+        const size_t head = i / D, d = i % D;           // (batch row, step, key head), channel
+        const float *x = part + head * group * D + d;
+        float s = x[0];
+        for (int r = 1; r < group; ++r) s += x[(size_t)r * D];
+        out[i] = from_f32<T>(s);
+    }
+}
+
+template <typename T>
+static cudaError_t launch_step_t(const LinattnParams &p, cudaStream_t s) {
+    auto run = [&](auto kernel, int lpr) {
+        const int rows = kStepThreads / lpr * kStepRowsPerThread;
+        kernel<<<dim3((p.Dv + rows - 1) / rows, p.Hv, p.B), kStepThreads, 0, s>>>(p);
+    };
+    if (p.Dk % 4 != 0) {
+        if (p.Dk <= 32) run(linattn_step_kernel<T, 1, 32, 1>, 32);
+        else if (p.Dk <= 128) run(linattn_step_kernel<T, 1, 32, 4>, 32);
+        else run(linattn_step_kernel<T, 1, 32, 8>, 32);
+    } else if (p.Dk <= 32) run(linattn_step_kernel<T, 4, 8, 1>, 8);
+    else if (p.Dk <= 64) run(linattn_step_kernel<T, 4, 16, 1>, 16);
+    else if (p.Dk <= 128) run(linattn_step_kernel<T, 4, 32, 1>, 32);
+    else run(linattn_step_kernel<T, 4, 32, 2>, 32);
+    return cudaGetLastError();
+}
+
+cudaError_t launch_linattn_step(const LinattnParams &p, int dtype, cudaStream_t s) {
+    timing_mark("linattn_step", 0, s);
+    const cudaError_t e = dtype == 0 ? launch_step_t<float>(p, s) : launch_step_t<__nv_bfloat16>(p, s);
+    timing_mark("linattn_step", 1, s);
+    return e;
+}
+
+template <typename T>
+static cudaError_t launch_sums_t(const LinattnParams &p, cudaStream_t s) {
+    const size_t n = (size_t)p.B * p.T * p.Hk * p.Dk;
+    const size_t ctas = (n + kSumThreads - 1) / kSumThreads;
+    linattn_sum_kernel<T><<<dim3((unsigned)(ctas < 8192 ? ctas : 8192), 2), kSumThreads, 0, s>>>(p);
+    return cudaGetLastError();
+}
+
+cudaError_t launch_linattn_sums(const LinattnParams &p, int dtype, cudaStream_t s) {
+    timing_mark("linattn_sums", 0, s);
+    const cudaError_t e = dtype == 0 ? launch_sums_t<float>(p, s) : launch_sums_t<__nv_bfloat16>(p, s);
+    timing_mark("linattn_sums", 1, s);
+    return e;
+}
+
+template <typename T>
+static cudaError_t launch_walk_t(const LinattnParams &p, cudaStream_t s) {
+    int blocks[3] = {0, 0, 0}, widest = 1;
+    for (int i = 0; i < p.sweeps; ++i) {
+        blocks[i] = (p.sweep[i].Dc + kWalkBlock - 1) / kWalkBlock;
+        widest = p.sweep[i].Db > widest ? p.sweep[i].Db : widest;
+    }
+    const dim3 grid(blocks[0] + blocks[1] + blocks[2], p.Hv, p.B);
+    if (widest <= 64) linattn_walk_kernel<T, 1><<<grid, kWalkThreads, 0, s>>>(p, blocks[0], blocks[1]);
+    else if (widest <= 128) linattn_walk_kernel<T, 2><<<grid, kWalkThreads, 0, s>>>(p, blocks[0], blocks[1]);
+    else linattn_walk_kernel<T, 4><<<grid, kWalkThreads, 0, s>>>(p, blocks[0], blocks[1]);
+    return cudaGetLastError();
+}
+
+cudaError_t launch_linattn_steps(const LinattnParams &p, int dtype, cudaStream_t s) {
+    timing_mark("linattn_walk", 0, s);
+    cudaError_t e = dtype == 0 ? launch_walk_t<float>(p, s) : launch_walk_t<__nv_bfloat16>(p, s);
+    timing_mark("linattn_walk", 1, s);
+    if (e == cudaSuccess && p.part_dq != nullptr) e = launch_linattn_sums(p, dtype, s);
+    return e;
+}
+
+}  // namespace gdn

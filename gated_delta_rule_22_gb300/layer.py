@@ -1,6 +1,6 @@
 """Binding of the layer operators of libgdn.so (include/gdn.h): the short causal convolution, the
-selective state space scan, the group norm and the projection. Argument marshalling only, as in
-binding.py.
+selective state space scan, the linear attention with a decay, the group norm, the norms around a block
+and the projection. Argument marshalling only, as in binding.py.
 
 Inputs that the header gives a row stride may be slices of a wider tensor along the last dimension
 (x[..., :C] of a contiguous tensor); everything else must be contiguous. A call with stream=s is the
@@ -41,6 +41,16 @@ class GdnLinearShape(ctypes.Structure):
     _fields_ = [("M", _I), ("N", _I), ("K", _I), ("act", _I), ("dtype", _I), ("ldx", _LL), ("ldw", _LL), ("ldres", _LL)]
 
 
+class GdnLinattnShape(ctypes.Structure):
+    _fields_ = [("B", _I), ("T", _I), ("Hk", _I), ("Hv", _I), ("Dk", _I), ("Dv", _I), ("dtype", _I), ("ldq", _LL), ("ldk", _LL),
+                ("ldv", _LL)]
+
+
+class GdnResnormShape(ctypes.Structure):
+    _fields_ = [("M", _I), ("D", _I), ("gate_rows", _I), ("act", _I), ("post", _I), ("pre", _I), ("dtype", _I), ("eps", ctypes.c_float),
+                ("ldx", _LL), ("ldh", _LL), ("ldz", _LL)]
+
+
 _declared = None
 
 
@@ -57,14 +67,20 @@ def _library():
             ("gdn_scan_bwd", GdnScanShape, [_VP] * 10 + [_SZ] + [_VP] * 12 + [_SZ, _VP]),
             ("gdn_norm_fwd", GdnNormShape, [_VP] * 7), ("gdn_norm_bwd", GdnNormShape, [_VP] * 11 + [_SZ, _VP]),
             ("gdn_linear_fwd", GdnLinearShape, [_VP] * 7 + [_SZ, _VP]),
-            ("gdn_linear_bwd", GdnLinearShape, [_VP] * 8 + [_SZ, _VP])):
+            ("gdn_linear_bwd", GdnLinearShape, [_VP] * 8 + [_SZ, _VP]),
+            ("gdn_linattn_fwd", GdnLinattnShape, [_VP] * 9 + [_SZ, _VP]),
+            ("gdn_linattn_bwd", GdnLinattnShape, [_VP] * 13 + [_SZ, _VP]),
+            ("gdn_resnorm_fwd", GdnResnormShape, [_VP] * 10), ("gdn_resnorm_bwd", GdnResnormShape, [_VP] * 16 + [_SZ, _VP])):
         f = getattr(lib, name)
         f.restype, f.argtypes = ctypes.c_int, [P(shape)] + args
     for name, shape in (("gdn_conv_bwd_workspace_bytes", GdnConvShape), ("gdn_scan_ckpt_bytes", GdnScanShape),
                         ("gdn_scan_fwd_workspace_bytes", GdnScanShape), ("gdn_scan_bwd_workspace_bytes", GdnScanShape),
                         ("gdn_norm_bwd_workspace_bytes", GdnNormShape),
                         ("gdn_linear_fwd_workspace_bytes", GdnLinearShape),
-                        ("gdn_linear_bwd_workspace_bytes", GdnLinearShape)):
+                        ("gdn_linear_bwd_workspace_bytes", GdnLinearShape),
+                        ("gdn_linattn_fwd_workspace_bytes", GdnLinattnShape),
+                        ("gdn_linattn_bwd_workspace_bytes", GdnLinattnShape),
+                        ("gdn_resnorm_bwd_workspace_bytes", GdnResnormShape)):
         f = getattr(lib, name)
         f.restype, f.argtypes = ctypes.c_size_t, [P(shape)]
     _declared = lib
@@ -478,4 +494,174 @@ def gdn_linear_bwd(x, W, dy, pre=None, *, act="none", want_dx=True, want_dW=True
          _at(workspace), _size(workspace), _stream_of(dev))
     if rc:
         _raise("gdn_linear_bwd", rc)
+    return out
+
+
+# ------------------------------------------------------------ linear attention with a decay
+def _linattn_args(q, k, v, g, S0, lens):
+    B, T, Hk, Dk = q.shape
+    Hv, Dv = v.shape[-2:]
+    dev, dt = q.device, q.dtype
+    if q.numel() > INT_MAX or v.numel() > INT_MAX:
+        _int_sizes("gdn_linattn", B, T, Hk, Hv, Dk, Dv)
+    ldq, ldk = _rows("q", q, (B, T, Hk, Dk), dt, dev, 2), _rows("k", k, (B, T, Hk, Dk), dt, dev, 2)
+    ldv = _rows("v", v, (B, T, Hv, Dv), dt, dev, 2)
+    _check("g", g, (Hv,), _F32, dev)
+    if S0 is not None:
+        _check("S0", S0, (B, Hv, Dv, Dk), _F32, dev)
+    if lens is not None:
+        _check("lens", lens, (B,), _I32, dev)
+    return GdnLinattnShape(B, T, Hk, Hv, Dk, Dv, _type(q), ldq, ldk, ldv), B, T, Hv, Dk, Dv
+
+
+def gdn_linattn_fwd_workspace_bytes(shape: GdnLinattnShape) -> int:
+    return _library().gdn_linattn_fwd_workspace_bytes(ctypes.byref(shape))
+
+
+def gdn_linattn_bwd_workspace_bytes(shape: GdnLinattnShape) -> int:
+    return _library().gdn_linattn_bwd_workspace_bytes(ctypes.byref(shape))
+
+
+def gdn_linattn_fwd(q, k, v, g, S0=None, lens=None, *, y=None, S_T=None, workspace=None, want_S_T=True, stream=None):
+    """y, S_T = gdn_linattn_fwd(q, k, v, g[, S0, lens]) on CUDA tensors (see include/gdn.h): linear
+    attention of q, k [B, T, Hk, Dk] and v [B, T, Hv, Dv] whose state [B, Hv, Dv, Dk] decays by g [Hv] at
+    every step. With T = 1, S_T may be S0: the state updated in place."""
+    if stream is not None:
+        return _under(stream, gdn_linattn_fwd, locals())
+    lib = _library()
+    shape, B, T, Hv, Dk, Dv = _linattn_args(q, k, v, g, S0, lens)
+    dev, dt = q.device, q.dtype
+    if y is not None:
+        _check("y", y, (B, T, Hv, Dv), dt, dev)
+    if S_T is not None:
+        _check("S_T", S_T, (B, Hv, Dv, Dk), _F32, dev)
+    if not q.is_cuda:
+        _require_cuda(q)
+    if y is None:
+        y = _new_like(v)
+    if S_T is None and want_S_T:
+        S_T = _empty((B, Hv, Dv, Dk), dtype=_F32, device=dev) if S0 is None else _empty_like(S0)
+    if workspace is not None or T > 1:                 # a single step needs none
+        workspace = _scratch("workspace", workspace, lib.gdn_linattn_fwd_workspace_bytes(_byref(shape)), dev)
+    rc = lib.gdn_linattn_fwd(_byref(shape), q.data_ptr(), k.data_ptr(), v.data_ptr(), g.data_ptr(), _at(S0), _at(lens), _at(y), _at(S_T),
+                             _at(workspace), _size(workspace), _stream_of(dev))
+    if rc:
+        _raise("gdn_linattn_fwd", rc)
+    return y, S_T
+
+
+def gdn_linattn_bwd(q, k, v, g, dy, S0=None, lens=None, dS_T=None, *, workspace=None, want_dS0=True, stream=None):
+    """dict(dq, dk, dv, dS0) = gdn_linattn_bwd(q, k, v, g, dy, ...) for the inputs of gdn_linattn_fwd.
+    dS0 is None with want_dS0=False."""
+    if stream is not None:
+        return _under(stream, gdn_linattn_bwd, locals())
+    lib = _library()
+    shape, B, T, Hv, Dk, Dv = _linattn_args(q, k, v, g, S0, lens)
+    dev, dt = q.device, q.dtype
+    _check("dy", dy, (B, T, Hv, Dv), dt, dev)
+    if dS_T is not None:
+        _check("dS_T", dS_T, (B, Hv, Dv, Dk), _F32, dev)
+    if not q.is_cuda:
+        _require_cuda(q)
+    workspace = _scratch("workspace", workspace, lib.gdn_linattn_bwd_workspace_bytes(_byref(shape)), dev)
+    out = {"dq": _new_like(q), "dk": _new_like(k), "dv": _empty_like(dy),
+           "dS0": _empty((B, Hv, Dv, Dk), dtype=_F32, device=dev) if want_dS0 else None}
+    rc = lib.gdn_linattn_bwd(_byref(shape), q.data_ptr(), k.data_ptr(), v.data_ptr(), g.data_ptr(), _at(S0), _at(lens), dy.data_ptr(), _at(dS_T),
+         _at(out["dq"]), _at(out["dk"]), _at(out["dv"]), _at(out["dS0"]), _at(workspace), _size(workspace), _stream_of(dev))
+    if rc:
+        _raise("gdn_linattn_bwd", rc)
+    return out
+
+
+# ------------------------------------------------------------------------ norms around a block
+def _resnorm_args(x, h, z, scale, w_post, w_pre, post, pre, act, eps):
+    dev, dt = x.device, x.dtype
+    D = x.shape[-1]
+    rows, gate_rows = x.numel() // max(D, 1), 1
+    if x.numel() > INT_MAX:
+        _int_sizes("gdn_resnorm", rows, D)
+    ldx, ldh, ldz = _rows("x", x, x.shape, dt, dev), _rows("h", h, x.shape, dt, dev), 0
+    if z is not None:
+        lead = z.dim() - 1
+        if lead < 0 or lead >= x.dim() or z.shape[-1] != D or z.shape[:lead] != x.shape[:lead]:
+            raise ValueError(f"z has shape {tuple(z.shape)}, expected {tuple(x.shape)} or its last dimension behind some of its first ones")
+        gate_rows = rows // max(z.numel() // max(D, 1), 1)
+        ldz = _rows("z", z, z.shape, dt, dev)
+    for name, w, norm in (("scale", scale, True), ("w_post", w_post, post), ("w_pre", w_pre, pre)):
+        if w is not None:
+            if not norm:
+                raise ValueError(f"{name} is given, but its norm is off")
+            _check(name, w, (D,), _F32, dev)
+    return GdnResnormShape(rows, D, gate_rows, _act(act), 1 if post else 0, 1 if pre else 0, _type(x), eps, ldx, ldh, ldz)
+
+
+def gdn_resnorm_fwd(x, h, z=None, scale=None, w_post=None, w_pre=None, *, post=True, pre=True, act="none", eps=1e-5, r=None, y=None,
+                    stats=None, want_stats=True, stream=None):
+    """r, y, stats = gdn_resnorm_fwd(x, h[, z, scale, w_post, w_pre]) on CUDA tensors (see include/gdn.h):
+    r = x + scale act(z) norm(h) w_post, y = norm(r) w_pre, root mean square norms over the last
+    dimension. z has x's shape, or some of its first dimensions and the last ([B, D] for x [B, T, D]: a row
+    for each sequence). post=False: h is added as it is; pre=False: y is None. r may be x (packed): the
+    stream updated in place. stats [..., 2] is what gdn_resnorm_bwd needs."""
+    if stream is not None:
+        return _under(stream, gdn_resnorm_fwd, locals())
+    lib = _library()
+    shape = _resnorm_args(x, h, z, scale, w_post, w_pre, post, pre, act, eps)
+    dev, dt = x.device, x.dtype
+    if r is not None:
+        _check("r", r, x.shape, dt, dev)
+    if y is not None:
+        if not pre:
+            raise ValueError("y is given, but its norm is off")
+        _check("y", y, x.shape, dt, dev)
+    if stats is not None:
+        _check("stats", stats, x.shape[:-1] + (2,), _F32, dev)
+    if not x.is_cuda:
+        _require_cuda(x)
+    if r is None:
+        r = _new_like(x)
+    if y is None and pre:
+        y = _new_like(x)
+    if stats is None and want_stats:
+        stats = _empty(x.shape[:-1] + (2,), dtype=_F32, device=dev)
+    rc = lib.gdn_resnorm_fwd(_byref(shape), x.data_ptr(), h.data_ptr(), _at(z), _at(scale), _at(w_post), _at(w_pre), r.data_ptr(), _at(y),
+                             _at(stats), _stream_of(dev))
+    if rc:
+        _raise("gdn_resnorm_fwd", rc)
+    return r, y, stats
+
+
+def gdn_resnorm_bwd_workspace_bytes(shape: GdnResnormShape) -> int:
+    return _library().gdn_resnorm_bwd_workspace_bytes(ctypes.byref(shape))
+
+
+def gdn_resnorm_bwd(x, h, stats, dy=None, dr=None, z=None, scale=None, w_post=None, w_pre=None, *, post=True, pre=True, act="none", eps=1e-5,
+                    workspace=None, stream=None):
+    """dict(dx, dh, dz, dscale, dw_post, dw_pre) = gdn_resnorm_bwd(x, h, stats, dy, dr[, z, scale, w_post,
+    w_pre]) for the inputs and stats of gdn_resnorm_fwd and the gradients of y (None with pre=False) and r
+    (None: zeros). dz, dscale, dw_post and dw_pre (float32) are None where their input was."""
+    if stream is not None:
+        return _under(stream, gdn_resnorm_bwd, locals())
+    lib = _library()
+    shape = _resnorm_args(x, h, z, scale, w_post, w_pre, post, pre, act, eps)
+    dev, dt = x.device, x.dtype
+    _check("stats", stats, x.shape[:-1] + (2,), _F32, dev)
+    if (dy is None) == bool(pre):
+        raise ValueError("dy is needed: the gradient of y" if pre else "dy is given, but its norm is off")
+    if dy is not None:
+        _check("dy", dy, x.shape, dt, dev)
+    if dr is not None:
+        _check("dr", dr, x.shape, dt, dev)
+    elif not pre:
+        raise ValueError("dr is needed: the gradient of r")
+    if not x.is_cuda:
+        _require_cuda(x)
+    workspace = _scratch("workspace", workspace, lib.gdn_resnorm_bwd_workspace_bytes(_byref(shape)), dev)
+    vec = lambda t: None if t is None else _empty_like(t)  # noqa: E731
+    out = {"dx": _new_like(x), "dh": _new_like(h), "dz": None if z is None else _new_like(z), "dscale": vec(scale),
+           "dw_post": vec(w_post), "dw_pre": vec(w_pre)}
+    rc = lib.gdn_resnorm_bwd(_byref(shape), x.data_ptr(), h.data_ptr(), _at(z), _at(scale), _at(w_post), _at(w_pre), stats.data_ptr(), _at(dy),
+         _at(dr), _at(out["dx"]), _at(out["dh"]), _at(out["dz"]), _at(out["dscale"]), _at(out["dw_post"]), _at(out["dw_pre"]),
+         _at(workspace), _size(workspace), _stream_of(dev))
+    if rc:
+        _raise("gdn_resnorm_bwd", rc)
     return out

@@ -289,8 +289,9 @@ GDN_API int gdn_gates_bwd(const gdn_shape *shape, const void *a, const void *b, 
 
 /*
  * ---- The operators that stand beside the recurrence in a layer: the short causal convolution in
- * front of it, the selective state space scan (the sibling recurrence of hybrid stacks), the group
- * norm with its gate behind it, and the projections around it.
+ * front of it, the selective state space scan and the linear attention with a decay (the sibling
+ * recurrences of hybrid stacks), the group norm with its gate behind it, the norms around a block on
+ * the residual stream, and the projections around it.
  *
  * The conventions above hold, with these additions:
  *   - Inputs that a shape gives a row stride (ldx, ldu, ...: elements from one step, or row, to the
@@ -437,6 +438,73 @@ GDN_API int gdn_linear_fwd(const gdn_linear_shape *shape, const void *x, const v
 GDN_API int gdn_linear_bwd(const gdn_linear_shape *shape, const void *x, const void *W, const void *pre,
                            const void *dy, void *dx, void *dW, void *dbias, void *workspace,
                            size_t workspace_bytes, void *stream);
+
+/*
+ * Linear attention with a constant decay for each value head: the recurrence above without its
+ * correction. For every batch row and value head h, with key head hk = h / (Hv / Hk) and g = g[h]:
+ *     S_t = g S_{t-1} + outer(v_t, k_t),     y_t = S_t q_t
+ *   q, k, dq, dk [B,T,Hk,Dk]   v, y, dy, dv [B,T,Hv,Dv]   (dtype; q, k, v with row strides)
+ *   g [Hv] float32, 0 <= g <= 1: a constant of the layer, without a gradient
+ *   S0, S_T, dS_T, dS0 [B,Hv,Dv,Dk] float32, each may be NULL (S0, dS_T: zeros)
+ * Dk and Dv are 1 to 256, Hv a multiple of Hk (else GDN_ERR_UNSUPPORTED_SHAPE). Prompts and training run
+ * in chunks of 128 steps on the tensor cores (bf16; q, k and v 16-byte aligned, Dk, Dv and the row
+ * strides multiples of 8) or step by step (float32 and the rest); a single step is one pass over the
+ * state, and with T = 1 S_T may be S0 itself (updated in place). In chunks, a q, k, v or dy that is not
+ * finite at a valid step makes outputs of its chunk of the same row and head NaN, earlier steps' too.
+ * The backward computes the states again from k, v and S0; the forward saves nothing. dq and dk are
+ * summed over the value heads of each key head in ascending order.
+ * workspace: gdn_linattn_fwd_workspace_bytes / gdn_linattn_bwd_workspace_bytes bytes (0: may be NULL).
+ */
+typedef struct {
+    int B, T, Hk, Hv, Dk, Dv; /* batch rows, steps, key heads, value heads, key dim, value dim */
+    int dtype;                /* a gdn_dtype */
+    long long ldq, ldk, ldv;  /* elements between steps, 0: Hk * Dk (Hv * Dv for v) */
+} gdn_linattn_shape;
+
+GDN_API size_t gdn_linattn_fwd_workspace_bytes(const gdn_linattn_shape *shape);
+GDN_API size_t gdn_linattn_bwd_workspace_bytes(const gdn_linattn_shape *shape);
+GDN_API int gdn_linattn_fwd(const gdn_linattn_shape *shape, const void *q, const void *k, const void *v, const float *g,
+                            const float *S0, const int *lens, void *y, float *S_T, void *workspace,
+                            size_t workspace_bytes, void *stream);
+GDN_API int gdn_linattn_bwd(const gdn_linattn_shape *shape, const void *q, const void *k, const void *v, const float *g,
+                            const float *S0, const int *lens, const void *dy, const float *dS_T, void *dq, void *dk,
+                            void *dv, float *dS0, void *workspace, size_t workspace_bytes, void *stream);
+
+/*
+ * The residual stream between two blocks: the norm of a block's output h, its gate and residual
+ * scale, the addition onto the stream x, and the norm in front of the next block, in one pass.
+ *     n = h / sqrt(mean(h^2) + eps) w_post   (post == 0: n = h)
+ *     r = x + scale act(z) n
+ *     y = r / sqrt(mean(r^2) + eps) w_pre    (pre == 0: no y)
+ *   x, h, r, y, dy, dr, dx, dh [M,D] (dtype; x, h with row strides; r may be x where x is packed:
+ *   the stream updated in place)   scale, w_post, w_pre [D] float32 or NULL (1)
+ *   z [M / gate_rows, D] (dtype, row stride) or NULL (no gate): row m reads row m / gate_rows, so that a
+ *   gate of one row for each sequence is not repeated in memory
+ *   stats [M,2] float32 or NULL: 1 / sqrt(...) of h and of r (1 without the norm), for the backward
+ * y is formed from r before its rounding. D is 1 to 16384; M a multiple of gate_rows; eps > 0 and finite;
+ * w_post is NULL where post is 0, w_pre and y where pre is 0.
+ * The backward takes dy (pre != 0) and dr, the gradient that reaches r by other ways (NULL: zeros; needed
+ * where pre is 0), and returns dx, dh and, where the pointers are not NULL, dz (needs z; the shape of
+ * z, packed), dscale, dw_post (needs post) and dw_pre (needs pre), float32. It forms r again from x and h.
+ * Its workspace of gdn_resnorm_bwd_workspace_bytes(shape) bytes holds partial sums.
+ */
+typedef struct {
+    int M, D;       /* rows, channels */
+    int gate_rows;  /* consecutive rows that share a row of z; 0: 1 */
+    int act;        /* a gdn_act, of the gate */
+    int post, pre;  /* 0: without the norm of h, without the norm of r */
+    int dtype;      /* a gdn_dtype */
+    float eps;
+    long long ldx, ldh, ldz; /* elements between rows, 0: D */
+} gdn_resnorm_shape;
+
+GDN_API int gdn_resnorm_fwd(const gdn_resnorm_shape *shape, const void *x, const void *h, const void *z, const float *scale,
+                            const float *w_post, const float *w_pre, void *r, void *y, float *stats, void *stream);
+GDN_API size_t gdn_resnorm_bwd_workspace_bytes(const gdn_resnorm_shape *shape);
+GDN_API int gdn_resnorm_bwd(const gdn_resnorm_shape *shape, const void *x, const void *h, const void *z, const float *scale,
+                            const float *w_post, const float *w_pre, const float *stats, const void *dy, const void *dr,
+                            void *dx, void *dh, void *dz, float *dscale, float *dw_post, float *dw_pre, void *workspace,
+                            size_t workspace_bytes, void *stream);
 
 /* Static description of a return code. */
 GDN_API const char *gdn_strerror(int code);

@@ -18,7 +18,8 @@ BUILD_DIR = os.path.join(PKG, "_build")
 
 SOURCES = ["gdn_api.cu", "gdn_fwd.cu", "gdn_bwd.cu", "gdn_gates.cu", "gdn_chunk.cu", "gdn_chunk_bwd.cu",
            "gdn_diag.cu", "gdn_segments.cu", "gdn_decode.cu", "gdn_layer_api.cu", "gdn_conv.cu", "gdn_scan.cu",
-           "gdn_scan_bwd.cu", "gdn_norm.cu", "gdn_linear.cu", "gdn_linattn.cu", "gdn_resnorm.cu"]
+           "gdn_scan_bwd.cu", "gdn_norm.cu", "gdn_linear.cu", "gdn_linattn.cu",
+           "gdn_linattn_chunk.cu", "gdn_resnorm.cu"]
 NVCC_FLAGS = [
     "-gencode", "arch=compute_103a,code=sm_103a", "-lineinfo", "-O3", "-std=c++17",
     "-Xcompiler", "-fPIC", "-Xcompiler", "-fvisibility=hidden",

@@ -19,6 +19,9 @@ int api_device_status_address(int **out);
 // rows * ld apart), 128-byte swizzle; what lies outside an array reads as zero. box_blocks = 0: 3-D
 // {cols, rows, planes}, box {64, box_rows, 1}. Else (cols a multiple of 64) 4-D {64, rows, cols / 64,
 // planes}, box {64, box_rows, box_blocks, 1}: box_blocks neighbouring boxes of 64 columns by one copy.
+// Tensor map of a bf16 [B][T][H][D] array with `ld` elements between steps: 4-D {D, H, T, B}, box {64, 1,
+// box_t, 1}, 128-byte swizzle; what lies outside reads as zero.
+int api_heads_map(CUtensorMap *map, const void *ptr, int B, int T, int H, int D, long long ld, int box_t);
 int api_planes_map(CUtensorMap *map, const void *ptr, uint64_t cols, uint64_t rows, uint64_t planes, uint64_t ld, int box_rows,
                    int box_blocks);
 
@@ -85,20 +88,36 @@ struct LinattnSweep {
     int a_keys, b_keys, c_keys;   // the operand's heads are key heads
     int Db, Dc, rev;
     int init_t;                // init lies transposed, [Db][Dc]
-    int sums;                  // out is float32 [B][T][Hv][Dc], to be summed over the value heads of a key head
+    int sums;                  // out is float32 planes [B][T][Hv][Dc], one for each block of Db, to be added (LinattnSum)
+    int a_map, b_map, c_map;   // tensor maps of the operands
 };
+
+// A sweep's outputs from its float32 ones: the sum over `planes` and `group` value heads, in ascending order.
+struct LinattnSum {
+    const float *part;         // [planes][B][T][heads][group][D]
+    void *out;                 // [B][T][heads][D]
+    size_t plane;
+    int planes, group, heads, D;
+};
+
+struct LinattnMaps { CUtensorMap map[4]; };   // q, k, v, dy
 
 struct LinattnParams {
     LinattnSweep sweep[3];
-    int sweeps;
+    LinattnSum sum[3];
+    int sweeps, sums;
     const float *g;
     const int *lens;
     int *status;
     int B, T, Hk, Hv, Dk, Dv;
-    // backward with shared keys: the float32 sums of dq and dk by value head, and their outputs
-    float *part_dq, *part_dk;
-    void *dq, *dk;
+    // chunked form: each row's chunks are taken in `segs` segments of seg_chunks; seg_state holds what the earlier
+    // segments leave, from a zero state, [seg_units][128][128]
+    int segs, seg_chunks;
+    size_t seg_units;
+    float *seg_state;
 };
+
+constexpr int kLinattnChunk = 128;   // steps of a chunk
 
 struct ResnormParams {
     const void *x, *h, *z, *dy, *dr;
@@ -134,7 +153,10 @@ cudaError_t launch_scan_bwd(const ScanParams &p, int dtype, cudaStream_t s);
 cudaError_t launch_norm_fwd(const NormParams &p, int dtype, cudaStream_t s);
 cudaError_t launch_norm_bwd(const NormParams &p, int dtype, cudaStream_t s);
 cudaError_t launch_linattn_step(const LinattnParams &p, int dtype, cudaStream_t s);    // T = 1, the forward's sweep
-cudaError_t launch_linattn_steps(const LinattnParams &p, int dtype, cudaStream_t s);   // all sweeps, then the sums over heads
+cudaError_t launch_linattn_steps(const LinattnParams &p, int dtype, cudaStream_t s);   // all sweeps, then their sums
+void linattn_segments(LinattnParams *p);                                               // chooses segs, seg_chunks and seg_units
+cudaError_t launch_linattn_chunks(const LinattnParams &p, const LinattnMaps &maps, cudaStream_t s);
+cudaError_t launch_linattn_sums(const LinattnParams &p, int dtype, cudaStream_t s);
 cudaError_t launch_resnorm_fwd(const ResnormParams &p, int dtype, cudaStream_t s);
 cudaError_t launch_resnorm_bwd(const ResnormParams &p, int dtype, cudaStream_t s);
 // These return a GDN_* code (they encode tensor maps).

@@ -154,11 +154,71 @@ int linattn_plan(const gdn_linattn_shape *s, gdn::LinattnParams *p, long long (&
     return GDN_OK;
 }
 
-// Backward with shared keys: dq and dk by value head, float32.
-size_t linattn_part_bytes(const gdn::LinattnParams &p) {
-    return p.Hv == p.Hk ? 0 : up256((size_t)p.B * p.T * p.Hv * p.Dk * 4);
+// Whether the chunked form reads these sizes (bf16 rows that TMA can), and these addresses.
+bool linattn_chunks(const gdn::LinattnParams &p, int dtype, const long long (&ld)[3]) {
+    return dtype == GDN_BF16 && p.T > 1 && p.Dk % 8 == 0 && p.Dv % 8 == 0 && ld[0] % 8 == 0 && ld[1] % 8 == 0 && ld[2] % 8 == 0;
 }
-size_t linattn_bwd_ws(const gdn::LinattnParams &p) { return 2 * linattn_part_bytes(p); }
+
+// The call's sweeps, with the float32 sums and segment states that they need placed in `ws`; returns the bytes of
+// these. `io`: the forward's q, k, v, y, S0, S_T, or the backward's q, k, v, dy, S0, dS_T, dq, dk, dv, dS0.
+struct LinattnIo {
+    const void *q, *k, *v, *dy;
+    const float *S0, *dS_T;
+    void *y, *dq, *dk, *dv;
+    float *S_T, *dS0;
+};
+size_t linattn_sweeps(gdn::LinattnParams *p, const LinattnIo &io, const long long (&ld)[3], bool bwd, bool chunks, char *ws) {
+    const long long ldy = (long long)p->Hv * p->Dv;
+    void *outs[3] = {bwd ? io.dq : io.y, io.dk, io.dv};
+    if (!bwd) {
+        p->sweeps = 1;
+        p->sweep[0] = {io.q, io.k, io.v, io.S0, io.S_T, nullptr, ld[0], ld[1], ld[2], 1, 1, 0, p->Dk, p->Dv, 0, 0, 0, 0, 1, 2};
+    } else {
+        p->sweeps = 3;
+        p->sweep[0] = {io.dy, io.v, io.k, io.S0, nullptr, nullptr, ldy, ld[2], ld[1], 0, 0, 1, p->Dv, p->Dk, 0, 1, 0, 3, 2, 1};
+        p->sweep[1] = {io.v, io.dy, io.q, io.dS_T, nullptr, nullptr, ld[2], ldy, ld[0], 0, 0, 1, p->Dv, p->Dk, 1, 1, 0, 2, 3, 0};
+        p->sweep[2] = {io.k, io.q, io.dy, io.dS_T, io.dS0, nullptr, ld[1], ld[0], ldy, 1, 1, 0, p->Dk, p->Dv, 1, 0, 0, 1, 0, 3};
+    }
+    size_t used = 0;
+    p->sums = 0;
+    for (int i = 0; i < p->sweeps; ++i) {
+        gdn::LinattnSweep &w = p->sweep[i];
+        const int planes = chunks ? (w.Db + 127) / 128 : 1, group = w.c_keys ? p->Hv / p->Hk : 1;
+        w.out = outs[i];
+        if (planes * group == 1) continue;
+        const size_t plane = (size_t)p->B * p->T * p->Hv * w.Dc;
+        w.sums = 1;
+        w.out = ws + used;
+        p->sum[p->sums++] = {static_cast<const float *>(w.out), outs[i], plane, planes, group, p->Hv / group, w.Dc};
+        used += up256(planes * plane * 4);
+    }
+    p->segs = 1;
+    if (chunks) {
+        gdn::linattn_segments(p);
+        p->seg_state = reinterpret_cast<float *>(ws + used);
+        used += up256(p->seg_units * gdn::kLinattnChunk * 128 * 4);
+    }
+    return used;
+}
+size_t linattn_ws(gdn::LinattnParams p, int dtype, const long long (&ld)[3], bool bwd) {
+    const size_t steps = linattn_sweeps(&p, {}, ld, bwd, false, nullptr);
+    const size_t chunks = linattn_chunks(p, dtype, ld) ? linattn_sweeps(&p, {}, ld, bwd, true, nullptr) : 0;
+    return steps > chunks ? steps : chunks;
+}
+int linattn_run(gdn::LinattnParams *p, const LinattnIo &io, int dtype, const long long (&ld)[3], bool bwd, void *ws, cudaStream_t s) {
+    const bool chunks = linattn_chunks(*p, dtype, ld) && aligned16(io.q) && aligned16(io.k) && aligned16(io.v);
+    linattn_sweeps(p, io, ld, bwd, chunks, static_cast<char *>(ws));
+    if (!chunks) return gdn::api_cuda_status(gdn::launch_linattn_steps(*p, dtype, s));
+    gdn::LinattnMaps maps = {};
+    int rc;
+    if ((rc = gdn::api_device_status_address(&p->status)) != GDN_OK ||
+        (rc = gdn::api_heads_map(&maps.map[0], io.q, p->B, p->T, p->Hk, p->Dk, ld[0], gdn::kLinattnChunk)) != GDN_OK ||
+        (rc = gdn::api_heads_map(&maps.map[1], io.k, p->B, p->T, p->Hk, p->Dk, ld[1], gdn::kLinattnChunk)) != GDN_OK ||
+        (rc = gdn::api_heads_map(&maps.map[2], io.v, p->B, p->T, p->Hv, p->Dv, ld[2], gdn::kLinattnChunk)) != GDN_OK ||
+        (bwd && (rc = gdn::api_heads_map(&maps.map[3], io.dy, p->B, p->T, p->Hv, p->Dv, (long long)p->Hv * p->Dv, gdn::kLinattnChunk)) != GDN_OK))
+        return rc;
+    return gdn::api_cuda_status(gdn::launch_linattn_chunks(*p, maps, s));
+}
 
 int resnorm_plan(const gdn_resnorm_shape *s, gdn::ResnormParams *p) {
     if (s == nullptr || s->M <= 0 || s->D <= 0 || s->gate_rows < 0 || s->ldx < 0 || s->ldh < 0 || s->ldz < 0) return GDN_ERR_INVALID_ARG;
@@ -370,29 +430,36 @@ int gdn_linear_bwd(const gdn_linear_shape *shape, const void *x, const void *W, 
     return gdn::launch_linear_bwd(p, shape->dtype, (cudaStream_t)stream);
 }
 
-size_t gdn_linattn_fwd_workspace_bytes(const gdn_linattn_shape *) { return 0; }
+size_t gdn_linattn_fwd_workspace_bytes(const gdn_linattn_shape *shape) {
+    gdn::LinattnParams p;
+    long long ld[3];
+    return linattn_plan(shape, &p, ld) == GDN_OK ? linattn_ws(p, shape->dtype, ld, false) : 0;
+}
 
 size_t gdn_linattn_bwd_workspace_bytes(const gdn_linattn_shape *shape) {
     gdn::LinattnParams p;
     long long ld[3];
-    return linattn_plan(shape, &p, ld) == GDN_OK ? linattn_bwd_ws(p) : 0;
+    return linattn_plan(shape, &p, ld) == GDN_OK ? linattn_ws(p, shape->dtype, ld, true) : 0;
 }
 
 int gdn_linattn_fwd(const gdn_linattn_shape *shape, const void *q, const void *k, const void *v, const float *g, const float *S0,
-                    const int *lens, void *y, float *S_T, void *workspace, size_t, void *stream) {
+                    const int *lens, void *y, float *S_T, void *workspace, size_t workspace_bytes, void *stream) {
     gdn::LinattnParams p;
     long long ld[3];
     int rc = linattn_plan(shape, &p, ld);
     if (rc != GDN_OK) return rc;
-    if (!q || !k || !v || !g || !y) return GDN_ERR_INVALID_ARG;
+    const size_t need = linattn_ws(p, shape->dtype, ld, false);
+    if (!q || !k || !v || !g || !y || (need > 0 && !workspace)) return GDN_ERR_INVALID_ARG;
     if (S_T != nullptr && S_T == S0 && p.T != 1) return GDN_ERR_INVALID_ARG;
     if ((rc = packed_ok({g, S0, lens, y, S_T, workspace})) != GDN_OK || (rc = strided_ok({q, k, v}, elem(shape->dtype))) != GDN_OK) return rc;
+    if (workspace_bytes < need) return GDN_ERR_WORKSPACE_TOO_SMALL;
     gdn::api_clear_error();
     p.g = g; p.lens = lens;
-    p.sweeps = 1;
-    p.sweep[0] = {q, k, v, S0, S_T, y, ld[0], ld[1], ld[2], 1, 1, 0, p.Dk, p.Dv, 0, 0, 0};
-    if (p.T == 1) return gdn::api_cuda_status(gdn::launch_linattn_step(p, shape->dtype, (cudaStream_t)stream));
-    return gdn::api_cuda_status(gdn::launch_linattn_steps(p, shape->dtype, (cudaStream_t)stream));
+    LinattnIo io = {};
+    io.q = q; io.k = k; io.v = v; io.S0 = S0; io.y = y; io.S_T = S_T;
+    if (p.T > 1) return linattn_run(&p, io, shape->dtype, ld, false, workspace, (cudaStream_t)stream);
+    linattn_sweeps(&p, io, ld, false, false, nullptr);
+    return gdn::api_cuda_status(gdn::launch_linattn_step(p, shape->dtype, (cudaStream_t)stream));
 }
 
 int gdn_linattn_bwd(const gdn_linattn_shape *shape, const void *q, const void *k, const void *v, const float *g, const float *S0,
@@ -402,7 +469,7 @@ int gdn_linattn_bwd(const gdn_linattn_shape *shape, const void *q, const void *k
     long long ld[3];
     int rc = linattn_plan(shape, &p, ld);
     if (rc != GDN_OK) return rc;
-    const size_t need = linattn_bwd_ws(p);
+    const size_t need = linattn_ws(p, shape->dtype, ld, true);
     if (!q || !k || !v || !g || !dy || !dq || !dk || !dv || (need > 0 && !workspace)) return GDN_ERR_INVALID_ARG;
     if ((rc = packed_ok({g, S0, lens, dy, dS_T, dq, dk, dv, dS0, workspace})) != GDN_OK ||
         (rc = strided_ok({q, k, v}, elem(shape->dtype))) != GDN_OK)
@@ -410,20 +477,9 @@ int gdn_linattn_bwd(const gdn_linattn_shape *shape, const void *q, const void *k
     if (workspace_bytes < need) return GDN_ERR_WORKSPACE_TOO_SMALL;
     gdn::api_clear_error();
     p.g = g; p.lens = lens;
-    const int shared = p.Hv != p.Hk;
-    void *out_q = dq, *out_k = dk;
-    if (shared) {
-        p.part_dq = static_cast<float *>(workspace);
-        p.part_dk = reinterpret_cast<float *>(static_cast<char *>(workspace) + linattn_part_bytes(p));
-        p.dq = dq; p.dk = dk;
-        out_q = p.part_dq; out_k = p.part_dk;
-    }
-    const long long ldy = (long long)p.Hv * p.Dv;
-    p.sweeps = 3;
-    p.sweep[0] = {dy, v, k, S0, nullptr, out_q, ldy, ld[2], ld[1], 0, 0, 1, p.Dv, p.Dk, 0, 1, shared};
-    p.sweep[1] = {v, dy, q, dS_T, nullptr, out_k, ld[2], ldy, ld[0], 0, 0, 1, p.Dv, p.Dk, 1, 1, shared};
-    p.sweep[2] = {k, q, dy, dS_T, dS0, dv, ld[1], ld[0], ldy, 1, 1, 0, p.Dk, p.Dv, 1, 0, 0};
-    return gdn::api_cuda_status(gdn::launch_linattn_steps(p, shape->dtype, (cudaStream_t)stream));
+    LinattnIo io = {};
+    io.q = q; io.k = k; io.v = v; io.dy = dy; io.S0 = S0; io.dS_T = dS_T; io.dq = dq; io.dk = dk; io.dv = dv; io.dS0 = dS0;
+    return linattn_run(&p, io, shape->dtype, ld, true, workspace, (cudaStream_t)stream);
 }
 
 int gdn_resnorm_fwd(const gdn_resnorm_shape *shape, const void *x, const void *h, const void *z, const float *scale, const float *w_post,

@@ -1,6 +1,6 @@
 // gdn_linattn.cu -- linear attention with a constant decay for each value head: the single step, the
-// step-by-step form of prompts and gradients (float32, and bf16 that TMA cannot read), and the sums of dq and
-// dk over the value heads of a key head. (gdn_linattn_chunk.cu holds the chunked form.)
+// step-by-step form of prompts and gradients (float32, and bf16 that TMA cannot read), and the sums of sweeps'
+// float32 outputs. (gdn_linattn_chunk.cu holds the chunked form.)
 //
 //     S_t = g S_{t-1} + v_t k_t^T,   y_t = S_t q_t
 //     dq_t = S_t^T dy_t;   R_t = g R_{t+1} + dy_t q_t^T,   dk_t = R_t^T v_t,   dv_t = R_t k_t,   dS0 = g R_0
@@ -215,18 +215,19 @@ __global__ void __launch_bounds__(kWalkThreads) linattn_walk_kernel(const Linatt
     }
 }
 
-// ---- dq and dk: the float32 rows of the value heads of a key head, added in ascending order
+// ---- outputs from the sweeps' float32 ones: planes (blocks of Db) and the value heads of a key head, added in
+// ascending order
 template <typename T>
 __global__ void __launch_bounds__(kSumThreads) linattn_sum_kernel(const LinattnParams p) {
-    const float *part = blockIdx.y == 0 ? p.part_dq : p.part_dk;
-    T *out = static_cast<T *>(blockIdx.y == 0 ? p.dq : p.dk);
-    const int group = p.Hv / p.Hk, D = p.Dk;
-    const size_t n = (size_t)p.B * p.T * p.Hk * D;
+    const LinattnSum &w = p.sum[blockIdx.y];
+    T *out = static_cast<T *>(w.out);
+    const size_t n = (size_t)p.B * p.T * w.heads * w.D;
     for (size_t i = (size_t)blockIdx.x * kSumThreads + threadIdx.x; i < n; i += (size_t)gridDim.x * kSumThreads) {
-        const size_t head = i / D, d = i % D;           // (batch row, step, key head), channel
-        const float *x = part + head * group * D + d;
-        float s = x[0];
-        for (int r = 1; r < group; ++r) s += x[(size_t)r * D];
+        const size_t head = i / w.D, d = i % w.D;       // (batch row, step, head), channel
+        const float *x = w.part + head * w.group * w.D + d;
+        float s = 0.f;
+        for (int r = 0; r < w.group; ++r)
+            for (int q = 0; q < w.planes; ++q) s += x[q * w.plane + (size_t)r * w.D];
         out[i] = from_f32<T>(s);
     }
 }
@@ -257,9 +258,13 @@ cudaError_t launch_linattn_step(const LinattnParams &p, int dtype, cudaStream_t 
 
 template <typename T>
 static cudaError_t launch_sums_t(const LinattnParams &p, cudaStream_t s) {
-    const size_t n = (size_t)p.B * p.T * p.Hk * p.Dk;
+    size_t n = 0;
+    for (int i = 0; i < p.sums; ++i) {
+        const size_t m = (size_t)p.B * p.T * p.sum[i].heads * p.sum[i].D;
+        n = m > n ? m : n;
+    }
     const size_t ctas = (n + kSumThreads - 1) / kSumThreads;
-    linattn_sum_kernel<T><<<dim3((unsigned)(ctas < 8192 ? ctas : 8192), 2), kSumThreads, 0, s>>>(p);
+    linattn_sum_kernel<T><<<dim3((unsigned)(ctas < 8192 ? ctas : 8192), p.sums), kSumThreads, 0, s>>>(p);
     return cudaGetLastError();
 }
 
@@ -288,7 +293,7 @@ cudaError_t launch_linattn_steps(const LinattnParams &p, int dtype, cudaStream_t
     timing_mark("linattn_walk", 0, s);
     cudaError_t e = dtype == 0 ? launch_walk_t<float>(p, s) : launch_walk_t<__nv_bfloat16>(p, s);
     timing_mark("linattn_walk", 1, s);
-    if (e == cudaSuccess && p.part_dq != nullptr) e = launch_linattn_sums(p, dtype, s);
+    if (e == cudaSuccess && p.sums > 0) e = launch_linattn_sums(p, dtype, s);
     return e;
 }
 

@@ -1,0 +1,455 @@
+// gdn_linattn_chunk.cu -- the sweeps of the linear attention with a decay (LinattnSweep in gdn_layer.cuh),
+// bf16, in chunks of 128 steps on the tcgen05 tensor cores.
+//
+// For a chunk of L valid steps with incoming state Z [Dc][Db] (forward; local steps i, m = 0 .. L - 1):
+//     out_i = sum_{m <= i} g^(i-m) (a_i . b_m) c_m + g^(i+1) Z a_i
+//     Z'    = g^L Z + sum_m g^(L-1-m) c_m b_m^T
+// Backwards, with Z the adjoint that the later steps leave behind, decayed up to the step in front of them:
+//     out_i = sum_{m >= i} g^(m-i) (a_i . b_m) c_m + g^(L-1-i) Z a_i,    Z' = g^L Z + sum_m g^(m+1) c_m b_m^T
+// Every exponent is at least 0, so that no decay, however strong, divides by an underflow.
+//
+// A CTA takes one sweep of one (batch row, value head), one block of up to 128 columns of Db and of Dc (the
+// sweep is linear in b's columns and splits over c's; blocks of Db are added in float32 afterwards), and a
+// segment of the chunks. Four products of 128 x 128 x 128 per chunk, their operands as TMA brings them:
+//     P = a b^T        both K-major                  -> tensor memory; its decayed, masked bf16 copy stays there
+//     O1 = P~ c        P~ from tensor memory, c MN-major
+//     O2 = a Z^T       Z as bf16 in shared memory
+//     U = c^T b~       both MN-major; b~_m = g^(L-1-m) b_m as three bf16 terms (24 bits: the state is float32)
+//                      that take the places of b, a and Z, which are read by then; where no state leaves the
+//                      call, two terms (16 bits, beside Z's rounding to 8 for O2)
+// out = O1 + g^(i+1) O2 is formed in float32, and the state is kept in registers, Z' = g^L Z + U, so that the
+// truncating additions of the tensor cores never run over more than a chunk. Rounded to bf16 besides
+// the outputs: P~ and Z as an operand, each a relative 2^-9 of terms of either sign.
+//
+// Warps 0-3 mask P and write outputs; warps 4-7 hold the state; one warp fetches (two chunks deep), two
+// issue products: P and O1, and O2 and U, so that neither chain waits for the other.
+#include "gdn.h"
+#include "gdn_layer.cuh"
+#include "gdn_umma.cuh"
+
+namespace gdn {
+
+namespace {
+
+constexpr int kC = kLinattnChunk;
+constexpr int kThreads = 11 * 32;
+constexpr int kTile = 64 * kC * 2;                 // 64 columns of a chunk: 128 rows of 128 bytes
+constexpr int kOperand = 2 * kTile;
+constexpr int kStage = 3 * kOperand;               // a, b, c
+constexpr size_t kSmem = 1024 + 2 * kStage + kOperand + 136 * 4 + 16 * 8 + 16;
+// tensor memory columns
+constexpr int kColP = 0, kColO1 = 128, kColO2 = 256, kColU = 384;
+
+struct SweepArgs {
+    LinattnParams p;
+    int blocks[3];                                 // column blocks of each sweep (of Db times of Dc)
+    int state_only;                                // write the segments' end states from zero, nothing else
+};
+
+__device__ __forceinline__ uint64_t desc_k(uint32_t start) { return umma_sdesc(start, 16u, 1024u) | (uint64_t)2 << 61; }
+__device__ __forceinline__ uint64_t desc_mn(uint32_t start) { return umma_sdesc(start, kTile, 1024u) | (uint64_t)2 << 61; }
+
+// D (+)= A B with A (bf16 pairs, one 32-bit column per two of K) in tensor memory; executed by a whole warp
+__device__ __forceinline__ void umma_bf16_tw(uint32_t d_tmem, uint32_t a_tmem, uint64_t bdesc, uint32_t idesc, bool accumulate, uint32_t lead) {
+    asm volatile(
+        "{\n .reg .pred p, q;\n setp.ne.b32 p, %4, 0;\n setp.ne.b32 q, %5, 0;\n"
+        " @q tcgen05.mma.cta_group::1.kind::f16 [%0], [%1], %2, %3, p;\n}" ::"r"(d_tmem),
+        "r"(a_tmem), "l"(bdesc), "r"(idesc), "r"((uint32_t)accumulate), "r"(lead)
+        : "memory");
+}
+
+// The 16-byte piece `piece` (8 columns) of row r of an operand's tiles in the 128-byte swizzle
+__device__ __forceinline__ uint4 *piece_at(unsigned char *operand, int r, int piece) {
+    return reinterpret_cast<uint4 *>(operand + (piece >> 3) * kTile + r * 128 + (((piece & 7) ^ (r & 7)) << 4));
+}
+
+// mbar_wait by a whole warp, with one answer
+__device__ __forceinline__ bool all_wait(uint64_t *bar, uint32_t parity) { return __all_sync(kFullMask, mbar_wait(bar, parity)); }
+
+__device__ __forceinline__ void write_zeros(const LinattnSweep &w, size_t at, int n) {
+    if (w.sums)
+        for (int i = 0; i < n; i += 4) *reinterpret_cast<float4 *>(static_cast<float *>(w.out) + at + i) = make_float4(0.f, 0.f, 0.f, 0.f);
+    else
+        for (int i = 0; i < n; i += 8) *reinterpret_cast<uint4 *>(static_cast<__nv_bfloat16 *>(w.out) + at + i) = make_uint4(0u, 0u, 0u, 0u);
+}
+
+}  // namespace
+
+__global__ void __launch_bounds__(kThreads, 1) linattn_chunk_kernel(const __grid_constant__ LinattnMaps maps, const __grid_constant__ SweepArgs cp) {
+    extern __shared__ unsigned char smem_raw[];
+    unsigned char *smem = reinterpret_cast<unsigned char *>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~(uintptr_t)1023);
+    unsigned char *zb = smem + 2 * kStage;                                   // the state as an operand [e][d]
+    float *pw = reinterpret_cast<float *>(zb + kOperand);                    // g^0 .. g^128
+    uint64_t *full = reinterpret_cast<uint64_t *>(pw + 136), *empty = full + 2;
+    uint64_t *p_full = full + 4, *pt_full = full + 5, *o1_full = full + 6, *o2_full = full + 7, *o_empty = full + 8, *bt_full = full + 9,
+             *u_full = full + 10, *z_full = full + 11;
+    uint32_t *tmem_slot = reinterpret_cast<uint32_t *>(full + 16);
+    const LinattnParams &p = cp.p;
+    const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+
+    // this CTA's sweep, column blocks and segment
+    int x = blockIdx.x;
+    const int segs = cp.state_only ? p.segs - 1 : p.segs;
+    const int seg = x % segs;
+    x /= segs;
+    const int which = x < cp.blocks[0] ? 0 : x < cp.blocks[0] + cp.blocks[1] ? 1 : 2;
+    const int unit = ((blockIdx.z * gridDim.y + blockIdx.y) * (gridDim.x / segs) + x) * (p.segs - 1);     // of its segments' states
+    if (which > 0) x -= cp.blocks[0];
+    if (which > 1) x -= cp.blocks[1];
+    const LinattnSweep &w = p.sweep[which];
+    const int nc = (w.Dc + 127) / 128, db0 = x / nc * 128, dc0 = x % nc * 128;
+    const int Db = min(w.Db - db0, 128), Dc = min(w.Dc - dc0, 128);
+    const int h = blockIdx.y, b = blockIdx.z, hk = h / (p.Hv / p.Hk);
+    const size_t head = (size_t)b * p.Hv + h;
+    const int n = row_length(p.lens, b, p.T), chunks = (n + kC - 1) / kC;
+    const int first = seg * p.seg_chunks, last = min(first + p.seg_chunks, chunks);       // in the order of the sweep
+    const bool rev = w.rev != 0, masked = p.lens != nullptr;
+    const int terms = w.last != nullptr ? 3 : 2;
+    auto chunk_of = [&](int i) { return rev ? chunks - 1 - i : i; };
+    auto length_of = [&](int i) { return min(kC, n - chunk_of(i) * kC); };
+    const int Dbp = (Db + 15) / 16 * 16, Dcp = (Dc + 15) / 16 * 16;                        // (zeros behind Db, Dc)
+    const int work = cp.state_only ? (last < chunks ? last - first : 0) : last - first;   // (<= 0: none)
+
+    if (threadIdx.x == 0) {
+        for (int i = 0; i < 2; ++i) {
+            mbar_init(full + i, 1);
+            mbar_init(empty + i, cp.state_only ? 1 : 2);
+        }
+        for (uint64_t *bar : {p_full, o1_full, o2_full, u_full}) mbar_init(bar, 1);
+        for (uint64_t *bar : {pt_full, o_empty, bt_full, z_full}) mbar_init(bar, 128);
+        fence_mbar_init();
+    }
+    if (warp == 8) tmem_alloc(tmem_slot, 512);
+    {
+        const float g = p.g[h], lg = log2f(g);
+        for (int i = threadIdx.x; i <= kC; i += kThreads) pw[i] = i == 0 ? 1.f : exp2f(i * lg);
+    }
+    tc_fence_before();
+    __syncthreads();
+    tc_fence_after();
+    const uint32_t tmem = *tmem_slot;
+    const size_t out_step = (size_t)p.Hv * w.Dc;
+    const size_t out0 = (size_t)(db0 / 128) * p.B * p.T * out_step + (size_t)b * p.T * out_step + (size_t)h * w.Dc + dc0;
+    bool ok = true;
+
+    if (warp < 4) {                                // ---- decay and mask P, write the outputs
+        const uint32_t lanes = tmem + ((uint32_t)warp << 21);
+        const int i = threadIdx.x;                 // this thread's step of the chunk
+        for (int k = 0; k < work && !cp.state_only; ++k) {
+            const int L = length_of(first + k), t0 = chunk_of(first + k) * kC;
+            const uint32_t ph = k & 1;
+            if (!(ok = all_wait(p_full, ph))) break;
+            tc_fence_after();
+#pragma unroll
+            for (int cb = 0; cb < 4; ++cb) {
+                float v[32];
+                if (rev ? cb >= warp : cb <= warp) {
+                    tmem_ld32f(lanes + kColP + 32 * cb, v);
+                    tmem_wait_ld();
+                    if (cb == warp) {
+#pragma unroll
+                        for (int r = 0; r < 32; ++r) {
+                            const int e = rev ? r - lane : lane - r;
+                            const float d = pw[max(e, 0)];
+                            v[r] = e >= 0 && (!rev || 32 * cb + r < L) ? v[r] * d : 0.f;
+                        }
+                    } else {
+                        const float f = pw[rev ? 32 * cb - i : i - 32 * cb - 31];
+#pragma unroll
+                        for (int r = 0; r < 32; ++r) {
+                            const float d = f * pw[rev ? r : 31 - r];
+                            v[r] = !rev || 32 * cb + r < L ? v[r] * d : 0.f;
+                        }
+                    }
+                } else {
+#pragma unroll
+                    for (int r = 0; r < 32; ++r) v[r] = 0.f;
+                }
+                float packed[16];
+#pragma unroll
+                for (int r = 0; r < 16; ++r) packed[r] = __uint_as_float(pack2_bf16(v[2 * r], v[2 * r + 1]));
+                tmem_st16f(lanes + kColP + 16 * cb, packed);
+            }
+            tmem_wait_st();
+            tc_fence_before();
+            mbar_arrive(pt_full);
+            if (!(ok = all_wait(o2_full, ph) && all_wait(o1_full, ph))) break;
+            tc_fence_after();
+            const float s = pw[rev ? max(L - 1 - i, 0) : i + 1];
+            const size_t at = out0 + (size_t)(t0 + i) * out_step;
+#pragma unroll
+            for (int cb = 0; cb < 4; ++cb) {
+                if (32 * cb >= Dc) break;
+                float o1[32], o2[32];
+                tmem_ld32f(lanes + kColO1 + 32 * cb, o1);
+                tmem_ld32f(lanes + kColO2 + 32 * cb, o2);
+                tmem_wait_ld();
+#pragma unroll
+                for (int r = 0; r < 32; ++r) o1[r] = fmaf(s, o2[r], o1[r]);
+                if (i >= L) continue;
+                if (w.sums) {
+                    float *out = static_cast<float *>(w.out) + at + 32 * cb;
+#pragma unroll
+                    for (int r = 0; r < 32; r += 4)
+                        if (32 * cb + r < Dc) *reinterpret_cast<float4 *>(out + r) = make_float4(o1[r], o1[r + 1], o1[r + 2], o1[r + 3]);
+                } else {
+                    __nv_bfloat16 *out = static_cast<__nv_bfloat16 *>(w.out) + at + 32 * cb;
+#pragma unroll
+                    for (int r = 0; r < 32; r += 8)
+                        if (32 * cb + r < Dc)
+                            *reinterpret_cast<uint4 *>(out + r) = make_uint4(pack2_bf16(o1[r], o1[r + 1]), pack2_bf16(o1[r + 2], o1[r + 3]),
+                                                                             pack2_bf16(o1[r + 4], o1[r + 5]), pack2_bf16(o1[r + 6], o1[r + 7]));
+                }
+            }
+            tc_fence_before();
+            mbar_arrive(o_empty);
+        }
+        // zeros behind the row: this segment's share of the steps
+        if (!cp.state_only) {
+            const int from = max(n, seg * p.seg_chunks * kC), to = seg == p.segs - 1 ? p.T : min(p.T, (seg + 1) * p.seg_chunks * kC);
+            for (int t = from + i; t < to; t += 128) write_zeros(w, out0 + (size_t)t * out_step, Dc);
+        }
+    } else if (warp < 8) {                         // ---- the state: thread e holds row e
+        const int e = threadIdx.x - 128;
+        const uint32_t lanes = tmem + ((uint32_t)(warp - 4) << 21);
+        float Z[128];
+        const bool row = e < Dc;
+        const float *init = cp.state_only ? nullptr : w.init;
+#pragma unroll
+        for (int d = 0; d < 128; ++d) {
+            Z[d] = 0.f;
+            if (init != nullptr && row && d < Db)
+                Z[d] = w.init_t ? init[(head * w.Db + db0 + d) * w.Dc + dc0 + e] : init[(head * w.Dc + dc0 + e) * w.Db + db0 + d];
+        }
+        if (!cp.state_only && work > 0)            // through the earlier segments
+            for (int s = 0; s < seg; ++s) {
+                const int lo = s * p.seg_chunks, hi = lo + p.seg_chunks;      // whole segments, but for the row's end
+                const int steps = rev ? min(n, (chunks - lo) * kC) - (chunks - hi) * kC : p.seg_chunks * kC;
+                const float decay = exp2f(steps * log2f(p.g[h]));
+                const float4 *E = reinterpret_cast<const float4 *>(p.seg_state) + (size_t)(unit + s) * (kC * 32);
+#pragma unroll
+                for (int d = 0; d < 32; ++d) {
+                    const float4 u = E[d * 128 + e];
+                    Z[4 * d] = fmaf(decay, Z[4 * d], u.x);
+                    Z[4 * d + 1] = fmaf(decay, Z[4 * d + 1], u.y);
+                    Z[4 * d + 2] = fmaf(decay, Z[4 * d + 2], u.z);
+                    Z[4 * d + 3] = fmaf(decay, Z[4 * d + 3], u.w);
+                }
+            }
+        auto put_operand = [&]() {
+#pragma unroll
+            for (int c = 0; c < 16; ++c)
+                if (8 * c < Dbp)
+                    *piece_at(zb, e, c) = make_uint4(pack2_bf16(Z[8 * c], Z[8 * c + 1]), pack2_bf16(Z[8 * c + 2], Z[8 * c + 3]),
+                                                     pack2_bf16(Z[8 * c + 4], Z[8 * c + 5]), pack2_bf16(Z[8 * c + 6], Z[8 * c + 7]));
+        };
+        // Steps behind the row in the k-th chunk, where they are not beyond T (which reads as zeros): c may hold
+        // anything there, and 0 x NaN is NaN.
+        auto clear = [&](int k) {
+            const int L = length_of(first + k);
+            if (!masked || L == kC) return true;
+            if (!all_wait(full + (k & 1), k >> 1 & 1)) return false;
+            if (e >= L)
+                for (int c = 0; c < (Dc > 64 ? 16 : 8); ++c) *piece_at(smem + (k & 1) * kStage + 2 * kOperand, e, c) = make_uint4(0u, 0u, 0u, 0u);
+            return true;
+        };
+        if (work > 0 && !cp.state_only) {
+            put_operand();
+            ok = clear(0);
+            fence_proxy_async();
+            mbar_arrive(z_full);
+        }
+        for (int k = 0; k < work && ok; ++k) {
+            const int L = length_of(first + k), j = e;
+            const uint32_t ph = k & 1;
+            // b~: this thread's step j, weighted, as bf16 terms in the places of b, a and the state
+            // (o2_full: P has been read too)
+            if (!(ok = cp.state_only ? all_wait(full + (k & 1), k >> 1 & 1) && clear(k) : all_wait(o2_full, ph))) break;
+            unsigned char *a = smem + (k & 1) * kStage, *bb = a + kOperand;
+            const float wj = pw[j < L ? (rev ? j + 1 : L - 1 - j) : 0];
+#pragma unroll 4
+            for (int c = 0; c < 16; ++c) {
+                if (8 * c >= Dbp) break;
+                uint4 *at = piece_at(bb, j, c);
+                const uint4 raw = *at;
+                const uint32_t in[4] = {raw.x, raw.y, raw.z, raw.w};
+                uint32_t t0[4], t1[4], t2[4];
+#pragma unroll
+                for (int q = 0; q < 4; ++q) {
+                    const float lo = __uint_as_float(in[q] << 16), hi = __uint_as_float(in[q] & 0xffff0000u);
+                    float x0 = j < L ? lo * wj : 0.f, x1 = j < L ? hi * wj : 0.f;
+                    t0[q] = pack2_bf16(x0, x1);
+                    x0 -= __uint_as_float(t0[q] << 16);
+                    x1 -= __uint_as_float(t0[q] & 0xffff0000u);
+                    t1[q] = pack2_bf16(x0, x1);
+                    x0 -= __uint_as_float(t1[q] << 16);
+                    x1 -= __uint_as_float(t1[q] & 0xffff0000u);
+                    t2[q] = pack2_bf16(x0, x1);
+                }
+                *at = make_uint4(t0[0], t0[1], t0[2], t0[3]);
+                *piece_at(a, j, c) = make_uint4(t1[0], t1[1], t1[2], t1[3]);
+                if (terms == 3) *piece_at(zb, j, c) = make_uint4(t2[0], t2[1], t2[2], t2[3]);
+            }
+            fence_proxy_async();
+            mbar_arrive(bt_full);
+            if (!(ok = all_wait(u_full, ph))) break;
+            tc_fence_after();
+            const float decay = pw[L];
+#pragma unroll
+            for (int cb = 0; cb < 4; ++cb) {
+                if (32 * cb >= Db) break;
+                float u[32];
+                tmem_ld32f(lanes + kColU + 32 * cb, u);
+                tmem_wait_ld();
+#pragma unroll
+                for (int r = 0; r < 32; ++r) Z[32 * cb + r] = fmaf(decay, Z[32 * cb + r], u[r]);
+            }
+            tc_fence_before();
+            if (k + 1 < work) {
+                if (!cp.state_only) {
+                    put_operand();
+                    ok = clear(k + 1);
+                    fence_proxy_async();
+                }
+                mbar_arrive(z_full);
+            }
+        }
+        if (cp.state_only) {
+            float4 *E = reinterpret_cast<float4 *>(p.seg_state) + (size_t)(unit + seg) * (kC * 32);
+            if (work > 0)
+#pragma unroll
+                for (int d = 0; d < 32; ++d) E[d * 128 + e] = make_float4(Z[4 * d], Z[4 * d + 1], Z[4 * d + 2], Z[4 * d + 3]);
+        } else if (w.last != nullptr && row && seg == (chunks > 0 ? (chunks - 1) / p.seg_chunks : 0)) {
+#pragma unroll
+            for (int d = 0; d < 128; d += 4)
+                if (d < Db)                        // (Db is a multiple of 8)
+                    *reinterpret_cast<float4 *>(w.last + (head * w.Dc + dc0 + e) * w.Db + db0 + d) = make_float4(Z[d], Z[d + 1], Z[d + 2], Z[d + 3]);
+        }
+    } else if (warp == 8) {                        // ---- fetch a, b and c
+        if (lane == 0) {
+            const int nb = Db > 64 ? 2 : 1, nd = Dc > 64 ? 2 : 1;
+            const unsigned bytes = ((cp.state_only ? 1 : 2) * nb + nd) * kTile;
+            int k = 0;
+            for (; k < work; ++k) {
+                const int t0 = chunk_of(first + k) * kC, s = k & 1;
+                if (k >= 2 && !(ok = mbar_wait(empty + s, (k >> 1 & 1) ^ 1))) break;
+                unsigned char *st = smem + s * kStage;
+                mbar_expect_tx(full + s, bytes);
+                for (int i = 0; i < nb; ++i) {
+                    if (!cp.state_only)
+                        tma_load_4d(st + i * kTile, &maps.map[w.a_map], full + s, db0 + 64 * i, w.a_keys ? hk : h, t0, b);
+                    tma_load_4d(st + kOperand + i * kTile, &maps.map[w.b_map], full + s, db0 + 64 * i, w.b_keys ? hk : h, t0, b);
+                }
+                for (int i = 0; i < nd; ++i)
+                    tma_load_4d(st + 2 * kOperand + i * kTile, &maps.map[w.c_map], full + s, dc0 + 64 * i, w.c_keys ? hk : h, t0, b);
+            }
+            for (int i = max(k - 2, 0); i < k; ++i) mbar_wait(full + (i & 1), i >> 1 & 1);     // no copy outlives the CTA
+        }
+        __syncwarp();
+    } else if (warp == 9) {                        // ---- issue P and O1
+        if (!cp.state_only) {
+            const uint32_t lead = elect_one_sync();
+            const uint32_t idesc_p = umma_idesc(1, 128, 128), idesc_o = umma_idesc_t(1, 128, Dcp, false, true);
+            for (int k = 0; k < work; ++k) {
+                const uint32_t ph = k & 1;
+                const uint32_t a = smem_addr(smem) + (k & 1) * kStage, bb = a + kOperand, c = bb + kOperand;
+                // (P takes the place of the last chunk's P~; and not two of them before the other warp has seen one)
+                if (!(ok = all_wait(full + (k & 1), k >> 1 & 1) && (k == 0 || (all_wait(o1_full, ph ^ 1) && all_wait(o2_full, ph ^ 1))))) break;
+                tc_fence_after();
+                for (int q = 0; 16 * q < Db; ++q) {
+                    const uint32_t off = (q >> 2) * kTile + (q & 3) * 32;
+                    umma_bf16_w(tmem + kColP, desc_k(a + off), desc_k(bb + off), idesc_p, q > 0, lead);
+                }
+                umma_commit_w(p_full, lead);
+                ok = all_wait(pt_full, ph) && (k == 0 || all_wait(o_empty, ph ^ 1)) &&
+                     (!(masked && length_of(first + k) < kC) || all_wait(o2_full, ph));           // (c is cleared by then)
+                if (!ok) break;
+                tc_fence_after();
+                uint64_t cd = desc_mn(c);
+#pragma unroll
+                for (int q = 0; q < kC / 16; ++q, cd += 2048 >> 4) umma_bf16_tw(tmem + kColO1, tmem + kColP + 8 * q, cd, idesc_o, q > 0, lead);
+                umma_commit_w(o1_full, lead);
+                umma_commit_w(empty + (k & 1), lead);
+            }
+        }
+    } else {                                       // ---- issue O2 and U
+        const uint32_t lead = elect_one_sync();
+        const uint32_t idesc_o = umma_idesc(1, 128, Dcp), idesc_u = umma_idesc_t(1, 128, Dbp, true, true);
+        for (int k = 0; k < work; ++k) {
+            const uint32_t ph = k & 1;
+            const uint32_t a = smem_addr(smem) + (k & 1) * kStage, bb = a + kOperand, c = bb + kOperand, z = smem_addr(zb);
+            if (!(ok = all_wait(full + (k & 1), k >> 1 & 1))) break;
+            if (!cp.state_only) {
+                if (!(ok = all_wait(z_full, ph) && all_wait(p_full, ph) && (k == 0 || all_wait(o_empty, ph ^ 1)))) break;
+                tc_fence_after();
+                for (int q = 0; 16 * q < Db; ++q) {
+                    const uint32_t off = (q >> 2) * kTile + (q & 3) * 32;
+                    umma_bf16_w(tmem + kColO2, desc_k(a + off), desc_k(z + off), idesc_o, q > 0, lead);
+                }
+                umma_commit_w(o2_full, lead);
+            } else if (k > 0 && !(ok = all_wait(z_full, ph ^ 1))) {
+                break;
+            }
+            if (!(ok = all_wait(bt_full, ph))) break;
+            tc_fence_after();
+            for (int term = terms - 1; term >= 0; --term) {                  // smallest first
+                uint64_t cd = desc_mn(c), bd = desc_mn(term == 0 ? bb : term == 1 ? a : z);
+#pragma unroll
+                for (int q = 0; q < kC / 16; ++q, cd += 2048 >> 4, bd += 2048 >> 4)
+                    umma_bf16_w(tmem + kColU, cd, bd, idesc_u, term < terms - 1 || q > 0, lead);
+            }
+            umma_commit_w(u_full, lead);
+            umma_commit_w(empty + (k & 1), lead);
+        }
+    }
+    if (!ok && lane == 0) report_status(p.status, kStatusTimeout);
+    __syncwarp();
+    tc_fence_before();
+    __syncthreads();
+    if (warp == 8) tmem_dealloc(tmem, 512);
+}
+
+// Segments of a row's chunks, where one CTA for each head and block of columns leaves SMs idle: as many as
+// fill them once.
+void linattn_segments(LinattnParams *p) {
+    const int chunks = (p->T + kC - 1) / kC;
+    long long ctas = 0;
+    for (int i = 0; i < p->sweeps; ++i) ctas += (long long)((p->sweep[i].Db + 127) / 128) * ((p->sweep[i].Dc + 127) / 128);
+    ctas *= (long long)p->B * p->Hv;
+    long long segs = 152 / ctas;
+    if (segs > chunks / 2) segs = chunks / 2;
+    if (segs > 32) segs = 32;
+    if (segs < 2) segs = 1;
+    p->seg_chunks = (int)((chunks + segs - 1) / segs);
+    p->segs = (chunks + p->seg_chunks - 1) / p->seg_chunks;
+    p->seg_units = (size_t)ctas * (p->segs - 1);
+}
+
+cudaError_t launch_linattn_chunks(const LinattnParams &p, const LinattnMaps &maps, cudaStream_t s) {
+    cudaError_t e = allow_smem<linattn_chunk_kernel>((int)kSmem);
+    if (e != cudaSuccess) return e;
+    SweepArgs cp = {};
+    cp.p = p;
+    int blocks = 0;
+    for (int i = 0; i < p.sweeps; ++i) {
+        cp.blocks[i] = ((p.sweep[i].Db + 127) / 128) * ((p.sweep[i].Dc + 127) / 128);
+        blocks += cp.blocks[i];
+    }
+    if (p.segs > 1) {
+        cp.state_only = 1;
+        timing_mark("linattn_states", 0, s);
+        linattn_chunk_kernel<<<dim3(blocks * (p.segs - 1), p.Hv, p.B), kThreads, kSmem, s>>>(maps, cp);
+        e = cudaGetLastError();
+        timing_mark("linattn_states", 1, s);
+        if (e != cudaSuccess) return e;
+        cp.state_only = 0;
+    }
+    timing_mark("linattn_chunk", 0, s);
+    linattn_chunk_kernel<<<dim3(blocks * p.segs, p.Hv, p.B), kThreads, kSmem, s>>>(maps, cp);
+    e = cudaGetLastError();
+    timing_mark("linattn_chunk", 1, s);
+    if (e == cudaSuccess && p.sums > 0) e = launch_linattn_sums(p, 1, s);
+    return e;
+}
+
+}  // namespace gdn

@@ -21,22 +21,28 @@
 // truncating additions of the tensor cores never run over more than a chunk. Rounded to bf16 besides
 // the outputs: P~ and Z as an operand, each a relative 2^-9 of terms of either sign.
 //
-// Warps 0-3 mask P and write outputs; warps 4-7 hold the state; one warp fetches (two chunks deep), two
+// Warps 0-3 mask P and write outputs; warps 4-11 hold the state (each four one half of its columns, so that
+// the products with one half run under the additions to the other); one warp fetches (two chunks deep), two
 // issue products: P and O1, and O2 and U, so that neither chain waits for the other.
 #include "gdn.h"
 #include "gdn_layer.cuh"
 #include "gdn_umma.cuh"
+
+#include <type_traits>
 
 namespace gdn {
 
 namespace {
 
 constexpr int kC = kLinattnChunk;
-constexpr int kThreads = 11 * 32;
+constexpr int kThreads = 16 * 32;                  // (the last warp only completes its group)
+// registers of a thread: launched with 128, then dealt out again
+constexpr int kLaunchRegs = 128, kOutRegs = 104, kStateRegs = 160, kIssueRegs = 64;
+static_assert(kOutRegs + 2 * kStateRegs + kIssueRegs <= 4 * kLaunchRegs, "register split exceeds the launch's registers");
 constexpr int kTile = 64 * kC * 2;                 // 64 columns of a chunk: 128 rows of 128 bytes
 constexpr int kOperand = 2 * kTile;
 constexpr int kStage = 3 * kOperand;               // a, b, c
-constexpr size_t kSmem = 1024 + 2 * kStage + kOperand + 136 * 4 + 16 * 8 + 16;
+constexpr size_t kSmem = 1024 + 2 * kStage + kOperand + (136 + 32) * 4 + 16 * 8 + 16;
 // tensor memory columns
 constexpr int kColP = 0, kColO1 = 128, kColO2 = 256, kColU = 384;
 
@@ -66,6 +72,39 @@ __device__ __forceinline__ uint4 *piece_at(unsigned char *operand, int r, int pi
 // mbar_wait by a whole warp, with one answer
 __device__ __forceinline__ bool all_wait(uint64_t *bar, uint32_t parity) { return __all_sync(kFullMask, mbar_wait(bar, parity)); }
 
+// 32 bytes of a row, at once where they are aligned to that (every lane has a row of its own, and a store of 32
+// rows takes a cycle for each)
+__device__ __forceinline__ void store_piece2(void *p, float a, float b, float c, float d, float e, float f, float g, float h, bool wide) {
+    if (wide) {
+        asm volatile("st.global.v8.f32 [%0], {%1,%2,%3,%4,%5,%6,%7,%8};" ::"l"(p), "f"(a), "f"(b), "f"(c), "f"(d), "f"(e), "f"(f), "f"(g), "f"(h)
+                     : "memory");
+    } else {
+        *static_cast<float4 *>(p) = make_float4(a, b, c, d);
+        *(static_cast<float4 *>(p) + 1) = make_float4(e, f, g, h);
+    }
+}
+
+// b w for a pair of b and w = w0 + w1 + w2 as bf16 terms, in packed bf16 arithmetic (in float32 the conversions
+// alone cost as much): t0 = b w0 rounded; the product of two bf16 has 16 bits, so its rest is a bf16 exactly; t1 =
+// that rest + b w1 rounded, some 2^-9 of the product. Three terms: what t1 lost (a two-sum, and the rest of b w1,
+// both exact) + b w2, some 2^-18, with an error of 2^-26 of the product.
+using bf16x2 = __nv_bfloat162;
+__device__ __forceinline__ uint32_t bits(const bf16x2 &x) { return *reinterpret_cast<const uint32_t *>(&x); }
+template <bool THREE>
+__device__ __forceinline__ void split_product(uint32_t b, bf16x2 w0, bf16x2 w1, bf16x2 w2, uint32_t &t0, uint32_t &t1, uint32_t &t2) {
+    const bf16x2 x = *reinterpret_cast<const bf16x2 *>(&b), a = __hmul2_rn(x, w0), rest = __hfma2(x, w0, __hneg2(a));
+    t0 = bits(a);
+    if (!THREE) {
+        t1 = bits(__hfma2(x, w1, rest));
+        return;
+    }
+    const bf16x2 u = __hmul2_rn(x, w1), u_rest = __hfma2(x, w1, __hneg2(u));
+    const bf16x2 m = __hadd2_rn(rest, u), v = __hsub2_rn(m, rest);
+    const bf16x2 lost = __hadd2_rn(__hsub2_rn(rest, __hsub2_rn(m, v)), __hsub2_rn(u, v));
+    t1 = bits(m);
+    t2 = bits(__hfma2(x, w2, __hadd2_rn(lost, u_rest)));
+}
+
 __device__ __forceinline__ void write_zeros(const LinattnSweep &w, size_t at, int n) {
     if (w.sums)
         for (int i = 0; i < n; i += 4) *reinterpret_cast<float4 *>(static_cast<float *>(w.out) + at + i) = make_float4(0.f, 0.f, 0.f, 0.f);
@@ -80,9 +119,11 @@ __global__ void __launch_bounds__(kThreads, 1) linattn_chunk_kernel(const __grid
     unsigned char *smem = reinterpret_cast<unsigned char *>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~(uintptr_t)1023);
     unsigned char *zb = smem + 2 * kStage;                                   // the state as an operand [e][d]
     float *pw = reinterpret_cast<float *>(zb + kOperand);                    // g^0 .. g^128
-    uint64_t *full = reinterpret_cast<uint64_t *>(pw + 136), *empty = full + 2;
-    uint64_t *p_full = full + 4, *pt_full = full + 5, *o1_full = full + 6, *o2_full = full + 7, *o_empty = full + 8, *bt_full = full + 9,
-             *u_full = full + 10, *z_full = full + 11;
+    float *pw_back = pw + 136;                                               // g^31 .. g^0
+    uint64_t *full = reinterpret_cast<uint64_t *>(pw_back + 32), *empty = full + 2;
+    uint64_t *p_full = full + 4, *pt_full = full + 5, *o1_full = full + 6, *o2_full = full + 7, *o_empty = full + 8;
+    uint64_t *u_full = full + 9, *bt_full = full + 10, *z_full = full + 12;  // (the last two: one for each half of the columns)
+    uint64_t *p_seen = full + 14;
     uint32_t *tmem_slot = reinterpret_cast<uint32_t *>(full + 16);
     const LinattnParams &p = cp.p;
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
@@ -104,7 +145,6 @@ __global__ void __launch_bounds__(kThreads, 1) linattn_chunk_kernel(const __grid
     const int n = row_length(p.lens, b, p.T), chunks = (n + kC - 1) / kC;
     const int first = seg * p.seg_chunks, last = min(first + p.seg_chunks, chunks);       // in the order of the sweep
     const bool rev = w.rev != 0, masked = p.lens != nullptr;
-    const int terms = w.last != nullptr ? 3 : 2;
     auto chunk_of = [&](int i) { return rev ? chunks - 1 - i : i; };
     auto length_of = [&](int i) { return min(kC, n - chunk_of(i) * kC); };
     const int Dbp = (Db + 15) / 16 * 16, Dcp = (Dc + 15) / 16 * 16;                        // (zeros behind Db, Dc)
@@ -116,23 +156,33 @@ __global__ void __launch_bounds__(kThreads, 1) linattn_chunk_kernel(const __grid
             mbar_init(empty + i, cp.state_only ? 1 : 2);
         }
         for (uint64_t *bar : {p_full, o1_full, o2_full, u_full}) mbar_init(bar, 1);
-        for (uint64_t *bar : {pt_full, o_empty, bt_full, z_full}) mbar_init(bar, 128);
+        for (uint64_t *bar : {pt_full, o_empty, bt_full, bt_full + 1, z_full, z_full + 1}) mbar_init(bar, 128);
+        mbar_init(p_seen, 1 + (Dbp > 64 ? 8 : 4));
         fence_mbar_init();
     }
-    if (warp == 8) tmem_alloc(tmem_slot, 512);
+    if (warp == 12) tmem_alloc(tmem_slot, 512);
     {
-        const float g = p.g[h], lg = log2f(g);
+        const float lg = log2f(p.g[h]);
         for (int i = threadIdx.x; i <= kC; i += kThreads) pw[i] = i == 0 ? 1.f : exp2f(i * lg);
+        if (threadIdx.x < 32) pw_back[threadIdx.x] = threadIdx.x == 31 ? 1.f : exp2f((31 - (int)threadIdx.x) * lg);
     }
     tc_fence_before();
     __syncthreads();
     tc_fence_after();
     const uint32_t tmem = *tmem_slot;
+    // Terms of b~: where the state leaves the call, the chunks that still count in it by 1 / 16 hold 24 bits.
+    const float lg = log2f(p.g[h]);
+    auto terms_of = [&](int i) {
+        const int after = rev ? chunk_of(i) * kC : max(n - (chunk_of(i) + 1) * kC, 0);        // steps that follow it in the sweep
+        return w.last != nullptr && (after == 0 || after * lg >= -4.f) ? 3 : 2;
+    };
     const size_t out_step = (size_t)p.Hv * w.Dc;
     const size_t out0 = (size_t)(db0 / 128) * p.B * p.T * out_step + (size_t)b * p.T * out_step + (size_t)h * w.Dc + dc0;
     bool ok = true;
 
     if (warp < 4) {                                // ---- decay and mask P, write the outputs
+        regs_dec<kOutRegs>();
+        const bool wide = ((uintptr_t)w.out & 31) == 0 && w.Dc % 16 == 0;
         const uint32_t lanes = tmem + ((uint32_t)warp << 21);
         const int i = threadIdx.x;                 // this thread's step of the chunk
         for (int k = 0; k < work && !cp.state_only; ++k) {
@@ -140,7 +190,7 @@ __global__ void __launch_bounds__(kThreads, 1) linattn_chunk_kernel(const __grid
             const uint32_t ph = k & 1;
             if (!(ok = all_wait(p_full, ph))) break;
             tc_fence_after();
-#pragma unroll
+#pragma unroll 1
             for (int cb = 0; cb < 4; ++cb) {
                 float v[32];
                 if (rev ? cb >= warp : cb <= warp) {
@@ -155,11 +205,18 @@ __global__ void __launch_bounds__(kThreads, 1) linattn_chunk_kernel(const __grid
                         }
                     } else {
                         const float f = pw[rev ? 32 * cb - i : i - 32 * cb - 31];
+                        const float4 *d4 = reinterpret_cast<const float4 *>(rev ? pw : pw_back);
 #pragma unroll
-                        for (int r = 0; r < 32; ++r) {
-                            const float d = f * pw[rev ? r : 31 - r];
-                            v[r] = !rev || 32 * cb + r < L ? v[r] * d : 0.f;
+                        for (int r = 0; r < 32; r += 4) {
+                            const float4 d = d4[r / 4];
+                            float2 x = __fmul2_rn(make_float2(v[r], v[r + 1]), __fmul2_rn(make_float2(d.x, d.y), make_float2(f, f)));
+                            v[r] = x.x; v[r + 1] = x.y;
+                            x = __fmul2_rn(make_float2(v[r + 2], v[r + 3]), __fmul2_rn(make_float2(d.z, d.w), make_float2(f, f)));
+                            v[r + 2] = x.x; v[r + 3] = x.y;
                         }
+                        if (rev && L < kC)
+#pragma unroll
+                            for (int r = 0; r < 32; ++r) v[r] = 32 * cb + r < L ? v[r] : 0.f;
                     }
                 } else {
 #pragma unroll
@@ -177,28 +234,36 @@ __global__ void __launch_bounds__(kThreads, 1) linattn_chunk_kernel(const __grid
             tc_fence_after();
             const float s = pw[rev ? max(L - 1 - i, 0) : i + 1];
             const size_t at = out0 + (size_t)(t0 + i) * out_step;
-#pragma unroll
-            for (int cb = 0; cb < 4; ++cb) {
-                if (32 * cb >= Dc) break;
+#pragma unroll 1
+            for (int cb = 0; 32 * cb < Dc; ++cb) {
                 float o1[32], o2[32];
                 tmem_ld32f(lanes + kColO1 + 32 * cb, o1);
                 tmem_ld32f(lanes + kColO2 + 32 * cb, o2);
                 tmem_wait_ld();
 #pragma unroll
-                for (int r = 0; r < 32; ++r) o1[r] = fmaf(s, o2[r], o1[r]);
+                for (int r = 0; r < 32; r += 2) {
+                    const float2 x = __ffma2_rn(make_float2(s, s), make_float2(o2[r], o2[r + 1]), make_float2(o1[r], o1[r + 1]));
+                    o1[r] = x.x;
+                    o1[r + 1] = x.y;
+                }
                 if (i >= L) continue;
                 if (w.sums) {
                     float *out = static_cast<float *>(w.out) + at + 32 * cb;
 #pragma unroll
-                    for (int r = 0; r < 32; r += 4)
-                        if (32 * cb + r < Dc) *reinterpret_cast<float4 *>(out + r) = make_float4(o1[r], o1[r + 1], o1[r + 2], o1[r + 3]);
+                    for (int r = 0; r < 32; r += 8)
+                        if (32 * cb + r < Dc) store_piece2(out + r, o1[r], o1[r + 1], o1[r + 2], o1[r + 3], o1[r + 4], o1[r + 5], o1[r + 6], o1[r + 7], wide);
                 } else {
                     __nv_bfloat16 *out = static_cast<__nv_bfloat16 *>(w.out) + at + 32 * cb;
+                    float y[16];
 #pragma unroll
-                    for (int r = 0; r < 32; r += 8)
-                        if (32 * cb + r < Dc)
-                            *reinterpret_cast<uint4 *>(out + r) = make_uint4(pack2_bf16(o1[r], o1[r + 1]), pack2_bf16(o1[r + 2], o1[r + 3]),
-                                                                             pack2_bf16(o1[r + 4], o1[r + 5]), pack2_bf16(o1[r + 6], o1[r + 7]));
+                    for (int r = 0; r < 16; ++r) y[r] = __uint_as_float(pack2_bf16(o1[2 * r], o1[2 * r + 1]));
+#pragma unroll
+                    for (int r = 0; r < 16; r += 8) {
+                        if (32 * cb + 2 * r + 8 < Dc)
+                            store_piece2(out + 2 * r, y[r], y[r + 1], y[r + 2], y[r + 3], y[r + 4], y[r + 5], y[r + 6], y[r + 7], wide);
+                        else if (32 * cb + 2 * r < Dc)
+                            *reinterpret_cast<float4 *>(out + 2 * r) = make_float4(y[r], y[r + 1], y[r + 2], y[r + 3]);
+                    }
                 }
             }
             tc_fence_before();
@@ -209,26 +274,28 @@ __global__ void __launch_bounds__(kThreads, 1) linattn_chunk_kernel(const __grid
             const int from = max(n, seg * p.seg_chunks * kC), to = seg == p.segs - 1 ? p.T : min(p.T, (seg + 1) * p.seg_chunks * kC);
             for (int t = from + i; t < to; t += 128) write_zeros(w, out0 + (size_t)t * out_step, Dc);
         }
-    } else if (warp < 8) {                         // ---- the state: thread e holds row e
-        const int e = threadIdx.x - 128;
-        const uint32_t lanes = tmem + ((uint32_t)(warp - 4) << 21);
-        float Z[128];
+    } else if (warp < 12) {                        // ---- the state: a thread holds half of row e
+        regs_inc<kStateRegs>();
+        const int e = threadIdx.x & 127, half = (warp - 4) >> 2, d0 = 64 * half;
+        const uint32_t lanes = tmem + ((uint32_t)(warp & 3) << 21) + kColU + d0;
+        float Z[64];
         const bool row = e < Dc;
+        const int work_here = d0 < Dbp ? work : 0;
         const float *init = cp.state_only ? nullptr : w.init;
 #pragma unroll
-        for (int d = 0; d < 128; ++d) {
+        for (int d = 0; d < 64; ++d) {
             Z[d] = 0.f;
-            if (init != nullptr && row && d < Db)
-                Z[d] = w.init_t ? init[(head * w.Db + db0 + d) * w.Dc + dc0 + e] : init[(head * w.Dc + dc0 + e) * w.Db + db0 + d];
+            if (init != nullptr && row && d0 + d < Db)
+                Z[d] = w.init_t ? init[(head * w.Db + db0 + d0 + d) * w.Dc + dc0 + e] : init[(head * w.Dc + dc0 + e) * w.Db + db0 + d0 + d];
         }
-        if (!cp.state_only && work > 0)            // through the earlier segments
+        if (!cp.state_only && work_here > 0)       // through the earlier segments
             for (int s = 0; s < seg; ++s) {
                 const int lo = s * p.seg_chunks, hi = lo + p.seg_chunks;      // whole segments, but for the row's end
                 const int steps = rev ? min(n, (chunks - lo) * kC) - (chunks - hi) * kC : p.seg_chunks * kC;
                 const float decay = exp2f(steps * log2f(p.g[h]));
-                const float4 *E = reinterpret_cast<const float4 *>(p.seg_state) + (size_t)(unit + s) * (kC * 32);
+                const float4 *E = reinterpret_cast<const float4 *>(p.seg_state) + (size_t)(unit + s) * (kC * 32) + half * (kC * 16);
 #pragma unroll
-                for (int d = 0; d < 32; ++d) {
+                for (int d = 0; d < 16; ++d) {
                     const float4 u = E[d * 128 + e];
                     Z[4 * d] = fmaf(decay, Z[4 * d], u.x);
                     Z[4 * d + 1] = fmaf(decay, Z[4 * d + 1], u.y);
@@ -238,71 +305,76 @@ __global__ void __launch_bounds__(kThreads, 1) linattn_chunk_kernel(const __grid
             }
         auto put_operand = [&]() {
 #pragma unroll
-            for (int c = 0; c < 16; ++c)
-                if (8 * c < Dbp)
-                    *piece_at(zb, e, c) = make_uint4(pack2_bf16(Z[8 * c], Z[8 * c + 1]), pack2_bf16(Z[8 * c + 2], Z[8 * c + 3]),
-                                                     pack2_bf16(Z[8 * c + 4], Z[8 * c + 5]), pack2_bf16(Z[8 * c + 6], Z[8 * c + 7]));
+            for (int c = 0; c < 8; ++c)
+                *piece_at(zb, e, 8 * half + c) = make_uint4(pack2_bf16(Z[8 * c], Z[8 * c + 1]), pack2_bf16(Z[8 * c + 2], Z[8 * c + 3]),
+                                                            pack2_bf16(Z[8 * c + 4], Z[8 * c + 5]), pack2_bf16(Z[8 * c + 6], Z[8 * c + 7]));
         };
         // Steps behind the row in the k-th chunk, where they are not beyond T (which reads as zeros): c may hold
         // anything there, and 0 x NaN is NaN.
         auto clear = [&](int k) {
             const int L = length_of(first + k);
-            if (!masked || L == kC) return true;
+            if (!masked || L == kC || half != 0) return true;
             if (!all_wait(full + (k & 1), k >> 1 & 1)) return false;
             if (e >= L)
                 for (int c = 0; c < (Dc > 64 ? 16 : 8); ++c) *piece_at(smem + (k & 1) * kStage + 2 * kOperand, e, c) = make_uint4(0u, 0u, 0u, 0u);
             return true;
         };
-        if (work > 0 && !cp.state_only) {
+        if (work_here > 0 && !cp.state_only) {
             put_operand();
             ok = clear(0);
             fence_proxy_async();
-            mbar_arrive(z_full);
+            mbar_arrive(z_full + half);
         }
-        for (int k = 0; k < work && ok; ++k) {
-            const int L = length_of(first + k), j = e;
+        for (int k = 0; k < work_here && ok; ++k) {
+            const int L = length_of(first + k), j = e, terms = terms_of(first + k);
             const uint32_t ph = k & 1;
-            // b~: this thread's step j, weighted, as bf16 terms in the places of b, a and the state
-            // (o2_full: P has been read too)
-            if (!(ok = cp.state_only ? all_wait(full + (k & 1), k >> 1 & 1) && clear(k) : all_wait(o2_full, ph))) break;
+            // b~: this thread's step j, weighted, as bf16 terms: the first takes b's place once P is there, the others,
+            // formed meanwhile, those of a and the state once O2 is
+            if (!(ok = cp.state_only ? all_wait(full + (k & 1), k >> 1 & 1) && clear(k) : all_wait(p_full, ph))) break;
+            if (lane == 0) mbar_arrive(p_seen);
             unsigned char *a = smem + (k & 1) * kStage, *bb = a + kOperand;
             const float wj = pw[j < L ? (rev ? j + 1 : L - 1 - j) : 0];
-#pragma unroll 4
-            for (int c = 0; c < 16; ++c) {
-                if (8 * c >= Dbp) break;
-                uint4 *at = piece_at(bb, j, c);
-                const uint4 raw = *at;
-                const uint32_t in[4] = {raw.x, raw.y, raw.z, raw.w};
-                uint32_t t0[4], t1[4], t2[4];
+            const bf16x2 w0 = __float2bfloat162_rn(wj), w1 = __float2bfloat162_rn(wj - __low2float(w0)),
+                                 w2 = __float2bfloat162_rn(wj - __low2float(w0) - __low2float(w1));
+            auto write_terms = [&](auto three) {
+                constexpr bool THREE = decltype(three)::value;
+                uint32_t t1[32], t2[THREE ? 32 : 1];
 #pragma unroll
-                for (int q = 0; q < 4; ++q) {
-                    const float lo = __uint_as_float(in[q] << 16), hi = __uint_as_float(in[q] & 0xffff0000u);
-                    float x0 = j < L ? lo * wj : 0.f, x1 = j < L ? hi * wj : 0.f;
-                    t0[q] = pack2_bf16(x0, x1);
-                    x0 -= __uint_as_float(t0[q] << 16);
-                    x1 -= __uint_as_float(t0[q] & 0xffff0000u);
-                    t1[q] = pack2_bf16(x0, x1);
-                    x0 -= __uint_as_float(t1[q] << 16);
-                    x1 -= __uint_as_float(t1[q] & 0xffff0000u);
-                    t2[q] = pack2_bf16(x0, x1);
+                for (int c = 0; c < 8; ++c) {
+                    uint4 *at = piece_at(bb, j, 8 * half + c);
+                    uint4 raw = *at;
+                    if (j >= L) raw = make_uint4(0u, 0u, 0u, 0u);
+                    const uint32_t in[4] = {raw.x, raw.y, raw.z, raw.w};
+                    uint32_t t0[4];
+#pragma unroll
+                    for (int q = 0; q < 4; ++q) split_product<THREE>(in[q], w0, w1, w2, t0[q], t1[4 * c + q], t2[THREE ? 4 * c + q : 0]);
+                    *at = make_uint4(t0[0], t0[1], t0[2], t0[3]);
                 }
-                *at = make_uint4(t0[0], t0[1], t0[2], t0[3]);
-                *piece_at(a, j, c) = make_uint4(t1[0], t1[1], t1[2], t1[3]);
-                if (terms == 3) *piece_at(zb, j, c) = make_uint4(t2[0], t2[1], t2[2], t2[3]);
-            }
+                if (!cp.state_only && !all_wait(o2_full, ph)) return false;
+#pragma unroll
+                for (int c = 0; c < 8; ++c) {
+                    *piece_at(a, j, 8 * half + c) = make_uint4(t1[4 * c], t1[4 * c + 1], t1[4 * c + 2], t1[4 * c + 3]);
+                    if constexpr (THREE) *piece_at(zb, j, 8 * half + c) = make_uint4(t2[4 * c], t2[4 * c + 1], t2[4 * c + 2], t2[4 * c + 3]);
+                }
+                return true;
+            };
+            if (!(ok = terms == 3 ? write_terms(std::true_type()) : write_terms(std::false_type()))) break;
             fence_proxy_async();
-            mbar_arrive(bt_full);
+            mbar_arrive(bt_full + half);
             if (!(ok = all_wait(u_full, ph))) break;
             tc_fence_after();
-            const float decay = pw[L];
+            const float2 decay = make_float2(pw[L], pw[L]);
 #pragma unroll
-            for (int cb = 0; cb < 4; ++cb) {
-                if (32 * cb >= Db) break;
+            for (int cb = 0; cb < 2; ++cb) {
                 float u[32];
-                tmem_ld32f(lanes + kColU + 32 * cb, u);
+                tmem_ld32f(lanes + 32 * cb, u);
                 tmem_wait_ld();
 #pragma unroll
-                for (int r = 0; r < 32; ++r) Z[32 * cb + r] = fmaf(decay, Z[32 * cb + r], u[r]);
+                for (int r = 0; r < 32; r += 2) {
+                    const float2 z = __ffma2_rn(decay, make_float2(Z[32 * cb + r], Z[32 * cb + r + 1]), make_float2(u[r], u[r + 1]));
+                    Z[32 * cb + r] = z.x;
+                    Z[32 * cb + r + 1] = z.y;
+                }
             }
             tc_fence_before();
             if (k + 1 < work) {
@@ -311,21 +383,23 @@ __global__ void __launch_bounds__(kThreads, 1) linattn_chunk_kernel(const __grid
                     ok = clear(k + 1);
                     fence_proxy_async();
                 }
-                mbar_arrive(z_full);
+                mbar_arrive(z_full + half);
             }
         }
         if (cp.state_only) {
-            float4 *E = reinterpret_cast<float4 *>(p.seg_state) + (size_t)(unit + seg) * (kC * 32);
+            float4 *E = reinterpret_cast<float4 *>(p.seg_state) + (size_t)(unit + seg) * (kC * 32) + half * (kC * 16);
             if (work > 0)
 #pragma unroll
-                for (int d = 0; d < 32; ++d) E[d * 128 + e] = make_float4(Z[4 * d], Z[4 * d + 1], Z[4 * d + 2], Z[4 * d + 3]);
+                for (int d = 0; d < 16; ++d) E[d * 128 + e] = make_float4(Z[4 * d], Z[4 * d + 1], Z[4 * d + 2], Z[4 * d + 3]);
         } else if (w.last != nullptr && row && seg == (chunks > 0 ? (chunks - 1) / p.seg_chunks : 0)) {
 #pragma unroll
-            for (int d = 0; d < 128; d += 4)
-                if (d < Db)                        // (Db is a multiple of 8)
-                    *reinterpret_cast<float4 *>(w.last + (head * w.Dc + dc0 + e) * w.Db + db0 + d) = make_float4(Z[d], Z[d + 1], Z[d + 2], Z[d + 3]);
+            for (int d = 0; d < 64; d += 4)
+                if (d0 + d < Db)                   // (Db is a multiple of 8)
+                    *reinterpret_cast<float4 *>(w.last + (head * w.Dc + dc0 + e) * w.Db + db0 + d0 + d) = make_float4(Z[d], Z[d + 1], Z[d + 2], Z[d + 3]);
         }
-    } else if (warp == 8) {                        // ---- fetch a, b and c
+    } else {
+    regs_dec<kIssueRegs>();
+    if (warp == 12) {                              // ---- fetch a, b and c
         if (lane == 0) {
             const int nb = Db > 64 ? 2 : 1, nd = Dc > 64 ? 2 : 1;
             const unsigned bytes = ((cp.state_only ? 1 : 2) * nb + nd) * kTile;
@@ -346,15 +420,15 @@ __global__ void __launch_bounds__(kThreads, 1) linattn_chunk_kernel(const __grid
             for (int i = max(k - 2, 0); i < k; ++i) mbar_wait(full + (i & 1), i >> 1 & 1);     // no copy outlives the CTA
         }
         __syncwarp();
-    } else if (warp == 9) {                        // ---- issue P and O1
+    } else if (warp == 13) {                       // ---- issue P and O1
         if (!cp.state_only) {
             const uint32_t lead = elect_one_sync();
             const uint32_t idesc_p = umma_idesc(1, 128, 128), idesc_o = umma_idesc_t(1, 128, Dcp, false, true);
             for (int k = 0; k < work; ++k) {
                 const uint32_t ph = k & 1;
                 const uint32_t a = smem_addr(smem) + (k & 1) * kStage, bb = a + kOperand, c = bb + kOperand;
-                // (P takes the place of the last chunk's P~; and not two of them before the other warp has seen one)
-                if (!(ok = all_wait(full + (k & 1), k >> 1 & 1) && (k == 0 || (all_wait(o1_full, ph ^ 1) && all_wait(o2_full, ph ^ 1))))) break;
+                // (P takes the place of the last chunk's P~, and is issued when all have seen that the last one was there)
+                if (!(ok = all_wait(full + (k & 1), k >> 1 & 1) && (k == 0 || (all_wait(o1_full, ph ^ 1) && all_wait(p_seen, ph ^ 1))))) break;
                 tc_fence_after();
                 for (int q = 0; 16 * q < Db; ++q) {
                     const uint32_t off = (q >> 2) * kTile + (q & 3) * 32;
@@ -372,25 +446,33 @@ __global__ void __launch_bounds__(kThreads, 1) linattn_chunk_kernel(const __grid
                 umma_commit_w(empty + (k & 1), lead);
             }
         }
-    } else {                                       // ---- issue O2 and U
+    } else if (warp == 14) {                       // ---- issue O2 and U
         const uint32_t lead = elect_one_sync();
         const uint32_t idesc_o = umma_idesc(1, 128, Dcp), idesc_u = umma_idesc_t(1, 128, Dbp, true, true);
+        const int halves = Dbp > 64 ? 2 : 1;
         for (int k = 0; k < work; ++k) {
             const uint32_t ph = k & 1;
             const uint32_t a = smem_addr(smem) + (k & 1) * kStage, bb = a + kOperand, c = bb + kOperand, z = smem_addr(zb);
+            const int terms = terms_of(first + k);
             if (!(ok = all_wait(full + (k & 1), k >> 1 & 1))) break;
             if (!cp.state_only) {
-                if (!(ok = all_wait(z_full, ph) && all_wait(p_full, ph) && (k == 0 || all_wait(o_empty, ph ^ 1)))) break;
-                tc_fence_after();
-                for (int q = 0; 16 * q < Db; ++q) {
-                    const uint32_t off = (q >> 2) * kTile + (q & 3) * 32;
-                    umma_bf16_w(tmem + kColO2, desc_k(a + off), desc_k(z + off), idesc_o, q > 0, lead);
+                if (!(ok = all_wait(p_full, ph))) break;
+                if (lane == 0) mbar_arrive(p_seen);
+                if (!(ok = (k == 0 || all_wait(o_empty, ph ^ 1)))) break;
+                for (int half = 0; half < halves && ok; ++half) {            // half of the state's columns at a time
+                    if (!(ok = all_wait(z_full + half, ph))) break;
+                    tc_fence_after();
+                    for (int q = 0; q < 4 && 64 * half + 16 * q < Db; ++q) {
+                        const uint32_t off = half * kTile + q * 32;
+                        umma_bf16_w(tmem + kColO2, desc_k(a + off), desc_k(z + off), idesc_o, half + q > 0, lead);
+                    }
                 }
+                if (!ok) break;
                 umma_commit_w(o2_full, lead);
-            } else if (k > 0 && !(ok = all_wait(z_full, ph ^ 1))) {
-                break;
             }
-            if (!(ok = all_wait(bt_full, ph))) break;
+            for (int half = 0; half < halves && ok; ++half)
+                ok = all_wait(bt_full + half, ph) && !(cp.state_only && k > 0 && !all_wait(z_full + half, ph ^ 1));
+            if (!ok) break;
             tc_fence_after();
             for (int term = terms - 1; term >= 0; --term) {                  // smallest first
                 uint64_t cd = desc_mn(c), bd = desc_mn(term == 0 ? bb : term == 1 ? a : z);
@@ -402,11 +484,12 @@ __global__ void __launch_bounds__(kThreads, 1) linattn_chunk_kernel(const __grid
             umma_commit_w(empty + (k & 1), lead);
         }
     }
+    }
     if (!ok && lane == 0) report_status(p.status, kStatusTimeout);
     __syncwarp();
     tc_fence_before();
     __syncthreads();
-    if (warp == 8) tmem_dealloc(tmem, 512);
+    if (warp == 12) tmem_dealloc(tmem, 512);
 }
 
 // Segments of a row's chunks, where one CTA for each head and block of columns leaves SMs idle: as many as

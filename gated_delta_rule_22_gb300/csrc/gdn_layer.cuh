@@ -124,7 +124,7 @@ struct ResnormParams {
     const float *scale, *w_post, *w_pre, *stats_in;
     void *r, *y, *dx, *dh, *dz;
     float *stats, *dscale, *dw_post, *dw_pre;
-    float *part;               // backward: [ctas][3][D] partial sums of dscale, dw_post, dw_pre
+    float *part;               // backward: [ctas][2][D] partial sums of what dscale and dw_post are made of, and of dw_pre
     float *part_z;             // backward, gate_rows > 1: [units][D] partial sums of dz before act'(z)
     long long ldx, ldh, ldz;
     int M, D, gate_rows, act, post, pre;

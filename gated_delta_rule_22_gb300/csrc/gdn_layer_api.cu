@@ -238,7 +238,7 @@ int resnorm_plan(const gdn_resnorm_shape *s, gdn::ResnormParams *p) {
     return GDN_OK;
 }
 
-size_t resnorm_part_bytes(const gdn::ResnormParams &p) { return up256((size_t)p.ctas * 3 * p.D * 4); }
+size_t resnorm_part_bytes(const gdn::ResnormParams &p) { return up256((size_t)p.ctas * 2 * p.D * 4); }
 size_t resnorm_ws(const gdn::ResnormParams &p) {
     return resnorm_part_bytes(p) + (p.gate_rows > 1 ? up256((size_t)p.units * p.D * 4) : 0);
 }

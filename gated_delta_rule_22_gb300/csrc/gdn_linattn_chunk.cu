@@ -69,6 +69,11 @@ __device__ __forceinline__ uint4 *piece_at(unsigned char *operand, int r, int pi
     return reinterpret_cast<uint4 *>(operand + (piece >> 3) * kTile + r * 128 + (((piece & 7) ^ (r & 7)) << 4));
 }
 
+// One arrival for what a warp has done
+__device__ __forceinline__ void warp_arrive(uint64_t *bar, int lane) {
+    __syncwarp();
+    if (lane == 0) mbar_arrive(bar);
+}
 // mbar_wait by a whole warp, with one answer
 __device__ __forceinline__ bool all_wait(uint64_t *bar, uint32_t parity) { return __all_sync(kFullMask, mbar_wait(bar, parity)); }
 
@@ -156,7 +161,7 @@ __global__ void __launch_bounds__(kThreads, 1) linattn_chunk_kernel(const __grid
             mbar_init(empty + i, cp.state_only ? 1 : 2);
         }
         for (uint64_t *bar : {p_full, o1_full, o2_full, u_full}) mbar_init(bar, 1);
-        for (uint64_t *bar : {pt_full, o_empty, bt_full, bt_full + 1, z_full, z_full + 1}) mbar_init(bar, 128);
+        for (uint64_t *bar : {pt_full, o_empty, bt_full, bt_full + 1, z_full, z_full + 1}) mbar_init(bar, 4);    // warps
         mbar_init(p_seen, 1 + (Dbp > 64 ? 8 : 4));
         fence_mbar_init();
     }
@@ -229,7 +234,7 @@ __global__ void __launch_bounds__(kThreads, 1) linattn_chunk_kernel(const __grid
             }
             tmem_wait_st();
             tc_fence_before();
-            mbar_arrive(pt_full);
+            warp_arrive(pt_full, lane);
             if (!(ok = all_wait(o2_full, ph) && all_wait(o1_full, ph))) break;
             tc_fence_after();
             const float s = pw[rev ? max(L - 1 - i, 0) : i + 1];
@@ -267,7 +272,7 @@ __global__ void __launch_bounds__(kThreads, 1) linattn_chunk_kernel(const __grid
                 }
             }
             tc_fence_before();
-            mbar_arrive(o_empty);
+            warp_arrive(o_empty, lane);
         }
         // zeros behind the row: this segment's share of the steps
         if (!cp.state_only) {
@@ -283,10 +288,17 @@ __global__ void __launch_bounds__(kThreads, 1) linattn_chunk_kernel(const __grid
         const int work_here = d0 < Dbp ? work : 0;
         const float *init = cp.state_only ? nullptr : w.init;
 #pragma unroll
-        for (int d = 0; d < 64; ++d) {
-            Z[d] = 0.f;
-            if (init != nullptr && row && d0 + d < Db)
-                Z[d] = w.init_t ? init[(head * w.Db + db0 + d0 + d) * w.Dc + dc0 + e] : init[(head * w.Dc + dc0 + e) * w.Db + db0 + d0 + d];
+        for (int d = 0; d < 64; d += 4) {          // (Db is a multiple of 8)
+            float4 z = make_float4(0.f, 0.f, 0.f, 0.f);
+            if (init != nullptr && row && d0 + d < Db) {
+                if (!w.init_t) {
+                    z = *reinterpret_cast<const float4 *>(init + (head * w.Dc + dc0 + e) * w.Db + db0 + d0 + d);
+                } else {
+                    const float *at = init + (head * w.Db + db0 + d0 + d) * w.Dc + dc0 + e;
+                    z = make_float4(at[0], at[w.Dc], at[2 * w.Dc], at[3 * w.Dc]);
+                }
+            }
+            Z[d] = z.x; Z[d + 1] = z.y; Z[d + 2] = z.z; Z[d + 3] = z.w;
         }
         if (!cp.state_only && work_here > 0)       // through the earlier segments
             for (int s = 0; s < seg; ++s) {
@@ -323,7 +335,7 @@ __global__ void __launch_bounds__(kThreads, 1) linattn_chunk_kernel(const __grid
             put_operand();
             ok = clear(0);
             fence_proxy_async();
-            mbar_arrive(z_full + half);
+            warp_arrive(z_full + half, lane);
         }
         for (int k = 0; k < work_here && ok; ++k) {
             const int L = length_of(first + k), j = e, terms = terms_of(first + k);
@@ -338,17 +350,27 @@ __global__ void __launch_bounds__(kThreads, 1) linattn_chunk_kernel(const __grid
                                  w2 = __float2bfloat162_rn(wj - __low2float(w0) - __low2float(w1));
             auto write_terms = [&](auto three) {
                 constexpr bool THREE = decltype(three)::value;
+                constexpr int BATCH = THREE ? 4 : 8;                          // pieces read at once
                 uint32_t t1[32], t2[THREE ? 32 : 1];
 #pragma unroll
-                for (int c = 0; c < 8; ++c) {
-                    uint4 *at = piece_at(bb, j, 8 * half + c);
-                    uint4 raw = *at;
-                    if (j >= L) raw = make_uint4(0u, 0u, 0u, 0u);
-                    const uint32_t in[4] = {raw.x, raw.y, raw.z, raw.w};
-                    uint32_t t0[4];
+                for (int c0 = 0; c0 < 8; c0 += BATCH) {
+                    uint4 raw[BATCH];
 #pragma unroll
-                    for (int q = 0; q < 4; ++q) split_product<THREE>(in[q], w0, w1, w2, t0[q], t1[4 * c + q], t2[THREE ? 4 * c + q : 0]);
-                    *at = make_uint4(t0[0], t0[1], t0[2], t0[3]);
+                    for (int c = 0; c < BATCH; ++c) {
+                        raw[c] = *piece_at(bb, j, 8 * half + c0 + c);
+                        if (j >= L) raw[c] = make_uint4(0u, 0u, 0u, 0u);
+                    }
+#pragma unroll
+                    for (int c = 0; c < BATCH; ++c) {
+                        const uint32_t in[4] = {raw[c].x, raw[c].y, raw[c].z, raw[c].w};
+                        uint32_t t0[4];
+#pragma unroll
+                        for (int q = 0; q < 4; ++q) {
+                            const int at = 4 * (c0 + c) + q;
+                            split_product<THREE>(in[q], w0, w1, w2, t0[q], t1[at], t2[THREE ? at : 0]);
+                        }
+                        *piece_at(bb, j, 8 * half + c0 + c) = make_uint4(t0[0], t0[1], t0[2], t0[3]);
+                    }
                 }
                 if (!cp.state_only && !all_wait(o2_full, ph)) return false;
 #pragma unroll
@@ -360,21 +382,19 @@ __global__ void __launch_bounds__(kThreads, 1) linattn_chunk_kernel(const __grid
             };
             if (!(ok = terms == 3 ? write_terms(std::true_type()) : write_terms(std::false_type()))) break;
             fence_proxy_async();
-            mbar_arrive(bt_full + half);
+            warp_arrive(bt_full + half, lane);
             if (!(ok = all_wait(u_full, ph))) break;
             tc_fence_after();
             const float2 decay = make_float2(pw[L], pw[L]);
+            float u[64];
+            tmem_ld32f(lanes, u);
+            tmem_ld32f(lanes + 32, u + 32);
+            tmem_wait_ld();
 #pragma unroll
-            for (int cb = 0; cb < 2; ++cb) {
-                float u[32];
-                tmem_ld32f(lanes + 32 * cb, u);
-                tmem_wait_ld();
-#pragma unroll
-                for (int r = 0; r < 32; r += 2) {
-                    const float2 z = __ffma2_rn(decay, make_float2(Z[32 * cb + r], Z[32 * cb + r + 1]), make_float2(u[r], u[r + 1]));
-                    Z[32 * cb + r] = z.x;
-                    Z[32 * cb + r + 1] = z.y;
-                }
+            for (int r = 0; r < 64; r += 2) {
+                const float2 z = __ffma2_rn(decay, make_float2(Z[r], Z[r + 1]), make_float2(u[r], u[r + 1]));
+                Z[r] = z.x;
+                Z[r + 1] = z.y;
             }
             tc_fence_before();
             if (k + 1 < work) {
@@ -383,7 +403,7 @@ __global__ void __launch_bounds__(kThreads, 1) linattn_chunk_kernel(const __grid
                     ok = clear(k + 1);
                     fence_proxy_async();
                 }
-                mbar_arrive(z_full + half);
+                warp_arrive(z_full + half, lane);
             }
         }
         if (cp.state_only) {

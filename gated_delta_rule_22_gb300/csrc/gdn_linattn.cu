@@ -172,7 +172,7 @@ __global__ void __launch_bounds__(kWalkThreads) linattn_walk_kernel(const Linatt
         __syncthreads();
         if (it + 1 < tiles) fetch(w.rev ? tile - 1 : tile + 1);
         if (row0 >= Dc) continue;                       // (a warp without rows stages only)
-        for (int k = 0; k < steps; ++k) {
+        auto step = [&](int k) {
             const int i = w.rev ? steps - 1 - k : k;
             const float gs = first ? 1.f : g;
             const float2 g2 = make_float2(gs, gs);
@@ -183,11 +183,12 @@ __global__ void __launch_bounds__(kWalkThreads) linattn_walk_kernel(const Linatt
                 av[m] = *reinterpret_cast<const float2 *>(&sa[i][2 * lane + 64 * m]);
                 bv[m] = *reinterpret_cast<const float2 *>(&sb[i][2 * lane + 64 * m]);
             }
-            float y[kWalkRows];
+            float y[kWalkRows], c[kWalkRows];
+            *reinterpret_cast<float4 *>(c) = *reinterpret_cast<const float4 *>(&sc[i][warp * kWalkRows]);
+            *reinterpret_cast<float4 *>(c + 4) = *reinterpret_cast<const float4 *>(&sc[i][warp * kWalkRows + 4]);
 #pragma unroll
             for (int r = 0; r < kWalkRows; ++r) {
-                const float c = sc[i][warp * kWalkRows + r];
-                const float2 c2 = make_float2(c, c);
+                const float2 c2 = make_float2(c[r], c[r]);
                 float2 acc = make_float2(0.f, 0.f);
 #pragma unroll
                 for (int m = 0; m < E2; ++m) {
@@ -196,10 +197,21 @@ __global__ void __launch_bounds__(kWalkThreads) linattn_walk_kernel(const Linatt
                 }
                 y[r] = acc.x + acc.y;
             }
-            const float sum = transpose_reduce<kWalkRows>(y, lane);    // lane l: row l / 4
-            const int row = row0 + (lane >> 2);
-            if ((lane & 3) == 0 && row < Dc) put(t0 + i, row, sum);
+            return transpose_reduce<kWalkRows>(y, lane);               // lane l: row l / 4
+        };
+        const int row = row0 + (lane >> 2);
+        auto put_step = [&](int k, float sum) {
+            if ((lane & 3) == 0 && row < Dc) put(t0 + (w.rev ? steps - 1 - k : k), row, sum);
+        };
+        int k = 0;
+        for (; k + 4 <= steps; k += 4) {               // the sums of four steps at once
+            float sum[4];
+#pragma unroll
+            for (int u = 0; u < 4; ++u) sum[u] = step(k + u);
+#pragma unroll
+            for (int u = 0; u < 4; ++u) put_step(k + u, sum[u]);
         }
+        for (; k < steps; ++k) put_step(k, step(k));
     }
     for (int i = tid; i < (T_ - n) * kWalkBlock; i += kWalkThreads)    // zeros behind the row
         if (e0 + i % kWalkBlock < Dc) put(n + i / kWalkBlock, e0 + i % kWalkBlock, 0.f);
@@ -217,18 +229,26 @@ __global__ void __launch_bounds__(kWalkThreads) linattn_walk_kernel(const Linatt
 
 // ---- outputs from the sweeps' float32 ones: planes (blocks of Db) and the value heads of a key head, added in
 // ascending order
-template <typename T>
+template <typename T, int V>
 __global__ void __launch_bounds__(kSumThreads) linattn_sum_kernel(const LinattnParams p) {
     const LinattnSum &w = p.sum[blockIdx.y];
     T *out = static_cast<T *>(w.out);
-    const size_t n = (size_t)p.B * p.T * w.heads * w.D;
+    const int pieces = w.D / V, add = w.group * w.planes;
+    const size_t n = (size_t)p.B * p.T * w.heads * pieces;
     for (size_t i = (size_t)blockIdx.x * kSumThreads + threadIdx.x; i < n; i += (size_t)gridDim.x * kSumThreads) {
-        const size_t head = i / w.D, d = i % w.D;       // (batch row, step, head), channel
-        const float *x = w.part + head * w.group * w.D + d;
-        float s = 0.f;
-        for (int r = 0; r < w.group; ++r)
-            for (int q = 0; q < w.planes; ++q) s += x[q * w.plane + (size_t)r * w.D];
-        out[i] = from_f32<T>(s);
+        const size_t head = i / pieces;                 // (batch row, step, head)
+        const float *x = w.part + head * w.group * w.D + (i - head * pieces) * V;
+        float s[V];
+#pragma unroll
+        for (int v = 0; v < V; ++v) s[v] = 0.f;
+#pragma unroll 4
+        for (int r = 0; r < add; ++r) {
+            float e[V];
+            load_vec<float, V>(x + (r % w.planes) * w.plane + (size_t)(r / w.planes) * w.D, e);
+#pragma unroll
+            for (int v = 0; v < V; ++v) s[v] += e[v];
+        }
+        store_vec<T, V>(out + i * V, s);
     }
 }
 
@@ -259,12 +279,16 @@ cudaError_t launch_linattn_step(const LinattnParams &p, int dtype, cudaStream_t 
 template <typename T>
 static cudaError_t launch_sums_t(const LinattnParams &p, cudaStream_t s) {
     size_t n = 0;
+    bool vec = true;
     for (int i = 0; i < p.sums; ++i) {
         const size_t m = (size_t)p.B * p.T * p.sum[i].heads * p.sum[i].D;
         n = m > n ? m : n;
+        vec = vec && p.sum[i].D % 4 == 0;
     }
-    const size_t ctas = (n + kSumThreads - 1) / kSumThreads;
-    linattn_sum_kernel<T><<<dim3((unsigned)(ctas < 8192 ? ctas : 8192), p.sums), kSumThreads, 0, s>>>(p);
+    const size_t ctas = (n / (vec ? 4 : 1) + kSumThreads - 1) / kSumThreads;
+    const dim3 grid((unsigned)(ctas < 152 * 32 ? ctas : 152 * 32), p.sums);
+    if (vec) linattn_sum_kernel<T, 4><<<grid, kSumThreads, 0, s>>>(p);
+    else linattn_sum_kernel<T, 1><<<grid, kSumThreads, 0, s>>>(p);
     return cudaGetLastError();
 }
 

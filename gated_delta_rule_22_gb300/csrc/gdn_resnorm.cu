@@ -20,11 +20,25 @@ namespace gdn {
 
 namespace {
 
-__device__ __forceinline__ float act_rt(int act, float x) {
-    return act == kActSilu ? silu_hw(x) : act == kActGelu ? gelu_f(x) : x;
+__device__ __forceinline__ float2 mul2(float2 a, float2 b) { return __fmul2_rn(a, b); }
+__device__ __forceinline__ float2 fma2(float2 a, float2 b, float2 c) { return __ffma2_rn(a, b, c); }
+__device__ __forceinline__ float2 both(float x) { return make_float2(x, x); }
+
+template <int ACT>
+__device__ __forceinline__ float2 act2(float2 x) {
+    return ACT == kActSilu ? mul2(x, sigmoid2_hw(x)) : ACT == kActGelu ? make_float2(gelu_f(x.x), gelu_f(x.y)) : x;
 }
 __device__ __forceinline__ float dact_rt(int act, float x) {
     return act == kActSilu ? dsilu_hw(x) : act == kActGelu ? dgelu_f(x) : 1.f;
+}
+template <int ACT>
+__device__ __forceinline__ float2 dact2(float2 x) { return make_float2(dact_rt(ACT, x.x), dact_rt(ACT, x.y)); }
+// f<ACT>() for the activation of the call: the test is made once per row, not per element.
+template <typename F>
+__device__ __forceinline__ void with_act(int act, F f) {
+    if (act == kActSilu) f(std::integral_constant<int, kActSilu>());
+    else if (act == kActGelu) f(std::integral_constant<int, kActGelu>());
+    else f(std::integral_constant<int, kActNone>());
 }
 
 // N sums over the LPR lanes of a row: a part of a warp, or a CTA of LPR threads (through shared memory, two
@@ -54,47 +68,53 @@ struct RowSum {
     }
 };
 
-// A row by LPR lanes, lane j holding channels (i LPR + j) V .. + V - 1 for i < IT (D <= LPR V IT); CTAs of
-// at least 128 threads.
+// A row by LPR lanes, lane j holding channels (i LPR + j) V .. + V - 1 for i < IT (D <= LPR V IT), as E / 2
+// pairs for the packed instructions; CTAs of at least 128 threads.
 template <typename T, int V, int LPR, int IT>
 struct RowLane {
-    static constexpr int kThreads = LPR < 128 ? 128 : LPR, kRows = kThreads / LPR, E = V * IT;
+    static constexpr int kThreads = LPR < 128 ? 128 : LPR, kRows = kThreads / LPR, E = V * IT, P = E / 2;
     int j, slot, D;
     __device__ __forceinline__ explicit RowLane(int D_) : j(threadIdx.x % LPR), slot(threadIdx.x / LPR), D(D_) {}
     __device__ __forceinline__ int col(int i) const { return (i * LPR + j) * V; }
     __device__ __forceinline__ bool ok(int i) const { return col(i) < D; }
-    __device__ __forceinline__ void read(const T *t, float (&o)[E]) const {
-#pragma unroll
-        for (int i = 0; i < IT; ++i) {
-            float e[V];
-            unpack<T, V>(ok(i) ? load_raw<T, V>(t + col(i)) : Raw<T, V>(), e);
-#pragma unroll
-            for (int v = 0; v < V; ++v) o[i * V + v] = e[v];
-        }
+    __device__ __forceinline__ static void set(float2 (&o)[P], int e, float x) {
+        if (e % 2) o[e / 2].y = x;
+        else o[e / 2].x = x;
     }
-    __device__ __forceinline__ void store(void *t, size_t at, const float (&x)[E]) const {
+    __device__ __forceinline__ static float get(const float2 (&x)[P], int e) { return e % 2 ? x[e / 2].y : x[e / 2].x; }
+    __device__ __forceinline__ static void place(const Raw<T, V> &raw, int i, float2 (&o)[P]) {
+        float e[V];
+        unpack<T, V>(raw, e);
+#pragma unroll
+        for (int v = 0; v < V; ++v) set(o, i * V + v, e[v]);
+    }
+    __device__ __forceinline__ void read(const T *t, float2 (&o)[P]) const {
+#pragma unroll
+        for (int i = 0; i < IT; ++i) place(ok(i) ? load_raw<T, V>(t + col(i)) : Raw<T, V>(), i, o);
+    }
+    __device__ __forceinline__ void store(T *t, const float2 (&x)[P]) const {
 #pragma unroll
         for (int i = 0; i < IT; ++i) {
             float e[V];
 #pragma unroll
-            for (int v = 0; v < V; ++v) e[v] = x[i * V + v];
-            if (ok(i)) store_vec<T, V>(static_cast<T *>(t) + at + col(i), e);
+            for (int v = 0; v < V; ++v) e[v] = get(x, i * V + v);
+            if (ok(i)) store_vec<T, V>(t + col(i), e);
         }
     }
     // the product of two parameters of the lane's channels, 1 where there are none
-    __device__ __forceinline__ void params(const float *a, const float *b, float (&o)[E]) const {
+    __device__ __forceinline__ void params(const float *a, const float *b, float2 (&o)[P]) const {
 #pragma unroll
         for (int i = 0; i < IT; ++i)
 #pragma unroll
             for (int v = 0; v < V; ++v)
-                o[i * V + v] = (a != nullptr && ok(i) ? a[col(i) + v] : 1.f) * (b != nullptr && ok(i) ? b[col(i) + v] : 1.f);
+                set(o, i * V + v, (a != nullptr && ok(i) ? a[col(i) + v] : 1.f) * (b != nullptr && ok(i) ? b[col(i) + v] : 1.f));
     }
-    __device__ __forceinline__ void put(float *t, const float (&x)[E]) const {
+    __device__ __forceinline__ void put(float *t, const float2 (&x)[P]) const {
 #pragma unroll
         for (int i = 0; i < IT; ++i)
             if (ok(i))
 #pragma unroll
-                for (int v = 0; v < V; ++v) t[col(i) + v] = x[i * V + v];
+                for (int v = 0; v < V; ++v) t[col(i) + v] = get(x, i * V + v);
     }
 };
 
@@ -112,12 +132,12 @@ struct RowRing {
     __device__ __forceinline__ unsigned char *at(int slot, int t, int i) const {
         return base + ((size_t)(slot * N + t) * IT + i) * Lane::kThreads * 16;
     }
-    // starts the copies of a row: its N addresses, null where a tensor is not there (row behind the last: all null)
-    __device__ __forceinline__ void fetch(const Lane &lane, const T *const (&src)[N]) {
+    // starts the copies of a row (in: there is one), tensor t's from src[t], null where it is not there
+    __device__ __forceinline__ void fetch(const Lane &lane, const T *const (&src)[N], bool in) {
         if constexpr (kRing) {
 #pragma unroll
             for (int t = 0; t < N; ++t)
-                if (src[t] != nullptr)
+                if (in && src[t] != nullptr)
 #pragma unroll
                     for (int i = 0; i < IT; ++i)
                         if (lane.ok(i)) cp_async16(at(put, t, i), src[t] + lane.col(i), 16);
@@ -128,19 +148,16 @@ struct RowRing {
     __device__ __forceinline__ void arrive() const {
         if constexpr (kRing) cp_async_wait<kAhead - 1>();
     }
-    // tensor t of the row that arrived, as floats (zeros behind the row's end)
-    __device__ __forceinline__ void read(const Lane &lane, int t, const T *src, float (&o)[Lane::E]) const {
+    // tensor t of the row that arrived, as floats (zeros behind the row's end); without a ring, from src
+    __device__ __forceinline__ void read(const Lane &lane, int t, const T *src, bool in, float2 (&o)[Lane::P]) const {
 #pragma unroll
         for (int i = 0; i < IT; ++i) {
-            float e[V];
             Raw<T, V> raw = Raw<T, V>();
             if (lane.ok(i)) {
                 if constexpr (kRing) raw = *reinterpret_cast<const Raw<T, V> *>(at(take, t, i));
-                else if (src != nullptr) raw = load_raw<T, V>(src + lane.col(i));
+                else if (in) raw = load_raw<T, V>(src + lane.col(i));
             }
-            unpack<T, V>(raw, e);
-#pragma unroll
-            for (int v = 0; v < V; ++v) o[i * V + v] = e[v];
+            Lane::place(raw, i, o);
         }
     }
     // after a run of rows: nothing under way, the next row fetched is the next one read
@@ -158,66 +175,72 @@ __global__ void __launch_bounds__(LPR < 128 ? 128 : LPR) resnorm_fwd_kernel(cons
     using Lane = RowLane<T, V, LPR, IT>;
     using Ring = RowRing<Lane, T, V, IT, 3>;
     extern __shared__ __align__(16) unsigned char smem[];
-    constexpr int E = Lane::E;
+    constexpr int P = Lane::P;
     const Lane at(p.D);
     Ring ring(smem);
     RowSum<LPR, 1> row_sum;
     const int rows = gridDim.x * Lane::kRows;
     const float inv_D = 1.f / p.D;
+    int m = blockIdx.x * Lane::kRows + at.slot;
+    const T *const x0 = static_cast<const T *>(p.x), *const h0 = static_cast<const T *>(p.h), *const z0 = static_cast<const T *>(p.z);
     const T *src[3];
     auto locate = [&](int row) {
-        const bool in = row < p.M;
-        src[0] = in ? static_cast<const T *>(p.x) + (size_t)row * p.ldx : nullptr;
-        src[1] = in ? static_cast<const T *>(p.h) + (size_t)row * p.ldh : nullptr;
-        src[2] = in && p.z != nullptr ? static_cast<const T *>(p.z) + (size_t)(row / p.gate_rows) * p.ldz : nullptr;
+        src[0] = x0 + (size_t)row * p.ldx;
+        src[1] = h0 + (size_t)row * p.ldh;
+        src[2] = z0 == nullptr ? nullptr : z0 + (size_t)(p.gate_rows == 1 ? row : row / p.gate_rows) * p.ldz;
     };
-    int m = blockIdx.x * Lane::kRows + at.slot;
-    for (int i = 0; i < Ring::kAhead - 1; ++i) {
-        locate(m + i * rows);
-        ring.fetch(at, src);
+    int next = m;                                          // the next row to be fetched
+    for (int i = 0; i < Ring::kAhead - 1; ++i, next += rows) {
+        locate(next);
+        ring.fetch(at, src, next < p.M);
     }
-    float k[E], wr[E];
+    float2 k[P], wr[P];
     at.params(p.scale, p.w_post, k);
     at.params(p.w_pre, nullptr, wr);
-    // (all lanes of a warp walk together: a row behind the last is computed from zeros and not stored)
-    for (; m - at.slot < p.M; m += rows) {
+    // (all lanes of a warp walk together: a row behind the last is computed from anything and not stored)
+    for (; m - at.slot < p.M; m += rows, next += rows) {
         const bool live = m < p.M;
-        locate(m + (Ring::kAhead - 1) * rows);
-        ring.fetch(at, src);
+        locate(next);
+        ring.fetch(at, src, next < p.M);
         ring.arrive();
-        locate(m);
-        float x[E], h[E];
-        ring.read(at, 0, src[0], x);
-        ring.read(at, 1, src[1], h);
+        if (!Ring::kRing) locate(m);
+        float2 x[P], h[P];
+        ring.read(at, 0, src[0], live, x);
+        ring.read(at, 1, src[1], live, h);
         float rs = 1.f;
         if (p.post) {
-            float q[1] = {0.f};
+            float2 s = both(0.f);
 #pragma unroll
-            for (int e = 0; e < E; ++e) q[0] = fmaf(h[e], h[e], q[0]);
+            for (int e = 0; e < P; ++e) s = fma2(h[e], h[e], s);
+            float q[1] = {s.x + s.y};
             row_sum(q);
             rs = 1.f / sqrtf(fmaf(q[0], inv_D, p.eps));
         }
-        if (p.z != nullptr) {
-            float z[E];
-            ring.read(at, 2, src[2], z);
 #pragma unroll
-            for (int e = 0; e < E; ++e) x[e] = fmaf(k[e] * act_rt(p.act, z[e]), h[e] * rs, x[e]);
-        } else {
+        for (int e = 0; e < P; ++e) h[e] = mul2(h[e], both(rs));
+        if (z0 != nullptr) {
+            float2 z[P];
+            ring.read(at, 2, src[2], live, z);
+            with_act(p.act, [&](auto act) {
 #pragma unroll
-            for (int e = 0; e < E; ++e) x[e] = fmaf(k[e], h[e] * rs, x[e]);
+                for (int e = 0; e < P; ++e) h[e] = mul2(h[e], act2<decltype(act)::value>(z[e]));
+            });
         }
+#pragma unroll
+        for (int e = 0; e < P; ++e) x[e] = fma2(k[e], h[e], x[e]);
         ring.done();
-        if (live) at.store(p.r, (size_t)m * p.D, x);
+        if (live) at.store(static_cast<T *>(p.r) + (size_t)m * p.D, x);
         float rr = 1.f;
         if (p.pre) {
-            float q[1] = {0.f};
+            float2 s = both(0.f);
 #pragma unroll
-            for (int e = 0; e < E; ++e) q[0] = fmaf(x[e], x[e], q[0]);
+            for (int e = 0; e < P; ++e) s = fma2(x[e], x[e], s);
+            float q[1] = {s.x + s.y};
             row_sum(q);
             rr = 1.f / sqrtf(fmaf(q[0], inv_D, p.eps));
 #pragma unroll
-            for (int e = 0; e < E; ++e) x[e] = x[e] * rr * wr[e];
-            if (live) at.store(p.y, (size_t)m * p.D, x);
+            for (int e = 0; e < P; ++e) x[e] = mul2(mul2(x[e], both(rr)), wr[e]);
+            if (live) at.store(static_cast<T *>(p.y) + (size_t)m * p.D, x);
         }
         if (live && p.stats != nullptr && at.j == 0) *reinterpret_cast<float2 *>(p.stats + 2 * (size_t)m) = make_float2(rs, rr);
     }
@@ -226,130 +249,136 @@ __global__ void __launch_bounds__(LPR < 128 ? 128 : LPR) resnorm_fwd_kernel(cons
 // A CTA takes units of p.unit consecutive rows that share a row of z (gate_rows = 1: any rows), sums Q and dw_pre
 // over all its units into its slice of the partial sums, and the gate's gradient over each.
 template <typename T, int V, int LPR, int IT>
-__global__ void __launch_bounds__(LPR < 128 ? 128 : LPR) resnorm_bwd_kernel(const ResnormParams p) {
+__global__ void __launch_bounds__(LPR < 128 ? 128 : LPR, LPR <= 256 ? 2 : 1) resnorm_bwd_kernel(const ResnormParams p) {
     using Lane = RowLane<T, V, LPR, IT>;
     using Ring = RowRing<Lane, T, V, IT, 5>;
     extern __shared__ __align__(16) unsigned char smem[];
-    constexpr int E = Lane::E, ROWS = Lane::kRows;
+    constexpr int P = Lane::P, ROWS = Lane::kRows;
     const Lane at(p.D);
     Ring ring(smem);
     RowSum<LPR, 3> row_sum;
     const float inv_D = 1.f / p.D;
-    const bool shared_z = p.z != nullptr && p.gate_rows > 1;
-    float k[E], wr[E], Q[E], dwr[E], dzs[E];
+    const T *const z0 = static_cast<const T *>(p.z);
+    const bool shared_z = z0 != nullptr && p.gate_rows > 1;
+    float2 k[P], wr[P], Q[P], dwr[P], dzs[P];
     at.params(p.scale, p.w_post, k);
     at.params(p.w_pre, nullptr, wr);
 #pragma unroll
-    for (int e = 0; e < E; ++e) Q[e] = dwr[e] = 0.f;
+    for (int e = 0; e < P; ++e) Q[e] = dwr[e] = both(0.f);
     // the slots' sums of a CTA, in ascending order
-    auto over_slots = [&](float (&x)[E]) {
+    auto over_slots = [&](float2 (&x)[P]) {
         if constexpr (ROWS > 1) {
-            __shared__ float buf[ROWS][LPR * E];
+            __shared__ float2 buf[ROWS][LPR * P];
             __syncthreads();
 #pragma unroll
-            for (int e = 0; e < E; ++e) buf[at.slot][e * LPR + at.j] = x[e];
+            for (int e = 0; e < P; ++e) buf[at.slot][e * LPR + at.j] = x[e];
             __syncthreads();
             if (at.slot == 0)
                 for (int s = 1; s < ROWS; ++s)
 #pragma unroll
-                    for (int e = 0; e < E; ++e) x[e] += buf[s][e * LPR + at.j];
+                    for (int e = 0; e < P; ++e) x[e] = __fadd2_rn(x[e], buf[s][e * LPR + at.j]);
         }
     };
     const T *src[5];
-    auto locate = [&](int row, bool in) {
-        src[0] = in ? static_cast<const T *>(p.x) + (size_t)row * p.ldx : nullptr;
-        src[1] = in ? static_cast<const T *>(p.h) + (size_t)row * p.ldh : nullptr;
-        src[2] = in && p.pre ? static_cast<const T *>(p.dy) + (size_t)row * p.D : nullptr;
-        src[3] = in && p.dr != nullptr ? static_cast<const T *>(p.dr) + (size_t)row * p.D : nullptr;
-        src[4] = in && p.z != nullptr ? static_cast<const T *>(p.z) + (size_t)(row / p.gate_rows) * p.ldz : nullptr;
+    auto locate = [&](int row) {
+        src[0] = static_cast<const T *>(p.x) + (size_t)row * p.ldx;
+        src[1] = static_cast<const T *>(p.h) + (size_t)row * p.ldh;
+        src[2] = p.dy == nullptr ? nullptr : static_cast<const T *>(p.dy) + (size_t)row * p.D;
+        src[3] = p.dr == nullptr ? nullptr : static_cast<const T *>(p.dr) + (size_t)row * p.D;
+        src[4] = z0 == nullptr ? nullptr : z0 + (size_t)(p.gate_rows == 1 ? row : row / p.gate_rows) * p.ldz;
     };
     for (int unit = blockIdx.x; unit < p.units; unit += p.ctas) {
         const int gate = unit / p.per_gate, span = shared_z ? p.gate_rows : p.M;
         const int first = gate * span + unit % p.per_gate * p.unit;
         const int last = min(first + p.unit, min((gate + 1) * span, p.M));
 #pragma unroll
-        for (int e = 0; e < E; ++e) dzs[e] = 0.f;
-        for (int i = 0; i < Ring::kAhead - 1; ++i) {
-            const int m = first + i * ROWS + at.slot;
-            locate(m, m < last);
-            ring.fetch(at, src);
+        for (int e = 0; e < P; ++e) dzs[e] = both(0.f);
+        int next = first + at.slot;
+        for (int i = 0; i < Ring::kAhead - 1; ++i, next += ROWS) {
+            locate(next);
+            ring.fetch(at, src, next < last);
         }
-        for (int m0 = first; m0 < last; m0 += ROWS) {
-            const int m = m0 + at.slot, ahead = m + (Ring::kAhead - 1) * ROWS;
+        for (int m = first + at.slot; m - at.slot < last; m += ROWS, next += ROWS) {
             const bool live = m < last;
-            locate(ahead, ahead < last);
-            ring.fetch(at, src);
-            const float2 st = live ? *reinterpret_cast<const float2 *>(p.stats_in + 2 * (size_t)m) : make_float2(0.f, 0.f);
+            locate(next);
+            ring.fetch(at, src, next < last);
+            const float2 st = live ? *reinterpret_cast<const float2 *>(p.stats_in + 2 * (size_t)m) : both(0.f);
             ring.arrive();
-            locate(m, live);
-            // rh, hh, dr + rstd_r e, u; and the row's sums (a row behind the last adds nothing: its hh and rh are zeros)
-            float rh[E], hh[E], g[E], u[E], q[3] = {0.f, 0.f, 0.f};
-            ring.read(at, 0, src[0], rh);
-            ring.read(at, 1, src[1], hh);
-            if (p.z != nullptr) {
-                ring.read(at, 4, src[4], u);
-#pragma unroll
-                for (int e = 0; e < E; ++e) u[e] = act_rt(p.act, u[e]);
-            } else {
-#pragma unroll
-                for (int e = 0; e < E; ++e) u[e] = 1.f;
-            }
-#pragma unroll
-            for (int e = 0; e < E; ++e) {
-                hh[e] *= st.x;
-                rh[e] = fmaf(k[e] * u[e], hh[e], rh[e]) * st.y;
-            }
-            if (!live)
-#pragma unroll
-                for (int e = 0; e < E; ++e) hh[e] = rh[e] = u[e] = 0.f;
-            if (p.dr != nullptr) ring.read(at, 3, src[3], g);
+            if (!Ring::kRing) locate(m);
+            // rh, v = u hh, g = dr + rstd_r e, and the row's sums; a row behind the last is one of zeros
+            float2 rh[P], hh[P], g[P], v[P], z[P];
+            ring.read(at, 0, src[0], live, rh);
+            ring.read(at, 1, src[1], live, hh);
+            if (p.dr != nullptr) ring.read(at, 3, src[3], live, g);
             else
 #pragma unroll
-                for (int e = 0; e < E; ++e) g[e] = 0.f;
-            if (p.pre) {
-                float dy[E];
-                ring.read(at, 2, src[2], dy);
+                for (int e = 0; e < P; ++e) g[e] = both(0.f);
+            if (z0 != nullptr) ring.read(at, 4, src[4], live, z);
+            if (!live)
 #pragma unroll
-                for (int e = 0; e < E; ++e) {
-                    if (live) dwr[e] = fmaf(dy[e], rh[e], dwr[e]);
-                    dy[e] *= wr[e];
-                    q[0] = fmaf(dy[e], rh[e], q[0]);
-                    g[e] = fmaf(st.y, dy[e], g[e]);
+                for (int e = 0; e < P; ++e) rh[e] = hh[e] = g[e] = z[e] = both(0.f);
+#pragma unroll
+            for (int e = 0; e < P; ++e) v[e] = hh[e] = mul2(hh[e], both(st.x));
+            if (z0 != nullptr)
+                with_act(p.act, [&](auto act) {
+#pragma unroll
+                    for (int e = 0; e < P; ++e) v[e] = mul2(act2<decltype(act)::value>(z[e]), hh[e]);
+                });
+#pragma unroll
+            for (int e = 0; e < P; ++e) rh[e] = mul2(fma2(k[e], v[e], rh[e]), both(st.y));
+            float2 q0 = both(0.f), q1 = both(0.f), q2 = both(0.f);
+            if (p.pre) {
+                float2 dy[P];
+                ring.read(at, 2, src[2], live, dy);
+#pragma unroll
+                for (int e = 0; e < P; ++e) {
+                    if (ROWS > 1 && !live) dy[e] = both(0.f);
+                    dwr[e] = fma2(dy[e], rh[e], dwr[e]);
+                    dy[e] = mul2(dy[e], wr[e]);
+                    q0 = fma2(dy[e], rh[e], q0);
+                    g[e] = fma2(both(st.y), dy[e], g[e]);
                 }
             }
 #pragma unroll
-            for (int e = 0; e < E; ++e) {
-                const float t = k[e] * u[e] * hh[e];
-                q[1] = fmaf(g[e], t, q[1]);
-                q[2] = fmaf(rh[e], t, q[2]);
+            for (int e = 0; e < P; ++e) {
+                const float2 t = mul2(k[e], v[e]);
+                q1 = fma2(g[e], t, q1);
+                q2 = fma2(rh[e], t, q2);
             }
             ring.done();
+            float q[3] = {q0.x + q0.y, q1.x + q1.y, q2.x + q2.y};
             row_sum(q);
             const float c = p.pre ? st.y * q[0] * inv_D : 0.f, mean = p.post ? fmaf(-c, q[2], q[1]) * inv_D : 0.f;
-            float f[E];
 #pragma unroll
-            for (int e = 0; e < E; ++e) {
-                g[e] = fmaf(-c, rh[e], g[e]);                                    // gr
-                const float gu = g[e] * u[e];
-                if (live) Q[e] = fmaf(gu, hh[e], Q[e]);
-                f[e] = st.x * fmaf(-hh[e], mean, gu * k[e]);
+            for (int e = 0; e < P; ++e) {
+                g[e] = fma2(both(-c), rh[e], g[e]);                              // gr
+                Q[e] = fma2(g[e], v[e], Q[e]);
             }
-            if (live) {
-                at.store(p.dx, (size_t)m * p.D, g);
-                at.store(p.dh, (size_t)m * p.D, f);
-            }
-            if (p.dz != nullptr) {
-                if (shared_z) {
+            if (live) at.store(static_cast<T *>(p.dx) + (size_t)m * p.D, g);
+            float2 f[P];
 #pragma unroll
-                    for (int e = 0; e < E; ++e) dzs[e] = live ? fmaf(g[e] * k[e], hh[e], dzs[e]) : dzs[e];
-                } else if (live) {
-                    float z[E];
-                    at.read(static_cast<const T *>(p.z) + (size_t)m * p.ldz, z);   // (again, from the cache)
-#pragma unroll
-                    for (int e = 0; e < E; ++e) z[e] = g[e] * k[e] * hh[e] * dact_rt(p.act, z[e]);
-                    at.store(p.dz, (size_t)m * p.D, z);
-                }
+            for (int e = 0; e < P; ++e) {
+                const float2 gk = mul2(g[e], k[e]);
+                f[e] = gk;
+                g[e] = mul2(gk, hh[e]);                                          // dz before act'(z)
             }
+            if (z0 != nullptr) {
+                with_act(p.act, [&](auto act) {
+                    constexpr int ACT = decltype(act)::value;
+#pragma unroll
+                    for (int e = 0; e < P; ++e) f[e] = mul2(f[e], act2<ACT>(z[e]));
+                    if (!shared_z && ACT != kActNone)
+#pragma unroll
+                        for (int e = 0; e < P; ++e) g[e] = mul2(g[e], dact2<ACT>(z[e]));
+                });
+                if (shared_z)
+#pragma unroll
+                    for (int e = 0; e < P; ++e) dzs[e] = __fadd2_rn(dzs[e], g[e]);
+                else if (live && p.dz != nullptr) at.store(static_cast<T *>(p.dz) + (size_t)m * p.D, g);
+            }
+#pragma unroll
+            for (int e = 0; e < P; ++e) f[e] = mul2(fma2(both(-mean), hh[e], f[e]), both(st.x));
+            if (live) at.store(static_cast<T *>(p.dh) + (size_t)m * p.D, f);
         }
         ring.restart();
         if (shared_z && p.dz != nullptr) {

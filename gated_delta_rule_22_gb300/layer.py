@@ -575,23 +575,28 @@ def gdn_linattn_bwd(q, k, v, g, dy, S0=None, lens=None, dS_T=None, *, workspace=
 
 # ------------------------------------------------------------------------ norms around a block
 def _resnorm_args(x, h, z, scale, w_post, w_pre, post, pre, act, eps):
-    dev, dt = x.device, x.dtype
-    D = x.shape[-1]
-    rows, gate_rows = x.numel() // max(D, 1), 1
-    if x.numel() > INT_MAX:
+    dev, dt, size = x.device, x.dtype, x.shape
+    D, n = size[-1], x.numel()
+    rows, gate_rows = n // max(D, 1), 1
+    if n > INT_MAX:
         _int_sizes("gdn_resnorm", rows, D)
-    ldx, ldh, ldz = _rows("x", x, x.shape, dt, dev), _rows("h", h, x.shape, dt, dev), 0
+    ldx, ldh, ldz = _rows("x", x, size, dt, dev), _rows("h", h, size, dt, dev), 0
     if z is not None:
         lead = z.dim() - 1
-        if lead < 0 or lead >= x.dim() or z.shape[-1] != D or z.shape[:lead] != x.shape[:lead]:
-            raise ValueError(f"z has shape {tuple(z.shape)}, expected {tuple(x.shape)} or its last dimension behind some of its first ones")
+        if lead < 0 or lead >= x.dim() or z.shape[-1] != D or z.shape[:lead] != size[:lead]:
+            raise ValueError(f"z has shape {tuple(z.shape)}, expected {tuple(size)} or its last dimension behind some of its first ones")
         gate_rows = rows // max(z.numel() // max(D, 1), 1)
         ldz = _rows("z", z, z.shape, dt, dev)
-    for name, w, norm in (("scale", scale, True), ("w_post", w_post, post), ("w_pre", w_pre, pre)):
-        if w is not None:
-            if not norm:
-                raise ValueError(f"{name} is given, but its norm is off")
-            _check(name, w, (D,), _F32, dev)
+    if scale is not None:
+        _check("scale", scale, (D,), _F32, dev)
+    if w_post is not None:
+        if not post:
+            raise ValueError("w_post is given, but its norm is off")
+        _check("w_post", w_post, (D,), _F32, dev)
+    if w_pre is not None:
+        if not pre:
+            raise ValueError("w_pre is given, but its norm is off")
+        _check("w_pre", w_pre, (D,), _F32, dev)
     return GdnResnormShape(rows, D, gate_rows, _act(act), 1 if post else 0, 1 if pre else 0, _type(x), eps, ldx, ldh, ldz)
 
 

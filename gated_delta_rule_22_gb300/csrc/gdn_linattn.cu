@@ -16,9 +16,6 @@ namespace {
 constexpr int kStepThreads = 256;
 constexpr int kStepRowsPerThread = 4;
 
-constexpr int kWalkThreads = 256, kWalkWarps = kWalkThreads / 32;
-constexpr int kWalkRows = 8;                            // state rows of a warp
-constexpr int kWalkBlock = kWalkWarps * kWalkRows;      // state rows of a CTA
 constexpr int kWalkTile = 16;                           // steps staged at once
 
 constexpr int kSumThreads = 256;
@@ -92,14 +89,15 @@ __global__ void __launch_bounds__(kStepThreads) linattn_step_kernel(const Linatt
         }
 }
 
-// ---- step by step. A warp holds kWalkRows rows of the state X [Dc][Db] in registers, lane l the columns
-// 2 l + 64 m and the next (pairs, for the packed instructions); a CTA holds kWalkBlock rows of one sweep,
-// head and batch row and stages kWalkTile steps of a, b and c in shared memory as float32, the next tile's
-// elements in registers meanwhile. A step is two packed instructions and a half per pair of state elements,
-// and nine shuffles for the eight rows' outputs.
-template <typename T, int E2>
-__global__ void __launch_bounds__(kWalkThreads) linattn_walk_kernel(const LinattnParams p, int blocks0, int blocks1) {
+// ---- step by step. A warp holds ROWS rows of the state X [Dc][Db] in registers, lane l the columns
+// 2 l + 64 m and the next (pairs, for the packed instructions); a CTA holds ROWS WARPS rows of one sweep,
+// head and batch row and stages some steps of a, b and c in shared memory as float32, the next tile's
+// elements in registers meanwhile. A step is three packed instructions per pair of state elements; the outputs
+// of four steps are summed over the lanes together, 31 shuffles in five rounds.
+template <typename T, int E2, int WARPS, int ROWS>
+__global__ void __launch_bounds__(32 * WARPS) linattn_walk_kernel(const LinattnParams p, int blocks0, int blocks1) {
     constexpr int W = 64 * E2;                          // staged columns of a and b
+    constexpr int kWalkThreads = 32 * WARPS, kWalkBlock = WARPS * ROWS;     // threads, state rows of a CTA
     constexpr int LA = kWalkTile * W / kWalkThreads, LC = kWalkTile * kWalkBlock / kWalkThreads;
     __shared__ __align__(16) float sa[kWalkTile][W], sb[kWalkTile][W], sc[kWalkTile][kWalkBlock];
     const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
@@ -107,7 +105,7 @@ __global__ void __launch_bounds__(kWalkThreads) linattn_walk_kernel(const Linatt
     const LinattnSweep &w = p.sweep[which];
     const int block = blockIdx.x - (which == 0 ? 0 : which == 1 ? blocks0 : blocks0 + blocks1);
     const int h = blockIdx.y, b = blockIdx.z, hk = h / (p.Hv / p.Hk), T_ = p.T;
-    const int Db = w.Db, Dc = w.Dc, e0 = block * kWalkBlock, row0 = e0 + warp * kWalkRows;
+    const int Db = w.Db, Dc = w.Dc, e0 = block * kWalkBlock, row0 = e0 + warp * ROWS;
     const int n = row_length(p.lens, b, T_);
     const float g = p.g[h];
     const size_t head = (size_t)b * p.Hv + h;
@@ -115,14 +113,14 @@ __global__ void __launch_bounds__(kWalkThreads) linattn_walk_kernel(const Linatt
     const T *b_ = static_cast<const T *>(w.b) + (size_t)b * T_ * w.ldb + (size_t)(w.b_keys ? hk : h) * Db;
     const T *c_ = static_cast<const T *>(w.c) + (size_t)b * T_ * w.ldc + (size_t)(w.c_keys ? hk : h) * Dc + e0;
     // the state
-    float2 s[kWalkRows][E2];
+    float2 s[ROWS][E2];
     auto place = [&](int r, int m, int i) {             // of an element of the state in init and last
         const int row = row0 + r, col = 2 * lane + 64 * m + i;
         return w.init_t ? (head * Db + col) * Dc + row : (head * Dc + row) * Db + col;
     };
     auto inside = [&](int r, int m, int i) { return row0 + r < Dc && 2 * lane + 64 * m + i < Db; };
 #pragma unroll
-    for (int r = 0; r < kWalkRows; ++r)
+    for (int r = 0; r < ROWS; ++r)
 #pragma unroll
         for (int m = 0; m < E2; ++m) {
             s[r][m].x = w.init != nullptr && inside(r, m, 0) ? w.init[place(r, m, 0)] : 0.f;
@@ -172,7 +170,7 @@ __global__ void __launch_bounds__(kWalkThreads) linattn_walk_kernel(const Linatt
         __syncthreads();
         if (it + 1 < tiles) fetch(w.rev ? tile - 1 : tile + 1);
         if (row0 >= Dc) continue;                       // (a warp without rows stages only)
-        auto step = [&](int k) {
+        auto step = [&](int k, float *y) {
             const int i = w.rev ? steps - 1 - k : k;
             const float gs = first ? 1.f : g;
             const float2 g2 = make_float2(gs, gs);
@@ -183,11 +181,11 @@ __global__ void __launch_bounds__(kWalkThreads) linattn_walk_kernel(const Linatt
                 av[m] = *reinterpret_cast<const float2 *>(&sa[i][2 * lane + 64 * m]);
                 bv[m] = *reinterpret_cast<const float2 *>(&sb[i][2 * lane + 64 * m]);
             }
-            float y[kWalkRows], c[kWalkRows];
-            *reinterpret_cast<float4 *>(c) = *reinterpret_cast<const float4 *>(&sc[i][warp * kWalkRows]);
-            *reinterpret_cast<float4 *>(c + 4) = *reinterpret_cast<const float4 *>(&sc[i][warp * kWalkRows + 4]);
+            float c[ROWS];
 #pragma unroll
-            for (int r = 0; r < kWalkRows; ++r) {
+            for (int r = 0; r < ROWS; r += 4) *reinterpret_cast<float4 *>(c + r) = *reinterpret_cast<const float4 *>(&sc[i][warp * ROWS + r]);
+#pragma unroll
+            for (int r = 0; r < ROWS; ++r) {
                 const float2 c2 = make_float2(c[r], c[r]);
                 float2 acc = make_float2(0.f, 0.f);
 #pragma unroll
@@ -197,28 +195,33 @@ __global__ void __launch_bounds__(kWalkThreads) linattn_walk_kernel(const Linatt
                 }
                 y[r] = acc.x + acc.y;
             }
-            return transpose_reduce<kWalkRows>(y, lane);               // lane l: row l / 4
         };
-        const int row = row0 + (lane >> 2);
-        auto put_step = [&](int k, float sum) {
-            if ((lane & 3) == 0 && row < Dc) put(t0 + (w.rev ? steps - 1 - k : k), row, sum);
-        };
-        int k = 0;
-        for (; k + 4 <= steps; k += 4) {               // the sums of four steps at once
-            float sum[4];
+        for (int k = 0; k < steps; k += 4) {           // the sums of four steps are formed together
+            float y[4 * ROWS];
+            if (k + 4 <= steps) {
 #pragma unroll
-            for (int u = 0; u < 4; ++u) sum[u] = step(k + u);
+                for (int u = 0; u < 4; ++u) step(k + u, y + u * ROWS);
+            } else {
 #pragma unroll
-            for (int u = 0; u < 4; ++u) put_step(k + u, sum[u]);
+                for (int u = 0; u < 4; ++u) {
+                    if (k + u < steps) step(k + u, y + u * ROWS);
+                    else
+#pragma unroll
+                        for (int r = 0; r < ROWS; ++r) y[u * ROWS + r] = 0.f;
+                }
+            }
+            const float sum = transpose_reduce<4 * ROWS>(y, lane);
+            constexpr int SHARE = 32 / (4 * ROWS);     // lanes with the same sum
+            const int at = lane / SHARE, ku = k + at / ROWS, row = row0 + at % ROWS;
+            if (lane % SHARE == 0 && ku < steps && row < Dc) put(t0 + (w.rev ? steps - 1 - ku : ku), row, sum);
         }
-        for (; k < steps; ++k) put_step(k, step(k));
     }
     for (int i = tid; i < (T_ - n) * kWalkBlock; i += kWalkThreads)    // zeros behind the row
         if (e0 + i % kWalkBlock < Dc) put(n + i / kWalkBlock, e0 + i % kWalkBlock, 0.f);
     if (w.last != nullptr) {
         const float gl = w.rev && n > 0 ? g : 1.f;
 #pragma unroll
-        for (int r = 0; r < kWalkRows; ++r)
+        for (int r = 0; r < ROWS; ++r)
 #pragma unroll
             for (int m = 0; m < E2; ++m) {
                 if (inside(r, m, 0)) w.last[place(r, m, 0)] = gl * s[r][m].x;
@@ -299,18 +302,25 @@ cudaError_t launch_linattn_sums(const LinattnParams &p, int dtype, cudaStream_t 
     return e;
 }
 
-template <typename T>
-static cudaError_t launch_walk_t(const LinattnParams &p, cudaStream_t s) {
+template <typename T, int WARPS, int ROWS>
+static cudaError_t launch_walk_w(const LinattnParams &p, cudaStream_t s) {
     int blocks[3] = {0, 0, 0}, widest = 1;
     for (int i = 0; i < p.sweeps; ++i) {
-        blocks[i] = (p.sweep[i].Dc + kWalkBlock - 1) / kWalkBlock;
+        blocks[i] = (p.sweep[i].Dc + WARPS * ROWS - 1) / (WARPS * ROWS);
         widest = p.sweep[i].Db > widest ? p.sweep[i].Db : widest;
     }
     const dim3 grid(blocks[0] + blocks[1] + blocks[2], p.Hv, p.B);
-    if (widest <= 64) linattn_walk_kernel<T, 1><<<grid, kWalkThreads, 0, s>>>(p, blocks[0], blocks[1]);
-    else if (widest <= 128) linattn_walk_kernel<T, 2><<<grid, kWalkThreads, 0, s>>>(p, blocks[0], blocks[1]);
-    else linattn_walk_kernel<T, 4><<<grid, kWalkThreads, 0, s>>>(p, blocks[0], blocks[1]);
+    if (widest <= 64) linattn_walk_kernel<T, 1, WARPS, ROWS><<<grid, 32 * WARPS, 0, s>>>(p, blocks[0], blocks[1]);
+    else if (widest <= 128) linattn_walk_kernel<T, 2, WARPS, ROWS><<<grid, 32 * WARPS, 0, s>>>(p, blocks[0], blocks[1]);
+    else linattn_walk_kernel<T, 4, WARPS, ROWS><<<grid, 32 * WARPS, 0, s>>>(p, blocks[0], blocks[1]);
     return cudaGetLastError();
+}
+// Eight warps of eight rows share what is staged; four of four rows where that would leave SMs idle.
+template <typename T>
+static cudaError_t launch_walk_t(const LinattnParams &p, cudaStream_t s) {
+    long long ctas = 0;
+    for (int i = 0; i < p.sweeps; ++i) ctas += (p.sweep[i].Dc + 63) / 64;
+    return ctas * p.Hv * p.B < 152 ? launch_walk_w<T, 4, 4>(p, s) : launch_walk_w<T, 8, 8>(p, s);
 }
 
 cudaError_t launch_linattn_steps(const LinattnParams &p, int dtype, cudaStream_t s) {

@@ -11,19 +11,20 @@
 // A CTA takes one sweep of one (batch row, value head), one block of up to 128 columns of Db and of Dc (the
 // sweep is linear in b's columns and splits over c's; blocks of Db are added in float32 afterwards), and a
 // segment of the chunks. Four products of 128 x 128 x 128 per chunk, their operands as TMA brings them:
-//     P = a b^T        both K-major                  -> tensor memory; its decayed, masked bf16 copy stays there
+//     P = a b^T        both K-major                  -> tensor memory; its decayed, masked bf16 copy P~ takes its place
 //     O1 = P~ c        P~ from tensor memory, c MN-major
 //     O2 = a Z^T       Z as bf16 in shared memory
-//     U = c^T b~       both MN-major; b~_m = g^(L-1-m) b_m as three bf16 terms (24 bits: the state is float32)
-//                      that take the places of b, a and Z, which are read by then; where no state leaves the
-//                      call, two terms (16 bits, beside Z's rounding to 8 for O2)
+//     U = c^T b~       both MN-major; b~_m = g^(L-1-m) b_m takes b's place once P has read it
 // out = O1 + g^(i+1) O2 is formed in float32, and the state is kept in registers, Z' = g^L Z + U, so that the
-// truncating additions of the tensor cores never run over more than a chunk. Rounded to bf16 besides
-// the outputs: P~ and Z as an operand, each a relative 2^-9 of terms of either sign.
+// truncating additions of the tensor cores never run over more than a chunk.
+// Rounded to bf16 besides the outputs: Z as an operand, and either b~ or P~ (the other one has two terms, 16 bits):
+// each a relative 2^-9 of terms of either sign, so that a chunk's own steps add one rounding to that of the
+// output and earlier steps at most two. b~ is the one rounded, since U then needs nothing but b's place and the
+// chain from state to state is short; where the state leaves the call and the chunk still counts in it by
+// 2^-13, b~ has two terms (by 1 / 16: three, 24 bits), which take the places of a and Z once O2 has read them.
 //
-// Warps 0-3 mask P and write outputs; warps 4-11 hold the state (each four one half of its columns, so that
-// the products with one half run under the additions to the other); one warp fetches (two chunks deep), two
-// issue products: P and O1, and O2 and U, so that neither chain waits for the other.
+// Warps 0-7 mask P, warps 8-11 write outputs, warps 12-19 hold the state (each four half of its columns); one warp
+// fetches (two chunks deep), two issue products: P and O1, and O2 and U, so that neither chain waits for the other.
 #include "gdn.h"
 #include "gdn_layer.cuh"
 #include "gdn_umma.cuh"
@@ -35,14 +36,15 @@ namespace gdn {
 namespace {
 
 constexpr int kC = kLinattnChunk;
-constexpr int kThreads = 16 * 32;                  // (the last warp only completes its group)
-// registers of a thread: launched with 128, then dealt out again
-constexpr int kLaunchRegs = 128, kOutRegs = 104, kStateRegs = 160, kIssueRegs = 64;
-static_assert(kOutRegs + 2 * kStateRegs + kIssueRegs <= 4 * kLaunchRegs, "register split exceeds the launch's registers");
+constexpr int kParts = 2, kPart = 128 / kParts;    // the state's columns by two groups of four warps
+constexpr int kOutWarp = 8, kStateWarp = 12, kFetchWarp = kStateWarp + 4 * kParts, kThreads = (kFetchWarp + 4) * 32;
+// registers of a thread: launched with kLaunchRegs, then dealt out again
+constexpr int kLaunchRegs = 80, kMaskRegs = 56, kOutRegs = 64, kStateRegs = 128, kIssueRegs = 48;
+static_assert(2 * kMaskRegs + kOutRegs + kParts * kStateRegs + kIssueRegs <= kThreads / 128 * kLaunchRegs, "register split exceeds the launch's registers");
 constexpr int kTile = 64 * kC * 2;                 // 64 columns of a chunk: 128 rows of 128 bytes
 constexpr int kOperand = 2 * kTile;
 constexpr int kStage = 3 * kOperand;               // a, b, c
-constexpr size_t kSmem = 1024 + 2 * kStage + kOperand + (136 + 32) * 4 + 16 * 8 + 16;
+constexpr size_t kSmem = 1024 + 2 * kStage + kOperand + (32 + 136 + 16) * 4 + 24 * 8 + 16;
 // tensor memory columns
 constexpr int kColP = 0, kColO1 = 128, kColO2 = 256, kColU = 384;
 
@@ -89,6 +91,12 @@ __device__ __forceinline__ void store_piece2(void *p, float a, float b, float c,
     }
 }
 
+// b w for a pair of b, rounded once
+__device__ __forceinline__ uint32_t weigh(uint32_t b, float w) {
+    const float2 x = __fmul2_rn(make_float2(__uint_as_float(b << 16), __uint_as_float(b & 0xffff0000u)), make_float2(w, w));
+    return pack2_bf16(x.x, x.y);
+}
+
 // b w for a pair of b and w = w0 + w1 + w2 as bf16 terms, in packed bf16 arithmetic (in float32 the conversions
 // alone cost as much): t0 = b w0 rounded; the product of two bf16 has 16 bits, so its rest is a bf16 exactly; t1 =
 // that rest + b w1 rounded, some 2^-9 of the product. Three terms: what t1 lost (a two-sum, and the rest of b w1,
@@ -123,13 +131,12 @@ __global__ void __launch_bounds__(kThreads, 1) linattn_chunk_kernel(const __grid
     extern __shared__ unsigned char smem_raw[];
     unsigned char *smem = reinterpret_cast<unsigned char *>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~(uintptr_t)1023);
     unsigned char *zb = smem + 2 * kStage;                                   // the state as an operand [e][d]
-    float *pw = reinterpret_cast<float *>(zb + kOperand);                    // g^0 .. g^128
-    float *pw_back = pw + 136;                                               // g^31 .. g^0
-    uint64_t *full = reinterpret_cast<uint64_t *>(pw_back + 32), *empty = full + 2;
+    float *pw = reinterpret_cast<float *>(zb + kOperand) + 32;               // g^0 .. g^128, zeros for -32 .. -1
+    float *pw_back = pw + 136;                                               // g^15 .. g^0
+    uint64_t *full = reinterpret_cast<uint64_t *>(pw_back + 16), *empty = full + 2;
     uint64_t *p_full = full + 4, *pt_full = full + 5, *o1_full = full + 6, *o2_full = full + 7, *o_empty = full + 8;
-    uint64_t *u_full = full + 9, *bt_full = full + 10, *z_full = full + 12;  // (the last two: one for each half of the columns)
-    uint64_t *p_seen = full + 14;
-    uint32_t *tmem_slot = reinterpret_cast<uint32_t *>(full + 16);
+    uint64_t *u_full = full + 9, *p_seen = full + 10, *bt_full = full + 12, *z_full = bt_full + kParts;  // (the last two: one for each part)
+    uint32_t *tmem_slot = reinterpret_cast<uint32_t *>(full + 24);
     const LinattnParams &p = cp.p;
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
 
@@ -161,114 +168,130 @@ __global__ void __launch_bounds__(kThreads, 1) linattn_chunk_kernel(const __grid
             mbar_init(empty + i, cp.state_only ? 1 : 2);
         }
         for (uint64_t *bar : {p_full, o1_full, o2_full, u_full}) mbar_init(bar, 1);
-        for (uint64_t *bar : {pt_full, o_empty, bt_full, bt_full + 1, z_full, z_full + 1}) mbar_init(bar, 4);    // warps
-        mbar_init(p_seen, 1 + (Dbp > 64 ? 8 : 4));
+        mbar_init(pt_full, 8);                     // (warps)
+        mbar_init(o_empty, 4);
+        for (int i = 0; i < 2 * kParts; ++i) mbar_init(bt_full + i, 4);
+        mbar_init(p_seen, 1 + 4 * ((Dbp + kPart - 1) / kPart));
         fence_mbar_init();
     }
-    if (warp == 12) tmem_alloc(tmem_slot, 512);
+    if (warp == kFetchWarp) tmem_alloc(tmem_slot, 512);
     {
         const float lg = log2f(p.g[h]);
         for (int i = threadIdx.x; i <= kC; i += kThreads) pw[i] = i == 0 ? 1.f : exp2f(i * lg);
-        if (threadIdx.x < 32) pw_back[threadIdx.x] = threadIdx.x == 31 ? 1.f : exp2f((31 - (int)threadIdx.x) * lg);
+        if (threadIdx.x < 32) pw[(int)threadIdx.x - 32] = 0.f;
+        if (threadIdx.x < 16) pw_back[threadIdx.x] = threadIdx.x == 15 ? 1.f : exp2f((15 - (int)threadIdx.x) * lg);
     }
     tc_fence_before();
     __syncthreads();
     tc_fence_after();
     const uint32_t tmem = *tmem_slot;
-    // Terms of b~: where the state leaves the call, the chunks that still count in it by 1 / 16 hold 24 bits.
+    // Terms of b~
     const float lg = log2f(p.g[h]);
     auto terms_of = [&](int i) {
         const int after = rev ? chunk_of(i) * kC : max(n - (chunk_of(i) + 1) * kC, 0);        // steps that follow it in the sweep
-        return w.last != nullptr && (after == 0 || after * lg >= -4.f) ? 3 : 2;
+        const float weight = after == 0 ? 0.f : after * lg;                                  // (its log2)
+        return w.last == nullptr ? 1 : weight >= -4.f ? 3 : weight >= -13.f ? 2 : 1;
     };
     const size_t out_step = (size_t)p.Hv * w.Dc;
     const size_t out0 = (size_t)(db0 / 128) * p.B * p.T * out_step + (size_t)b * p.T * out_step + (size_t)h * w.Dc + dc0;
     bool ok = true;
 
-    if (warp < 4) {                                // ---- decay and mask P, write the outputs
-        regs_dec<kOutRegs>();
-        const bool wide = ((uintptr_t)w.out & 31) == 0 && w.Dc % 16 == 0;
-        const uint32_t lanes = tmem + ((uint32_t)warp << 21);
-        const int i = threadIdx.x;                 // this thread's step of the chunk
+    if (warp < kOutWarp) {                         // ---- decay and mask P, columns 64 (warp / 4) and on
+        regs_dec<kMaskRegs>();
+        const int part = warp >> 2, i = threadIdx.x & 127;                  // this thread's step of the chunk
+        const uint32_t mine = tmem + ((uint32_t)(warp & 3) << 21) + kColP + 64 * part;
         for (int k = 0; k < work && !cp.state_only; ++k) {
-            const int L = length_of(first + k), t0 = chunk_of(first + k) * kC;
-            const uint32_t ph = k & 1;
-            if (!(ok = all_wait(p_full, ph))) break;
+            const int L = length_of(first + k);
+            const bool two = terms_of(first + k) == 1;
+            if (!(ok = all_wait(p_full, k & 1))) break;
             tc_fence_after();
 #pragma unroll 1
-            for (int cb = 0; cb < 4; ++cb) {
-                float v[32];
-                if (rev ? cb >= warp : cb <= warp) {
-                    tmem_ld32f(lanes + kColP + 32 * cb, v);
+            for (int cb = 0; cb < 4; ++cb) {       // 16 columns, from m0
+                const int m0 = 64 * part + 16 * cb, near = (warp & 3) * 32;      // (rows near .. near + 31)
+                float v[16];
+                if (rev ? m0 + 15 >= near : m0 <= near + 31) {
+                    tmem_ld16f(mine + 16 * cb, v);
                     tmem_wait_ld();
-                    if (cb == warp) {
-#pragma unroll
-                        for (int r = 0; r < 32; ++r) {
-                            const int e = rev ? r - lane : lane - r;
-                            const float d = pw[max(e, 0)];
-                            v[r] = e >= 0 && (!rev || 32 * cb + r < L) ? v[r] * d : 0.f;
-                        }
-                    } else {
-                        const float f = pw[rev ? 32 * cb - i : i - 32 * cb - 31];
+                    if (rev ? m0 >= near + 32 : m0 + 16 <= near) {          // g^|i-m| as a product of two powers
+                        const float f = pw[rev ? m0 - i : i - m0 - 15];
                         const float4 *d4 = reinterpret_cast<const float4 *>(rev ? pw : pw_back);
 #pragma unroll
-                        for (int r = 0; r < 32; r += 4) {
+                        for (int r = 0; r < 16; r += 4) {
                             const float4 d = d4[r / 4];
                             float2 x = __fmul2_rn(make_float2(v[r], v[r + 1]), __fmul2_rn(make_float2(d.x, d.y), make_float2(f, f)));
                             v[r] = x.x; v[r + 1] = x.y;
                             x = __fmul2_rn(make_float2(v[r + 2], v[r + 3]), __fmul2_rn(make_float2(d.z, d.w), make_float2(f, f)));
                             v[r + 2] = x.x; v[r + 3] = x.y;
                         }
-                        if (rev && L < kC)
+                    } else {
+                        const int e0 = rev ? m0 - i : i - m0;
 #pragma unroll
-                            for (int r = 0; r < 32; ++r) v[r] = 32 * cb + r < L ? v[r] : 0.f;
+                        for (int r = 0; r < 16; ++r) {
+                            v[r] *= pw[rev ? e0 + r : e0 - r];      // (0 where negative)
+                        }
                     }
+                    if (L < kC)                    // (what lies behind the row may be anything)
+#pragma unroll
+                        for (int r = 0; r < 16; ++r) v[r] = m0 + r < L ? v[r] : 0.f;
                 } else {
 #pragma unroll
-                    for (int r = 0; r < 32; ++r) v[r] = 0.f;
+                    for (int r = 0; r < 16; ++r) v[r] = 0.f;
                 }
-                float packed[16];
+                uint32_t hi[8];                    // its terms take its place: no warp waits for another
 #pragma unroll
-                for (int r = 0; r < 16; ++r) packed[r] = __uint_as_float(pack2_bf16(v[2 * r], v[2 * r + 1]));
-                tmem_st16f(lanes + kColP + 16 * cb, packed);
+                for (int r = 0; r < 8; ++r) hi[r] = pack2_bf16(v[2 * r], v[2 * r + 1]);
+                tmem_st8(mine + 16 * cb, hi);
+                if (two) {
+                    uint32_t lo[8];
+#pragma unroll
+                    for (int r = 0; r < 8; ++r) {
+                        const float2 x = __ffma2_rn(make_float2(__uint_as_float(hi[r] << 16), __uint_as_float(hi[r] & 0xffff0000u)), make_float2(-1.f, -1.f),
+                                                    make_float2(v[2 * r], v[2 * r + 1]));
+                        lo[r] = pack2_bf16(x.x, x.y);
+                    }
+                    tmem_st8(mine + 16 * cb + 8, lo);
+                }
             }
             tmem_wait_st();
             tc_fence_before();
             warp_arrive(pt_full, lane);
+        }
+    } else if (warp < kStateWarp) {                // ---- the outputs
+        regs_dec<kOutRegs>();
+        const bool wide = ((uintptr_t)w.out & 31) == 0 && w.Dc % 16 == 0;
+        const uint32_t lanes = tmem + ((uint32_t)(warp & 3) << 21);
+        const int i = threadIdx.x & 127;           // this thread's step of the chunk
+        for (int k = 0; k < work && !cp.state_only; ++k) {
+            const int L = length_of(first + k), t0 = chunk_of(first + k) * kC;
+            const uint32_t ph = k & 1;
             if (!(ok = all_wait(o2_full, ph) && all_wait(o1_full, ph))) break;
             tc_fence_after();
             const float s = pw[rev ? max(L - 1 - i, 0) : i + 1];
             const size_t at = out0 + (size_t)(t0 + i) * out_step;
 #pragma unroll 1
-            for (int cb = 0; 32 * cb < Dc; ++cb) {
-                float o1[32], o2[32];
-                tmem_ld32f(lanes + kColO1 + 32 * cb, o1);
-                tmem_ld32f(lanes + kColO2 + 32 * cb, o2);
+            for (int c = 0; c < Dc; c += 16) {
+                float o1[16], o2[16];
+                tmem_ld16f(lanes + kColO1 + c, o1);
+                tmem_ld16f(lanes + kColO2 + c, o2);
                 tmem_wait_ld();
 #pragma unroll
-                for (int r = 0; r < 32; r += 2) {
+                for (int r = 0; r < 16; r += 2) {
                     const float2 x = __ffma2_rn(make_float2(s, s), make_float2(o2[r], o2[r + 1]), make_float2(o1[r], o1[r + 1]));
                     o1[r] = x.x;
                     o1[r + 1] = x.y;
                 }
                 if (i >= L) continue;
                 if (w.sums) {
-                    float *out = static_cast<float *>(w.out) + at + 32 * cb;
-#pragma unroll
-                    for (int r = 0; r < 32; r += 8)
-                        if (32 * cb + r < Dc) store_piece2(out + r, o1[r], o1[r + 1], o1[r + 2], o1[r + 3], o1[r + 4], o1[r + 5], o1[r + 6], o1[r + 7], wide);
+                    float *out = static_cast<float *>(w.out) + at + c;
+                    store_piece2(out, o1[0], o1[1], o1[2], o1[3], o1[4], o1[5], o1[6], o1[7], wide);
+                    if (c + 8 < Dc) store_piece2(out + 8, o1[8], o1[9], o1[10], o1[11], o1[12], o1[13], o1[14], o1[15], wide);
                 } else {
-                    __nv_bfloat16 *out = static_cast<__nv_bfloat16 *>(w.out) + at + 32 * cb;
-                    float y[16];
+                    __nv_bfloat16 *out = static_cast<__nv_bfloat16 *>(w.out) + at + c;
+                    float y[8];
 #pragma unroll
-                    for (int r = 0; r < 16; ++r) y[r] = __uint_as_float(pack2_bf16(o1[2 * r], o1[2 * r + 1]));
-#pragma unroll
-                    for (int r = 0; r < 16; r += 8) {
-                        if (32 * cb + 2 * r + 8 < Dc)
-                            store_piece2(out + 2 * r, y[r], y[r + 1], y[r + 2], y[r + 3], y[r + 4], y[r + 5], y[r + 6], y[r + 7], wide);
-                        else if (32 * cb + 2 * r < Dc)
-                            *reinterpret_cast<float4 *>(out + 2 * r) = make_float4(y[r], y[r + 1], y[r + 2], y[r + 3]);
-                    }
+                    for (int r = 0; r < 8; ++r) y[r] = __uint_as_float(pack2_bf16(o1[2 * r], o1[2 * r + 1]));
+                    if (c + 8 < Dc) store_piece2(out, y[0], y[1], y[2], y[3], y[4], y[5], y[6], y[7], wide);
+                    else *reinterpret_cast<float4 *>(out) = make_float4(y[0], y[1], y[2], y[3]);
                 }
             }
             tc_fence_before();
@@ -279,16 +302,16 @@ __global__ void __launch_bounds__(kThreads, 1) linattn_chunk_kernel(const __grid
             const int from = max(n, seg * p.seg_chunks * kC), to = seg == p.segs - 1 ? p.T : min(p.T, (seg + 1) * p.seg_chunks * kC);
             for (int t = from + i; t < to; t += 128) write_zeros(w, out0 + (size_t)t * out_step, Dc);
         }
-    } else if (warp < 12) {                        // ---- the state: a thread holds half of row e
+    } else if (warp < kFetchWarp) {                // ---- the state: a thread holds a part of row e
         regs_inc<kStateRegs>();
-        const int e = threadIdx.x & 127, half = (warp - 4) >> 2, d0 = 64 * half;
+        const int e = threadIdx.x & 127, part = (warp - kStateWarp) >> 2, d0 = kPart * part;
         const uint32_t lanes = tmem + ((uint32_t)(warp & 3) << 21) + kColU + d0;
-        float Z[64];
+        float Z[kPart];
         const bool row = e < Dc;
         const int work_here = d0 < Dbp ? work : 0;
         const float *init = cp.state_only ? nullptr : w.init;
 #pragma unroll
-        for (int d = 0; d < 64; d += 4) {          // (Db is a multiple of 8)
+        for (int d = 0; d < kPart; d += 4) {       // (Db is a multiple of 8)
             float4 z = make_float4(0.f, 0.f, 0.f, 0.f);
             if (init != nullptr && row && d0 + d < Db) {
                 if (!w.init_t) {
@@ -305,9 +328,9 @@ __global__ void __launch_bounds__(kThreads, 1) linattn_chunk_kernel(const __grid
                 const int lo = s * p.seg_chunks, hi = lo + p.seg_chunks;      // whole segments, but for the row's end
                 const int steps = rev ? min(n, (chunks - lo) * kC) - (chunks - hi) * kC : p.seg_chunks * kC;
                 const float decay = exp2f(steps * log2f(p.g[h]));
-                const float4 *E = reinterpret_cast<const float4 *>(p.seg_state) + (size_t)(unit + s) * (kC * 32) + half * (kC * 16);
+                const float4 *E = reinterpret_cast<const float4 *>(p.seg_state) + (size_t)(unit + s) * (kC * 32) + part * (kC * kPart / 4);
 #pragma unroll
-                for (int d = 0; d < 16; ++d) {
+                for (int d = 0; d < kPart / 4; ++d) {
                     const float4 u = E[d * 128 + e];
                     Z[4 * d] = fmaf(decay, Z[4 * d], u.x);
                     Z[4 * d + 1] = fmaf(decay, Z[4 * d + 1], u.y);
@@ -317,15 +340,15 @@ __global__ void __launch_bounds__(kThreads, 1) linattn_chunk_kernel(const __grid
             }
         auto put_operand = [&]() {
 #pragma unroll
-            for (int c = 0; c < 8; ++c)
-                *piece_at(zb, e, 8 * half + c) = make_uint4(pack2_bf16(Z[8 * c], Z[8 * c + 1]), pack2_bf16(Z[8 * c + 2], Z[8 * c + 3]),
+            for (int c = 0; c < kPart / 8; ++c)
+                *piece_at(zb, e, kPart / 8 * part + c) = make_uint4(pack2_bf16(Z[8 * c], Z[8 * c + 1]), pack2_bf16(Z[8 * c + 2], Z[8 * c + 3]),
                                                             pack2_bf16(Z[8 * c + 4], Z[8 * c + 5]), pack2_bf16(Z[8 * c + 6], Z[8 * c + 7]));
         };
         // Steps behind the row in the k-th chunk, where they are not beyond T (which reads as zeros): c may hold
         // anything there, and 0 x NaN is NaN.
         auto clear = [&](int k) {
             const int L = length_of(first + k);
-            if (!masked || L == kC || half != 0) return true;
+            if (!masked || L == kC || part != 0) return true;
             if (!all_wait(full + (k & 1), k >> 1 & 1)) return false;
             if (e >= L)
                 for (int c = 0; c < (Dc > 64 ? 16 : 8); ++c) *piece_at(smem + (k & 1) * kStage + 2 * kOperand, e, c) = make_uint4(0u, 0u, 0u, 0u);
@@ -335,7 +358,7 @@ __global__ void __launch_bounds__(kThreads, 1) linattn_chunk_kernel(const __grid
             put_operand();
             ok = clear(0);
             fence_proxy_async();
-            warp_arrive(z_full + half, lane);
+            warp_arrive(z_full + part, lane);
         }
         for (int k = 0; k < work_here && ok; ++k) {
             const int L = length_of(first + k), j = e, terms = terms_of(first + k);
@@ -348,78 +371,92 @@ __global__ void __launch_bounds__(kThreads, 1) linattn_chunk_kernel(const __grid
             const float wj = pw[j < L ? (rev ? j + 1 : L - 1 - j) : 0];
             const bf16x2 w0 = __float2bfloat162_rn(wj), w1 = __float2bfloat162_rn(wj - __low2float(w0)),
                                  w2 = __float2bfloat162_rn(wj - __low2float(w0) - __low2float(w1));
-            auto write_terms = [&](auto three) {
-                constexpr bool THREE = decltype(three)::value;
-                constexpr int BATCH = THREE ? 4 : 8;                          // pieces read at once
-                uint32_t t1[32], t2[THREE ? 32 : 1];
+            // (three terms: the second half of the pieces, whose terms the registers do not hold, behind that wait)
+            auto write_terms = [&](auto terms_) {
+                constexpr int TERMS = decltype(terms_)::value;
+                constexpr int N = kPart / 8, BATCH = 4, HELD = TERMS == 3 ? N / 2 : N;     // pieces, those read and those held at once
+                for (int h = 0; h < N; h += HELD) {
+                    const int first_piece = N * part + h;
+                    uint32_t t1[TERMS > 1 ? 4 * HELD : 1], t2[TERMS > 2 ? 4 * HELD : 1];
 #pragma unroll
-                for (int c0 = 0; c0 < 8; c0 += BATCH) {
-                    uint4 raw[BATCH];
+                    for (int c0 = 0; c0 < HELD; c0 += BATCH) {
+                        uint4 raw[BATCH];
 #pragma unroll
-                    for (int c = 0; c < BATCH; ++c) {
-                        raw[c] = *piece_at(bb, j, 8 * half + c0 + c);
-                        if (j >= L) raw[c] = make_uint4(0u, 0u, 0u, 0u);
-                    }
-#pragma unroll
-                    for (int c = 0; c < BATCH; ++c) {
-                        const uint32_t in[4] = {raw[c].x, raw[c].y, raw[c].z, raw[c].w};
-                        uint32_t t0[4];
-#pragma unroll
-                        for (int q = 0; q < 4; ++q) {
-                            const int at = 4 * (c0 + c) + q;
-                            split_product<THREE>(in[q], w0, w1, w2, t0[q], t1[at], t2[THREE ? at : 0]);
+                        for (int c = 0; c < BATCH; ++c) {
+                            raw[c] = *piece_at(bb, j, first_piece + c0 + c);
+                            if (j >= L) raw[c] = make_uint4(0u, 0u, 0u, 0u);
                         }
-                        *piece_at(bb, j, 8 * half + c0 + c) = make_uint4(t0[0], t0[1], t0[2], t0[3]);
-                    }
-                }
-                if (!cp.state_only && !all_wait(o2_full, ph)) return false;
 #pragma unroll
-                for (int c = 0; c < 8; ++c) {
-                    *piece_at(a, j, 8 * half + c) = make_uint4(t1[4 * c], t1[4 * c + 1], t1[4 * c + 2], t1[4 * c + 3]);
-                    if constexpr (THREE) *piece_at(zb, j, 8 * half + c) = make_uint4(t2[4 * c], t2[4 * c + 1], t2[4 * c + 2], t2[4 * c + 3]);
+                        for (int c = 0; c < BATCH; ++c) {
+                            const uint32_t in[4] = {raw[c].x, raw[c].y, raw[c].z, raw[c].w};
+                            uint32_t t0[4];
+#pragma unroll
+                            for (int q = 0; q < 4; ++q) {
+                                const int at = 4 * (c0 + c) + q;
+                                if constexpr (TERMS == 1) t0[q] = weigh(in[q], wj);
+                                else split_product<TERMS == 3>(in[q], w0, w1, w2, t0[q], t1[at], t2[TERMS == 3 ? at : 0]);
+                            }
+                            *piece_at(bb, j, first_piece + c0 + c) = make_uint4(t0[0], t0[1], t0[2], t0[3]);
+                        }
+                    }
+                    if constexpr (TERMS > 1) {
+                        if (h == 0 && !cp.state_only && !all_wait(o2_full, ph)) return false;
+#pragma unroll
+                        for (int c = 0; c < HELD; ++c) {
+                            *piece_at(a, j, first_piece + c) = make_uint4(t1[4 * c], t1[4 * c + 1], t1[4 * c + 2], t1[4 * c + 3]);
+                            if constexpr (TERMS > 2) *piece_at(zb, j, first_piece + c) = make_uint4(t2[4 * c], t2[4 * c + 1], t2[4 * c + 2], t2[4 * c + 3]);
+                        }
+                    }
                 }
                 return true;
             };
-            if (!(ok = terms == 3 ? write_terms(std::true_type()) : write_terms(std::false_type()))) break;
+            ok = terms == 1 ? write_terms(std::integral_constant<int, 1>()) :
+                 terms == 2 ? write_terms(std::integral_constant<int, 2>()) : write_terms(std::integral_constant<int, 3>());
+            if (!ok) break;
             fence_proxy_async();
-            warp_arrive(bt_full + half, lane);
+            warp_arrive(bt_full + part, lane);
             if (!(ok = all_wait(u_full, ph))) break;
             tc_fence_after();
             const float2 decay = make_float2(pw[L], pw[L]);
-            float u[64];
-            tmem_ld32f(lanes, u);
-            tmem_ld32f(lanes + 32, u + 32);
-            tmem_wait_ld();
 #pragma unroll
-            for (int r = 0; r < 64; r += 2) {
-                const float2 z = __ffma2_rn(decay, make_float2(Z[r], Z[r + 1]), make_float2(u[r], u[r + 1]));
-                Z[r] = z.x;
-                Z[r + 1] = z.y;
+            for (int c = 0; c < kPart; c += 32) {
+                float u[32];
+                tmem_ld32f(lanes + c, u);
+                tmem_wait_ld();
+#pragma unroll
+                for (int r = 0; r < 32; r += 2) {
+                    const float2 z = __ffma2_rn(decay, make_float2(Z[c + r], Z[c + r + 1]), make_float2(u[r], u[r + 1]));
+                    Z[c + r] = z.x;
+                    Z[c + r + 1] = z.y;
+                }
             }
             tc_fence_before();
             if (k + 1 < work) {
                 if (!cp.state_only) {
+                    if (terms == 1 && !(ok = all_wait(o2_full, ph))) break;    // (the last state has been read)
                     put_operand();
                     ok = clear(k + 1);
                     fence_proxy_async();
                 }
-                warp_arrive(z_full + half, lane);
+                warp_arrive(z_full + part, lane);
             }
         }
         if (cp.state_only) {
-            float4 *E = reinterpret_cast<float4 *>(p.seg_state) + (size_t)(unit + seg) * (kC * 32) + half * (kC * 16);
+            float4 *E = reinterpret_cast<float4 *>(p.seg_state) + (size_t)(unit + seg) * (kC * 32) + part * (kC * kPart / 4);
             if (work > 0)
 #pragma unroll
-                for (int d = 0; d < 16; ++d) E[d * 128 + e] = make_float4(Z[4 * d], Z[4 * d + 1], Z[4 * d + 2], Z[4 * d + 3]);
+                for (int d = 0; d < kPart / 4; ++d) E[d * 128 + e] = make_float4(Z[4 * d], Z[4 * d + 1], Z[4 * d + 2], Z[4 * d + 3]);
         } else if (w.last != nullptr && row && seg == (chunks > 0 ? (chunks - 1) / p.seg_chunks : 0)) {
+            const bool wide = ((uintptr_t)w.last & 31) == 0;                 // (Db is a multiple of 8)
 #pragma unroll
-            for (int d = 0; d < 64; d += 4)
-                if (d0 + d < Db)                   // (Db is a multiple of 8)
-                    *reinterpret_cast<float4 *>(w.last + (head * w.Dc + dc0 + e) * w.Db + db0 + d0 + d) = make_float4(Z[d], Z[d + 1], Z[d + 2], Z[d + 3]);
+            for (int d = 0; d < kPart; d += 8)
+                if (d0 + d < Db)
+                    store_piece2(w.last + (head * w.Dc + dc0 + e) * w.Db + db0 + d0 + d, Z[d], Z[d + 1], Z[d + 2], Z[d + 3], Z[d + 4], Z[d + 5], Z[d + 6],
+                                 Z[d + 7], wide);
         }
     } else {
     regs_dec<kIssueRegs>();
-    if (warp == 12) {                              // ---- fetch a, b and c
+    if (warp == kFetchWarp) {                      // ---- fetch a, b and c
         if (lane == 0) {
             const int nb = Db > 64 ? 2 : 1, nd = Dc > 64 ? 2 : 1;
             const unsigned bytes = ((cp.state_only ? 1 : 2) * nb + nd) * kTile;
@@ -440,7 +477,7 @@ __global__ void __launch_bounds__(kThreads, 1) linattn_chunk_kernel(const __grid
             for (int i = max(k - 2, 0); i < k; ++i) mbar_wait(full + (i & 1), i >> 1 & 1);     // no copy outlives the CTA
         }
         __syncwarp();
-    } else if (warp == 13) {                       // ---- issue P and O1
+    } else if (warp == kFetchWarp + 1) {           // ---- issue P and O1
         if (!cp.state_only) {
             const uint32_t lead = elect_one_sync();
             const uint32_t idesc_p = umma_idesc(1, 128, 128), idesc_o = umma_idesc_t(1, 128, Dcp, false, true);
@@ -459,40 +496,26 @@ __global__ void __launch_bounds__(kThreads, 1) linattn_chunk_kernel(const __grid
                      (!(masked && length_of(first + k) < kC) || all_wait(o2_full, ph));           // (c is cleared by then)
                 if (!ok) break;
                 tc_fence_after();
-                uint64_t cd = desc_mn(c);
+                const bool two = terms_of(first + k) == 1;
+                for (int term = two ? 1 : 0; term >= 0; --term) {            // smallest first
+                    uint64_t cd = desc_mn(c);
 #pragma unroll
-                for (int q = 0; q < kC / 16; ++q, cd += 2048 >> 4) umma_bf16_tw(tmem + kColO1, tmem + kColP + 8 * q, cd, idesc_o, q > 0, lead);
+                    for (int q = 0; q < kC / 16; ++q, cd += 2048 >> 4)
+                        umma_bf16_tw(tmem + kColO1, tmem + kColP + 16 * q + 8 * term, cd, idesc_o, (two && term == 0) || q > 0, lead);
+                }
                 umma_commit_w(o1_full, lead);
                 umma_commit_w(empty + (k & 1), lead);
             }
         }
-    } else if (warp == 14) {                       // ---- issue O2 and U
+    } else if (warp == kFetchWarp + 2) {           // ---- issue O2 and U
         const uint32_t lead = elect_one_sync();
         const uint32_t idesc_o = umma_idesc(1, 128, Dcp), idesc_u = umma_idesc_t(1, 128, Dbp, true, true);
-        const int halves = Dbp > 64 ? 2 : 1;
-        for (int k = 0; k < work; ++k) {
-            const uint32_t ph = k & 1;
+        const int parts = (Dbp + kPart - 1) / kPart;
+        // (z_full: the state's operand is written, and the last U read)
+        auto issue_u = [&](int k, int terms) {
             const uint32_t a = smem_addr(smem) + (k & 1) * kStage, bb = a + kOperand, c = bb + kOperand, z = smem_addr(zb);
-            const int terms = terms_of(first + k);
-            if (!(ok = all_wait(full + (k & 1), k >> 1 & 1))) break;
-            if (!cp.state_only) {
-                if (!(ok = all_wait(p_full, ph))) break;
-                if (lane == 0) mbar_arrive(p_seen);
-                if (!(ok = (k == 0 || all_wait(o_empty, ph ^ 1)))) break;
-                for (int half = 0; half < halves && ok; ++half) {            // half of the state's columns at a time
-                    if (!(ok = all_wait(z_full + half, ph))) break;
-                    tc_fence_after();
-                    for (int q = 0; q < 4 && 64 * half + 16 * q < Db; ++q) {
-                        const uint32_t off = half * kTile + q * 32;
-                        umma_bf16_w(tmem + kColO2, desc_k(a + off), desc_k(z + off), idesc_o, half + q > 0, lead);
-                    }
-                }
-                if (!ok) break;
-                umma_commit_w(o2_full, lead);
-            }
-            for (int half = 0; half < halves && ok; ++half)
-                ok = all_wait(bt_full + half, ph) && !(cp.state_only && k > 0 && !all_wait(z_full + half, ph ^ 1));
-            if (!ok) break;
+            for (int part = 0; part < parts; ++part)
+                if (!all_wait(bt_full + part, k & 1) || (cp.state_only && k > 0 && !all_wait(z_full + part, (k & 1) ^ 1))) return false;
             tc_fence_after();
             for (int term = terms - 1; term >= 0; --term) {                  // smallest first
                 uint64_t cd = desc_mn(c), bd = desc_mn(term == 0 ? bb : term == 1 ? a : z);
@@ -501,6 +524,28 @@ __global__ void __launch_bounds__(kThreads, 1) linattn_chunk_kernel(const __grid
                     umma_bf16_w(tmem + kColU, cd, bd, idesc_u, term < terms - 1 || q > 0, lead);
             }
             umma_commit_w(u_full, lead);
+            return true;
+        };
+        for (int k = 0; k < work; ++k) {
+            const uint32_t ph = k & 1;
+            const uint32_t a = smem_addr(smem) + (k & 1) * kStage, z = smem_addr(zb);
+            const int terms = terms_of(first + k);
+            if (!(ok = all_wait(full + (k & 1), k >> 1 & 1))) break;
+            if (!cp.state_only) {
+                if (!(ok = all_wait(p_full, ph))) break;
+                if (lane == 0) mbar_arrive(p_seen);
+                for (int part = 0; part < parts && ok; ++part) ok = all_wait(z_full + part, ph);
+                // the next state's product first, where it needs no place of a or Z
+                if (ok && terms == 1) ok = issue_u(k, terms);
+                if (!ok || !(ok = (k == 0 || all_wait(o_empty, ph ^ 1)))) break;
+                tc_fence_after();
+                for (int q = 0; 16 * q < Db; ++q) {
+                    const uint32_t off = (q >> 2) * kTile + (q & 3) * 32;
+                    umma_bf16_w(tmem + kColO2, desc_k(a + off), desc_k(z + off), idesc_o, q > 0, lead);
+                }
+                umma_commit_w(o2_full, lead);
+            }
+            if ((cp.state_only || terms > 1) && !(ok = issue_u(k, terms))) break;
             umma_commit_w(empty + (k & 1), lead);
         }
     }
@@ -509,7 +554,7 @@ __global__ void __launch_bounds__(kThreads, 1) linattn_chunk_kernel(const __grid
     __syncwarp();
     tc_fence_before();
     __syncthreads();
-    if (warp == 12) tmem_dealloc(tmem, 512);
+    if (warp == kFetchWarp) tmem_dealloc(tmem, 512);
 }
 
 // Segments of a row's chunks, where one CTA for each head and block of columns leaves SMs idle: as many as

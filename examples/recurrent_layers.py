@@ -1,10 +1,10 @@
-"""Two recurrent layers built from the library's calls, as a model would run them: a gated delta rule
-layer and a selective scan layer, each for prompts, single tokens (state carried and updated in
-place) and training steps (forward and backward).
+"""Recurrent layers built from the library's calls, as a model would run them: a gated delta rule layer, a
+selective scan layer and blocks of linear attention on a residual stream, each for prompts, single
+tokens (state carried and updated in place) and training steps (forward and backward).
 
     python examples/recurrent_layers.py
 
-prints, for both layers, how far a prompt continued token by token is from one long prompt, and the
+prints, for each of them, how far a prompt continued token by token is from one long prompt, and the
 time of a prompt, a token and a training step. PyTorch holds the tensors; every operation on them
 other than slicing, copying and adding gradients is a call of the library.
 """
@@ -169,6 +169,70 @@ class SelectiveScanLayer:
                 "dtaps": cb["dw"], "dbias": cb["dbias"], "dA_log": sc["dA_log"], "dD": sc["dD"], "ddt_bias": sc["ddt_bias"]}
 
 
+class LinearAttentionBlocks:
+    """Blocks on a residual stream: norm -> projection to q, k, v and z -> linear attention with a decay for
+    each head -> head norm gated by z -> projection -> norm, residual scale and addition onto the stream,
+    with the norm in front of the next block. Returns the stream's norm behind the last block."""
+
+    def __init__(self, width=512, Hk=2, Hv=4, Dk=64, Dv=64, blocks=2, seed=3):
+        gen = torch.Generator(device="cuda")
+        gen.manual_seed(seed)
+        self.Hk, self.Hv, self.Dk, self.Dv, self.width = Hk, Hv, Dk, Dv, width
+        self.nk, self.nv = Hk * Dk, Hv * Dv
+        around = lambda n, mean: mean + _normal(gen, n, scale=0.1, dtype=F32)  # noqa: E731
+        self.g = torch.exp(-torch.exp2(-8.0 * torch.arange(1, Hv + 1, device="cuda") / Hv))
+        self.w_first = around(width, 1.0)
+        self.blocks = []
+        for _ in range(blocks):
+            W_in = _normal(gen, 2 * (self.nk + self.nv), width, scale=width ** -0.5, dtype=F32)
+            W_in[:self.nk] *= Dk ** -0.5
+            self.blocks.append(dict(W_in=W_in.to(BF16), w_head=around(self.nv, 1.0), W_out=_normal(gen, width, self.nv, scale=self.nv ** -0.5),
+                                    scale=around(width, 0.5), w_post=around(width, 1.0), w_pre=around(width, 1.0)))
+
+    def start(self, B):
+        return [torch.zeros(B, self.Hv, self.Dv, self.Dk, device="cuda") for _ in self.blocks]
+
+    def _split(self, p):
+        a, b, c = self.nk, 2 * self.nk, 2 * self.nk + self.nv
+        return (p[..., :a].unflatten(-1, (self.Hk, self.Dk)), p[..., a:b].unflatten(-1, (self.Hk, self.Dk)),
+                p[..., b:c].unflatten(-1, (self.Hv, self.Dv)), p[..., c:])
+
+    def forward(self, x, state=None, train=False, lens=None):
+        B, T, _ = x.shape
+        states = self.start(B) if state is None else state
+        n, first_stats = gdn.gdn_norm_fwd(x, 1, self.w_first, act="none", center=False)
+        ends, kept, first = [], [], x
+        for w, S0 in zip(self.blocks, states):
+            p, _ = gdn.gdn_linear_fwd(n, w["W_in"])
+            q, k, v, z = self._split(p)
+            o, S = gdn.gdn_linattn_fwd(q, k, v, self.g, S0, lens, S_T=S0 if T == 1 and not train else None)
+            o = o.view(B, T, self.nv)
+            m, head_stats = gdn.gdn_norm_fwd(o, self.Hv, w["w_head"], None, z, act="silu", center=False)
+            h, _ = gdn.gdn_linear_fwd(m, w["W_out"])
+            r, y, stats = gdn.gdn_resnorm_fwd(x, h, None, w["scale"], w["w_post"], w["w_pre"])
+            kept.append(dict(n=n, p=p, S0=S0, o=o, m=m, head_stats=head_stats, h=h, x=x, stats=stats))
+            ends.append(S)
+            x, n = r, y
+        return n, (dict(blocks=kept, x=first, first_stats=first_stats, lens=lens) if train else ends)
+
+    def backward(self, c, dy):
+        """Gradients of x and of the parameters for the cotangent dy of what forward returns."""
+        dn, dx, grads = dy, None, []
+        for w, s in zip(reversed(self.blocks), reversed(c["blocks"])):
+            B, T, _ = dn.shape
+            rb = gdn.gdn_resnorm_bwd(s["x"], s["h"], s["stats"], dn, dx, None, w["scale"], w["w_post"], w["w_pre"])
+            out = gdn.gdn_linear_bwd(s["m"], w["W_out"], rb["dh"], want_dbias=False)
+            q, k, v, z = self._split(s["p"])
+            nb = gdn.gdn_norm_bwd(s["o"], self.Hv, s["head_stats"], out["dx"], w["w_head"], None, z, act="silu", center=False)
+            a = gdn.gdn_linattn_bwd(q, k, v, self.g, nb["dx"].view(B, T, self.Hv, self.Dv), s["S0"], c["lens"], want_dS0=False)
+            dp = torch.cat([a["dq"].flatten(-2), a["dk"].flatten(-2), a["dv"].flatten(-2), nb["dz"]], -1)
+            inp = gdn.gdn_linear_bwd(s["n"], w["W_in"], dp, want_dbias=False)
+            grads.insert(0, dict(W_in=inp["dW"], w_head=nb["dw"], W_out=out["dW"], scale=rb["dscale"], w_post=rb["dw_post"], w_pre=rb["dw_pre"]))
+            dn, dx = inp["dx"], rb["dx"]
+        first = gdn.gdn_norm_bwd(c["x"], 1, c["first_stats"], dn, self.w_first, act="none", center=False)
+        return {"dx": dx + first["dx"], "dw_first": first["dw"], "blocks": grads}
+
+
 def continued(layer, x, tokens):
     """The outputs of x with its last `tokens` steps taken one at a time behind the prompt."""
     T = x.shape[1]
@@ -195,7 +259,7 @@ def _time_us(f, reps=20):
 def main():
     gen = torch.Generator(device="cuda")
     gen.manual_seed(2)
-    for layer in (GatedDeltaLayer(), SelectiveScanLayer()):
+    for layer in (GatedDeltaLayer(), SelectiveScanLayer(), LinearAttentionBlocks()):
         x = _normal(gen, 2, 260, 512)
         whole, _ = layer.forward(x)
         off = (continued(layer, x, 4).double() - whole.double()).norm() / whole.double().norm()

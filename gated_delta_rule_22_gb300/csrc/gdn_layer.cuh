@@ -125,7 +125,7 @@ struct ResnormParams {
     void *r, *y, *dx, *dh, *dz;
     float *stats, *dscale, *dw_post, *dw_pre;
     float *part;               // backward: [ctas][2][D] partial sums of what dscale and dw_post are made of, and of dw_pre
-    float *part_z;             // backward, gate_rows > 1: [units][D] partial sums of dz before act'(z)
+    float *part_z;             // backward, more than one unit for a row of z: [units][D] partial sums of dz before act'(z)
     long long ldx, ldh, ldz;
     int M, D, gate_rows, act, post, pre;
     int unit, per_gate, units, ctas;   // backward: rows of a unit, units of a row of z, units, CTAs that take them

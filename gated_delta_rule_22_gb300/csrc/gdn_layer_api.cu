@@ -154,9 +154,11 @@ int linattn_plan(const gdn_linattn_shape *s, gdn::LinattnParams *p, long long (&
     return GDN_OK;
 }
 
-// Whether the chunked form reads these sizes (bf16 rows that TMA can), and these addresses.
+// Whether the chunked form takes these sizes: bf16 rows that TMA can read, and more than a few steps (64 rows of 32
+// heads of 128 x 128, forward and backward: 8 steps 197 and 395 us in chunks, 168 and 477 step by step; 4 steps
+// 196 and 392 us, 151 and 402; 16 steps 198 and 400 us, 230 and 666).
 bool linattn_chunks(const gdn::LinattnParams &p, int dtype, const long long (&ld)[3]) {
-    return dtype == GDN_BF16 && p.T > 1 && p.Dk % 8 == 0 && p.Dv % 8 == 0 && ld[0] % 8 == 0 && ld[1] % 8 == 0 && ld[2] % 8 == 0;
+    return dtype == GDN_BF16 && p.T >= 8 && p.Dk % 8 == 0 && p.Dv % 8 == 0 && ld[0] % 8 == 0 && ld[1] % 8 == 0 && ld[2] % 8 == 0;
 }
 
 // The call's sweeps, with the float32 sums and segment states that they need placed in `ws`; returns the bytes of
@@ -240,7 +242,7 @@ int resnorm_plan(const gdn_resnorm_shape *s, gdn::ResnormParams *p) {
 
 size_t resnorm_part_bytes(const gdn::ResnormParams &p) { return up256((size_t)p.ctas * 2 * p.D * 4); }
 size_t resnorm_ws(const gdn::ResnormParams &p) {
-    return resnorm_part_bytes(p) + (p.gate_rows > 1 ? up256((size_t)p.units * p.D * 4) : 0);
+    return resnorm_part_bytes(p) + (p.gate_rows > 1 && p.per_gate > 1 ? up256((size_t)p.units * p.D * 4) : 0);
 }
 
 // bf16 x and W with packed rows are read in place by TMA, so they are 16-byte aligned like every packed

@@ -98,6 +98,7 @@ template <typename T, int E2, int WARPS, int ROWS>
 __global__ void __launch_bounds__(32 * WARPS) linattn_walk_kernel(const LinattnParams p, int blocks0, int blocks1) {
     constexpr int W = 64 * E2;                          // staged columns of a and b
     constexpr int kWalkThreads = 32 * WARPS, kWalkBlock = WARPS * ROWS;     // threads, state rows of a CTA
+    static_assert(kWalkThreads % kWalkBlock == 0, "whole steps of zeros at once");
     constexpr int LA = kWalkTile * W / kWalkThreads, LC = kWalkTile * kWalkBlock / kWalkThreads;
     __shared__ __align__(16) float sa[kWalkTile][W], sb[kWalkTile][W], sc[kWalkTile][kWalkBlock];
     const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
@@ -119,10 +120,15 @@ __global__ void __launch_bounds__(32 * WARPS) linattn_walk_kernel(const LinattnP
         return w.init_t ? (head * Db + col) * Dc + row : (head * Dc + row) * Db + col;
     };
     auto inside = [&](int r, int m, int i) { return row0 + r < Dc && 2 * lane + 64 * m + i < Db; };
+    const bool pairs = !w.init_t && Db % 2 == 0;        // of a row's elements in init and last, aligned to 8 bytes
 #pragma unroll
     for (int r = 0; r < ROWS; ++r)
 #pragma unroll
         for (int m = 0; m < E2; ++m) {
+            if (pairs) {
+                s[r][m] = w.init != nullptr && inside(r, m, 0) ? *reinterpret_cast<const float2 *>(w.init + place(r, m, 0)) : make_float2(0.f, 0.f);
+                continue;
+            }
             s[r][m].x = w.init != nullptr && inside(r, m, 0) ? w.init[place(r, m, 0)] : 0.f;
             s[r][m].y = w.init != nullptr && inside(r, m, 1) ? w.init[place(r, m, 1)] : 0.f;
         }
@@ -216,14 +222,18 @@ __global__ void __launch_bounds__(32 * WARPS) linattn_walk_kernel(const LinattnP
             if (lane % SHARE == 0 && ku < steps && row < Dc) put(t0 + (w.rev ? steps - 1 - ku : ku), row, sum);
         }
     }
-    for (int i = tid; i < (T_ - n) * kWalkBlock; i += kWalkThreads)    // zeros behind the row
-        if (e0 + i % kWalkBlock < Dc) put(n + i / kWalkBlock, e0 + i % kWalkBlock, 0.f);
+    if (e0 + tid % kWalkBlock < Dc)                     // zeros behind the row
+        for (int t = n + tid / kWalkBlock; t < T_; t += kWalkThreads / kWalkBlock) put(t, e0 + tid % kWalkBlock, 0.f);
     if (w.last != nullptr) {
         const float gl = w.rev && n > 0 ? g : 1.f;
 #pragma unroll
         for (int r = 0; r < ROWS; ++r)
 #pragma unroll
             for (int m = 0; m < E2; ++m) {
+                if (pairs) {
+                    if (inside(r, m, 0)) *reinterpret_cast<float2 *>(w.last + place(r, m, 0)) = make_float2(gl * s[r][m].x, gl * s[r][m].y);
+                    continue;
+                }
                 if (inside(r, m, 0)) w.last[place(r, m, 0)] = gl * s[r][m].x;
                 if (inside(r, m, 1)) w.last[place(r, m, 1)] = gl * s[r][m].y;
             }
@@ -315,12 +325,14 @@ static cudaError_t launch_walk_w(const LinattnParams &p, cudaStream_t s) {
     else linattn_walk_kernel<T, 4, WARPS, ROWS><<<grid, 32 * WARPS, 0, s>>>(p, blocks[0], blocks[1]);
     return cudaGetLastError();
 }
-// Eight warps of eight rows share what is staged; four of four rows where that would leave SMs idle.
+// Eight warps of eight rows share what is staged; four of four rows where that would leave SMs idle or where reading
+// the state is the work (float32, 1024 steps of 8 heads of 128 x 128: 142 us, 259 with the large ones; of 4 x 32
+// heads 565 and 443; bf16, 64 x 32 heads: 2 steps 148 and 159 us).
 template <typename T>
 static cudaError_t launch_walk_t(const LinattnParams &p, cudaStream_t s) {
     long long ctas = 0;
     for (int i = 0; i < p.sweeps; ++i) ctas += (p.sweep[i].Dc + 63) / 64;
-    return ctas * p.Hv * p.B < 152 ? launch_walk_w<T, 4, 4>(p, s) : launch_walk_w<T, 8, 8>(p, s);
+    return ctas * p.Hv * p.B < 152 || p.T < 16 ? launch_walk_w<T, 4, 4>(p, s) : launch_walk_w<T, 8, 8>(p, s);
 }
 
 cudaError_t launch_linattn_steps(const LinattnParams &p, int dtype, cudaStream_t s) {

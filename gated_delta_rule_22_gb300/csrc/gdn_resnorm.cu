@@ -179,29 +179,29 @@ __global__ void __launch_bounds__(LPR < 128 ? 128 : LPR) resnorm_fwd_kernel(cons
     const Lane at(p.D);
     Ring ring(smem);
     RowSum<LPR, 1> row_sum;
-    const int rows = gridDim.x * Lane::kRows;
+    const unsigned rows = gridDim.x * Lane::kRows, M = p.M;    // (row numbers run past the last by some rounds)
     const float inv_D = 1.f / p.D;
-    int m = blockIdx.x * Lane::kRows + at.slot;
+    unsigned m = blockIdx.x * Lane::kRows + at.slot;
     const T *const x0 = static_cast<const T *>(p.x), *const h0 = static_cast<const T *>(p.h), *const z0 = static_cast<const T *>(p.z);
     const T *src[3];
-    auto locate = [&](int row) {
+    auto locate = [&](unsigned row) {
         src[0] = x0 + (size_t)row * p.ldx;
         src[1] = h0 + (size_t)row * p.ldh;
         src[2] = z0 == nullptr ? nullptr : z0 + (size_t)(p.gate_rows == 1 ? row : row / p.gate_rows) * p.ldz;
     };
-    int next = m;                                          // the next row to be fetched
+    unsigned next = m;                                     // the next row to be fetched
     for (int i = 0; i < Ring::kAhead - 1; ++i, next += rows) {
         locate(next);
-        ring.fetch(at, src, next < p.M);
+        ring.fetch(at, src, next < M);
     }
     float2 k[P], wr[P];
     at.params(p.scale, p.w_post, k);
     at.params(p.w_pre, nullptr, wr);
     // (all lanes of a warp walk together: a row behind the last is computed from anything and not stored)
-    for (; m - at.slot < p.M; m += rows, next += rows) {
-        const bool live = m < p.M;
+    for (; m - at.slot < M; m += rows, next += rows) {
+        const bool live = m < M;
         locate(next);
-        ring.fetch(at, src, next < p.M);
+        ring.fetch(at, src, next < M);
         ring.arrive();
         if (!Ring::kRing) locate(m);
         float2 x[P], h[P];
@@ -290,7 +290,7 @@ __global__ void __launch_bounds__(LPR < 128 ? 128 : LPR, LPR <= 256 ? 2 : 1) res
     for (int unit = blockIdx.x; unit < p.units; unit += p.ctas) {
         const int gate = unit / p.per_gate, span = shared_z ? p.gate_rows : p.M;
         const int first = gate * span + unit % p.per_gate * p.unit;
-        const int last = min(first + p.unit, min((gate + 1) * span, p.M));
+        const int last = first + min(p.unit, min((gate + 1) * span, p.M) - first);
 #pragma unroll
         for (int e = 0; e < P; ++e) dzs[e] = both(0.f);
         int next = first + at.slot;
@@ -383,7 +383,15 @@ __global__ void __launch_bounds__(LPR < 128 ? 128 : LPR, LPR <= 256 ? 2 : 1) res
         ring.restart();
         if (shared_z && p.dz != nullptr) {
             over_slots(dzs);
-            if (at.slot == 0) at.put(p.part_z + (size_t)unit * p.D, dzs);
+            if (at.slot == 0 && p.per_gate > 1) {
+                at.put(p.part_z + (size_t)unit * p.D, dzs);
+            } else if (at.slot == 0) {
+                float2 z[P];
+                at.read(z0 + (size_t)gate * p.ldz, z);
+#pragma unroll
+                for (int e = 0; e < P; ++e) dzs[e] = mul2(dzs[e], make_float2(dact_rt(p.act, z[e].x), dact_rt(p.act, z[e].y)));
+                at.store(static_cast<T *>(p.dz) + (size_t)gate * p.D, dzs);
+            }
         }
     }
     over_slots(Q);
@@ -409,7 +417,7 @@ __global__ void __launch_bounds__(256) resnorm_sum_kernel(const ResnormParams p)
     if (p.dw_post != nullptr) p.dw_post[i] = p.scale != nullptr ? s * p.scale[i] : s;
 }
 
-// dz of a gate whose rows are shared: the units' sums, times act'(z).
+// dz of a gate whose rows are shared by more than one unit: the units' sums, times act'(z).
 template <typename T>
 __global__ void __launch_bounds__(256) resnorm_gate_kernel(const ResnormParams p) {
     const int gate = blockIdx.y;
@@ -495,17 +503,8 @@ static cudaError_t launch_bwd_t(const ResnormParams &p, cudaStream_t s) {
     if (e != cudaSuccess) return e;
     timing_mark("resnorm_sum", 0, s);
     if (p.dscale != nullptr || p.dw_post != nullptr || p.dw_pre != nullptr) resnorm_sum_kernel<<<(2 * p.D + 31) / 32, 256, 0, s>>>(p);
-    if (p.dz != nullptr && p.gate_rows > 1) {
-        // (the rows of z on the grid's second axis, at most 65535 of them at a time)
-        const int gates = p.M / p.gate_rows;
-        for (int g0 = 0; g0 < gates; g0 += 65535) {
-            ResnormParams q = p;
-            q.part_z += (size_t)g0 * p.per_gate * p.D;
-            q.z = static_cast<const T *>(p.z) + (size_t)g0 * p.ldz;
-            q.dz = static_cast<T *>(p.dz) + (size_t)g0 * p.D;
-            resnorm_gate_kernel<T><<<dim3((p.D + 31) / 32, gates - g0 < 65535 ? gates - g0 : 65535), 256, 0, s>>>(q);
-        }
-    }
+    if (p.dz != nullptr && p.gate_rows > 1 && p.per_gate > 1)                   // (fewer gates than CTAs then)
+        resnorm_gate_kernel<T><<<dim3((p.D + 31) / 32, p.M / p.gate_rows), 256, 0, s>>>(p);
     timing_mark("resnorm_sum", 1, s);
     return cudaGetLastError();
 }

@@ -450,7 +450,8 @@ GDN_API int gdn_linear_bwd(const gdn_linear_shape *shape, const void *x, const v
  * in chunks of 128 steps on the tensor cores (bf16; q, k and v 16-byte aligned, Dk, Dv and the row
  * strides multiples of 8) or step by step (float32 and the rest); a single step is one pass over the
  * state, and with T = 1 S_T may be S0 itself (updated in place). In chunks, a q, k, v or dy that is not
- * finite at a valid step makes outputs of its chunk of the same row and head NaN, earlier steps' too.
+ * finite at a valid step makes outputs of its chunk of the same row and head NaN, those of other steps of it too,
+ * and the states behind it.
  * The backward computes the states again from k, v and S0; the forward saves nothing. dq and dk are
  * summed over the value heads of each key head in ascending order.
  * workspace: gdn_linattn_fwd_workspace_bytes / gdn_linattn_bwd_workspace_bytes bytes (0: may be NULL).

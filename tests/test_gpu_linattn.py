@@ -2,9 +2,9 @@
 steps, both forms (step by step, in chunks), layouts, lengths and decays at which they can go wrong.
 
 Tolerances (2-norm of the error over that of the output). A bf16 output is off by at most 2^-8 of
-itself; in chunks the products of a pair of steps and the states are rounded to bf16 on the way, and their
-terms' errors, of either sign, add as the terms' squares do: at most 2^-8 sqrt(1 + 1) together, 1.5 x 2^-8
-with room for terms that partly cancel. float32 outputs, step by step: n roundings of 2^-24 of a sum's
+itself, 0.43 x 2^-8 in the 2-norm (rounding errors are uniform); in chunks the states and their weighted
+inputs are rounded to bf16 on the way, and these terms' errors, of either sign, add as the terms' squares do: at
+most 0.43 x 2^-8 sqrt(1 + 1 + 1) together, and twice that, 1.5 x 2^-8, where terms partly cancel. float32 outputs, step by step: n roundings of 2^-24 of a sum's
 running value, of either sign, and the dot products' Dk: 2^-24 sqrt(2 n + D), up to some 2e-6 at n = 400.
 The float32 states of the chunked form hold 24 bits of k and the decay's powers (2 ulp of exp2 and log2, times
 the exponent): 2^-20 covers ages up to log2 = 8, beyond which nothing counts."""
@@ -193,8 +193,68 @@ def test_gradients_against_differences():
         assert abs(numeric - exact) <= 1e-3 * abs(exact) + 1e-3 * (way.norm() * d[grad].norm()).item() / way.numel() ** 0.5, name
 
 
-def test_gdn_beside_it_is_unmoved():
-    """Streams: the call under an explicit stream gives the same bits."""
+@pytest.mark.parametrize("dt", [BF16, F32], ids=["bf16", "f32"])
+@pytest.mark.parametrize("shape", [(1, 1500, 1, 1, 64, 64), (2, 1029, 1, 2, 136, 64), (1, 2100, 1, 1, 24, 40)], ids=lambda s: "x".join(map(str, s)))
+def test_long_rows_of_few_heads(shape, dt):
+    """Few heads: the chunked form takes a row in segments."""
+    check(make(12, *shape, dt), what="long")
+
+
+@pytest.mark.parametrize("decay", ["mixed", "one", "zero"])
+def test_segments_of_ragged_rows(decay):
+    a = make(13, 4, 1300, 1, 1, 64, 64, BF16, decay)
+    lens = torch.tensor([1300, 130, 700, 0], device="cuda", dtype=torch.int32)
+    for b, n in enumerate(lens.tolist()):
+        for t in ("q", "k", "v", "dy"):
+            a[t][b, n:] = float("nan")
+    got = check(a, lens, what=decay)
+    assert all(torch.all(got[n][0][b, L:] == 0) for n in ("y", "dq", "dk", "dv") for b, L in enumerate(lens.tolist()))
+
+
+def test_the_forms_agree():
+    """The same bf16 inputs in chunks, and (from addresses that TMA cannot read) step by step: they differ by the
+    chunked form's roundings, and the states by their last bits."""
+    a = make(14, 2, 600, 2, 4, 128, 64, BF16, wide=16)
+    off = dict(a)
+    for n in ("q", "k", "v"):
+        t = torch.zeros(*a[n].shape[:2], a[n].shape[2] * a[n].shape[3] + 1, device="cuda", dtype=BF16)
+        off[n] = t[..., 1:].unflatten(-1, a[n].shape[2:]).copy_(a[n])
+    y, S = gdn().gdn_linattn_fwd(a["q"], a["k"], a["v"], a["g"], a["S0"])
+    y2, S2 = gdn().gdn_linattn_fwd(off["q"], off["k"], off["v"], off["g"], off["S0"])
+    assert R.rel(y, y2) <= TOL[BF16] and R.rel(S, S2) <= TOL_STATE and not torch.equal(y, y2)
+
+
+def test_two_streams_at_once():
+    """Calls that overlap on two streams, each with its own memory, give the bits of calls one by one."""
+    sets = [make(15 + i, 2, 1000, 1, 2, 64, 64, BF16) for i in range(2)]
+    run = lambda a, s: (*gdn().gdn_linattn_fwd(a["q"], a["k"], a["v"], a["g"], a["S0"], stream=s),  # noqa: E731
+                        *gdn().gdn_linattn_bwd(a["q"], a["k"], a["v"], a["g"], a["dy"], a["S0"], None, a["dS_T"], stream=s).values())
+    want = [run(a, None) for a in sets]
+    torch.cuda.synchronize()
+    streams = [torch.cuda.Stream() for _ in sets]
+    for _ in range(5):
+        got = [run(a, s) for a, s in zip(sets, streams)]
+        torch.cuda.synchronize()
+        assert all(torch.equal(x, y) for w, g in zip(want, got) for x, y in zip(w, g))
+
+
+def test_another_row_or_head_that_is_not_finite():
+    """What is not finite stays in its row and head."""
+    a = make(17, 3, 400, 2, 2, 64, 64, BF16)
+    run = lambda: (*gdn().gdn_linattn_fwd(a["q"], a["k"], a["v"], a["g"], a["S0"]),  # noqa: E731
+                   *gdn().gdn_linattn_bwd(a["q"], a["k"], a["v"], a["g"], a["dy"], a["S0"], None, a["dS_T"]).values())
+    clean = run()
+    a["v"][1, 200, 1] = float("inf")
+    a["q"][1, 250, 1, 3] = float("nan")
+    for x, y in zip(clean, run()):
+        heads = 1 if x.dim() == 4 and x.shape[1] == 2 else 2            # states [B, H, ...], the rest [B, T, H, ...]
+        keep = torch.ones_like(x, dtype=torch.bool)
+        keep[1].select(heads - 1, 1)[...] = False
+        assert torch.equal(x[keep], y[keep])
+
+
+def test_under_an_explicit_stream():
+    """The call under an explicit stream gives the same bits."""
     a = make(11, 2, 300, 1, 2, 128, 128, BF16)
     y, S = gdn().gdn_linattn_fwd(a["q"], a["k"], a["v"], a["g"], a["S0"])
     d = gdn().gdn_linattn_bwd(a["q"], a["k"], a["v"], a["g"], a["dy"], a["S0"], None, a["dS_T"])

@@ -83,12 +83,13 @@ struct LinattnSweep {
     const void *a, *b, *c;
     const float *init;         // the state before the first step taken; null: zeros
     float *last;               // the state behind the last (rev: decayed once more); null: not wanted
-    void *out;                 // [B][T][Ho][Dc] in the call's type, or (sums) float32 by value head
+    void *out;                 // [B][T][heads][Dc] in the call's type, the heads those of c
+    float *part;               // (sums) float32 outputs by value head instead, [blocks of Db][B][T][Hv][Dc], to be added
     long long lda, ldb, ldc;   // elements between steps
     int a_keys, b_keys, c_keys;   // the operand's heads are key heads
     int Db, Dc, rev;
     int init_t;                // init lies transposed, [Db][Dc]
-    int sums;                  // out is float32 planes [B][T][Hv][Dc], one for each block of Db, to be added (LinattnSum)
+    int sums;                  // out is formed from part (LinattnSum)
     int a_map, b_map, c_map;   // tensor maps of the operands
 };
 
@@ -110,10 +111,9 @@ struct LinattnParams {
     const int *lens;
     int *status;
     int B, T, Hk, Hv, Dk, Dv;
-    // chunked form: each row's chunks are taken in `segs` segments of seg_chunks; seg_state holds what the earlier
-    // segments leave, from a zero state, [seg_units][128][128]
+    // chunked form: each row's chunks are taken in `segs` segments of seg_chunks; seg_state holds what the segments up to
+    // each but the last leave, from a zero state: [CTAs / segs][segs - 1][128][128]
     int segs, seg_chunks;
-    size_t seg_units;
     float *seg_state;
 };
 
@@ -154,7 +154,7 @@ cudaError_t launch_norm_fwd(const NormParams &p, int dtype, cudaStream_t s);
 cudaError_t launch_norm_bwd(const NormParams &p, int dtype, cudaStream_t s);
 cudaError_t launch_linattn_step(const LinattnParams &p, int dtype, cudaStream_t s);    // T = 1, the forward's sweep
 cudaError_t launch_linattn_steps(const LinattnParams &p, int dtype, cudaStream_t s);   // all sweeps, then their sums
-void linattn_segments(LinattnParams *p);                                               // chooses segs, seg_chunks and seg_units
+size_t linattn_segments(LinattnParams *p);                                             // chooses segs and seg_chunks; the states of seg_state
 cudaError_t launch_linattn_chunks(const LinattnParams &p, const LinattnMaps &maps, cudaStream_t s);
 cudaError_t launch_linattn_sums(const LinattnParams &p, int dtype, cudaStream_t s);
 cudaError_t launch_resnorm_fwd(const ResnormParams &p, int dtype, cudaStream_t s);

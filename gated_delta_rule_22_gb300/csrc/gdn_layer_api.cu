@@ -161,8 +161,8 @@ bool linattn_chunks(const gdn::LinattnParams &p, int dtype, const long long (&ld
     return dtype == GDN_BF16 && p.T >= 8 && p.Dk % 8 == 0 && p.Dv % 8 == 0 && ld[0] % 8 == 0 && ld[1] % 8 == 0 && ld[2] % 8 == 0;
 }
 
-// The call's sweeps, with the float32 sums and segment states that they need placed in `ws`; returns the bytes of
-// these. `io`: the forward's q, k, v, y, S0, S_T, or the backward's q, k, v, dy, S0, dS_T, dq, dk, dv, dS0.
+// The call's sweeps, with the float32 outputs and segment states that they need placed in `ws`; returns the bytes
+// of these.
 struct LinattnIo {
     const void *q, *k, *v, *dy;
     const float *S0, *dS_T;
@@ -171,34 +171,31 @@ struct LinattnIo {
 };
 size_t linattn_sweeps(gdn::LinattnParams *p, const LinattnIo &io, const long long (&ld)[3], bool bwd, bool chunks, char *ws) {
     const long long ldy = (long long)p->Hv * p->Dv;
-    void *outs[3] = {bwd ? io.dq : io.y, io.dk, io.dv};
     if (!bwd) {
         p->sweeps = 1;
-        p->sweep[0] = {io.q, io.k, io.v, io.S0, io.S_T, nullptr, ld[0], ld[1], ld[2], 1, 1, 0, p->Dk, p->Dv, 0, 0, 0, 0, 1, 2};
+        p->sweep[0] = {io.q, io.k, io.v, io.S0, io.S_T, io.y, nullptr, ld[0], ld[1], ld[2], 1, 1, 0, p->Dk, p->Dv, 0, 0, 0, 0, 1, 2};
     } else {
         p->sweeps = 3;
-        p->sweep[0] = {io.dy, io.v, io.k, io.S0, nullptr, nullptr, ldy, ld[2], ld[1], 0, 0, 1, p->Dv, p->Dk, 0, 1, 0, 3, 2, 1};
-        p->sweep[1] = {io.v, io.dy, io.q, io.dS_T, nullptr, nullptr, ld[2], ldy, ld[0], 0, 0, 1, p->Dv, p->Dk, 1, 1, 0, 2, 3, 0};
-        p->sweep[2] = {io.k, io.q, io.dy, io.dS_T, io.dS0, nullptr, ld[1], ld[0], ldy, 1, 1, 0, p->Dk, p->Dv, 1, 0, 0, 1, 0, 3};
+        p->sweep[0] = {io.dy, io.v, io.k, io.S0, nullptr, io.dq, nullptr, ldy, ld[2], ld[1], 0, 0, 1, p->Dv, p->Dk, 0, 1, 0, 3, 2, 1};
+        p->sweep[1] = {io.v, io.dy, io.q, io.dS_T, nullptr, io.dk, nullptr, ld[2], ldy, ld[0], 0, 0, 1, p->Dv, p->Dk, 1, 1, 0, 2, 3, 0};
+        p->sweep[2] = {io.k, io.q, io.dy, io.dS_T, io.dS0, io.dv, nullptr, ld[1], ld[0], ldy, 1, 1, 0, p->Dk, p->Dv, 1, 0, 0, 1, 0, 3};
     }
     size_t used = 0;
     p->sums = 0;
     for (int i = 0; i < p->sweeps; ++i) {
         gdn::LinattnSweep &w = p->sweep[i];
         const int planes = chunks ? (w.Db + 127) / 128 : 1, group = w.c_keys ? p->Hv / p->Hk : 1;
-        w.out = outs[i];
         if (planes * group == 1) continue;
         const size_t plane = (size_t)p->B * p->T * p->Hv * w.Dc;
         w.sums = 1;
-        w.out = ws + used;
-        p->sum[p->sums++] = {static_cast<const float *>(w.out), outs[i], plane, planes, group, p->Hv / group, w.Dc};
+        w.part = reinterpret_cast<float *>(ws + used);
+        p->sum[p->sums++] = {w.part, w.out, plane, planes, group, p->Hv / group, w.Dc};
         used += up256(planes * plane * 4);
     }
-    p->segs = 1;
     if (chunks) {
-        gdn::linattn_segments(p);
+        const size_t states = gdn::linattn_segments(p);
         p->seg_state = reinterpret_cast<float *>(ws + used);
-        used += up256(p->seg_units * gdn::kLinattnChunk * 128 * 4);
+        used += up256(states * gdn::kLinattnChunk * 128 * 4);
     }
     return used;
 }

@@ -154,7 +154,7 @@ __global__ void __launch_bounds__(32 * WARPS) linattn_walk_kernel(const LinattnP
     const size_t out0 = (size_t)b * T_ * out_step + (size_t)h * Dc;
     auto put = [&](int t, int row, float x) {
         const size_t at = out0 + (size_t)t * out_step + row;
-        if (w.sums) static_cast<float *>(w.out)[at] = x;
+        if (w.sums) w.part[at] = x;
         else static_cast<T *>(w.out)[at] = from_f32<T>(x);
     };
     if (tiles > 0) fetch(w.rev ? tiles - 1 : 0);

@@ -21,7 +21,7 @@
 // each a relative 2^-9 of terms of either sign, so that a chunk's own steps add one rounding to that of the
 // output and earlier steps at most two. b~ is the one rounded, since U then needs nothing but b's place and the
 // chain from state to state is short; where the state leaves the call and the chunk still counts in it by
-// 2^-13, b~ has two terms (by 1 / 16: three, 24 bits), which take the places of a and Z once O2 has read them.
+// 2^-12, b~ has two terms (by 1 / 8: three, 24 bits), which take the places of a and Z once O2 has read them.
 //
 // Warps 0-7 mask P, warps 8-11 write outputs, warps 12-19 hold the state (each four half of its columns); one warp
 // fetches (two chunks deep), two issue products: P and O1, and O2 and U, so that neither chain waits for the other.
@@ -120,7 +120,7 @@ __device__ __forceinline__ void split_product(uint32_t b, bf16x2 w0, bf16x2 w1, 
 
 __device__ __forceinline__ void write_zeros(const LinattnSweep &w, size_t at, int n) {
     if (w.sums)
-        for (int i = 0; i < n; i += 4) *reinterpret_cast<float4 *>(static_cast<float *>(w.out) + at + i) = make_float4(0.f, 0.f, 0.f, 0.f);
+        for (int i = 0; i < n; i += 4) *reinterpret_cast<float4 *>(w.part + at + i) = make_float4(0.f, 0.f, 0.f, 0.f);
     else
         for (int i = 0; i < n; i += 8) *reinterpret_cast<uint4 *>(static_cast<__nv_bfloat16 *>(w.out) + at + i) = make_uint4(0u, 0u, 0u, 0u);
 }
@@ -190,7 +190,7 @@ __global__ void __launch_bounds__(kThreads, 1) linattn_chunk_kernel(const __grid
     auto terms_of = [&](int i) {
         const int after = rev ? chunk_of(i) * kC : max(n - (chunk_of(i) + 1) * kC, 0);        // steps that follow it in the sweep
         const float weight = after == 0 ? 0.f : after * lg;                                  // (its log2)
-        return w.last == nullptr ? 1 : weight >= -4.f ? 3 : weight >= -13.f ? 2 : 1;
+        return w.last == nullptr ? 1 : weight >= -3.f ? 3 : weight >= -12.f ? 2 : 1;
     };
     const size_t out_step = (size_t)p.Hv * w.Dc;
     const size_t out0 = (size_t)(db0 / 128) * p.B * p.T * out_step + (size_t)b * p.T * out_step + (size_t)h * w.Dc + dc0;
@@ -258,7 +258,7 @@ __global__ void __launch_bounds__(kThreads, 1) linattn_chunk_kernel(const __grid
         }
     } else if (warp < kStateWarp) {                // ---- the outputs
         regs_dec<kOutRegs>();
-        const bool wide = ((uintptr_t)w.out & 31) == 0 && w.Dc % 16 == 0;
+        const bool wide = ((uintptr_t)(w.sums ? w.part : w.out) & 31) == 0 && w.Dc % 16 == 0;
         const uint32_t lanes = tmem + ((uint32_t)(warp & 3) << 21);
         const int i = threadIdx.x & 127;           // this thread's step of the chunk
         for (int k = 0; k < work && !cp.state_only; ++k) {
@@ -282,7 +282,7 @@ __global__ void __launch_bounds__(kThreads, 1) linattn_chunk_kernel(const __grid
                 }
                 if (i >= L) continue;
                 if (w.sums) {
-                    float *out = static_cast<float *>(w.out) + at + c;
+                    float *out = w.part + at + c;
                     store_piece2(out, o1[0], o1[1], o1[2], o1[3], o1[4], o1[5], o1[6], o1[7], wide);
                     if (c + 8 < Dc) store_piece2(out + 8, o1[8], o1[9], o1[10], o1[11], o1[12], o1[13], o1[14], o1[15], wide);
                 } else {
@@ -323,21 +323,18 @@ __global__ void __launch_bounds__(kThreads, 1) linattn_chunk_kernel(const __grid
             }
             Z[d] = z.x; Z[d + 1] = z.y; Z[d + 2] = z.z; Z[d + 3] = z.w;
         }
-        if (!cp.state_only && work_here > 0)       // through the earlier segments
-            for (int s = 0; s < seg; ++s) {
-                const int lo = s * p.seg_chunks, hi = lo + p.seg_chunks;      // whole segments, but for the row's end
-                const int steps = rev ? min(n, (chunks - lo) * kC) - (chunks - hi) * kC : p.seg_chunks * kC;
-                const float decay = exp2f(steps * log2f(p.g[h]));
-                const float4 *E = reinterpret_cast<const float4 *>(p.seg_state) + (size_t)(unit + s) * (kC * 32) + part * (kC * kPart / 4);
+        if (!cp.state_only && work_here > 0 && seg > 0) {                    // through the earlier segments
+            const float decay = exp2f((rev ? n - (chunks - first) * kC : first * kC) * lg);
+            const float4 *E = reinterpret_cast<const float4 *>(p.seg_state) + (size_t)(unit + seg - 1) * (kC * 32) + part * (kC * kPart / 4);
 #pragma unroll
-                for (int d = 0; d < kPart / 4; ++d) {
-                    const float4 u = E[d * 128 + e];
-                    Z[4 * d] = fmaf(decay, Z[4 * d], u.x);
-                    Z[4 * d + 1] = fmaf(decay, Z[4 * d + 1], u.y);
-                    Z[4 * d + 2] = fmaf(decay, Z[4 * d + 2], u.z);
-                    Z[4 * d + 3] = fmaf(decay, Z[4 * d + 3], u.w);
-                }
+            for (int d = 0; d < kPart / 4; ++d) {
+                const float4 u = E[d * 128 + e];
+                Z[4 * d] = fmaf(decay, Z[4 * d], u.x);
+                Z[4 * d + 1] = fmaf(decay, Z[4 * d + 1], u.y);
+                Z[4 * d + 2] = fmaf(decay, Z[4 * d + 2], u.z);
+                Z[4 * d + 3] = fmaf(decay, Z[4 * d + 3], u.w);
             }
+        }
         auto put_operand = [&]() {
 #pragma unroll
             for (int c = 0; c < kPart / 8; ++c)
@@ -360,64 +357,62 @@ __global__ void __launch_bounds__(kThreads, 1) linattn_chunk_kernel(const __grid
             fence_proxy_async();
             warp_arrive(z_full + part, lane);
         }
-        for (int k = 0; k < work_here && ok; ++k) {
-            const int L = length_of(first + k), j = e, terms = terms_of(first + k);
-            const uint32_t ph = k & 1;
-            // b~: this thread's step j, weighted, as bf16 terms: the first takes b's place once P is there, the others,
-            // formed meanwhile, those of a and the state once O2 is
-            if (!(ok = cp.state_only ? all_wait(full + (k & 1), k >> 1 & 1) && clear(k) : all_wait(p_full, ph))) break;
+        // b~ of the k-th chunk: this thread's step of it, weighted, as bf16 terms: the first takes b's place once P is there,
+        // the others, formed meanwhile, those of a and the state once O2 is (three terms: the second half of the
+        // pieces, whose terms the registers do not hold, behind that wait)
+        auto write_terms = [&](int k, auto terms_) {
+            constexpr int TERMS = decltype(terms_)::value;
+            constexpr int N = kPart / 8, BATCH = 4, HELD = TERMS == 3 ? N / 2 : N;     // pieces, those read and those held at once
+            const int L = length_of(first + k);
+            if (!(cp.state_only ? all_wait(full + (k & 1), k >> 1 & 1) && clear(k) : all_wait(p_full, k & 1))) return false;
             if (lane == 0) mbar_arrive(p_seen);
             unsigned char *a = smem + (k & 1) * kStage, *bb = a + kOperand;
-            const float wj = pw[j < L ? (rev ? j + 1 : L - 1 - j) : 0];
+            const float wj = pw[e < L ? (rev ? e + 1 : L - 1 - e) : 0];
             const bf16x2 w0 = __float2bfloat162_rn(wj), w1 = __float2bfloat162_rn(wj - __low2float(w0)),
-                                 w2 = __float2bfloat162_rn(wj - __low2float(w0) - __low2float(w1));
-            // (three terms: the second half of the pieces, whose terms the registers do not hold, behind that wait)
-            auto write_terms = [&](auto terms_) {
-                constexpr int TERMS = decltype(terms_)::value;
-                constexpr int N = kPart / 8, BATCH = 4, HELD = TERMS == 3 ? N / 2 : N;     // pieces, those read and those held at once
-                for (int h = 0; h < N; h += HELD) {
-                    const int first_piece = N * part + h;
-                    uint32_t t1[TERMS > 1 ? 4 * HELD : 1], t2[TERMS > 2 ? 4 * HELD : 1];
+                         w2 = __float2bfloat162_rn(wj - __low2float(w0) - __low2float(w1));
+            for (int h = 0; h < N; h += HELD) {
+                const int first_piece = N * part + h;
+                uint32_t t1[TERMS > 1 ? 4 * HELD : 1], t2[TERMS > 2 ? 4 * HELD : 1];
 #pragma unroll
-                    for (int c0 = 0; c0 < HELD; c0 += BATCH) {
-                        uint4 raw[BATCH];
+                for (int c0 = 0; c0 < HELD; c0 += BATCH) {
+                    uint4 raw[BATCH];
 #pragma unroll
-                        for (int c = 0; c < BATCH; ++c) {
-                            raw[c] = *piece_at(bb, j, first_piece + c0 + c);
-                            if (j >= L) raw[c] = make_uint4(0u, 0u, 0u, 0u);
-                        }
-#pragma unroll
-                        for (int c = 0; c < BATCH; ++c) {
-                            const uint32_t in[4] = {raw[c].x, raw[c].y, raw[c].z, raw[c].w};
-                            uint32_t t0[4];
-#pragma unroll
-                            for (int q = 0; q < 4; ++q) {
-                                const int at = 4 * (c0 + c) + q;
-                                if constexpr (TERMS == 1) t0[q] = weigh(in[q], wj);
-                                else split_product<TERMS == 3>(in[q], w0, w1, w2, t0[q], t1[at], t2[TERMS == 3 ? at : 0]);
-                            }
-                            *piece_at(bb, j, first_piece + c0 + c) = make_uint4(t0[0], t0[1], t0[2], t0[3]);
-                        }
+                    for (int c = 0; c < BATCH; ++c) {
+                        raw[c] = *piece_at(bb, e, first_piece + c0 + c);
+                        if (e >= L) raw[c] = make_uint4(0u, 0u, 0u, 0u);
                     }
-                    if constexpr (TERMS > 1) {
-                        if (h == 0 && !cp.state_only && !all_wait(o2_full, ph)) return false;
 #pragma unroll
-                        for (int c = 0; c < HELD; ++c) {
-                            *piece_at(a, j, first_piece + c) = make_uint4(t1[4 * c], t1[4 * c + 1], t1[4 * c + 2], t1[4 * c + 3]);
-                            if constexpr (TERMS > 2) *piece_at(zb, j, first_piece + c) = make_uint4(t2[4 * c], t2[4 * c + 1], t2[4 * c + 2], t2[4 * c + 3]);
+                    for (int c = 0; c < BATCH; ++c) {
+                        const uint32_t in[4] = {raw[c].x, raw[c].y, raw[c].z, raw[c].w};
+                        uint32_t t0[4];
+#pragma unroll
+                        for (int q = 0; q < 4; ++q) {
+                            const int at = 4 * (c0 + c) + q;
+                            if constexpr (TERMS == 1) t0[q] = weigh(in[q], wj);
+                            else split_product<TERMS == 3>(in[q], w0, w1, w2, t0[q], t1[at], t2[TERMS == 3 ? at : 0]);
                         }
+                        *piece_at(bb, e, first_piece + c0 + c) = make_uint4(t0[0], t0[1], t0[2], t0[3]);
                     }
                 }
-                return true;
-            };
-            ok = terms == 1 ? write_terms(std::integral_constant<int, 1>()) :
-                 terms == 2 ? write_terms(std::integral_constant<int, 2>()) : write_terms(std::integral_constant<int, 3>());
-            if (!ok) break;
+                if constexpr (TERMS > 1) {
+                    if (h == 0 && !cp.state_only && !all_wait(o2_full, k & 1)) return false;
+#pragma unroll
+                    for (int c = 0; c < HELD; ++c) {
+                        *piece_at(a, e, first_piece + c) = make_uint4(t1[4 * c], t1[4 * c + 1], t1[4 * c + 2], t1[4 * c + 3]);
+                        if constexpr (TERMS > 2) *piece_at(zb, e, first_piece + c) = make_uint4(t2[4 * c], t2[4 * c + 1], t2[4 * c + 2], t2[4 * c + 3]);
+                    }
+                }
+            }
             fence_proxy_async();
             warp_arrive(bt_full + part, lane);
-            if (!(ok = all_wait(u_full, ph))) break;
+            return true;
+        };
+        // the state behind the k-th chunk
+        auto add_u = [&](int k) {
+            if (!all_wait(u_full, k & 1)) return false;
             tc_fence_after();
-            const float2 decay = make_float2(pw[L], pw[L]);
+            const float gl = pw[length_of(first + k)];
+            const float2 decay = make_float2(gl, gl);
 #pragma unroll
             for (int c = 0; c < kPart; c += 32) {
                 float u[32];
@@ -431,16 +426,29 @@ __global__ void __launch_bounds__(kThreads, 1) linattn_chunk_kernel(const __grid
                 }
             }
             tc_fence_before();
-            if (k + 1 < work) {
+            return true;
+        };
+        for (int k = 0; k < work_here && ok; ++k) {
+            const int terms = terms_of(first + k);
+            // (without outputs one term is written under the last chunk's U; more take places that that may still read)
+            const bool ahead = cp.state_only && terms == 1;
+            if (ahead && !(ok = write_terms(k, std::integral_constant<int, 1>()))) break;
+            if (k > 0) {
+                if (!(ok = add_u(k - 1))) break;
                 if (!cp.state_only) {
-                    if (terms == 1 && !(ok = all_wait(o2_full, ph))) break;    // (the last state has been read)
+                    // (the last state has been read: by U of several terms already)
+                    if (terms_of(first + k - 1) == 1 && !(ok = all_wait(o2_full, (k - 1) & 1))) break;
                     put_operand();
-                    ok = clear(k + 1);
+                    ok = clear(k);
                     fence_proxy_async();
                 }
                 warp_arrive(z_full + part, lane);
             }
+            if (ahead || !ok) continue;
+            ok = terms == 1 ? write_terms(k, std::integral_constant<int, 1>()) :
+                 terms == 2 ? write_terms(k, std::integral_constant<int, 2>()) : write_terms(k, std::integral_constant<int, 3>());
         }
+        if (ok && work_here > 0) ok = add_u(work - 1);
         if (cp.state_only) {
             float4 *E = reinterpret_cast<float4 *>(p.seg_state) + (size_t)(unit + seg) * (kC * 32) + part * (kC * kPart / 4);
             if (work > 0)
@@ -557,20 +565,37 @@ __global__ void __launch_bounds__(kThreads, 1) linattn_chunk_kernel(const __grid
     if (warp == kFetchWarp) tmem_dealloc(tmem, 512);
 }
 
-// Segments of a row's chunks, where one CTA for each head and block of columns leaves SMs idle: as many as
-// fill them once.
-void linattn_segments(LinattnParams *p) {
+// What the segments up to each leave, from what each leaves: E_s += g^(steps of s) E_{s-1}. All segments here but the
+// first hold whole chunks only.
+__global__ void __launch_bounds__(256) linattn_join_kernel(const LinattnParams p) {
+    const int b = blockIdx.z, h = blockIdx.y, blocks = gridDim.x / 16, x = blockIdx.x / 16;
+    const int chunks = (row_length(p.lens, b, p.T) + kC - 1) / kC;
+    const float decay = exp2f(p.seg_chunks * kC * log2f(p.g[h]));
+    float4 *E = reinterpret_cast<float4 *>(p.seg_state) + ((size_t)(b * gridDim.y + h) * blocks + x) * (p.segs - 1) * (kC * 32) +
+                blockIdx.x % 16 * 256 + threadIdx.x;
+    float4 sum = make_float4(0.f, 0.f, 0.f, 0.f);
+    for (int s = 0; s < p.segs - 1 && (s + 1) * p.seg_chunks < chunks; ++s, E += kC * 32) {
+        const float4 u = *E;
+        sum = make_float4(fmaf(decay, sum.x, u.x), fmaf(decay, sum.y, u.y), fmaf(decay, sum.z, u.z), fmaf(decay, sum.w, u.w));
+        *E = sum;
+    }
+}
+
+static int sweep_blocks(const LinattnSweep &w) { return ((w.Db + 127) / 128) * ((w.Dc + 127) / 128); }
+
+// Segments of a row's chunks, where one CTA for each head and column block leaves SMs idle: as many as fill
+// them once.
+size_t linattn_segments(LinattnParams *p) {
     const int chunks = (p->T + kC - 1) / kC;
     long long ctas = 0;
-    for (int i = 0; i < p->sweeps; ++i) ctas += (long long)((p->sweep[i].Db + 127) / 128) * ((p->sweep[i].Dc + 127) / 128);
+    for (int i = 0; i < p->sweeps; ++i) ctas += sweep_blocks(p->sweep[i]);
     ctas *= (long long)p->B * p->Hv;
     long long segs = 152 / ctas;
     if (segs > chunks / 2) segs = chunks / 2;
-    if (segs > 32) segs = 32;
     if (segs < 2) segs = 1;
     p->seg_chunks = (int)((chunks + segs - 1) / segs);
     p->segs = (chunks + p->seg_chunks - 1) / p->seg_chunks;
-    p->seg_units = (size_t)ctas * (p->segs - 1);
+    return (size_t)ctas * (p->segs - 1);
 }
 
 cudaError_t launch_linattn_chunks(const LinattnParams &p, const LinattnMaps &maps, cudaStream_t s) {
@@ -579,25 +604,28 @@ cudaError_t launch_linattn_chunks(const LinattnParams &p, const LinattnMaps &map
     SweepArgs cp = {};
     cp.p = p;
     int blocks = 0;
-    for (int i = 0; i < p.sweeps; ++i) {
-        cp.blocks[i] = ((p.sweep[i].Db + 127) / 128) * ((p.sweep[i].Dc + 127) / 128);
-        blocks += cp.blocks[i];
-    }
+    for (int i = 0; i < p.sweeps; ++i) blocks += cp.blocks[i] = sweep_blocks(p.sweep[i]);
+    auto run = [&](const char *name, int segs) {
+        timing_mark(name, 0, s);
+        linattn_chunk_kernel<<<dim3(blocks * segs, p.Hv, p.B), kThreads, kSmem, s>>>(maps, cp);
+        const cudaError_t err = cudaGetLastError();
+        timing_mark(name, 1, s);
+        return err;
+    };
     if (p.segs > 1) {
         cp.state_only = 1;
-        timing_mark("linattn_states", 0, s);
-        linattn_chunk_kernel<<<dim3(blocks * (p.segs - 1), p.Hv, p.B), kThreads, kSmem, s>>>(maps, cp);
-        e = cudaGetLastError();
-        timing_mark("linattn_states", 1, s);
-        if (e != cudaSuccess) return e;
+        if ((e = run("linattn_states", p.segs - 1)) != cudaSuccess) return e;
         cp.state_only = 0;
     }
-    timing_mark("linattn_chunk", 0, s);
-    linattn_chunk_kernel<<<dim3(blocks * p.segs, p.Hv, p.B), kThreads, kSmem, s>>>(maps, cp);
-    e = cudaGetLastError();
-    timing_mark("linattn_chunk", 1, s);
-    if (e == cudaSuccess && p.sums > 0) e = launch_linattn_sums(p, 1, s);
-    return e;
+    if (p.segs > 2) {
+        timing_mark("linattn_join", 0, s);
+        linattn_join_kernel<<<dim3(blocks * 16, p.Hv, p.B), 256, 0, s>>>(p);
+        e = cudaGetLastError();
+        timing_mark("linattn_join", 1, s);
+        if (e != cudaSuccess) return e;
+    }
+    if ((e = run("linattn_chunk", p.segs)) != cudaSuccess) return e;
+    return p.sums > 0 ? launch_linattn_sums(p, 1, s) : cudaSuccess;
 }
 
 }  // namespace gdn

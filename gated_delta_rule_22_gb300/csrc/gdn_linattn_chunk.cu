@@ -39,7 +39,7 @@ constexpr int kC = kLinattnChunk;
 constexpr int kParts = 2, kPart = 128 / kParts;    // the state's columns by two groups of four warps
 constexpr int kOutWarp = 8, kStateWarp = 12, kFetchWarp = kStateWarp + 4 * kParts, kThreads = (kFetchWarp + 4) * 32;
 // registers of a thread: launched with kLaunchRegs, then dealt out again
-constexpr int kLaunchRegs = 80, kMaskRegs = 56, kOutRegs = 64, kStateRegs = 128, kIssueRegs = 48;
+constexpr int kLaunchRegs = 80, kMaskRegs = 64, kOutRegs = 64, kStateRegs = 120, kIssueRegs = 48;
 static_assert(2 * kMaskRegs + kOutRegs + kParts * kStateRegs + kIssueRegs <= kThreads / 128 * kLaunchRegs, "register split exceeds the launch's registers");
 constexpr int kTile = 64 * kC * 2;                 // 64 columns of a chunk: 128 rows of 128 bytes
 constexpr int kOperand = 2 * kTile;
@@ -76,8 +76,12 @@ __device__ __forceinline__ void warp_arrive(uint64_t *bar, int lane) {
     __syncwarp();
     if (lane == 0) mbar_arrive(bar);
 }
-// mbar_wait by a whole warp, with one answer
-__device__ __forceinline__ bool all_wait(uint64_t *bar, uint32_t parity) { return __all_sync(kFullMask, mbar_wait(bar, parity)); }
+// mbar_wait by a whole warp, with one answer, and together from there (tensor memory is read by whole warps)
+__device__ __forceinline__ bool all_wait(uint64_t *bar, uint32_t parity) {
+    const bool there = __all_sync(kFullMask, mbar_wait(bar, parity));
+    __syncwarp();
+    return there;
+}
 
 // 32 bytes of a row, at once where they are aligned to that (every lane has a row of its own, and a store of 32
 // rows takes a cycle for each)
@@ -192,6 +196,8 @@ __global__ void __launch_bounds__(kThreads, 1) linattn_chunk_kernel(const __grid
         const float weight = after == 0 ? 0.f : after * lg;                                  // (its log2)
         return w.last == nullptr ? 1 : weight >= -3.f ? 3 : weight >= -12.f ? 2 : 1;
     };
+    // Whether P~ has two: with b~ of one, and where P is a part of the products of a pair of steps, which may cancel
+    auto two_of = [&](int i) { return w.Db > 128 || terms_of(i) == 1; };
     const size_t out_step = (size_t)p.Hv * w.Dc;
     const size_t out0 = (size_t)(db0 / 128) * p.B * p.T * out_step + (size_t)b * p.T * out_step + (size_t)h * w.Dc + dc0;
     bool ok = true;
@@ -202,7 +208,7 @@ __global__ void __launch_bounds__(kThreads, 1) linattn_chunk_kernel(const __grid
         const uint32_t mine = tmem + ((uint32_t)(warp & 3) << 21) + kColP + 64 * part;
         for (int k = 0; k < work && !cp.state_only; ++k) {
             const int L = length_of(first + k);
-            const bool two = terms_of(first + k) == 1;
+            const bool two = two_of(first + k);
             if (!(ok = all_wait(p_full, k & 1))) break;
             tc_fence_after();
 #pragma unroll 1
@@ -280,19 +286,21 @@ __global__ void __launch_bounds__(kThreads, 1) linattn_chunk_kernel(const __grid
                     o1[r] = x.x;
                     o1[r + 1] = x.y;
                 }
-                if (i >= L) continue;
-                if (w.sums) {
-                    float *out = w.part + at + c;
-                    store_piece2(out, o1[0], o1[1], o1[2], o1[3], o1[4], o1[5], o1[6], o1[7], wide);
-                    if (c + 8 < Dc) store_piece2(out + 8, o1[8], o1[9], o1[10], o1[11], o1[12], o1[13], o1[14], o1[15], wide);
-                } else {
-                    __nv_bfloat16 *out = static_cast<__nv_bfloat16 *>(w.out) + at + c;
-                    float y[8];
+                if (i < L) {
+                    if (w.sums) {
+                        float *out = w.part + at + c;
+                        store_piece2(out, o1[0], o1[1], o1[2], o1[3], o1[4], o1[5], o1[6], o1[7], wide);
+                        if (c + 8 < Dc) store_piece2(out + 8, o1[8], o1[9], o1[10], o1[11], o1[12], o1[13], o1[14], o1[15], wide);
+                    } else {
+                        __nv_bfloat16 *out = static_cast<__nv_bfloat16 *>(w.out) + at + c;
+                        float y[8];
 #pragma unroll
-                    for (int r = 0; r < 8; ++r) y[r] = __uint_as_float(pack2_bf16(o1[2 * r], o1[2 * r + 1]));
-                    if (c + 8 < Dc) store_piece2(out, y[0], y[1], y[2], y[3], y[4], y[5], y[6], y[7], wide);
-                    else *reinterpret_cast<float4 *>(out) = make_float4(y[0], y[1], y[2], y[3]);
+                        for (int r = 0; r < 8; ++r) y[r] = __uint_as_float(pack2_bf16(o1[2 * r], o1[2 * r + 1]));
+                        if (c + 8 < Dc) store_piece2(out, y[0], y[1], y[2], y[3], y[4], y[5], y[6], y[7], wide);
+                        else *reinterpret_cast<float4 *>(out) = make_float4(y[0], y[1], y[2], y[3]);
+                    }
                 }
+                __syncwarp();                      // (the loads above are the whole warp's)
             }
             tc_fence_before();
             warp_arrive(o_empty, lane);
@@ -404,7 +412,6 @@ __global__ void __launch_bounds__(kThreads, 1) linattn_chunk_kernel(const __grid
                 }
             }
             fence_proxy_async();
-            warp_arrive(bt_full + part, lane);
             return true;
         };
         // the state behind the k-th chunk
@@ -433,6 +440,7 @@ __global__ void __launch_bounds__(kThreads, 1) linattn_chunk_kernel(const __grid
             // (without outputs one term is written under the last chunk's U; more take places that that may still read)
             const bool ahead = cp.state_only && terms == 1;
             if (ahead && !(ok = write_terms(k, std::integral_constant<int, 1>()))) break;
+            if (k == 0 && ahead) warp_arrive(bt_full + part, lane);
             if (k > 0) {
                 if (!(ok = add_u(k - 1))) break;
                 if (!cp.state_only) {
@@ -442,11 +450,15 @@ __global__ void __launch_bounds__(kThreads, 1) linattn_chunk_kernel(const __grid
                     ok = clear(k);
                     fence_proxy_async();
                 }
+                // (what was written ahead is announced here, when the last U has been issued: bt_full is never two phases
+                // ahead of the warp that waits for it)
+                if (ahead) warp_arrive(bt_full + part, lane);
                 warp_arrive(z_full + part, lane);
             }
             if (ahead || !ok) continue;
             ok = terms == 1 ? write_terms(k, std::integral_constant<int, 1>()) :
                  terms == 2 ? write_terms(k, std::integral_constant<int, 2>()) : write_terms(k, std::integral_constant<int, 3>());
+            warp_arrive(bt_full + part, lane);
         }
         if (ok && work_here > 0) ok = add_u(work - 1);
         if (cp.state_only) {
@@ -504,7 +516,7 @@ __global__ void __launch_bounds__(kThreads, 1) linattn_chunk_kernel(const __grid
                      (!(masked && length_of(first + k) < kC) || all_wait(o2_full, ph));           // (c is cleared by then)
                 if (!ok) break;
                 tc_fence_after();
-                const bool two = terms_of(first + k) == 1;
+                const bool two = two_of(first + k);
                 for (int term = two ? 1 : 0; term >= 0; --term) {            // smallest first
                     uint64_t cd = desc_mn(c);
 #pragma unroll

@@ -8,6 +8,8 @@ most 0.43 x 2^-8 sqrt(1 + 1 + 1) together, and twice that, 1.5 x 2^-8, where ter
 running value, of either sign, and the dot products' Dk: 2^-24 sqrt(2 n + D), up to some 2e-6 at n = 400.
 The float32 states of the chunked form hold 24 bits of k and the decay's powers (2 ulp of exp2 and log2, times
 the exponent): 2^-20 covers ages up to log2 = 8, beyond which nothing counts."""
+import random
+
 import pytest
 
 torch = pytest.importorskip("torch")
@@ -222,6 +224,34 @@ def test_the_forms_agree():
     y, S = gdn().gdn_linattn_fwd(a["q"], a["k"], a["v"], a["g"], a["S0"])
     y2, S2 = gdn().gdn_linattn_fwd(off["q"], off["k"], off["v"], off["g"], off["S0"])
     assert R.rel(y, y2) <= TOL[BF16] and R.rel(S, S2) <= TOL_STATE and not torch.equal(y, y2)
+
+
+def test_both_forms_on_many_shapes():
+    """Random sizes, lengths, decays and states, bf16, in chunks against step by step: tail chunks of every length
+    among them, rows behind which lies NaN, dims in one and two blocks, and no wait that runs out."""
+    rng = random.Random(5)
+    for _ in range(120):
+        B, Hk, group = rng.randint(1, 4), rng.randint(1, 3), rng.choice([1, 1, 2, 3])
+        dim = lambda: rng.choice([64, 128, 192, 256, 8 * rng.randint(1, 32)])  # noqa: E731
+        T = rng.choice([rng.randint(8, 140), rng.randint(120, 600), rng.randint(600, 1500)])
+        a = make(rng.randint(0, 10 ** 6), B, T, Hk, Hk * group, dim(), dim(), BF16, rng.choice(["mixed", "mixed", "one", "long", "tiny"]))
+        lens = None if rng.random() < 0.4 else torch.tensor([rng.randint(0, T) for _ in range(B)], device="cuda", dtype=torch.int32)
+        for b, n in enumerate([] if lens is None else lens.tolist()):
+            for t in ("q", "k", "v", "dy"):
+                a[t][b, n:] = float("nan")
+        off = dict(a)
+        for n in ("q", "k", "v"):
+            t = torch.zeros(B, T, a[n].shape[2] * a[n].shape[3] + 1, device="cuda", dtype=BF16)
+            off[n] = t[..., 1:].unflatten(-1, a[n].shape[2:]).copy_(a[n])
+        S0, dS_T = (a["S0"], a["dS_T"]) if rng.random() < 0.5 else (None, None)
+        run = lambda s: dict(zip(("y", "S_T"), gdn().gdn_linattn_fwd(s["q"], s["k"], s["v"], s["g"], S0, lens)),  # noqa: E731
+                             **gdn().gdn_linattn_bwd(s["q"], s["k"], s["v"], s["g"], s["dy"], S0, lens, dS_T))
+        mine, other = run(a), run(off)
+        torch.cuda.synchronize()
+        assert gdn().gdn_device_status() == 0
+        for n, x in mine.items():
+            tol = TOL_STATE if n in ("S_T", "dS0") else 2 ** -8 + TOL[BF16]       # (both round their outputs)
+            assert R.rel(x, other[n]) <= tol, (n, a["q"].shape, a["v"].shape, lens, R.rel(x, other[n]))
 
 
 def test_two_streams_at_once():

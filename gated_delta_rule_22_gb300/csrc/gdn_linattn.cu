@@ -7,6 +7,10 @@
 //
 // Forward and gradients are the same sweep (LinattnSweep in gdn_layer.cuh) over other operands, so that one
 // kernel computes them all.
+//
+// Measured: one step of 64 rows of 32 heads of 128 x 128, 43 us, 6.2 TB/s of state. Step by step in float32, 8 x 1024
+// steps of 32 heads of 128 x 128: 856 us, 20 TFLOP/s of the two products of a step; 1 x 1024 steps of 8 heads
+// 142 us, 140 ns a step: latency of its sums over lanes.
 #include "gdn_layer.cuh"
 
 namespace gdn {

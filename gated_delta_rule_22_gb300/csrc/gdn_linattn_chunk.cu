@@ -25,6 +25,12 @@
 //
 // Warps 0-7 mask P, warps 8-11 write outputs, warps 12-19 hold the state (each four half of its columns); one warp
 // fetches (two chunks deep), two issue products: P and O1, and O2 and U, so that neither chain waits for the other.
+//
+// Bound by latency: a chunk takes some 6500 cycles, 3.4 us (its tensor products 2600), the loop of P, its mask and
+// O1 in one place of tensor memory, and the chain of b~, U and the state beside it; where the state leaves the
+// call and b~ has several terms, up to 9000. What carries the loops: code short enough for the instruction cache,
+// one arrival per warp, work of one kind in each warp. 4 x 4096 steps of 32 heads of 128 x 128: forward 128 us,
+// 4.2 TB/s of q, k, v and y, backward 357 us, 2.6 TB/s; 4 x 2048 with 16 key heads and a carried state 75 us.
 #include "gdn.h"
 #include "gdn_layer.cuh"
 #include "gdn_umma.cuh"

@@ -119,19 +119,26 @@ struct RowLane {
     }
 };
 
-// What a thread reads of the next rows, on its way through shared memory: kAhead rows of N tensors, 16 bytes for
-// each piece. Rows that are not in pieces of 16 bytes are loaded when they are used.
+template <int BYTES>
+__device__ __forceinline__ void copy_async(void *dst, const void *src) {
+    if constexpr (BYTES == 16) cp_async16(dst, src, 16);
+    else asm volatile("cp.async.ca.shared.global [%0], [%1], %2;" ::"r"(smem_addr(dst)), "l"(src), "n"(BYTES) : "memory");
+}
+
+// What a thread reads of the next rows, on its way through shared memory: kAhead rows of N tensors, in pieces of
+// 16, 8 or 4 bytes. Rows whose pieces are smaller are loaded when they are used.
 template <typename Lane, typename T, int V, int IT, int N>
 struct RowRing {
-    static constexpr bool kRing = V * (int)sizeof(T) == 16 && (size_t)Lane::kThreads * N * IT * 16 * 2 <= 200 * 1024;
-    static constexpr size_t kSlot = (size_t)Lane::kThreads * N * IT * 16;     // bytes of a row of the CTA
+    static constexpr int kPiece = V * (int)sizeof(T);
+    static constexpr bool kRing = kPiece >= 4 && (size_t)Lane::kThreads * N * IT * kPiece * 2 <= 200 * 1024;
+    static constexpr size_t kSlot = (size_t)Lane::kThreads * N * IT * kPiece;     // bytes of a row of the CTA
     static constexpr int kAhead = !kRing ? 1 : kSlot * 4 <= 88 * 1024 ? 4 : kSlot * 3 <= 100 * 1024 ? 3 : 2;
     static constexpr size_t kBytes = kRing ? kSlot * kAhead : 0;
     unsigned char *base;
     int put = 0, take = 0;
-    __device__ __forceinline__ explicit RowRing(unsigned char *smem) : base(smem + threadIdx.x * 16) {}
+    __device__ __forceinline__ explicit RowRing(unsigned char *smem) : base(smem + threadIdx.x * kPiece) {}
     __device__ __forceinline__ unsigned char *at(int slot, int t, int i) const {
-        return base + ((size_t)(slot * N + t) * IT + i) * Lane::kThreads * 16;
+        return base + ((size_t)(slot * N + t) * IT + i) * Lane::kThreads * kPiece;
     }
     // starts the copies of a row (in: there is one), tensor t's from src[t], null where it is not there
     __device__ __forceinline__ void fetch(const Lane &lane, const T *const (&src)[N], bool in) {
@@ -141,7 +148,7 @@ struct RowRing {
                 if (in && src[t] != nullptr)
 #pragma unroll
                     for (int i = 0; i < IT; ++i)
-                        if (lane.ok(i)) cp_async16(at(put, t, i), src[t] + lane.col(i), 16);
+                        if (lane.ok(i)) copy_async<kPiece>(at(put, t, i), src[t] + lane.col(i));
             cp_async_commit();
             put = put + 1 == kAhead ? 0 : put + 1;
         }
@@ -442,12 +449,13 @@ void resnorm_units(ResnormParams *p, int dtype) {
     p->ctas = p->units < target ? p->units : target;
 }
 
-// f(kernel parameters as types): the form for D channels of a type, in 16-byte pieces or one by one
+// f(kernel parameters as types): the form for D channels of a type, in pieces of `width` of them (16 bytes, two or one).
+// 999 x 1030 in float32 with a gate, in pairs and one by one: forward 11 and 15 us, backward 17 and 28.
 template <typename T, typename F>
-static cudaError_t with_row(int D, bool vec, F f) {
+static cudaError_t with_row(int D, int width, F f) {
     constexpr int V = 16 / (int)sizeof(T), W = 8 / V;      // W: pieces of eight channels
 #define GDN_ROW(V_, LPR_, IT_) return f(std::integral_constant<int, V_>(), std::integral_constant<int, LPR_>(), std::integral_constant<int, IT_>())
-    if (vec) {
+    if (width == V) {
         if (D <= 64) GDN_ROW(V, 8, W);
         if (D <= 256) GDN_ROW(V, 32, W);
         if (D <= 512) GDN_ROW(V, 32, 2 * W);
@@ -457,6 +465,13 @@ static cudaError_t with_row(int D, bool vec, F f) {
         if (D <= 8192) GDN_ROW(V, 512, 2 * W);
         GDN_ROW(V, 1024, 2 * W);
     }
+    if (width == 2) {
+        if (D <= 256) GDN_ROW(2, 32, 4);
+        if (D <= 1024) GDN_ROW(2, 128, 4);
+        if (D <= 2048) GDN_ROW(2, 256, 4);
+        if (D <= 4096) GDN_ROW(2, 512, 4);
+        GDN_ROW(2, 1024, 8);
+    }
     if (D <= 256) GDN_ROW(1, 32, 8);
     if (D <= 1024) GDN_ROW(1, 128, 8);
     if (D <= 4096) GDN_ROW(1, 512, 8);
@@ -464,19 +479,21 @@ static cudaError_t with_row(int D, bool vec, F f) {
 #undef GDN_ROW
 }
 
-static bool whole(const void *p, int bytes) { return p == nullptr || ((uintptr_t)p & (bytes - 1)) == 0; }
-
-// 16-byte pieces of every row: D and the row strides multiples of a piece, the addresses aligned to it
+// Channels of a piece of every row: D and the row strides multiples of it, the addresses aligned to it
 template <typename T>
-static bool rows_vec(const ResnormParams &p) {
-    constexpr int V = 16 / (int)sizeof(T);
-    return p.D % V == 0 && p.ldx % V == 0 && p.ldh % V == 0 && (p.z == nullptr || p.ldz % V == 0) && whole(p.x, 16) && whole(p.h, 16) &&
-           whole(p.z, 16);
+static int rows_width(const ResnormParams &p) {
+    for (int v : {16 / (int)sizeof(T), 2}) {
+        const uintptr_t bytes = v * sizeof(T);
+        if (p.D % v == 0 && p.ldx % v == 0 && p.ldh % v == 0 && (p.z == nullptr || p.ldz % v == 0) &&
+            (((uintptr_t)p.x | (uintptr_t)p.h | (uintptr_t)p.z) & (bytes - 1)) == 0)
+            return v;
+    }
+    return 1;
 }
 
 template <typename T>
 static cudaError_t launch_fwd_t(const ResnormParams &p, cudaStream_t s) {
-    return with_row<T>(p.D, rows_vec<T>(p), [&](auto v, auto lpr, auto it) {
+    return with_row<T>(p.D, rows_width<T>(p), [&](auto v, auto lpr, auto it) {
         constexpr int V = decltype(v)::value, LPR = decltype(lpr)::value, IT = decltype(it)::value;
         using Lane = RowLane<T, V, LPR, IT>;
         using Ring = RowRing<Lane, T, V, IT, 3>;
@@ -491,7 +508,7 @@ static cudaError_t launch_fwd_t(const ResnormParams &p, cudaStream_t s) {
 template <typename T>
 static cudaError_t launch_bwd_t(const ResnormParams &p, cudaStream_t s) {
     timing_mark("resnorm_bwd", 0, s);
-    cudaError_t e = with_row<T>(p.D, rows_vec<T>(p), [&](auto v, auto lpr, auto it) {
+    cudaError_t e = with_row<T>(p.D, rows_width<T>(p), [&](auto v, auto lpr, auto it) {
         constexpr int V = decltype(v)::value, LPR = decltype(lpr)::value, IT = decltype(it)::value;
         using Lane = RowLane<T, V, LPR, IT>;
         using Ring = RowRing<Lane, T, V, IT, 5>;

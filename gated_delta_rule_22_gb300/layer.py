@@ -9,6 +9,7 @@ call under torch.cuda.stream(s).
 from __future__ import annotations
 
 import ctypes
+from functools import lru_cache
 
 import torch
 
@@ -167,6 +168,10 @@ def _raise(name, rc):
 _empty, _empty_like, _byref = torch.empty, torch.empty_like, ctypes.byref
 _current_device, _raw_stream = torch._C._cuda_getDevice, torch._C._cuda_getCurrentRawStream
 _BF16, _F32, _I32 = torch.bfloat16, torch.float32, torch.int32
+
+
+# A shape structure holds sizes alone, which a program repeats; the library only reads it.
+_linattn_shape, _resnorm_shape = lru_cache(256)(GdnLinattnShape), lru_cache(256)(GdnResnormShape)
 
 
 def _new_like(t):
@@ -511,7 +516,7 @@ def _linattn_args(q, k, v, g, S0, lens):
         _check("S0", S0, (B, Hv, Dv, Dk), _F32, dev)
     if lens is not None:
         _check("lens", lens, (B,), _I32, dev)
-    return GdnLinattnShape(B, T, Hk, Hv, Dk, Dv, _type(q), ldq, ldk, ldv), B, T, Hv, Dk, Dv
+    return _linattn_shape(B, T, Hk, Hv, Dk, Dv, _type(q), ldq, ldk, ldv), B, T, Hv, Dk, Dv
 
 
 def gdn_linattn_fwd_workspace_bytes(shape: GdnLinattnShape) -> int:
@@ -597,7 +602,7 @@ def _resnorm_args(x, h, z, scale, w_post, w_pre, post, pre, act, eps):
         if not pre:
             raise ValueError("w_pre is given, but its norm is off")
         _check("w_pre", w_pre, (D,), _F32, dev)
-    return GdnResnormShape(rows, D, gate_rows, _act(act), 1 if post else 0, 1 if pre else 0, _type(x), eps, ldx, ldh, ldz)
+    return _resnorm_shape(rows, D, gate_rows, _act(act), 1 if post else 0, 1 if pre else 0, _type(x), eps, ldx, ldh, ldz)
 
 
 def gdn_resnorm_fwd(x, h, z=None, scale=None, w_post=None, w_pre=None, *, post=True, pre=True, act="none", eps=1e-5, r=None, y=None,

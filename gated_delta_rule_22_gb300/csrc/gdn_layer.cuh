@@ -85,20 +85,31 @@ struct LinattnSweep {
     float *last;               // the state behind the last (rev: decayed once more); null: not wanted
     void *out;                 // [B][T][heads][Dc] in the call's type, the heads those of c
     float *part;               // (sums) float32 outputs by value head instead, [blocks of Db][B][T][Hv][Dc], to be added
+                               // or written to rows that are no multiples of 8
     long long lda, ldb, ldc;   // elements between steps
     int a_keys, b_keys, c_keys;   // the operand's heads are key heads
     int Db, Dc, rev;
     int init_t;                // init lies transposed, [Db][Dc]
     int sums;                  // out is formed from part (LinattnSum)
     int a_map, b_map, c_map;   // tensor maps of the operands
+    int Db_of, Dc_of;          // the dims of init, last and out: Db and Dc, which the chunked form pads to multiples of 8
+    float *states;             // step by step: what the segments up to each but the last leave, [segs - 1][B][Hv][Dc][Db]
 };
 
 // A sweep's outputs from its float32 ones: the sum over `planes` and `group` value heads, in ascending order.
 struct LinattnSum {
-    const float *part;         // [planes][B][T][heads][group][D]
+    const float *part;         // [planes][B][T][heads][group][pitch]
     void *out;                 // [B][T][heads][D]
     size_t plane;
-    int planes, group, heads, D;
+    int planes, group, heads, D, pitch;
+};
+
+// A bf16 operand that TMA cannot read (rows or strides that are no multiples of 8), copied to rows padded with zeros.
+struct LinattnCopy {
+    const void *in;            // [B][T][H][D], ld elements between steps
+    void *out;                 // [B][T][H][pitch]
+    long long ld;
+    int H, D, pitch;
 };
 
 struct LinattnMaps { CUtensorMap map[4]; };   // q, k, v, dy
@@ -106,18 +117,21 @@ struct LinattnMaps { CUtensorMap map[4]; };   // q, k, v, dy
 struct LinattnParams {
     LinattnSweep sweep[3];
     LinattnSum sum[3];
-    int sweeps, sums;
+    LinattnCopy copy[4];
+    int sweeps, sums, copies;
     const float *g;
     const int *lens;
     int *status;
     int B, T, Hk, Hv, Dk, Dv;
-    // chunked form: each row's chunks are taken in `segs` segments of seg_chunks; seg_state holds what the segments up to
-    // each but the last leave, from a zero state: [CTAs / segs][segs - 1][128][128]
+    // A row is taken in `segs` segments of seg_chunks chunks (step by step: of seg_chunks tiles of kLinattnTile steps).
+    // seg_state: chunked form, what the segments up to each but the last leave, from a zero state: [CTAs /
+    // segs][segs - 1][128][128]
     int segs, seg_chunks;
     float *seg_state;
 };
 
 constexpr int kLinattnChunk = 128;   // steps of a chunk
+constexpr int kLinattnTile = 16;     // steps staged at once, step by step
 
 struct ResnormParams {
     const void *x, *h, *z, *dy, *dr;
@@ -155,7 +169,9 @@ cudaError_t launch_norm_bwd(const NormParams &p, int dtype, cudaStream_t s);
 cudaError_t launch_linattn_step(const LinattnParams &p, int dtype, cudaStream_t s);    // T = 1, the forward's sweep
 cudaError_t launch_linattn_steps(const LinattnParams &p, int dtype, cudaStream_t s);   // all sweeps, then their sums
 size_t linattn_segments(LinattnParams *p);                                             // chooses segs and seg_chunks; the states of seg_state
+void linattn_step_segments(LinattnParams *p);                                          // the same, step by step
 cudaError_t launch_linattn_chunks(const LinattnParams &p, const LinattnMaps &maps, cudaStream_t s);
+cudaError_t launch_linattn_copies(const LinattnParams &p, cudaStream_t s);
 cudaError_t launch_linattn_sums(const LinattnParams &p, int dtype, cudaStream_t s);
 cudaError_t launch_resnorm_fwd(const ResnormParams &p, int dtype, cudaStream_t s);
 cudaError_t launch_resnorm_bwd(const ResnormParams &p, int dtype, cudaStream_t s);

@@ -154,11 +154,20 @@ int linattn_plan(const gdn_linattn_shape *s, gdn::LinattnParams *p, long long (&
     return GDN_OK;
 }
 
-// Whether the chunked form takes these sizes: bf16 rows that TMA can read, and more than a few steps (64 rows of 32
-// heads of 128 x 128, forward and backward: 8 steps 197 and 395 us in chunks, 168 and 477 step by step; 4 steps
-// 196 and 392 us, 151 and 402; 16 steps 198 and 400 us, 230 and 666).
+int up8(int n) { return (n + 7) / 8 * 8; }
+
+// Whether TMA can read rows of heads of D channels, ld elements between steps.
+bool tma_rows(int D, long long ld) { return D % 8 == 0 && ld % 8 == 0; }
+
+// Whether the chunked form takes these sizes: bf16, and more than a few steps (64 rows of 32 heads of 128 x 128,
+// forward and backward: 8 steps 197 and 395 us in chunks, 168 and 477 step by step; 4 steps 196 and 392 us, 151 and 402;
+// 16 steps 198 and 400 us, 230 and 666), more of them where operands have to be copied first (in chunks against step by
+// step: 16 rows of 32 heads of 100 x 100, backward: 32 steps 131 and 222 us, 64 steps 148 and 391; 2 rows of 8 heads of
+// 40 x 75: 64 steps 15 and 15 us, 128 steps 15 and 28; 1 row of 8 heads of 75 x 100, forward: 64 steps 18 and 14 us,
+// 128 steps 19 and 22).
 bool linattn_chunks(const gdn::LinattnParams &p, int dtype, const long long (&ld)[3]) {
-    return dtype == GDN_BF16 && p.T >= 8 && p.Dk % 8 == 0 && p.Dv % 8 == 0 && ld[0] % 8 == 0 && ld[1] % 8 == 0 && ld[2] % 8 == 0;
+    const bool rows = tma_rows(p.Dk, ld[0]) && tma_rows(p.Dk, ld[1]) && tma_rows(p.Dv, ld[2]);
+    return dtype == GDN_BF16 && p.T >= (rows ? 8 : 64);
 }
 
 // The call's sweeps, with the float32 outputs and segment states that they need placed in `ws`; returns the bytes
@@ -184,18 +193,39 @@ size_t linattn_sweeps(gdn::LinattnParams *p, const LinattnIo &io, const long lon
     p->sums = 0;
     for (int i = 0; i < p->sweeps; ++i) {
         gdn::LinattnSweep &w = p->sweep[i];
+        w.Db_of = w.Db;
+        w.Dc_of = w.Dc;
+        if (chunks) {
+            w.Db = up8(w.Db);
+            w.Dc = up8(w.Dc);
+        }
         const int planes = chunks ? (w.Db + 127) / 128 : 1, group = w.c_keys ? p->Hv / p->Hk : 1;
-        if (planes * group == 1) continue;
+        if (planes * group == 1 && w.Dc == w.Dc_of) continue;
         const size_t plane = (size_t)p->B * p->T * p->Hv * w.Dc;
         w.sums = 1;
         w.part = reinterpret_cast<float *>(ws + used);
-        p->sum[p->sums++] = {w.part, w.out, plane, planes, group, p->Hv / group, w.Dc};
+        p->sum[p->sums++] = {w.part, w.out, plane, planes, group, p->Hv / group, w.Dc_of, w.Dc};
         used += up256(planes * plane * 4);
     }
+    p->copies = 0;
     if (chunks) {
+        const gdn::LinattnCopy operands[4] = {{io.q, nullptr, ld[0], p->Hk, p->Dk, up8(p->Dk)}, {io.k, nullptr, ld[1], p->Hk, p->Dk, up8(p->Dk)},
+                                              {io.v, nullptr, ld[2], p->Hv, p->Dv, up8(p->Dv)}, {io.dy, nullptr, ldy, p->Hv, p->Dv, up8(p->Dv)}};
+        for (int i = 0; i < (bwd ? 4 : 3); ++i) {
+            if (tma_rows(operands[i].D, operands[i].ld)) continue;
+            gdn::LinattnCopy &c = p->copy[p->copies++] = operands[i];
+            c.out = ws + used;
+            used += up256((size_t)p->B * p->T * c.H * c.pitch * 2);
+        }
         const size_t states = gdn::linattn_segments(p);
         p->seg_state = reinterpret_cast<float *>(ws + used);
         used += up256(states * gdn::kLinattnChunk * 128 * 4);
+    } else {
+        gdn::linattn_step_segments(p);
+        for (int i = 0; i < p->sweeps; ++i) {
+            p->sweep[i].states = reinterpret_cast<float *>(ws + used);
+            used += up256((size_t)(p->segs - 1) * p->B * p->Hv * p->Dk * p->Dv * 4);
+        }
     }
     return used;
 }
@@ -205,17 +235,28 @@ size_t linattn_ws(gdn::LinattnParams p, int dtype, const long long (&ld)[3], boo
     return steps > chunks ? steps : chunks;
 }
 int linattn_run(gdn::LinattnParams *p, const LinattnIo &io, int dtype, const long long (&ld)[3], bool bwd, void *ws, cudaStream_t s) {
-    const bool chunks = linattn_chunks(*p, dtype, ld) && aligned16(io.q) && aligned16(io.k) && aligned16(io.v);
+    // (an operand that is read in place is aligned to 16 bytes, or the call goes step by step)
+    const bool there = (!tma_rows(p->Dk, ld[0]) || aligned16(io.q)) && (!tma_rows(p->Dk, ld[1]) || aligned16(io.k)) &&
+                       (!tma_rows(p->Dv, ld[2]) || aligned16(io.v));
+    const bool chunks = linattn_chunks(*p, dtype, ld) && there;
     linattn_sweeps(p, io, ld, bwd, chunks, static_cast<char *>(ws));
     if (!chunks) return gdn::api_cuda_status(gdn::launch_linattn_steps(*p, dtype, s));
     gdn::LinattnMaps maps = {};
     int rc;
-    if ((rc = gdn::api_device_status_address(&p->status)) != GDN_OK ||
-        (rc = gdn::api_heads_map(&maps.map[0], io.q, p->B, p->T, p->Hk, p->Dk, ld[0], gdn::kLinattnChunk)) != GDN_OK ||
-        (rc = gdn::api_heads_map(&maps.map[1], io.k, p->B, p->T, p->Hk, p->Dk, ld[1], gdn::kLinattnChunk)) != GDN_OK ||
-        (rc = gdn::api_heads_map(&maps.map[2], io.v, p->B, p->T, p->Hv, p->Dv, ld[2], gdn::kLinattnChunk)) != GDN_OK ||
-        (bwd && (rc = gdn::api_heads_map(&maps.map[3], io.dy, p->B, p->T, p->Hv, p->Dv, (long long)p->Hv * p->Dv, gdn::kLinattnChunk)) != GDN_OK))
-        return rc;
+    if ((rc = gdn::api_device_status_address(&p->status)) != GDN_OK) return rc;
+    const void *operands[4] = {io.q, io.k, io.v, io.dy};
+    const long long lds[4] = {ld[0], ld[1], ld[2], (long long)p->Hv * p->Dv};
+    for (int i = 0, copy = 0; i < (bwd ? 4 : 3); ++i) {
+        const int H = i < 2 ? p->Hk : p->Hv, D = i < 2 ? p->Dk : p->Dv;
+        const bool copied = !tma_rows(D, lds[i]);
+        const void *at = copied ? p->copy[copy++].out : operands[i];
+        if ((rc = gdn::api_heads_map(&maps.map[i], at, p->B, p->T, H, up8(D), copied ? (long long)H * up8(D) : lds[i], gdn::kLinattnChunk)) != GDN_OK)
+            return rc;
+    }
+    if (p->copies > 0) {
+        const cudaError_t e = gdn::launch_linattn_copies(*p, s);
+        if (e != cudaSuccess) return gdn::api_cuda_status(e);
+    }
     return gdn::api_cuda_status(gdn::launch_linattn_chunks(*p, maps, s));
 }
 

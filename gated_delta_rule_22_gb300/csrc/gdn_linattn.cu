@@ -1,6 +1,6 @@
 // gdn_linattn.cu -- linear attention with a constant decay for each value head: the single step, the
-// step-by-step form of prompts and gradients (float32, and bf16 that TMA cannot read), and the sums of sweeps'
-// float32 outputs. (gdn_linattn_chunk.cu holds the chunked form.)
+// step-by-step form of prompts and gradients (float32; bf16 of a few steps or at unaligned addresses), the sums of
+// sweeps' float32 outputs, and copies that TMA can read. (gdn_linattn_chunk.cu holds the chunked form.)
 //
 //     S_t = g S_{t-1} + v_t k_t^T,   y_t = S_t q_t
 //     dq_t = S_t^T dy_t;   R_t = g R_{t+1} + dy_t q_t^T,   dk_t = R_t^T v_t,   dv_t = R_t k_t,   dS0 = g R_0
@@ -9,8 +9,8 @@
 // kernel computes them all.
 //
 // Measured: one step of 64 rows of 32 heads of 128 x 128, 43 us, 6.2 TB/s of state. Step by step in float32, 8 x 1024
-// steps of 32 heads of 128 x 128: 856 us, 20 TFLOP/s of the two products of a step; 1 x 1024 steps of 8 heads
-// 142 us, 140 ns a step: latency of its sums over lanes.
+// steps of 32 heads of 128 x 128: 860 to 890 us, 19 TFLOP/s of the two products of a step. Few rows are bound by the latency
+// of a step's sums over lanes, 135 ns: 1 x 1024 steps of 8 heads 136 us, in segments 75.
 #include "gdn_layer.cuh"
 
 namespace gdn {
@@ -20,7 +20,7 @@ namespace {
 constexpr int kStepThreads = 256;
 constexpr int kStepRowsPerThread = 4;
 
-constexpr int kWalkTile = 16;                           // steps staged at once
+constexpr int kWalkTile = kLinattnTile;                 // steps staged at once
 
 constexpr int kSumThreads = 256;
 
@@ -98,7 +98,8 @@ __global__ void __launch_bounds__(kStepThreads) linattn_step_kernel(const Linatt
 // head and batch row and stages some steps of a, b and c in shared memory as float32, the next tile's
 // elements in registers meanwhile. A step is three packed instructions per pair of state elements; the outputs
 // of four steps are summed over the lanes together, 31 shuffles in five rounds.
-template <typename T, int E2, int WARPS, int ROWS>
+// STATE: the segments' end states from zero, nothing else.
+template <typename T, int E2, int WARPS, int ROWS, bool STATE>
 __global__ void __launch_bounds__(32 * WARPS) linattn_walk_kernel(const LinattnParams p, int blocks0, int blocks1) {
     constexpr int W = 64 * E2;                          // staged columns of a and b
     constexpr int kWalkThreads = 32 * WARPS, kWalkBlock = WARPS * ROWS;     // threads, state rows of a CTA
@@ -106,9 +107,11 @@ __global__ void __launch_bounds__(32 * WARPS) linattn_walk_kernel(const LinattnP
     constexpr int LA = kWalkTile * W / kWalkThreads, LC = kWalkTile * kWalkBlock / kWalkThreads;
     __shared__ __align__(16) float sa[kWalkTile][W], sb[kWalkTile][W], sc[kWalkTile][kWalkBlock];
     const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
-    const int which = (int)blockIdx.x < blocks0 ? 0 : (int)blockIdx.x < blocks0 + blocks1 ? 1 : 2;
+    constexpr bool SEGMENTS = WARPS == 4;               // (the large CTAs take whole rows)
+    const int segs = !SEGMENTS ? 1 : STATE ? p.segs - 1 : p.segs, seg = SEGMENTS ? blockIdx.x % segs : 0, x = SEGMENTS ? blockIdx.x / segs : blockIdx.x;
+    const int which = x < blocks0 ? 0 : x < blocks0 + blocks1 ? 1 : 2;
     const LinattnSweep &w = p.sweep[which];
-    const int block = blockIdx.x - (which == 0 ? 0 : which == 1 ? blocks0 : blocks0 + blocks1);
+    const int block = x - (which == 0 ? 0 : which == 1 ? blocks0 : blocks0 + blocks1);
     const int h = blockIdx.y, b = blockIdx.z, hk = h / (p.Hv / p.Hk), T_ = p.T;
     const int Db = w.Db, Dc = w.Dc, e0 = block * kWalkBlock, row0 = e0 + warp * ROWS;
     const int n = row_length(p.lens, b, T_);
@@ -125,10 +128,18 @@ __global__ void __launch_bounds__(32 * WARPS) linattn_walk_kernel(const LinattnP
     };
     auto inside = [&](int r, int m, int i) { return row0 + r < Dc && 2 * lane + 64 * m + i < Db; };
     const bool pairs = !w.init_t && Db % 2 == 0;        // of a row's elements in init and last, aligned to 8 bytes
+    const int tiles = (n + kWalkTile - 1) / kWalkTile;
+    const int first_tile = SEGMENTS ? seg * p.seg_chunks : 0;                                       // in the order of the sweep
+    const int last_tile = SEGMENTS ? min(first_tile + p.seg_chunks, tiles) : tiles;
+    if (STATE && last_tile >= tiles) return;            // (nothing follows)
 #pragma unroll
     for (int r = 0; r < ROWS; ++r)
 #pragma unroll
         for (int m = 0; m < E2; ++m) {
+            if (STATE) {
+                s[r][m] = make_float2(0.f, 0.f);
+                continue;
+            }
             if (pairs) {
                 s[r][m] = w.init != nullptr && inside(r, m, 0) ? *reinterpret_cast<const float2 *>(w.init + place(r, m, 0)) : make_float2(0.f, 0.f);
                 continue;
@@ -136,7 +147,20 @@ __global__ void __launch_bounds__(32 * WARPS) linattn_walk_kernel(const LinattnP
             s[r][m].x = w.init != nullptr && inside(r, m, 0) ? w.init[place(r, m, 0)] : 0.f;
             s[r][m].y = w.init != nullptr && inside(r, m, 1) ? w.init[place(r, m, 1)] : 0.f;
         }
-    const int tiles = (n + kWalkTile - 1) / kWalkTile;
+    auto state_at = [&](int of, int r, int m, int i) -> float & {          // of the state behind segment `of`
+        return w.states[(((size_t)of * p.B + b) * p.Hv + h) * Dc * Db + (size_t)(row0 + r) * Db + 2 * lane + 64 * m + i];
+    };
+    if (SEGMENTS && !STATE && seg > 0 && first_tile < tiles) {      // through the earlier segments
+        const int before = w.rev ? n - (tiles - first_tile) * kWalkTile - 1 : first_tile * kWalkTile;
+        const float decay = exp2f(before == 0 ? 0.f : before * log2f(g));
+#pragma unroll
+        for (int r = 0; r < ROWS; ++r)
+#pragma unroll
+            for (int m = 0; m < E2; ++m) {
+                if (inside(r, m, 0)) s[r][m].x = fmaf(decay, s[r][m].x, state_at(seg - 1, r, m, 0));
+                if (inside(r, m, 1)) s[r][m].y = fmaf(decay, s[r][m].y, state_at(seg - 1, r, m, 1));
+            }
+    }
     T ra[LA], rb[LA], rc[LC];
     auto fetch = [&](int tile) {
         const int t0 = tile * kWalkTile;
@@ -144,7 +168,7 @@ __global__ void __launch_bounds__(32 * WARPS) linattn_walk_kernel(const LinattnP
         for (int i = 0; i < LA; ++i) {
             const int t = t0 + (tid + i * kWalkThreads) / W, col = (tid + i * kWalkThreads) % W;
             const bool ok = t < n && col < Db;
-            ra[i] = ok ? a_[(size_t)t * w.lda + col] : from_f32<T>(0.f);
+            if (!STATE) ra[i] = ok ? a_[(size_t)t * w.lda + col] : from_f32<T>(0.f);
             rb[i] = ok ? b_[(size_t)t * w.ldb + col] : from_f32<T>(0.f);
         }
 #pragma unroll
@@ -161,15 +185,15 @@ __global__ void __launch_bounds__(32 * WARPS) linattn_walk_kernel(const LinattnP
         if (w.sums) w.part[at] = x;
         else static_cast<T *>(w.out)[at] = from_f32<T>(x);
     };
-    if (tiles > 0) fetch(w.rev ? tiles - 1 : 0);
-    bool first = w.rev != 0;                            // backwards the first step does not decay the state
-    for (int it = 0; it < tiles; ++it) {
+    if (first_tile < last_tile) fetch(w.rev ? tiles - 1 - first_tile : first_tile);
+    bool first = w.rev && seg == 0;                     // backwards the first step does not decay the state
+    for (int it = first_tile; it < last_tile; ++it) {
         const int tile = w.rev ? tiles - 1 - it : it, t0 = tile * kWalkTile, steps = min(kWalkTile, n - t0);
         __syncthreads();
 #pragma unroll
         for (int i = 0; i < LA; ++i) {
             const int j = tid + i * kWalkThreads;
-            sa[j / W][j % W] = to_f32(ra[i]);
+            if (!STATE) sa[j / W][j % W] = to_f32(ra[i]);
             sb[j / W][j % W] = to_f32(rb[i]);
         }
 #pragma unroll
@@ -178,7 +202,7 @@ __global__ void __launch_bounds__(32 * WARPS) linattn_walk_kernel(const LinattnP
             sc[j / kWalkBlock][j % kWalkBlock] = to_f32(rc[i]);
         }
         __syncthreads();
-        if (it + 1 < tiles) fetch(w.rev ? tile - 1 : tile + 1);
+        if (it + 1 < last_tile) fetch(w.rev ? tile - 1 : tile + 1);
         if (row0 >= Dc) continue;                       // (a warp without rows stages only)
         auto step = [&](int k, float *y) {
             const int i = w.rev ? steps - 1 - k : k;
@@ -188,7 +212,7 @@ __global__ void __launch_bounds__(32 * WARPS) linattn_walk_kernel(const LinattnP
             float2 av[E2], bv[E2];
 #pragma unroll
             for (int m = 0; m < E2; ++m) {
-                av[m] = *reinterpret_cast<const float2 *>(&sa[i][2 * lane + 64 * m]);
+                av[m] = STATE ? make_float2(0.f, 0.f) : *reinterpret_cast<const float2 *>(&sa[i][2 * lane + 64 * m]);
                 bv[m] = *reinterpret_cast<const float2 *>(&sb[i][2 * lane + 64 * m]);
             }
             float c[ROWS];
@@ -201,7 +225,7 @@ __global__ void __launch_bounds__(32 * WARPS) linattn_walk_kernel(const LinattnP
 #pragma unroll
                 for (int m = 0; m < E2; ++m) {
                     s[r][m] = __ffma2_rn(g2, s[r][m], __fmul2_rn(c2, bv[m]));
-                    acc = __ffma2_rn(s[r][m], av[m], acc);
+                    if (!STATE) acc = __ffma2_rn(s[r][m], av[m], acc);
                 }
                 y[r] = acc.x + acc.y;
             }
@@ -220,15 +244,28 @@ __global__ void __launch_bounds__(32 * WARPS) linattn_walk_kernel(const LinattnP
                         for (int r = 0; r < ROWS; ++r) y[u * ROWS + r] = 0.f;
                 }
             }
+            if (STATE) continue;
             const float sum = transpose_reduce<4 * ROWS>(y, lane);
             constexpr int SHARE = 32 / (4 * ROWS);     // lanes with the same sum
             const int at = lane / SHARE, ku = k + at / ROWS, row = row0 + at % ROWS;
             if (lane % SHARE == 0 && ku < steps && row < Dc) put(t0 + (w.rev ? steps - 1 - ku : ku), row, sum);
         }
     }
-    if (e0 + tid % kWalkBlock < Dc)                     // zeros behind the row
-        for (int t = n + tid / kWalkBlock; t < T_; t += kWalkThreads / kWalkBlock) put(t, e0 + tid % kWalkBlock, 0.f);
-    if (w.last != nullptr) {
+    if (STATE) {
+#pragma unroll
+        for (int r = 0; r < ROWS; ++r)
+#pragma unroll
+            for (int m = 0; m < E2; ++m) {
+                if (inside(r, m, 0)) state_at(seg, r, m, 0) = s[r][m].x;
+                if (inside(r, m, 1)) state_at(seg, r, m, 1) = s[r][m].y;
+            }
+        return;
+    }
+    if (e0 + tid % kWalkBlock < Dc) {                   // zeros behind the row, by turns
+        constexpr int ZEROS = kWalkThreads / kWalkBlock;
+        for (long long t = n + (long long)seg * ZEROS + tid / kWalkBlock; t < T_; t += segs * ZEROS) put((int)t, e0 + tid % kWalkBlock, 0.f);
+    }
+    if (w.last != nullptr && (!SEGMENTS || seg == (tiles > 0 ? (tiles - 1) / p.seg_chunks : 0))) {
         const float gl = w.rev && n > 0 ? g : 1.f;
 #pragma unroll
         for (int r = 0; r < ROWS; ++r)
@@ -254,19 +291,49 @@ __global__ void __launch_bounds__(kSumThreads) linattn_sum_kernel(const LinattnP
     const size_t n = (size_t)p.B * p.T * w.heads * pieces;
     for (size_t i = (size_t)blockIdx.x * kSumThreads + threadIdx.x; i < n; i += (size_t)gridDim.x * kSumThreads) {
         const size_t head = i / pieces;                 // (batch row, step, head)
-        const float *x = w.part + head * w.group * w.D + (i - head * pieces) * V;
+        const float *x = w.part + head * w.group * w.pitch + (i - head * pieces) * V;
         float s[V];
 #pragma unroll
         for (int v = 0; v < V; ++v) s[v] = 0.f;
 #pragma unroll 4
         for (int r = 0; r < add; ++r) {
             float e[V];
-            load_vec<float, V>(x + (r % w.planes) * w.plane + (size_t)(r / w.planes) * w.D, e);
+            load_vec<float, V>(x + (r % w.planes) * w.plane + (size_t)(r / w.planes) * w.pitch, e);
 #pragma unroll
             for (int v = 0; v < V; ++v) s[v] += e[v];
         }
         store_vec<T, V>(out + i * V, s);
     }
+}
+
+// ---- rows that TMA can read, from rows that it cannot: eight elements of a padded row by a thread
+__global__ void __launch_bounds__(kSumThreads) linattn_copy_kernel(const LinattnParams p) {
+    const LinattnCopy &w = p.copy[blockIdx.y];
+    const int pieces = w.pitch / 8;
+    const size_t n = (size_t)p.B * p.T * w.H * pieces;
+    for (size_t i = (size_t)blockIdx.x * kSumThreads + threadIdx.x; i < n; i += (size_t)gridDim.x * kSumThreads) {
+        const size_t head = i / pieces, row = head / w.H;
+        const int c0 = (int)(i - head * pieces) * 8;
+        const unsigned short *in = static_cast<const unsigned short *>(w.in) + row * w.ld + (head - row * w.H) * w.D;
+        uint32_t x[8];
+#pragma unroll
+        for (int c = 0; c < 8; ++c) x[c] = c0 + c < w.D ? in[c0 + c] : 0u;
+        static_cast<uint4 *>(w.out)[i] = make_uint4(x[0] | x[1] << 16, x[2] | x[3] << 16, x[4] | x[5] << 16, x[6] | x[7] << 16);
+    }
+}
+
+cudaError_t launch_linattn_copies(const LinattnParams &p, cudaStream_t s) {
+    size_t n = 0;
+    for (int i = 0; i < p.copies; ++i) {
+        const size_t m = (size_t)p.B * p.T * p.copy[i].H * (p.copy[i].pitch / 8);
+        n = m > n ? m : n;
+    }
+    const size_t ctas = (n + kSumThreads - 1) / kSumThreads;
+    timing_mark("linattn_copy", 0, s);
+    linattn_copy_kernel<<<dim3((unsigned)(ctas < 152 * 32 ? ctas : 152 * 32), p.copies), kSumThreads, 0, s>>>(p);
+    const cudaError_t e = cudaGetLastError();
+    timing_mark("linattn_copy", 1, s);
+    return e;
 }
 
 template <typename T>
@@ -300,7 +367,7 @@ static cudaError_t launch_sums_t(const LinattnParams &p, cudaStream_t s) {
     for (int i = 0; i < p.sums; ++i) {
         const size_t m = (size_t)p.B * p.T * p.sum[i].heads * p.sum[i].D;
         n = m > n ? m : n;
-        vec = vec && p.sum[i].D % 4 == 0;
+        vec = vec && p.sum[i].D % 4 == 0 && p.sum[i].pitch % 4 == 0;
     }
     const size_t ctas = (n / (vec ? 4 : 1) + kSumThreads - 1) / kSumThreads;
     const dim3 grid((unsigned)(ctas < 152 * 32 ? ctas : 152 * 32), p.sums);
@@ -316,27 +383,74 @@ cudaError_t launch_linattn_sums(const LinattnParams &p, int dtype, cudaStream_t 
     return e;
 }
 
-template <typename T, int WARPS, int ROWS>
+// ---- what the segments up to each leave, from what each leaves: E_s += g^(steps of s) E_{s-1}. All segments here but
+// the first hold whole tiles only.
+__global__ void __launch_bounds__(kSumThreads) linattn_walk_join_kernel(const LinattnParams p) {
+    const int b = blockIdx.z, h = blockIdx.y, which = blockIdx.x % p.sweeps, n = p.Dk * p.Dv;
+    const int tiles = (row_length(p.lens, b, p.T) + kWalkTile - 1) / kWalkTile;
+    const float decay = exp2f(p.seg_chunks * kWalkTile * log2f(p.g[h]));
+    const size_t step = (size_t)p.B * p.Hv * n;
+    for (int i = blockIdx.x / p.sweeps * kSumThreads + threadIdx.x; i < n; i += gridDim.x / p.sweeps * kSumThreads) {
+        float *E = p.sweep[which].states + ((size_t)b * p.Hv + h) * n + i, sum = 0.f;
+        for (int s = 0; s < p.segs - 1 && (s + 1) * p.seg_chunks < tiles; ++s, E += step) *E = sum = fmaf(decay, sum, *E);
+    }
+}
+
+template <typename T, int WARPS, int ROWS, bool STATE>
 static cudaError_t launch_walk_w(const LinattnParams &p, cudaStream_t s) {
     int blocks[3] = {0, 0, 0}, widest = 1;
     for (int i = 0; i < p.sweeps; ++i) {
         blocks[i] = (p.sweep[i].Dc + WARPS * ROWS - 1) / (WARPS * ROWS);
         widest = p.sweep[i].Db > widest ? p.sweep[i].Db : widest;
     }
-    const dim3 grid(blocks[0] + blocks[1] + blocks[2], p.Hv, p.B);
-    if (widest <= 64) linattn_walk_kernel<T, 1, WARPS, ROWS><<<grid, 32 * WARPS, 0, s>>>(p, blocks[0], blocks[1]);
-    else if (widest <= 128) linattn_walk_kernel<T, 2, WARPS, ROWS><<<grid, 32 * WARPS, 0, s>>>(p, blocks[0], blocks[1]);
-    else linattn_walk_kernel<T, 4, WARPS, ROWS><<<grid, 32 * WARPS, 0, s>>>(p, blocks[0], blocks[1]);
+    const dim3 grid((blocks[0] + blocks[1] + blocks[2]) * (STATE ? p.segs - 1 : p.segs), p.Hv, p.B);
+    if (widest <= 64) linattn_walk_kernel<T, 1, WARPS, ROWS, STATE><<<grid, 32 * WARPS, 0, s>>>(p, blocks[0], blocks[1]);
+    else if (widest <= 128) linattn_walk_kernel<T, 2, WARPS, ROWS, STATE><<<grid, 32 * WARPS, 0, s>>>(p, blocks[0], blocks[1]);
+    else linattn_walk_kernel<T, 4, WARPS, ROWS, STATE><<<grid, 32 * WARPS, 0, s>>>(p, blocks[0], blocks[1]);
     return cudaGetLastError();
 }
-// Eight warps of eight rows share what is staged; four of four rows where that would leave SMs idle or where reading
-// the state is the work (float32, 1024 steps of 8 heads of 128 x 128: 142 us, 259 with the large ones; of 4 x 32
-// heads 565 and 443; bf16, 64 x 32 heads: 2 steps 148 and 159 us).
-template <typename T>
-static cudaError_t launch_walk_t(const LinattnParams &p, cudaStream_t s) {
+
+// CTAs of eight warps of eight rows share what is staged; of four warps of four rows where that would leave SMs idle
+// or where reading the state is the work (float32, 1024 steps of 8 heads of 128 x 128: 142 us before segments, 259 with the
+// large ones; of 4 x 32 heads 565 and 443; bf16, 64 x 32 heads: 2 steps 148 and 159 us).
+static bool walk_small(const LinattnParams &p) {
     long long ctas = 0;
     for (int i = 0; i < p.sweeps; ++i) ctas += (p.sweep[i].Dc + 63) / 64;
-    return ctas * p.Hv * p.B < 152 || p.T < 16 ? launch_walk_w<T, 4, 4>(p, s) : launch_walk_w<T, 8, 8>(p, s);
+    return ctas * p.Hv * p.B < 152 || p.T < 16;
+}
+
+// Segments of a row, where the small CTAs leave room for more of them (two to four on an SM, by their registers): as
+// many as fill it, of 64 steps at least. float32, 1024 steps of 128 x 128, whole and in segments: 4 heads 136 and 40 us,
+// 16 heads 136 and 124, 24 heads (two segments) 185 and 175; 128 steps of 8 heads 20.8 and 20.9.
+void linattn_step_segments(LinattnParams *p) {
+    const int tiles = (p->T + kWalkTile - 1) / kWalkTile;
+    long long ctas = 0;
+    int widest = 1;
+    for (int i = 0; i < p->sweeps; ++i) {
+        ctas += (p->sweep[i].Dc + 15) / 16;
+        widest = p->sweep[i].Db > widest ? p->sweep[i].Db : widest;
+    }
+    ctas *= (long long)p->Hv * p->B;
+    long long segs = walk_small(*p) ? 152 * (widest <= 64 ? 4 : widest <= 128 ? 3 : 2) / ctas : 1;
+    if (segs > tiles / 4) segs = tiles / 4;
+    if (segs < 2) segs = 1;
+    p->seg_chunks = (int)((tiles + segs - 1) / segs);
+    p->segs = (tiles + p->seg_chunks - 1) / p->seg_chunks;
+}
+
+template <typename T>
+static cudaError_t launch_walk_t(const LinattnParams &p, cudaStream_t s) {
+    if (!walk_small(p)) return launch_walk_w<T, 8, 8, false>(p, s);
+    if (p.segs > 1) {
+        cudaError_t e = launch_walk_w<T, 4, 4, true>(p, s);
+        if (e == cudaSuccess && p.segs > 2) {
+            const int ctas = (p.Dk * p.Dv + kSumThreads - 1) / kSumThreads;
+            linattn_walk_join_kernel<<<dim3(p.sweeps * ctas, p.Hv, p.B), kSumThreads, 0, s>>>(p);
+            e = cudaGetLastError();
+        }
+        if (e != cudaSuccess) return e;
+    }
+    return launch_walk_w<T, 4, 4, false>(p, s);
 }
 
 cudaError_t launch_linattn_steps(const LinattnParams &p, int dtype, cudaStream_t s) {

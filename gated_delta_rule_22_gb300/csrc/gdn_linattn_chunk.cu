@@ -137,6 +137,8 @@ __device__ __forceinline__ void write_zeros(const LinattnSweep &w, size_t at, in
 
 }  // namespace
 
+// WHOLE: the states' rows are of whole pieces of eight.
+template <bool WHOLE>
 __global__ void __launch_bounds__(kThreads, 1) linattn_chunk_kernel(const __grid_constant__ LinattnMaps maps, const __grid_constant__ SweepArgs cp) {
     extern __shared__ unsigned char smem_raw[];
     unsigned char *smem = reinterpret_cast<unsigned char *>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~(uintptr_t)1023);
@@ -321,18 +323,26 @@ __global__ void __launch_bounds__(kThreads, 1) linattn_chunk_kernel(const __grid
         const int e = threadIdx.x & 127, part = (warp - kStateWarp) >> 2, d0 = kPart * part;
         const uint32_t lanes = tmem + ((uint32_t)(warp & 3) << 21) + kColU + d0;
         float Z[kPart];
-        const bool row = e < Dc;
+        const bool row = e < Dc && (WHOLE || dc0 + e < w.Dc_of);
         const int work_here = d0 < Dbp ? work : 0;
         const float *init = cp.state_only ? nullptr : w.init;
 #pragma unroll
-        for (int d = 0; d < kPart; d += 4) {       // (Db is a multiple of 8)
+        for (int d = 0; d < kPart; d += 4) {
             float4 z = make_float4(0.f, 0.f, 0.f, 0.f);
             if (init != nullptr && row && d0 + d < Db) {
-                if (!w.init_t) {
+                if (WHOLE && !w.init_t) {
                     z = *reinterpret_cast<const float4 *>(init + (head * w.Dc + dc0 + e) * w.Db + db0 + d0 + d);
-                } else {
+                } else if (WHOLE) {
                     const float *at = init + (head * w.Db + db0 + d0 + d) * w.Dc + dc0 + e;
                     z = make_float4(at[0], at[w.Dc], at[2 * w.Dc], at[3 * w.Dc]);
+                } else {
+                    float x[4];
+#pragma unroll
+                    for (int i = 0; i < 4; ++i) {
+                        const int col = db0 + d0 + d + i;
+                        x[i] = col >= w.Db_of ? 0.f : w.init_t ? init[(head * w.Db_of + col) * w.Dc_of + dc0 + e] : init[(head * w.Dc_of + dc0 + e) * w.Db_of + col];
+                    }
+                    z = make_float4(x[0], x[1], x[2], x[3]);
                 }
             }
             Z[d] = z.x; Z[d + 1] = z.y; Z[d + 2] = z.z; Z[d + 3] = z.w;
@@ -473,12 +483,19 @@ __global__ void __launch_bounds__(kThreads, 1) linattn_chunk_kernel(const __grid
 #pragma unroll
                 for (int d = 0; d < kPart / 4; ++d) E[d * 128 + e] = make_float4(Z[4 * d], Z[4 * d + 1], Z[4 * d + 2], Z[4 * d + 3]);
         } else if (w.last != nullptr && row && seg == (chunks > 0 ? (chunks - 1) / p.seg_chunks : 0)) {
-            const bool wide = ((uintptr_t)w.last & 31) == 0;                 // (Db is a multiple of 8)
+            const bool wide = ((uintptr_t)w.last & 31) == 0;
 #pragma unroll
-            for (int d = 0; d < kPart; d += 8)
-                if (d0 + d < Db)
-                    store_piece2(w.last + (head * w.Dc + dc0 + e) * w.Db + db0 + d0 + d, Z[d], Z[d + 1], Z[d + 2], Z[d + 3], Z[d + 4], Z[d + 5], Z[d + 6],
-                                 Z[d + 7], wide);
+            for (int d = 0; d < kPart; d += 8) {
+                if (d0 + d >= Db) break;
+                float *out = w.last + (head * (WHOLE ? w.Dc : w.Dc_of) + dc0 + e) * (WHOLE ? w.Db : w.Db_of) + db0 + d0 + d;
+                if (WHOLE) {
+                    store_piece2(out, Z[d], Z[d + 1], Z[d + 2], Z[d + 3], Z[d + 4], Z[d + 5], Z[d + 6], Z[d + 7], wide);
+                } else {
+#pragma unroll
+                    for (int i = 0; i < 8; ++i)
+                        if (db0 + d0 + d + i < w.Db_of) out[i] = Z[d + i];
+                }
+            }
         }
     } else {
     regs_dec<kIssueRegs>();
@@ -617,15 +634,17 @@ size_t linattn_segments(LinattnParams *p) {
 }
 
 cudaError_t launch_linattn_chunks(const LinattnParams &p, const LinattnMaps &maps, cudaStream_t s) {
-    cudaError_t e = allow_smem<linattn_chunk_kernel>((int)kSmem);
+    const bool whole = p.Dk % 8 == 0 && p.Dv % 8 == 0;
+    cudaError_t e = whole ? allow_smem<linattn_chunk_kernel<true>>((int)kSmem) : allow_smem<linattn_chunk_kernel<false>>((int)kSmem);
     if (e != cudaSuccess) return e;
+    auto *kernel = whole ? linattn_chunk_kernel<true> : linattn_chunk_kernel<false>;
     SweepArgs cp = {};
     cp.p = p;
     int blocks = 0;
     for (int i = 0; i < p.sweeps; ++i) blocks += cp.blocks[i] = sweep_blocks(p.sweep[i]);
     auto run = [&](const char *name, int segs) {
         timing_mark(name, 0, s);
-        linattn_chunk_kernel<<<dim3(blocks * segs, p.Hv, p.B), kThreads, kSmem, s>>>(maps, cp);
+        kernel<<<dim3(blocks * segs, p.Hv, p.B), kThreads, kSmem, s>>>(maps, cp);
         const cudaError_t err = cudaGetLastError();
         timing_mark(name, 1, s);
         return err;

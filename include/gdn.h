@@ -447,11 +447,11 @@ GDN_API int gdn_linear_bwd(const gdn_linear_shape *shape, const void *x, const v
  *   g [Hv] float32, 0 <= g <= 1: a constant of the layer, without a gradient
  *   S0, S_T, dS_T, dS0 [B,Hv,Dv,Dk] float32, each may be NULL (S0, dS_T: zeros)
  * Dk and Dv are 1 to 256, Hv a multiple of Hk (else GDN_ERR_UNSUPPORTED_SHAPE). Prompts and training run
- * in chunks of 128 steps on the tensor cores (bf16; q, k and v 16-byte aligned, Dk, Dv and the row
- * strides multiples of 8) or step by step (float32 and the rest); a single step is one pass over the
- * state, and with T = 1 S_T may be S0 itself (updated in place). In chunks, a q, k, v or dy that is not
- * finite at a valid step makes outputs of its chunk of the same row and head NaN, those of other steps of it too,
- * and the states behind it.
+ * in chunks of 128 steps on the tensor cores (bf16, 8 steps or more; q, k and v whose dims or row strides are no
+ * multiples of 8 are copied into the workspace, for 64 steps or more; those that are have to be 16-byte
+ * aligned) or step by step (float32 and the rest); a single step is one pass over the state, and with T = 1
+ * S_T may be S0 itself (updated in place). In chunks, a q, k, v or dy that is not finite at a valid step makes
+ * outputs of its chunk of the same row and head NaN, those of other steps of it too, and the states behind it.
  * The backward computes the states again from k, v and S0; the forward saves nothing. dq and dk are
  * summed over the value heads of each key head in ascending order.
  * workspace: gdn_linattn_fwd_workspace_bytes / gdn_linattn_bwd_workspace_bytes bytes (0: may be NULL).

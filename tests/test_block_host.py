@@ -94,7 +94,8 @@ def test_linattn_workspace(lib):
     assert need(Dk=0) == 0 and need(Hv=5) == 0
     rows = 2 * 300 * 4 * 64 * 4                                                              # dq (dk) by value head
     assert need(dtype=0) >= 2 * rows
-    assert need(dtype=0, Hk=4) == 0
+    assert need(dtype=0, Hk=4, T=40) == 0 and need(Hk=4, T=2000, Dv=64) > 0                   # (segments' states)
+    assert need(Hk=4, Dk=63) > need(Hk=4)                                                    # copies of unaligned rows
 
 
 @pytest.mark.parametrize("name", ["gdn_resnorm_fwd", "gdn_resnorm_bwd"])

@@ -44,6 +44,13 @@ def make(seed, B, T, Hk, Hv, Dk, Dv, dt, decay="mixed", wide=0):
                 dS_T=rnd(B, Hv, Dv, Dk, scale=0.3))
 
 
+def unaligned(t):
+    """t in rows of whole 16 bytes, at an address that is none: what the chunked form does not take."""
+    n = t.shape[2] * t.shape[3]
+    wide = torch.zeros(*t.shape[:2], n // 8 * 8 + 8, device="cuda", dtype=t.dtype)
+    return wide[..., 1:1 + n].unflatten(-1, t.shape[2:]).copy_(t)
+
+
 def reference(a, lens, state, train):
     leaves = {n: a[n].double() for n in ("q", "k", "v")}
     leaves["S0"] = a["S0"].double() if state else torch.zeros_like(a["S0"], dtype=torch.float64)
@@ -72,6 +79,7 @@ def check(a, lens=None, state=True, train=True, what=""):
 
 
 SHAPES = [  # B, T, Hk, Hv, Dk, Dv
+    (2, 300, 2, 4, 75, 33), (1, 200, 1, 1, 130, 129), (2, 140, 1, 2, 1, 7), (1, 100, 1, 1, 255, 9),
     (1, 2, 1, 1, 8, 8), (2, 5, 1, 2, 16, 24), (1, 127, 2, 2, 64, 64), (2, 128, 1, 1, 128, 128), (1, 129, 2, 4, 128, 64),
     (3, 300, 1, 3, 64, 128), (2, 257, 2, 2, 96, 120), (1, 400, 1, 2, 192, 128), (1, 260, 1, 1, 256, 256), (2, 140, 2, 2, 40, 75),
     (1, 33, 1, 1, 1, 1), (1, 150, 1, 5, 250, 3), (1, 70, 1, 1, 3, 250), (2, 130, 1, 4, 136, 200),
@@ -202,9 +210,10 @@ def test_long_rows_of_few_heads(shape, dt):
     check(make(12, *shape, dt), what="long")
 
 
+@pytest.mark.parametrize("dt", [BF16, F32], ids=["bf16", "f32"])
 @pytest.mark.parametrize("decay", ["mixed", "one", "zero"])
-def test_segments_of_ragged_rows(decay):
-    a = make(13, 4, 1300, 1, 1, 64, 64, BF16, decay)
+def test_segments_of_ragged_rows(decay, dt):
+    a = make(13, 4, 1300, 1, 1, 64, 64, dt, decay)
     lens = torch.tensor([1300, 130, 700, 0], device="cuda", dtype=torch.int32)
     for b, n in enumerate(lens.tolist()):
         for t in ("q", "k", "v", "dy"):
@@ -219,8 +228,7 @@ def test_the_forms_agree():
     a = make(14, 2, 600, 2, 4, 128, 64, BF16, wide=16)
     off = dict(a)
     for n in ("q", "k", "v"):
-        t = torch.zeros(*a[n].shape[:2], a[n].shape[2] * a[n].shape[3] + 1, device="cuda", dtype=BF16)
-        off[n] = t[..., 1:].unflatten(-1, a[n].shape[2:]).copy_(a[n])
+        off[n] = unaligned(a[n])
     y, S = gdn().gdn_linattn_fwd(a["q"], a["k"], a["v"], a["g"], a["S0"])
     y2, S2 = gdn().gdn_linattn_fwd(off["q"], off["k"], off["v"], off["g"], off["S0"])
     assert R.rel(y, y2) <= TOL[BF16] and R.rel(S, S2) <= TOL_STATE and not torch.equal(y, y2)
@@ -232,7 +240,7 @@ def test_both_forms_on_many_shapes():
     rng = random.Random(5)
     for _ in range(120):
         B, Hk, group = rng.randint(1, 4), rng.randint(1, 3), rng.choice([1, 1, 2, 3])
-        dim = lambda: rng.choice([64, 128, 192, 256, 8 * rng.randint(1, 32)])  # noqa: E731
+        dim = lambda: rng.choice([64, 128, 192, 256, 8 * rng.randint(1, 32), rng.randint(1, 255)])  # noqa: E731
         T = rng.choice([rng.randint(8, 140), rng.randint(120, 600), rng.randint(600, 1500)])
         a = make(rng.randint(0, 10 ** 6), B, T, Hk, Hk * group, dim(), dim(), BF16, rng.choice(["mixed", "mixed", "one", "long", "tiny"]))
         lens = None if rng.random() < 0.4 else torch.tensor([rng.randint(0, T) for _ in range(B)], device="cuda", dtype=torch.int32)
@@ -240,9 +248,9 @@ def test_both_forms_on_many_shapes():
             for t in ("q", "k", "v", "dy"):
                 a[t][b, n:] = float("nan")
         off = dict(a)
-        for n in ("q", "k", "v"):
-            t = torch.zeros(B, T, a[n].shape[2] * a[n].shape[3] + 1, device="cuda", dtype=BF16)
-            off[n] = t[..., 1:].unflatten(-1, a[n].shape[2:]).copy_(a[n])
+        odd = a["q"].shape[-1] % 8 or a["v"].shape[-1] % 8              # (copied, at any address)
+        for n in ("q", "k", "v", "dy"):
+            off[n] = a[n].float() if odd else unaligned(a[n]) if n != "dy" else a[n]
         S0, dS_T = (a["S0"], a["dS_T"]) if rng.random() < 0.5 else (None, None)
         run = lambda s: dict(zip(("y", "S_T"), gdn().gdn_linattn_fwd(s["q"], s["k"], s["v"], s["g"], S0, lens)),  # noqa: E731
                              **gdn().gdn_linattn_bwd(s["q"], s["k"], s["v"], s["g"], s["dy"], S0, lens, dS_T))

@@ -420,8 +420,8 @@ static bool walk_small(const LinattnParams &p) {
 }
 
 // Segments of a row, where the small CTAs leave room for more of them (two to four on an SM, by their registers): as
-// many as fill it, of 64 steps at least. float32, 1024 steps of 128 x 128, whole and in segments: 4 heads 136 and 40 us,
-// 16 heads 136 and 124, 24 heads (two segments) 185 and 175; 128 steps of 8 heads 20.8 and 20.9.
+// many as fill it, of 32 steps at least. float32, 1024 steps of 128 x 128, whole and in segments: 4 heads 136 and 40 us,
+// 16 heads 136 and 124, 24 heads (two segments) 185 and 175; 128 steps of 8 heads 20.8 and 19.4.
 void linattn_step_segments(LinattnParams *p) {
     const int tiles = (p->T + kWalkTile - 1) / kWalkTile;
     long long ctas = 0;
@@ -432,7 +432,7 @@ void linattn_step_segments(LinattnParams *p) {
     }
     ctas *= (long long)p->Hv * p->B;
     long long segs = walk_small(*p) ? 152 * (widest <= 64 ? 4 : widest <= 128 ? 3 : 2) / ctas : 1;
-    if (segs > tiles / 4) segs = tiles / 4;
+    if (segs > tiles / 2) segs = tiles / 2;
     if (segs < 2) segs = 1;
     p->seg_chunks = (int)((tiles + segs - 1) / segs);
     p->segs = (tiles + p->seg_chunks - 1) / p->seg_chunks;

@@ -602,7 +602,7 @@ def _resnorm_args(x, h, z, scale, w_post, w_pre, post, pre, act, eps):
         if not pre:
             raise ValueError("w_pre is given, but its norm is off")
         _check("w_pre", w_pre, (D,), _F32, dev)
-    return _resnorm_shape(rows, D, gate_rows, _act(act), 1 if post else 0, 1 if pre else 0, _type(x), eps, ldx, ldh, ldz)
+    return _resnorm_shape(rows, D, gate_rows, _act(act), 1 if post else 0, 1 if pre else 0, _type(x), float(eps), ldx, ldh, ldz)
 
 
 def gdn_resnorm_fwd(x, h, z=None, scale=None, w_post=None, w_pre=None, *, post=True, pre=True, act="none", eps=1e-5, r=None, y=None,

@@ -43,6 +43,7 @@ namespace {
 
 constexpr int kC = kLinattnChunk;
 constexpr int kParts = 2, kPart = 128 / kParts;    // the state's columns by two groups of four warps
+constexpr int kMaskGroup = 2;                      // blocks of 16 columns of P~ that are announced at once
 constexpr int kOutWarp = 8, kStateWarp = 12, kFetchWarp = kStateWarp + 4 * kParts, kThreads = (kFetchWarp + 4) * 32;
 // registers of a thread: launched with kLaunchRegs, then dealt out again
 constexpr int kLaunchRegs = 80, kMaskRegs = 64, kOutRegs = 64, kStateRegs = 120, kIssueRegs = 48;
@@ -101,18 +102,17 @@ __device__ __forceinline__ void store_piece2(void *p, float a, float b, float c,
     }
 }
 
-// b w for a pair of b, rounded once
-__device__ __forceinline__ uint32_t weigh(uint32_t b, float w) {
-    const float2 x = __fmul2_rn(make_float2(__uint_as_float(b << 16), __uint_as_float(b & 0xffff0000u)), make_float2(w, w));
-    return pack2_bf16(x.x, x.y);
-}
-
 // b w for a pair of b and w = w0 + w1 + w2 as bf16 terms, in packed bf16 arithmetic (in float32 the conversions
 // alone cost as much): t0 = b w0 rounded; the product of two bf16 has 16 bits, so its rest is a bf16 exactly; t1 =
 // that rest + b w1 rounded, some 2^-9 of the product. Three terms: what t1 lost (a two-sum, and the rest of b w1,
 // both exact) + b w2, some 2^-18, with an error of 2^-26 of the product.
 using bf16x2 = __nv_bfloat162;
 __device__ __forceinline__ uint32_t bits(const bf16x2 &x) { return *reinterpret_cast<const uint32_t *>(&x); }
+// b w for a pair of b and w = w0 + w1, rounded once (but for some 2^-18)
+__device__ __forceinline__ uint32_t weigh(uint32_t b, bf16x2 w0, bf16x2 w1) {
+    const bf16x2 x = *reinterpret_cast<const bf16x2 *>(&b);
+    return bits(__hfma2(x, w0, __hmul2_rn(x, w1)));
+}
 template <bool THREE>
 __device__ __forceinline__ void split_product(uint32_t b, bf16x2 w0, bf16x2 w1, bf16x2 w2, uint32_t &t0, uint32_t &t1, uint32_t &t2) {
     const bf16x2 x = *reinterpret_cast<const bf16x2 *>(&b), a = __hmul2_rn(x, w0), rest = __hfma2(x, w0, __hneg2(a));
@@ -146,8 +146,9 @@ __global__ void __launch_bounds__(kThreads, 1) linattn_chunk_kernel(const __grid
     float *pw = reinterpret_cast<float *>(zb + kOperand) + 32;               // g^0 .. g^128, zeros for -32 .. -1
     float *pw_back = pw + 136;                                               // g^15 .. g^0
     uint64_t *full = reinterpret_cast<uint64_t *>(pw_back + 16), *empty = full + 2;
-    uint64_t *p_full = full + 4, *pt_full = full + 5, *o1_full = full + 6, *o2_full = full + 7, *o_empty = full + 8;
+    uint64_t *p_full = full + 4, *o1_full = full + 6, *o2_full = full + 7, *o_empty = full + 8;
     uint64_t *u_full = full + 9, *p_seen = full + 10, *bt_full = full + 12, *z_full = bt_full + kParts;  // (the last two: one for each part)
+    uint64_t *pt_full = z_full + kParts;                                     // (groups of a part's columns, then those of the other)
     uint32_t *tmem_slot = reinterpret_cast<uint32_t *>(full + 24);
     const LinattnParams &p = cp.p;
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
@@ -180,7 +181,7 @@ __global__ void __launch_bounds__(kThreads, 1) linattn_chunk_kernel(const __grid
             mbar_init(empty + i, cp.state_only ? 1 : 2);
         }
         for (uint64_t *bar : {p_full, o1_full, o2_full, u_full}) mbar_init(bar, 1);
-        mbar_init(pt_full, 8);                     // (warps)
+        for (int i = 0; i < 8 / kMaskGroup; ++i) mbar_init(pt_full + i, 4);  // (warps)
         mbar_init(o_empty, 4);
         for (int i = 0; i < 2 * kParts; ++i) mbar_init(bt_full + i, 4);
         mbar_init(p_seen, 1 + 4 * ((Dbp + kPart - 1) / kPart));
@@ -252,23 +253,28 @@ __global__ void __launch_bounds__(kThreads, 1) linattn_chunk_kernel(const __grid
                     for (int r = 0; r < 16; ++r) v[r] = 0.f;
                 }
                 uint32_t hi[8];                    // its terms take its place: no warp waits for another
-#pragma unroll
-                for (int r = 0; r < 8; ++r) hi[r] = pack2_bf16(v[2 * r], v[2 * r + 1]);
-                tmem_st8(mine + 16 * cb, hi);
-                if (two) {
+                if (two) {                         // (the first cut off, not rounded: the second holds the rest)
                     uint32_t lo[8];
 #pragma unroll
                     for (int r = 0; r < 8; ++r) {
-                        const float2 x = __ffma2_rn(make_float2(__uint_as_float(hi[r] << 16), __uint_as_float(hi[r] & 0xffff0000u)), make_float2(-1.f, -1.f),
-                                                    make_float2(v[2 * r], v[2 * r + 1]));
+                        const uint32_t e0 = __float_as_uint(v[2 * r]), e1 = __float_as_uint(v[2 * r + 1]);
+                        hi[r] = __byte_perm(e0, e1, 0x7632);
+                        const float2 x = __fadd2_rn(make_float2(v[2 * r], v[2 * r + 1]),
+                                                    make_float2(-__uint_as_float(e0 & 0xffff0000u), -__uint_as_float(e1 & 0xffff0000u)));
                         lo[r] = pack2_bf16(x.x, x.y);
                     }
                     tmem_st8(mine + 16 * cb + 8, lo);
+                } else {
+#pragma unroll
+                    for (int r = 0; r < 8; ++r) hi[r] = pack2_bf16(v[2 * r], v[2 * r + 1]);
+                }
+                tmem_st8(mine + 16 * cb, hi);
+                if (cb % kMaskGroup == kMaskGroup - 1) {
+                    tmem_wait_st();
+                    tc_fence_before();
+                    warp_arrive(pt_full + (4 * part + cb) / kMaskGroup, lane);
                 }
             }
-            tmem_wait_st();
-            tc_fence_before();
-            warp_arrive(pt_full, lane);
         }
     } else if (warp < kStateWarp) {                // ---- the outputs
         regs_dec<kOutRegs>();
@@ -412,7 +418,7 @@ __global__ void __launch_bounds__(kThreads, 1) linattn_chunk_kernel(const __grid
 #pragma unroll
                         for (int q = 0; q < 4; ++q) {
                             const int at = 4 * (c0 + c) + q;
-                            if constexpr (TERMS == 1) t0[q] = weigh(in[q], wj);
+                            if constexpr (TERMS == 1) t0[q] = weigh(in[q], w0, w1);
                             else split_product<TERMS == 3>(in[q], w0, w1, w2, t0[q], t1[at], t2[TERMS == 3 ? at : 0]);
                         }
                         *piece_at(bb, e, first_piece + c0 + c) = make_uint4(t0[0], t0[1], t0[2], t0[3]);
@@ -535,17 +541,24 @@ __global__ void __launch_bounds__(kThreads, 1) linattn_chunk_kernel(const __grid
                     umma_bf16_w(tmem + kColP, desc_k(a + off), desc_k(bb + off), idesc_p, q > 0, lead);
                 }
                 umma_commit_w(p_full, lead);
-                ok = all_wait(pt_full, ph) && (k == 0 || all_wait(o_empty, ph ^ 1)) &&
+                ok = (k == 0 || all_wait(o_empty, ph ^ 1)) &&
                      (!(masked && length_of(first + k) < kC) || all_wait(o2_full, ph));           // (c is cleared by then)
                 if (!ok) break;
-                tc_fence_after();
                 const bool two = two_of(first + k);
-                for (int term = two ? 1 : 0; term >= 0; --term) {            // smallest first
-                    uint64_t cd = desc_mn(c);
+                const uint64_t cd = desc_mn(c);
+                // The products of each group of columns as soon as it is there, those of the half with more zeros first
+#pragma unroll 1
+                for (int j = 0; j < 8 && ok; j += kMaskGroup) {
+                    const int q0 = (j / kMaskGroup + (rev ? 0 : 1)) % 2 * 4 + j / (2 * kMaskGroup) * kMaskGroup;
+                    if (!(ok = all_wait(pt_full + q0 / kMaskGroup, ph))) break;
+                    tc_fence_after();
+                    for (int term = two ? 1 : 0; term >= 0; --term)          // smallest first
 #pragma unroll
-                    for (int q = 0; q < kC / 16; ++q, cd += 2048 >> 4)
-                        umma_bf16_tw(tmem + kColO1, tmem + kColP + 16 * q + 8 * term, cd, idesc_o, (two && term == 0) || q > 0, lead);
+                        for (int q = q0; q < q0 + kMaskGroup; ++q)
+                            umma_bf16_tw(tmem + kColO1, tmem + kColP + 16 * q + 8 * term, cd + q * (2048 >> 4), idesc_o,
+                                         j > 0 || q > q0 || (two && term == 0), lead);
                 }
+                if (!ok) break;
                 umma_commit_w(o1_full, lead);
                 umma_commit_w(empty + (k & 1), lead);
             }

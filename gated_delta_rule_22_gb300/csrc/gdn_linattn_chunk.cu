@@ -26,11 +26,16 @@
 // Warps 0-7 mask P, warps 8-11 write outputs, warps 12-19 hold the state (each four half of its columns); one warp
 // fetches (two chunks deep), two issue products: P and O1, and O2 and U, so that neither chain waits for the other.
 //
-// Bound by latency: a chunk takes some 6500 cycles, 3.4 us (its tensor products 2600), the loop of P, its mask and
-// O1 in one place of tensor memory, and the chain of b~, U and the state beside it; where the state leaves the
-// call and b~ has several terms, up to 9000. What carries the loops: code short enough for the instruction cache,
-// one arrival per warp, work of one kind in each warp. 4 x 4096 steps of 32 heads of 128 x 128: forward 128 us,
-// 4.2 TB/s of q, k, v and y, backward 357 us, 2.6 TB/s; 4 x 2048 with 16 key heads and a carried state 75 us.
+// A chunk takes some 6000 cycles, 3.2 us: P is there after 900, P~'s first columns after 3000 and its last after 4800,
+// b~ after 3000, and from there the tensor cores are busy with U, O2 and O1 until 5700; the outputs leave under the next
+// chunk's P and mask, 3300 cycles. All of these share one shared memory, whose bandwidth takes some 2000 cycles for the
+// products' operands, 800 for TMA's writes, 800 for b~ and Z and more for the mask's powers and the stores' rows, so
+// that more warps, more columns at once or loads further ahead in any of them slowed the others (483 to 491 us for what
+// is 440 so). O1 begins with the columns that are there, those of the half with more zeros first. Where the state leaves the
+// call and b~ has several terms, a chunk takes up to 9000 cycles. What carries the loops: code short enough for the
+// instruction cache, one arrival per warp, work of one kind in each warp. 4 x 4096 steps of 32 heads of 128 x 128: forward
+// 113 us (127 with S_T), 4.7 TB/s of q, k, v and y, backward 321 us, 2.9 TB/s; 4 x 2048 with 16 key heads and a carried
+// state 75 to 78 us.
 #include "gdn.h"
 #include "gdn_layer.cuh"
 #include "gdn_umma.cuh"
@@ -43,7 +48,7 @@ namespace {
 
 constexpr int kC = kLinattnChunk;
 constexpr int kParts = 2, kPart = 128 / kParts;    // the state's columns by two groups of four warps
-constexpr int kMaskGroup = 2;                      // blocks of 16 columns of P~ that are announced at once
+constexpr int kMaskGroup = 2;                      // blocks of 16 columns of P~ that are announced at once (4: 456 us for 451, 1: 497)
 constexpr int kOutWarp = 8, kStateWarp = 12, kFetchWarp = kStateWarp + 4 * kParts, kThreads = (kFetchWarp + 4) * 32;
 // registers of a thread: launched with kLaunchRegs, then dealt out again
 constexpr int kLaunchRegs = 80, kMaskRegs = 64, kOutRegs = 64, kStateRegs = 120, kIssueRegs = 48;
@@ -189,10 +194,10 @@ __global__ void __launch_bounds__(kThreads, 1) linattn_chunk_kernel(const __grid
     }
     if (warp == kFetchWarp) tmem_alloc(tmem_slot, 512);
     {
-        const float lg = log2f(p.g[h]);
-        for (int i = threadIdx.x; i <= kC; i += kThreads) pw[i] = i == 0 ? 1.f : exp2f(i * lg);
+        const float g = p.g[h];
+        for (int i = threadIdx.x; i <= kC; i += kThreads) pw[i] = powf(g, (float)i);
         if (threadIdx.x < 32) pw[(int)threadIdx.x - 32] = 0.f;
-        if (threadIdx.x < 16) pw_back[threadIdx.x] = threadIdx.x == 15 ? 1.f : exp2f((15 - (int)threadIdx.x) * lg);
+        if (threadIdx.x < 16) pw_back[threadIdx.x] = powf(g, (float)(15 - (int)threadIdx.x));
     }
     tc_fence_before();
     __syncthreads();
@@ -354,7 +359,7 @@ __global__ void __launch_bounds__(kThreads, 1) linattn_chunk_kernel(const __grid
             Z[d] = z.x; Z[d + 1] = z.y; Z[d + 2] = z.z; Z[d + 3] = z.w;
         }
         if (!cp.state_only && work_here > 0 && seg > 0) {                    // through the earlier segments
-            const float decay = exp2f((rev ? n - (chunks - first) * kC : first * kC) * lg);
+            const float decay = powf(p.g[h], (float)(rev ? n - (chunks - first) * kC : first * kC));
             const float4 *E = reinterpret_cast<const float4 *>(p.seg_state) + (size_t)(unit + seg - 1) * (kC * 32) + part * (kC * kPart / 4);
 #pragma unroll
             for (int d = 0; d < kPart / 4; ++d) {
@@ -618,7 +623,7 @@ __global__ void __launch_bounds__(kThreads, 1) linattn_chunk_kernel(const __grid
 __global__ void __launch_bounds__(256) linattn_join_kernel(const LinattnParams p) {
     const int b = blockIdx.z, h = blockIdx.y, blocks = gridDim.x / 16, x = blockIdx.x / 16;
     const int chunks = (row_length(p.lens, b, p.T) + kC - 1) / kC;
-    const float decay = exp2f(p.seg_chunks * kC * log2f(p.g[h]));
+    const float decay = powf(p.g[h], (float)(p.seg_chunks * kC));
     float4 *E = reinterpret_cast<float4 *>(p.seg_state) + ((size_t)(b * gridDim.y + h) * blocks + x) * (p.segs - 1) * (kC * 32) +
                 blockIdx.x % 16 * 256 + threadIdx.x;
     float4 sum = make_float4(0.f, 0.f, 0.f, 0.f);

@@ -6,7 +6,7 @@ itself, 0.43 x 2^-8 in the 2-norm (rounding errors are uniform); in chunks the s
 inputs are rounded to bf16 on the way, and these terms' errors, of either sign, add as the terms' squares do: at
 most 0.43 x 2^-8 sqrt(1 + 1 + 1) together, and twice that, 1.5 x 2^-8, where terms partly cancel. float32 outputs, step by step: n roundings of 2^-24 of a sum's
 running value, of either sign, and the dot products' Dk: 2^-24 sqrt(2 n + D), up to some 2e-6 at n = 400.
-The float32 states of the chunked form hold 24 bits of k and the decay's powers (2 ulp of exp2 and log2, times
+The float32 states of the chunked form hold 24 bits of k and the decay's powers (4 ulp of powf; step by step 2 ulp of exp2 and log2, times
 the exponent): 2^-20 covers ages up to log2 = 8, beyond which nothing counts."""
 import random
 
@@ -220,6 +220,22 @@ def test_segments_of_ragged_rows(decay, dt):
             a[t][b, n:] = float("nan")
     got = check(a, lens, what=decay)
     assert all(torch.all(got[n][0][b, L:] == 0) for n in ("y", "dq", "dk", "dv") for b, L in enumerate(lens.tolist()))
+
+
+@pytest.mark.parametrize("wide", [2, 6, 18])
+def test_row_strides_that_are_copied(wide):
+    """Rows whose stride is no multiple of 8 elements, with NaN between them and behind the sequences."""
+    a = make(18, 3, 200, 2, 4, 64, 40, BF16, wide=wide)
+    lens = torch.tensor([200, 67, 0], device="cuda", dtype=torch.int32)
+    for b, n in enumerate(lens.tolist()):
+        for t in ("q", "k", "v", "dy"):
+            a[t][b, n:] = float("nan")
+    for t in ("q", "k", "v"):
+        base = a[t]._base if a[t]._base is not None else a[t]
+        flat = base.view(3, 200, -1)
+        flat[..., :wide // 2] = float("nan")
+        flat[..., flat.shape[-1] - wide // 2:] = float("nan")
+    check(a, lens, what="copied")
 
 
 def test_the_forms_agree():

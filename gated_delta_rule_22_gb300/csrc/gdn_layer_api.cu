@@ -279,8 +279,17 @@ int resnorm_plan(const gdn_resnorm_shape *s, gdn::ResnormParams *p) {
 }
 
 size_t resnorm_part_bytes(const gdn::ResnormParams &p) { return up256((size_t)p.ctas * 2 * p.D * 4); }
-size_t resnorm_ws(const gdn::ResnormParams &p) {
-    return resnorm_part_bytes(p) + (p.gate_rows > 1 && p.per_gate > 1 ? up256((size_t)p.units * p.D * 4) : 0);
+// A backward without z: no rows share a gate, whatever gate_rows is.
+void resnorm_without_gate(gdn::ResnormParams *p, int dtype) {
+    p->gate_rows = 1;
+    gdn::resnorm_units(p, dtype);
+}
+// Room for the call with z and for the one without: the size query does not know which it will be.
+size_t resnorm_ws(gdn::ResnormParams p, int dtype) {
+    const size_t gated = resnorm_part_bytes(p) + (p.gate_rows > 1 && p.per_gate > 1 ? up256((size_t)p.units * p.D * 4) : 0);
+    resnorm_without_gate(&p, dtype);
+    const size_t plain = resnorm_part_bytes(p);
+    return gated > plain ? gated : plain;
 }
 
 // bf16 x and W with packed rows are read in place by TMA, so they are 16-byte aligned like every packed
@@ -537,7 +546,7 @@ int gdn_resnorm_fwd(const gdn_resnorm_shape *shape, const void *x, const void *h
 
 size_t gdn_resnorm_bwd_workspace_bytes(const gdn_resnorm_shape *shape) {
     gdn::ResnormParams p;
-    return resnorm_plan(shape, &p) == GDN_OK ? resnorm_ws(p) : 0;
+    return resnorm_plan(shape, &p) == GDN_OK ? resnorm_ws(p, shape->dtype) : 0;
 }
 
 int gdn_resnorm_bwd(const gdn_resnorm_shape *shape, const void *x, const void *h, const void *z, const float *scale, const float *w_post,
@@ -551,7 +560,8 @@ int gdn_resnorm_bwd(const gdn_resnorm_shape *shape, const void *x, const void *h
     if ((rc = packed_ok({scale, w_post, w_pre, stats, dy, dr, dx, dh, dz, dscale, dw_post, dw_pre, workspace})) != GDN_OK ||
         (rc = strided_ok({x, h, z}, elem(shape->dtype))) != GDN_OK)
         return rc;
-    if (workspace_bytes < resnorm_ws(p)) return GDN_ERR_WORKSPACE_TOO_SMALL;
+    if (workspace_bytes < resnorm_ws(p, shape->dtype)) return GDN_ERR_WORKSPACE_TOO_SMALL;
+    if (z == nullptr) resnorm_without_gate(&p, shape->dtype);
     gdn::api_clear_error();
     p.x = x; p.h = h; p.z = z; p.scale = scale; p.w_post = w_post; p.w_pre = w_pre; p.stats_in = stats; p.dy = dy; p.dr = dr;
     p.dx = dx; p.dh = dh; p.dz = dz; p.dscale = dscale; p.dw_post = dw_post; p.dw_pre = dw_pre;

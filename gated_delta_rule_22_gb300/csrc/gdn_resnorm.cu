@@ -254,7 +254,7 @@ __global__ void __launch_bounds__(LPR < 128 ? 128 : LPR) resnorm_fwd_kernel(cons
     }
 }
 
-// A CTA takes units of p.unit consecutive rows that share a row of z (gate_rows = 1: any rows), sums Q and dw_pre
+// A CTA takes units of p.unit consecutive rows that share a row of z (gate_rows = 1, as it is without z: any rows), sums Q and dw_pre
 // over all its units into its slice of the partial sums, and the gate's gradient over each.
 template <typename T, int V, int LPR, int IT>
 __global__ void __launch_bounds__(LPR < 128 ? 128 : LPR, LPR <= 256 ? 2 : 1) resnorm_bwd_kernel(const ResnormParams p) {
@@ -267,7 +267,7 @@ __global__ void __launch_bounds__(LPR < 128 ? 128 : LPR, LPR <= 256 ? 2 : 1) res
     RowSum<LPR, 3> row_sum;
     const float inv_D = 1.f / p.D;
     const T *const z0 = static_cast<const T *>(p.z);
-    const bool shared_z = z0 != nullptr && p.gate_rows > 1;
+    const bool shared_z = p.gate_rows > 1;
     float2 k[P], wr[P], Q[P], dwr[P], dzs[P];
     at.params(p.scale, p.w_post, k);
     at.params(p.w_pre, nullptr, wr);

@@ -491,7 +491,7 @@ GDN_API int gdn_linattn_bwd(const gdn_linattn_shape *shape, const void *q, const
  */
 typedef struct {
     int M, D;       /* rows, channels */
-    int gate_rows;  /* consecutive rows that share a row of z; 0: 1 */
+    int gate_rows;  /* consecutive rows that share a row of z; 0: 1. Without z it has no effect */
     int act;        /* a gdn_act, of the gate */
     int post, pre;  /* 0: without the norm of h, without the norm of r */
     int dtype;      /* a gdn_dtype */

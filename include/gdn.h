@@ -38,7 +38,7 @@
  *     over the value heads that share a kv head) runs in a fixed order that depends
  *     only on the problem, not on the grid or the GPU's SM count, and a batch row's
  *     results do not depend on the other rows (B = 8 gives, bit for bit, what eight
- *     B = 1 calls give).
+ *     B = 1 calls give), but for the operators beside the recurrence that say otherwise.
  *   - There is no host fallback: if the GPU cannot run a kernel the call returns
  *     GDN_ERR_CUDA.
  */
@@ -306,8 +306,10 @@ GDN_API int gdn_gates_bwd(const gdn_shape *shape, const void *a, const void *b, 
  *     used, leave the carried state alone, and their outputs and gradients are written as zeros. A
  *     row of length 0 passes its state through.
  *   - The buffers of a call may not overlap, except where a call says so.
- *   - Results are bitwise deterministic. How the scan splits a sequence and the projection its sums
- *     depends on all of a call's sizes, so there a row's last bits may differ between batch sizes.
+ *   - Results are bitwise deterministic. How the scan and the linear attention (more than one step)
+ *     split a sequence, the projection its sums and the norms around a block the gradient of a gate
+ *     that rows share depends on all of a call's sizes, so there a row's last bits may differ between
+ *     batch sizes.
  * Sizes: every size at least 1; a tensor of 2^40 elements or more, B or G above 65535, rows (B * T,
  * M) of 2^31 - 65536 or more, more than 2^22 channels of the convolution or the scan, and M, N or K
  * of the projection above 4000000 are GDN_ERR_UNSUPPORTED_SHAPE.

@@ -83,3 +83,67 @@ def test_resnorm_gradients_with_a_gate_whose_own_is_not_wanted(M, gate_rows):
     with_dz, without = resnorm_bwd_abi(a, stats, gate_rows, z), resnorm_bwd_abi(a, stats, gate_rows, z, want_dz=False)
     assert without["dz"] is None and with_dz["dz"].isfinite().all()
     assert all(torch.equal(with_dz[n], without[n]) for n in with_dz if n != "dz")
+
+
+def linattn_inputs(seed, B, T, Hk, Hv, Dk, Dv, dt, g=None):
+    gen = torch.Generator(device="cuda")
+    gen.manual_seed(seed)
+    rnd = lambda *s, scale=1.0: torch.randn(*s, generator=gen, device="cuda") * scale  # noqa: E731
+    decay = torch.exp(-torch.exp2(-8.0 * (torch.arange(Hv, device="cuda") + 0.5) / Hv)) if g is None else torch.full((Hv,), g, device="cuda")
+    return dict(q=rnd(B, T, Hk, Dk, scale=Dk ** -0.5).to(dt), k=rnd(B, T, Hk, Dk).to(dt), v=rnd(B, T, Hv, Dv).to(dt), g=decay, S0=rnd(B, Hv, Dv, Dk),
+                dy=rnd(B, T, Hv, Dv).to(dt), dS_T=rnd(B, Hv, Dv, Dk, scale=0.3))
+
+
+def linattn(a, train=True, rows=slice(None), state=True):
+    a = {n: t if n == "g" else t[rows] for n, t in a.items()}
+    S0, dS_T = (a["S0"], a["dS_T"]) if state else (None, None)
+    out = dict(zip(("y", "S_T"), gdn().gdn_linattn_fwd(a["q"], a["k"], a["v"], a["g"], S0)))
+    if train:
+        out.update(gdn().gdn_linattn_bwd(a["q"], a["k"], a["v"], a["g"], a["dy"], S0, None, dS_T))
+    return out
+
+
+@pytest.mark.parametrize("dt", [BF16, F32], ids=["bf16", "f32"])
+@pytest.mark.parametrize("T", [1, 5, 600])
+def test_linattn_rows_beside_others_and_alone(T, dt):
+    """40 rows of 4 heads fill the SMs and go whole, one goes in segments: a row's results differ by what both are
+    off the definition at most (twice 1.5 x 2^-8 in bf16, twice 4e-6 in float32, states twice 2^-20). A single step has no
+    segments: the same bits."""
+    a = linattn_inputs(1, 40, T, 2, 4, 64, 64, dt)
+    whole = linattn(a)
+    for b in (0, 17, 39):
+        for n, x in linattn(a, rows=slice(b, b + 1)).items():
+            if T == 1 and n in ("y", "S_T"):
+                assert torch.equal(x[0], whole[n][b]), n
+            else:
+                tol = 2 ** -19 if n in ("S_T", "dS0") else 3 * 2 ** -8 if dt is BF16 else 8e-6
+                assert R.rel(x[0], whole[n][b].double()) <= tol, (n, b, R.rel(x[0], whole[n][b].double()))
+
+
+@pytest.mark.parametrize("dt", [BF16, F32], ids=["bf16", "f32"])
+@pytest.mark.parametrize("gate", [None, "sequence", "step"])
+def test_resnorm_rows_beside_others_and_alone(gate, dt):
+    """The same bits for a batch and for its rows one by one, but for the gradient of a gate that a sequence's steps
+    share, whose units are cut by the number of sequences: sums of 700 float32 terms of either sign in two orders (each off
+    by a few 2^-24 of them), rounded once."""
+    B, T, D = 6, 700, 192
+    rows = resnorm_rows(3, B * T, D, dt)
+    a = {n: t.view(B, T, D) if t.dim() == 2 else t for n, t in rows.items()}
+    z = None if gate is None else torch.randn(*((B, D) if gate == "sequence" else (B, T, D)), device="cuda").to(dt)
+
+    def run(s):
+        x, h, dy, dr = (a[n][s] for n in ("x", "h", "dy", "dr"))
+        p = (None if z is None else z[s], a["scale"], a["w_post"], a["w_pre"])
+        r, y, stats = gdn().gdn_resnorm_fwd(x, h, *p, act="silu")
+        d = gdn().gdn_resnorm_bwd(x, h, stats, dy, dr, *p, act="silu")
+        return {"r": r, "y": y, "stats": stats, "dx": d["dx"], "dh": d["dh"], "dz": d["dz"]}
+
+    whole = run(slice(None))
+    for b in range(B):
+        for n, x in run(slice(b, b + 1)).items():
+            if n == "dz" and gate is None:
+                assert x is None
+            elif n == "dz" and gate == "sequence":
+                assert R.rel(x[0], whole[n][b].double()) <= (2 ** -8 if dt is BF16 else 16 * 2 ** -24)
+            else:
+                assert torch.equal(x[0], whole[n][b]), n

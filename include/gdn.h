@@ -300,7 +300,7 @@ GDN_API int gdn_gates_bwd(const gdn_shape *shape, const void *a, const void *b, 
  *     type (more than one packed bf16 row of the projection's x or W: 16 bytes, except in its
  *     forward with M <= 32). Everything else is packed and 16-byte aligned.
  *   - Parameters that are small (convolution taps, norm weights, A_log, ...) and their gradients are
- *     float32; arithmetic is float32.
+ *     float32; arithmetic is float32, but for the operands of the linear attention's chunks (see there).
  *   - lens ([B] int32, may be NULL: every row has T steps; values are clamped to 0..T) gives each
  *     row's number of valid steps. The steps behind them hold anything, NaN included: they are not
  *     used, leave the carried state alone, and their outputs and gradients are written as zeros. A
@@ -454,6 +454,14 @@ GDN_API int gdn_linear_bwd(const gdn_linear_shape *shape, const void *x, const v
  * aligned) or step by step (float32 and the rest); a single step is one pass over the state, and with T = 1
  * S_T may be S0 itself (updated in place). In chunks, a q, k, v or dy that is not finite at a valid step makes
  * outputs of its chunk of the same row and head NaN, those of other steps of it too, and the states behind it.
+ * Rounding in chunks: sums and the state that is carried on are float32, but the tensor cores' operands are bf16.
+ * For y, dq, dk and dv the state is rounded to bf16 where it is read, and so is one of the decayed products
+ * (a . b) and the weighted inputs of the state; the other one has 16 bits or more (which one also depends on
+ * whether S_T, or dS0, is asked for). These outputs are off by some 2.0e-3 to 2.7e-3 of their norm, where bf16
+ * alone takes 1.7e-3. S_T and dS0: what a step adds has 24 bits where its chunk of 128 steps still counts by
+ * 1/8 or more at the end, 16 down to 2^-12 and 8 below, so that each step's part is off by at most 2^-19 of
+ * outer(v_t, k_t) (outer(dy_t, q_t)) before its decay, besides float32's own roundings. Where the late steps are zero,
+ * S_T holds what is left of the early ones to no more than that.
  * The backward computes the states again from k, v and S0; the forward saves nothing. dq and dk are
  * summed over the value heads of each key head in ascending order.
  * workspace: gdn_linattn_fwd_workspace_bytes / gdn_linattn_bwd_workspace_bytes bytes (0: may be NULL).

@@ -147,3 +147,33 @@ def test_resnorm_rows_beside_others_and_alone(gate, dt):
                 assert R.rel(x[0], whole[n][b].double()) <= (2 ** -8 if dt is BF16 else 16 * 2 ** -24)
             else:
                 assert torch.equal(x[0], whole[n][b]), n
+
+
+@pytest.mark.parametrize("carried", [True, False])
+@pytest.mark.parametrize("g", [1.0, 2 ** (-2.9 / 128), 2 ** (-3.1 / 128), 2 ** (-11.9 / 128), 2 ** (-12.1 / 128), 2 ** (-11.9 / 384), 2 ** (-12.1 / 384)])
+@pytest.mark.parametrize("T", [512, 450])
+def test_states_where_the_number_of_terms_changes(T, g, carried):
+    """S_T and dS0 in chunks at decays with a chunk's weight on either side of 1/8 and of 2^-12, and without a decay,
+    against float64. The weights' powers are off by 4 ulp at most, 2^-21; the tensor cores cut a sum off at each of a
+    chunk's eight products, half of 2^-23 of a running sum that grows by its square root, 0.67 x 2^-21 together; the two-term
+    chunks' part is less than 2^-22: 2^-20 of the norm. With one term fewer in the last chunk it would be 2^-18, in an earlier
+    one 2^-14."""
+    a = linattn_inputs(T, 2, T, 2, 4, 64, 72, BF16, g)
+    got = linattn(a, state=carried)
+    leaves = {n: a[n].double() for n in ("q", "k", "v")}
+    leaves["S0"] = a["S0"].double() if carried else torch.zeros_like(a["S0"], dtype=torch.float64)
+    (_, S), grads = R.with_grads(lambda **kw: K.linattn(**kw, g=a["g"].double(), lens=None), leaves, (a["dy"].double(), a["dS_T"].double() if carried else None))
+    for mine, ref in ((got["S_T"], S), (got["dS0"], grads["S0"])):
+        assert R.rel(mine, ref) <= 2 ** -20, R.rel(mine, ref)
+
+
+def test_states_behind_steps_of_zeros():
+    """A row whose last 400 steps add nothing: element by element within 2^-19 of what its steps add before their decay,
+    and 2^-20 of itself."""
+    a = linattn_inputs(7, 2, 900, 1, 4, 64, 64, BF16)
+    a["v"][:, 500:] = 0.0
+    _, S = gdn().gdn_linattn_fwd(a["q"], a["k"], a["v"], a["g"])
+    _, ref = K.linattn(a["q"].double(), a["k"].double(), a["v"].double(), a["g"].double(), None, None)
+    k = a["k"].double().abs().repeat_interleave(4, 2)
+    bound = 2 ** -19 * torch.einsum("bthv,bthk->bhvk", a["v"].double().abs(), k) + 2 ** -20 * ref.abs()
+    assert torch.all((S.double() - ref).abs() <= bound)

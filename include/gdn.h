@@ -452,8 +452,13 @@ GDN_API int gdn_linear_bwd(const gdn_linear_shape *shape, const void *x, const v
  * in chunks of 128 steps on the tensor cores (bf16, 8 steps or more; q, k and v whose dims or row strides are no
  * multiples of 8 are copied into the workspace, for 64 steps or more; those that are have to be 16-byte
  * aligned) or step by step (float32 and the rest); a single step is one pass over the state, and with T = 1
- * S_T may be S0 itself (updated in place). In chunks, a q, k, v or dy that is not finite at a valid step makes
- * outputs of its chunk of the same row and head NaN, those of other steps of it too, and the states behind it.
+ * S_T may be S0 itself (updated in place).
+ * Not finite at a valid step: in chunks (of the row's steps 0 to 127, 128 to 255, ...) a q, k, v or dy that is not
+ * finite, or a product a . b beyond float32, may make NaN of any output of its chunk in the same row and head (of a
+ * shared key head: in all that share it), of steps in front of it too, and of the states behind it. Step by step
+ * (float32, fewer steps, other addresses) steps in front of it, or behind it for dk and dv, keep their values: so a
+ * bf16 prompt of 7 steps and one of 8 differ there. In both forms the outputs y and dq of earlier chunks, and dk and dv
+ * of later ones, are as without it.
  * Rounding in chunks: sums and the state that is carried on are float32, but the tensor cores' operands are bf16.
  * For y, dq, dk and dv the state is rounded to bf16 where it is read, and so is one of the decayed products
  * (a . b) and the weighted inputs of the state; the other one has 16 bits or more (which one also depends on

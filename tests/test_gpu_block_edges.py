@@ -177,3 +177,34 @@ def test_states_behind_steps_of_zeros():
     k = a["k"].double().abs().repeat_interleave(4, 2)
     bound = 2 ** -19 * torch.einsum("bthv,bthk->bhvk", a["v"].double().abs(), k) + 2 ** -20 * ref.abs()
     assert torch.all((S.double() - ref).abs() <= bound)
+
+
+@pytest.mark.parametrize("dt,T,bad", [(BF16, 500, 200), (BF16, 1600, 900), (BF16, 7, 3), (F32, 500, 200), (F32, 1600, 900)])
+def test_what_is_not_finite_reaches(dt, T, bad):
+    """A NaN in k and an infinity in v at one step: y and dq of earlier chunks (step by step: of earlier steps), dk and
+    dv of later ones, the other head and the other row keep their bits."""
+    a = linattn_inputs(5, 2, T, 2, 2, 64, 64, dt)
+    clean = linattn(a)
+    a["k"][1, bad, 0, 5], a["v"][1, bad, 0, 7] = float("nan"), float("inf")
+    dirty = linattn(a)
+    unit = 128 if dt is BF16 and T >= 8 else 1
+    first, last = bad // unit * unit, (bad // unit + 1) * unit
+    for n, x in dirty.items():
+        assert torch.equal(x[0], clean[n][0]), n
+        if n in ("S_T", "dS0"):
+            assert torch.equal(x[1, 1], clean[n][1, 1])
+            continue
+        assert torch.equal(x[1, :, 1], clean[n][1, :, 1]), n
+        kept = slice(0, first) if n in ("y", "dq") else slice(last, T)
+        assert torch.equal(x[1, kept, 0], clean[n][1, kept, 0]), n
+    assert dirty["y"][1, bad, 0].isnan().all() and dirty["S_T"][1, 0].isnan().any()
+
+
+@pytest.mark.parametrize("T", [7, 300])
+def test_a_query_that_is_not_finite_reaches_its_own_step(T):
+    a = linattn_inputs(6, 1, T, 1, 1, 64, 64, BF16)
+    clean = linattn(a, train=False)
+    a["q"][0, 5, 0, 0] = float("nan")
+    y, S = linattn(a, train=False).values()
+    keep = torch.arange(T, device="cuda") != 5
+    assert y[0, 5].isnan().all() and torch.equal(y[0, keep], clean["y"][0, keep]) and torch.equal(S, clean["S_T"])

@@ -19,11 +19,11 @@ int api_device_status_address(int **out);
 // rows * ld apart), 128-byte swizzle; what lies outside an array reads as zero. box_blocks = 0: 3-D
 // {cols, rows, planes}, box {64, box_rows, 1}. Else (cols a multiple of 64) 4-D {64, rows, cols / 64,
 // planes}, box {64, box_rows, box_blocks, 1}: box_blocks neighbouring boxes of 64 columns by one copy.
+int api_planes_map(CUtensorMap *map, const void *ptr, uint64_t cols, uint64_t rows, uint64_t planes, uint64_t ld, int box_rows,
+                   int box_blocks);
 // Tensor map of a bf16 [B][T][H][D] array with `ld` elements between steps: 4-D {D, H, T, B}, box {64, 1,
 // box_t, 1}, 128-byte swizzle; what lies outside reads as zero.
 int api_heads_map(CUtensorMap *map, const void *ptr, int B, int T, int H, int D, long long ld, int box_t);
-int api_planes_map(CUtensorMap *map, const void *ptr, uint64_t cols, uint64_t rows, uint64_t planes, uint64_t ld, int box_rows,
-                   int box_blocks);
 
 // ---- parameter blocks
 struct ConvParams {

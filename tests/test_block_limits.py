@@ -17,3 +17,22 @@ def test_resnorm_workspace_holds_the_call_without_a_gate(lib, M, D, gate_rows): 
     assert need(gate_rows=gate_rows) >= need(gate_rows=1) > 0
     assert H.call(lib, "gdn_resnorm_bwd", H.resnorm_shape(M=M, D=D, gate_rows=gate_rows), z=None, dz=None,
                   **{"#workspace": need(gate_rows=gate_rows) - 1}) == H.SMALL
+
+
+@pytest.mark.parametrize("what", [dict(B=1, T=4096, Hk=1, Hv=1), dict(Dk=63, Hk=4), dict(ldq=129, Hk=2, Hv=4, T=64), dict(dtype=0, B=1, Hk=1, Hv=1, T=4096),
+                                  dict(Dk=256, Dv=256, Hk=4)],
+                         ids=["segments", "copies", "odd stride", "segments step by step", "wide keys"])
+def test_linattn_forward_refuses_a_small_workspace(lib, what):  # noqa: F811
+    """Forward calls that need room: for segments' states, copies of rows, float32 outputs."""
+    shape = H.linattn_shape(**what)
+    need = lib.gdn_linattn_fwd_workspace_bytes(ctypes.byref(shape))
+    assert need > 0
+    for room in (0, need - 1):
+        assert H.call(lib, "gdn_linattn_fwd", shape, **{"#workspace": room}) == H.SMALL
+    assert H.call(lib, "gdn_linattn_fwd", shape, workspace=None) == H.INVALID
+    assert H.call(lib, "gdn_linattn_fwd", shape, workspace=H.FAKE + 8) == H.MISALIGNED
+
+
+@pytest.mark.parametrize("what", [dict(T=1), dict(T=7, Hk=4, dtype=0), dict(B=40, Hk=4, T=300)])
+def test_linattn_forward_without_a_workspace(lib, what):  # noqa: F811
+    assert lib.gdn_linattn_fwd_workspace_bytes(ctypes.byref(H.linattn_shape(**what))) == 0

@@ -1,6 +1,7 @@
 """Linear attention with a decay and the norms around a block on the GPU: calls of the C ABI that the binding
 does not make, and what the header says of one row, one prompt or one input beside the others."""
 import ctypes
+import random
 
 import pytest
 
@@ -208,3 +209,110 @@ def test_a_query_that_is_not_finite_reaches_its_own_step(T):
     y, S = linattn(a, train=False).values()
     keep = torch.arange(T, device="cuda") != 5
     assert y[0, 5].isnan().all() and torch.equal(y[0, keep], clean["y"][0, keep]) and torch.equal(S, clean["S_T"])
+
+
+@pytest.mark.parametrize("dt", [BF16, F32], ids=["bf16", "f32"])
+def test_linattn_tensors_of_more_than_2_to_the_31_elements(dt):
+    """v, y, dy, dv and the value heads' float32 dq and dk pass 2^31 elements: the last row's last steps against a call of
+    its last 568 steps alone (g = 0.8: what lies 500 steps off counts by 2^-160), as far apart as each is off."""
+    B, T, Hk, Hv, D, tail = 2, 35000, 2, 256, 128, 568
+    if dt is F32:
+        T = 34888                                                       # (whole tiles of 16 steps in the tail as well)
+    gen = torch.Generator(device="cuda")
+    gen.manual_seed(1)
+    rnd = lambda *s: torch.randn(*s, generator=gen, device="cuda", dtype=dt)  # noqa: E731
+    q, k, v, dy = rnd(B, T, Hk, D), rnd(B, T, Hk, D), rnd(B, T, Hv, D), rnd(B, T, Hv, D)
+    assert v.numel() > 2 ** 31
+    g = torch.full((Hv,), 0.8, device="cuda")
+    cut = [t[1:, T - tail:].contiguous() for t in (q, k, v, dy)]
+    y0, S0 = gdn().gdn_linattn_fwd(*cut[:3], g)
+    d0 = gdn().gdn_linattn_bwd(*cut[:3], g, cut[3])
+    y, S = gdn().gdn_linattn_fwd(q, k, v, g)
+    tol = 3 * 2 ** -8 if dt is BF16 else 8e-6
+    assert R.rel(y[1, -64:], y0[0, -64:]) <= tol and R.rel(S[1], S0[0]) <= 2 ** -19
+    del y, S
+    d = gdn().gdn_linattn_bwd(q, k, v, g, dy, want_dS0=False)
+    for n in ("dq", "dk", "dv"):
+        assert R.rel(d[n][1, -64:], d0[n][0, -64:]) <= tol, n
+
+
+def test_resnorm_rows_behind_2_to_the_31_elements():
+    """Row by row the same bits as a call of the last rows alone."""
+    M, D, tail = 265000, 8192, 100
+    a = {n: torch.randn(M, D, device="cuda", dtype=BF16) for n in ("x", "h", "dy", "dr")}
+    assert a["x"].numel() > 2 ** 31
+    w = torch.rand(D, device="cuda")
+
+    def run(rows):
+        x, h, dy, dr = (a[n][rows] for n in ("x", "h", "dy", "dr"))
+        r, y, stats = gdn().gdn_resnorm_fwd(x, h, None, w, w, w)
+        d = gdn().gdn_resnorm_bwd(x, h, stats, dy, dr, None, w, w, w)
+        return [t[-tail:].clone() for t in (r, y, stats, d["dx"], d["dh"])]
+
+    assert all(torch.equal(x, y) for x, y in zip(run(slice(None)), run(slice(M - tail, M))))
+
+
+def linattn_abi(a, lens, state, strides):
+    """Forward and backward as a C program calls them: workspaces of exactly the size asked for, and outputs preset to
+    NaN, all with guards behind them."""
+    from gated_delta_rule_22_gb300 import layer as Ly
+    B, T, Hk, Dk = a["q"].shape
+    Hv, Dv = a["v"].shape[2:]
+    lib, dt, guards = Ly._library(), a["q"].dtype, []
+    shape = ctypes.byref(Ly.GdnLinattnShape(B, T, Hk, Hv, Dk, Dv, 1 if dt is BF16 else 0, *strides))
+
+    def guarded(size, dtype):
+        n = 1
+        for d in size:
+            n *= d
+        whole = torch.full((n + 64,), float("nan") if dtype is not torch.uint8 else 0x5a, dtype=dtype, device="cuda")
+        guards.append(whole[n:])
+        return whole[:n].view(size)
+
+    S0, dS_T = (a["S0"], a["dS_T"]) if state else (None, None)
+    out = {"y": guarded(a["v"].shape, dt), "S_T": guarded(a["S0"].shape, F32), "dq": guarded(a["q"].shape, dt), "dk": guarded(a["q"].shape, dt),
+           "dv": guarded(a["v"].shape, dt), "dS0": guarded(a["S0"].shape, F32)}
+    stream = ctypes.c_void_p(torch.cuda.current_stream().cuda_stream)
+    need = lib.gdn_linattn_fwd_workspace_bytes(shape), lib.gdn_linattn_bwd_workspace_bytes(shape)
+    ws = [guarded((n,), torch.uint8) for n in need]
+    ins = [_at(a[n]) for n in ("q", "k", "v", "g")] + [_at(S0), _at(lens)]
+    assert lib.gdn_linattn_fwd(shape, *ins, _at(out["y"]), _at(out["S_T"]), _at(ws[0]), need[0], stream) == 0
+    assert lib.gdn_linattn_bwd(shape, *ins, _at(a["dy"]), _at(dS_T), *(_at(out[n]) for n in ("dq", "dk", "dv", "dS0")), _at(ws[1]), need[1], stream) == 0
+    torch.cuda.synchronize()
+    assert gdn().gdn_device_status() == 0
+    assert all(torch.all(t == 0x5a) if t.dtype is torch.uint8 else t.isnan().all() for t in guards)
+    return out
+
+
+@pytest.mark.parametrize("seed", range(24))
+def test_linattn_in_workspaces_of_the_size_asked_for(seed):
+    """Random sizes and strides (each of q, k and v packed, or with a stride that TMA reads, or one that it does not, at
+    any address), in both types, with rows of any length and NaN behind them: the definition, and nothing written
+    behind an output or a workspace."""
+    rng = random.Random(seed)
+    dt = BF16 if seed % 3 else F32
+    B, Hk, group = rng.randint(1, 3), rng.randint(1, 3), rng.choice([1, 2, 3])
+    T, dim = rng.choice([1, 2, 7, 8, 63, 64, 65, 129, 300, 700]), lambda: rng.choice([rng.randint(1, 256), 64, 128, 8 * rng.randint(1, 32)])
+    Dk, Dv = dim(), dim()
+    a = linattn_inputs(seed, B, T, Hk, Hk * group, Dk, Dv, dt)
+    lens = torch.tensor([rng.randint(0, T) for _ in range(B)], device="cuda", dtype=torch.int32) if rng.random() < 0.6 else None
+    strides = []
+    for n in ("q", "k", "v"):
+        width, pad = a[n].shape[2] * a[n].shape[3], rng.choice([0, 8, 16, 1, 3])
+        before = rng.choice([0, pad // 2, 1, pad]) if pad else 0
+        wide = torch.full((B, T, width + pad), float("nan"), device="cuda", dtype=dt)
+        a[n] = wide[..., before:before + width].unflatten(-1, a[n].shape[2:]).copy_(a[n])
+        strides.append(width + pad)
+    for b, n in enumerate([] if lens is None else lens.tolist()):
+        for t in ("q", "k", "v", "dy"):
+            a[t][b, n:] = float("nan")
+    state = rng.random() < 0.5
+    got = linattn_abi(a, lens, state, strides)
+    leaves = {n: a[n].double() for n in ("q", "k", "v")}
+    leaves["S0"] = a["S0"].double() if state else torch.zeros_like(a["S0"], dtype=torch.float64)
+    ok = (torch.arange(T, device="cuda") < (T if lens is None else lens[:, None])).expand(B, T)[:, :, None, None]
+    cot = (torch.where(ok, a["dy"].double(), 0.0), a["dS_T"].double() if state else None)
+    (y, S), grads = R.with_grads(lambda **kw: K.linattn(**kw, g=a["g"].double(), lens=lens), leaves, cot)
+    for n, ref in {"y": y, "S_T": S, **{"d" + n: t for n, t in grads.items()}}.items():
+        tol = 2 ** -18 if n in ("S_T", "dS0") else 1.5 * 2 ** -8 if dt is BF16 else 4e-6
+        assert R.rel(got[n], ref) <= tol, (n, T, Dk, Dv, strides, R.rel(got[n], ref))

@@ -8,9 +8,11 @@
 // Forward and gradients are the same sweep (LinattnSweep in gdn_layer.cuh) over other operands, so that one
 // kernel computes them all.
 //
-// Measured: one step of 64 rows of 32 heads of 128 x 128, 43 us, 6.2 TB/s of state. Step by step in float32, 8 x 1024
-// steps of 32 heads of 128 x 128: 860 to 890 us, 19 TFLOP/s of the two products of a step. Few rows are bound by the latency
-// of a step's sums over lanes, 135 ns: 1 x 1024 steps of 8 heads 136 us, in segments 75.
+// Measured: one step of 64 rows of 32 heads of 128 x 128, 43 us, 6.2 TB/s of state; two to four steps, step by step, 151 to 155 (the
+// state in pieces of 8 bytes, by small CTAs). Step by step in float32, 8 x 1024 steps of 32 heads of 128 x 128: 860 to 890 us, 19
+// TFLOP/s of the two products of a step. Few rows are bound by the latency of a step's sums over lanes, 135 ns: 1 x 1024 steps of
+// 8 heads 136 us, in segments 74. bf16 at addresses that TMA cannot read, 4 x 1024 of 32 heads: 537 us, in chunks 49. The large
+// CTAs' form of dims above 128 spills 312 bytes of a thread in bf16.
 #include "gdn_layer.cuh"
 
 namespace gdn {

@@ -29,13 +29,14 @@
 // A chunk takes some 6000 cycles, 3.2 us: P is there after 900, P~'s first columns after 3000 and its last after 4800,
 // b~ after 3000, and from there the tensor cores are busy with U, O2 and O1 until 5700; the outputs leave under the next
 // chunk's P and mask, 3300 cycles. All of these share one shared memory, whose bandwidth takes some 2000 cycles for the
-// products' operands, 800 for TMA's writes, 800 for b~ and Z and more for the mask's powers and the stores' rows, so
-// that more warps, more columns at once or loads further ahead in any of them slowed the others (483 to 491 us for what
-// is 440 so). O1 begins with the columns that are there, those of the half with more zeros first. Where the state leaves the
+// products' operands, 800 for TMA's writes, 800 for b~ and Z and besides those the mask's powers and the stores' rows:
+// more warps, more columns at once or loads further ahead in any of them slowed the others (483 to 491 us for what
+// is 440 so). The rest is roles that wait for one another; the two have not been told apart. O1 begins with the
+// columns that are there, those of the half with more zeros first. Where the state leaves the
 // call and b~ has several terms, a chunk takes up to 9000 cycles. What carries the loops: code short enough for the
-// instruction cache, one arrival per warp, work of one kind in each warp. 4 x 4096 steps of 32 heads of 128 x 128: forward
-// 113 us (127 with S_T), 4.7 TB/s of q, k, v and y, backward 321 us, 2.9 TB/s; 4 x 2048 with 16 key heads and a carried
-// state 75 to 78 us.
+// instruction cache, one arrival per warp, work of one kind in each warp (80 registers at launch, 280 bytes spilled). 4 x 4096
+// steps of 32 heads of 128 x 128: forward 111 us, 4.9 TB/s of q, k, v and y (127 with S_T), backward 317 us, 3.0 TB/s; 4 rows of up to 2048
+// with 16 key heads and a carried state 77 us.
 #include "gdn.h"
 #include "gdn_layer.cuh"
 #include "gdn_umma.cuh"

@@ -11,8 +11,10 @@
 //
 // Bound by memory: every tensor is read once and every output written once. What a thread reads of a row
 // it copies into shared memory itself, asynchronously and some rows ahead (a ring of its own, so that
-// nobody waits for anybody but for the row's sums). 32768 x 2048 in bf16: forward 94 us, 5.7 TB/s; backward 153 us,
-// 5.3 TB/s, and 10 for the parameters' sums. 8192 x 4096 with a gate for each sequence, forward: 57 us, 4.7 TB/s.
+// nobody waits for anybody but for the row's sums). 32768 x 2048 in bf16: forward 94 to 101 us, 5.3 to 5.7 TB/s; backward 153 us,
+// 5.3 TB/s, and 10 for the parameters' sums. 8192 x 4096 with a gate for each sequence, forward: 56 us, 4.75 TB/s. 8192 x 8192:
+// forward 97 us, 5.5 TB/s, backward 264 and 12; 4096 x 16384: 107, and 542 and 15: the backward of more than 4096 channels
+// spills.
 #include "gdn_layer.cuh"
 
 #include <type_traits>
@@ -451,6 +453,10 @@ void resnorm_units(ResnormParams *p, int dtype) {
 
 // f(kernel parameters as types): the form for D channels of a type, in pieces of `width` of them (16 bytes, two or one).
 // 999 x 1030 in float32 with a gate, in pairs and one by one: forward 11 and 15 us, backward 17 and 28.
+// Eight channels of a thread on as few threads as hold the row, so that its sums meet in few places; sixteen where a
+// warp can hold it so (to 512 channels) and where it would need more than 512 threads. The backward's five tensors, parameters and
+// sums of eight channels are 126 registers; of sixteen it spills, 490 bytes of a thread with 512 threads, 1500 to 2200
+// with 1024: 2^26 channels in bf16 in rows of 4096 take it 173 us, of 8192 264, of 16384 542.
 template <typename T, typename F>
 static cudaError_t with_row(int D, int width, F f) {
     constexpr int V = 16 / (int)sizeof(T), W = 8 / V;      // W: pieces of eight channels

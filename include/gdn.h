@@ -450,8 +450,9 @@ GDN_API int gdn_linear_bwd(const gdn_linear_shape *shape, const void *x, const v
  *   S0, S_T, dS_T, dS0 [B,Hv,Dv,Dk] float32, each may be NULL (S0, dS_T: zeros)
  * Dk and Dv are 1 to 256, Hv a multiple of Hk (else GDN_ERR_UNSUPPORTED_SHAPE). Prompts and training run
  * in chunks of 128 steps on the tensor cores (bf16, 8 steps or more; q, k and v whose dims or row strides are no
- * multiples of 8 are copied into the workspace, for 64 steps or more; those that are have to be 16-byte
- * aligned) or step by step (float32 and the rest); a single step is one pass over the state, and with T = 1
+ * multiples of 8 are copied into the workspace, for 64 steps or more; where they are, the address has to be a
+ * multiple of 16 bytes, or the call goes step by step: ten times slower) or step by step (float32, and bf16 of
+ * fewer steps); a single step is one pass over the state, and with T = 1
  * S_T may be S0 itself (updated in place).
  * Not finite at a valid step: in chunks (of the row's steps 0 to 127, 128 to 255, ...) a q, k, v or dy that is not
  * finite, or a product a . b beyond float32, may make NaN of any output of its chunk in the same row and head (of a
